@@ -412,6 +412,156 @@ sv_status spec_verify_tree(const void* target_logits, const void* draft_logits, 
                            int32_t V, int32_t* out_tokens, int32_t* out_path, int32_t* out_len,
                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The target model's key/value cache around a verification step
+ * ------------------------------------------------------------------------
+ * A decode step over a tree (or chain) of drafted tokens writes the nodes'
+ * keys and values behind each sequence's context (spec_kv_append), attends
+ * from every node to the context and to its ancestors (spec_tree_attention),
+ * verifies (spec_verify_tree), and moves the kept path's entries to
+ * consecutive positions (spec_kv_commit).  spec_kv_read returns ranges of the
+ * cache as dense rows.
+ *
+ * The cache is paged.  Position p of sequence b lives in page
+ * page_table[b][p / page_size] at slot p % page_size; a page holds page_size
+ * positions of every head of one layer:
+ *   k, v     [layers][num_pages][n_kv_heads][page_size][head_dim]
+ *   k_scale, v_scale  [layers][num_pages][n_kv_heads][page_size] float32 with
+ *            SV_KV_E4M3 (each entry stands for its e4m3 value times its
+ *            scale), NULL with SV_KV_BF16
+ * All pointers are device memory, 16-byte aligned.  head_dim: a multiple of
+ * 16 from 64 to 256; page_size: a power of two from 8 to 1024.  Only
+ * spec_kv_commit looks past layer 0: for a call on layer l pass that layer's
+ * pointers and layers = 1.
+ *
+ * Node n of a sequence with kv_len context positions is stored at position
+ * kv_len + n; trees are given as in spec_verify_tree (parent[n] < n for
+ * n >= 1, node 0 the root, at most 32 nodes), parent == NULL being the chain
+ * parent[n] = n - 1.
+ *
+ * Device data that cannot be used (a length outside the page table, a page
+ * outside [0, num_pages), a malformed tree, a position outside the rotation
+ * table) never traps and touches no memory outside the buffers: the sequence
+ * or token it belongs to is not written to the cache, its output rows are
+ * NaN (spec_kv_commit: nothing moves, its length stays), and bit 2 of
+ * `errors` is set.  `errors` is a device uint32 that the calls only OR into
+ * (zero it once; sv_workspace_errors reads and clears it), or NULL.
+ * Calls are asynchronous on `stream` and allocate nothing.
+ */
+typedef enum { SV_KV_BF16 = 0, SV_KV_E4M3 = 1 } sv_kv_format;
+
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* page_table;   /* [B][max_pages] */
+    int32_t max_pages;
+    int32_t format;              /* sv_kv_format */
+    int32_t layers;
+    int32_t num_pages;
+    int32_t n_kv_heads;
+    int32_t page_size;
+    int32_t head_dim;
+} sv_kv_cache;
+
+/*
+ * New tokens of spec_kv_append.  Rows are tokens: q [n_heads][head_dim] at
+ * element t * q_stride of token t, k and v [n_kv_heads][head_dim] likewise
+ * (slices of one fused projection, for instance); element type `dtype`;
+ * addresses and strides multiples of 16 bytes.
+ *   padded  row_start == NULL: token i of sequence b is row b * S + i;
+ *           n_new[b] <= S of them are real (NULL: all S).
+ *   packed  row_start [B + 1]: sequence b's tokens are the rows row_start[b]
+ *           to row_start[b + 1] - 1 of `rows`; n_new, parent and S unused.
+ * q may be NULL (keys and values only).  q_out [rows][n_heads][head_dim]
+ * receives the queries, zeros in the rows of no real token; q_out may be q
+ * where q_stride is n_heads * head_dim.
+ *
+ * In one pass, in fp32, each query and key head's row x becomes
+ *   x rsqrt(mean(x^2) + eps) * norm        (q_norm / k_norm NULL: x itself),
+ * and its first rotary_dim elements are rotated pair by pair,
+ *   (a, c) -> (a cos - c sin, c cos + a sin),
+ * a pair being elements (i, i + rotary_dim / 2), or (2i, 2i + 1) with
+ * `interleaved`, its angle entry i of row p of cos_sin [max_positions]
+ * [rotary_dim] (cosines, then sines; NULL: no rotation), p = kv_len + the
+ * node's depth (the token's index without a tree).  rotary_dim is a multiple
+ * of 16.  Keys and values are then rounded once to the cache's format; with
+ * SV_KV_E4M3 each (token, head) row x is stored as the nearest e4m3 values of
+ * x / scale, scale = max(amax|x| / 448, 2^-100) (a row that holds a NaN or an
+ * infinity reads back as NaN).
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_stride;
+    int64_t k_stride;
+    int64_t v_stride;
+    const void* q_norm;          /* [head_dim] of dtype */
+    const void* k_norm;
+    const float* cos_sin;
+    const int32_t* parent;       /* [B][S] */
+    const int32_t* n_new;        /* [B] */
+    const int32_t* row_start;    /* [B + 1] */
+    void* q_out;
+    int32_t dtype;               /* sv_dtype of q, k, v, the norms and q_out */
+    int32_t n_heads;
+    int32_t B;
+    int32_t S;
+    int32_t rows;                /* B * S when padded */
+    int32_t max_positions;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    float eps;
+} sv_kv_tokens;
+
+sv_status spec_kv_append(const sv_kv_cache* cache, const sv_kv_tokens* tokens, const int32_t* kv_len,
+                         uint32_t* errors, cudaStream_t stream);
+
+/*
+ * spec_tree_attention -- out[b][n] = sum_j softmax_j(scale q[b][n] . k_j) v_j
+ * for every node n < n_nodes[b] (NULL: all Nmax) and query head, over the
+ * keys of the kv head that n_heads / n_kv_heads query heads share, at the
+ * positions j < kv_len[b] and at kv_len[b] + m for m = n and its ancestors.
+ * The nodes' keys and values are in the cache (spec_kv_append).  Nmax = 1 is
+ * an ordinary decode step.  q: element (b * Nmax + n) * q_stride, a multiple
+ * of 8; out [B][Nmax][n_heads][head_dim], zeros for n >= n_nodes[b]; both
+ * bf16 (fp32 is SV_ERR_UNSUPPORTED).  Products accumulate in fp32, softmax
+ * statistics are fp32; the weights are rounded to bf16 for the second
+ * product.  Cache entries behind a sequence's nodes are never used: they may
+ * hold anything.  workspace: >= sv_attention_workspace_size() bytes, 256-byte
+ * aligned, not initialised; calls that overlap need one each.
+ */
+size_t sv_attention_workspace_size(int32_t Nmax, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, const int32_t* n_nodes,
+                              const int32_t* parent, const void* q, int64_t q_stride, sv_dtype dtype,
+                              int32_t n_heads, int32_t B, int32_t Nmax, float scale, void* out,
+                              uint32_t* errors, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
+/*
+ * spec_kv_commit -- after spec_verify_tree: in every layer the entries of the
+ * kept nodes out_path[b][0 .. out_len[b] - 1] (out_path [B][Nmax], as
+ * spec_verify_tree writes it) move to the positions kv_len[b] + 1, + 2, ...
+ * (the root stays at kv_len[b]), and kv_len_out[b] = kv_len[b] + 1 +
+ * out_len[b].  A sequence with out_len -1 keeps its length and entries.
+ * kv_len_out may be kv_len (one small launch more).
+ */
+sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* kv_len, const int32_t* out_path,
+                         const int32_t* out_len, int32_t B, int32_t Nmax, int32_t* kv_len_out,
+                         uint32_t* errors, cudaStream_t stream);
+
+/*
+ * spec_kv_read -- rows row_start[b] .. row_start[b + 1] - 1 of k_out and v_out
+ * [rows][n_kv_heads][head_dim] (dtype, 16-byte aligned) receive the entries of
+ * sequence b at the positions start[b], start[b] + 1, ..., each value (times
+ * its scale) rounded once to dtype.  Rows of no sequence are zeros.
+ */
+sv_status spec_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32_t* row_start,
+                       int32_t B, int32_t rows, sv_dtype dtype, void* k_out, void* v_out,
+                       uint32_t* errors, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,7 +12,10 @@ Entry points (same names as the C ABI):
   sv_max_vocab, sv_status_string, sv_abi_version, sv_workspace_errors
 plus ``Workspace`` (a device buffer of sv_workspace_size bytes), ``Stats``
 (a device sv_stats) and ``SVOptions`` / ``SVDiag`` (the ctypes mirrors of
-sv_options / sv_diag).
+sv_options / sv_diag), and, from ``kv_cache.py`` on first use, the paged
+key/value cache around a verification step:
+  spec_kv_append, spec_tree_attention, spec_kv_commit, spec_kv_read,
+  sv_attention_workspace_size
 """
 from __future__ import annotations
 
@@ -453,11 +456,28 @@ def spec_verify_host(target, draft, draft_tokens, uniforms, temperature, K, stag
 
 def sv_workspace_errors(workspace: Workspace, stream=None) -> int:
     """Device-side error flags of the last call on ``workspace`` (synchronises):
-    bit 0 a bounded wait gave up, bit 1 a wrong temperature hint."""
+    bit 0 a bounded wait gave up, bit 1 a wrong temperature hint, bit 2
+    unusable cache metadata."""
     flags = ctypes.c_uint32(0)
     sp, _ = _stream(stream)
     st = _load().sv_workspace_errors(workspace.ptr, ctypes.byref(flags), sp)
-    # the status only restates the flags (timeout: bit 0; invalid argument: bit 1)
-    if st not in (SV_OK, SV_ERR_TIMEOUT) and not (st == SV_ERR_INVALID_ARG and flags.value & 2):
+    # the status only restates the flags (timeout: bit 0; invalid argument: bits 1 and 2)
+    if st not in (SV_OK, SV_ERR_TIMEOUT) and not (st == SV_ERR_INVALID_ARG and flags.value & 6):
         _check(st, "sv_workspace_errors")
     return int(flags.value)
+
+
+# ---------------------------------------------------------------------------
+# the key/value cache (kv_cache.py imports torch, so it is loaded on first use)
+# ---------------------------------------------------------------------------
+_KV_NAMES = ("spec_kv_append", "spec_tree_attention", "spec_kv_commit", "spec_kv_read",
+             "sv_attention_workspace_size", "SVKvCache", "SVKvTokens", "SV_KV_BF16", "SV_KV_E4M3")
+
+
+def __getattr__(name):
+    if name not in _KV_NAMES:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import kv_cache
+    for n in _KV_NAMES:
+        globals()[n] = getattr(kv_cache, n)
+    return globals()[name]

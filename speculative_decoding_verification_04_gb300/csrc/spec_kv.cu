@@ -1,0 +1,292 @@
+// spec_kv.cu -- host layer and C ABI of the paged key/value cache and the
+// attention over it: argument checks, launch shapes.  Nothing here allocates,
+// synchronises or keeps state between calls.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/specverify.h"
+#include "sv_attention.cuh"
+
+namespace sv {
+namespace {
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// The cache description, checked.  Row counts stay below 2^31 so that a row
+// is an int coordinate; byte offsets are 64-bit everywhere.
+sv_status check_cache(const sv_kv_cache* c, bool need_table, KvCache* out)
+{
+    if (!c || !c->k || !c->v || (need_table && !c->page_table) ||
+        (c->format != SV_KV_BF16 && c->format != SV_KV_E4M3))
+        return SV_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->n_kv_heads < 1 || c->layers < 1 || c->max_pages < 1)
+        return SV_ERR_INVALID_ARG;
+    if (c->format == SV_KV_E4M3 ? (!c->k_scale || !c->v_scale) : (c->k_scale || c->v_scale))
+        return SV_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || ((uintptr_t)c->k_scale & 3) || ((uintptr_t)c->v_scale & 3) ||
+        ((uintptr_t)c->page_table & 3))
+        return SV_ERR_INVALID_ARG;
+    if (c->head_dim < 64 || c->head_dim > 256 || c->head_dim % 16 || c->page_size < 8 || c->page_size > 1024 ||
+        (c->page_size & (c->page_size - 1)))
+        return SV_ERR_UNSUPPORTED;
+    if ((long long)c->num_pages * c->n_kv_heads * c->page_size > 0x7fffffffLL ||
+        (long long)c->max_pages * c->page_size > 0x7fffffffLL)
+        return SV_ERR_UNSUPPORTED;
+    out->k = static_cast<unsigned char*>(c->k);
+    out->v = static_cast<unsigned char*>(c->v);
+    out->k_scale = c->k_scale;
+    out->v_scale = c->v_scale;
+    out->table = c->page_table;
+    out->max_pages = c->max_pages;
+    out->layers = c->layers;
+    out->num_pages = c->num_pages;
+    out->Hkv = c->n_kv_heads;
+    out->D = c->head_dim;
+    out->page_shift = __builtin_ctz(c->page_size);
+    return SV_OK;
+}
+
+sv_status launched(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
+
+// Warps a token's work of `passes` warp passes is spread over: all of them
+// while the tokens alone leave the GPU's SMs short of warps, one per four
+// passes once there are plenty (a warp's token lookup is then shared by them).
+int warps_per_token(int passes, long long tokens)
+{
+    const long long want = 152 * 16;
+    const int most = std::max(1, passes), least = std::max(1, (passes + 3) / 4);
+    const long long w = tokens > 0 ? (want + tokens - 1) / tokens : most;
+    return (int)std::min<long long>(most, std::max<long long>(least, w));
+}
+
+template <typename T, bool E4M3>
+cudaError_t launch_append(AppendArgs& a, cudaStream_t st)
+{
+    const int units = a.c.D / 16, lpr = units <= 4 ? 4 : units <= 8 ? 8 : 16;
+    const int heads = (a.has_q ? a.Hq : 0) + 2 * a.c.Hkv, rpw = 32 / lpr;
+    a.wpt = warps_per_token((heads + rpw - 1) / rpw, a.rows);
+    const long long warps = (long long)a.rows * a.wpt;
+    const unsigned grid = (unsigned)((warps + 7) / 8);
+    if (lpr == 4)
+        sv_append_kernel<T, 4, E4M3><<<grid, 256, 0, st>>>(a);
+    else if (lpr == 8)
+        sv_append_kernel<T, 8, E4M3><<<grid, 256, 0, st>>>(a);
+    else
+        sv_append_kernel<T, 16, E4M3><<<grid, 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, bool E4M3>
+cudaError_t launch_read(ReadArgs& a, cudaStream_t st)
+{
+    const int units = 2 * a.c.Hkv * (a.c.D / 16);
+    a.wpt = warps_per_token((units + 31) / 32, a.rows);
+    const long long warps = (long long)a.rows * a.wpt;
+    sv_read_kernel<T, E4M3><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" {
+
+sv_status spec_kv_append(const sv_kv_cache* cache, const sv_kv_tokens* x, const int32_t* kv_len,
+                         uint32_t* errors, cudaStream_t stream)
+{
+    if (!x)
+        return SV_ERR_INVALID_ARG;
+    sv::AppendArgs a{};
+    sv_status st = sv::check_cache(cache, x->rows > 0, &a.c);
+    if (st != SV_OK)
+        return st;
+    const bool packed = x->row_start != nullptr;
+    if ((x->dtype != SV_DTYPE_F32 && x->dtype != SV_DTYPE_BF16) || x->B < 0 || x->rows < 0 ||
+        (!packed && (x->S < 0 || (long long)x->B * x->S != x->rows)))
+        return SV_ERR_INVALID_ARG;
+    if (x->rows == 0)
+        return SV_OK;
+    const int s = x->dtype == SV_DTYPE_BF16 ? 2 : 4, D = cache->head_dim;
+    if (x->B < 1 || !x->k || !x->v || !kv_len || (x->q && (!x->q_out || x->n_heads < 1)) ||
+        (packed && (x->parent || x->n_new)) || (x->parent && x->S > SV_K_MAX))
+        return SV_ERR_INVALID_ARG;
+    if (x->cos_sin && (x->rotary_dim < 16 || x->rotary_dim > D || x->rotary_dim % 16 || x->max_positions < 1))
+        return SV_ERR_INVALID_ARG;
+    if (!(x->eps >= 0.0f))
+        return SV_ERR_INVALID_ARG;
+    const void* vec[] = {x->q, x->k, x->v, x->q_norm, x->k_norm, x->cos_sin, x->q_out};
+    for (const void* p : vec)
+        if (!sv::aligned16(p))
+            return SV_ERR_INVALID_ARG;
+    const void* word[] = {x->parent, x->n_new, x->row_start, kv_len, errors};
+    for (const void* p : word)
+        if ((uintptr_t)p & 3)
+            return SV_ERR_INVALID_ARG;
+    if ((x->q && (x->q_stride * s) % 16) || (x->k_stride * s) % 16 || (x->v_stride * s) % 16)
+        return SV_ERR_INVALID_ARG;
+    if (x->q && (const void*)x->q_out == x->q && x->q_stride != (long long)x->n_heads * D)
+        return SV_ERR_INVALID_ARG;
+    if (x->n_heads > (1 << 16) || cache->n_kv_heads > (1 << 16) ||
+        (long long)x->rows * (x->n_heads + 2 * cache->n_kv_heads) > 0x3fffffffLL)
+        return SV_ERR_UNSUPPORTED;
+    a.q = x->q;
+    a.k = x->k;
+    a.v = x->v;
+    a.q_stride = x->q_stride;
+    a.k_stride = x->k_stride;
+    a.v_stride = x->v_stride;
+    a.q_norm = x->q_norm;
+    a.k_norm = x->k_norm;
+    a.cos_sin = x->cos_sin;
+    a.parent = x->parent;
+    a.n_new = x->n_new;
+    a.row_start = x->row_start;
+    a.kv_len = kv_len;
+    a.q_out = x->q_out;
+    a.err = errors;
+    a.has_q = x->q != nullptr;
+    a.has_qn = x->q_norm != nullptr;
+    a.has_kn = x->k_norm != nullptr;
+    a.has_rot = x->cos_sin != nullptr;
+    a.has_parent = x->parent != nullptr;
+    a.has_n = x->n_new != nullptr;
+    a.packed = packed;
+    a.has_err = errors != nullptr;
+    a.Hq = x->n_heads;
+    a.B = x->B;
+    a.S = x->S;
+    a.rows = x->rows;
+    a.max_positions = x->max_positions;
+    a.rot = x->rotary_dim;
+    a.interleaved = x->interleaved != 0;
+    a.eps = x->eps;
+    const bool e4m3 = cache->format == SV_KV_E4M3;
+    if (x->dtype == SV_DTYPE_BF16)
+        return sv::launched(e4m3 ? sv::launch_append<__nv_bfloat16, true>(a, stream)
+                                 : sv::launch_append<__nv_bfloat16, false>(a, stream));
+    return sv::launched(e4m3 ? sv::launch_append<float, true>(a, stream) : sv::launch_append<float, false>(a, stream));
+}
+
+size_t sv_attention_workspace_size(int32_t Nmax, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim)
+{
+    if (Nmax < 1 || Nmax > sv::kNodeMax || n_kv_heads < 1 || n_heads < n_kv_heads || n_heads % n_kv_heads ||
+        head_dim < 64 || head_dim > 256 || head_dim % 16)
+        return 0;
+    return 256;
+}
+
+sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, const int32_t* n_nodes,
+                              const int32_t* parent, const void* q, int64_t q_stride, sv_dtype dtype,
+                              int32_t n_heads, int32_t B, int32_t Nmax, float scale, void* out,
+                              uint32_t* errors, void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    sv::AttnArgs a{};
+    sv_status st = sv::check_cache(cache, B > 0, &a.c);
+    if (st != SV_OK)
+        return st;
+    if (B < 0 || Nmax < 1 || Nmax > sv::kNodeMax || n_heads < 1 || n_heads % cache->n_kv_heads ||
+        (dtype != SV_DTYPE_F32 && dtype != SV_DTYPE_BF16) || !(scale > -3e38f && scale < 3e38f))
+        return SV_ERR_INVALID_ARG;
+    if (dtype != SV_DTYPE_BF16)
+        return SV_ERR_UNSUPPORTED;
+    if (B == 0)
+        return SV_OK;
+    if (!kv_len || !q || !out || !sv::aligned16(q) || !sv::aligned16(out) || q_stride % 8 ||
+        (((uintptr_t)kv_len | (uintptr_t)n_nodes | (uintptr_t)parent | (uintptr_t)errors) & 3))
+        return SV_ERR_INVALID_ARG;
+    if ((long long)B * Nmax * n_heads > 0x3fffffffLL)
+        return SV_ERR_UNSUPPORTED;
+    if (!workspace || ((uintptr_t)workspace & 255) ||
+        workspace_bytes < sv_attention_workspace_size(Nmax, n_heads, cache->n_kv_heads, cache->head_dim))
+        return SV_ERR_NO_MEMORY;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.q_stride = q_stride;
+    a.kv_len = kv_len;
+    a.n_nodes = n_nodes;
+    a.parent = parent;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.err = errors;
+    a.has_n = n_nodes != nullptr;
+    a.has_parent = parent != nullptr;
+    a.has_err = errors != nullptr;
+    a.Hq = n_heads;
+    a.B = B;
+    a.Nmax = Nmax;
+    a.scale_log2 = scale * 1.44269504088896341f;
+    const unsigned grid = (unsigned)(B * Nmax * n_heads);
+    if (cache->format == SV_KV_E4M3)
+        sv::sv_attention_kernel<true><<<grid, 128, 0, stream>>>(a);
+    else
+        sv::sv_attention_kernel<false><<<grid, 128, 0, stream>>>(a);
+    return sv::launched(cudaGetLastError());
+}
+
+sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* kv_len, const int32_t* out_path,
+                         const int32_t* out_len, int32_t B, int32_t Nmax, int32_t* kv_len_out,
+                         uint32_t* errors, cudaStream_t stream)
+{
+    sv::CommitArgs a{};
+    sv_status st = sv::check_cache(cache, B > 0, &a.c);
+    if (st != SV_OK)
+        return st;
+    if (B < 0 || Nmax < 1 || Nmax > sv::kNodeMax)
+        return SV_ERR_INVALID_ARG;
+    if (B == 0)
+        return SV_OK;
+    if (!kv_len || !out_path || !out_len || !kv_len_out ||
+        (((uintptr_t)kv_len | (uintptr_t)out_path | (uintptr_t)out_len | (uintptr_t)kv_len_out | (uintptr_t)errors) & 3))
+        return SV_ERR_INVALID_ARG;
+    if (cache->layers > 65535)
+        return SV_ERR_UNSUPPORTED;
+    a.kv_len = kv_len;
+    a.path = out_path;
+    a.len = out_len;
+    a.kv_len_out = kv_len_out;
+    a.err = errors;
+    a.layer_rows = (long long)cache->num_pages * cache->n_kv_heads * cache->page_size;
+    a.elem = cache->format == SV_KV_E4M3 ? 1 : 2;
+    a.Nmax = Nmax;
+    a.has_err = errors != nullptr;
+    a.in_place = kv_len_out == kv_len;
+    sv::sv_commit_kernel<<<dim3((unsigned)B, (unsigned)cache->layers), 128, 0, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess)
+        return SV_ERR_CUDA;
+    if (a.in_place)
+        sv::sv_commit_len_kernel<<<(unsigned)((B + 7) / 8), 256, 0, stream>>>(a, B);
+    return sv::launched(cudaGetLastError());
+}
+
+sv_status spec_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32_t* row_start, int32_t B,
+                       int32_t rows, sv_dtype dtype, void* k_out, void* v_out, uint32_t* errors,
+                       cudaStream_t stream)
+{
+    sv::ReadArgs a{};
+    sv_status st = sv::check_cache(cache, rows > 0, &a.c);
+    if (st != SV_OK)
+        return st;
+    if (B < 0 || rows < 0 || (dtype != SV_DTYPE_F32 && dtype != SV_DTYPE_BF16))
+        return SV_ERR_INVALID_ARG;
+    if (rows == 0)
+        return SV_OK;
+    if (B < 1 || !start || !row_start || !k_out || !v_out || !sv::aligned16(k_out) || !sv::aligned16(v_out) ||
+        (((uintptr_t)start | (uintptr_t)row_start | (uintptr_t)errors) & 3))
+        return SV_ERR_INVALID_ARG;
+    if (cache->n_kv_heads > (1 << 16) || (long long)rows * cache->n_kv_heads > 0x3fffffffLL)
+        return SV_ERR_UNSUPPORTED;
+    a.start = start;
+    a.row_start = row_start;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.err = errors;
+    a.B = B;
+    a.rows = rows;
+    a.has_err = errors != nullptr;
+    const bool e4m3 = cache->format == SV_KV_E4M3;
+    if (dtype == SV_DTYPE_BF16)
+        return sv::launched(e4m3 ? sv::launch_read<__nv_bfloat16, true>(a, stream)
+                                 : sv::launch_read<__nv_bfloat16, false>(a, stream));
+    return sv::launched(e4m3 ? sv::launch_read<float, true>(a, stream) : sv::launch_read<float, false>(a, stream));
+}
+
+}  // extern "C"

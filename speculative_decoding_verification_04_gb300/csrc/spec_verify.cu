@@ -1179,7 +1179,7 @@ sv_status sv_workspace_errors(void* workspace, uint32_t* flags, cudaStream_t str
     if (cudaMemsetAsync(workspace, 0, 4, stream) != cudaSuccess)
         return SV_ERR_CUDA;
     *flags = v;
-    return (v & sv::kErrWaitTimeout) ? SV_ERR_TIMEOUT : (v & sv::kErrHint) ? SV_ERR_INVALID_ARG : SV_OK;
+    return (v & sv::kErrWaitTimeout) ? SV_ERR_TIMEOUT : (v & (sv::kErrHint | sv::kErrCache)) ? SV_ERR_INVALID_ARG : SV_OK;
 }
 
 size_t sv_host_staging_size(int32_t B, int32_t Kmax, int32_t V, sv_dtype dtype)

@@ -34,8 +34,9 @@ enum : int {
 };
 
 // bit 0: a bounded wait gave up; bit 1: a sequence the caller's temperature
-// hint called greedy has a nonzero device temperature (its outputs are -1)
-enum : uint32_t { kErrWaitTimeout = 1u, kErrHint = 2u };
+// hint called greedy has a nonzero device temperature (its outputs are -1);
+// bit 2: unusable cache metadata (lengths, pages, trees, positions)
+enum : uint32_t { kErrWaitTimeout = 1u, kErrHint = 2u, kErrCache = 4u };
 
 struct Args {
     const void* tgt;
