@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/specverify.h"
 #include "sv_attention.cuh"
@@ -85,6 +86,114 @@ cudaError_t launch_read(ReadArgs& a, cudaStream_t st)
     const long long warps = (long long)a.rows * a.wpt;
     sv_read_kernel<T, E4M3><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a);
     return cudaGetLastError();
+}
+
+// --- attention -------------------------------------------------------------
+constexpr int kSmemMax = 232448;   // dynamic shared memory a CTA may have
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor map encoder (the library does not link the driver).
+EncodeTiled tensor_map_encoder()
+{
+    static std::atomic<void*> found{nullptr};
+    void* f = found.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            return nullptr;
+        found.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+}
+
+// Rows of one tensor of the cache: [num_pages * Hkv * page_size][head_dim].
+bool cache_map(CUtensorMap* m, void* base, const AttnArgs& a, bool e4m3)
+{
+    const EncodeTiled encode = tensor_map_encoder();
+    if (!encode)
+        return false;
+    const int elem = e4m3 ? 1 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.c.D, ((cuuint64_t)a.c.num_pages * a.c.Hkv) << a.c.page_shift};
+    const cuuint64_t strides[1] = {(cuuint64_t)a.c.D * elem};
+    const cuuint32_t box[2] = {(cuuint32_t)(e4m3 ? a.raw_pitch : 64), (cuuint32_t)a.box_rows}, ones[2] = {1, 1};
+    return encode(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  !e4m3 || a.raw_swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How the rows of a key head are spread: groups of at most kRowsMax rows, the
+// two softmax warpgroups' halves of a group.
+void attention_rows(int Nmax, int G, int* groups, int* rows)
+{
+    const int all = Nmax * G;
+    *groups = (all + kRowsMax - 1) / kRowsMax;
+    *rows = (all + *groups - 1) / *groups;
+}
+
+size_t attention_part_bytes(int rows, int D) { return (size_t)2 * kAttnMaxCtas * rows * (D + 2) * 4; }
+
+template <int NT, bool E4M3>
+cudaError_t launch_attention(AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int nsm, cudaStream_t st)
+{
+    const int nwg = a.rows > 16 ? 2 : 1;
+    const int fixed = (int)sizeof(AttnShared) + nwg * (kHalfBytes + NT * 128 * ((a.c.D + 63) / 64));
+    int room = kSmemMax - fixed;
+    const int operand = a.c.D <= 64 ? kHalfBytes : 2 * kHalfBytes;   // a bf16 chunk of 128 columns
+    if (E4M3) {
+        a.conv = 3;
+        a.conv_bytes = operand;
+        a.slot_bytes = kTile * a.raw_pitch;
+        room -= a.conv * a.conv_bytes;
+    } else {
+        a.conv = a.conv_bytes = 0;
+        a.slot_bytes = operand;
+    }
+    a.slots = std::min(kMaxSlots, room / a.slot_bytes);
+    const int smem = fixed + a.slots * a.slot_bytes + a.conv * a.conv_bytes;
+    static std::atomic<unsigned long long> ready{0};   // devices whose limit has been raised
+    if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute(sv_attention_kernel<NT, E4M3>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    const int ctas = std::min(nsm, kAttnMaxCtas);
+    sv_attention_kernel<NT, E4M3><<<ctas, E4M3 ? 448 : 320, smem, st>>>(a, mk, mv);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    // a page table of one tile: no item can be cut
+    if (((long long)a.c.max_pages << a.c.page_shift) <= kTile)
+        return cudaSuccess;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((a.rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sv_attention_combine, a, ctas);
+}
+
+template <bool E4M3>
+cudaError_t launch_attention_rows(AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int nsm, cudaStream_t st)
+{
+    a.half = a.rows > 16 ? (a.rows + 1) / 2 : a.rows;
+    switch ((a.half + 15) / 16) {
+    case 1: return launch_attention<16, E4M3>(a, mk, mv, dev, nsm, st);
+    case 2: return launch_attention<32, E4M3>(a, mk, mv, dev, nsm, st);
+    case 3: return launch_attention<48, E4M3>(a, mk, mv, dev, nsm, st);
+    default: return launch_attention<64, E4M3>(a, mk, mv, dev, nsm, st);
+    }
 }
 
 }  // namespace
@@ -173,7 +282,9 @@ size_t sv_attention_workspace_size(int32_t Nmax, int32_t n_heads, int32_t n_kv_h
     if (Nmax < 1 || Nmax > sv::kNodeMax || n_kv_heads < 1 || n_heads < n_kv_heads || n_heads % n_kv_heads ||
         head_dim < 64 || head_dim > 256 || head_dim % 16)
         return 0;
-    return 256;
+    int groups, rows;
+    sv::attention_rows(Nmax, n_heads / n_kv_heads, &groups, &rows);
+    return (sv::kAttnMaxCtas * 8 + sv::attention_part_bytes(rows, head_dim) + 255) / 256 * 256;
 }
 
 sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, const int32_t* n_nodes,
@@ -214,12 +325,27 @@ sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, c
     a.B = B;
     a.Nmax = Nmax;
     a.scale_log2 = scale * 1.44269504088896341f;
-    const unsigned grid = (unsigned)(B * Nmax * n_heads);
-    if (cache->format == SV_KV_E4M3)
-        sv::sv_attention_kernel<true><<<grid, 128, 0, stream>>>(a);
-    else
-        sv::sv_attention_kernel<false><<<grid, 128, 0, stream>>>(a);
-    return sv::launched(cudaGetLastError());
+    a.G = n_heads / cache->n_kv_heads;
+    sv::attention_rows(Nmax, a.G, &a.groups, &a.rows);
+    const bool e4m3 = cache->format == SV_KV_E4M3;
+    a.nd = cache->head_dim > 128 ? 2 : 1;
+    a.box_rows = std::min(cache->page_size, sv::kTile);
+    a.raw_pitch = std::min(cache->head_dim, 128);
+    a.raw_swizzled = cache->head_dim >= 128;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    a.part_o = reinterpret_cast<float*>(ws);
+    ws += (size_t)2 * sv::kAttnMaxCtas * a.rows * cache->head_dim * 4;
+    a.part_ml = reinterpret_cast<float*>(ws);
+    ws += (size_t)2 * sv::kAttnMaxCtas * a.rows * 2 * 4;
+    a.meta = reinterpret_cast<int*>(ws);
+    int dev = 0, nsm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return SV_ERR_CUDA;
+    CUtensorMap mk, mv;
+    if (!sv::cache_map(&mk, a.c.k, a, e4m3) || !sv::cache_map(&mv, a.c.v, a, e4m3))
+        return SV_ERR_CUDA;
+    return sv::launched(e4m3 ? sv::launch_attention_rows<true>(a, mk, mv, dev, nsm, stream)
+                             : sv::launch_attention_rows<false>(a, mk, mv, dev, nsm, stream));
 }
 
 sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* kv_len, const int32_t* out_path,

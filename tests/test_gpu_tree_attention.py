@@ -194,6 +194,30 @@ def test_infinite_and_nan_entries_reach_only_their_rows(dev, fmt):
     assert torch.equal(got[~hit], ref[~hit])
 
 
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "e4m3_scale"])
+def test_values_of_a_node_reach_only_its_descendants(dev, fmt, what):
+    """A node's values that are not finite make the rows that see it NaN; the
+    other rows of the tree keep every bit."""
+    ctx, N = [250, 31], 7          # the first tree straddles two tiles
+    q, cache, nodes, parents = make(ctx, N, "binary", 4, 2, 128, fmt[:4], 16, dev, seed=14)
+    ref = call(q, cache, ctx, nodes, parents, dev)
+    for b, node in ((0, 1), (0, 6), (1, 5)):
+        page, slot = cache.at(b, [ctx[b] + node])
+        if fmt == "bf16":
+            cache.v[page, 0, slot, 77] = what
+        elif fmt == "e4m3":
+            cache.v.view(torch.uint8)[page, 0, slot, 77] = 0xff
+        else:
+            cache.v_scale[page, 0, slot] = what
+    got = call(q, cache, ctx, nodes, parents, dev)
+    hit = torch.zeros(got.shape, dtype=torch.bool, device=dev)
+    for b, n in ((0, 1), (0, 3), (0, 4), (0, 6), (1, 5)):
+        hit[b, n, :2] = True
+    assert got[hit].isnan().all()
+    assert torch.equal(got[~hit], ref[~hit])
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_unusable_sequences_are_reported_and_isolated(dev, fmt):
     ctx, N = [150, 300, 90, 40, 260, 33, 20], 6
