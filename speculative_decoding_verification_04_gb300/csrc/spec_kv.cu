@@ -119,53 +119,60 @@ bool cache_map(CUtensorMap* m, void* base, const AttnArgs& a, bool e4m3)
     const int elem = e4m3 ? 1 : 2;
     const cuuint64_t dims[2] = {(cuuint64_t)a.c.D, ((cuuint64_t)a.c.num_pages * a.c.Hkv) << a.c.page_shift};
     const cuuint64_t strides[1] = {(cuuint64_t)a.c.D * elem};
-    const cuuint32_t box[2] = {(cuuint32_t)(e4m3 ? a.raw_pitch : 64), (cuuint32_t)a.box_rows}, ones[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)(e4m3 ? 128 : 64), (cuuint32_t)a.box_rows}, ones[2] = {1, 1};
     return encode(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
                   box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  !e4m3 || a.raw_swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How the rows of a key head are spread: groups of at most kRowsMax rows, the
-// two softmax warpgroups' halves of a group.
-void attention_rows(int Nmax, int G, int* groups, int* rows)
+// How the rows of a key head are spread: groups of at most `most` rows.
+void attention_rows(int Nmax, int G, int most, int* groups, int* rows)
 {
     const int all = Nmax * G;
-    *groups = (all + kRowsMax - 1) / kRowsMax;
+    *groups = (all + most - 1) / most;
     *rows = (all + *groups - 1) / *groups;
 }
 
 size_t attention_part_bytes(int rows, int D) { return (size_t)2 * kAttnMaxCtas * rows * (D + 2) * 4; }
 
-template <int NT, bool E4M3>
+template <int NT, int NWG, bool E4M3>
 cudaError_t launch_attention(AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int nsm, cudaStream_t st)
 {
-    const int nwg = a.rows > 16 ? 2 : 1;
-    const int fixed = (int)sizeof(AttnShared) + nwg * (kHalfBytes + NT * 128 * ((a.c.D + 63) / 64));
+    constexpr int N = NT * NWG;
+    const int q_bytes = E4M3 ? 3 * N * 128 * a.nd : N * 128 * ((a.c.D + 63) / 64);
+    const int fixed = (int)sizeof(AttnShared) + (N + 63) / 64 * kHalfBytes + q_bytes;
     int room = kSmemMax - fixed;
     const int operand = a.c.D <= 64 ? kHalfBytes : 2 * kHalfBytes;   // a bf16 chunk of 128 columns
     if (E4M3) {
-        a.conv = 3;
+        a.conv = 2;
         a.conv_bytes = operand;
-        a.slot_bytes = kTile * a.raw_pitch;
+        a.k_bytes = a.v_bytes = kHalfBytes;
         room -= a.conv * a.conv_bytes;
     } else {
         a.conv = a.conv_bytes = 0;
-        a.slot_bytes = operand;
+        a.k_bytes = a.v_bytes = operand;
     }
-    a.slots = std::min(kMaxSlots, room / a.slot_bytes);
-    const int smem = fixed + a.slots * a.slot_bytes + a.conv * a.conv_bytes;
+    const int slots = std::min(2 * kMaxSlots, room / a.k_bytes);
+    a.kslots = slots / 2;
+    a.vslots = slots - a.kslots;
+    const int smem = fixed + slots * a.k_bytes + a.conv * a.conv_bytes;
     static std::atomic<unsigned long long> ready{0};   // devices whose limit has been raised
     if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
-        const cudaError_t e = cudaFuncSetAttribute(sv_attention_kernel<NT, E4M3>,
+        const cudaError_t e = cudaFuncSetAttribute(sv_attention_kernel<NT, NWG, E4M3>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
         if (e != cudaSuccess)
             return e;
+        // the warpgroups share out what the block is launched with: with fewer registers they would wait for ever
+        cudaFuncAttributes fa;
+        const cudaError_t e2 = cudaFuncGetAttributes(&fa, sv_attention_kernel<NT, NWG, E4M3>);
+        if (e2 != cudaSuccess || fa.numRegs != kAttnRegs<E4M3>)
+            return e2 != cudaSuccess ? e2 : cudaErrorInvalidConfiguration;
         if (dev < 64)
             ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     const int ctas = std::min(nsm, kAttnMaxCtas);
-    sv_attention_kernel<NT, E4M3><<<ctas, E4M3 ? 448 : 320, smem, st>>>(a, mk, mv);
+    sv_attention_kernel<NT, NWG, E4M3><<<ctas, attn_threads(E4M3), smem, st>>>(a, mk, mv);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
@@ -188,11 +195,13 @@ template <bool E4M3>
 cudaError_t launch_attention_rows(AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int nsm, cudaStream_t st)
 {
     a.half = a.rows > 16 ? (a.rows + 1) / 2 : a.rows;
+    if (a.rows <= 16)
+        return launch_attention<16, 1, E4M3>(a, mk, mv, dev, nsm, st);
     switch ((a.half + 15) / 16) {
-    case 1: return launch_attention<16, E4M3>(a, mk, mv, dev, nsm, st);
-    case 2: return launch_attention<32, E4M3>(a, mk, mv, dev, nsm, st);
-    case 3: return launch_attention<48, E4M3>(a, mk, mv, dev, nsm, st);
-    default: return launch_attention<64, E4M3>(a, mk, mv, dev, nsm, st);
+    case 1: return launch_attention<16, 2, E4M3>(a, mk, mv, dev, nsm, st);
+    case 2: return launch_attention<32, 2, E4M3>(a, mk, mv, dev, nsm, st);
+    case 3: return launch_attention<48, 2, E4M3>(a, mk, mv, dev, nsm, st);
+    default: return launch_attention<64, 2, E4M3>(a, mk, mv, dev, nsm, st);
     }
 }
 
@@ -283,7 +292,7 @@ size_t sv_attention_workspace_size(int32_t Nmax, int32_t n_heads, int32_t n_kv_h
         head_dim < 64 || head_dim > 256 || head_dim % 16)
         return 0;
     int groups, rows;
-    sv::attention_rows(Nmax, n_heads / n_kv_heads, &groups, &rows);
+    sv::attention_rows(Nmax, n_heads / n_kv_heads, sv::attn_rows_max(false, head_dim), &groups, &rows);   // never fewer rows
     return (sv::kAttnMaxCtas * 8 + sv::attention_part_bytes(rows, head_dim) + 255) / 256 * 256;
 }
 
@@ -326,12 +335,10 @@ sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, c
     a.Nmax = Nmax;
     a.scale_log2 = scale * 1.44269504088896341f;
     a.G = n_heads / cache->n_kv_heads;
-    sv::attention_rows(Nmax, a.G, &a.groups, &a.rows);
     const bool e4m3 = cache->format == SV_KV_E4M3;
+    sv::attention_rows(Nmax, a.G, sv::attn_rows_max(e4m3, cache->head_dim), &a.groups, &a.rows);
     a.nd = cache->head_dim > 128 ? 2 : 1;
     a.box_rows = std::min(cache->page_size, sv::kTile);
-    a.raw_pitch = std::min(cache->head_dim, 128);
-    a.raw_swizzled = cache->head_dim >= 128;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     a.part_o = reinterpret_cast<float*>(ws);
     ws += (size_t)2 * sv::kAttnMaxCtas * a.rows * cache->head_dim * 4;

@@ -8,13 +8,21 @@
 // long side on the tensor core's 128 lanes:
 //   S^T [128 positions x rows] = K_tile Q^T        (K and Q as they lie)
 //   O^T [head_dim x rows]     += V_tile^T P^T      (V and P with positions as k)
-// A thread of the softmax then owns one position of a tile and every row: the
-// e4m3 cache's scales are one multiplier a thread, the exponentials cost what
-// the rows cost (no padding to 128), and the tree mask is one bit a row.  The
-// price is that a row's maximum runs across threads; it is kept lazily: the
-// weights are relative to a running reference that moves only when some score
-// exceeds it by more than 2^8 (a vote a tile), so the cross-thread maximum and
-// the rescaling of O are rare.
+// A thread of the softmax then owns one position of a tile and half of the
+// rows: the e4m3 cache's scales are one multiplier a thread, the exponentials
+// cost what the rows cost (no padding to 128), and the tree mask is one bit a
+// row.  The price is that a row's maximum runs across threads, so it is not
+// kept: weights are exp2(score - reference) with a reference a row that starts
+// at zero and moves only when a score is above it by more than kLazy, or the
+// first scores are all below it by more (a vote a tile).  fp32 sums and bf16
+// weights keep their relative precision at any such distance, so this is the
+// softmax's value to rounding.
+//
+// An e4m3 cache's keys go to the tensor core as they are: each query element
+// is split into an e4m3 and two e5m2 terms, which hold a bf16's eight bits
+// exactly (to 2^-25 of the row group's largest element), and the three
+// products add up in the same accumulator.  Its values become bf16 in shared
+// memory, because the weights need more range than two or three 8-bit terms.
 //
 // Work is (sequence, key head, row group) items of 128-position tiles, laid
 // end to end and cut into equal runs, one to a CTA.  An item cut by a run's
@@ -28,10 +36,12 @@ namespace sv {
 
 constexpr int kAttnMaxCtas = 160;
 constexpr int kTile = 128;                 // positions a tile
-constexpr int kRowsMax = 128;              // query rows a CTA
-constexpr int kHalfBytes = kTile * 128;    // 128 rows of 64 bf16 elements
-constexpr float kLazy = 8.0f;              // log2 of the largest weight before the reference moves
-constexpr int kMaxSlots = 12, kMaxConv = 4;
+// Query rows a CTA: 128, but 64 where the three 8-bit terms of wider heads'
+// queries would leave the loads no room.
+__host__ __device__ constexpr int attn_rows_max(bool e4m3, int D) { return e4m3 && D > 128 ? 64 : 128; }
+constexpr int kHalfBytes = kTile * 128;    // 128 swizzled rows of 128 bytes
+constexpr float kLazy = 32.0f;             // log2 of how far a weight may lie from one
+constexpr int kMaxSlots = 8;
 
 struct AttnArgs {
     KvCache c;
@@ -50,10 +60,9 @@ struct AttnArgs {
     int groups, rows;        // row groups of a key head; rows of one group
     int half;                // rows of the first warpgroup (the second has the rest)
     int nd;                  // 128-wide chunks of head_dim
-    int slots, conv;         // ring sizes
-    int slot_bytes, conv_bytes;
+    int kslots, vslots, conv;         // ring sizes
+    int k_bytes, v_bytes, conv_bytes; // of one slot
     int box_rows;            // rows of one TMA box (a page, or a tile)
-    int raw_pitch, raw_swizzled;
     float scale_log2;        // scale * log2(e)
 };
 
@@ -104,20 +113,69 @@ struct Run {
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == s.tiles; }
 };
 
+// The order in which a part's operands are loaded and multiplied: K(0), then
+// K(j + 1) and V(j) for every tile j, so that the next scores are on their way
+// while the softmax works.  Step s of 2 n: is it a K, and of which tile.
+__device__ __forceinline__ bool step_is_k(int s, int n) { return s == 0 || ((s & 1) && s < 2 * n - 1); }
+__device__ __forceinline__ int step_tile(int s, int n)
+{
+    return s == 0 ? 0 : step_is_k(s, n) ? (s + 1) >> 1 : s == 2 * n - 1 ? n - 1 : (s >> 1) - 1;
+}
+
 struct AttnShared {
-    uint64_t full[kMaxSlots], empty[kMaxSlots];    // TMA slots
-    uint64_t cfull[kMaxConv], cempty[kMaxConv];    // converted slots (e4m3)
-    uint64_t q_full[2], s_full[2][2], s_empty[2][2], p_full[2], o_full[2];
-    uint64_t drain;
+    uint64_t kfull[kMaxSlots], kempty[kMaxSlots];  // K slots
+    uint64_t vfull[kMaxSlots], vempty[kMaxSlots];  // V slots
+    uint64_t cfull[2], cempty[2];                  // converted V slots (e4m3)
+    uint64_t q_full, s_full[2], s_empty[2], p_full, o_full, drain;
+    long long t_begin, t_end, sum[16];
     uint32_t tmem;
     int abort;
-    long long t_begin, t_end, sum[14];
     int b, hg, tile, active;
     unsigned poison[2];
     int unset[2];
+    float top[2][4];
     alignas(16) float negm[2][64];                 // minus the rows' references
+    float scratch[2][5 * 64];
     unsigned anc[2][64];                           // the rows' ancestor bits
+    int row_out[2][64];                            // where the rows' results go (-1: nowhere)
 };
+
+// The dynamic shared memory.  Every role derives its own pointers (through a
+// zero the compiler does not see): shared ones would hold registers in all of
+// them, and the roles have few.
+struct AttnLayout {
+    unsigned char *k, *v, *c, *p, *q;   // K, V, converted V slots; P; Q (bf16, or three 8-bit terms)
+    AttnShared* sh;
+    int q_part;                         // bytes of one 8-bit term of Q
+};
+
+template <int N, bool E4M3>
+__device__ __forceinline__ AttnLayout attn_layout(const AttnArgs& a, unsigned char* smem)
+{
+    int zero;
+    asm volatile("mov.u32 %0, 0;" : "=r"(zero));
+    AttnLayout L;
+    L.k = smem + zero;
+    L.v = L.k + a.kslots * a.k_bytes;
+    L.c = L.v + a.vslots * a.v_bytes;
+    L.p = L.c + (E4M3 ? a.conv * a.conv_bytes : 0);
+    L.q = L.p + (N + 63) / 64 * kHalfBytes;
+    L.q_part = N * 128 * a.nd;
+    L.sh = reinterpret_cast<AttnShared*>(L.q + (E4M3 ? 3 * L.q_part : N * 128 * ((a.c.D + 63) / 64)));
+    return L;
+}
+
+__device__ __forceinline__ Run run_of(const AttnArgs& a, const AttnShared& shared)
+{
+    const volatile AttnShared& sh = shared;
+    Run r;
+    r.left = sh.active ? sh.t_end - sh.t_begin : 0;
+    r.b = sh.active ? sh.b : 0;
+    r.hg = sh.hg;
+    r.tile = sh.tile;
+    r.s = seq_lens(a, r.b);
+    return r;
+}
 
 // A wait that ends: on a timeout every later wait of the CTA gives up too.
 // The warps that own named barriers run on regardless (they all reach the
@@ -146,27 +204,35 @@ struct Ring {
             phase ^= 1;
         }
     }
+    __device__ __forceinline__ void back(int n)
+    {
+        if (slot == 0) {
+            slot = n;
+            phase ^= 1;
+        }
+        --slot;
+    }
 };
 
-// e4m3 bytes to bf16, exactly: the eight bits' exponent and mantissa fields
-// land in the bf16's low exponent and high mantissa bits, which is the value
-// times 2^-120 (subnormals included); one multiplication restores it.
-__device__ __forceinline__ uint32_t bf16x2_scale(uint32_t x)
+// Four e4m3 values (bytes 0 .. 3 of w) as four bf16, in the order 0, 2, 1, 3,
+// exactly: the eight bits' exponent and mantissa fields land in the bf16's low
+// exponent and high mantissa bits, which is the value times 2^-120 (subnormals
+// included); one multiplication restores it.
+__device__ __forceinline__ uint32_t bf16x2_restore(uint32_t x)
 {
     uint32_t y;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7b807b80u));   // 2^120
     return y;
 }
 
-// Four e4m3 values as four bf16 in order.
 __device__ __forceinline__ uint2 e4m3_to_bf16(uint32_t w)
 {
-    // bytes 0 and 2 / 1 and 3 in the high bytes of 16-bit lanes
-    const uint32_t e = w << 8, s = 0x80008000u, m = 0x07f007f0u;
-    const uint32_t even = bf16x2_scale((e & s) | ((e & 0x7f007f00u) >> 4));   // v0, v2
-    const uint32_t odd = bf16x2_scale((w & s) | ((w >> 4) & m));              // v1, v3
-    return make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
+    constexpr uint32_t s = 0x80008000u, m = 0x07f007f0u;
+    return make_uint2(bf16x2_restore(((w << 8) & s) | ((w << 4) & m)), bf16x2_restore((w & s) | ((w >> 4) & m)));
 }
+
+// The head_dim element at a lane of the converted values' order.
+__device__ __forceinline__ int converted_element(int lane) { return (lane & ~3) | ((lane & 1) << 1) | ((lane >> 1) & 1); }
 
 __device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w)
 {
@@ -185,8 +251,8 @@ __device__ __forceinline__ bool chunk_nan_e4m3(uint4 w)
 __device__ __noinline__ uint2 e4m3_keep_nan(uint32_t w, uint2 y)
 {
     const uint32_t m = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    y.x |= ((m >> 7) & 1u) * 0x7fffu | ((m >> 15) & 1u) * 0x7fff0000u;
-    y.y |= ((m >> 23) & 1u) * 0x7fffu | (m >> 31) * 0x7fff0000u;
+    y.x |= ((m >> 7) & 1u) * 0x7fffu | ((m >> 23) & 1u) * 0x7fff0000u;
+    y.y |= ((m >> 15) & 1u) * 0x7fffu | (m >> 31) * 0x7fff0000u;
     return y;
 }
 
@@ -196,59 +262,248 @@ __device__ __forceinline__ bool chunk_nonfinite(uint4 w, bool e4m3)
                 : bf16_pair_nonfinite(w.x) || bf16_pair_nonfinite(w.y) || bf16_pair_nonfinite(w.z) || bf16_pair_nonfinite(w.w);
 }
 
-// NT: rows (TMEM columns) a softmax warpgroup handles; E4M3: four more warps
-// convert the cache's bytes to bf16 operands.
-template <int NT, bool E4M3>
-__global__ void __launch_bounds__(E4M3 ? 448 : 320, 1)
+// A query element (scaled so that the group's largest is below 256) as an
+// e4m3 and two e5m2 terms; what is not finite becomes NaN.
+__device__ __forceinline__ void split_q(float x, uint32_t& h, uint32_t& m, uint32_t& l)
+{
+    h = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+    float r = x - __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)h, __NV_E4M3)));
+    m = __nv_cvt_float_to_fp8(r, __NV_SATFINITE, __NV_E5M2);
+    r -= __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)m, __NV_E5M2)));
+    l = __nv_cvt_float_to_fp8(r, __NV_SATFINITE, __NV_E5M2);
+    if (!isfinite(x)) {
+        h = 0x7f;
+        m = l = 0;
+    }
+}
+
+// One lane: the products of a K slot (bf16, or e4m3 with the three terms of
+// Q).  `steps`: 32-byte steps of the contraction in this slot.  Descriptors
+// differ by constants in their low words.
+template <int N, bool E4M3>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t k, uint32_t q, uint32_t q_part, int steps, bool add)
+{
+    const uint32_t ka = tc_desc_lo(k, 16), qb = tc_desc_lo(q, 16);
+    if (E4M3) {
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            const uint32_t id = tc_idesc(128, N, 0, p > 0, false, false), qp = qb + p * (q_part >> 4);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (s < steps)
+                    tc_mma_f8(d, tc_desc(ka + 2 * s), tc_desc(qp + 2 * s), id, add || p + s > 0);
+        }
+    } else {
+        constexpr uint32_t id = tc_idesc(128, N, 1, 1, false, false);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            if (s < steps)
+                tc_mma_bf16(d, tc_desc(ka + (s >> 2) * (kHalfBytes / 16) + (s & 3) * 2),
+                            tc_desc(qb + (s >> 2) * (N * 128 / 16) + (s & 3) * 2), id, add || s > 0);
+    }
+}
+
+// One lane: a V slot (bf16 operands) times P.  `steps`: 16-position steps.
+template <int N>
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t v, uint32_t p, uint32_t lbo, int steps, bool add)
+{
+    constexpr uint32_t id = tc_idesc(128, N, 1, 1, true, true);
+    const uint32_t va = tc_desc_lo(v, lbo), pb = tc_desc_lo(p, kHalfBytes);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        if (s < steps)
+            tc_mma_bf16(d, tc_desc(va + s * (2048 / 16)), tc_desc(pb + s * (2048 / 16)), id, add || s > 0);
+}
+
+// The rare step of the softmax, by the warpgroup's 128 threads: rows whose
+// scores lie too far from their references get new ones (their maxima over
+// this tile), and the sums in TMEM are rescaled.  scratch[0 .. NT) then holds
+// the factors of what was summed so far.
+template <int NT>
+__device__ __forceinline__ void move_references(float* scratch, float* negm, int* unset_flag, uint32_t s_at, uint32_t o_at,
+                                                int o_chunks, int o_pitch, float mult, unsigned long long seen, int t, int bar)
+{
+    const int lane = t & 31, warp = t >> 5;
+#pragma unroll 1
+    for (int c = 0; c < NT; c += 16) {
+        float s[16], keep = 0.0f;
+        tmem_ld16(s_at + c, s);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float x = warp_redux_max((seen >> (c + k)) & 1 ? fmaf(s[k], mult, negm[c + k]) : -INFINITY);
+            keep = lane == k ? x : keep;
+        }
+        if (lane < 16)
+            scratch[warp * NT + c + lane] = keep;
+    }
+    bar_sync(bar, 128);
+    bool unset = false;
+    if (t < NT) {
+        const float x = fmaxf(fmaxf(scratch[t], scratch[NT + t]), fmaxf(scratch[2 * NT + t], scratch[3 * NT + t]));
+        float f = 1.0f, delta = 0.0f;
+        // +0 marks a row that has no reference yet: nothing is in its sums
+        const float old = negm[t];
+        if (__float_as_uint(old) == 0u) {
+            unset = x == -INFINITY;
+            delta = unset ? 0.0f : x;
+        } else if (x > 0.0f) {
+            delta = x;
+            f = ex2_approx(-x);
+        }
+        if (!unset) {
+            const float now = old - delta;
+            negm[t] = __float_as_uint(now) == 0u ? -0.0f : now;
+        }
+        scratch[t] = f;
+    }
+    unset = bar_any(bar, 128, unset);
+    if (t == 0)
+        *unset_flag = unset;
+#pragma unroll 1
+    for (int i = 0; i < o_chunks; ++i)
+#pragma unroll 1
+        for (int c = 0; c < NT; c += 16) {
+            float o[16];
+            tmem_ld16(o_at + i * o_pitch + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                o[k] *= scratch[c + k];
+            tmem_st16(o_at + i * o_pitch + c, o);
+        }
+    tmem_wait_st();
+}
+
+// C of a position's scores, in powers of two relative to the rows' references;
+// -infinity where the row does not see the position.
+template <int C>
+__device__ __forceinline__ void load_scores(uint32_t at, const float* negm, float mult, bool masked, unsigned long long seen, float (&s)[C])
+{
+#pragma unroll
+    for (int i = 0; i < C / 16; ++i)
+        tmem_ld16(at + 16 * i, s + 16 * i);
+    tmem_wait_ld();
+    const uint64_t m2 = f2_pack(mult, mult);
+    const ulonglong2* nm = reinterpret_cast<const ulonglong2*>(negm);
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) {
+        const ulonglong2 x = nm[i];
+        f2_unpack(f2_fma(f2_pack(s[4 * i], s[4 * i + 1]), m2, x.x), s[4 * i], s[4 * i + 1]);
+        f2_unpack(f2_fma(f2_pack(s[4 * i + 2], s[4 * i + 3]), m2, x.y), s[4 * i + 2], s[4 * i + 3]);
+    }
+    if (masked) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            s[i] = (seen >> i) & 1 ? s[i] : -INFINITY;
+    }
+}
+
+// What a row group's start needs besides Q: the rows' ancestors and places,
+// and which nodes' values are not finite (the rows that see them end as NaN;
+// the others must not meet them, see the products).  Returns whether the tree
+// is malformed.
+template <bool E4M3>
+__device__ __forceinline__ bool begin_rows(const AttnArgs& a, AttnShared& sh, const Run& run, int h, int g, int part, int w, int NT, int t)
+{
+    const int lane = t & 31, bar = 1 + w, nn = run.s.nn, ctx = run.s.ctx;
+    const int mine = w == 0 ? min(a.half, a.rows) : a.rows - a.half, first = g * a.rows + w * a.half;
+    int par;
+    const bool bad = !tree_parents(a.parent + (long long)run.b * a.Nmax, a.has_parent, nn, lane, par);
+    if (t < 64) {
+        const int rr = first + t, node = rr / a.G;
+        int at = t < mine && rr < nn * a.G && !bad ? node : -1;
+        unsigned anc = 0;
+        for (int d = 0; d < kNodeMax && __any_sync(kFull, at >= 0); ++d) {
+            if (at >= 0)
+                anc |= 1u << at;
+            const int up = __shfl_sync(kFull, par, max(at, 0));
+            at = at >= 0 ? up : -1;
+        }
+        sh.anc[w][t] = anc;
+        sh.negm[w][t] = 0.0f;
+        sh.row_out[w][t] = t >= mine || rr >= a.Nmax * a.G ? -1
+                           : run.whole()                   ? (run.b * a.Nmax + node) * a.Hq + h * a.G + rr - node * a.G
+                                                           : part * a.rows + w * a.half + t;
+    }
+    if (t == 0) {
+        sh.poison[w] = 0;
+        sh.unset[w] = 0;
+    }
+    bar_sync(bar, 128);
+    if (nn > 1 && run.t1 * kTile > ctx) {
+        const int m = t >> 2, pos = ctx + m, bytes = a.c.D * (E4M3 ? 1 : 2);
+        bool hit = false;
+        if (m < nn && pos >= run.t0 * kTile && pos < run.t1 * kTile) {
+            const int page = kv_page(a.c, run.b, pos);
+            if (page >= 0) {
+                const long long row = kv_row(a.c, page, pos) + ((long long)h << a.c.page_shift);
+                const uint4* v = reinterpret_cast<const uint4*>(a.c.v + row * bytes);
+                for (int i = t & 3; i < bytes / 16; i += 4)
+                    hit |= chunk_nonfinite(v[i], E4M3);
+                if (E4M3)
+                    hit |= !isfinite(a.c.v_scale[row]);
+            }
+        }
+        if (hit)
+            atomicOr(&sh.poison[w], 1u << m);
+        bar_sync(bar, 128);
+    }
+    return bad;
+}
+
+// Registers a thread: the softmax's warpgroups hold NT scores and NT sums a
+// thread, the others little; the shares add up to the launch's.
+__host__ __device__ constexpr int attn_threads(bool e4m3) { return e4m3 ? 512 : 384; }
+
+template <bool E4M3> constexpr int kAttnRegs = E4M3 ? 128 : 168;          // at launch
+template <bool E4M3> constexpr int kRegsSoftmax = E4M3 ? 168 : 208;       // warps 0 .. 7
+template <bool E4M3> constexpr int kRegsIssue = E4M3 ? 72 : 88;           // warps 8 .. 11
+constexpr int kRegsConvert = 104;                                         // warps 12 .. 15
+static_assert(512 * kAttnRegs<true> == 256 * kRegsSoftmax<true> + 128 * kRegsIssue<true> + 128 * kRegsConvert &&
+              384 * kAttnRegs<false> == 256 * kRegsSoftmax<false> + 128 * kRegsIssue<false>,
+              "register shares");
+
+// NT: rows (TMEM columns) a softmax warpgroup handles; NWG: softmax
+// warpgroups with rows; E4M3: four more warps make bf16 operands of V.
+template <int NT, int NWG, bool E4M3>
+__global__ void __launch_bounds__(attn_threads(E4M3), 1)
     sv_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v)
 {
-    constexpr int kThreads = E4M3 ? 448 : 320, kWarps = kThreads / 32;
+    constexpr int kThreads = attn_threads(E4M3), kWarps = kThreads / 32, N = NT * NWG;
     extern __shared__ __align__(1024) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = a.c.D;
-    const int nwg = a.rows > 16 ? 2 : 1;
-    // layout: operand slots, P, Q, the small things
-    unsigned char* s_raw = smem;                                                    // a.slots * a.slot_bytes
-    unsigned char* s_conv = s_raw + (E4M3 ? a.conv * a.conv_bytes : 0);             // e4m3: conv slots first
-    if (E4M3) {
-        unsigned char* t = s_raw;
-        s_raw = s_conv;
-        s_conv = t;
-    }
-    unsigned char* s_p = s_raw + a.slots * a.slot_bytes;
-    const int q_bytes = NT * 128 * ((D + 63) / 64);
-    unsigned char* s_q = s_p + nwg * kHalfBytes;
-    AttnShared& sh = *reinterpret_cast<AttnShared*>(s_q + nwg * q_bytes);
-
-    // --- the CTA's run of tiles --------------------------------------------
+    {
+    AttnShared& sh = *attn_layout<N, E4M3>(a, smem).sh;
     if (warp == 8) {
         tmem_alloc(smem_addr(&sh.tmem), 512);
     } else if (tid == 9 * 32) {
         sh.abort = 0;
-        for (int i = 0; i < a.slots; ++i) {
-            mbar_init(smem_addr(&sh.full[i]), 1);
-            mbar_init(smem_addr(&sh.empty[i]), E4M3 ? 4 : 1);
+        for (int i = 0; i < a.kslots; ++i) {
+            mbar_init(smem_addr(&sh.kfull[i]), 1);
+            mbar_init(smem_addr(&sh.kempty[i]), 1);
         }
-        for (int i = 0; i < a.conv; ++i) {
+        for (int i = 0; i < a.vslots; ++i) {
+            mbar_init(smem_addr(&sh.vfull[i]), 1);
+            mbar_init(smem_addr(&sh.vempty[i]), E4M3 ? 4 : 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.cfull[i]), 4);
             mbar_init(smem_addr(&sh.cempty[i]), 1);
+            mbar_init(smem_addr(&sh.s_full[i]), 1);
+            mbar_init(smem_addr(&sh.s_empty[i]), 4 * NWG);
         }
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(smem_addr(&sh.q_full[w]), 4);
-            mbar_init(smem_addr(&sh.p_full[w]), 4);
-            mbar_init(smem_addr(&sh.o_full[w]), 1);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(smem_addr(&sh.s_full[w][i]), 1);
-                mbar_init(smem_addr(&sh.s_empty[w][i]), 4);
-            }
-        }
+        mbar_init(smem_addr(&sh.q_full), 4 * NWG);
+        mbar_init(smem_addr(&sh.p_full), 4 * NWG);
+        mbar_init(smem_addr(&sh.o_full), 1);
         mbar_init(smem_addr(&sh.drain), 1);
         fence_mbar_init();
         tma_prefetch_map(&map_k);
         tma_prefetch_map(&map_v);
     }
     {
-        // tiles of all sequences before each thread's share of them
+        // the CTA's run: tiles of all sequences before each thread's share of them
         const int share = (a.B + kThreads - 1) / kThreads, b0 = min(tid * share, a.B), b1 = min(b0 + share, a.B);
         const int per = a.c.Hkv * a.groups;
         long long mine = 0;
@@ -297,257 +552,30 @@ __global__ void __launch_bounds__(E4M3 ? 448 : 320, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
-    Run run;
-    run.left = 0;
-    run.tile = 0;
-    run.s.tiles = -1;
-    if (sh.active) {
-        run.left = sh.t_end - sh.t_begin;
-        run.b = sh.b;
-        run.hg = sh.hg;
-        run.tile = sh.tile;
-        run.s = seq_lens(a, run.b);
     }
-    const uint32_t ring_full = smem_addr(sh.full), ring_empty = smem_addr(sh.empty);
-
-    if (warp == 9) {
-        // --- TMA producer ----------------------------------------------------
-        // Slots are filled in the order the products take them: K(0), then
-        // K(j + 1), V(j) for every tile j.
-        Ring r;
-        int issued = 0;
-        const int boxes = kTile / a.box_rows;
-        bool go = true;
-        while (go && run.next(a)) {
-            if (run.s.len == 0)
-                continue;
-            const int h = run.hg / a.groups;
-            for (int step = 0; go && step < 2 * (run.t1 - run.t0); ++step) {
-                // steps: K0, K1, V0, K2, V1, ..., K(n-1), V(n-2), V(n-1)
-                const int n = run.t1 - run.t0;
-                const bool is_k = step == 0 || ((step & 1) && (step + 1) / 2 < n);
-                const int j = run.t0 + (step == 0 ? 0 : is_k ? (step + 1) / 2 : step == 2 * n - 1 ? n - 1 : step / 2 - 1);
-                const int valid = min(kTile, run.s.len - j * kTile);
-                // lane l: the tile's box l
-                int row = -1;
-                if (lane < boxes && lane * a.box_rows < valid) {
-                    const int pos = j * kTile + lane * a.box_rows;
-                    const int page = kv_page(a.c, run.b, pos);
-                    if (page >= 0)
-                        row = (int)kv_row(a.c, page, pos) + (h << a.c.page_shift);
-                }
-                const unsigned have = __ballot_sync(kFull, row >= 0);
-                for (int c = 0; go && c < a.nd; ++c) {
-                    go = cta_wait(sh, &sh.empty[r.slot], r.phase ^ 1);
-                    if (!go)
-                        break;
-                    const uint32_t bar = ring_full + 8 * r.slot, dst = smem_addr(s_raw) + r.slot * a.slot_bytes;
-                    const int halves = E4M3 ? 1 : min(2, (D - 128 * c + 63) / 64);
-                    const int pitch = E4M3 ? a.raw_pitch : 128;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(bar, __popc(have) * a.box_rows * pitch * halves);
-                    __syncwarp();
-                    if (row >= 0)
-                        for (int x = 0; x < halves; ++x)
-                            tma_load_2d(dst + x * kHalfBytes + lane * a.box_rows * pitch, is_k ? &map_k : &map_v,
-                                        128 * c + 64 * x, row, bar);
-                    __syncwarp();
-                    r.step(a.slots);
-                    issued = min(issued + 1, a.slots);
-                }
-            }
-        }
-        // copies in flight land before the CTA's memory is given back
-        if (!go)
-            for (int i = 0; i < issued; ++i) {
-                if (r.slot == 0) {
-                    r.slot = a.slots;
-                    r.phase ^= 1;
-                }
-                --r.slot;
-                mbar_wait_bounded(ring_full + 8 * r.slot, r.phase, kWaitSpins);
-            }
-    } else if (warp == 8) {
-        // --- MMA -------------------------------------------------------------
-        Ring r;
-        uint32_t item = 0;        // items with keys so far (parity of q_full)
-        uint32_t n_tiles = 0;     // tiles so far (parity of p_full, buffer of S)
-        const int ring = E4M3 ? a.conv : a.slots;
-        uint64_t* const full = E4M3 ? sh.cfull : sh.full;
-        const uint32_t op_empty = E4M3 ? smem_addr(sh.cempty) : ring_empty;
-        const uint32_t ops = smem_addr(E4M3 ? s_conv : s_raw), op_bytes = E4M3 ? a.conv_bytes : a.slot_bytes;
-        const uint32_t q0 = smem_addr(s_q), p0 = smem_addr(s_p);
-        constexpr uint32_t kIdS = tc_idesc_bf16(128, NT, false, false), kIdO = tc_idesc_bf16(128, NT, true, true);
-        bool go = true;
-        while (go && run.next(a)) {
-            if (run.s.len == 0)
-                continue;
-            for (int w = 0; go && w < nwg; ++w)
-                go = cta_wait(sh, &sh.q_full[w], item & 1);
-            ++item;
-            const int n = run.t1 - run.t0;
-            for (int step = 0; go && step < 2 * n; ++step) {
-                const bool is_k = step == 0 || ((step & 1) && (step + 1) / 2 < n);
-                const int jj = step == 0 ? 0 : is_k ? (step + 1) / 2 : step == 2 * n - 1 ? n - 1 : step / 2 - 1;
-                const int j = run.t0 + jj;
-                const uint32_t g = n_tiles + jj;   // the CTA's tile count
-                for (int c = 0; go && c < a.nd; ++c) {
-                    go = cta_wait(sh, &full[r.slot], r.phase);
-                    if (!go)
-                        break;
-                    tc_fence_after();
-                    const uint32_t base = ops + r.slot * op_bytes;
-                    const int width = min(128, D - 128 * c);
-                    if (is_k) {
-                        for (int w = 0; go && w < nwg; ++w) {
-                            if (c == 0) {
-                                go = cta_wait(sh, &sh.s_empty[w][g & 1], ((g >> 1) & 1) ^ 1);
-                                if (!go)
-                                    break;
-                                tc_fence_after();
-                            }
-                            if (lane == 0) {
-                                const uint32_t q = q0 + w * q_bytes + 2 * c * (NT * 128), d = tmem + (2 * w + (g & 1)) * NT;
-                                for (int s = 0; s < width / 16; ++s)
-                                    tc_mma_bf16(d, tc_desc_sw128(base + (s >> 2) * kHalfBytes + (s & 3) * 32, 16, 1024),
-                                                tc_desc_sw128(q + (s >> 2) * (NT * 128) + (s & 3) * 32, 16, 1024), kIdS, c + s > 0);
-                                if (c == a.nd - 1)
-                                    tc_commit(smem_addr(&sh.s_full[w][g & 1]));
-                            }
-                        }
-                    } else {
-                        const int valid = min(kTile, run.s.len - j * kTile), ksteps = (valid + 15) / 16;
-                        if (!E4M3) {
-                            // rows behind the last position may hold anything: zeros instead of 0 * NaN.  A node's
-                            // values are seen by some rows only: what is not finite there is zeroed too (the rows
-                            // that do see it are set to NaN at the end).
-                            unsigned char* v = s_raw + r.slot * a.slot_bytes;
-                            bool wrote = false;
-                            const int chunks = width > 64 ? 16 : 8;
-                            for (int i = valid * chunks + lane; i < ksteps * 16 * chunks; i += 32) {
-                                const int row = i / chunks, ch = i % chunks;
-                                *reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
-                                wrote = true;
-                            }
-                            const int row = run.s.ctx + lane - j * kTile;
-                            if (run.s.nn > 1 && lane < run.s.nn && row >= 0 && row < kTile)
-                                for (int ch = 0; ch < chunks; ++ch) {
-                                    uint4* p = reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 + (ch & 7) * 16);
-                                    if (chunk_nonfinite(*p, false)) {
-                                        *p = make_uint4(0, 0, 0, 0);
-                                        wrote = true;
-                                    }
-                                }
-                            if (wrote)
-                                fence_proxy_async();
-                            __syncwarp();
-                        }
-                        for (int w = 0; go && w < nwg; ++w) {
-                            if (c == 0) {
-                                go = cta_wait(sh, &sh.p_full[w], g & 1);
-                                if (!go)
-                                    break;
-                                tc_fence_after();
-                            }
-                            if (lane == 0) {
-                                const uint32_t p = p0 + w * kHalfBytes, d = tmem + (4 + w * a.nd + c) * NT;
-                                const uint32_t lbo = width > 64 ? kHalfBytes : 0;
-                                for (int s = 0; s < ksteps; ++s)
-                                    tc_mma_bf16(d, tc_desc_sw128(base + s * 2048, lbo, 1024), tc_desc_sw128(p + s * 2048, 0, 1024), kIdO, jj + s > 0);
-                                if (c == a.nd - 1)
-                                    tc_commit(smem_addr(&sh.o_full[w]));
-                            }
-                        }
-                    }
-                    if (lane == 0)
-                        tc_commit(op_empty + 8 * r.slot);
-                    __syncwarp();
-                    r.step(ring);
-                }
-            }
-            n_tiles += n;
-        }
-        if (!go) {   // products in flight end before TMEM is given back
-            if (lane == 0)
-                tc_commit(smem_addr(&sh.drain));
-            __syncwarp();
-            mbar_wait_bounded(smem_addr(&sh.drain), 0, kWaitSpins);
-        }
-    } else if (E4M3 && warp >= 10) {
-        // --- e4m3 bytes to bf16 operands -----------------------------------------
-        Ring r, w;
-        const int t = tid - 320;
-        bool go = true;
-        while (go && run.next(a)) {
-            if (run.s.len == 0)
-                continue;
-            const int n = run.t1 - run.t0;
-            for (int step = 0; go && step < 2 * n; ++step) {
-                const bool is_k = step == 0 || ((step & 1) && (step + 1) / 2 < n);
-                const int jj = step == 0 ? 0 : is_k ? (step + 1) / 2 : step == 2 * n - 1 ? n - 1 : step / 2 - 1;
-                const int valid = min(kTile, run.s.len - (run.t0 + jj) * kTile), rows = (valid + 15) & ~15;
-                const int node0 = run.s.nn > 1 ? run.s.ctx - (run.t0 + jj) * kTile : kTile;   // first row of a node
-                for (int c = 0; go && c < a.nd; ++c) {
-                    go = cta_wait(sh, &sh.full[r.slot], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
-                    if (!go)
-                        break;
-                    const unsigned char* src = s_raw + r.slot * a.slot_bytes;
-                    unsigned char* dst = s_conv + w.slot * a.conv_bytes;
-                    // a thread takes one row: 16 bytes of the row to two 16-byte bf16 chunks at a time; rows of a
-                    // warp differ in their swizzle, so neither side's accesses collide
-                    if (t < rows) {
-                        const int pieces = min(128, D - 128 * c) / 16, key = t & 7;
-#pragma unroll 4
-                        for (int i = 0; i < pieces; ++i) {
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (t < valid)
-                                x = *reinterpret_cast<const uint4*>(src + t * a.raw_pitch + ((a.raw_swizzled ? i ^ key : i) << 4));
-                            const bool nan = chunk_nan_e4m3(x);
-                            if (nan && t >= node0 && !is_k)
-                                x = make_uint4(0, 0, 0, 0);
-                            uint2 y0 = e4m3_to_bf16(x.x), y1 = e4m3_to_bf16(x.y), y2 = e4m3_to_bf16(x.z), y3 = e4m3_to_bf16(x.w);
-                            if (nan) {
-                                y0 = e4m3_keep_nan(x.x, y0);
-                                y1 = e4m3_keep_nan(x.y, y1);
-                                y2 = e4m3_keep_nan(x.z, y2);
-                                y3 = e4m3_keep_nan(x.w, y3);
-                            }
-                            unsigned char* o = dst + (i >> 2) * kHalfBytes + t * 128;
-                            const int ch = 2 * (i & 3);
-                            *reinterpret_cast<uint4*>(o + ((ch ^ key) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
-                            *reinterpret_cast<uint4*>(o + (((ch + 1) ^ key) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
-                        }
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(ring_empty + 8 * r.slot);
-                        mbar_arrive(smem_addr(&sh.cfull[w.slot]));
-                    }
-                    r.step(a.slots);
-                    w.step(a.conv);
-                }
-            }
-        }
-    } else if (warp < 4 * nwg) {
+    // (The register moves stand inside the warpgroups' branches: ptxas budgets
+    // what they dominate.)
+    if (warp < 8) {
+        regs_grow<kRegsSoftmax<E4M3>>();
+        if (warp < 4 * NWG) {
         // --- softmax: one position a thread, NT rows ------------------------------
+        const AttnLayout L = attn_layout<N, E4M3>(a, smem);
+        AttnShared& sh = *L.sh;
+        Run run = run_of(a, sh);
+        const uint32_t tmem = sh.tmem, tmem_o = tmem + 2 * N;   // S (two buffers of N columns), then O
         const int w = warp >> 2, t = tid & 127, bar = 1 + w;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        unsigned char* const p_buf = s_p + w * kHalfBytes;
-        float* const scratch = reinterpret_cast<float*>(p_buf);   // [4][NT], while no P is in it
+        float* const scratch = sh.scratch[w];
         float* const negm = sh.negm[w];
         uint32_t n_tiles = 0;
         while (run.next(a)) {
             const int h = run.hg / a.groups, g = run.hg - h * a.groups;
             const int ctx = run.s.ctx, nn = run.s.nn, len = run.s.len;
             const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
-            const int item = run.b * (a.c.Hkv * a.groups) + run.hg;
-            if (!run.whole() && t == 0 && w == 0)
-                a.meta[part ^ 1] = item;   // meta[2i]: begun here, meta[2i + 1]: continued here
+            if (!run.whole() && t == 0 && w == 0)   // meta[2i]: begun here, meta[2i + 1]: continued here
+                a.meta[part ^ 1] = run.b * (a.c.Hkv * a.groups) + run.hg;
             // row c of this warpgroup: row `w * half + c` of the group
             const int mine = w == 0 ? min(a.half, a.rows) : a.rows - a.half, first = g * a.rows + w * a.half;
-            const int total_rows = nn * a.G, all_rows = a.Nmax * a.G;
             if (len == 0) {
                 // no position, or unusable lengths: zeros, or NaN
                 const float x = run.s.ok ? 0.0f : NAN;
@@ -555,81 +583,83 @@ __global__ void __launch_bounds__(E4M3 ? 448 : 320, 1)
                     atomicOr(a.err, kErrCache);
                 for (int i = t; i < mine * D; i += 128) {
                     const int rr = first + i / D, node = rr / a.G;
-                    if (rr < all_rows)
+                    if (rr < a.Nmax * a.G)
                         a.out[(((long long)run.b * a.Nmax + node) * a.Hq + h * a.G + rr - node * a.G) * D + i % D] =
                             __float2bfloat16_rn(node < nn ? x : 0.0f);
                 }
                 continue;
             }
             // queries to shared memory, swizzled as the product reads them
+            float q_unscale = 1.0f;
             {
-                const int per = D / 8;
-                for (int i = t; i < NT * per; i += 128) {
+                const int per = (E4M3 ? 128 * a.nd : (D + 63) & ~63) / 8;
+                auto load_q = [&](int i) {
                     const int row = i / per, ch = i - row * per, rr = first + row;
                     uint4 x = make_uint4(0, 0, 0, 0);
-                    if (row < mine && rr < total_rows) {
+                    if (row < mine && rr < nn * a.G && 8 * ch < D) {
                         const int node = rr / a.G;
                         x = __ldg(reinterpret_cast<const uint4*>(a.q + ((long long)run.b * a.Nmax + node) * a.q_stride +
                                                                  (long long)(h * a.G + rr - node * a.G) * D) + ch);
                     }
-                    *reinterpret_cast<uint4*>(s_q + w * q_bytes + (ch >> 3) * (NT * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = x;
+                    return x;
+                };
+                float scale = 1.0f;
+                if (E4M3) {
+                    // a power of two that brings the group's largest element to [128, 256)
+                    float top = 0.0f;
+                    for (int i = t; i < mine * per; i += 128) {
+                        float y[8];
+                        Elem<__nv_bfloat16>::unpack(load_q(i), y);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            top = fmaxf(top, isfinite(y[k]) ? fabsf(y[k]) : 0.0f);
+                    }
+                    top = warp_redux_max(top);
+                    if (lane == 0)
+                        sh.top[w][warp & 3] = top;
+                    bar_sync(bar, 128);
+                    top = fmaxf(fmaxf(sh.top[w][0], sh.top[w][1]), fmaxf(sh.top[w][2], sh.top[w][3]));
+                    const int e = top > 0.0f ? min(max(261 - (int)(__float_as_uint(top) >> 23), 1), 253) : 127;
+                    scale = __uint_as_float((uint32_t)e << 23);
+                    q_unscale = __uint_as_float((uint32_t)(254 - e) << 23);
+                }
+                for (int i = t; i < NT * per; i += 128) {
+                    const int row = i / per, ch = i - row * per, at = w * NT + row;
+                    const uint4 x = load_q(i);
+                    if (E4M3) {
+                        float y[8];
+                        Elem<__nv_bfloat16>::unpack(x, y);
+                        uint32_t p[3][2] = {};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            uint32_t u, v, z;
+                            split_q(y[k] * scale, u, v, z);
+                            p[0][k >> 2] |= u << (8 * (k & 3));
+                            p[1][k >> 2] |= v << (8 * (k & 3));
+                            p[2][k >> 2] |= z << (8 * (k & 3));
+                        }
+                        unsigned char* o = L.q + (ch >> 4) * (N * 128) + at * 128 + ((((ch & 15) >> 1) ^ (at & 7)) << 4) + (ch & 1) * 8;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k)
+                            *reinterpret_cast<uint2*>(o + k * L.q_part) = make_uint2(p[k][0], p[k][1]);
+                    } else {
+                        *reinterpret_cast<uint4*>(L.q + (ch >> 3) * (N * 128) + at * 128 + (((ch & 7) ^ (at & 7)) << 4)) = x;
+                    }
                 }
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.q_full[w]));
+                    mbar_arrive(smem_addr(&sh.q_full));
             }
-            // the rows' ancestors; nodes whose values are not finite
-            bool bad;
-            {
-                int par;
-                bad = !tree_parents(a.parent + (long long)run.b * a.Nmax, a.has_parent, nn, lane, par);
-                if (t < 64) {
-                    const int rr = first + t;
-                    int at = t < mine && rr < total_rows && !bad ? rr / a.G : -1;
-                    unsigned anc = 0;
-                    for (int d = 0; d < kNodeMax && __any_sync(kFull, at >= 0); ++d) {
-                        if (at >= 0)
-                            anc |= 1u << at;
-                        const int up = __shfl_sync(kFull, par, max(at, 0));
-                        at = at >= 0 ? up : -1;
-                    }
-                    sh.anc[w][t] = anc;
-                    if (t < NT)
-                        negm[t] = 0.0f;
-                }
-                if (t == 0) {
-                    sh.poison[w] = 0;
-                    sh.unset[w] = 1;
-                }
-                bar_sync(bar, 128);
-                if (nn > 1 && run.t1 * kTile > ctx) {
-                    const int m = t >> 2, pos = ctx + m, bytes = D * (E4M3 ? 1 : 2);
-                    bool hit = false;
-                    if (m < nn && pos >= run.t0 * kTile && pos < run.t1 * kTile) {
-                        const int page = kv_page(a.c, run.b, pos);
-                        if (page >= 0) {
-                            const long long row = kv_row(a.c, page, pos) + ((long long)h << a.c.page_shift);
-                            const uint4* v = reinterpret_cast<const uint4*>(a.c.v + row * bytes);
-                            for (int i = t & 3; i < bytes / 16; i += 4)
-                                hit |= chunk_nonfinite(v[i], E4M3);
-                            if (E4M3)
-                                hit |= !isfinite(a.c.v_scale[row]);
-                        }
-                    }
-                    if (hit)
-                        atomicOr(&sh.poison[w], 1u << m);
-                    bar_sync(bar, 128);
-                }
-            }
+            bool bad = begin_rows<E4M3>(a, sh, run, h, g, part, w, NT, t);
             const unsigned poison = sh.poison[w];
+            const float scale_log2 = E4M3 ? a.scale_log2 * q_unscale : a.scale_log2;
 
             uint64_t l2[NT / 2];   // this thread's share of the rows' sums, in pairs
 #pragma unroll
             for (int i = 0; i < NT / 2; ++i)
                 l2[i] = 0;
             // pages and scales one tile ahead
-            int page = -1, page_next = -1;
             float ks = 1.0f, vs = 1.0f, ks_next = 1.0f, vs_next = 1.0f;
             auto page_of = [&](int j) {
                 const int pos = j * kTile + t;
@@ -641,17 +671,13 @@ __global__ void __launch_bounds__(E4M3 ? 448 : 320, 1)
                     k = v = 0.0f;
                     if (j < run.t1 && pos < len && pg >= 0) {
                         const long long row = kv_row(a.c, pg, pos) + ((long long)h << a.c.page_shift);
-                        // a scale that is not finite marks a row that held something that was not
                         k = a.c.k_scale[row];
                         v = a.c.v_scale[row];
-                        k = isfinite(k) ? k : NAN;
-                        v = isfinite(v) ? v : NAN;
                     }
                 }
             };
-            page = page_of(run.t0);
+            int page = page_of(run.t0), page_next = page_of(run.t0 + 1);
             scales_of(run.t0, page, ks, vs);
-            page_next = page_of(run.t0 + 1);
 
             for (int j = run.t0; j < run.t1; ++j) {
                 const uint32_t gt = n_tiles + (j - run.t0);
@@ -659,141 +685,100 @@ __global__ void __launch_bounds__(E4M3 ? 448 : 320, 1)
                 scales_of(j + 1, page_next, ks_next, vs_next);
                 page = page_next;
                 page_next = page_of(j + 2);
-                const int pos = j * kTile + t;
                 const bool first_tile = j == run.t0;
-                const float mult = E4M3 ? a.scale_log2 * ks : a.scale_log2;
+                // a scale that is not finite marks a row that held something that was not
+                const float mult = E4M3 ? scale_log2 * (isfinite(ks) ? ks : NAN) : scale_log2;
+                float vscale = E4M3 ? (isfinite(vs) ? vs : NAN) : 1.0f;
 
-                cta_wait(sh, &sh.s_full[w][gt & 1], (gt >> 1) & 1);
+                cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
                 tc_fence_after();
-                float s[NT];
-#pragma unroll
-                for (int i = 0; i < NT / 16; ++i)
-                    tmem_ld16(tmem + lanes + (2 * w + (gt & 1)) * NT + 16 * i, s + 16 * i);
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.s_empty[w][gt & 1]));
-
-                // scores in powers of two, relative to the rows' references
-                float top = -INFINITY;
-                {
-                    const uint64_t m2 = f2_pack(mult, mult);
-                    const ulonglong2* nm = reinterpret_cast<const ulonglong2*>(negm);
-#pragma unroll
-                    for (int i = 0; i < NT / 4; ++i) {
-                        const ulonglong2 x = nm[i];
-                        f2_unpack(f2_fma(f2_pack(s[4 * i], s[4 * i + 1]), m2, x.x), s[4 * i], s[4 * i + 1]);
-                        f2_unpack(f2_fma(f2_pack(s[4 * i + 2], s[4 * i + 3]), m2, x.y), s[4 * i + 2], s[4 * i + 3]);
+                const uint32_t s_at = tmem + lanes + (gt & 1) * N + w * NT;
+                // what this position's scores are seen by: every row in the context, a node's descendants behind it
+                const bool tail = (j + 1) * kTile > ctx;   // the tile holds nodes, or ends the sequence
+                unsigned long long seen = ~0ull;
+                if (tail) {
+                    const int m = j * kTile + t - ctx;
+                    if (m >= 0) {
+                        seen = 0;
+                        if (m < nn && !((poison >> m) & 1u)) {
+#pragma unroll 4
+                            for (int i = 0; i < NT; ++i)
+                                seen |= (unsigned long long)((sh.anc[w][i] >> m) & 1u) << i;
+                        } else {
+                            vscale = 0.0f;
+                        }
                     }
                 }
-                if ((j + 1) * kTile > ctx) {   // the tile holds nodes, or ends the sequence
-                    const int m = pos - ctx;
-                    const bool dead = m >= 0 && (m >= nn || ((poison >> (m & 31)) & 1u));
+                // are all scores near enough to the references?  (A second look at TMEM is cheaper than the
+                // registers that would keep the scores over the vote.)
+                constexpr int C = NT % 32 ? 16 : 32;
+                float top = -INFINITY, low = INFINITY;
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
-                        if (m >= 0 && (dead || !((sh.anc[w][i] >> (m & 31)) & 1u)))
-                            s[i] = -INFINITY;
-                    if (dead)
-                        vs = 0.0f;
+                for (int c = 0; c < NT; c += C) {
+                    float s[C];
+                    load_scores<C>(s_at + c, negm + c, mult, tail, seen >> c, s);
+#pragma unroll
+                    for (int i = 0; i < C; i += 2)
+                        top = max3(top, s[i], s[i + 1]);
+                    if (first_tile) {
+#pragma unroll
+                        for (int i = 0; i < C; i += 2)
+                            low = min3(low, s[i], s[i + 1]);
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < NT / 2; ++i)
-                    top = max3(top, s[2 * i], s[2 * i + 1]);
-                const bool moved = bar_any(bar, 128, top > kLazy) || sh.unset[w];
-                if (!first_tile) {   // the previous tile's product is done with P (and O)
-                    cta_wait(sh, &sh.o_full[w], (gt - 1) & 1);
+                bool move = bar_any(bar, 128, top > kLazy) || sh.unset[w];
+                if (first_tile) {
+                    // no reference yet: zero will do if some position's scores are all near enough
+                    move = !bar_any(bar, 128, low >= -kLazy) || move;
+                    if (!move && t < NT)
+                        negm[t] = -0.0f;
+                } else {   // the previous tile's product is done with P (and O)
+                    cta_wait(sh, &sh.o_full, (gt - 1) & 1);
                     tc_fence_after();
                 }
-                if (moved) {
-                    // the rows' maxima over the 128 positions, and the references moved to them
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const float x = warp_redux_max(s[i]);
-                        if (lane == (i & 31))
-                            scratch[(warp & 3) * NT + i] = x;
-                    }
-                    bar_sync(bar, 128);
-                    float f = 1.0f, delta = 0.0f;
-                    bool unset = false;
-                    if (t < NT) {
-                        const float x = fmaxf(fmaxf(scratch[t], scratch[NT + t]), fmaxf(scratch[2 * NT + t], scratch[3 * NT + t]));
-                        // negm == +0 marks a row without a reference: no score has been seen
-                        const float old = negm[t];
-                        const bool fresh = __float_as_uint(old) == 0u;
-                        if (fresh) {
-                            unset = x == -INFINITY;
-                            delta = unset ? 0.0f : x;
-                        } else if (x > 0.0f) {
-                            delta = x;
-                            f = ex2_approx(-x);
-                        }
-                        if (!unset) {
-                            const float now = old - delta;
-                            negm[t] = __float_as_uint(now) == 0u ? -0.0f : now;
-                        }
-                    }
-                    if (t < NT) {
-                        scratch[t] = f;
-                        scratch[NT + t] = delta;
-                    }
-                    unset = bar_any(bar, 128, unset);
-                    if (t == 0)
-                        sh.unset[w] = unset;
+                if (move) {
+                    move_references<NT>(scratch, negm, &sh.unset[w], s_at, tmem_o + lanes + w * NT, first_tile ? 0 : a.nd, N, mult, seen, t, bar);
 #pragma unroll
                     for (int i = 0; i < NT / 4; ++i) {
-                        const float4 d = reinterpret_cast<const float4*>(scratch + NT)[i];
                         const ulonglong2 f4 = reinterpret_cast<const ulonglong2*>(scratch)[i];
-                        s[4 * i] -= d.x;
-                        s[4 * i + 1] -= d.y;
-                        s[4 * i + 2] -= d.z;
-                        s[4 * i + 3] -= d.w;
                         l2[2 * i] = f2_mul(l2[2 * i], f4.x);
                         l2[2 * i + 1] = f2_mul(l2[2 * i + 1], f4.y);
                     }
-                    if (!first_tile) {
-                        for (int c = 0; c < a.nd; ++c)
-#pragma unroll
-                            for (int i = 0; i < NT / 16; ++i) {
-                                float o[16];
-                                const uint32_t at = tmem + lanes + (4 + w * a.nd + c) * NT + 16 * i;
-                                tmem_ld16(at, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    o[k] *= scratch[16 * i + k];
-                                tmem_st16(at, o);
-                            }
-                        tmem_wait_st();
-                    }
-                    bar_sync(bar, 128);   // scratch is P again
+                    bar_sync(bar, 128);   // the scratch may be written again
                 }
                 // weights: fp32 sums, rounded once to bf16 for the second product (a weight's relative error of
                 // 2^-9 averages out over the positions and stays below the result's own rounding)
-                {
-                    const uint64_t v2 = f2_pack(vs, vs);
+                const uint64_t v2 = f2_pack(vscale, vscale);
 #pragma unroll
-                    for (int i = 0; i < NT / 8; ++i) {
+                for (int c = 0; c < NT; c += C) {
+                    float s[C];
+                    load_scores<C>(s_at + c, negm + c, mult, tail, seen >> c, s);
+#pragma unroll
+                    for (int i = 0; i < C / 8; ++i) {
                         uint32_t x[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float e0 = ex2_approx(s[8 * i + 2 * k]), e1 = ex2_approx(s[8 * i + 2 * k + 1]);
-                            uint64_t e = f2_pack(e0, e1);
-                            l2[4 * i + k] = f2_add(l2[4 * i + k], e);
+                            uint64_t e = f2_pack(ex2_approx(s[8 * i + 2 * k]), ex2_approx(s[8 * i + 2 * k + 1]));
+                            l2[c / 2 + 4 * i + k] = f2_add(l2[c / 2 + 4 * i + k], e);
                             if (E4M3)
                                 e = f2_mul(e, v2);
                             float lo, hi;
                             f2_unpack(e, lo, hi);
                             x[k] = bf16_pair(lo, hi);
                         }
-                        *reinterpret_cast<uint4*>(p_buf + t * 128 + ((i ^ (t & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+                        // P: rows of 64 of the CTA's N columns a position, swizzled
+                        const int at = w * (NT / 8) + c / 8 + i;
+                        *reinterpret_cast<uint4*>(L.p + (at >> 3) * kHalfBytes + t * 128 + (((at ^ t) & 7) << 4)) =
+                            make_uint4(x[0], x[1], x[2], x[3]);
                     }
                 }
-                fence_proxy_async();
                 tc_fence_before();
+                fence_proxy_async();
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.p_full[w]));
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&sh.s_empty[gt & 1]));
+                    mbar_arrive(smem_addr(&sh.p_full));
+                }
                 ks = ks_next;
                 vs = vs_next;
             }
@@ -819,7 +804,7 @@ __global__ void __launch_bounds__(E4M3 ? 448 : 320, 1)
                     }
                 sum[i] = x[0] + __shfl_xor_sync(kFull, x[0], 16);
             }
-            cta_wait(sh, &sh.o_full[w], (n_tiles - 1) & 1);
+            cta_wait(sh, &sh.o_full, (n_tiles - 1) & 1);
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < NT / 16; ++i)
@@ -829,57 +814,268 @@ __global__ void __launch_bounds__(E4M3 ? 448 : 320, 1)
             if (t == 0 && bad && a.has_err)
                 atomicOr(a.err, *reinterpret_cast<volatile int*>(&sh.abort) ? kErrWaitTimeout : kErrCache);
             float* const fin = scratch + 4 * NT;
+            const bool whole = run.whole();
             if (t < NT) {
                 float l = (scratch[t] + scratch[NT + t]) + (scratch[2 * NT + t] + scratch[3 * NT + t]);
                 if (bad || (sh.anc[w][t] & poison))
                     l = NAN;
-                if (run.whole()) {
-                    fin[t] = l == 0.0f ? 0.0f : 1.0f / l;
-                } else {
-                    fin[t] = 1.0f;
-                    if (t < mine) {
-                        float* ml = a.part_ml + ((long long)part * a.rows + w * a.half + t) * 2;
-                        ml[0] = -negm[t];
-                        ml[1] = l;
-                    }
+                fin[t] = !whole ? 1.0f : l == 0.0f || first + t >= nn * a.G ? 0.0f : 1.0f / l;
+                if (!whole && t < mine) {
+                    float* ml = a.part_ml + ((long long)part * a.rows + w * a.half + t) * 2;
+                    ml[0] = -negm[t];
+                    ml[1] = l;
                 }
             }
             bar_sync(bar, 128);
             for (int c = 0; c < a.nd; ++c) {
-                const int d = 128 * c + t;
-#pragma unroll
-                for (int i = 0; i < NT / 16; ++i) {
+                const int d = 128 * c + (E4M3 ? converted_element(t) : t);
+                for (int i = 0; i < NT; i += 16) {
                     float o[16];
-                    tmem_ld16(tmem + lanes + (4 + w * a.nd + c) * NT + 16 * i, o);
+                    tmem_ld16(tmem_o + lanes + c * N + w * NT + i, o);
                     tmem_wait_ld();
                     if (d < D) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const int row = 16 * i + k, rr = first + row;
-                            if (row < mine) {
-                                if (run.whole()) {
-                                    const int node = rr / a.G;
-                                    if (rr < all_rows)
-                                        a.out[(((long long)run.b * a.Nmax + node) * a.Hq + h * a.G + rr - node * a.G) * D + d] =
-                                            __float2bfloat16_rn(node < nn ? o[k] * fin[row] : 0.0f);
-                                } else {
-                                    a.part_o[((long long)part * a.rows + w * a.half + row) * D + d] = o[k];
-                                }
+                            const int at = sh.row_out[w][i + k];
+                            const float f = fin[i + k];
+                            if (at >= 0) {
+                                if (whole)
+                                    a.out[(long long)at * D + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : o[k] * f);
+                                else
+                                    a.part_o[(long long)at * D + d] = o[k];
                             }
                         }
                     }
                 }
             }
             tc_fence_before();
-            bar_sync(bar, 128);   // O and the scratch are read before the next item's product and P
+            bar_sync(bar, 128);   // O and the scratch are read before the next item's product and sums
         }
+        }
+    } else if (E4M3 && warp >= 12) {
+        regs_shrink<kRegsConvert>();
+        // --- e4m3 values to bf16 operands ---------------------------------------
+        const AttnLayout L = attn_layout<N, E4M3>(a, smem);
+        AttnShared& sh = *L.sh;
+        Run run = run_of(a, sh);
+        // A thread takes one position's row: rows of a warp differ in their
+        // swizzle, so neither the loads nor the stores collide.
+        Ring r, w;
+        const int t = tid - 384, key = t & 7;
+        bool go = true;
+        while (go && run.next(a)) {
+            if (run.s.len == 0)
+                continue;
+            for (int j = run.t0; go && j < run.t1; ++j) {
+                const int valid = min(kTile, run.s.len - j * kTile), rows = (valid + 15) & ~15;
+                const int node0 = run.s.nn > 1 ? run.s.ctx - j * kTile : kTile;   // first row of a node
+                for (int c = 0; go && c < a.nd; ++c) {
+                    go = cta_wait(sh, &sh.vfull[r.slot], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
+                    if (!go)
+                        break;
+                    const unsigned char* src = L.v + r.slot * a.v_bytes + t * 128;
+                    unsigned char* dst = L.c + w.slot * a.conv_bytes + t * 128;
+                    if (t < rows) {
+                        const int pieces = min(128, D - 128 * c) / 16;
+#pragma unroll 4
+                        for (int i = 0; i < pieces; ++i) {
+                            uint4 x = *reinterpret_cast<const uint4*>(src + ((i ^ key) << 4));
+                            const bool nan = chunk_nan_e4m3(x);
+                            if (t >= valid || (nan && t >= node0))
+                                x = make_uint4(0, 0, 0, 0);
+                            uint2 y0 = e4m3_to_bf16(x.x), y1 = e4m3_to_bf16(x.y), y2 = e4m3_to_bf16(x.z), y3 = e4m3_to_bf16(x.w);
+                            if (nan) {
+                                y0 = e4m3_keep_nan(x.x, y0);
+                                y1 = e4m3_keep_nan(x.y, y1);
+                                y2 = e4m3_keep_nan(x.z, y2);
+                                y3 = e4m3_keep_nan(x.w, y3);
+                            }
+                            unsigned char* o = dst + (i >> 2) * kHalfBytes;
+                            const int ch = 2 * (i & 3);
+                            *reinterpret_cast<uint4*>(o + ((ch ^ key) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
+                            *reinterpret_cast<uint4*>(o + (((ch + 1) ^ key) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
+                        }
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&sh.vempty[r.slot]));
+                        mbar_arrive(smem_addr(&sh.cfull[w.slot]));
+                    }
+                    r.step(a.vslots);
+                    w.step(a.conv);
+                }
+            }
+        }
+    } else {
+        regs_shrink<kRegsIssue<E4M3>>();
+    if (warp == 9) {
+        // --- TMA producer ------------------------------------------------------
+        const AttnLayout L = attn_layout<N, E4M3>(a, smem);
+        AttnShared& sh = *L.sh;
+        Run run = run_of(a, sh);
+        Ring rk, rv;
+        int nk = 0, nv = 0;   // slots that may still be filling
+        const int boxes = kTile / a.box_rows;
+        bool go = true;
+        while (go && run.next(a)) {
+            if (run.s.len == 0)
+                continue;
+            const int h = run.hg / a.groups, n = run.t1 - run.t0;
+            // lane l: row of the tile's box l, -1 where it holds no position (or its page is unusable)
+            auto box_row = [&](int j) {
+                const int pos = j * kTile + lane * a.box_rows;
+                if (j >= run.t1 || lane >= boxes || pos >= run.s.len)
+                    return -1;
+                const int page = kv_page(a.c, run.b, pos);
+                return page < 0 ? -1 : (int)kv_row(a.c, page, pos) + (h << a.c.page_shift);
+            };
+            int row = box_row(run.t0), row_k = row, ahead = box_row(run.t0 + 1);   // tiles of the next V, of the last K, after it
+            for (int step = 0; go && step < 2 * n; ++step) {
+                const bool is_k = step_is_k(step, n);
+                if (is_k && step > 0) {
+                    row_k = ahead;
+                    ahead = box_row(run.t0 + step_tile(step, n) + 1);
+                }
+                const int at = is_k ? row_k : row;
+                const unsigned have = __ballot_sync(kFull, at >= 0);
+                Ring& r = is_k ? rk : rv;
+                for (int c = 0; go && c < a.nd; ++c) {
+                    go = cta_wait(sh, is_k ? &sh.kempty[r.slot] : &sh.vempty[r.slot], r.phase ^ 1);
+                    if (!go)
+                        break;
+                    const uint32_t bar = smem_addr(is_k ? &sh.kfull[r.slot] : &sh.vfull[r.slot]);
+                    const uint32_t dst = is_k ? smem_addr(L.k) + r.slot * a.k_bytes : smem_addr(L.v) + r.slot * a.v_bytes;
+                    const int halves = E4M3 ? 1 : min(2, (D - 128 * c + 63) / 64);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar, __popc(have) * a.box_rows * 128 * halves);
+                    __syncwarp();
+                    if (at >= 0)
+                        for (int x = 0; x < halves; ++x)
+                            tma_load_2d(dst + x * kHalfBytes + lane * a.box_rows * 128, is_k ? &map_k : &map_v, 128 * c + 64 * x, at, bar);
+                    __syncwarp();
+                    if (is_k) {
+                        rk.step(a.kslots);
+                        nk = min(nk + 1, a.kslots);
+                    } else {
+                        rv.step(a.vslots);
+                        nv = min(nv + 1, a.vslots);
+                    }
+                }
+                if (!is_k)
+                    row = row_k;
+            }
+        }
+        if (!go) {   // copies in flight land before the CTA's memory is given back
+            for (; nk > 0; --nk) {
+                rk.back(a.kslots);
+                mbar_wait_bounded(smem_addr(&sh.kfull[rk.slot]), rk.phase, kWaitSpins);
+            }
+            for (; nv > 0; --nv) {
+                rv.back(a.vslots);
+                mbar_wait_bounded(smem_addr(&sh.vfull[rv.slot]), rv.phase, kWaitSpins);
+            }
+        }
+    } else if (warp == 8) {
+        // --- MMA ---------------------------------------------------------------
+        const AttnLayout L = attn_layout<N, E4M3>(a, smem);
+        AttnShared& sh = *L.sh;
+        Run run = run_of(a, sh);
+        const uint32_t tmem = sh.tmem, tmem_o = tmem + 2 * N;   // S (two buffers of N columns), then O
+        Ring rk, rv;
+        uint32_t item = 0;        // items with positions so far (parity of q_full)
+        uint32_t n_tiles = 0;     // tiles so far (parity of p_full, buffer of S)
+        const int vring = E4M3 ? a.conv : a.vslots;
+        const uint32_t k0 = smem_addr(L.k), v0 = smem_addr(E4M3 ? L.c : L.v), v_bytes = E4M3 ? a.conv_bytes : a.v_bytes;
+        const uint32_t q0 = smem_addr(L.q), p0 = smem_addr(L.p);
+        uint64_t* const vfull = E4M3 ? sh.cfull : sh.vfull;
+        uint64_t* const vempty = E4M3 ? sh.cempty : sh.vempty;
+        bool go = true;
+        while (go && run.next(a)) {
+            if (run.s.len == 0)
+                continue;
+            go = cta_wait(sh, &sh.q_full, item & 1);
+            ++item;
+            const int n = run.t1 - run.t0;
+            for (int step = 0; go && step < 2 * n; ++step) {
+                const bool is_k = step_is_k(step, n);
+                const int jj = step_tile(step, n), valid = min(kTile, run.s.len - (run.t0 + jj) * kTile);
+                const uint32_t g = n_tiles + jj;   // the CTA's tile count
+                for (int c = 0; go && c < a.nd; ++c) {
+                    const int width = min(128, D - 128 * c);
+                    if (is_k) {
+                        go = cta_wait(sh, &sh.kfull[rk.slot], rk.phase) &&
+                             (c > 0 || cta_wait(sh, &sh.s_empty[g & 1], ((g >> 1) & 1) ^ 1));
+                        if (!go)
+                            break;
+                        tc_fence_after();
+                        if (lane == 0) {
+                            mma_scores<N, E4M3>(tmem + (g & 1) * N, k0 + rk.slot * a.k_bytes, q0 + (E4M3 ? c : 2 * c) * (N * 128), L.q_part,
+                                                E4M3 ? (width + 31) / 32 : width / 16, c > 0);
+                            if (c == a.nd - 1)
+                                tc_commit(smem_addr(&sh.s_full[g & 1]));
+                            tc_commit(smem_addr(&sh.kempty[rk.slot]));
+                        }
+                        __syncwarp();
+                        rk.step(a.kslots);
+                    } else {
+                        go = cta_wait(sh, &vfull[rv.slot], rv.phase);
+                        if (!go)
+                            break;
+                        const int ksteps = (valid + 15) / 16;
+                        if (!E4M3 && (run.t0 + jj + 1) * kTile > run.s.ctx) {
+                            // rows behind the last position may hold anything: zeros instead of 0 * NaN.  A node's
+                            // values are seen by some rows only: what is not finite there is zeroed too (the rows
+                            // that do see it are set to NaN at the end).
+                            unsigned char* v = L.v + rv.slot * a.v_bytes;
+                            const int chunks = width > 64 ? 16 : 8;
+                            for (int i = valid * chunks + lane; i < ksteps * 16 * chunks; i += 32) {
+                                const int row = i / chunks, ch = i % chunks;
+                                *reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            const int row = run.s.ctx + lane - (run.t0 + jj) * kTile;
+                            if (run.s.nn > 1 && lane < run.s.nn && row >= 0 && row < kTile)
+                                for (int ch = 0; ch < chunks; ++ch) {
+                                    uint4* p = reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 + ((ch ^ lane) & 7) * 16);
+                                    if (chunk_nonfinite(*p, false))
+                                        *p = make_uint4(0, 0, 0, 0);
+                                }
+                            fence_proxy_async();
+                            __syncwarp();
+                        }
+                        if (c == 0) {
+                            go = cta_wait(sh, &sh.p_full, g & 1);
+                            if (!go)
+                                break;
+                        }
+                        tc_fence_after();
+                        if (lane == 0) {
+                            mma_values<N>(tmem_o + c * N, v0 + rv.slot * v_bytes, p0, width > 64 ? kHalfBytes : 0, ksteps, jj > 0);
+                            if (c == a.nd - 1)
+                                tc_commit(smem_addr(&sh.o_full));
+                            tc_commit(smem_addr(&vempty[rv.slot]));
+                        }
+                        __syncwarp();
+                        rv.step(vring);
+                    }
+                }
+            }
+            n_tiles += n;
+        }
+        if (!go) {   // products in flight end before TMEM is given back
+            if (lane == 0)
+                tc_commit(smem_addr(&sh.drain));
+            __syncwarp();
+            mbar_wait_bounded(smem_addr(&sh.drain), 0, kWaitSpins);
+        }
+    }
     }
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 8)
-        tmem_free(tmem, 512);
+        tmem_free(attn_layout<N, E4M3>(a, smem).sh->tmem, 512);
 }
 
 // Items cut between CTAs: CTA i's last item, if it does not end it, is joined

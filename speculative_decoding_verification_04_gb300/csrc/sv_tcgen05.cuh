@@ -34,7 +34,8 @@ __device__ __forceinline__ void tc_commit(uint32_t mbar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar) : "memory");
 }
 
-// D[tmem] (+)= A B, bf16 operands in shared memory, fp32 accumulation.
+// D[tmem] (+)= A B on shared-memory operands, fp32 accumulation: bf16, 16
+// elements of the contraction a call; 8-bit floats, 32.
 __device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
@@ -44,21 +45,32 @@ __device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t a, uint64_t b, 
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
 }
 
-// Instruction descriptor: fp32 result, bf16 operands, M x N, and which
-// operands lie with M (N) contiguous instead of K.
-__host__ __device__ constexpr uint32_t tc_idesc_bf16(int M, int N, bool a_mn, bool b_mn)
+__device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
 }
 
-// Shared-memory descriptor of an operand in 128-byte swizzled rows.  `sbo` is
-// the distance between groups of eight rows; `lbo`, for operands with M (N)
-// contiguous, the one between blocks of 64 such elements.
-__device__ __forceinline__ uint64_t tc_desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo)
+// Instruction descriptors: fp32 result, M x N, and which operands lie with M
+// (N) contiguous instead of the contraction.  8-bit formats: 0 e4m3, 1 e5m2.
+__host__ __device__ constexpr uint32_t tc_idesc(int M, int N, int a_format, int b_format, bool a_mn, bool b_mn)
 {
-    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+    return (1u << 4) | ((uint32_t)a_format << 7) | ((uint32_t)b_format << 10) | ((uint32_t)a_mn << 15) |
+           ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Shared-memory descriptor of an operand in 128-byte swizzled rows, eight-row
+// groups 1024 bytes apart; `lbo`, for operands with M (N) contiguous, is the
+// distance between blocks of 128 bytes of M (N).  The low word holds what
+// differs between the steps of a product (addresses in units of 16 bytes).
+__device__ __forceinline__ uint32_t tc_desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+
+__device__ __forceinline__ uint64_t tc_desc(uint32_t lo)
+{
+    return (uint64_t)lo | ((uint64_t)((1024 >> 4) | (1u << 14) | (2u << 29)) << 32);
 }
 
 // Sixteen TMEM columns of the warp's 32 lanes, one lane a thread.
@@ -101,6 +113,11 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// Move registers between warpgroups (every warp of one calls; the shares of
+// all warpgroups add up to what the block was launched with).
+template <int N> __device__ __forceinline__ void regs_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // Maximum over the warp (NaN lanes are passed over).
 __device__ __forceinline__ float warp_redux_max(float x)
 {
@@ -113,6 +130,13 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float y;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float y;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 
