@@ -526,7 +526,7 @@ sv_status spec_kv_append(const sv_kv_cache* cache, const sv_kv_tokens* tokens, c
  * positions j < kv_len[b] and at kv_len[b] + m for m = n and its ancestors.
  * The nodes' keys and values are in the cache (spec_kv_append).  Nmax = 1 is
  * an ordinary decode step.  q: element (b * Nmax + n) * q_stride, a multiple
- * of 8; out [B][Nmax][n_heads][head_dim], zeros for n >= n_nodes[b]; both
+ * of 8 and at least n_heads * head_dim; out [B][Nmax][n_heads][head_dim], zeros for n >= n_nodes[b]; both
  * bf16 (fp32 is SV_ERR_UNSUPPORTED).  Products accumulate in fp32, softmax
  * statistics are fp32; the weights are rounded to bf16 for the second
  * product.  Cache entries behind a sequence's nodes are never used: they may

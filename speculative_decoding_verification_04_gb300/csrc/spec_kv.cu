@@ -25,7 +25,7 @@ sv_status check_cache(const sv_kv_cache* c, bool need_table, KvCache* out)
         return SV_ERR_INVALID_ARG;
     if (c->format == SV_KV_E4M3 ? (!c->k_scale || !c->v_scale) : (c->k_scale || c->v_scale))
         return SV_ERR_INVALID_ARG;
-    if (!aligned16(c->k) || !aligned16(c->v) || ((uintptr_t)c->k_scale & 3) || ((uintptr_t)c->v_scale & 3) ||
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
         ((uintptr_t)c->page_table & 3))
         return SV_ERR_INVALID_ARG;
     if (c->head_dim < 64 || c->head_dim > 256 || c->head_dim % 16 || c->page_size < 8 || c->page_size > 1024 ||
@@ -126,18 +126,42 @@ bool cache_map(CUtensorMap* m, void* base, const AttnArgs& a, bool e4m3)
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How the rows of a key head are spread: groups of at most `most` rows.
-void attention_rows(int Nmax, int G, int most, int* groups, int* rows)
+// The queries: [B * Nmax][Hq][D], a box being one row group.
+bool query_map(CUtensorMap* m, const AttnArgs& a)
 {
-    const int all = Nmax * G;
-    *groups = (all + most - 1) / most;
-    *rows = (all + *groups - 1) / *groups;
+    const EncodeTiled encode = tensor_map_encoder();
+    if (!encode)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.c.D, (cuuint64_t)a.Hq, (cuuint64_t)a.B * a.Nmax};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.c.D * 2, (cuuint64_t)(a.B * (long long)a.Nmax > 1 ? a.q_stride : (long long)a.Hq * a.c.D) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.heads, (cuuint32_t)a.nodes}, ones[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(a.q), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a key head's rows (Nmax nodes by G query heads) are spread over groups of
+// at most `most`: whole nodes while a node's heads fit, evenly.
+struct RowGroups {
+    int nodes, heads, head_blocks, groups, rows;
+};
+
+RowGroups attention_rows(int Nmax, int G, int most)
+{
+    RowGroups r;
+    r.head_blocks = (G + most - 1) / most;
+    r.heads = (G + r.head_blocks - 1) / r.head_blocks;
+    const int fit = std::max(1, most / r.heads), blocks = (Nmax + fit - 1) / fit;
+    r.nodes = (Nmax + blocks - 1) / blocks;
+    r.groups = blocks * r.head_blocks;
+    r.rows = r.nodes * r.heads;
+    return r;
 }
 
 size_t attention_part_bytes(int rows, int D) { return (size_t)2 * kAttnMaxCtas * rows * (D + 2) * 4; }
 
 template <int NT, int NWG, bool E4M3>
-cudaError_t launch_attention(AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int nsm, cudaStream_t st)
+cudaError_t launch_attention(AttnArgs& a, const CUtensorMap (&m)[3], int dev, int nsm, cudaStream_t st)
 {
     constexpr int N = NT * NWG;
     const int q_bytes = E4M3 ? 3 * N * 128 * a.nd : N * 128 * ((a.c.D + 63) / 64);
@@ -172,7 +196,7 @@ cudaError_t launch_attention(AttnArgs& a, const CUtensorMap& mk, const CUtensorM
             ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     const int ctas = std::min(nsm, kAttnMaxCtas);
-    sv_attention_kernel<NT, NWG, E4M3><<<ctas, attn_threads(E4M3), smem, st>>>(a, mk, mv);
+    sv_attention_kernel<NT, NWG, E4M3><<<ctas, attn_threads(E4M3), smem, st>>>(a, m[0], m[1], m[2]);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
@@ -192,16 +216,15 @@ cudaError_t launch_attention(AttnArgs& a, const CUtensorMap& mk, const CUtensorM
 }
 
 template <bool E4M3>
-cudaError_t launch_attention_rows(AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int nsm, cudaStream_t st)
+cudaError_t launch_attention_rows(AttnArgs& a, const CUtensorMap (&m)[3], int dev, int nsm, cudaStream_t st)
 {
-    a.half = a.rows > 16 ? (a.rows + 1) / 2 : a.rows;
     if (a.rows <= 16)
-        return launch_attention<16, 1, E4M3>(a, mk, mv, dev, nsm, st);
-    switch ((a.half + 15) / 16) {
-    case 1: return launch_attention<16, 2, E4M3>(a, mk, mv, dev, nsm, st);
-    case 2: return launch_attention<32, 2, E4M3>(a, mk, mv, dev, nsm, st);
-    case 3: return launch_attention<48, 2, E4M3>(a, mk, mv, dev, nsm, st);
-    default: return launch_attention<64, 2, E4M3>(a, mk, mv, dev, nsm, st);
+        return launch_attention<16, 1, E4M3>(a, m, dev, nsm, st);
+    switch ((a.rows + 31) / 32) {
+    case 1: return launch_attention<16, 2, E4M3>(a, m, dev, nsm, st);
+    case 2: return launch_attention<32, 2, E4M3>(a, m, dev, nsm, st);
+    case 3: return launch_attention<48, 2, E4M3>(a, m, dev, nsm, st);
+    default: return launch_attention<64, 2, E4M3>(a, m, dev, nsm, st);
     }
 }
 
@@ -291,8 +314,8 @@ size_t sv_attention_workspace_size(int32_t Nmax, int32_t n_heads, int32_t n_kv_h
     if (Nmax < 1 || Nmax > sv::kNodeMax || n_kv_heads < 1 || n_heads < n_kv_heads || n_heads % n_kv_heads ||
         head_dim < 64 || head_dim > 256 || head_dim % 16)
         return 0;
-    int groups, rows;
-    sv::attention_rows(Nmax, n_heads / n_kv_heads, sv::attn_rows_max(false, head_dim), &groups, &rows);   // never fewer rows
+    // the format is not known here: 128-row groups are never smaller than 64-row ones
+    const int rows = sv::attention_rows(Nmax, n_heads / n_kv_heads, sv::attn_rows_max(false, head_dim)).rows;
     return (sv::kAttnMaxCtas * 8 + sv::attention_part_bytes(rows, head_dim) + 255) / 256 * 256;
 }
 
@@ -313,6 +336,7 @@ sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, c
     if (B == 0)
         return SV_OK;
     if (!kv_len || !q || !out || !sv::aligned16(q) || !sv::aligned16(out) || q_stride % 8 ||
+        ((long long)B * Nmax > 1 && q_stride < (long long)n_heads * cache->head_dim) ||
         (((uintptr_t)kv_len | (uintptr_t)n_nodes | (uintptr_t)parent | (uintptr_t)errors) & 3))
         return SV_ERR_INVALID_ARG;
     if ((long long)B * Nmax * n_heads > 0x3fffffffLL)
@@ -336,7 +360,12 @@ sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, c
     a.scale_log2 = scale * 1.44269504088896341f;
     a.G = n_heads / cache->n_kv_heads;
     const bool e4m3 = cache->format == SV_KV_E4M3;
-    sv::attention_rows(Nmax, a.G, sv::attn_rows_max(e4m3, cache->head_dim), &a.groups, &a.rows);
+    const sv::RowGroups rg = sv::attention_rows(Nmax, a.G, sv::attn_rows_max(e4m3, cache->head_dim));
+    a.nodes = rg.nodes;
+    a.heads = rg.heads;
+    a.head_blocks = rg.head_blocks;
+    a.groups = rg.groups;
+    a.rows = rg.rows;
     a.nd = cache->head_dim > 128 ? 2 : 1;
     a.box_rows = std::min(cache->page_size, sv::kTile);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -348,11 +377,12 @@ sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, c
     int dev = 0, nsm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return SV_ERR_CUDA;
-    CUtensorMap mk, mv;
-    if (!sv::cache_map(&mk, a.c.k, a, e4m3) || !sv::cache_map(&mv, a.c.v, a, e4m3))
+    CUtensorMap m[3];
+    if (!sv::cache_map(&m[0], a.c.k, a, e4m3) || !sv::cache_map(&m[1], a.c.v, a, e4m3) ||
+        (e4m3 ? (m[2] = m[0], false) : !sv::query_map(&m[2], a)))
         return SV_ERR_CUDA;
-    return sv::launched(e4m3 ? sv::launch_attention_rows<true>(a, mk, mv, dev, nsm, stream)
-                             : sv::launch_attention_rows<false>(a, mk, mv, dev, nsm, stream));
+    return sv::launched(e4m3 ? sv::launch_attention_rows<true>(a, m, dev, nsm, stream)
+                             : sv::launch_attention_rows<false>(a, m, dev, nsm, stream));
 }
 
 sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* kv_len, const int32_t* out_path,

@@ -24,6 +24,11 @@
 // products add up in the same accumulator.  Its values become bf16 in shared
 // memory, because the weights need more range than two or three 8-bit terms.
 //
+// Warps: 0-7 softmax (two warpgroups), 8 MMA issue, 9 TMA, 10-11 what an item
+// needs before its first tile (tree masks, e4m3 queries), and for e4m3 caches
+// 12-15 conversion of values.  Tiles run through them in one stream across
+// items: K(g + 1) is loaded and multiplied before V(g).
+//
 // Work is (sequence, key head, row group) items of 128-position tiles, laid
 // end to end and cut into equal runs, one to a CTA.  An item cut by a run's
 // end leaves partial sums in the workspace, which sv_attention_combine joins.
@@ -36,12 +41,13 @@ namespace sv {
 
 constexpr int kAttnMaxCtas = 160;
 constexpr int kTile = 128;                 // positions a tile
+constexpr int kHalfBytes = kTile * 128;    // 128 swizzled rows of 128 bytes
+constexpr float kLazy = 24.0f;             // log2 of how far a weight may lie from one
+constexpr int kMaxSlots = 8;
+constexpr int kScaleSlots = 4;             // tiles of scales in flight
 // Query rows a CTA: 128, but 64 where the three 8-bit terms of wider heads'
 // queries would leave the loads no room.
 __host__ __device__ constexpr int attn_rows_max(bool e4m3, int D) { return e4m3 && D > 128 ? 64 : 128; }
-constexpr int kHalfBytes = kTile * 128;    // 128 swizzled rows of 128 bytes
-constexpr float kLazy = 32.0f;             // log2 of how far a weight may lie from one
-constexpr int kMaxSlots = 8;
 
 struct AttnArgs {
     KvCache c;
@@ -57,14 +63,26 @@ struct AttnArgs {
     int* meta;               // [CTAs][2]: the item a CTA begins / continues without ending it alone
     int has_n, has_parent, has_err;
     int Hq, G, B, Nmax;
-    int groups, rows;        // row groups of a key head; rows of one group
-    int half;                // rows of the first warpgroup (the second has the rest)
+    // row groups of a key head: blocks of `nodes` nodes by blocks of `heads` of
+    // its query heads; rows = nodes * heads, row r being head r % heads of node
+    // r / heads of the block
+    int nodes, heads, head_blocks, groups, rows;
     int nd;                  // 128-wide chunks of head_dim
     int kslots, vslots, conv;         // ring sizes
     int k_bytes, v_bytes, conv_bytes; // of one slot
     int box_rows;            // rows of one TMA box (a page, or a tile)
     float scale_log2;        // scale * log2(e)
 };
+
+// Row r of group g: its node (of the sequence) and query head (of the key
+// head's), false past either.
+__device__ __forceinline__ bool attn_row(const AttnArgs& a, int g, int r, int& node, int& head)
+{
+    const int nb = g / a.head_blocks, n = r / a.heads;
+    node = nb * a.nodes + n;
+    head = (g - nb * a.head_blocks) * a.heads + r - n * a.heads;
+    return r < a.rows && node < a.Nmax && head < a.G;
+}
 
 // One sequence's lengths; tiles >= 1 so that every output row has an item.
 struct SeqLens {
@@ -85,7 +103,8 @@ __device__ __forceinline__ SeqLens seq_lens(const AttnArgs& a, int b)
     return s;
 }
 
-// A CTA's run of tiles, an item (or a part of one) at a time.
+// A CTA's run of tiles, an item (or a part of one) at a time.  The items of
+// no position are passed over but for the role that writes their rows.
 struct Run {
     long long left;
     int b, hg, tile;
@@ -93,51 +112,76 @@ struct Run {
     // the current part
     int t0, t1;
 
-    __device__ __forceinline__ bool next(const AttnArgs& a)
+    __device__ __forceinline__ bool next(const AttnArgs& a, bool empty_too = false)
     {
-        if (left <= 0)
-            return false;
-        if (tile == s.tiles) {
-            tile = 0;
-            if (++hg == a.c.Hkv * a.groups) {
-                hg = 0;
-                s = seq_lens(a, ++b);
+        do {
+            if (left <= 0)
+                return false;
+            if (tile == s.tiles) {
+                tile = 0;
+                if (++hg == a.c.Hkv * a.groups) {
+                    hg = 0;
+                    s = seq_lens(a, ++b);
+                }
             }
-        }
-        t0 = tile;
-        t1 = (int)min((long long)s.tiles, t0 + left);
-        left -= t1 - t0;
-        tile = t1;
+            t0 = tile;
+            t1 = (int)min((long long)s.tiles, t0 + left);
+            left -= t1 - t0;
+            tile = t1;
+        } while (s.len == 0 && !empty_too);
         return true;
     }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == s.tiles; }
 };
 
-// The order in which a part's operands are loaded and multiplied: K(0), then
-// K(j + 1) and V(j) for every tile j, so that the next scores are on their way
-// while the softmax works.  Step s of 2 n: is it a K, and of which tile.
-__device__ __forceinline__ bool step_is_k(int s, int n) { return s == 0 || ((s & 1) && s < 2 * n - 1); }
-__device__ __forceinline__ int step_tile(int s, int n)
-{
-    return s == 0 ? 0 : step_is_k(s, n) ? (s + 1) >> 1 : s == 2 * n - 1 ? n - 1 : (s >> 1) - 1;
-}
+// The same a tile at a time.
+struct Tiles {
+    Run run;
+    int j;          // the tile
+    bool more;      // there is one
+
+    __device__ __forceinline__ void start(const AttnArgs& a, const Run& r)
+    {
+        run = r;
+        more = run.next(a);
+        j = run.t0;
+    }
+    __device__ __forceinline__ void step(const AttnArgs& a)
+    {
+        if (++j == run.t1) {
+            more = run.next(a);
+            j = run.t0;
+        }
+    }
+    __device__ __forceinline__ int valid() const { return min(kTile, run.s.len - j * kTile); }
+};
+
+// What an item's rows need to know, prepared while the one before is worked on.
+struct ItemInfo {
+    unsigned anc[128];     // the rows' ancestor bits (0: no row)
+    int row_out[128];      // where their results go (-1: nowhere)
+    unsigned poison;       // nodes whose values are not finite
+    unsigned bad;          // malformed tree, unusable page
+    float q_unscale;       // undoes the queries' power of two (e4m3)
+};
 
 struct AttnShared {
     uint64_t kfull[kMaxSlots], kempty[kMaxSlots];  // K slots
     uint64_t vfull[kMaxSlots], vempty[kMaxSlots];  // V slots
     uint64_t cfull[2], cempty[2];                  // converted V slots (e4m3)
-    uint64_t q_full, s_full[2], s_empty[2], p_full, o_full, drain;
+    uint64_t sfull[kScaleSlots], sempty[kScaleSlots];   // scales (e4m3)
+    uint64_t q_full, q_empty, info_full[2], info_empty[2];
+    uint64_t s_full[2], s_empty[2], p_full, o_full, drain;
     long long t_begin, t_end, sum[16];
     uint32_t tmem;
     int abort;
     int b, hg, tile, active;
-    unsigned poison[2];
     int unset[2];
-    float top[2][4];
-    alignas(16) float negm[2][64];                 // minus the rows' references
+    float top[2];
+    alignas(16) float negm[128];                   // minus the rows' references
     float scratch[2][5 * 64];
-    unsigned anc[2][64];                           // the rows' ancestor bits
-    int row_out[2][64];                            // where the rows' results go (-1: nowhere)
+    alignas(128) float scale[kScaleSlots][2][kTile];
+    ItemInfo info[2];
 };
 
 // The dynamic shared memory.  Every role derives its own pointers (through a
@@ -173,6 +217,7 @@ __device__ __forceinline__ Run run_of(const AttnArgs& a, const AttnShared& share
     r.b = sh.active ? sh.b : 0;
     r.hg = sh.hg;
     r.tile = sh.tile;
+    r.t0 = r.t1 = 0;
     r.s = seq_lens(a, r.b);
     return r;
 }
@@ -262,18 +307,22 @@ __device__ __forceinline__ bool chunk_nonfinite(uint4 w, bool e4m3)
                 : bf16_pair_nonfinite(w.x) || bf16_pair_nonfinite(w.y) || bf16_pair_nonfinite(w.z) || bf16_pair_nonfinite(w.w);
 }
 
-// A query element (scaled so that the group's largest is below 256) as an
-// e4m3 and two e5m2 terms; what is not finite becomes NaN.
-__device__ __forceinline__ void split_q(float x, uint32_t& h, uint32_t& m, uint32_t& l)
+// Two query elements (scaled so that the group's largest is below 256) as an
+// e4m3 and two e5m2 terms each; what is not finite becomes NaN.  The
+// differences are exact in fp16 (down to 2^-24).
+__device__ __forceinline__ void split_q(float x0, float x1, uint32_t& h, uint32_t& m, uint32_t& l)
 {
-    h = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-    float r = x - __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)h, __NV_E4M3)));
-    m = __nv_cvt_float_to_fp8(r, __NV_SATFINITE, __NV_E5M2);
-    r -= __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)m, __NV_E5M2)));
-    l = __nv_cvt_float_to_fp8(r, __NV_SATFINITE, __NV_E5M2);
-    if (!isfinite(x)) {
-        h = 0x7f;
-        m = l = 0;
+    const __half2 x = __floats2half2_rn(x0, x1);
+    h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(x), __NV_SATFINITE, __NV_E4M3);
+    const __half2 r = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3)));
+    m = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(r), __NV_SATFINITE, __NV_E5M2);
+    const __half2 r2 = __hsub2(r, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)m, __NV_E5M2)));
+    l = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(r2), __NV_SATFINITE, __NV_E5M2);
+    if (!isfinite(x0) || !isfinite(x1)) {
+        const uint32_t keep = isfinite(x0) ? 0x00ffu : isfinite(x1) ? 0xff00u : 0u;
+        h = (h & keep) | (0x7f7fu & ~keep);
+        m &= keep;
+        l &= keep;
     }
 }
 
@@ -375,15 +424,28 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
     tmem_wait_st();
 }
 
-// C of a position's scores, in powers of two relative to the rows' references;
+// Sixteen (or 32) of a position's scores as they come off the tensor core;
 // -infinity where the row does not see the position.
 template <int C>
-__device__ __forceinline__ void load_scores(uint32_t at, const float* negm, float mult, bool masked, unsigned long long seen, float (&s)[C])
+__device__ __forceinline__ void raw_scores(uint32_t at, bool masked, unsigned long long seen, float (&s)[C])
 {
 #pragma unroll
     for (int i = 0; i < C / 16; ++i)
         tmem_ld16(at + 16 * i, s + 16 * i);
     tmem_wait_ld();
+    if (masked) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            s[i] = (seen >> i) & 1 ? s[i] : -INFINITY;
+    }
+}
+
+// The same in powers of two relative to the rows' references.
+template <int C>
+__device__ __forceinline__ void relative_scores(uint32_t at, const float* negm, float mult, bool masked, unsigned long long seen,
+                                                float (&s)[C])
+{
+    raw_scores<C>(at, false, 0, s);
     const uint64_t m2 = f2_pack(mult, mult);
     const ulonglong2* nm = reinterpret_cast<const ulonglong2*>(negm);
 #pragma unroll
@@ -399,110 +461,101 @@ __device__ __forceinline__ void load_scores(uint32_t at, const float* negm, floa
     }
 }
 
-// What a row group's start needs besides Q: the rows' ancestors and places,
-// and which nodes' values are not finite (the rows that see them end as NaN;
-// the others must not meet them, see the products).  Returns whether the tree
-// is malformed.
-template <bool E4M3>
-__device__ __forceinline__ bool begin_rows(const AttnArgs& a, AttnShared& sh, const Run& run, int h, int g, int part, int w, int NT, int t)
+// C weights of a position: rounded to bf16 once, with the position's value
+// scale on them, into P; their sums.  A weight's rounding (a bf16 unit of
+// 2^-8) averages out over the positions.  ROUNDED sums take what P holds, so
+// that the rounding of a weight that dominates its row cancels; that costs
+// three instructions a pair, which the launches of few rows have to spare.
+template <int C, bool E4M3, bool ROUNDED>
+__device__ __forceinline__ void weigh(const float (&s)[C], float vscale, float vunscale, uint64_t* l2, unsigned char* p_row, int at, int t)
 {
-    const int lane = t & 31, bar = 1 + w, nn = run.s.nn, ctx = run.s.ctx;
-    const int mine = w == 0 ? min(a.half, a.rows) : a.rows - a.half, first = g * a.rows + w * a.half;
-    int par;
-    const bool bad = !tree_parents(a.parent + (long long)run.b * a.Nmax, a.has_parent, nn, lane, par);
-    if (t < 64) {
-        const int rr = first + t, node = rr / a.G;
-        int at = t < mine && rr < nn * a.G && !bad ? node : -1;
-        unsigned anc = 0;
-        for (int d = 0; d < kNodeMax && __any_sync(kFull, at >= 0); ++d) {
-            if (at >= 0)
-                anc |= 1u << at;
-            const int up = __shfl_sync(kFull, par, max(at, 0));
-            at = at >= 0 ? up : -1;
-        }
-        sh.anc[w][t] = anc;
-        sh.negm[w][t] = 0.0f;
-        sh.row_out[w][t] = t >= mine || rr >= a.Nmax * a.G ? -1
-                           : run.whole()                   ? (run.b * a.Nmax + node) * a.Hq + h * a.G + rr - node * a.G
-                                                           : part * a.rows + w * a.half + t;
-    }
-    if (t == 0) {
-        sh.poison[w] = 0;
-        sh.unset[w] = 0;
-    }
-    bar_sync(bar, 128);
-    if (nn > 1 && run.t1 * kTile > ctx) {
-        const int m = t >> 2, pos = ctx + m, bytes = a.c.D * (E4M3 ? 1 : 2);
-        bool hit = false;
-        if (m < nn && pos >= run.t0 * kTile && pos < run.t1 * kTile) {
-            const int page = kv_page(a.c, run.b, pos);
-            if (page >= 0) {
-                const long long row = kv_row(a.c, page, pos) + ((long long)h << a.c.page_shift);
-                const uint4* v = reinterpret_cast<const uint4*>(a.c.v + row * bytes);
-                for (int i = t & 3; i < bytes / 16; i += 4)
-                    hit |= chunk_nonfinite(v[i], E4M3);
-                if (E4M3)
-                    hit |= !isfinite(a.c.v_scale[row]);
+    const uint64_t v2 = f2_pack(vscale, vscale), u2 = f2_pack(vunscale, vunscale);
+#pragma unroll
+    for (int i = 0; i < C / 8; ++i) {
+        uint32_t x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint64_t e = f2_pack(ex2_approx(s[8 * i + 2 * k]), ex2_approx(s[8 * i + 2 * k + 1]));
+            if (!ROUNDED)
+                l2[4 * i + k] = f2_add(l2[4 * i + k], e);
+            if (E4M3)
+                e = f2_mul(e, v2);
+            float lo, hi;
+            f2_unpack(e, lo, hi);
+            x[k] = bf16_pair(lo, hi);
+            if (ROUNDED) {
+                const uint64_t r = f2_pack(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u));
+                l2[4 * i + k] = E4M3 ? f2_fma(r, u2, l2[4 * i + k]) : f2_add(r, l2[4 * i + k]);
             }
         }
-        if (hit)
-            atomicOr(&sh.poison[w], 1u << m);
-        bar_sync(bar, 128);
+        // P: rows of 64 of the CTA's N columns a position, swizzled
+        *reinterpret_cast<uint4*>(p_row + ((at + i) >> 3) * kHalfBytes + ((((at + i) ^ t) & 7) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
     }
-    return bad;
 }
 
-// Registers a thread: the softmax's warpgroups hold NT scores and NT sums a
-// thread, the others little; the shares add up to the launch's.
 __host__ __device__ constexpr int attn_threads(bool e4m3) { return e4m3 ? 512 : 384; }
 
+// Registers a thread: the softmax's warpgroups hold a row's sums and half of
+// its scores a thread, the others little.  The shares add up to the launch's.
 template <bool E4M3> constexpr int kAttnRegs = E4M3 ? 128 : 168;          // at launch
-template <bool E4M3> constexpr int kRegsSoftmax = E4M3 ? 168 : 208;       // warps 0 .. 7
-template <bool E4M3> constexpr int kRegsIssue = E4M3 ? 72 : 88;           // warps 8 .. 11
-constexpr int kRegsConvert = 104;                                         // warps 12 .. 15
+template <bool E4M3> constexpr int kRegsSoftmax = E4M3 ? 160 : 200;       // warps 0 .. 7
+template <bool E4M3> constexpr int kRegsIssue = E4M3 ? 96 : 104;          // warps 8 .. 11
+constexpr int kRegsConvert = 96;                                          // warps 12 .. 15
 static_assert(512 * kAttnRegs<true> == 256 * kRegsSoftmax<true> + 128 * kRegsIssue<true> + 128 * kRegsConvert &&
               384 * kAttnRegs<false> == 256 * kRegsSoftmax<false> + 128 * kRegsIssue<false>,
               "register shares");
 
 // NT: rows (TMEM columns) a softmax warpgroup handles; NWG: softmax
-// warpgroups with rows; E4M3: four more warps make bf16 operands of V.
+// warpgroups with rows.
 template <int NT, int NWG, bool E4M3>
 __global__ void __launch_bounds__(attn_threads(E4M3), 1)
     sv_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
-                        const __grid_constant__ CUtensorMap map_v)
+                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q)
 {
     constexpr int kThreads = attn_threads(E4M3), kWarps = kThreads / 32, N = NT * NWG;
     extern __shared__ __align__(1024) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = a.c.D;
     {
-    AttnShared& sh = *attn_layout<N, E4M3>(a, smem).sh;
-    if (warp == 8) {
-        tmem_alloc(smem_addr(&sh.tmem), 512);
-    } else if (tid == 9 * 32) {
-        sh.abort = 0;
-        for (int i = 0; i < a.kslots; ++i) {
-            mbar_init(smem_addr(&sh.kfull[i]), 1);
-            mbar_init(smem_addr(&sh.kempty[i]), 1);
+        const AttnLayout L = attn_layout<N, E4M3>(a, smem);
+        AttnShared& sh = *L.sh;
+        if (warp == 8) {
+            tmem_alloc(smem_addr(&sh.tmem), 512);
+        } else if (tid == 9 * 32) {
+            sh.abort = 0;
+            for (int i = 0; i < a.kslots; ++i) {
+                mbar_init(smem_addr(&sh.kfull[i]), 1);
+                mbar_init(smem_addr(&sh.kempty[i]), 1);
+            }
+            for (int i = 0; i < a.vslots; ++i) {
+                mbar_init(smem_addr(&sh.vfull[i]), 1);
+                mbar_init(smem_addr(&sh.vempty[i]), E4M3 ? 4 : 1);
+            }
+            for (int i = 0; i < kScaleSlots; ++i) {
+                mbar_init(smem_addr(&sh.sfull[i]), 1);
+                mbar_init(smem_addr(&sh.sempty[i]), 4 * NWG);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_addr(&sh.cfull[i]), 4);
+                mbar_init(smem_addr(&sh.cempty[i]), 1);
+                mbar_init(smem_addr(&sh.s_full[i]), 1);
+                mbar_init(smem_addr(&sh.s_empty[i]), 4 * NWG);
+                mbar_init(smem_addr(&sh.info_full[i]), 2);
+                mbar_init(smem_addr(&sh.info_empty[i]), 4 * NWG);
+            }
+            mbar_init(smem_addr(&sh.q_full), E4M3 ? 2 : 1);
+            mbar_init(smem_addr(&sh.q_empty), 1);
+            mbar_init(smem_addr(&sh.p_full), 4 * NWG);
+            mbar_init(smem_addr(&sh.o_full), 1);
+            mbar_init(smem_addr(&sh.drain), 1);
+            fence_mbar_init();
+            tma_prefetch_map(&map_k);
+            tma_prefetch_map(&map_v);
         }
-        for (int i = 0; i < a.vslots; ++i) {
-            mbar_init(smem_addr(&sh.vfull[i]), 1);
-            mbar_init(smem_addr(&sh.vempty[i]), E4M3 ? 4 : 1);
+        if (!E4M3) {   // the rows of no query stay zeros
+            for (int i = tid; i < N * 8 * ((D + 63) / 64); i += kThreads)
+                reinterpret_cast<uint4*>(L.q)[i] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async();
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&sh.cfull[i]), 4);
-            mbar_init(smem_addr(&sh.cempty[i]), 1);
-            mbar_init(smem_addr(&sh.s_full[i]), 1);
-            mbar_init(smem_addr(&sh.s_empty[i]), 4 * NWG);
-        }
-        mbar_init(smem_addr(&sh.q_full), 4 * NWG);
-        mbar_init(smem_addr(&sh.p_full), 4 * NWG);
-        mbar_init(smem_addr(&sh.o_full), 1);
-        mbar_init(smem_addr(&sh.drain), 1);
-        fence_mbar_init();
-        tma_prefetch_map(&map_k);
-        tma_prefetch_map(&map_v);
-    }
-    {
         // the CTA's run: tiles of all sequences before each thread's share of them
         const int share = (a.B + kThreads - 1) / kThreads, b0 = min(tid * share, a.B), b1 = min(b0 + share, a.B);
         const int per = a.c.Hkv * a.groups;
@@ -548,527 +601,645 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
             sh.active = i < act;
             a.meta[2 * i] = a.meta[2 * i + 1] = -1;
         }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    }
+
     // (The register moves stand inside the warpgroups' branches: ptxas budgets
     // what they dominate.)
     if (warp < 8) {
         regs_grow<kRegsSoftmax<E4M3>>();
         if (warp < 4 * NWG) {
-        // --- softmax: one position a thread, NT rows ------------------------------
+            // --- softmax: one position a thread, NT rows --------------------------
+            const AttnLayout L = attn_layout<N, E4M3>(a, smem);
+            AttnShared& sh = *L.sh;
+            Run run = run_of(a, sh);
+            const int w = warp >> 2, t = tid & 127, bar = 1 + w;
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t tmem = sh.tmem + lanes + w * NT, tmem_o = tmem + 2 * N;   // S (two buffers of N columns), then O
+            float* const scratch = sh.scratch[w];
+            float* const negm = sh.negm + w * NT;
+            uint32_t gt = 0, items = 0;   // tiles, items so far
+            Ring rs;
+            while (run.next(a, true)) {
+                const int ctx = run.s.ctx, nn = run.s.nn;
+                const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
+                const bool whole = run.whole();
+                if (!whole && tid == 0)   // meta[2i]: begun here, meta[2i + 1]: continued here
+                    a.meta[part ^ 1] = run.b * (a.c.Hkv * a.groups) + run.hg;
+                if (run.s.len == 0) {
+                    // no position, or unusable lengths: zeros, or NaN
+                    const int h = run.hg / a.groups, g = run.hg - h * a.groups;
+                    const float x = run.s.ok ? 0.0f : NAN;
+                    if (!run.s.ok && tid == 0 && a.has_err)
+                        atomicOr(a.err, kErrCache);
+                    for (int r = w * NT + (warp & 3); r < min(a.rows, (w + 1) * NT); r += 4) {
+                        int node, head;
+                        if (attn_row(a, g, r, node, head))
+                            for (int d = lane; d < D; d += 32)
+                                a.out[(((long long)run.b * a.Nmax + node) * a.Hq + h * a.G + head) * D + d] =
+                                    __float2bfloat16_rn(node < nn ? x : 0.0f);
+                    }
+                    continue;
+                }
+                const ItemInfo& info = sh.info[items & 1];
+                cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
+                const unsigned poison = info.poison;
+                const float scale_log2 = E4M3 ? a.scale_log2 * info.q_unscale : a.scale_log2;
+                if (t < NT)
+                    negm[t] = 0.0f;   // read by others after the first vote only
+                if (t == 0)
+                    sh.unset[w] = 0;
+                bool plain = true;    // every reference is zero
+                uint64_t l2[NT / 2];  // this thread's share of the rows' sums, in pairs
+#pragma unroll
+                for (int i = 0; i < NT / 2; ++i)
+                    l2[i] = 0;
+
+                for (int j = run.t0; j < run.t1; ++j, ++gt) {
+                    const bool first_tile = j == run.t0;
+                    float mult = scale_log2, vscale = 1.0f, vunscale = 1.0f;
+                    if (E4M3) {
+                        cta_wait(sh, &sh.sfull[rs.slot], rs.phase);
+                        const float ks = sh.scale[rs.slot][0][t];
+                        vscale = sh.scale[rs.slot][1][t];
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_addr(&sh.sempty[rs.slot]));
+                        rs.step(kScaleSlots);
+                        // a scale that is not finite marks a row that held something that was not
+                        mult *= isfinite(ks) ? ks : NAN;
+                        vscale = isfinite(vscale) ? vscale : NAN;
+                        vscale = fabsf(vscale) < 0x1p-100f ? 0x1p-100f : vscale;   // (all of such a row's values are zero in the sum)
+                    }
+                    // what this position's scores are seen by: every row in the context, a node's descendants behind it
+                    const bool tail = (j + 1) * kTile > ctx;   // the tile holds nodes, or ends the sequence
+                    unsigned long long seen = ~0ull;
+                    if (tail) {
+                        const int m = j * kTile + t - ctx;
+                        if (m >= 0) {
+                            seen = 0;
+                            if (m < nn && !((poison >> m) & 1u)) {
+#pragma unroll 4
+                                for (int i = 0; i < NT; ++i)
+                                    seen |= (unsigned long long)((info.anc[w * NT + i] >> m) & 1u) << i;
+                            } else {   // nothing sees it: its scales may be anything
+                                vscale = 1.0f;
+                                mult = scale_log2;
+                            }
+                        }
+                    }
+                    if (E4M3 && NWG == 1)
+                        vunscale = __frcp_rn(vscale);
+                    const uint32_t s_at = tmem + (gt & 1) * N;
+                    constexpr int C = NT % 32 ? 16 : 32;
+
+                    cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
+                    tc_fence_after();
+                    // are all scores near enough to the references?  (A second look at TMEM is cheaper than the
+                    // registers that would keep the scores over the vote.)
+                    if (plain) {
+                        float top = -INFINITY, low = INFINITY;
+#pragma unroll
+                        for (int c = 0; c < NT; c += C) {
+                            float s[C];
+                            raw_scores<C>(s_at + c, tail, seen >> c, s);
+#pragma unroll
+                            for (int i = 0; i < C; i += 2)
+                                top = max3(top, s[i], s[i + 1]);
+                            if (first_tile) {
+#pragma unroll
+                                for (int i = 0; i < C; i += 2)
+                                    low = min3(low, s[i], s[i + 1]);
+                            }
+                        }
+                        plain = !bar_any(bar, 128, top * mult > kLazy || mult < 0.0f);
+                        if (first_tile)   // zero will do as a reference if some position's scores are all near enough
+                            plain = bar_any(bar, 128, low * mult >= -kLazy) && plain;
+                    }
+                    if (!first_tile) {   // the previous tile's product is done with P (and O)
+                        cta_wait(sh, &sh.o_full, (gt - 1) & 1);
+                        tc_fence_after();
+                    }
+                    unsigned char* const p_row = L.p + t * 128;
+                    if (plain) {
+#pragma unroll
+                        for (int c = 0; c < NT; c += C) {
+                            float s[C];
+                            raw_scores<C>(s_at + c, false, 0, s);
+                            const uint64_t m2 = f2_pack(mult, mult);
+#pragma unroll
+                            for (int i = 0; i < C; i += 2)
+                                f2_unpack(f2_mul(f2_pack(s[i], s[i + 1]), m2), s[i], s[i + 1]);
+                            if (tail) {
+#pragma unroll
+                                for (int i = 0; i < C; ++i)
+                                    s[i] = (seen >> (c + i)) & 1 ? s[i] : -INFINITY;
+                            }
+                            weigh<C, E4M3, NWG == 1>(s, vscale, vunscale, l2 + c / 2, p_row, (w * NT + c) / 8, t);
+                        }
+                    } else {
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < NT; c += 16) {
+                            float s[16];
+                            relative_scores<16>(s_at + c, negm + c, mult, tail, seen >> c, s);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2)
+                                top = max3(top, s[i], s[i + 1]);
+                        }
+                        // +0 marks a row without a reference: a part that was plain until now has them all (zeros)
+                        if (!first_tile && t < NT && __float_as_uint(negm[t]) == 0u && !sh.unset[w])
+                            negm[t] = -0.0f;
+                        if (bar_any(bar, 128, top > kLazy || first_tile) || sh.unset[w]) {
+                            move_references<NT>(scratch, negm, &sh.unset[w], s_at, tmem_o, first_tile ? 0 : a.nd, N, mult, seen, t, bar);
+#pragma unroll
+                            for (int i = 0; i < NT / 4; ++i) {
+                                const ulonglong2 f4 = reinterpret_cast<const ulonglong2*>(scratch)[i];
+                                l2[2 * i] = f2_mul(l2[2 * i], f4.x);
+                                l2[2 * i + 1] = f2_mul(l2[2 * i + 1], f4.y);
+                            }
+                            bar_sync(bar, 128);   // the scratch may be written again
+                        }
+#pragma unroll
+                        for (int c = 0; c < NT; c += 16) {
+                            float s[16];
+                            relative_scores<16>(s_at + c, negm + c, mult, tail, seen >> c, s);
+                            weigh<16, E4M3, NWG == 1>(s, vscale, vunscale, l2 + c / 2, p_row, (w * NT + c) / 8, t);
+                        }
+                    }
+                    tc_fence_before();
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&sh.s_empty[gt & 1]));
+                        mbar_arrive(smem_addr(&sh.p_full));
+                    }
+                }
+
+                // the rows' sums over the 128 threads, while the last product runs
+                float sum[NT / 16];
+#pragma unroll
+                for (int i = 0; i < NT / 16; ++i) {
+                    // lane c (of 16) ends with column 16 i + c: halve the columns, double the lanes summed
+                    float x[16];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        f2_unpack(l2[8 * i + k], x[2 * k], x[2 * k + 1]);
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                        for (int k = 0; k < o; ++k) {
+                            const bool up = lane & o;
+                            const float send = up ? x[k] : x[k + o];
+                            const float keep = up ? x[k + o] : x[k];
+                            x[k] = keep + __shfl_xor_sync(kFull, send, o);
+                        }
+                    sum[i] = x[0] + __shfl_xor_sync(kFull, x[0], 16);
+                }
+#pragma unroll
+                for (int i = 0; i < NT / 16; ++i)
+                    if (lane < 16)
+                        scratch[(warp & 3) * NT + 16 * i + lane] = sum[i];
+                bar_sync(bar, 128);
+                float* const fin = scratch + 4 * NT;
+                const bool abort = *reinterpret_cast<volatile int*>(&sh.abort) != 0, bad = info.bad || abort;
+                if (t == 0 && bad && a.has_err)
+                    atomicOr(a.err, abort ? kErrWaitTimeout : kErrCache);
+                if (t < NT) {
+                    const unsigned anc = info.anc[w * NT + t];
+                    float l = (scratch[t] + scratch[NT + t]) + (scratch[2 * NT + t] + scratch[3 * NT + t]);
+                    if (bad || (anc & poison))
+                        l = NAN;
+                    fin[t] = !whole ? 1.0f : l == 0.0f || anc == 0 ? 0.0f : 1.0f / l;   // (anc == 0: no node's row)
+                    const int at = info.row_out[w * NT + t];
+                    if (!whole && at >= 0) {
+                        a.part_ml[(long long)at * 2] = -negm[t];
+                        a.part_ml[(long long)at * 2 + 1] = l;
+                    }
+                }
+                cta_wait(sh, &sh.o_full, (gt - 1) & 1);
+                tc_fence_after();
+                bar_sync(bar, 128);
+                for (int c = 0; c < a.nd; ++c) {
+                    const int d = 128 * c + (E4M3 ? converted_element(t) : t);
+#pragma unroll 1
+                    for (int i = 0; i < NT; i += 16) {
+                        float o[16];
+                        tmem_ld16(tmem_o + c * N + i, o);
+                        tmem_wait_ld();
+                        if (d < D) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int at = info.row_out[w * NT + i + k];
+                                const float f = fin[i + k];
+                                if (at >= 0) {
+                                    if (whole)
+                                        a.out[(long long)at * D + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : o[k] * f);
+                                    else
+                                        a.part_o[(long long)at * D + d] = o[k];
+                                }
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                bar_sync(bar, 128);   // O, the scratch and the item's rows have been read
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sh.info_empty[items & 1]));
+                ++items;
+            }
+        }
+    } else if (E4M3 && warp >= 12) {
+        regs_shrink<kRegsConvert>();
+        // --- e4m3 values to bf16 operands -------------------------------------------
+        // A thread takes one position's row: rows of a warp differ in their
+        // swizzle, so neither the loads nor the stores collide.
         const AttnLayout L = attn_layout<N, E4M3>(a, smem);
         AttnShared& sh = *L.sh;
-        Run run = run_of(a, sh);
-        const uint32_t tmem = sh.tmem, tmem_o = tmem + 2 * N;   // S (two buffers of N columns), then O
-        const int w = warp >> 2, t = tid & 127, bar = 1 + w;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        float* const scratch = sh.scratch[w];
-        float* const negm = sh.negm[w];
-        uint32_t n_tiles = 0;
-        while (run.next(a)) {
-            const int h = run.hg / a.groups, g = run.hg - h * a.groups;
-            const int ctx = run.s.ctx, nn = run.s.nn, len = run.s.len;
-            const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
-            if (!run.whole() && t == 0 && w == 0)   // meta[2i]: begun here, meta[2i + 1]: continued here
-                a.meta[part ^ 1] = run.b * (a.c.Hkv * a.groups) + run.hg;
-            // row c of this warpgroup: row `w * half + c` of the group
-            const int mine = w == 0 ? min(a.half, a.rows) : a.rows - a.half, first = g * a.rows + w * a.half;
-            if (len == 0) {
-                // no position, or unusable lengths: zeros, or NaN
-                const float x = run.s.ok ? 0.0f : NAN;
-                if (!run.s.ok && t == 0 && w == 0 && a.has_err)
-                    atomicOr(a.err, kErrCache);
-                for (int i = t; i < mine * D; i += 128) {
-                    const int rr = first + i / D, node = rr / a.G;
-                    if (rr < a.Nmax * a.G)
-                        a.out[(((long long)run.b * a.Nmax + node) * a.Hq + h * a.G + rr - node * a.G) * D + i % D] =
-                            __float2bfloat16_rn(node < nn ? x : 0.0f);
-                }
-                continue;
-            }
-            // queries to shared memory, swizzled as the product reads them
-            float q_unscale = 1.0f;
-            {
-                const int per = (E4M3 ? 128 * a.nd : (D + 63) & ~63) / 8;
-                auto load_q = [&](int i) {
-                    const int row = i / per, ch = i - row * per, rr = first + row;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (row < mine && rr < nn * a.G && 8 * ch < D) {
-                        const int node = rr / a.G;
-                        x = __ldg(reinterpret_cast<const uint4*>(a.q + ((long long)run.b * a.Nmax + node) * a.q_stride +
-                                                                 (long long)(h * a.G + rr - node * a.G) * D) + ch);
+        Tiles it;
+        it.start(a, run_of(a, sh));
+        Ring r, w;
+        const int t = tid - 384, key = t & 7;
+        for (; it.more; it.step(a)) {
+            const int valid = it.valid(), rows = (valid + 15) & ~15;
+            const int node0 = it.run.s.nn > 1 ? it.run.s.ctx - it.j * kTile : kTile;   // first row of a node
+            bool go = true;
+            for (int c = 0; go && c < a.nd; ++c) {
+                go = cta_wait(sh, &sh.vfull[r.slot], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
+                if (!go)
+                    break;
+                const unsigned char* src = L.v + r.slot * a.v_bytes + t * 128;
+                unsigned char* dst = L.c + w.slot * a.conv_bytes + t * 128;
+                if (t < rows) {
+                    const int pieces = min(128, D - 128 * c) / 16;
+#pragma unroll 4
+                    for (int i = 0; i < pieces; ++i) {
+                        uint4 x = *reinterpret_cast<const uint4*>(src + ((i ^ key) << 4));
+                        const bool nan = chunk_nan_e4m3(x);
+                        if (t >= valid || (nan && t >= node0))
+                            x = make_uint4(0, 0, 0, 0);
+                        uint2 y0 = e4m3_to_bf16(x.x), y1 = e4m3_to_bf16(x.y), y2 = e4m3_to_bf16(x.z), y3 = e4m3_to_bf16(x.w);
+                        if (nan) {
+                            y0 = e4m3_keep_nan(x.x, y0);
+                            y1 = e4m3_keep_nan(x.y, y1);
+                            y2 = e4m3_keep_nan(x.z, y2);
+                            y3 = e4m3_keep_nan(x.w, y3);
+                        }
+                        unsigned char* o = dst + (i >> 2) * kHalfBytes;
+                        const int ch = 2 * (i & 3);
+                        *reinterpret_cast<uint4*>(o + ((ch ^ key) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
+                        *reinterpret_cast<uint4*>(o + (((ch + 1) ^ key) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
                     }
-                    return x;
-                };
-                float scale = 1.0f;
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&sh.vempty[r.slot]));
+                    mbar_arrive(smem_addr(&sh.cfull[w.slot]));
+                }
+                r.step(a.vslots);
+                w.step(a.conv);
+            }
+            if (!go)
+                break;
+        }
+    } else {
+        regs_shrink<kRegsIssue<E4M3>>();
+        const AttnLayout L = attn_layout<N, E4M3>(a, smem);
+        AttnShared& sh = *L.sh;
+        if (warp == 9) {
+            // --- TMA -------------------------------------------------------------------
+            Ring rk, rv, rs;
+            int nk = 0, nv = 0, ns = 0, nq = 0;   // slots that may still be filling
+            uint32_t items = 0;
+            const int boxes = kTile / a.box_rows;
+            Tiles k, v;
+            k.start(a, run_of(a, sh));
+            v = k;
+            // lane l: row of a tile's box l, -1 where it holds no position (or its page is unusable)
+            auto box_row = [&](const Tiles& x) {
+                const int pos = x.j * kTile + lane * a.box_rows;
+                if (!x.more || lane >= boxes || pos >= x.run.s.len)
+                    return -1;
+                const int page = kv_page(a.c, x.run.b, pos);
+                return page < 0 ? -1 : (int)kv_row(a.c, page, pos) + ((x.run.hg / a.groups) << a.c.page_shift);
+            };
+            // rows of the tiles of the next V (two, in order) and of the K after the next
+            int row_v = -1, row_k = box_row(k);
+            bool go = true;
+            auto load = [&](bool is_k, int row, Ring& r, int slots) {
+                const unsigned have = __ballot_sync(kFull, row >= 0);
+                for (int c = 0; c < a.nd; ++c) {
+                    if (!cta_wait(sh, is_k ? &sh.kempty[r.slot] : &sh.vempty[r.slot], r.phase ^ 1))
+                        return false;
+                    const uint32_t bar = smem_addr(is_k ? &sh.kfull[r.slot] : &sh.vfull[r.slot]);
+                    const uint32_t dst = (is_k ? smem_addr(L.k) + r.slot * a.k_bytes : smem_addr(L.v) + r.slot * a.v_bytes) + lane * a.box_rows * 128;
+                    const int halves = E4M3 ? 1 : min(2, (D - 128 * c + 63) / 64);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar, __popc(have) * a.box_rows * 128 * halves);
+                    __syncwarp();
+                    if (row >= 0)
+                        for (int x = 0; x < halves; ++x)
+                            tma_load_2d(dst + x * kHalfBytes, is_k ? &map_k : &map_v, 128 * c + 64 * x, row, bar);
+                    r.step(slots);
+                    int& filling = is_k ? nk : nv;
+                    filling = min(filling + 1, slots);
+                }
+                return true;
+            };
+            while (go && v.more) {
+                if (k.more) {
+                    if (!E4M3 && k.j == k.run.t0) {   // a new item: its queries
+                        go = cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
+                        if (!go)
+                            break;
+                        ++items;
+                        nq = 1;
+                        if (lane == 0) {
+                            const int h = k.run.hg / a.groups, g = k.run.hg - h * a.groups, nb = g / a.head_blocks;
+                            mbar_arrive_expect_tx(smem_addr(&sh.q_full), a.rows * 128 * ((D + 63) / 64));
+                            for (int c = 0; c < (D + 63) / 64; ++c)
+                                tma_load_3d(smem_addr(L.q) + c * (N * 128), &map_q, 64 * c, h * a.G + (g - nb * a.head_blocks) * a.heads,
+                                            k.run.b * a.Nmax + nb * a.nodes, smem_addr(&sh.q_full));
+                        }
+                        __syncwarp();
+                    }
+                    go = load(true, row_k, rk, a.kslots);
+                    if (go && E4M3) {
+                        go = cta_wait(sh, &sh.sempty[rs.slot], rs.phase ^ 1);
+                        if (go) {
+                            const uint32_t bar = smem_addr(&sh.sfull[rs.slot]);
+                            const unsigned have = __ballot_sync(kFull, row_k >= 0);
+                            if (lane == 0)
+                                mbar_arrive_expect_tx(bar, __popc(have) * a.box_rows * 8);
+                            __syncwarp();
+                            if (row_k >= 0) {
+                                bulk_copy_g2s(smem_addr(&sh.scale[rs.slot][0][lane * a.box_rows]), a.c.k_scale + row_k, a.box_rows * 4, bar);
+                                bulk_copy_g2s(smem_addr(&sh.scale[rs.slot][1][lane * a.box_rows]), a.c.v_scale + row_k, a.box_rows * 4, bar);
+                            }
+                            rs.step(kScaleSlots);
+                            ns = min(ns + 1, kScaleSlots);
+                        }
+                    }
+                    if (!go)
+                        break;
+                }
+                // K runs one tile ahead of V
+                const bool first = v.j == k.j && v.run.hg == k.run.hg && v.run.b == k.run.b && k.more;
+                const int row_now = row_k;
+                if (k.more) {
+                    k.step(a);
+                    row_k = box_row(k);
+                }
+                if (!first) {
+                    go = load(false, row_v, rv, a.vslots);
+                    v.step(a);
+                }
+                row_v = row_now;
+            }
+            if (!go) {   // copies in flight land before the CTA's memory is given back
+                for (; nk > 0; --nk) {
+                    rk.back(a.kslots);
+                    mbar_wait_bounded(smem_addr(&sh.kfull[rk.slot]), rk.phase, kWaitSpins);
+                }
+                for (; nv > 0; --nv) {
+                    rv.back(a.vslots);
+                    mbar_wait_bounded(smem_addr(&sh.vfull[rv.slot]), rv.phase, kWaitSpins);
+                }
+                for (; ns > 0; --ns) {
+                    rs.back(kScaleSlots);
+                    mbar_wait_bounded(smem_addr(&sh.sfull[rs.slot]), rs.phase, kWaitSpins);
+                }
+                if (nq)
+                    mbar_wait_bounded(smem_addr(&sh.q_full), (items - 1) & 1, kWaitSpins);
+            }
+        } else if (warp == 8) {
+            // --- MMA issue -------------------------------------------------------------
+            const uint32_t tmem = sh.tmem, tmem_o = tmem + 2 * N;
+            Ring rk, rv;
+            uint32_t gk = 0, gv = 0, items = 0, vitems = 0;   // tiles of K and V so far; items
+            const int vring = E4M3 ? a.conv : a.vslots;
+            const uint32_t k0 = smem_addr(L.k), v0 = smem_addr(E4M3 ? L.c : L.v), v_bytes = E4M3 ? a.conv_bytes : a.v_bytes;
+            const uint32_t q0 = smem_addr(L.q), p0 = smem_addr(L.p);
+            uint64_t* const vfull = E4M3 ? sh.cfull : sh.vfull;
+            uint64_t* const vempty = E4M3 ? sh.cempty : sh.vempty;
+            Tiles k, v;
+            k.start(a, run_of(a, sh));
+            v = k;
+            bool go = true;
+            while (go && v.more) {
+                if (k.more) {
+                    if (k.j == k.run.t0)
+                        go = cta_wait(sh, &sh.q_full, items++ & 1);
+                    go = go && cta_wait(sh, &sh.s_empty[gk & 1], ((gk >> 1) & 1) ^ 1);
+                    for (int c = 0; go && c < a.nd; ++c) {
+                        const int width = min(128, D - 128 * c);
+                        go = cta_wait(sh, &sh.kfull[rk.slot], rk.phase);
+                        if (!go)
+                            break;
+                        tc_fence_after();
+                        if (lane == 0) {
+                            mma_scores<N, E4M3>(tmem + (gk & 1) * N, k0 + rk.slot * a.k_bytes, q0 + (E4M3 ? c : 2 * c) * (N * 128), L.q_part,
+                                                E4M3 ? (width + 31) / 32 : width / 16, c > 0);
+                            tc_commit(smem_addr(&sh.kempty[rk.slot]));
+                            if (c == a.nd - 1) {
+                                tc_commit(smem_addr(&sh.s_full[gk & 1]));
+                                if (k.j == k.run.t1 - 1)
+                                    tc_commit(smem_addr(&sh.q_empty));
+                            }
+                        }
+                        __syncwarp();
+                        rk.step(a.kslots);
+                    }
+                    if (!go)
+                        break;
+                    ++gk;
+                    k.step(a);
+                    if (gk == 1 && k.more)
+                        continue;   // K runs one tile ahead of V
+                }
+                const int valid = v.valid(), ksteps = (valid + 15) / 16;
+                const bool tail = (v.j + 1) * kTile > v.run.s.ctx;
+                for (int c = 0; go && c < a.nd; ++c) {
+                    const int width = min(128, D - 128 * c);
+                    go = cta_wait(sh, &vfull[rv.slot], rv.phase);
+                    if (!go)
+                        break;
+                    if (!E4M3 && tail) {
+                        // rows behind the last position may hold anything: zeros instead of 0 * NaN.  A node's
+                        // values are seen by some rows only: what is not finite there is zeroed too (the rows
+                        // that do see it are set to NaN at the end).
+                        unsigned char* x = L.v + rv.slot * a.v_bytes;
+                        const int chunks = width > 64 ? 16 : 8;
+                        for (int i = valid * chunks + lane; i < ksteps * 16 * chunks; i += 32) {
+                            const int row = i / chunks, ch = i % chunks;
+                            *reinterpret_cast<uint4*>(x + (ch >> 3) * kHalfBytes + row * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        go = cta_wait(sh, &sh.info_full[vitems & 1], (vitems >> 1) & 1);
+                        if (!go)
+                            break;
+                        const int row = v.run.s.ctx + lane - v.j * kTile;
+                        if (((sh.info[vitems & 1].poison >> lane) & 1u) && row >= 0 && row < kTile)
+                            for (int ch = 0; ch < chunks; ++ch) {
+                                uint4* p = reinterpret_cast<uint4*>(x + (ch >> 3) * kHalfBytes + row * 128 + ((ch ^ lane) & 7) * 16);
+                                if (chunk_nonfinite(*p, false))
+                                    *p = make_uint4(0, 0, 0, 0);
+                            }
+                        fence_proxy_async();
+                        __syncwarp();
+                    }
+                    if (c == 0) {
+                        go = cta_wait(sh, &sh.p_full, gv & 1);
+                        if (!go)
+                            break;
+                    }
+                    tc_fence_after();
+                    if (lane == 0) {
+                        mma_values<N>(tmem_o + c * N, v0 + rv.slot * v_bytes, p0, width > 64 ? kHalfBytes : 0, ksteps, v.j > v.run.t0);
+                        if (c == a.nd - 1)
+                            tc_commit(smem_addr(&sh.o_full));
+                        tc_commit(smem_addr(&vempty[rv.slot]));
+                    }
+                    __syncwarp();
+                    rv.step(vring);
+                }
+                ++gv;
+                if (v.j == v.run.t1 - 1)
+                    ++vitems;
+                v.step(a);
+            }
+            if (!go) {   // products in flight end before TMEM is given back
+                if (lane == 0)
+                    tc_commit(smem_addr(&sh.drain));
+                __syncwarp();
+                mbar_wait_bounded(smem_addr(&sh.drain), 0, kWaitSpins);
+            }
+        } else {
+            // --- the next item: its rows, its queries (e4m3) -----------------------------
+            const int t = tid - 320, bar = 3;   // 64 threads
+            Run run = run_of(a, sh);
+            uint32_t items = 0;
+            while (run.next(a)) {
+                ItemInfo& info = sh.info[items & 1];
+                if (!cta_wait(sh, &sh.info_empty[items & 1], ((items >> 1) & 1) ^ 1))
+                    sh.abort = 1;   // (the two warps share a barrier: both go on)
+                const int h = run.hg / a.groups, g = run.hg - h * a.groups, nn = run.s.nn, ctx = run.s.ctx;
+                const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
+                int par;
+                const bool tree = tree_parents(a.parent + (long long)run.b * a.Nmax, a.has_parent, nn, lane, par);
+                if (t == 0) {
+                    info.poison = 0;
+                    info.bad = !tree;
+                }
+                for (int r = t; r < 128; r += 64) {
+                    int node = 0, head = 0;
+                    const bool real = r < N && attn_row(a, g, r, node, head);
+                    int at = real && node < nn && tree ? node : -1;
+                    unsigned anc = 0;
+                    for (int d = 0; d < kNodeMax && __any_sync(kFull, at >= 0); ++d) {
+                        if (at >= 0)
+                            anc |= 1u << at;
+                        const int up = __shfl_sync(kFull, par, max(at, 0));
+                        at = at >= 0 ? up : -1;
+                    }
+                    // (a malformed tree's rows end as NaN, whatever they see)
+                    info.anc[r] = real && node < nn && !tree ? ~0u : anc;
+                    info.row_out[r] = !real         ? -1
+                                      : run.whole() ? (run.b * a.Nmax + node) * a.Hq + h * a.G + head
+                                                    : part * a.rows + r;
+                }
+                bar_sync(bar, 64);
+                {
+                    // the part's pages; its nodes' values
+                    bool bad = false;
+                    const int p1 = min(run.t1 * kTile, run.s.len);
+                    for (int pos = run.t0 * kTile + (t << a.c.page_shift); pos < p1; pos += 64 << a.c.page_shift)
+                        bad |= kv_page(a.c, run.b, pos) < 0;
+                    if (bad)
+                        info.bad = 1;
+                    const int m = t >> 1, pos = ctx + m, bytes = D * (E4M3 ? 1 : 2);
+                    if (nn > 1 && m < nn && pos >= run.t0 * kTile && pos < run.t1 * kTile) {
+                        const int page = kv_page(a.c, run.b, pos);
+                        if (page >= 0) {
+                            const long long row = kv_row(a.c, page, pos) + ((long long)h << a.c.page_shift);
+                            const uint4* x = reinterpret_cast<const uint4*>(a.c.v + row * bytes);
+                            bool hit = E4M3 && !isfinite(a.c.v_scale[row]);
+#pragma unroll 4
+                            for (int i = t & 1; i < bytes / 16; i += 2)
+                                hit |= chunk_nonfinite(x[i], E4M3);
+                            if (hit)
+                                atomicOr(&info.poison, 1u << m);
+                        }
+                    }
+                }
                 if (E4M3) {
+                    const int per = D / 8;
+                    auto load_q = [&](int i, int& row, int& ch) {
+                        row = i / per;
+                        ch = i - row * per;
+                        int node, head;
+                        if (!attn_row(a, g, row, node, head) || node >= nn)
+                            return make_uint4(0, 0, 0, 0);
+                        return __ldg(reinterpret_cast<const uint4*>(a.q + ((long long)run.b * a.Nmax + node) * a.q_stride +
+                                                                    (long long)(h * a.G + head) * D) + ch);
+                    };
                     // a power of two that brings the group's largest element to [128, 256)
                     float top = 0.0f;
-                    for (int i = t; i < mine * per; i += 128) {
+                    int row, ch;
+#pragma unroll 4
+                    for (int i = t; i < a.rows * per; i += 64) {
                         float y[8];
-                        Elem<__nv_bfloat16>::unpack(load_q(i), y);
+                        Elem<__nv_bfloat16>::unpack(load_q(i, row, ch), y);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             top = fmaxf(top, isfinite(y[k]) ? fabsf(y[k]) : 0.0f);
                     }
                     top = warp_redux_max(top);
                     if (lane == 0)
-                        sh.top[w][warp & 3] = top;
-                    bar_sync(bar, 128);
-                    top = fmaxf(fmaxf(sh.top[w][0], sh.top[w][1]), fmaxf(sh.top[w][2], sh.top[w][3]));
+                        sh.top[warp - 10] = top;
+                    bar_sync(bar, 64);
+                    top = fmaxf(sh.top[0], sh.top[1]);
                     const int e = top > 0.0f ? min(max(261 - (int)(__float_as_uint(top) >> 23), 1), 253) : 127;
-                    scale = __uint_as_float((uint32_t)e << 23);
-                    q_unscale = __uint_as_float((uint32_t)(254 - e) << 23);
-                }
-                for (int i = t; i < NT * per; i += 128) {
-                    const int row = i / per, ch = i - row * per, at = w * NT + row;
-                    const uint4 x = load_q(i);
-                    if (E4M3) {
-                        float y[8];
-                        Elem<__nv_bfloat16>::unpack(x, y);
-                        uint32_t p[3][2] = {};
+                    const float scale = __uint_as_float((uint32_t)e << 23);
+                    if (t == 0)
+                        info.q_unscale = __uint_as_float((uint32_t)(254 - e) << 23);
+                    cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
+                    const int wide = 16 * a.nd;   // chunks of 8 elements a row, with the padding
+                    for (int i = t; i < N * wide; i += 64) {   // zeros where there is no element
+                        const int rr = i / wide, cc = i - rr * wide;
+                        if (rr >= a.rows || cc >= per) {
+                            unsigned char* o = L.q + (cc >> 4) * (N * 128) + rr * 128 + ((((cc & 15) >> 1) ^ (rr & 7)) << 4) + (cc & 1) * 8;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            uint32_t u, v, z;
-                            split_q(y[k] * scale, u, v, z);
-                            p[0][k >> 2] |= u << (8 * (k & 3));
-                            p[1][k >> 2] |= v << (8 * (k & 3));
-                            p[2][k >> 2] |= z << (8 * (k & 3));
+                            for (int k = 0; k < 3; ++k)
+                                *reinterpret_cast<uint2*>(o + k * L.q_part) = make_uint2(0, 0);
                         }
-                        unsigned char* o = L.q + (ch >> 4) * (N * 128) + at * 128 + ((((ch & 15) >> 1) ^ (at & 7)) << 4) + (ch & 1) * 8;
+                    }
+#pragma unroll 2
+                    for (int i = t; i < a.rows * per; i += 64) {
+                        float y[8];
+                        Elem<__nv_bfloat16>::unpack(load_q(i, row, ch), y);
+                        uint32_t p[3][4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            split_q(y[2 * k] * scale, y[2 * k + 1] * scale, p[0][k], p[1][k], p[2][k]);
+                        unsigned char* o = L.q + (ch >> 4) * (N * 128) + row * 128 + ((((ch & 15) >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
 #pragma unroll
                         for (int k = 0; k < 3; ++k)
-                            *reinterpret_cast<uint2*>(o + k * L.q_part) = make_uint2(p[k][0], p[k][1]);
-                    } else {
-                        *reinterpret_cast<uint4*>(L.q + (ch >> 3) * (N * 128) + at * 128 + (((ch & 7) ^ (at & 7)) << 4)) = x;
-                    }
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.q_full));
-            }
-            bool bad = begin_rows<E4M3>(a, sh, run, h, g, part, w, NT, t);
-            const unsigned poison = sh.poison[w];
-            const float scale_log2 = E4M3 ? a.scale_log2 * q_unscale : a.scale_log2;
-
-            uint64_t l2[NT / 2];   // this thread's share of the rows' sums, in pairs
-#pragma unroll
-            for (int i = 0; i < NT / 2; ++i)
-                l2[i] = 0;
-            // pages and scales one tile ahead
-            float ks = 1.0f, vs = 1.0f, ks_next = 1.0f, vs_next = 1.0f;
-            auto page_of = [&](int j) {
-                const int pos = j * kTile + t;
-                return j < run.t1 && pos < len ? kv_page(a.c, run.b, pos) : 0;
-            };
-            auto scales_of = [&](int j, int pg, float& k, float& v) {
-                if (E4M3) {
-                    const int pos = j * kTile + t;
-                    k = v = 0.0f;
-                    if (j < run.t1 && pos < len && pg >= 0) {
-                        const long long row = kv_row(a.c, pg, pos) + ((long long)h << a.c.page_shift);
-                        k = a.c.k_scale[row];
-                        v = a.c.v_scale[row];
-                    }
-                }
-            };
-            int page = page_of(run.t0), page_next = page_of(run.t0 + 1);
-            scales_of(run.t0, page, ks, vs);
-
-            for (int j = run.t0; j < run.t1; ++j) {
-                const uint32_t gt = n_tiles + (j - run.t0);
-                bad |= page < 0;
-                scales_of(j + 1, page_next, ks_next, vs_next);
-                page = page_next;
-                page_next = page_of(j + 2);
-                const bool first_tile = j == run.t0;
-                // a scale that is not finite marks a row that held something that was not
-                const float mult = E4M3 ? scale_log2 * (isfinite(ks) ? ks : NAN) : scale_log2;
-                float vscale = E4M3 ? (isfinite(vs) ? vs : NAN) : 1.0f;
-
-                cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
-                tc_fence_after();
-                const uint32_t s_at = tmem + lanes + (gt & 1) * N + w * NT;
-                // what this position's scores are seen by: every row in the context, a node's descendants behind it
-                const bool tail = (j + 1) * kTile > ctx;   // the tile holds nodes, or ends the sequence
-                unsigned long long seen = ~0ull;
-                if (tail) {
-                    const int m = j * kTile + t - ctx;
-                    if (m >= 0) {
-                        seen = 0;
-                        if (m < nn && !((poison >> m) & 1u)) {
-#pragma unroll 4
-                            for (int i = 0; i < NT; ++i)
-                                seen |= (unsigned long long)((sh.anc[w][i] >> m) & 1u) << i;
-                        } else {
-                            vscale = 0.0f;
-                        }
-                    }
-                }
-                // are all scores near enough to the references?  (A second look at TMEM is cheaper than the
-                // registers that would keep the scores over the vote.)
-                constexpr int C = NT % 32 ? 16 : 32;
-                float top = -INFINITY, low = INFINITY;
-#pragma unroll
-                for (int c = 0; c < NT; c += C) {
-                    float s[C];
-                    load_scores<C>(s_at + c, negm + c, mult, tail, seen >> c, s);
-#pragma unroll
-                    for (int i = 0; i < C; i += 2)
-                        top = max3(top, s[i], s[i + 1]);
-                    if (first_tile) {
-#pragma unroll
-                        for (int i = 0; i < C; i += 2)
-                            low = min3(low, s[i], s[i + 1]);
-                    }
-                }
-                bool move = bar_any(bar, 128, top > kLazy) || sh.unset[w];
-                if (first_tile) {
-                    // no reference yet: zero will do if some position's scores are all near enough
-                    move = !bar_any(bar, 128, low >= -kLazy) || move;
-                    if (!move && t < NT)
-                        negm[t] = -0.0f;
-                } else {   // the previous tile's product is done with P (and O)
-                    cta_wait(sh, &sh.o_full, (gt - 1) & 1);
-                    tc_fence_after();
-                }
-                if (move) {
-                    move_references<NT>(scratch, negm, &sh.unset[w], s_at, tmem_o + lanes + w * NT, first_tile ? 0 : a.nd, N, mult, seen, t, bar);
-#pragma unroll
-                    for (int i = 0; i < NT / 4; ++i) {
-                        const ulonglong2 f4 = reinterpret_cast<const ulonglong2*>(scratch)[i];
-                        l2[2 * i] = f2_mul(l2[2 * i], f4.x);
-                        l2[2 * i + 1] = f2_mul(l2[2 * i + 1], f4.y);
-                    }
-                    bar_sync(bar, 128);   // the scratch may be written again
-                }
-                // weights: fp32 sums, rounded once to bf16 for the second product (a weight's relative error of
-                // 2^-9 averages out over the positions and stays below the result's own rounding)
-                const uint64_t v2 = f2_pack(vscale, vscale);
-#pragma unroll
-                for (int c = 0; c < NT; c += C) {
-                    float s[C];
-                    load_scores<C>(s_at + c, negm + c, mult, tail, seen >> c, s);
-#pragma unroll
-                    for (int i = 0; i < C / 8; ++i) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint64_t e = f2_pack(ex2_approx(s[8 * i + 2 * k]), ex2_approx(s[8 * i + 2 * k + 1]));
-                            l2[c / 2 + 4 * i + k] = f2_add(l2[c / 2 + 4 * i + k], e);
-                            if (E4M3)
-                                e = f2_mul(e, v2);
-                            float lo, hi;
-                            f2_unpack(e, lo, hi);
-                            x[k] = bf16_pair(lo, hi);
-                        }
-                        // P: rows of 64 of the CTA's N columns a position, swizzled
-                        const int at = w * (NT / 8) + c / 8 + i;
-                        *reinterpret_cast<uint4*>(L.p + (at >> 3) * kHalfBytes + t * 128 + (((at ^ t) & 7) << 4)) =
-                            make_uint4(x[0], x[1], x[2], x[3]);
-                    }
-                }
-                tc_fence_before();
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_addr(&sh.s_empty[gt & 1]));
-                    mbar_arrive(smem_addr(&sh.p_full));
-                }
-                ks = ks_next;
-                vs = vs_next;
-            }
-            n_tiles += run.t1 - run.t0;
-
-            // the rows' sums over the 128 threads, while the last product runs
-            float sum[NT / 16];
-#pragma unroll
-            for (int i = 0; i < NT / 16; ++i) {
-                // lane c (of 16) ends with column 16 i + c: halve the columns, double the lanes summed
-                float x[16];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    f2_unpack(l2[8 * i + k], x[2 * k], x[2 * k + 1]);
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-                    for (int k = 0; k < o; ++k) {
-                        const bool up = lane & o;
-                        const float send = up ? x[k] : x[k + o];
-                        const float keep = up ? x[k + o] : x[k];
-                        x[k] = keep + __shfl_xor_sync(kFull, send, o);
-                    }
-                sum[i] = x[0] + __shfl_xor_sync(kFull, x[0], 16);
-            }
-            cta_wait(sh, &sh.o_full, (n_tiles - 1) & 1);
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < NT / 16; ++i)
-                if (lane < 16)
-                    scratch[(warp & 3) * NT + 16 * i + lane] = sum[i];
-            bad = bar_any(bar, 128, bad) || *reinterpret_cast<volatile int*>(&sh.abort);
-            if (t == 0 && bad && a.has_err)
-                atomicOr(a.err, *reinterpret_cast<volatile int*>(&sh.abort) ? kErrWaitTimeout : kErrCache);
-            float* const fin = scratch + 4 * NT;
-            const bool whole = run.whole();
-            if (t < NT) {
-                float l = (scratch[t] + scratch[NT + t]) + (scratch[2 * NT + t] + scratch[3 * NT + t]);
-                if (bad || (sh.anc[w][t] & poison))
-                    l = NAN;
-                fin[t] = !whole ? 1.0f : l == 0.0f || first + t >= nn * a.G ? 0.0f : 1.0f / l;
-                if (!whole && t < mine) {
-                    float* ml = a.part_ml + ((long long)part * a.rows + w * a.half + t) * 2;
-                    ml[0] = -negm[t];
-                    ml[1] = l;
-                }
-            }
-            bar_sync(bar, 128);
-            for (int c = 0; c < a.nd; ++c) {
-                const int d = 128 * c + (E4M3 ? converted_element(t) : t);
-                for (int i = 0; i < NT; i += 16) {
-                    float o[16];
-                    tmem_ld16(tmem_o + lanes + c * N + w * NT + i, o);
-                    tmem_wait_ld();
-                    if (d < D) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int at = sh.row_out[w][i + k];
-                            const float f = fin[i + k];
-                            if (at >= 0) {
-                                if (whole)
-                                    a.out[(long long)at * D + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : o[k] * f);
-                                else
-                                    a.part_o[(long long)at * D + d] = o[k];
-                            }
-                        }
-                    }
-                }
-            }
-            tc_fence_before();
-            bar_sync(bar, 128);   // O and the scratch are read before the next item's product and sums
-        }
-        }
-    } else if (E4M3 && warp >= 12) {
-        regs_shrink<kRegsConvert>();
-        // --- e4m3 values to bf16 operands ---------------------------------------
-        const AttnLayout L = attn_layout<N, E4M3>(a, smem);
-        AttnShared& sh = *L.sh;
-        Run run = run_of(a, sh);
-        // A thread takes one position's row: rows of a warp differ in their
-        // swizzle, so neither the loads nor the stores collide.
-        Ring r, w;
-        const int t = tid - 384, key = t & 7;
-        bool go = true;
-        while (go && run.next(a)) {
-            if (run.s.len == 0)
-                continue;
-            for (int j = run.t0; go && j < run.t1; ++j) {
-                const int valid = min(kTile, run.s.len - j * kTile), rows = (valid + 15) & ~15;
-                const int node0 = run.s.nn > 1 ? run.s.ctx - j * kTile : kTile;   // first row of a node
-                for (int c = 0; go && c < a.nd; ++c) {
-                    go = cta_wait(sh, &sh.vfull[r.slot], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
-                    if (!go)
-                        break;
-                    const unsigned char* src = L.v + r.slot * a.v_bytes + t * 128;
-                    unsigned char* dst = L.c + w.slot * a.conv_bytes + t * 128;
-                    if (t < rows) {
-                        const int pieces = min(128, D - 128 * c) / 16;
-#pragma unroll 4
-                        for (int i = 0; i < pieces; ++i) {
-                            uint4 x = *reinterpret_cast<const uint4*>(src + ((i ^ key) << 4));
-                            const bool nan = chunk_nan_e4m3(x);
-                            if (t >= valid || (nan && t >= node0))
-                                x = make_uint4(0, 0, 0, 0);
-                            uint2 y0 = e4m3_to_bf16(x.x), y1 = e4m3_to_bf16(x.y), y2 = e4m3_to_bf16(x.z), y3 = e4m3_to_bf16(x.w);
-                            if (nan) {
-                                y0 = e4m3_keep_nan(x.x, y0);
-                                y1 = e4m3_keep_nan(x.y, y1);
-                                y2 = e4m3_keep_nan(x.z, y2);
-                                y3 = e4m3_keep_nan(x.w, y3);
-                            }
-                            unsigned char* o = dst + (i >> 2) * kHalfBytes;
-                            const int ch = 2 * (i & 3);
-                            *reinterpret_cast<uint4*>(o + ((ch ^ key) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
-                            *reinterpret_cast<uint4*>(o + (((ch + 1) ^ key) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
-                        }
+                            *reinterpret_cast<uint2*>(o + k * L.q_part) = make_uint2(p[k][0] | (p[k][1] << 16), p[k][2] | (p[k][3] << 16));
                     }
                     fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_addr(&sh.vempty[r.slot]));
-                        mbar_arrive(smem_addr(&sh.cfull[w.slot]));
-                    }
-                    r.step(a.vslots);
-                    w.step(a.conv);
                 }
-            }
-        }
-    } else {
-        regs_shrink<kRegsIssue<E4M3>>();
-    if (warp == 9) {
-        // --- TMA producer ------------------------------------------------------
-        const AttnLayout L = attn_layout<N, E4M3>(a, smem);
-        AttnShared& sh = *L.sh;
-        Run run = run_of(a, sh);
-        Ring rk, rv;
-        int nk = 0, nv = 0;   // slots that may still be filling
-        const int boxes = kTile / a.box_rows;
-        bool go = true;
-        while (go && run.next(a)) {
-            if (run.s.len == 0)
-                continue;
-            const int h = run.hg / a.groups, n = run.t1 - run.t0;
-            // lane l: row of the tile's box l, -1 where it holds no position (or its page is unusable)
-            auto box_row = [&](int j) {
-                const int pos = j * kTile + lane * a.box_rows;
-                if (j >= run.t1 || lane >= boxes || pos >= run.s.len)
-                    return -1;
-                const int page = kv_page(a.c, run.b, pos);
-                return page < 0 ? -1 : (int)kv_row(a.c, page, pos) + (h << a.c.page_shift);
-            };
-            int row = box_row(run.t0), row_k = row, ahead = box_row(run.t0 + 1);   // tiles of the next V, of the last K, after it
-            for (int step = 0; go && step < 2 * n; ++step) {
-                const bool is_k = step_is_k(step, n);
-                if (is_k && step > 0) {
-                    row_k = ahead;
-                    ahead = box_row(run.t0 + step_tile(step, n) + 1);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&sh.info_full[items & 1]));
+                    if (E4M3)
+                        mbar_arrive(smem_addr(&sh.q_full));
                 }
-                const int at = is_k ? row_k : row;
-                const unsigned have = __ballot_sync(kFull, at >= 0);
-                Ring& r = is_k ? rk : rv;
-                for (int c = 0; go && c < a.nd; ++c) {
-                    go = cta_wait(sh, is_k ? &sh.kempty[r.slot] : &sh.vempty[r.slot], r.phase ^ 1);
-                    if (!go)
-                        break;
-                    const uint32_t bar = smem_addr(is_k ? &sh.kfull[r.slot] : &sh.vfull[r.slot]);
-                    const uint32_t dst = is_k ? smem_addr(L.k) + r.slot * a.k_bytes : smem_addr(L.v) + r.slot * a.v_bytes;
-                    const int halves = E4M3 ? 1 : min(2, (D - 128 * c + 63) / 64);
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(bar, __popc(have) * a.box_rows * 128 * halves);
-                    __syncwarp();
-                    if (at >= 0)
-                        for (int x = 0; x < halves; ++x)
-                            tma_load_2d(dst + x * kHalfBytes + lane * a.box_rows * 128, is_k ? &map_k : &map_v, 128 * c + 64 * x, at, bar);
-                    __syncwarp();
-                    if (is_k) {
-                        rk.step(a.kslots);
-                        nk = min(nk + 1, a.kslots);
-                    } else {
-                        rv.step(a.vslots);
-                        nv = min(nv + 1, a.vslots);
-                    }
-                }
-                if (!is_k)
-                    row = row_k;
+                ++items;
             }
         }
-        if (!go) {   // copies in flight land before the CTA's memory is given back
-            for (; nk > 0; --nk) {
-                rk.back(a.kslots);
-                mbar_wait_bounded(smem_addr(&sh.kfull[rk.slot]), rk.phase, kWaitSpins);
-            }
-            for (; nv > 0; --nv) {
-                rv.back(a.vslots);
-                mbar_wait_bounded(smem_addr(&sh.vfull[rv.slot]), rv.phase, kWaitSpins);
-            }
-        }
-    } else if (warp == 8) {
-        // --- MMA ---------------------------------------------------------------
-        const AttnLayout L = attn_layout<N, E4M3>(a, smem);
-        AttnShared& sh = *L.sh;
-        Run run = run_of(a, sh);
-        const uint32_t tmem = sh.tmem, tmem_o = tmem + 2 * N;   // S (two buffers of N columns), then O
-        Ring rk, rv;
-        uint32_t item = 0;        // items with positions so far (parity of q_full)
-        uint32_t n_tiles = 0;     // tiles so far (parity of p_full, buffer of S)
-        const int vring = E4M3 ? a.conv : a.vslots;
-        const uint32_t k0 = smem_addr(L.k), v0 = smem_addr(E4M3 ? L.c : L.v), v_bytes = E4M3 ? a.conv_bytes : a.v_bytes;
-        const uint32_t q0 = smem_addr(L.q), p0 = smem_addr(L.p);
-        uint64_t* const vfull = E4M3 ? sh.cfull : sh.vfull;
-        uint64_t* const vempty = E4M3 ? sh.cempty : sh.vempty;
-        bool go = true;
-        while (go && run.next(a)) {
-            if (run.s.len == 0)
-                continue;
-            go = cta_wait(sh, &sh.q_full, item & 1);
-            ++item;
-            const int n = run.t1 - run.t0;
-            for (int step = 0; go && step < 2 * n; ++step) {
-                const bool is_k = step_is_k(step, n);
-                const int jj = step_tile(step, n), valid = min(kTile, run.s.len - (run.t0 + jj) * kTile);
-                const uint32_t g = n_tiles + jj;   // the CTA's tile count
-                for (int c = 0; go && c < a.nd; ++c) {
-                    const int width = min(128, D - 128 * c);
-                    if (is_k) {
-                        go = cta_wait(sh, &sh.kfull[rk.slot], rk.phase) &&
-                             (c > 0 || cta_wait(sh, &sh.s_empty[g & 1], ((g >> 1) & 1) ^ 1));
-                        if (!go)
-                            break;
-                        tc_fence_after();
-                        if (lane == 0) {
-                            mma_scores<N, E4M3>(tmem + (g & 1) * N, k0 + rk.slot * a.k_bytes, q0 + (E4M3 ? c : 2 * c) * (N * 128), L.q_part,
-                                                E4M3 ? (width + 31) / 32 : width / 16, c > 0);
-                            if (c == a.nd - 1)
-                                tc_commit(smem_addr(&sh.s_full[g & 1]));
-                            tc_commit(smem_addr(&sh.kempty[rk.slot]));
-                        }
-                        __syncwarp();
-                        rk.step(a.kslots);
-                    } else {
-                        go = cta_wait(sh, &vfull[rv.slot], rv.phase);
-                        if (!go)
-                            break;
-                        const int ksteps = (valid + 15) / 16;
-                        if (!E4M3 && (run.t0 + jj + 1) * kTile > run.s.ctx) {
-                            // rows behind the last position may hold anything: zeros instead of 0 * NaN.  A node's
-                            // values are seen by some rows only: what is not finite there is zeroed too (the rows
-                            // that do see it are set to NaN at the end).
-                            unsigned char* v = L.v + rv.slot * a.v_bytes;
-                            const int chunks = width > 64 ? 16 : 8;
-                            for (int i = valid * chunks + lane; i < ksteps * 16 * chunks; i += 32) {
-                                const int row = i / chunks, ch = i % chunks;
-                                *reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            const int row = run.s.ctx + lane - (run.t0 + jj) * kTile;
-                            if (run.s.nn > 1 && lane < run.s.nn && row >= 0 && row < kTile)
-                                for (int ch = 0; ch < chunks; ++ch) {
-                                    uint4* p = reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 + ((ch ^ lane) & 7) * 16);
-                                    if (chunk_nonfinite(*p, false))
-                                        *p = make_uint4(0, 0, 0, 0);
-                                }
-                            fence_proxy_async();
-                            __syncwarp();
-                        }
-                        if (c == 0) {
-                            go = cta_wait(sh, &sh.p_full, g & 1);
-                            if (!go)
-                                break;
-                        }
-                        tc_fence_after();
-                        if (lane == 0) {
-                            mma_values<N>(tmem_o + c * N, v0 + rv.slot * v_bytes, p0, width > 64 ? kHalfBytes : 0, ksteps, jj > 0);
-                            if (c == a.nd - 1)
-                                tc_commit(smem_addr(&sh.o_full));
-                            tc_commit(smem_addr(&vempty[rv.slot]));
-                        }
-                        __syncwarp();
-                        rv.step(vring);
-                    }
-                }
-            }
-            n_tiles += n;
-        }
-        if (!go) {   // products in flight end before TMEM is given back
-            if (lane == 0)
-                tc_commit(smem_addr(&sh.drain));
-            __syncwarp();
-            mbar_wait_bounded(smem_addr(&sh.drain), 0, kWaitSpins);
-        }
-    }
     }
     pdl_launch_dependents();
     tc_fence_before();
@@ -1097,10 +1268,10 @@ __global__ void __launch_bounds__(256) sv_attention_combine(const __grid_constan
             break;
     }
     const int per = a.c.Hkv * a.groups, b = item / per, hg = item - b * per, h = hg / a.groups, g = hg - h * a.groups;
-    const int row = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5), rr = g * a.rows + row;
-    if (row >= a.rows || rr >= a.Nmax * a.G)
+    const int row = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    int node, head;
+    if (!attn_row(a, g, row, node, head))
         return;
-    const int node = rr / a.G;
     const SeqLens s = seq_lens(a, b);
     // part p: CTA i's begun slot, then the continued slots of CTAs i + 1 ...
     auto slot = [&](int p) { return p == 0 ? 2LL * i + 1 : 2LL * (i + p); };
@@ -1138,7 +1309,7 @@ __global__ void __launch_bounds__(256) sv_attention_combine(const __grid_constan
                         acc[e] = fmaf(wp, o[lane + 32 * e], acc[e]);
         }
     }
-    __nv_bfloat16* out = a.out + (((long long)b * a.Nmax + node) * a.Hq + h * a.G + rr - node * a.G) * D;
+    __nv_bfloat16* out = a.out + (((long long)b * a.Nmax + node) * a.Hq + h * a.G + head) * D;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
