@@ -24,10 +24,11 @@
 // products add up in the same accumulator.  Its values become bf16 in shared
 // memory, because the weights need more range than two or three 8-bit terms.
 //
-// Warps: 0-7 softmax (two warpgroups), 8 MMA issue, 9 TMA, 10-11 what an item
-// needs before its first tile (tree masks, e4m3 queries), and for e4m3 caches
-// 12-15 conversion of values.  Tiles run through them in one stream across
-// items: K(g + 1) is loaded and multiplied before V(g).
+// Warps: 0-7 softmax (two warpgroups), 8 and 10 the issue of the first and the
+// second product (one warp for both would hold each back by the other's
+// issue), 9 TMA, 11 what an item needs before its first tile (tree masks), and
+// for e4m3 caches 12-15 the conversion of values and queries.  Tiles run
+// through them in one stream across items: K(g + 1) is loaded before V(g).
 //
 // Work is (sequence, key head, row group) items of 128-position tiles, laid
 // end to end and cut into equal runs, one to a CTA.  An item cut by a run's
@@ -157,12 +158,11 @@ struct Tiles {
 };
 
 // What an item's rows need to know, prepared while the one before is worked on.
-struct ItemInfo {
+struct alignas(16) ItemInfo {
     unsigned anc[128];     // the rows' ancestor bits (0: no row)
     int row_out[128];      // where their results go (-1: nowhere)
     unsigned poison;       // nodes whose values are not finite
     unsigned bad;          // malformed tree, unusable page
-    float q_unscale;       // undoes the queries' power of two (e4m3)
 };
 
 struct AttnShared {
@@ -171,13 +171,15 @@ struct AttnShared {
     uint64_t cfull[2], cempty[2];                  // converted V slots (e4m3)
     uint64_t sfull[kScaleSlots], sempty[kScaleSlots];   // scales (e4m3)
     uint64_t q_full, q_empty, info_full[2], info_empty[2];
-    uint64_t s_full[2], s_empty[2], p_full, o_full, drain;
+    uint64_t s_full[2], s_empty[2], p_full, o_full, drain[2];
     long long t_begin, t_end, sum[16];
     uint32_t tmem;
     int abort;
     int b, hg, tile, active;
     int unset[2];
-    float top[2];
+    float top[4];
+    float q_unscale[4];                            // undoes the queries' power of two (e4m3), by item: the first
+                                                   // product runs at most two ahead of the softmax
     alignas(16) float negm[128];                   // minus the rows' references
     float scratch[2][5 * 64];
     alignas(128) float scale[kScaleSlots][2][kTile];
@@ -424,63 +426,32 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
     tmem_wait_st();
 }
 
-// Sixteen (or 32) of a position's scores as they come off the tensor core;
-// -infinity where the row does not see the position.
-template <int C>
-__device__ __forceinline__ void raw_scores(uint32_t at, bool masked, unsigned long long seen, float (&s)[C])
-{
-#pragma unroll
-    for (int i = 0; i < C / 16; ++i)
-        tmem_ld16(at + 16 * i, s + 16 * i);
-    tmem_wait_ld();
-    if (masked) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            s[i] = (seen >> i) & 1 ? s[i] : -INFINITY;
-    }
-}
-
-// The same in powers of two relative to the rows' references.
-template <int C>
-__device__ __forceinline__ void relative_scores(uint32_t at, const float* negm, float mult, bool masked, unsigned long long seen,
-                                                float (&s)[C])
-{
-    raw_scores<C>(at, false, 0, s);
-    const uint64_t m2 = f2_pack(mult, mult);
-    const ulonglong2* nm = reinterpret_cast<const ulonglong2*>(negm);
-#pragma unroll
-    for (int i = 0; i < C / 4; ++i) {
-        const ulonglong2 x = nm[i];
-        f2_unpack(f2_fma(f2_pack(s[4 * i], s[4 * i + 1]), m2, x.x), s[4 * i], s[4 * i + 1]);
-        f2_unpack(f2_fma(f2_pack(s[4 * i + 2], s[4 * i + 3]), m2, x.y), s[4 * i + 2], s[4 * i + 3]);
-    }
-    if (masked) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            s[i] = (seen >> i) & 1 ? s[i] : -INFINITY;
-    }
-}
-
-// C weights of a position: rounded to bf16 once, with the position's value
+// Weights of a position from its scores s (times mult, minus the rows'
+// references if there are any): rounded to bf16 once, with the position's value
 // scale on them, into P; their sums.  A weight's rounding (a bf16 unit of
 // 2^-8) averages out over the positions.  ROUNDED sums take what P holds, so
 // that the rounding of a weight that dominates its row cancels; that costs
 // three instructions a pair, which the launches of few rows have to spare.
-template <int C, bool E4M3, bool ROUNDED>
-__device__ __forceinline__ void weigh(const float (&s)[C], float vscale, float vunscale, uint64_t* l2, unsigned char* p_row, int at, int t)
+template <int NT, bool E4M3, bool ROUNDED, bool PLAIN>
+__device__ __forceinline__ void weigh(const float (&s)[NT], float mult, const float* negm, float vscale, float vunscale, uint64_t (&l2)[NT / 2],
+                                      unsigned char* p_row, int at, int t)
 {
-    const uint64_t v2 = f2_pack(vscale, vscale), u2 = f2_pack(vunscale, vunscale);
+    const uint64_t m2 = f2_pack(mult, mult), v2 = f2_pack(vscale, vscale), u2 = f2_pack(vunscale, vunscale);
+    const ulonglong2* nm = reinterpret_cast<const ulonglong2*>(negm);
 #pragma unroll
-    for (int i = 0; i < C / 8; ++i) {
+    for (int i = 0; i < NT / 8; ++i) {
         uint32_t x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            uint64_t e = f2_pack(ex2_approx(s[8 * i + 2 * k]), ex2_approx(s[8 * i + 2 * k + 1]));
+            uint64_t e = f2_pack(s[8 * i + 2 * k], s[8 * i + 2 * k + 1]);
+            e = PLAIN ? f2_mul(e, m2) : f2_fma(e, m2, k & 1 ? nm[2 * i + k / 2].y : nm[2 * i + k / 2].x);
+            float lo, hi;
+            f2_unpack(e, lo, hi);
+            e = f2_pack(ex2_approx(lo), ex2_approx(hi));
             if (!ROUNDED)
                 l2[4 * i + k] = f2_add(l2[4 * i + k], e);
             if (E4M3)
                 e = f2_mul(e, v2);
-            float lo, hi;
             f2_unpack(e, lo, hi);
             x[k] = bf16_pair(lo, hi);
             if (ROUNDED) {
@@ -493,13 +464,40 @@ __device__ __forceinline__ void weigh(const float (&s)[C], float vscale, float v
     }
 }
 
+// A thread's element of NT rows of O: out(row's place, element, row's factor).
+template <int NT, typename F>
+__device__ __forceinline__ void store_rows(uint32_t o_at, const int* row_out, const float* fin, int d, int D, F out)
+{
+#pragma unroll
+    for (int i = 0; i < NT; i += 16) {
+        float o[16];
+        tmem_ld16(o_at + i, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+            const int4 at = *reinterpret_cast<const int4*>(row_out + i + k);
+            const float4 f = *reinterpret_cast<const float4*>(fin + i + k);
+            if (d < D) {
+                if (at.x >= 0)
+                    out(at.x, o[k], f.x);
+                if (at.y >= 0)
+                    out(at.y, o[k + 1], f.y);
+                if (at.z >= 0)
+                    out(at.z, o[k + 2], f.z);
+                if (at.w >= 0)
+                    out(at.w, o[k + 3], f.w);
+            }
+        }
+    }
+}
+
 __host__ __device__ constexpr int attn_threads(bool e4m3) { return e4m3 ? 512 : 384; }
 
 // Registers a thread: the softmax's warpgroups hold a row's sums and half of
 // its scores a thread, the others little.  The shares add up to the launch's.
 template <bool E4M3> constexpr int kAttnRegs = E4M3 ? 128 : 168;          // at launch
-template <bool E4M3> constexpr int kRegsSoftmax = E4M3 ? 160 : 200;       // warps 0 .. 7
-template <bool E4M3> constexpr int kRegsIssue = E4M3 ? 96 : 104;          // warps 8 .. 11
+template <bool E4M3> constexpr int kRegsSoftmax = E4M3 ? 168 : 200;       // warps 0 .. 7
+template <bool E4M3> constexpr int kRegsIssue = E4M3 ? 80 : 104;          // warps 8 .. 11
 constexpr int kRegsConvert = 96;                                          // warps 12 .. 15
 static_assert(512 * kAttnRegs<true> == 256 * kRegsSoftmax<true> + 128 * kRegsIssue<true> + 128 * kRegsConvert &&
               384 * kAttnRegs<false> == 256 * kRegsSoftmax<false> + 128 * kRegsIssue<false>,
@@ -539,23 +537,23 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                 mbar_init(smem_addr(&sh.cempty[i]), 1);
                 mbar_init(smem_addr(&sh.s_full[i]), 1);
                 mbar_init(smem_addr(&sh.s_empty[i]), 4 * NWG);
-                mbar_init(smem_addr(&sh.info_full[i]), 2);
+                mbar_init(smem_addr(&sh.info_full[i]), 1);
                 mbar_init(smem_addr(&sh.info_empty[i]), 4 * NWG);
             }
-            mbar_init(smem_addr(&sh.q_full), E4M3 ? 2 : 1);
+            mbar_init(smem_addr(&sh.q_full), 1);
             mbar_init(smem_addr(&sh.q_empty), 1);
             mbar_init(smem_addr(&sh.p_full), 4 * NWG);
             mbar_init(smem_addr(&sh.o_full), 1);
-            mbar_init(smem_addr(&sh.drain), 1);
+            mbar_init(smem_addr(&sh.drain[0]), 1);
+            mbar_init(smem_addr(&sh.drain[1]), 1);
             fence_mbar_init();
             tma_prefetch_map(&map_k);
             tma_prefetch_map(&map_v);
         }
-        if (!E4M3) {   // the rows of no query stay zeros
-            for (int i = tid; i < N * 8 * ((D + 63) / 64); i += kThreads)
-                reinterpret_cast<uint4*>(L.q)[i] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async();
-        }
+        // the rows of no query, and the elements past head_dim, stay zeros
+        for (int i = tid; i < (int)(reinterpret_cast<unsigned char*>(L.sh) - L.q) / 16; i += kThreads)
+            reinterpret_cast<uint4*>(L.q)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async();
         // the CTA's run: tiles of all sequences before each thread's share of them
         const int share = (a.B + kThreads - 1) / kThreads, b0 = min(tid * share, a.B), b1 = min(b0 + share, a.B);
         const int per = a.c.Hkv * a.groups;
@@ -646,11 +644,11 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                 const ItemInfo& info = sh.info[items & 1];
                 cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
                 const unsigned poison = info.poison;
-                const float scale_log2 = E4M3 ? a.scale_log2 * info.q_unscale : a.scale_log2;
                 if (t < NT)
                     negm[t] = 0.0f;   // read by others after the first vote only
                 if (t == 0)
                     sh.unset[w] = 0;
+                float scale_log2 = a.scale_log2;
                 bool plain = true;    // every reference is zero
                 uint64_t l2[NT / 2];  // this thread's share of the rows' sums, in pairs
 #pragma unroll
@@ -659,7 +657,7 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
 
                 for (int j = run.t0; j < run.t1; ++j, ++gt) {
                     const bool first_tile = j == run.t0;
-                    float mult = scale_log2, vscale = 1.0f, vunscale = 1.0f;
+                    float mult = a.scale_log2, vscale = 1.0f, vunscale = 1.0f;
                     if (E4M3) {
                         cta_wait(sh, &sh.sfull[rs.slot], rs.phase);
                         const float ks = sh.scale[rs.slot][0][t];
@@ -668,6 +666,11 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                         if (lane == 0)
                             mbar_arrive(smem_addr(&sh.sempty[rs.slot]));
                         rs.step(kScaleSlots);
+                        if (first_tile) {   // (the queries' power of two is there once their first product is)
+                            cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
+                            scale_log2 = a.scale_log2 * sh.q_unscale[items & 3];
+                        }
+                        mult = scale_log2;
                         // a scale that is not finite marks a row that held something that was not
                         mult *= isfinite(ks) ? ks : NAN;
                         vscale = isfinite(vscale) ? vscale : NAN;
@@ -692,31 +695,41 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                     }
                     if (E4M3 && NWG == 1)
                         vunscale = __frcp_rn(vscale);
+                    if (mult == 0.0f)
+                        mult = FLT_MIN;   // so that a hidden score's infinity stays one
                     const uint32_t s_at = tmem + (gt & 1) * N;
-                    constexpr int C = NT % 32 ? 16 : 32;
 
                     cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
                     tc_fence_after();
-                    // are all scores near enough to the references?  (A second look at TMEM is cheaper than the
-                    // registers that would keep the scores over the vote.)
-                    if (plain) {
-                        float top = -INFINITY, low = INFINITY;
+                    float s[NT];
 #pragma unroll
-                        for (int c = 0; c < NT; c += C) {
-                            float s[C];
-                            raw_scores<C>(s_at + c, tail, seen >> c, s);
+                    for (int i = 0; i < NT / 16; ++i)
+                        tmem_ld16(s_at + 16 * i, s + 16 * i);
+                    tmem_wait_ld();
+                    if (tail) {
+                        const float hidden = mult < 0.0f ? INFINITY : -INFINITY;
 #pragma unroll
-                            for (int i = 0; i < C; i += 2)
-                                top = max3(top, s[i], s[i + 1]);
-                            if (first_tile) {
+                        for (int i = 0; i < NT; ++i)
+                            s[i] = (seen >> i) & 1 ? s[i] : hidden;
+                    }
+                    if (plain) {   // are all scores near enough to the references?
+                        float top[4], low[4];
 #pragma unroll
-                                for (int i = 0; i < C; i += 2)
-                                    low = min3(low, s[i], s[i + 1]);
-                            }
+                        for (int k = 0; k < 4; ++k)
+                            top[k] = max3(s[4 * k], s[4 * k + 1], max3(s[4 * k + 2], s[4 * k + 3], -INFINITY));
+#pragma unroll
+                        for (int i = 16; i < NT; i += 2)
+                            top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], s[i], s[i + 1]);
+                        plain = !bar_any(bar, 128, max3(top[0], top[1], fmaxf(top[2], top[3])) * mult > kLazy || mult < 0.0f);
+                        if (first_tile) {   // zero will do as a reference if some position's scores are all near enough
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                low[k] = min3(s[4 * k], s[4 * k + 1], min3(s[4 * k + 2], s[4 * k + 3], INFINITY));
+#pragma unroll
+                            for (int i = 16; i < NT; i += 2)
+                                low[(i >> 1) & 3] = min3(low[(i >> 1) & 3], s[i], s[i + 1]);
+                            plain = bar_any(bar, 128, min3(low[0], low[1], fminf(low[2], low[3])) * mult >= -kLazy) && plain;
                         }
-                        plain = !bar_any(bar, 128, top * mult > kLazy || mult < 0.0f);
-                        if (first_tile)   // zero will do as a reference if some position's scores are all near enough
-                            plain = bar_any(bar, 128, low * mult >= -kLazy) && plain;
                     }
                     if (!first_tile) {   // the previous tile's product is done with P (and O)
                         cta_wait(sh, &sh.o_full, (gt - 1) & 1);
@@ -724,31 +737,12 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                     }
                     unsigned char* const p_row = L.p + t * 128;
                     if (plain) {
-#pragma unroll
-                        for (int c = 0; c < NT; c += C) {
-                            float s[C];
-                            raw_scores<C>(s_at + c, false, 0, s);
-                            const uint64_t m2 = f2_pack(mult, mult);
-#pragma unroll
-                            for (int i = 0; i < C; i += 2)
-                                f2_unpack(f2_mul(f2_pack(s[i], s[i + 1]), m2), s[i], s[i + 1]);
-                            if (tail) {
-#pragma unroll
-                                for (int i = 0; i < C; ++i)
-                                    s[i] = (seen >> (c + i)) & 1 ? s[i] : -INFINITY;
-                            }
-                            weigh<C, E4M3, NWG == 1>(s, vscale, vunscale, l2 + c / 2, p_row, (w * NT + c) / 8, t);
-                        }
+                        weigh<NT, E4M3, NWG == 1, true>(s, mult, negm, vscale, vunscale, l2, p_row, w * (NT / 8), t);
                     } else {
                         float top = -INFINITY;
-#pragma unroll 1
-                        for (int c = 0; c < NT; c += 16) {
-                            float s[16];
-                            relative_scores<16>(s_at + c, negm + c, mult, tail, seen >> c, s);
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2)
-                                top = max3(top, s[i], s[i + 1]);
-                        }
+                        for (int i = 0; i < NT; ++i)
+                            top = fmaxf(top, fmaf(s[i], mult, negm[i]));
                         // +0 marks a row without a reference: a part that was plain until now has them all (zeros)
                         if (!first_tile && t < NT && __float_as_uint(negm[t]) == 0u && !sh.unset[w])
                             negm[t] = -0.0f;
@@ -762,12 +756,7 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                             }
                             bar_sync(bar, 128);   // the scratch may be written again
                         }
-#pragma unroll
-                        for (int c = 0; c < NT; c += 16) {
-                            float s[16];
-                            relative_scores<16>(s_at + c, negm + c, mult, tail, seen >> c, s);
-                            weigh<16, E4M3, NWG == 1>(s, vscale, vunscale, l2 + c / 2, p_row, (w * NT + c) / 8, t);
-                        }
+                        weigh<NT, E4M3, NWG == 1, false>(s, mult, negm, vscale, vunscale, l2, p_row, w * (NT / 8), t);
                     }
                     tc_fence_before();
                     fence_proxy_async();
@@ -802,11 +791,27 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                 for (int i = 0; i < NT / 16; ++i)
                     if (lane < 16)
                         scratch[(warp & 3) * NT + 16 * i + lane] = sum[i];
-                bar_sync(bar, 128);
                 float* const fin = scratch + 4 * NT;
-                const bool abort = *reinterpret_cast<volatile int*>(&sh.abort) != 0, bad = info.bad || abort;
-                if (t == 0 && bad && a.has_err)
-                    atomicOr(a.err, abort ? kErrWaitTimeout : kErrCache);
+                if (bar_any(bar, 128, *reinterpret_cast<volatile int*>(&sh.abort) != 0)) {
+                    // a wait gave up: nothing of the item can be relied on, its rows are NaN
+                    const int h = run.hg / a.groups, g = run.hg - h * a.groups;
+                    if (tid == 0 && a.has_err)
+                        atomicOr(a.err, kErrWaitTimeout);
+                    for (int r = w * NT + (warp & 3); r < min(a.rows, (w + 1) * NT); r += 4) {
+                        int node, head;
+                        if (!attn_row(a, g, r, node, head))
+                            continue;
+                        if (!whole && lane < 2)
+                            a.part_ml[((long long)part * a.rows + r) * 2 + lane] = NAN;
+                        for (int d = lane; whole && d < D; d += 32)
+                            a.out[(((long long)run.b * a.Nmax + node) * a.Hq + h * a.G + head) * D + d] = __float2bfloat16_rn(NAN);
+                    }
+                    ++items;
+                    continue;
+                }
+                const bool bad = info.bad;
+                if (tid == 0 && bad && a.has_err)
+                    atomicOr(a.err, kErrCache);
                 if (t < NT) {
                     const unsigned anc = info.anc[w * NT + t];
                     float l = (scratch[t] + scratch[NT + t]) + (scratch[2 * NT + t] + scratch[3 * NT + t]);
@@ -824,25 +829,13 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                 bar_sync(bar, 128);
                 for (int c = 0; c < a.nd; ++c) {
                     const int d = 128 * c + (E4M3 ? converted_element(t) : t);
-#pragma unroll 1
-                    for (int i = 0; i < NT; i += 16) {
-                        float o[16];
-                        tmem_ld16(tmem_o + c * N + i, o);
-                        tmem_wait_ld();
-                        if (d < D) {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const int at = info.row_out[w * NT + i + k];
-                                const float f = fin[i + k];
-                                if (at >= 0) {
-                                    if (whole)
-                                        a.out[(long long)at * D + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : o[k] * f);
-                                    else
-                                        a.part_o[(long long)at * D + d] = o[k];
-                                }
-                            }
-                        }
-                    }
+                    const int* const row_out = info.row_out + w * NT;
+                    if (whole)
+                        store_rows<NT>(tmem_o + c * N, row_out, fin, d, D, [&](int at, float x, float f) {
+                            a.out[(long long)at * D + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : x * f);
+                        });
+                    else
+                        store_rows<NT>(tmem_o + c * N, row_out, fin, d, D, [&](int at, float x, float) { a.part_o[(long long)at * D + d] = x; });
                 }
                 tc_fence_before();
                 bar_sync(bar, 128);   // O, the scratch and the item's rows have been read
@@ -860,37 +853,124 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
         AttnShared& sh = *L.sh;
         Tiles it;
         it.start(a, run_of(a, sh));
+        Run ahead = it.run;      // the item after
+        bool more = it.more;
+        uint32_t items = 0;
         Ring r, w;
         const int t = tid - 384, key = t & 7;
+        // an item's queries, as three 8-bit terms (before its keys' first product)
+        auto queries = [&](const Run& x) {
+            const int h = x.hg / a.groups, g = x.hg - h * a.groups, nb = g / a.head_blocks;
+            const int node0 = nb * a.nodes, head0 = (g - nb * a.head_blocks) * a.heads;
+            const int live = min(a.nodes, x.s.nn - node0), heads = min(a.heads, a.G - head0), per = D / 8;
+            // thread t: chunks t, t + 128, ... of the rows' 8-element chunks
+            auto load_q = [&](int i) {
+                const int row = i / per, ch = i - row * per, n = row / a.heads, head = row - n * a.heads;
+                if (n >= live || head >= heads)
+                    return make_uint4(0, 0, 0, 0);
+                return __ldg(reinterpret_cast<const uint4*>(a.q + ((long long)x.b * a.Nmax + node0 + n) * a.q_stride +
+                                                            (long long)(h * a.G + head0 + head) * D) + ch);
+            };
+            // a power of two that brings the group's largest element to [128, 256)
+            const int chunks = a.rows * per;
+            float top = 0.0f;
+            for (int i = t; i < chunks; i += 512) {
+                uint4 q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    q[k] = i + 128 * k < chunks ? load_q(i + 128 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float y[8];
+                    Elem<__nv_bfloat16>::unpack(q[k], y);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        top = fmaxf(top, isfinite(y[e]) ? fabsf(y[e]) : 0.0f);
+                }
+            }
+            top = warp_redux_max(top);
+            if (lane == 0)
+                sh.top[warp & 3] = top;
+            bar_sync(3, 128);
+            top = fmaxf(fmaxf(sh.top[0], sh.top[1]), fmaxf(sh.top[2], sh.top[3]));
+            const int e = top > 0.0f ? min(max(261 - (int)(__float_as_uint(top) >> 23), 1), 253) : 127;
+            const float scale = __uint_as_float((uint32_t)e << 23);
+            cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
+            if (t == 0)
+                sh.q_unscale[items & 3] = __uint_as_float((uint32_t)(254 - e) << 23);
+            for (int i = t; i < chunks; i += 512) {
+                uint4 q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    q[k] = i + 128 * k < chunks ? load_q(i + 128 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (i + 128 * k < chunks) {
+                        const int row = (i + 128 * k) / per, ch = i + 128 * k - row * per;
+                        float y[8];
+                        Elem<__nv_bfloat16>::unpack(q[k], y);
+                        uint32_t p[3][4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            split_q(y[2 * c] * scale, y[2 * c + 1] * scale, p[0][c], p[1][c], p[2][c]);
+                        unsigned char* o = L.q + (ch >> 4) * (N * 128) + row * 128 + ((((ch & 15) >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
+#pragma unroll
+                        for (int c = 0; c < 3; ++c)
+                            *reinterpret_cast<uint2*>(o + c * L.q_part) = make_uint2(p[c][0] | (p[c][1] << 16), p[c][2] | (p[c][3] << 16));
+                    }
+            }
+            fence_proxy_async();
+            bar_sync(3, 128);   // (also: sh.top may be written again)
+            if (t == 0)
+                mbar_arrive(smem_addr(&sh.q_full));
+            ++items;
+        };
+        if (more) {
+            queries(it.run);
+            more = ahead.next(a);
+        }
         for (; it.more; it.step(a)) {
+            if (it.j == it.run.t1 - 1 && more) {   // the next item's queries, before this one's last values
+                queries(ahead);
+                more = ahead.next(a);
+            }
             const int valid = it.valid(), rows = (valid + 15) & ~15;
             const int node0 = it.run.s.nn > 1 ? it.run.s.ctx - it.j * kTile : kTile;   // first row of a node
-            bool go = true;
-            for (int c = 0; go && c < a.nd; ++c) {
-                go = cta_wait(sh, &sh.vfull[r.slot], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
-                if (!go)
-                    break;
+            for (int c = 0; c < a.nd; ++c) {
+                // (the warps share a barrier: after a timeout they all run on, doing nothing)
+                const bool go = cta_wait(sh, &sh.vfull[r.slot], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
                 const unsigned char* src = L.v + r.slot * a.v_bytes + t * 128;
                 unsigned char* dst = L.c + w.slot * a.conv_bytes + t * 128;
-                if (t < rows) {
-                    const int pieces = min(128, D - 128 * c) / 16;
-#pragma unroll 4
-                    for (int i = 0; i < pieces; ++i) {
-                        uint4 x = *reinterpret_cast<const uint4*>(src + ((i ^ key) << 4));
-                        const bool nan = chunk_nan_e4m3(x);
-                        if (t >= valid || (nan && t >= node0))
-                            x = make_uint4(0, 0, 0, 0);
-                        uint2 y0 = e4m3_to_bf16(x.x), y1 = e4m3_to_bf16(x.y), y2 = e4m3_to_bf16(x.z), y3 = e4m3_to_bf16(x.w);
-                        if (nan) {
-                            y0 = e4m3_keep_nan(x.x, y0);
-                            y1 = e4m3_keep_nan(x.y, y1);
-                            y2 = e4m3_keep_nan(x.z, y2);
-                            y3 = e4m3_keep_nan(x.w, y3);
+                const int pieces = min(128, D - 128 * c) / 16;
+                if (go && t < rows) {
+#pragma unroll 1
+                    for (int i = 0; i < pieces; i += 4) {
+                        // four 16-byte pieces at a time, so that their chains overlap (what is past the row is not used)
+                        uint4 x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            x[k] = t < valid ? *reinterpret_cast<const uint4*>(src + (((i + k) ^ key) << 4)) : make_uint4(0, 0, 0, 0);
+                        const bool nan = chunk_nan_e4m3(x[0]) | chunk_nan_e4m3(x[1]) | chunk_nan_e4m3(x[2]) | chunk_nan_e4m3(x[3]);
+                        if (nan && t >= node0) {   // a node's values are seen by some rows only (which end as NaN)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[k] = make_uint4(0, 0, 0, 0);
                         }
                         unsigned char* o = dst + (i >> 2) * kHalfBytes;
-                        const int ch = 2 * (i & 3);
-                        *reinterpret_cast<uint4*>(o + ((ch ^ key) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
-                        *reinterpret_cast<uint4*>(o + (((ch + 1) ^ key) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint2 y0 = e4m3_to_bf16(x[k].x), y1 = e4m3_to_bf16(x[k].y), y2 = e4m3_to_bf16(x[k].z), y3 = e4m3_to_bf16(x[k].w);
+                            *reinterpret_cast<uint4*>(o + (((2 * k) ^ key) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
+                            *reinterpret_cast<uint4*>(o + (((2 * k + 1) ^ key) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
+                        }
+                        if (nan && t < node0) {   // NaN, which the conversion reads as 480
+#pragma unroll 1
+                            for (int k = 0; k < 64; ++k)
+                                if ((src[(((i + (k >> 4)) ^ key) << 4) + (k & 15)] & 0x7f) == 0x7f) {
+                                    const int e = converted_element(k);   // where that element went
+                                    *reinterpret_cast<unsigned short*>(o + (((e >> 3) ^ key) << 4) + 2 * (e & 7)) = 0x7fff;
+                                }
+                        }
                     }
                 }
                 fence_proxy_async();
@@ -902,8 +982,6 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                 r.step(a.vslots);
                 w.step(a.conv);
             }
-            if (!go)
-                break;
         }
     } else {
         regs_shrink<kRegsIssue<E4M3>>();
@@ -1016,55 +1094,61 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                     mbar_wait_bounded(smem_addr(&sh.q_full), (items - 1) & 1, kWaitSpins);
             }
         } else if (warp == 8) {
-            // --- MMA issue -------------------------------------------------------------
-            const uint32_t tmem = sh.tmem, tmem_o = tmem + 2 * N;
-            Ring rk, rv;
-            uint32_t gk = 0, gv = 0, items = 0, vitems = 0;   // tiles of K and V so far; items
-            const int vring = E4M3 ? a.conv : a.vslots;
-            const uint32_t k0 = smem_addr(L.k), v0 = smem_addr(E4M3 ? L.c : L.v), v_bytes = E4M3 ? a.conv_bytes : a.v_bytes;
-            const uint32_t q0 = smem_addr(L.q), p0 = smem_addr(L.p);
-            uint64_t* const vfull = E4M3 ? sh.cfull : sh.vfull;
-            uint64_t* const vempty = E4M3 ? sh.cempty : sh.vempty;
-            Tiles k, v;
-            k.start(a, run_of(a, sh));
-            v = k;
+            // --- first product -----------------------------------------------------------
+            const uint32_t tmem = sh.tmem, k0 = smem_addr(L.k), q0 = smem_addr(L.q);
+            Ring rk;
+            uint32_t g = 0, items = 0;   // tiles, items so far
+            Tiles k;
             bool go = true;
-            while (go && v.more) {
-                if (k.more) {
-                    if (k.j == k.run.t0)
-                        go = cta_wait(sh, &sh.q_full, items++ & 1);
-                    go = go && cta_wait(sh, &sh.s_empty[gk & 1], ((gk >> 1) & 1) ^ 1);
-                    for (int c = 0; go && c < a.nd; ++c) {
-                        const int width = min(128, D - 128 * c);
-                        go = cta_wait(sh, &sh.kfull[rk.slot], rk.phase);
-                        if (!go)
-                            break;
-                        tc_fence_after();
-                        if (lane == 0) {
-                            mma_scores<N, E4M3>(tmem + (gk & 1) * N, k0 + rk.slot * a.k_bytes, q0 + (E4M3 ? c : 2 * c) * (N * 128), L.q_part,
-                                                E4M3 ? (width + 31) / 32 : width / 16, c > 0);
-                            tc_commit(smem_addr(&sh.kempty[rk.slot]));
-                            if (c == a.nd - 1) {
-                                tc_commit(smem_addr(&sh.s_full[gk & 1]));
-                                if (k.j == k.run.t1 - 1)
-                                    tc_commit(smem_addr(&sh.q_empty));
-                            }
-                        }
-                        __syncwarp();
-                        rk.step(a.kslots);
-                    }
+            for (k.start(a, run_of(a, sh)); k.more; k.step(a), ++g) {
+                if (k.j == k.run.t0)
+                    go = cta_wait(sh, &sh.q_full, items++ & 1);
+                go = go && cta_wait(sh, &sh.s_empty[g & 1], ((g >> 1) & 1) ^ 1);
+                for (int c = 0; go && c < a.nd; ++c) {
+                    const int width = min(128, D - 128 * c);
+                    go = cta_wait(sh, &sh.kfull[rk.slot], rk.phase);
                     if (!go)
                         break;
-                    ++gk;
-                    k.step(a);
-                    if (gk == 1 && k.more)
-                        continue;   // K runs one tile ahead of V
+                    tc_fence_after();
+                    if (lane == 0) {
+                        mma_scores<N, E4M3>(tmem + (g & 1) * N, k0 + rk.slot * a.k_bytes, q0 + (E4M3 ? c : 2 * c) * (N * 128), L.q_part,
+                                            E4M3 ? (width + 31) / 32 : width / 16, c > 0);
+                        tc_commit(smem_addr(&sh.kempty[rk.slot]));
+                        if (c == a.nd - 1) {
+                            tc_commit(smem_addr(&sh.s_full[g & 1]));
+                            if (k.j == k.run.t1 - 1)
+                                tc_commit(smem_addr(&sh.q_empty));
+                        }
+                    }
+                    __syncwarp();
+                    rk.step(a.kslots);
                 }
+                if (!go)
+                    break;
+            }
+            if (!go) {   // products in flight end before TMEM is given back
+                if (lane == 0)
+                    tc_commit(smem_addr(&sh.drain[0]));
+                __syncwarp();
+                mbar_wait_bounded(smem_addr(&sh.drain[0]), 0, kWaitSpins);
+            }
+        } else if (warp == 10) {
+            // --- second product ----------------------------------------------------------
+            const uint32_t tmem_o = sh.tmem + 2 * N, p0 = smem_addr(L.p);
+            const int ring = E4M3 ? a.conv : a.vslots;
+            const uint32_t v0 = smem_addr(E4M3 ? L.c : L.v), v_bytes = E4M3 ? a.conv_bytes : a.v_bytes;
+            uint64_t* const full = E4M3 ? sh.cfull : sh.vfull;
+            uint64_t* const empty = E4M3 ? sh.cempty : sh.vempty;
+            Ring rv;
+            uint32_t g = 0, items = 0;
+            Tiles v;
+            bool go = true;
+            for (v.start(a, run_of(a, sh)); v.more; ++g) {
                 const int valid = v.valid(), ksteps = (valid + 15) / 16;
                 const bool tail = (v.j + 1) * kTile > v.run.s.ctx;
                 for (int c = 0; go && c < a.nd; ++c) {
                     const int width = min(128, D - 128 * c);
-                    go = cta_wait(sh, &vfull[rv.slot], rv.phase);
+                    go = cta_wait(sh, &full[rv.slot], rv.phase);
                     if (!go)
                         break;
                     if (!E4M3 && tail) {
@@ -1077,11 +1161,11 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                             const int row = i / chunks, ch = i % chunks;
                             *reinterpret_cast<uint4*>(x + (ch >> 3) * kHalfBytes + row * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
-                        go = cta_wait(sh, &sh.info_full[vitems & 1], (vitems >> 1) & 1);
+                        go = cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
                         if (!go)
                             break;
                         const int row = v.run.s.ctx + lane - v.j * kTile;
-                        if (((sh.info[vitems & 1].poison >> lane) & 1u) && row >= 0 && row < kTile)
+                        if (((sh.info[items & 1].poison >> lane) & 1u) && row >= 0 && row < kTile)
                             for (int ch = 0; ch < chunks; ++ch) {
                                 uint4* p = reinterpret_cast<uint4*>(x + (ch >> 3) * kHalfBytes + row * 128 + ((ch ^ lane) & 7) * 16);
                                 if (chunk_nonfinite(*p, false))
@@ -1091,7 +1175,7 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                         __syncwarp();
                     }
                     if (c == 0) {
-                        go = cta_wait(sh, &sh.p_full, gv & 1);
+                        go = cta_wait(sh, &sh.p_full, g & 1);
                         if (!go)
                             break;
                     }
@@ -1100,143 +1184,95 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                         mma_values<N>(tmem_o + c * N, v0 + rv.slot * v_bytes, p0, width > 64 ? kHalfBytes : 0, ksteps, v.j > v.run.t0);
                         if (c == a.nd - 1)
                             tc_commit(smem_addr(&sh.o_full));
-                        tc_commit(smem_addr(&vempty[rv.slot]));
+                        tc_commit(smem_addr(&empty[rv.slot]));
                     }
                     __syncwarp();
-                    rv.step(vring);
+                    rv.step(ring);
                 }
-                ++gv;
+                if (!go)
+                    break;
                 if (v.j == v.run.t1 - 1)
-                    ++vitems;
+                    ++items;
                 v.step(a);
             }
-            if (!go) {   // products in flight end before TMEM is given back
+            if (!go) {
                 if (lane == 0)
-                    tc_commit(smem_addr(&sh.drain));
+                    tc_commit(smem_addr(&sh.drain[1]));
                 __syncwarp();
-                mbar_wait_bounded(smem_addr(&sh.drain), 0, kWaitSpins);
+                mbar_wait_bounded(smem_addr(&sh.drain[1]), 0, kWaitSpins);
             }
         } else {
-            // --- the next item: its rows, its queries (e4m3) -----------------------------
-            const int t = tid - 320, bar = 3;   // 64 threads
+            // --- the next item's rows ------------------------------------------------------
             Run run = run_of(a, sh);
             uint32_t items = 0;
-            while (run.next(a)) {
+            bool go = true;
+            while (go && run.next(a)) {
                 ItemInfo& info = sh.info[items & 1];
-                if (!cta_wait(sh, &sh.info_empty[items & 1], ((items >> 1) & 1) ^ 1))
-                    sh.abort = 1;   // (the two warps share a barrier: both go on)
                 const int h = run.hg / a.groups, g = run.hg - h * a.groups, nn = run.s.nn, ctx = run.s.ctx;
                 const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
                 int par;
                 const bool tree = tree_parents(a.parent + (long long)run.b * a.Nmax, a.has_parent, nn, lane, par);
-                if (t == 0) {
-                    info.poison = 0;
-                    info.bad = !tree;
-                }
-                for (int r = t; r < 128; r += 64) {
-                    int node = 0, head = 0;
-                    const bool real = r < N && attn_row(a, g, r, node, head);
-                    int at = real && node < nn && tree ? node : -1;
-                    unsigned anc = 0;
-                    for (int d = 0; d < kNodeMax && __any_sync(kFull, at >= 0); ++d) {
+                // lane n: node n and its ancestors
+                unsigned anc = lane < nn ? 1u << lane : 0u;
+                {
+                    int at = lane < nn && tree ? par : -1;
+                    while (__any_sync(kFull, at >= 0)) {   // parents are earlier nodes: at most 31 steps
                         if (at >= 0)
                             anc |= 1u << at;
                         const int up = __shfl_sync(kFull, par, max(at, 0));
                         at = at >= 0 ? up : -1;
                     }
-                    // (a malformed tree's rows end as NaN, whatever they see)
-                    info.anc[r] = real && node < nn && !tree ? ~0u : anc;
+                    if (!tree && lane < nn)
+                        anc = ~0u;   // (a malformed tree's rows end as NaN, whatever they see)
+                }
+                // the part's pages; its nodes' values, two nodes a turn and 16 lanes a node
+                bool bad = !tree;
+                const int p1 = min(run.t1 * kTile, run.s.len);
+                for (int pos = run.t0 * kTile + (lane << a.c.page_shift); pos < p1; pos += 32 << a.c.page_shift)
+                    bad |= kv_page(a.c, run.b, pos) < 0;
+                bad = __any_sync(kFull, bad);
+                unsigned poison = 0;
+                if (nn > 1 && run.t1 * kTile > ctx) {
+                    const int bytes = D * (E4M3 ? 1 : 2), l = lane & 15;
+                    // lane m: where node m's row lies
+                    long long row = -1;
+                    if (lane < nn && ctx + lane >= run.t0 * kTile && ctx + lane < run.t1 * kTile) {
+                        const int page = kv_page(a.c, run.b, ctx + lane);
+                        if (page >= 0)
+                            row = kv_row(a.c, page, ctx + lane) + ((long long)h << a.c.page_shift);
+                    }
+                    if (E4M3 && row >= 0 && !isfinite(a.c.v_scale[row]))
+                        poison = 1u << lane;
+#pragma unroll 8
+                    for (int m = lane >> 4; m < 32; m += 2) {
+                        const long long at = __shfl_sync(kFull, row, m);
+                        bool hit = false;
+                        if (at >= 0)
+                            for (int i = l; i < bytes / 16; i += 16)
+                                hit |= chunk_nonfinite(__ldg(reinterpret_cast<const uint4*>(a.c.v + at * bytes) + i), E4M3);
+                        poison |= hit ? 1u << m : 0u;
+                    }
+                    poison = __reduce_or_sync(kFull, poison);
+                }
+                go = cta_wait(sh, &sh.info_empty[items & 1], ((items >> 1) & 1) ^ 1);
+                if (!go)
+                    break;
+                if (lane == 0) {
+                    info.poison = poison;
+                    info.bad = bad;
+                }
+                for (int r = lane; r < (N + 31) / 32 * 32; r += 32) {
+                    int node = 0, head = 0;
+                    const bool real = r < N && attn_row(a, g, r, node, head);
+                    const unsigned its = __shfl_sync(kFull, anc, node & 31);
+                    info.anc[r] = real && node < nn ? its : 0u;
                     info.row_out[r] = !real         ? -1
                                       : run.whole() ? (run.b * a.Nmax + node) * a.Hq + h * a.G + head
                                                     : part * a.rows + r;
                 }
-                bar_sync(bar, 64);
-                {
-                    // the part's pages; its nodes' values
-                    bool bad = false;
-                    const int p1 = min(run.t1 * kTile, run.s.len);
-                    for (int pos = run.t0 * kTile + (t << a.c.page_shift); pos < p1; pos += 64 << a.c.page_shift)
-                        bad |= kv_page(a.c, run.b, pos) < 0;
-                    if (bad)
-                        info.bad = 1;
-                    const int m = t >> 1, pos = ctx + m, bytes = D * (E4M3 ? 1 : 2);
-                    if (nn > 1 && m < nn && pos >= run.t0 * kTile && pos < run.t1 * kTile) {
-                        const int page = kv_page(a.c, run.b, pos);
-                        if (page >= 0) {
-                            const long long row = kv_row(a.c, page, pos) + ((long long)h << a.c.page_shift);
-                            const uint4* x = reinterpret_cast<const uint4*>(a.c.v + row * bytes);
-                            bool hit = E4M3 && !isfinite(a.c.v_scale[row]);
-#pragma unroll 4
-                            for (int i = t & 1; i < bytes / 16; i += 2)
-                                hit |= chunk_nonfinite(x[i], E4M3);
-                            if (hit)
-                                atomicOr(&info.poison, 1u << m);
-                        }
-                    }
-                }
-                if (E4M3) {
-                    const int per = D / 8;
-                    auto load_q = [&](int i, int& row, int& ch) {
-                        row = i / per;
-                        ch = i - row * per;
-                        int node, head;
-                        if (!attn_row(a, g, row, node, head) || node >= nn)
-                            return make_uint4(0, 0, 0, 0);
-                        return __ldg(reinterpret_cast<const uint4*>(a.q + ((long long)run.b * a.Nmax + node) * a.q_stride +
-                                                                    (long long)(h * a.G + head) * D) + ch);
-                    };
-                    // a power of two that brings the group's largest element to [128, 256)
-                    float top = 0.0f;
-                    int row, ch;
-#pragma unroll 4
-                    for (int i = t; i < a.rows * per; i += 64) {
-                        float y[8];
-                        Elem<__nv_bfloat16>::unpack(load_q(i, row, ch), y);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            top = fmaxf(top, isfinite(y[k]) ? fabsf(y[k]) : 0.0f);
-                    }
-                    top = warp_redux_max(top);
-                    if (lane == 0)
-                        sh.top[warp - 10] = top;
-                    bar_sync(bar, 64);
-                    top = fmaxf(sh.top[0], sh.top[1]);
-                    const int e = top > 0.0f ? min(max(261 - (int)(__float_as_uint(top) >> 23), 1), 253) : 127;
-                    const float scale = __uint_as_float((uint32_t)e << 23);
-                    if (t == 0)
-                        info.q_unscale = __uint_as_float((uint32_t)(254 - e) << 23);
-                    cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
-                    const int wide = 16 * a.nd;   // chunks of 8 elements a row, with the padding
-                    for (int i = t; i < N * wide; i += 64) {   // zeros where there is no element
-                        const int rr = i / wide, cc = i - rr * wide;
-                        if (rr >= a.rows || cc >= per) {
-                            unsigned char* o = L.q + (cc >> 4) * (N * 128) + rr * 128 + ((((cc & 15) >> 1) ^ (rr & 7)) << 4) + (cc & 1) * 8;
-#pragma unroll
-                            for (int k = 0; k < 3; ++k)
-                                *reinterpret_cast<uint2*>(o + k * L.q_part) = make_uint2(0, 0);
-                        }
-                    }
-#pragma unroll 2
-                    for (int i = t; i < a.rows * per; i += 64) {
-                        float y[8];
-                        Elem<__nv_bfloat16>::unpack(load_q(i, row, ch), y);
-                        uint32_t p[3][4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            split_q(y[2 * k] * scale, y[2 * k + 1] * scale, p[0][k], p[1][k], p[2][k]);
-                        unsigned char* o = L.q + (ch >> 4) * (N * 128) + row * 128 + ((((ch & 15) >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
-#pragma unroll
-                        for (int k = 0; k < 3; ++k)
-                            *reinterpret_cast<uint2*>(o + k * L.q_part) = make_uint2(p[k][0] | (p[k][1] << 16), p[k][2] | (p[k][3] << 16));
-                    }
-                    fence_proxy_async();
-                }
                 __syncwarp();
-                if (lane == 0) {
+                if (lane == 0)
                     mbar_arrive(smem_addr(&sh.info_full[items & 1]));
-                    if (E4M3)
-                        mbar_arrive(smem_addr(&sh.q_full));
-                }
                 ++items;
             }
         }
