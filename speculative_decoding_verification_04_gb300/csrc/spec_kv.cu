@@ -190,13 +190,13 @@ cudaError_t launch_attention(AttnArgs& a, const CUtensorMap (&m)[3], int dev, in
         // the warpgroups share out what the block is launched with: with fewer registers they would wait for ever
         cudaFuncAttributes fa;
         const cudaError_t e2 = cudaFuncGetAttributes(&fa, sv_attention_kernel<NT, NWG, E4M3>);
-        if (e2 != cudaSuccess || fa.numRegs != kAttnRegs<E4M3>)
+        if (e2 != cudaSuccess || fa.numRegs != kAttnRegs)
             return e2 != cudaSuccess ? e2 : cudaErrorInvalidConfiguration;
         if (dev < 64)
             ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     const int ctas = std::min(nsm, kAttnMaxCtas);
-    sv_attention_kernel<NT, NWG, E4M3><<<ctas, attn_threads(E4M3), smem, st>>>(a, m[0], m[1], m[2]);
+    sv_attention_kernel<NT, NWG, E4M3><<<ctas, kAttnThreads, smem, st>>>(a, m[0], m[1], m[2]);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
@@ -367,7 +367,7 @@ sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, c
     a.groups = rg.groups;
     a.rows = rg.rows;
     a.nd = cache->head_dim > 128 ? 2 : 1;
-    a.box_rows = std::min(cache->page_size, sv::kTile);
+    a.box_rows = std::min(cache->page_size, sv::kQuarter);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     a.part_o = reinterpret_cast<float*>(ws);
     ws += (size_t)2 * sv::kAttnMaxCtas * a.rows * cache->head_dim * 4;

@@ -25,10 +25,12 @@
 // memory, because the weights need more range than two or three 8-bit terms.
 //
 // Warps: 0-7 softmax (two warpgroups), 8 and 10 the issue of the first and the
-// second product (one warp for both would hold each back by the other's
-// issue), 9 TMA, 11 what an item needs before its first tile (tree masks), and
-// for e4m3 caches 12-15 the conversion of values and queries.  Tiles run
-// through them in one stream across items: K(g + 1) is loaded before V(g).
+// second product, 9 bf16 queries, 11 what an item needs before its first tile
+// (tree masks), 12-15 the tiles: each loads a quarter of the positions (a TMA
+// copy of a page holds its warp for about 130 cycles, so one warp cannot load
+// small pages as fast as memory delivers them) and, for e4m3 caches, converts
+// its quarter of the values and makes the queries' terms.  Tiles run through
+// them in one stream across items.
 //
 // Work is (sequence, key head, row group) items of 128-position tiles, laid
 // end to end and cut into equal runs, one to a CTA.  An item cut by a run's
@@ -45,7 +47,7 @@ constexpr int kTile = 128;                 // positions a tile
 constexpr int kHalfBytes = kTile * 128;    // 128 swizzled rows of 128 bytes
 constexpr float kLazy = 24.0f;             // log2 of how far a weight may lie from one
 constexpr int kMaxSlots = 8;
-constexpr int kScaleSlots = 4;             // tiles of scales in flight
+constexpr int kQuarter = kTile / 4;        // positions a loading warp takes care of
 // Query rows a CTA: 128, but 64 where the three 8-bit terms of wider heads'
 // queries would leave the loads no room.
 __host__ __device__ constexpr int attn_rows_max(bool e4m3, int D) { return e4m3 && D > 128 ? 64 : 128; }
@@ -167,9 +169,9 @@ struct alignas(16) ItemInfo {
 
 struct AttnShared {
     uint64_t kfull[kMaxSlots], kempty[kMaxSlots];  // K slots
-    uint64_t vfull[kMaxSlots], vempty[kMaxSlots];  // V slots
+    uint64_t vfull[kMaxSlots], vempty[kMaxSlots];  // V slots (bf16)
+    uint64_t vpart[kMaxSlots][4];                  // quarters of V slots (e4m3)
     uint64_t cfull[2], cempty[2];                  // converted V slots (e4m3)
-    uint64_t sfull[kScaleSlots], sempty[kScaleSlots];   // scales (e4m3)
     uint64_t q_full, q_empty, info_full[2], info_empty[2];
     uint64_t s_full[2], s_empty[2], p_full, o_full, drain[2];
     long long t_begin, t_end, sum[16];
@@ -182,7 +184,6 @@ struct AttnShared {
                                                    // product runs at most two ahead of the softmax
     alignas(16) float negm[128];                   // minus the rows' references
     float scratch[2][5 * 64];
-    alignas(128) float scale[kScaleSlots][2][kTile];
     ItemInfo info[2];
 };
 
@@ -491,26 +492,130 @@ __device__ __forceinline__ void store_rows(uint32_t o_at, const int* row_out, co
     }
 }
 
-__host__ __device__ constexpr int attn_threads(bool e4m3) { return e4m3 ? 512 : 384; }
+// Lane l: the row of box l of a quarter of tile x, -1 where the box holds no
+// position (or its page is unusable).
+__device__ __forceinline__ int box_row(const AttnArgs& a, const Tiles& x, int quarter, int lane)
+{
+    const int pos = x.j * kTile + quarter * kQuarter + lane * a.box_rows;
+    if (!x.more || lane * a.box_rows >= kQuarter || pos >= x.run.s.len)
+        return -1;
+    const int page = kv_page(a.c, x.run.b, pos);
+    return page < 0 ? -1 : (int)kv_row(a.c, page, pos) + ((x.run.hg / a.groups) << a.c.page_shift);
+}
 
-// Registers a thread: the softmax's warpgroups hold a row's sums and half of
-// its scores a thread, the others little.  The shares add up to the launch's.
-template <bool E4M3> constexpr int kAttnRegs = E4M3 ? 128 : 168;          // at launch
-template <bool E4M3> constexpr int kRegsSoftmax = E4M3 ? 168 : 200;       // warps 0 .. 7
-template <bool E4M3> constexpr int kRegsIssue = E4M3 ? 80 : 104;          // warps 8 .. 11
-constexpr int kRegsConvert = 96;                                          // warps 12 .. 15
-static_assert(512 * kAttnRegs<true> == 256 * kRegsSoftmax<true> + 128 * kRegsIssue<true> + 128 * kRegsConvert &&
-              384 * kAttnRegs<false> == 256 * kRegsSoftmax<false> + 128 * kRegsIssue<false>,
-              "register shares");
+// One warp: the boxes of chunk c of a quarter tile into a slot's rows at dst.
+template <bool E4M3>
+__device__ __forceinline__ void load_boxes(const AttnArgs& a, uint32_t dst, uint32_t bar, const CUtensorMap* map, int c, int row, int lane)
+{
+    const uint32_t step = a.box_rows * 128;
+    const bool two = !E4M3 && a.c.D - 128 * c > 64;
+    const unsigned have = __ballot_sync(kFull, row >= 0);
+    if (lane == 0)
+        mbar_arrive_expect_tx(bar, __popc(have) * step * (two ? 2 : 1));
+    __syncwarp();
+    if (row >= 0) {
+        tma_load_2d(dst + lane * step, map, 128 * c, row, bar);
+        if (two)
+            tma_load_2d(dst + kHalfBytes + lane * step, map, 128 * c + 64, row, bar);
+    }
+    __syncwarp();
+}
+
+// One warp: what item number `items` of the CTA's run needs to know of its rows.
+template <int N, bool E4M3>
+__device__ __forceinline__ bool prepare_item(const AttnArgs& a, AttnShared& sh, const Run& run, uint32_t items, int lane)
+{
+    ItemInfo& info = sh.info[items & 1];
+    const int h = run.hg / a.groups, g = run.hg - h * a.groups, nn = run.s.nn, ctx = run.s.ctx;
+    const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
+    int par;
+    const bool tree = tree_parents(a.parent + (long long)run.b * a.Nmax, a.has_parent, nn, lane, par);
+    // lane n: node n and its ancestors
+    unsigned anc = lane < nn ? 1u << lane : 0u;
+    {
+        int at = lane < nn && tree ? par : -1;
+        while (__any_sync(kFull, at >= 0)) {   // parents are earlier nodes: at most 31 steps
+            if (at >= 0)
+                anc |= 1u << at;
+            const int up = __shfl_sync(kFull, par, max(at, 0));
+            at = at >= 0 ? up : -1;
+        }
+        if (!tree && lane < nn)
+            anc = ~0u;   // (a malformed tree's rows end as NaN, whatever they see)
+    }
+    // the part's pages; its nodes' values
+    bool bad = !tree;
+    const int p1 = min(run.t1 * kTile, run.s.len);
+    for (int pos = run.t0 * kTile + (lane << a.c.page_shift); pos < p1; pos += 32 << a.c.page_shift)
+        bad |= kv_page(a.c, run.b, pos) < 0;
+    bad = __any_sync(kFull, bad);
+    unsigned poison = 0;
+    if (nn > 1 && run.t1 * kTile > ctx) {
+        const int bytes = a.c.D * (E4M3 ? 1 : 2);
+        // lane m: where node m's row lies
+        long long row = -1;
+        if (lane < nn && ctx + lane >= run.t0 * kTile && ctx + lane < run.t1 * kTile) {
+            const int page = kv_page(a.c, run.b, ctx + lane);
+            if (page >= 0)
+                row = kv_row(a.c, page, ctx + lane) + ((long long)h << a.c.page_shift);
+        }
+        if (E4M3 && row >= 0 && !isfinite(a.c.v_scale[row]))
+            poison = 1u << lane;
+        if (row >= 0) {   // a lane reads its node's row, eight pieces in flight
+            const uint4* x = reinterpret_cast<const uint4*>(a.c.v + row * bytes);
+            bool hit = false;
+            for (int i = 0; i < bytes / 16; i += 8) {
+                uint4 y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    y[k] = i + k < bytes / 16 ? __ldg(x + i + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    hit |= chunk_nonfinite(y[k], E4M3);
+            }
+            if (hit)
+                poison = 1u << lane;
+        }
+        poison = __reduce_or_sync(kFull, poison);
+    }
+    if (!cta_wait(sh, &sh.info_empty[items & 1], ((items >> 1) & 1) ^ 1))
+        return false;
+    if (lane == 0) {
+        info.poison = poison;
+        info.bad = bad;
+    }
+    for (int r = lane; r < (N + 31) / 32 * 32; r += 32) {
+        int node = 0, head = 0;
+        const bool real = r < N && attn_row(a, g, r, node, head);
+        const unsigned its = __shfl_sync(kFull, anc, node & 31);
+        info.anc[r] = real && node < nn ? its : 0u;
+        info.row_out[r] = !real         ? -1
+                          : run.whole() ? (run.b * a.Nmax + node) * a.Hq + h * a.G + head
+                                        : part * a.rows + r;
+    }
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(smem_addr(&sh.info_full[items & 1]));
+    return true;
+}
+
+constexpr int kAttnThreads = 512;
+// Registers a thread: the softmax's warpgroups hold a row's scores and sums a
+// thread, the others little.  The shares add up to the launch's.
+constexpr int kAttnRegs = 128;       // at launch
+constexpr int kRegsSoftmax = 168;    // warps 0 .. 7
+constexpr int kRegsIssue = 72;       // warps 8 .. 11
+constexpr int kRegsTiles = 104;       // warps 12 .. 15
+static_assert(4 * kAttnRegs == 2 * kRegsSoftmax + kRegsIssue + kRegsTiles, "register shares");
 
 // NT: rows (TMEM columns) a softmax warpgroup handles; NWG: softmax
 // warpgroups with rows.
 template <int NT, int NWG, bool E4M3>
-__global__ void __launch_bounds__(attn_threads(E4M3), 1)
+__global__ void __launch_bounds__(kAttnThreads, 1)
     sv_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q)
 {
-    constexpr int kThreads = attn_threads(E4M3), kWarps = kThreads / 32, N = NT * NWG;
+    constexpr int kThreads = kAttnThreads, kWarps = kThreads / 32, N = NT * NWG;
     extern __shared__ __align__(1024) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = a.c.D;
     {
@@ -521,16 +626,14 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
         } else if (tid == 9 * 32) {
             sh.abort = 0;
             for (int i = 0; i < a.kslots; ++i) {
-                mbar_init(smem_addr(&sh.kfull[i]), 1);
+                mbar_init(smem_addr(&sh.kfull[i]), 4);
                 mbar_init(smem_addr(&sh.kempty[i]), 1);
             }
             for (int i = 0; i < a.vslots; ++i) {
-                mbar_init(smem_addr(&sh.vfull[i]), 1);
-                mbar_init(smem_addr(&sh.vempty[i]), E4M3 ? 4 : 1);
-            }
-            for (int i = 0; i < kScaleSlots; ++i) {
-                mbar_init(smem_addr(&sh.sfull[i]), 1);
-                mbar_init(smem_addr(&sh.sempty[i]), 4 * NWG);
+                mbar_init(smem_addr(&sh.vfull[i]), 4);
+                mbar_init(smem_addr(&sh.vempty[i]), 1);
+                for (int k = 0; k < 4; ++k)
+                    mbar_init(smem_addr(&sh.vpart[i][k]), 1);
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_addr(&sh.cfull[i]), 4);
@@ -607,7 +710,7 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
     // (The register moves stand inside the warpgroups' branches: ptxas budgets
     // what they dominate.)
     if (warp < 8) {
-        regs_grow<kRegsSoftmax<E4M3>>();
+        regs_grow<kRegsSoftmax>();
         if (warp < 4 * NWG) {
             // --- softmax: one position a thread, NT rows --------------------------
             const AttnLayout L = attn_layout<N, E4M3>(a, smem);
@@ -619,7 +722,6 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
             float* const scratch = sh.scratch[w];
             float* const negm = sh.negm + w * NT;
             uint32_t gt = 0, items = 0;   // tiles, items so far
-            Ring rs;
             while (run.next(a, true)) {
                 const int ctx = run.s.ctx, nn = run.s.nn;
                 const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
@@ -641,6 +743,23 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                     }
                     continue;
                 }
+                // pages and scales a tile ahead (e4m3)
+                const int h = run.hg / a.groups;
+                auto page_of = [&](int j) {
+                    const int pos = j * kTile + t;
+                    return E4M3 && j < run.t1 && pos < run.s.len ? kv_page(a.c, run.b, pos) : -1;
+                };
+                auto scales_of = [&](int j, int page, float& k, float& v) {
+                    k = v = 0.0f;
+                    if (E4M3 && page >= 0) {
+                        const long long row = kv_row(a.c, page, j * kTile + t) + ((long long)h << a.c.page_shift);
+                        k = __ldg(a.c.k_scale + row);
+                        v = __ldg(a.c.v_scale + row);
+                    }
+                };
+                float ks, vs, ks_next, vs_next;
+                int page_next = page_of(run.t0 + 1);
+                scales_of(run.t0, page_of(run.t0), ks, vs);
                 const ItemInfo& info = sh.info[items & 1];
                 cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
                 const unsigned poison = info.poison;
@@ -659,13 +778,9 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                     const bool first_tile = j == run.t0;
                     float mult = a.scale_log2, vscale = 1.0f, vunscale = 1.0f;
                     if (E4M3) {
-                        cta_wait(sh, &sh.sfull[rs.slot], rs.phase);
-                        const float ks = sh.scale[rs.slot][0][t];
-                        vscale = sh.scale[rs.slot][1][t];
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(smem_addr(&sh.sempty[rs.slot]));
-                        rs.step(kScaleSlots);
+                        scales_of(j + 1, page_next, ks_next, vs_next);
+                        page_next = page_of(j + 2);
+                        vscale = vs;
                         if (first_tile) {   // (the queries' power of two is there once their first product is)
                             cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
                             scale_log2 = a.scale_log2 * sh.q_unscale[items & 3];
@@ -765,6 +880,10 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                         mbar_arrive(smem_addr(&sh.s_empty[gt & 1]));
                         mbar_arrive(smem_addr(&sh.p_full));
                     }
+                    if (E4M3) {
+                        ks = ks_next;
+                        vs = vs_next;
+                    }
                 }
 
                 // the rows' sums over the 128 threads, while the last product runs
@@ -794,7 +913,7 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                 float* const fin = scratch + 4 * NT;
                 if (bar_any(bar, 128, *reinterpret_cast<volatile int*>(&sh.abort) != 0)) {
                     // a wait gave up: nothing of the item can be relied on, its rows are NaN
-                    const int h = run.hg / a.groups, g = run.hg - h * a.groups;
+                    const int g = run.hg - h * a.groups;
                     if (tid == 0 && a.has_err)
                         atomicOr(a.err, kErrWaitTimeout);
                     for (int r = w * NT + (warp & 3); r < min(a.rows, (w + 1) * NT); r += 4) {
@@ -844,20 +963,67 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                 ++items;
             }
         }
-    } else if (E4M3 && warp >= 12) {
-        regs_shrink<kRegsConvert>();
-        // --- e4m3 values to bf16 operands -------------------------------------------
-        // A thread takes one position's row: rows of a warp differ in their
-        // swizzle, so neither the loads nor the stores collide.
+    } else if (warp >= 12) {
+        regs_shrink<kRegsTiles>();
+        // --- tiles: a quarter of the positions a warp ----------------------------------
         const AttnLayout L = attn_layout<N, E4M3>(a, smem);
         AttnShared& sh = *L.sh;
+        const int quarter = warp & 3, t = tid - 384, key = t & 7;
+        // how far keys and values are asked for ahead of the tile that the loop is at: a slot less than there
+        // are, so that the one to be refilled is likely free
+        const int k_ahead = max(1, a.kslots / a.nd - 1), v_ahead = max(1, a.vslots / a.nd - 1);
+        Tiles k, v;
+        k.start(a, run_of(a, sh));
+        v = k;
+        Ring rk, rv;
+        int nk = 0, nv = 0;   // slots that may still be filling
+        int row_k = box_row(a, k, quarter, lane), row_v = row_k;
+        auto load_k = [&]() {
+            const int now = row_k;
+            k.step(a);
+            row_k = box_row(a, k, quarter, lane);   // on its way while this tile is asked for
+            for (int c = 0; c < a.nd; ++c) {
+                if (!cta_wait(sh, &sh.kempty[rk.slot], rk.phase ^ 1))
+                    return false;
+                load_boxes<E4M3>(a, smem_addr(L.k) + rk.slot * a.k_bytes + quarter * kQuarter * 128, smem_addr(&sh.kfull[rk.slot]), &map_k, c, now, lane);
+                rk.step(a.kslots);
+                nk = min(nk + 1, a.kslots);
+            }
+            return true;
+        };
+        auto load_v = [&]() {
+            const int now = row_v;
+            v.step(a);
+            row_v = box_row(a, v, quarter, lane);
+            for (int c = 0; c < a.nd; ++c) {
+                // (an e4m3 quarter is reloaded by the warp that has read it)
+                if (!E4M3 && !cta_wait(sh, &sh.vempty[rv.slot], rv.phase ^ 1))
+                    return false;
+                load_boxes<E4M3>(a, smem_addr(L.v) + rv.slot * a.v_bytes + quarter * kQuarter * 128,
+                                 smem_addr(E4M3 ? &sh.vpart[rv.slot][quarter] : &sh.vfull[rv.slot]), &map_v, c, now, lane);
+                rv.step(a.vslots);
+                nv = min(nv + 1, a.vslots);
+            }
+            return true;
+        };
+        bool go = true;
+        for (int i = 0; go && i < k_ahead && k.more; ++i)
+            go = load_k();
+        for (int i = 0; go && i < v_ahead && v.more; ++i)
+            go = load_v();
         Tiles it;
         it.start(a, run_of(a, sh));
+        if (!E4M3)
+            for (; go && it.more; it.step(a)) {
+                if (k.more)
+                    go = load_k();
+                if (go && v.more)
+                    go = load_v();
+            }
         Run ahead = it.run;      // the item after
         bool more = it.more;
         uint32_t items = 0;
         Ring r, w;
-        const int t = tid - 384, key = t & 7;
         // an item's queries, as three 8-bit terms (before its keys' first product)
         auto queries = [&](const Run& x) {
             const int h = x.hg / a.groups, g = x.hg - h * a.groups, nb = g / a.head_blocks;
@@ -925,11 +1091,14 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                 mbar_arrive(smem_addr(&sh.q_full));
             ++items;
         };
-        if (more) {
+        if (E4M3 && more) {
             queries(it.run);
             more = ahead.next(a);
         }
-        for (; it.more; it.step(a)) {
+        for (; E4M3 && it.more; it.step(a)) {
+            // (the warps share a barrier: after a timeout they all run on, doing nothing)
+            if (go && k.more)
+                go = load_k();
             if (it.j == it.run.t1 - 1 && more) {   // the next item's queries, before this one's last values
                 queries(ahead);
                 more = ahead.next(a);
@@ -937,8 +1106,7 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
             const int valid = it.valid(), rows = (valid + 15) & ~15;
             const int node0 = it.run.s.nn > 1 ? it.run.s.ctx - it.j * kTile : kTile;   // first row of a node
             for (int c = 0; c < a.nd; ++c) {
-                // (the warps share a barrier: after a timeout they all run on, doing nothing)
-                const bool go = cta_wait(sh, &sh.vfull[r.slot], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
+                go = go && cta_wait(sh, &sh.vpart[r.slot][quarter], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
                 const unsigned char* src = L.v + r.slot * a.v_bytes + t * 128;
                 unsigned char* dst = L.c + w.slot * a.conv_bytes + t * 128;
                 const int pieces = min(128, D - 128 * c) / 16;
@@ -975,124 +1143,49 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                 }
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_addr(&sh.vempty[r.slot]));
+                if (lane == 0)
                     mbar_arrive(smem_addr(&sh.cfull[w.slot]));
-                }
                 r.step(a.vslots);
                 w.step(a.conv);
             }
+            if (go && v.more)
+                go = load_v();
+        }
+        if (!go) {   // copies in flight land before the CTA's memory is given back
+            for (; nk > 0; --nk) {
+                rk.back(a.kslots);
+                mbar_wait_bounded(smem_addr(&sh.kfull[rk.slot]), rk.phase, kWaitSpins);
+            }
+            for (; nv > 0; --nv) {
+                rv.back(a.vslots);
+                mbar_wait_bounded(smem_addr(E4M3 ? &sh.vpart[rv.slot][quarter] : &sh.vfull[rv.slot]), rv.phase, kWaitSpins);
+            }
         }
     } else {
-        regs_shrink<kRegsIssue<E4M3>>();
+        regs_shrink<kRegsIssue>();
         const AttnLayout L = attn_layout<N, E4M3>(a, smem);
         AttnShared& sh = *L.sh;
         if (warp == 9) {
-            // --- TMA -------------------------------------------------------------------
-            Ring rk, rv, rs;
-            int nk = 0, nv = 0, ns = 0, nq = 0;   // slots that may still be filling
+            // --- bf16 queries --------------------------------------------------------------
+            Run run = run_of(a, sh);
             uint32_t items = 0;
-            const int boxes = kTile / a.box_rows;
-            Tiles k, v;
-            k.start(a, run_of(a, sh));
-            v = k;
-            // lane l: row of a tile's box l, -1 where it holds no position (or its page is unusable)
-            auto box_row = [&](const Tiles& x) {
-                const int pos = x.j * kTile + lane * a.box_rows;
-                if (!x.more || lane >= boxes || pos >= x.run.s.len)
-                    return -1;
-                const int page = kv_page(a.c, x.run.b, pos);
-                return page < 0 ? -1 : (int)kv_row(a.c, page, pos) + ((x.run.hg / a.groups) << a.c.page_shift);
-            };
-            // rows of the tiles of the next V (two, in order) and of the K after the next
-            int row_v = -1, row_k = box_row(k);
             bool go = true;
-            auto load = [&](bool is_k, int row, Ring& r, int slots) {
-                const unsigned have = __ballot_sync(kFull, row >= 0);
-                for (int c = 0; c < a.nd; ++c) {
-                    if (!cta_wait(sh, is_k ? &sh.kempty[r.slot] : &sh.vempty[r.slot], r.phase ^ 1))
-                        return false;
-                    const uint32_t bar = smem_addr(is_k ? &sh.kfull[r.slot] : &sh.vfull[r.slot]);
-                    const uint32_t dst = (is_k ? smem_addr(L.k) + r.slot * a.k_bytes : smem_addr(L.v) + r.slot * a.v_bytes) + lane * a.box_rows * 128;
-                    const int halves = E4M3 ? 1 : min(2, (D - 128 * c + 63) / 64);
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(bar, __popc(have) * a.box_rows * 128 * halves);
-                    __syncwarp();
-                    if (row >= 0)
-                        for (int x = 0; x < halves; ++x)
-                            tma_load_2d(dst + x * kHalfBytes, is_k ? &map_k : &map_v, 128 * c + 64 * x, row, bar);
-                    r.step(slots);
-                    int& filling = is_k ? nk : nv;
-                    filling = min(filling + 1, slots);
+            while (!E4M3 && run.next(a)) {
+                go = cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
+                if (!go)
+                    break;
+                ++items;
+                if (lane == 0) {
+                    const int h = run.hg / a.groups, g = run.hg - h * a.groups, nb = g / a.head_blocks;
+                    mbar_arrive_expect_tx(smem_addr(&sh.q_full), a.rows * 128 * ((D + 63) / 64));
+                    for (int c = 0; c < (D + 63) / 64; ++c)
+                        tma_load_3d(smem_addr(L.q) + c * (N * 128), &map_q, 64 * c, h * a.G + (g - nb * a.head_blocks) * a.heads,
+                                    run.b * a.Nmax + nb * a.nodes, smem_addr(&sh.q_full));
                 }
-                return true;
-            };
-            while (go && v.more) {
-                if (k.more) {
-                    if (!E4M3 && k.j == k.run.t0) {   // a new item: its queries
-                        go = cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
-                        if (!go)
-                            break;
-                        ++items;
-                        nq = 1;
-                        if (lane == 0) {
-                            const int h = k.run.hg / a.groups, g = k.run.hg - h * a.groups, nb = g / a.head_blocks;
-                            mbar_arrive_expect_tx(smem_addr(&sh.q_full), a.rows * 128 * ((D + 63) / 64));
-                            for (int c = 0; c < (D + 63) / 64; ++c)
-                                tma_load_3d(smem_addr(L.q) + c * (N * 128), &map_q, 64 * c, h * a.G + (g - nb * a.head_blocks) * a.heads,
-                                            k.run.b * a.Nmax + nb * a.nodes, smem_addr(&sh.q_full));
-                        }
-                        __syncwarp();
-                    }
-                    go = load(true, row_k, rk, a.kslots);
-                    if (go && E4M3) {
-                        go = cta_wait(sh, &sh.sempty[rs.slot], rs.phase ^ 1);
-                        if (go) {
-                            const uint32_t bar = smem_addr(&sh.sfull[rs.slot]);
-                            const unsigned have = __ballot_sync(kFull, row_k >= 0);
-                            if (lane == 0)
-                                mbar_arrive_expect_tx(bar, __popc(have) * a.box_rows * 8);
-                            __syncwarp();
-                            if (row_k >= 0) {
-                                bulk_copy_g2s(smem_addr(&sh.scale[rs.slot][0][lane * a.box_rows]), a.c.k_scale + row_k, a.box_rows * 4, bar);
-                                bulk_copy_g2s(smem_addr(&sh.scale[rs.slot][1][lane * a.box_rows]), a.c.v_scale + row_k, a.box_rows * 4, bar);
-                            }
-                            rs.step(kScaleSlots);
-                            ns = min(ns + 1, kScaleSlots);
-                        }
-                    }
-                    if (!go)
-                        break;
-                }
-                // K runs one tile ahead of V
-                const bool first = v.j == k.j && v.run.hg == k.run.hg && v.run.b == k.run.b && k.more;
-                const int row_now = row_k;
-                if (k.more) {
-                    k.step(a);
-                    row_k = box_row(k);
-                }
-                if (!first) {
-                    go = load(false, row_v, rv, a.vslots);
-                    v.step(a);
-                }
-                row_v = row_now;
+                __syncwarp();
             }
-            if (!go) {   // copies in flight land before the CTA's memory is given back
-                for (; nk > 0; --nk) {
-                    rk.back(a.kslots);
-                    mbar_wait_bounded(smem_addr(&sh.kfull[rk.slot]), rk.phase, kWaitSpins);
-                }
-                for (; nv > 0; --nv) {
-                    rv.back(a.vslots);
-                    mbar_wait_bounded(smem_addr(&sh.vfull[rv.slot]), rv.phase, kWaitSpins);
-                }
-                for (; ns > 0; --ns) {
-                    rs.back(kScaleSlots);
-                    mbar_wait_bounded(smem_addr(&sh.sfull[rs.slot]), rs.phase, kWaitSpins);
-                }
-                if (nq)
-                    mbar_wait_bounded(smem_addr(&sh.q_full), (items - 1) & 1, kWaitSpins);
-            }
+            if (!go && items)   // a copy in flight lands before the CTA's memory is given back
+                mbar_wait_bounded(smem_addr(&sh.q_full), (items - 1) & 1, kWaitSpins);
         } else if (warp == 8) {
             // --- first product -----------------------------------------------------------
             const uint32_t tmem = sh.tmem, k0 = smem_addr(L.k), q0 = smem_addr(L.q);
@@ -1202,79 +1295,11 @@ __global__ void __launch_bounds__(attn_threads(E4M3), 1)
                 mbar_wait_bounded(smem_addr(&sh.drain[1]), 0, kWaitSpins);
             }
         } else {
-            // --- the next item's rows ------------------------------------------------------
+            // --- an item's rows ------------------------------------------------------------
             Run run = run_of(a, sh);
             uint32_t items = 0;
-            bool go = true;
-            while (go && run.next(a)) {
-                ItemInfo& info = sh.info[items & 1];
-                const int h = run.hg / a.groups, g = run.hg - h * a.groups, nn = run.s.nn, ctx = run.s.ctx;
-                const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
-                int par;
-                const bool tree = tree_parents(a.parent + (long long)run.b * a.Nmax, a.has_parent, nn, lane, par);
-                // lane n: node n and its ancestors
-                unsigned anc = lane < nn ? 1u << lane : 0u;
-                {
-                    int at = lane < nn && tree ? par : -1;
-                    while (__any_sync(kFull, at >= 0)) {   // parents are earlier nodes: at most 31 steps
-                        if (at >= 0)
-                            anc |= 1u << at;
-                        const int up = __shfl_sync(kFull, par, max(at, 0));
-                        at = at >= 0 ? up : -1;
-                    }
-                    if (!tree && lane < nn)
-                        anc = ~0u;   // (a malformed tree's rows end as NaN, whatever they see)
-                }
-                // the part's pages; its nodes' values, two nodes a turn and 16 lanes a node
-                bool bad = !tree;
-                const int p1 = min(run.t1 * kTile, run.s.len);
-                for (int pos = run.t0 * kTile + (lane << a.c.page_shift); pos < p1; pos += 32 << a.c.page_shift)
-                    bad |= kv_page(a.c, run.b, pos) < 0;
-                bad = __any_sync(kFull, bad);
-                unsigned poison = 0;
-                if (nn > 1 && run.t1 * kTile > ctx) {
-                    const int bytes = D * (E4M3 ? 1 : 2), l = lane & 15;
-                    // lane m: where node m's row lies
-                    long long row = -1;
-                    if (lane < nn && ctx + lane >= run.t0 * kTile && ctx + lane < run.t1 * kTile) {
-                        const int page = kv_page(a.c, run.b, ctx + lane);
-                        if (page >= 0)
-                            row = kv_row(a.c, page, ctx + lane) + ((long long)h << a.c.page_shift);
-                    }
-                    if (E4M3 && row >= 0 && !isfinite(a.c.v_scale[row]))
-                        poison = 1u << lane;
-#pragma unroll 8
-                    for (int m = lane >> 4; m < 32; m += 2) {
-                        const long long at = __shfl_sync(kFull, row, m);
-                        bool hit = false;
-                        if (at >= 0)
-                            for (int i = l; i < bytes / 16; i += 16)
-                                hit |= chunk_nonfinite(__ldg(reinterpret_cast<const uint4*>(a.c.v + at * bytes) + i), E4M3);
-                        poison |= hit ? 1u << m : 0u;
-                    }
-                    poison = __reduce_or_sync(kFull, poison);
-                }
-                go = cta_wait(sh, &sh.info_empty[items & 1], ((items >> 1) & 1) ^ 1);
-                if (!go)
-                    break;
-                if (lane == 0) {
-                    info.poison = poison;
-                    info.bad = bad;
-                }
-                for (int r = lane; r < (N + 31) / 32 * 32; r += 32) {
-                    int node = 0, head = 0;
-                    const bool real = r < N && attn_row(a, g, r, node, head);
-                    const unsigned its = __shfl_sync(kFull, anc, node & 31);
-                    info.anc[r] = real && node < nn ? its : 0u;
-                    info.row_out[r] = !real         ? -1
-                                      : run.whole() ? (run.b * a.Nmax + node) * a.Hq + h * a.G + head
-                                                    : part * a.rows + r;
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.info_full[items & 1]));
+            while (run.next(a) && prepare_item<N, E4M3>(a, sh, run, items, lane))
                 ++items;
-            }
         }
     }
     pdl_launch_dependents();
