@@ -110,7 +110,7 @@ __device__ __forceinline__ SeqLens seq_lens(const AttnArgs& a, int b)
 // no position are passed over but for the role that writes their rows.
 struct Run {
     long long left;
-    int b, hg, tile;
+    int b, h, g, tile;   // sequence, key head, row group; the tile after the part
     SeqLens s;
     // the current part
     int t0, t1;
@@ -122,9 +122,12 @@ struct Run {
                 return false;
             if (tile == s.tiles) {
                 tile = 0;
-                if (++hg == a.c.Hkv * a.groups) {
-                    hg = 0;
-                    s = seq_lens(a, ++b);
+                if (++g == a.groups) {
+                    g = 0;
+                    if (++h == a.c.Hkv) {
+                        h = 0;
+                        s = seq_lens(a, ++b);
+                    }
                 }
             }
             t0 = tile;
@@ -177,7 +180,7 @@ struct AttnShared {
     long long t_begin, t_end, sum[16];
     uint32_t tmem;
     int abort;
-    int b, hg, tile, active;
+    int b, h, g, tile, active;
     int unset[2];
     float top[4];
     float q_unscale[4];                            // undoes the queries' power of two (e4m3), by item: the first
@@ -218,7 +221,8 @@ __device__ __forceinline__ Run run_of(const AttnArgs& a, const AttnShared& share
     Run r;
     r.left = sh.active ? sh.t_end - sh.t_begin : 0;
     r.b = sh.active ? sh.b : 0;
-    r.hg = sh.hg;
+    r.h = sh.h;
+    r.g = sh.g;
     r.tile = sh.tile;
     r.t0 = r.t1 = 0;
     r.s = seq_lens(a, r.b);
@@ -231,6 +235,8 @@ __device__ __forceinline__ Run run_of(const AttnArgs& a, const AttnShared& share
 __device__ __forceinline__ bool cta_wait(AttnShared& sh, uint64_t* bar, uint32_t parity)
 {
     const uint32_t addr = smem_addr(bar);
+    // (never unrolled: the kernel has some forty of these, and its code has to stay in the instruction caches)
+#pragma unroll 1
     for (uint32_t i = 0; i < kWaitSpins; ++i) {
         if (mbar_try_wait(addr, parity))
             return true;
@@ -239,6 +245,15 @@ __device__ __forceinline__ bool cta_wait(AttnShared& sh, uint64_t* bar, uint32_t
     }
     *reinterpret_cast<volatile int*>(&sh.abort) = 1;
     return false;
+}
+
+// The last resort's own wait, for copies and products in flight.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity)
+{
+    const uint32_t addr = smem_addr(bar);
+#pragma unroll 1
+    for (uint32_t i = 0; i < kWaitSpins && !mbar_try_wait(addr, parity); ++i)
+        ;
 }
 
 // Ring position: slot index and the parity its next wait takes.
@@ -370,7 +385,7 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t v, uint32_t p, u
 // The rare step of the softmax, by the warpgroup's 128 threads: rows whose
 // scores lie too far from their references get new ones (their maxima over
 // this tile), and the sums in TMEM are rescaled.  scratch[0 .. NT) then holds
-// the factors of what was summed so far.
+// the factors of what was summed so far, [NT .. 2 NT) how far references rose.
 template <int NT>
 __device__ __forceinline__ void move_references(float* scratch, float* negm, int* unset_flag, uint32_t s_at, uint32_t o_at,
                                                 int o_chunks, int o_pitch, float mult, unsigned long long seen, int t, int bar)
@@ -408,6 +423,7 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
             negm[t] = __float_as_uint(now) == 0u ? -0.0f : now;
         }
         scratch[t] = f;
+        scratch[NT + t] = delta;
     }
     unset = bar_any(bar, 128, unset);
     if (t == 0)
@@ -427,32 +443,27 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
     tmem_wait_st();
 }
 
-// Weights of a position from its scores s (times mult, minus the rows'
-// references if there are any): rounded to bf16 once, with the position's value
+// Weights exp2(s) of a position: rounded to bf16 once, with the position's value
 // scale on them, into P; their sums.  A weight's rounding (a bf16 unit of
 // 2^-8) averages out over the positions.  ROUNDED sums take what P holds, so
 // that the rounding of a weight that dominates its row cancels; that costs
 // three instructions a pair, which the launches of few rows have to spare.
-template <int NT, bool E4M3, bool ROUNDED, bool PLAIN>
-__device__ __forceinline__ void weigh(const float (&s)[NT], float mult, const float* negm, float vscale, float vunscale, uint64_t (&l2)[NT / 2],
-                                      unsigned char* p_row, int at, int t)
+template <int NT, bool E4M3, bool ROUNDED>
+__device__ __forceinline__ void weigh(const float (&s)[NT], float vscale, uint64_t (&l2)[NT / 2], unsigned char* p_row, int at, int t)
 {
-    const uint64_t m2 = f2_pack(mult, mult), v2 = f2_pack(vscale, vscale), u2 = f2_pack(vunscale, vunscale);
-    const ulonglong2* nm = reinterpret_cast<const ulonglong2*>(negm);
+    const float unscale = E4M3 && ROUNDED ? __frcp_rn(vscale) : 1.0f;
+    const uint64_t v2 = f2_pack(vscale, vscale), u2 = f2_pack(unscale, unscale);
 #pragma unroll
     for (int i = 0; i < NT / 8; ++i) {
         uint32_t x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            uint64_t e = f2_pack(s[8 * i + 2 * k], s[8 * i + 2 * k + 1]);
-            e = PLAIN ? f2_mul(e, m2) : f2_fma(e, m2, k & 1 ? nm[2 * i + k / 2].y : nm[2 * i + k / 2].x);
-            float lo, hi;
-            f2_unpack(e, lo, hi);
-            e = f2_pack(ex2_approx(lo), ex2_approx(hi));
+            uint64_t e = f2_pack(ex2_approx(s[8 * i + 2 * k]), ex2_approx(s[8 * i + 2 * k + 1]));
             if (!ROUNDED)
                 l2[4 * i + k] = f2_add(l2[4 * i + k], e);
             if (E4M3)
                 e = f2_mul(e, v2);
+            float lo, hi;
             f2_unpack(e, lo, hi);
             x[k] = bf16_pair(lo, hi);
             if (ROUNDED) {
@@ -469,13 +480,13 @@ __device__ __forceinline__ void weigh(const float (&s)[NT], float mult, const fl
 template <int NT, typename F>
 __device__ __forceinline__ void store_rows(uint32_t o_at, const int* row_out, const float* fin, int d, int D, F out)
 {
-#pragma unroll
-    for (int i = 0; i < NT; i += 16) {
-        float o[16];
-        tmem_ld16(o_at + i, o);
+#pragma unroll 1
+    for (int i = 0; i < NT; i += 8) {
+        float o[8];
+        tmem_ld8(o_at + i, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; k += 4) {
+        for (int k = 0; k < 8; k += 4) {
             const int4 at = *reinterpret_cast<const int4*>(row_out + i + k);
             const float4 f = *reinterpret_cast<const float4*>(fin + i + k);
             if (d < D) {
@@ -492,16 +503,47 @@ __device__ __forceinline__ void store_rows(uint32_t o_at, const int* row_out, co
     }
 }
 
-// Lane l: the row of box l of a quarter of tile x, -1 where the box holds no
-// position (or its page is unusable).
-__device__ __forceinline__ int box_row(const AttnArgs& a, const Tiles& x, int quarter, int lane)
+// Loads that stay where they are written (a plain one sinks to its first use,
+// an iteration later, and takes its latency there).
+__device__ __forceinline__ int load_now(const int* p)
 {
-    const int pos = x.j * kTile + quarter * kQuarter + lane * a.box_rows;
-    if (!x.more || lane * a.box_rows >= kQuarter || pos >= x.run.s.len)
-        return -1;
-    const int page = kv_page(a.c, x.run.b, pos);
-    return page < 0 ? -1 : (int)kv_row(a.c, page, pos) + ((x.run.hg / a.groups) << a.c.page_shift);
+    int x;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(x) : "l"(p));
+    return x;
 }
+
+__device__ __forceinline__ float load_now(const float* p)
+{
+    float x;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(p));
+    return x;
+}
+
+// The page table's entry for position pos of sequence b, as it is.
+__device__ __forceinline__ int page_entry(const AttnArgs& a, int b, int pos)
+{
+    return load_now(a.c.table + (long long)b * a.c.max_pages + (pos >> a.c.page_shift));
+}
+
+// The boxes of a quarter tile: lane l's is where its page starts, or nowhere.
+struct Boxes {
+    int page, pos, h;
+
+    // asks for the pages (the entries are looked at by row(), a tile later)
+    __device__ __forceinline__ void ask(const AttnArgs& a, const Tiles& x, int quarter, int lane)
+    {
+        pos = x.j * kTile + quarter * kQuarter + lane * a.box_rows;
+        h = x.run.h;
+        page = -1;
+        if (x.more && lane * a.box_rows < kQuarter && pos < x.run.s.len)
+            page = page_entry(a, x.run.b, pos);
+    }
+    // its first row, -1 where the box holds no position (or its page is unusable)
+    __device__ __forceinline__ int row(const AttnArgs& a) const
+    {
+        return (unsigned)page < (unsigned)a.c.num_pages ? (int)kv_row(a.c, page, pos) + (h << a.c.page_shift) : -1;
+    }
+};
 
 // One warp: the boxes of chunk c of a quarter tile into a slot's rows at dst.
 template <bool E4M3>
@@ -526,7 +568,7 @@ template <int N, bool E4M3>
 __device__ __forceinline__ bool prepare_item(const AttnArgs& a, AttnShared& sh, const Run& run, uint32_t items, int lane)
 {
     ItemInfo& info = sh.info[items & 1];
-    const int h = run.hg / a.groups, g = run.hg - h * a.groups, nn = run.s.nn, ctx = run.s.ctx;
+    const int h = run.h, g = run.g, nn = run.s.nn, ctx = run.s.ctx;
     const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
     int par;
     const bool tree = tree_parents(a.parent + (long long)run.b * a.Nmax, a.has_parent, nn, lane, par);
@@ -546,6 +588,7 @@ __device__ __forceinline__ bool prepare_item(const AttnArgs& a, AttnShared& sh, 
     // the part's pages; its nodes' values
     bool bad = !tree;
     const int p1 = min(run.t1 * kTile, run.s.len);
+#pragma unroll 1
     for (int pos = run.t0 * kTile + (lane << a.c.page_shift); pos < p1; pos += 32 << a.c.page_shift)
         bad |= kv_page(a.c, run.b, pos) < 0;
     bad = __any_sync(kFull, bad);
@@ -564,6 +607,7 @@ __device__ __forceinline__ bool prepare_item(const AttnArgs& a, AttnShared& sh, 
         if (row >= 0) {   // a lane reads its node's row, eight pieces in flight
             const uint4* x = reinterpret_cast<const uint4*>(a.c.v + row * bytes);
             bool hit = false;
+#pragma unroll 1
             for (int i = 0; i < bytes / 16; i += 8) {
                 uint4 y[8];
 #pragma unroll
@@ -584,6 +628,7 @@ __device__ __forceinline__ bool prepare_item(const AttnArgs& a, AttnShared& sh, 
         info.poison = poison;
         info.bad = bad;
     }
+#pragma unroll 1
     for (int r = lane; r < (N + 31) / 32 * 32; r += 32) {
         int node = 0, head = 0;
         const bool real = r < N && attn_row(a, g, r, node, head);
@@ -625,10 +670,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_alloc(smem_addr(&sh.tmem), 512);
         } else if (tid == 9 * 32) {
             sh.abort = 0;
+#pragma unroll 1
             for (int i = 0; i < a.kslots; ++i) {
                 mbar_init(smem_addr(&sh.kfull[i]), 4);
                 mbar_init(smem_addr(&sh.kempty[i]), 1);
             }
+#pragma unroll 1
             for (int i = 0; i < a.vslots; ++i) {
                 mbar_init(smem_addr(&sh.vfull[i]), 4);
                 mbar_init(smem_addr(&sh.vempty[i]), 1);
@@ -654,6 +701,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tma_prefetch_map(&map_v);
         }
         // the rows of no query, and the elements past head_dim, stay zeros
+#pragma unroll 1
         for (int i = tid; i < (int)(reinterpret_cast<unsigned char*>(L.sh) - L.q) / 16; i += kThreads)
             reinterpret_cast<uint4*>(L.q)[i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async();
@@ -661,6 +709,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int share = (a.B + kThreads - 1) / kThreads, b0 = min(tid * share, a.B), b1 = min(b0 + share, a.B);
         const int per = a.c.Hkv * a.groups;
         long long mine = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b)
             mine += (long long)seq_lens(a, b).tiles * per;
         long long incl = mine;
@@ -674,6 +723,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             sh.sum[warp] = incl;
         __syncthreads();
         long long before = 0, total = 0;
+#pragma unroll 1
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp)
                 before += sh.sum[w];
@@ -681,10 +731,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         const long long excl = before + incl - mine;
         const int act = (int)min((long long)gridDim.x, total), i = blockIdx.x;
-        const long long begin = total * i / act, end = total * (i + 1) / act;
+        const long long each = total / act, extra = total - each * act;
+        const long long begin = each * i + min((long long)i, extra), end = each * (i + 1) + min((long long)i + 1, extra);
         if (i < act && begin >= excl && begin < excl + mine) {
             long long at = excl;
             int b = b0;
+#pragma unroll 1
             for (;; ++b) {
                 const long long n = (long long)seq_lens(a, b).tiles * per;
                 if (begin < at + n)
@@ -693,8 +745,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             const int tiles = seq_lens(a, b).tiles;
             sh.b = b;
-            sh.hg = (int)((begin - at) / tiles);
-            sh.tile = (int)((begin - at) % tiles);
+            const int hg = (int)((begin - at) / tiles);
+            sh.h = hg / a.groups;
+            sh.g = hg - sh.h * a.groups;
+            sh.tile = (int)((begin - at) - (long long)hg * tiles);
             sh.t_begin = begin;
             sh.t_end = end;
         }
@@ -723,244 +777,221 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             float* const negm = sh.negm + w * NT;
             uint32_t gt = 0, items = 0;   // tiles, items so far
             while (run.next(a, true)) {
-                const int ctx = run.s.ctx, nn = run.s.nn;
+                const int ctx = run.s.ctx, nn = run.s.nn, h = run.h;
                 const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
                 const bool whole = run.whole();
                 if (!whole && tid == 0)   // meta[2i]: begun here, meta[2i + 1]: continued here
-                    a.meta[part ^ 1] = run.b * (a.c.Hkv * a.groups) + run.hg;
-                if (run.s.len == 0) {
-                    // no position, or unusable lengths: zeros, or NaN
-                    const int h = run.hg / a.groups, g = run.hg - h * a.groups;
-                    const float x = run.s.ok ? 0.0f : NAN;
-                    if (!run.s.ok && tid == 0 && a.has_err)
-                        atomicOr(a.err, kErrCache);
-                    for (int r = w * NT + (warp & 3); r < min(a.rows, (w + 1) * NT); r += 4) {
-                        int node, head;
-                        if (attn_row(a, g, r, node, head))
-                            for (int d = lane; d < D; d += 32)
-                                a.out[(((long long)run.b * a.Nmax + node) * a.Hq + h * a.G + head) * D + d] =
-                                    __float2bfloat16_rn(node < nn ? x : 0.0f);
-                    }
-                    continue;
-                }
-                // pages and scales a tile ahead (e4m3)
-                const int h = run.hg / a.groups;
-                auto page_of = [&](int j) {
-                    const int pos = j * kTile + t;
-                    return E4M3 && j < run.t1 && pos < run.s.len ? kv_page(a.c, run.b, pos) : -1;
-                };
-                auto scales_of = [&](int j, int page, float& k, float& v) {
-                    k = v = 0.0f;
-                    if (E4M3 && page >= 0) {
-                        const long long row = kv_row(a.c, page, j * kTile + t) + ((long long)h << a.c.page_shift);
-                        k = __ldg(a.c.k_scale + row);
-                        v = __ldg(a.c.v_scale + row);
-                    }
-                };
-                float ks, vs, ks_next, vs_next;
-                int page_next = page_of(run.t0 + 1);
-                scales_of(run.t0, page_of(run.t0), ks, vs);
-                const ItemInfo& info = sh.info[items & 1];
-                cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
-                const unsigned poison = info.poison;
-                if (t < NT)
-                    negm[t] = 0.0f;   // read by others after the first vote only
-                if (t == 0)
-                    sh.unset[w] = 0;
-                float scale_log2 = a.scale_log2;
-                bool plain = true;    // every reference is zero
-                uint64_t l2[NT / 2];  // this thread's share of the rows' sums, in pairs
-#pragma unroll
-                for (int i = 0; i < NT / 2; ++i)
-                    l2[i] = 0;
-
-                for (int j = run.t0; j < run.t1; ++j, ++gt) {
-                    const bool first_tile = j == run.t0;
-                    float mult = a.scale_log2, vscale = 1.0f, vunscale = 1.0f;
-                    if (E4M3) {
-                        scales_of(j + 1, page_next, ks_next, vs_next);
-                        page_next = page_of(j + 2);
-                        vscale = vs;
-                        if (first_tile) {   // (the queries' power of two is there once their first product is)
-                            cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
-                            scale_log2 = a.scale_log2 * sh.q_unscale[items & 3];
+                    a.meta[part ^ 1] = (run.b * a.c.Hkv + h) * a.groups + run.g;
+                bool lost = !run.s.ok;   // the item's rows are NaN
+                if (run.s.len != 0) {
+                    // pages and scales a tile ahead (e4m3)
+                    auto page_of = [&](int j) {
+                        const int pos = j * kTile + t;
+                        return E4M3 && j < run.t1 && pos < run.s.len ? page_entry(a, run.b, pos) : -1;
+                    };
+                    auto scales_of = [&](int j, int page, float& k, float& v) {
+                        k = v = 0.0f;
+                        if (E4M3 && (unsigned)page < (unsigned)a.c.num_pages) {
+                            const long long row = kv_row(a.c, page, j * kTile + t) + ((long long)h << a.c.page_shift);
+                            k = load_now(a.c.k_scale + row);
+                            v = load_now(a.c.v_scale + row);
                         }
-                        mult = scale_log2;
-                        // a scale that is not finite marks a row that held something that was not
-                        mult *= isfinite(ks) ? ks : NAN;
-                        vscale = isfinite(vscale) ? vscale : NAN;
-                        vscale = fabsf(vscale) < 0x1p-100f ? 0x1p-100f : vscale;   // (all of such a row's values are zero in the sum)
-                    }
-                    // what this position's scores are seen by: every row in the context, a node's descendants behind it
-                    const bool tail = (j + 1) * kTile > ctx;   // the tile holds nodes, or ends the sequence
-                    unsigned long long seen = ~0ull;
-                    if (tail) {
-                        const int m = j * kTile + t - ctx;
-                        if (m >= 0) {
-                            seen = 0;
-                            if (m < nn && !((poison >> m) & 1u)) {
-#pragma unroll 4
-                                for (int i = 0; i < NT; ++i)
-                                    seen |= (unsigned long long)((info.anc[w * NT + i] >> m) & 1u) << i;
-                            } else {   // nothing sees it: its scales may be anything
-                                vscale = 1.0f;
-                                mult = scale_log2;
+                    };
+                    float ks, vs, ks_next = 0.0f, vs_next = 0.0f;
+                    int page_next = page_of(run.t0);
+                    scales_of(run.t0, page_next, ks, vs);
+                    page_next = page_of(run.t0 + 1);
+                    const ItemInfo& info = sh.info[items & 1];
+                    cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
+                    const unsigned poison = info.poison;
+                    if (t < NT)
+                        negm[t] = 0.0f;
+                    if (t == 0)
+                        sh.unset[w] = 0;
+                    bar_sync(bar, 128);
+                    float scale_log2 = a.scale_log2;
+                    uint64_t l2[NT / 2];  // this thread's share of the rows' sums, in pairs
+#pragma unroll
+                    for (int i = 0; i < NT / 2; ++i)
+                        l2[i] = 0;
+
+#pragma unroll 1
+                    for (int j = run.t0; j < run.t1; ++j, ++gt) {
+                        const bool first_tile = j == run.t0;
+                        cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
+                        tc_fence_after();
+                        const uint32_t s_at = tmem + (gt & 1) * N;
+                        float s[NT];
+#pragma unroll
+                        for (int i = 0; i < NT / 16; ++i)
+                            tmem_ld16(s_at + 16 * i, s + 16 * i);
+                        float mult = a.scale_log2, vscale = 1.0f;
+                        if (E4M3) {
+                            if (first_tile)
+                                scale_log2 = a.scale_log2 * sh.q_unscale[items & 3];
+                            // a scale that is not finite marks a row that held something that was not
+                            mult = scale_log2 * (isfinite(ks) ? ks : NAN);
+                            vscale = isfinite(vs) ? vs : NAN;
+                            vscale = fabsf(vscale) < 0x1p-100f ? 0x1p-100f : vscale;   // (all of such a row's values are zero in the sum)
+                            scales_of(j + 1, page_next, ks_next, vs_next);
+                            page_next = page_of(j + 2);
+                        }
+                        // scores in powers of two, relative to the rows' references
+                        const uint64_t m2 = f2_pack(mult, mult);
+                        const ulonglong2* nm = reinterpret_cast<const ulonglong2*>(negm);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < NT / 4; ++i) {
+                            const ulonglong2 x = nm[i];
+                            f2_unpack(f2_fma(f2_pack(s[4 * i], s[4 * i + 1]), m2, x.x), s[4 * i], s[4 * i + 1]);
+                            f2_unpack(f2_fma(f2_pack(s[4 * i + 2], s[4 * i + 3]), m2, x.y), s[4 * i + 2], s[4 * i + 3]);
+                        }
+                        // who sees this position: every row in the context, a node's descendants behind it
+                        unsigned long long seen = ~0ull;
+                        if ((j + 1) * kTile > ctx) {   // the tile holds nodes, or ends the sequence
+                            const int m = j * kTile + t - ctx;
+                            if (m >= 0) {
+                                seen = 0;
+                                if (m < nn && !((poison >> m) & 1u)) {
+#pragma unroll 1
+                                    for (int i = 0; i < NT; ++i)
+                                        seen |= (unsigned long long)((info.anc[w * NT + i] >> m) & 1u) << i;
+                                } else {   // nothing does: its scales may be anything
+                                    vscale = 1.0f;
+                                }
                             }
+#pragma unroll
+                            for (int i = 0; i < NT; ++i)
+                                s[i] = (seen >> i) & 1 ? s[i] : -INFINITY;
                         }
-                    }
-                    if (E4M3 && NWG == 1)
-                        vunscale = __frcp_rn(vscale);
-                    if (mult == 0.0f)
-                        mult = FLT_MIN;   // so that a hidden score's infinity stays one
-                    const uint32_t s_at = tmem + (gt & 1) * N;
-
-                    cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
-                    tc_fence_after();
-                    float s[NT];
-#pragma unroll
-                    for (int i = 0; i < NT / 16; ++i)
-                        tmem_ld16(s_at + 16 * i, s + 16 * i);
-                    tmem_wait_ld();
-                    if (tail) {
-                        const float hidden = mult < 0.0f ? INFINITY : -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < NT; ++i)
-                            s[i] = (seen >> i) & 1 ? s[i] : hidden;
-                    }
-                    if (plain) {   // are all scores near enough to the references?
-                        float top[4], low[4];
+                        // are all scores near enough to the references?
+                        float top[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            top[k] = max3(s[4 * k], s[4 * k + 1], max3(s[4 * k + 2], s[4 * k + 3], -INFINITY));
+                            top[k] = max3(s[4 * k], s[4 * k + 1], fmaxf(s[4 * k + 2], s[4 * k + 3]));
 #pragma unroll
                         for (int i = 16; i < NT; i += 2)
                             top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], s[i], s[i + 1]);
-                        plain = !bar_any(bar, 128, max3(top[0], top[1], fmaxf(top[2], top[3])) * mult > kLazy || mult < 0.0f);
-                        if (first_tile) {   // zero will do as a reference if some position's scores are all near enough
+                        bool move = bar_any(bar, 128, max3(top[0], top[1], fmaxf(top[2], top[3])) > kLazy) || sh.unset[w];
+                        if (first_tile) {
+                            // no reference yet: zero will do if some position's scores are all near enough
+                            float low[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                low[k] = min3(s[4 * k], s[4 * k + 1], min3(s[4 * k + 2], s[4 * k + 3], INFINITY));
+                                low[k] = min3(s[4 * k], s[4 * k + 1], fminf(s[4 * k + 2], s[4 * k + 3]));
 #pragma unroll
                             for (int i = 16; i < NT; i += 2)
                                 low[(i >> 1) & 3] = min3(low[(i >> 1) & 3], s[i], s[i + 1]);
-                            plain = bar_any(bar, 128, min3(low[0], low[1], fminf(low[2], low[3])) * mult >= -kLazy) && plain;
+                            move = !bar_any(bar, 128, min3(low[0], low[1], fminf(low[2], low[3])) >= -kLazy) || move;
+                            if (!move && t < NT)
+                                negm[t] = -0.0f;   // (+0 marks a row without a reference)
+                        } else {   // the previous tile's product is done with P (and O)
+                            cta_wait(sh, &sh.o_full, (gt - 1) & 1);
+                            tc_fence_after();
                         }
-                    }
-                    if (!first_tile) {   // the previous tile's product is done with P (and O)
-                        cta_wait(sh, &sh.o_full, (gt - 1) & 1);
-                        tc_fence_after();
-                    }
-                    unsigned char* const p_row = L.p + t * 128;
-                    if (plain) {
-                        weigh<NT, E4M3, NWG == 1, true>(s, mult, negm, vscale, vunscale, l2, p_row, w * (NT / 8), t);
-                    } else {
-                        float top = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < NT; ++i)
-                            top = fmaxf(top, fmaf(s[i], mult, negm[i]));
-                        // +0 marks a row without a reference: a part that was plain until now has them all (zeros)
-                        if (!first_tile && t < NT && __float_as_uint(negm[t]) == 0u && !sh.unset[w])
-                            negm[t] = -0.0f;
-                        if (bar_any(bar, 128, top > kLazy || first_tile) || sh.unset[w]) {
+                        if (move) {
                             move_references<NT>(scratch, negm, &sh.unset[w], s_at, tmem_o, first_tile ? 0 : a.nd, N, mult, seen, t, bar);
 #pragma unroll
                             for (int i = 0; i < NT / 4; ++i) {
-                                const ulonglong2 f4 = reinterpret_cast<const ulonglong2*>(scratch)[i];
-                                l2[2 * i] = f2_mul(l2[2 * i], f4.x);
-                                l2[2 * i + 1] = f2_mul(l2[2 * i + 1], f4.y);
+                                const ulonglong2 f = reinterpret_cast<const ulonglong2*>(scratch)[i];
+                                const float4 d = reinterpret_cast<const float4*>(scratch + NT)[i];
+                                l2[2 * i] = f2_mul(l2[2 * i], f.x);
+                                l2[2 * i + 1] = f2_mul(l2[2 * i + 1], f.y);
+                                s[4 * i] -= d.x;
+                                s[4 * i + 1] -= d.y;
+                                s[4 * i + 2] -= d.z;
+                                s[4 * i + 3] -= d.w;
                             }
                             bar_sync(bar, 128);   // the scratch may be written again
                         }
-                        weigh<NT, E4M3, NWG == 1, false>(s, mult, negm, vscale, vunscale, l2, p_row, w * (NT / 8), t);
+                        weigh<NT, E4M3, NWG == 1>(s, vscale, l2, L.p + t * 128, w * (NT / 8), t);
+                        tc_fence_before();
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(smem_addr(&sh.s_empty[gt & 1]));
+                            mbar_arrive(smem_addr(&sh.p_full));
+                        }
+                        if (E4M3) {
+                            ks = ks_next;
+                            vs = vs_next;
+                        }
+                    }
+
+                    // the rows' sums over the 128 threads, while the last product runs
+#pragma unroll
+                    for (int i = 0; i < NT / 16; ++i) {
+                        // lane c (of 16) ends with column 16 i + c: halve the columns, double the lanes summed
+                        float x[16];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            f2_unpack(l2[8 * i + k], x[2 * k], x[2 * k + 1]);
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                            for (int k = 0; k < o; ++k) {
+                                const bool up = lane & o;
+                                const float send = up ? x[k] : x[k + o];
+                                const float keep = up ? x[k + o] : x[k];
+                                x[k] = keep + __shfl_xor_sync(kFull, send, o);
+                            }
+                        x[0] += __shfl_xor_sync(kFull, x[0], 16);
+                        if (lane < 16)
+                            scratch[(warp & 3) * NT + 16 * i + lane] = x[0];
+                    }
+                    float* const fin = scratch + 4 * NT;
+                    // (after a wait that gave up nothing of the item can be relied on)
+                    const bool abort = bar_any(bar, 128, *reinterpret_cast<volatile int*>(&sh.abort) != 0), bad = abort || info.bad;
+                    if (tid == 0 && bad && a.has_err)
+                        atomicOr(a.err, abort ? kErrWaitTimeout : kErrCache);
+                    lost |= abort;
+                    if (t < NT && !abort) {
+                        const unsigned anc = info.anc[w * NT + t];
+                        float l = (scratch[t] + scratch[NT + t]) + (scratch[2 * NT + t] + scratch[3 * NT + t]);
+                        if (bad || (anc & poison))
+                            l = NAN;
+                        fin[t] = l == 0.0f || anc == 0 ? 0.0f : __fdividef(1.0f, l);   // (anc == 0: no node's row)
+                        const int at = info.row_out[w * NT + t];
+                        if (!whole && at >= 0)
+                            reinterpret_cast<float2*>(a.part_ml)[at] = make_float2(-negm[t], l);
+                    }
+                    cta_wait(sh, &sh.o_full, (gt - 1) & 1);
+                    tc_fence_after();
+                    bar_sync(bar, 128);
+#pragma unroll 1
+                    for (int c = 0; c < a.nd && !abort; ++c) {
+                        const int d = 128 * c + (E4M3 ? converted_element(t) : t);
+                        const int* const row_out = info.row_out + w * NT;
+                        if (whole)
+                            store_rows<NT>(tmem_o + c * N, row_out, fin, d, D, [&](int at, float x, float f) {
+                                a.out[(long long)at * D + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : x * f);
+                            });
+                        else
+                            store_rows<NT>(tmem_o + c * N, row_out, fin, d, D, [&](int at, float x, float) { a.part_o[(long long)at * D + d] = x; });
                     }
                     tc_fence_before();
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_addr(&sh.s_empty[gt & 1]));
-                        mbar_arrive(smem_addr(&sh.p_full));
-                    }
-                    if (E4M3) {
-                        ks = ks_next;
-                        vs = vs_next;
-                    }
+                    bar_sync(bar, 128);   // O, the scratch and the item's rows have been read
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&sh.info_empty[items & 1]));
+                    ++items;
                 }
-
-                // the rows' sums over the 128 threads, while the last product runs
-                float sum[NT / 16];
-#pragma unroll
-                for (int i = 0; i < NT / 16; ++i) {
-                    // lane c (of 16) ends with column 16 i + c: halve the columns, double the lanes summed
-                    float x[16];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        f2_unpack(l2[8 * i + k], x[2 * k], x[2 * k + 1]);
-#pragma unroll
-                    for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-                        for (int k = 0; k < o; ++k) {
-                            const bool up = lane & o;
-                            const float send = up ? x[k] : x[k + o];
-                            const float keep = up ? x[k + o] : x[k];
-                            x[k] = keep + __shfl_xor_sync(kFull, send, o);
-                        }
-                    sum[i] = x[0] + __shfl_xor_sync(kFull, x[0], 16);
-                }
-#pragma unroll
-                for (int i = 0; i < NT / 16; ++i)
-                    if (lane < 16)
-                        scratch[(warp & 3) * NT + 16 * i + lane] = sum[i];
-                float* const fin = scratch + 4 * NT;
-                if (bar_any(bar, 128, *reinterpret_cast<volatile int*>(&sh.abort) != 0)) {
-                    // a wait gave up: nothing of the item can be relied on, its rows are NaN
-                    const int g = run.hg - h * a.groups;
-                    if (tid == 0 && a.has_err)
-                        atomicOr(a.err, kErrWaitTimeout);
+                if (run.s.len == 0 || lost) {
+                    // no position: zeros; unusable lengths, or a wait that gave up: NaN
+                    if (!run.s.ok && tid == 0 && a.has_err)
+                        atomicOr(a.err, kErrCache);
+#pragma unroll 1
                     for (int r = w * NT + (warp & 3); r < min(a.rows, (w + 1) * NT); r += 4) {
                         int node, head;
-                        if (!attn_row(a, g, r, node, head))
+                        if (!attn_row(a, run.g, r, node, head))
                             continue;
                         if (!whole && lane < 2)
                             a.part_ml[((long long)part * a.rows + r) * 2 + lane] = NAN;
+#pragma unroll 1
                         for (int d = lane; whole && d < D; d += 32)
-                            a.out[(((long long)run.b * a.Nmax + node) * a.Hq + h * a.G + head) * D + d] = __float2bfloat16_rn(NAN);
-                    }
-                    ++items;
-                    continue;
-                }
-                const bool bad = info.bad;
-                if (tid == 0 && bad && a.has_err)
-                    atomicOr(a.err, kErrCache);
-                if (t < NT) {
-                    const unsigned anc = info.anc[w * NT + t];
-                    float l = (scratch[t] + scratch[NT + t]) + (scratch[2 * NT + t] + scratch[3 * NT + t]);
-                    if (bad || (anc & poison))
-                        l = NAN;
-                    fin[t] = !whole ? 1.0f : l == 0.0f || anc == 0 ? 0.0f : 1.0f / l;   // (anc == 0: no node's row)
-                    const int at = info.row_out[w * NT + t];
-                    if (!whole && at >= 0) {
-                        a.part_ml[(long long)at * 2] = -negm[t];
-                        a.part_ml[(long long)at * 2 + 1] = l;
+                            a.out[(((long long)run.b * a.Nmax + node) * a.Hq + h * a.G + head) * D + d] =
+                                __float2bfloat16_rn(node < nn && lost ? NAN : 0.0f);
                     }
                 }
-                cta_wait(sh, &sh.o_full, (gt - 1) & 1);
-                tc_fence_after();
-                bar_sync(bar, 128);
-                for (int c = 0; c < a.nd; ++c) {
-                    const int d = 128 * c + (E4M3 ? converted_element(t) : t);
-                    const int* const row_out = info.row_out + w * NT;
-                    if (whole)
-                        store_rows<NT>(tmem_o + c * N, row_out, fin, d, D, [&](int at, float x, float f) {
-                            a.out[(long long)at * D + d] = __float2bfloat16_rn(f == 0.0f ? 0.0f : x * f);
-                        });
-                    else
-                        store_rows<NT>(tmem_o + c * N, row_out, fin, d, D, [&](int at, float x, float) { a.part_o[(long long)at * D + d] = x; });
-                }
-                tc_fence_before();
-                bar_sync(bar, 128);   // O, the scratch and the item's rows have been read
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.info_empty[items & 1]));
-                ++items;
             }
         }
     } else if (warp >= 12) {
@@ -977,11 +1008,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         v = k;
         Ring rk, rv;
         int nk = 0, nv = 0;   // slots that may still be filling
-        int row_k = box_row(a, k, quarter, lane), row_v = row_k;
+        Boxes box_k, box_v;
+        box_k.ask(a, k, quarter, lane);
+        box_v = box_k;
         auto load_k = [&]() {
-            const int now = row_k;
+            const int now = box_k.row(a);
             k.step(a);
-            row_k = box_row(a, k, quarter, lane);   // on its way while this tile is asked for
+            box_k.ask(a, k, quarter, lane);   // on its way while this tile is asked for
+#pragma unroll 1
             for (int c = 0; c < a.nd; ++c) {
                 if (!cta_wait(sh, &sh.kempty[rk.slot], rk.phase ^ 1))
                     return false;
@@ -992,9 +1026,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             return true;
         };
         auto load_v = [&]() {
-            const int now = row_v;
+            const int now = box_v.row(a);
             v.step(a);
-            row_v = box_row(a, v, quarter, lane);
+            box_v.ask(a, v, quarter, lane);
+#pragma unroll 1
             for (int c = 0; c < a.nd; ++c) {
                 // (an e4m3 quarter is reloaded by the warp that has read it)
                 if (!E4M3 && !cta_wait(sh, &sh.vempty[rv.slot], rv.phase ^ 1))
@@ -1007,27 +1042,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             return true;
         };
         bool go = true;
-        for (int i = 0; go && i < k_ahead && k.more; ++i)
-            go = load_k();
-        for (int i = 0; go && i < v_ahead && v.more; ++i)
-            go = load_v();
         Tiles it;
         it.start(a, run_of(a, sh));
-        if (!E4M3)
-            for (; go && it.more; it.step(a)) {
-                if (k.more)
-                    go = load_k();
-                if (go && v.more)
-                    go = load_v();
-            }
-        Run ahead = it.run;      // the item after
+        Run ahead = it.run;      // the next item whose queries are to be made
         bool more = it.more;
         uint32_t items = 0;
         Ring r, w;
         // an item's queries, as three 8-bit terms (before its keys' first product)
         auto queries = [&](const Run& x) {
-            const int h = x.hg / a.groups, g = x.hg - h * a.groups, nb = g / a.head_blocks;
-            const int node0 = nb * a.nodes, head0 = (g - nb * a.head_blocks) * a.heads;
+            const int nb = x.g / a.head_blocks, node0 = nb * a.nodes, head0 = (x.g - nb * a.head_blocks) * a.heads;
             const int live = min(a.nodes, x.s.nn - node0), heads = min(a.heads, a.G - head0), per = D / 8;
             // thread t: chunks t, t + 128, ... of the rows' 8-element chunks
             auto load_q = [&](int i) {
@@ -1035,11 +1058,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (n >= live || head >= heads)
                     return make_uint4(0, 0, 0, 0);
                 return __ldg(reinterpret_cast<const uint4*>(a.q + ((long long)x.b * a.Nmax + node0 + n) * a.q_stride +
-                                                            (long long)(h * a.G + head0 + head) * D) + ch);
+                                                            (long long)(x.h * a.G + head0 + head) * D) + ch);
             };
             // a power of two that brings the group's largest element to [128, 256)
             const int chunks = a.rows * per;
             float top = 0.0f;
+#pragma unroll 1
             for (int i = t; i < chunks; i += 512) {
                 uint4 q[4];
 #pragma unroll
@@ -1064,6 +1088,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
             if (t == 0)
                 sh.q_unscale[items & 3] = __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll 1
             for (int i = t; i < chunks; i += 512) {
                 uint4 q[4];
 #pragma unroll
@@ -1091,74 +1116,78 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 mbar_arrive(smem_addr(&sh.q_full));
             ++items;
         };
-        if (E4M3 && more) {
-            queries(it.run);
-            more = ahead.next(a);
-        }
-        for (; E4M3 && it.more; it.step(a)) {
-            // (the warps share a barrier: after a timeout they all run on, doing nothing)
-            if (go && k.more)
+        // step g asks for tile g + k_ahead of the keys, then (e4m3) converts the values of tile g, then asks for
+        // tile g + v_ahead of the values
+#pragma unroll 1
+        for (int g = -max(k_ahead, v_ahead); E4M3 ? it.more : go && (k.more || v.more); ++g) {
+            // (e4m3: the warps share a barrier: after a timeout they all run on, doing nothing)
+            if (go && k.more && g >= -k_ahead)
                 go = load_k();
-            if (it.j == it.run.t1 - 1 && more) {   // the next item's queries, before this one's last values
+            if (E4M3 && more && (items == 0 || (g >= 0 && it.j == it.run.t1 - 1))) {
+                // the first item's queries; the next one's, before this one's last values
                 queries(ahead);
                 more = ahead.next(a);
             }
-            const int valid = it.valid(), rows = (valid + 15) & ~15;
-            const int node0 = it.run.s.nn > 1 ? it.run.s.ctx - it.j * kTile : kTile;   // first row of a node
-            for (int c = 0; c < a.nd; ++c) {
-                go = go && cta_wait(sh, &sh.vpart[r.slot][quarter], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
-                const unsigned char* src = L.v + r.slot * a.v_bytes + t * 128;
-                unsigned char* dst = L.c + w.slot * a.conv_bytes + t * 128;
-                const int pieces = min(128, D - 128 * c) / 16;
-                if (go && t < rows) {
+            if (E4M3 && g >= 0) {
+                const int valid = it.valid(), rows = (valid + 15) & ~15;
+                const int node0 = it.run.s.nn > 1 ? it.run.s.ctx - it.j * kTile : kTile;   // first row of a node
 #pragma unroll 1
-                    for (int i = 0; i < pieces; i += 4) {
-                        // four 16-byte pieces at a time, so that their chains overlap (what is past the row is not used)
-                        uint4 x[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            x[k] = t < valid ? *reinterpret_cast<const uint4*>(src + (((i + k) ^ key) << 4)) : make_uint4(0, 0, 0, 0);
-                        const bool nan = chunk_nan_e4m3(x[0]) | chunk_nan_e4m3(x[1]) | chunk_nan_e4m3(x[2]) | chunk_nan_e4m3(x[3]);
-                        if (nan && t >= node0) {   // a node's values are seen by some rows only (which end as NaN)
+                for (int c = 0; c < a.nd; ++c) {
+                    go = go && cta_wait(sh, &sh.vpart[r.slot][quarter], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
+                    const unsigned char* src = L.v + r.slot * a.v_bytes + t * 128;
+                    unsigned char* dst = L.c + w.slot * a.conv_bytes + t * 128;
+                    const int pieces = min(128, D - 128 * c) / 16;
+                    if (go && t < rows) {
+#pragma unroll 1
+                        for (int i = 0; i < pieces; i += 4) {
+                            // four 16-byte pieces at a time, so that their chains overlap (what is past the row is not used)
+                            uint4 x[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                x[k] = make_uint4(0, 0, 0, 0);
-                        }
-                        unsigned char* o = dst + (i >> 2) * kHalfBytes;
+                                x[k] = t < valid ? *reinterpret_cast<const uint4*>(src + (((i + k) ^ key) << 4)) : make_uint4(0, 0, 0, 0);
+                            const bool nan = chunk_nan_e4m3(x[0]) | chunk_nan_e4m3(x[1]) | chunk_nan_e4m3(x[2]) | chunk_nan_e4m3(x[3]);
+                            if (nan && t >= node0) {   // a node's values are seen by some rows only (which end as NaN)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint2 y0 = e4m3_to_bf16(x[k].x), y1 = e4m3_to_bf16(x[k].y), y2 = e4m3_to_bf16(x[k].z), y3 = e4m3_to_bf16(x[k].w);
-                            *reinterpret_cast<uint4*>(o + (((2 * k) ^ key) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
-                            *reinterpret_cast<uint4*>(o + (((2 * k + 1) ^ key) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
-                        }
-                        if (nan && t < node0) {   // NaN, which the conversion reads as 480
+                                for (int k = 0; k < 4; ++k)
+                                    x[k] = make_uint4(0, 0, 0, 0);
+                            }
+                            unsigned char* o = dst + (i >> 2) * kHalfBytes;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint2 y0 = e4m3_to_bf16(x[k].x), y1 = e4m3_to_bf16(x[k].y), y2 = e4m3_to_bf16(x[k].z), y3 = e4m3_to_bf16(x[k].w);
+                                *reinterpret_cast<uint4*>(o + (((2 * k) ^ key) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
+                                *reinterpret_cast<uint4*>(o + (((2 * k + 1) ^ key) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
+                            }
+                            if (nan && t < node0) {   // NaN, which the conversion reads as 480
 #pragma unroll 1
-                            for (int k = 0; k < 64; ++k)
-                                if ((src[(((i + (k >> 4)) ^ key) << 4) + (k & 15)] & 0x7f) == 0x7f) {
-                                    const int e = converted_element(k);   // where that element went
-                                    *reinterpret_cast<unsigned short*>(o + (((e >> 3) ^ key) << 4) + 2 * (e & 7)) = 0x7fff;
-                                }
+                                for (int k = 0; k < 64; ++k)
+                                    if ((src[(((i + (k >> 4)) ^ key) << 4) + (k & 15)] & 0x7f) == 0x7f) {
+                                        const int e = converted_element(k);   // where that element went
+                                        *reinterpret_cast<unsigned short*>(o + (((e >> 3) ^ key) << 4) + 2 * (e & 7)) = 0x7fff;
+                                    }
+                            }
                         }
                     }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&sh.cfull[w.slot]));
+                    r.step(a.vslots);
+                    w.step(a.conv);
                 }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.cfull[w.slot]));
-                r.step(a.vslots);
-                w.step(a.conv);
+                it.step(a);
             }
-            if (go && v.more)
+            if (go && v.more && g >= -v_ahead)
                 go = load_v();
         }
         if (!go) {   // copies in flight land before the CTA's memory is given back
             for (; nk > 0; --nk) {
                 rk.back(a.kslots);
-                mbar_wait_bounded(smem_addr(&sh.kfull[rk.slot]), rk.phase, kWaitSpins);
+                drain_wait(&sh.kfull[rk.slot], rk.phase);
             }
             for (; nv > 0; --nv) {
                 rv.back(a.vslots);
-                mbar_wait_bounded(smem_addr(E4M3 ? &sh.vpart[rv.slot][quarter] : &sh.vfull[rv.slot]), rv.phase, kWaitSpins);
+                drain_wait(E4M3 ? &sh.vpart[rv.slot][quarter] : &sh.vfull[rv.slot], rv.phase);
             }
         }
     } else {
@@ -1176,8 +1205,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     break;
                 ++items;
                 if (lane == 0) {
-                    const int h = run.hg / a.groups, g = run.hg - h * a.groups, nb = g / a.head_blocks;
+                    const int h = run.h, g = run.g, nb = g / a.head_blocks;
                     mbar_arrive_expect_tx(smem_addr(&sh.q_full), a.rows * 128 * ((D + 63) / 64));
+#pragma unroll 1
                     for (int c = 0; c < (D + 63) / 64; ++c)
                         tma_load_3d(smem_addr(L.q) + c * (N * 128), &map_q, 64 * c, h * a.G + (g - nb * a.head_blocks) * a.heads,
                                     run.b * a.Nmax + nb * a.nodes, smem_addr(&sh.q_full));
@@ -1185,7 +1215,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 __syncwarp();
             }
             if (!go && items)   // a copy in flight lands before the CTA's memory is given back
-                mbar_wait_bounded(smem_addr(&sh.q_full), (items - 1) & 1, kWaitSpins);
+                drain_wait(&sh.q_full, (items - 1) & 1);
         } else if (warp == 8) {
             // --- first product -----------------------------------------------------------
             const uint32_t tmem = sh.tmem, k0 = smem_addr(L.k), q0 = smem_addr(L.q);
@@ -1197,6 +1227,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (k.j == k.run.t0)
                     go = cta_wait(sh, &sh.q_full, items++ & 1);
                 go = go && cta_wait(sh, &sh.s_empty[g & 1], ((g >> 1) & 1) ^ 1);
+#pragma unroll 1
                 for (int c = 0; go && c < a.nd; ++c) {
                     const int width = min(128, D - 128 * c);
                     go = cta_wait(sh, &sh.kfull[rk.slot], rk.phase);
@@ -1223,7 +1254,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0)
                     tc_commit(smem_addr(&sh.drain[0]));
                 __syncwarp();
-                mbar_wait_bounded(smem_addr(&sh.drain[0]), 0, kWaitSpins);
+                drain_wait(&sh.drain[0], 0);
             }
         } else if (warp == 10) {
             // --- second product ----------------------------------------------------------
@@ -1239,6 +1270,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (v.start(a, run_of(a, sh)); v.more; ++g) {
                 const int valid = v.valid(), ksteps = (valid + 15) / 16;
                 const bool tail = (v.j + 1) * kTile > v.run.s.ctx;
+#pragma unroll 1
                 for (int c = 0; go && c < a.nd; ++c) {
                     const int width = min(128, D - 128 * c);
                     go = cta_wait(sh, &full[rv.slot], rv.phase);
@@ -1250,6 +1282,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         // that do see it are set to NaN at the end).
                         unsigned char* x = L.v + rv.slot * a.v_bytes;
                         const int chunks = width > 64 ? 16 : 8;
+#pragma unroll 1
                         for (int i = valid * chunks + lane; i < ksteps * 16 * chunks; i += 32) {
                             const int row = i / chunks, ch = i % chunks;
                             *reinterpret_cast<uint4*>(x + (ch >> 3) * kHalfBytes + row * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -1259,6 +1292,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             break;
                         const int row = v.run.s.ctx + lane - v.j * kTile;
                         if (((sh.info[items & 1].poison >> lane) & 1u) && row >= 0 && row < kTile)
+#pragma unroll 1
                             for (int ch = 0; ch < chunks; ++ch) {
                                 uint4* p = reinterpret_cast<uint4*>(x + (ch >> 3) * kHalfBytes + row * 128 + ((ch ^ lane) & 7) * 16);
                                 if (chunk_nonfinite(*p, false))
@@ -1292,7 +1326,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0)
                     tc_commit(smem_addr(&sh.drain[1]));
                 __syncwarp();
-                mbar_wait_bounded(smem_addr(&sh.drain[1]), 0, kWaitSpins);
+                drain_wait(&sh.drain[1], 0);
             }
         } else {
             // --- an item's rows ------------------------------------------------------------
@@ -1328,7 +1362,7 @@ __global__ void __launch_bounds__(256) sv_attention_combine(const __grid_constan
         if (more < 32)
             break;
     }
-    const int per = a.c.Hkv * a.groups, b = item / per, hg = item - b * per, h = hg / a.groups, g = hg - h * a.groups;
+    const int per = a.c.Hkv * a.groups, b = item / per, h = (item - b * per) / a.groups, g = item - (b * a.c.Hkv + h) * a.groups;
     const int row = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
     int node, head;
     if (!attn_row(a, g, row, node, head))

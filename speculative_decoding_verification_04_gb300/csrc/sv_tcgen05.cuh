@@ -73,7 +73,7 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t lo)
     return (uint64_t)lo | ((uint64_t)((1024 >> 4) | (1u << 14) | (2u << 29)) << 32);
 }
 
-// Sixteen TMEM columns of the warp's 32 lanes, one lane a thread.
+// Sixteen (eight) TMEM columns of the warp's 32 lanes, one lane a thread.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, float* x)
 {
     uint32_t r[16];
@@ -84,6 +84,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float* x)
         : "r"(addr));
 #pragma unroll
     for (int i = 0; i < 16; ++i)
+        x[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, float* x)
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(addr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
         x[i] = __uint_as_float(r[i]);
 }
 
