@@ -1048,35 +1048,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         bool more = it.more;
         uint32_t items = 0;
         Ring r, w;
-        // an item's queries, as three 8-bit terms (before its keys' first product)
+        // an item's queries, as three 8-bit terms (before its keys' first product): a thread takes one 8-element
+        // chunk of every `stride`th row
+        const int per = D / 8, stride = 128 / per, row0 = t / per, ch = t - row0 * per;
         auto queries = [&](const Run& x) {
             const int nb = x.g / a.head_blocks, node0 = nb * a.nodes, head0 = (x.g - nb * a.head_blocks) * a.heads;
-            const int live = min(a.nodes, x.s.nn - node0), heads = min(a.heads, a.G - head0), per = D / 8;
-            // thread t: chunks t, t + 128, ... of the rows' 8-element chunks
-            auto load_q = [&](int i) {
-                const int row = i / per, ch = i - row * per, n = row / a.heads, head = row - n * a.heads;
-                if (n >= live || head >= heads)
-                    return make_uint4(0, 0, 0, 0);
-                return __ldg(reinterpret_cast<const uint4*>(a.q + ((long long)x.b * a.Nmax + node0 + n) * a.q_stride +
-                                                            (long long)(x.h * a.G + head0 + head) * D) + ch);
-            };
-            // a power of two that brings the group's largest element to [128, 256)
-            const int chunks = a.rows * per;
-            float top = 0.0f;
-#pragma unroll 1
-            for (int i = t; i < chunks; i += 512) {
-                uint4 q[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    q[k] = i + 128 * k < chunks ? load_q(i + 128 * k) : make_uint4(0, 0, 0, 0);
+            const int live = min(a.nodes, x.s.nn - node0), heads = min(a.heads, a.G - head0);
+            const uint4* const q = reinterpret_cast<const uint4*>(a.q + ((long long)x.b * a.Nmax + node0) * a.q_stride +
+                                                                  (long long)(x.h * a.G + head0) * D) + ch;
+            // the queries of four rows at a time, zeros where there is none
+            auto load_q = [&](int row, uint4 (&y)[4]) {
+                int n = row / a.heads, head = row - n * a.heads;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float y[8];
-                    Elem<__nv_bfloat16>::unpack(q[k], y);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        top = fmaxf(top, isfinite(y[e]) ? fabsf(y[e]) : 0.0f);
+                    y[k] = n < live && head < heads && row0 < stride ? __ldg(q + n * (a.q_stride / 8) + head * per) : make_uint4(0, 0, 0, 0);
+                    for (head += stride; head >= a.heads; head -= a.heads)
+                        ++n;
                 }
+            };
+            // a power of two that brings the group's largest element to [128, 256)
+            float top = 0.0f;
+#pragma unroll 1
+            for (int row = row0; row < a.rows; row += 4 * stride) {
+                uint4 y[4];
+                load_q(row, y);
+                uint32_t m = 0;   // magnitudes order as integers; what is not finite does not count
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t z[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t lo = (z[e] << 16) & 0x7fff0000u, hi = z[e] & 0x7fff0000u;
+                        m = max(m, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
+                    }
+                }
+                top = fmaxf(top, __uint_as_float(m));
             }
             top = warp_redux_max(top);
             if (lane == 0)
@@ -1089,26 +1095,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (t == 0)
                 sh.q_unscale[items & 3] = __uint_as_float((uint32_t)(254 - e) << 23);
 #pragma unroll 1
-            for (int i = t; i < chunks; i += 512) {
-                uint4 q[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    q[k] = i + 128 * k < chunks ? load_q(i + 128 * k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (i + 128 * k < chunks) {
-                        const int row = (i + 128 * k) / per, ch = i + 128 * k - row * per;
-                        float y[8];
-                        Elem<__nv_bfloat16>::unpack(q[k], y);
+            for (int row = row0; row < a.rows; row += 4 * stride) {
+                uint4 y[4];
+                load_q(row, y);
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    const int at = row + k * stride;
+                    if (at < a.rows && row0 < stride) {
+                        float z[8];
+                        Elem<__nv_bfloat16>::unpack(y[0], z);
                         uint32_t p[3][4];
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            split_q(y[2 * c] * scale, y[2 * c + 1] * scale, p[0][c], p[1][c], p[2][c]);
-                        unsigned char* o = L.q + (ch >> 4) * (N * 128) + row * 128 + ((((ch & 15) >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
+                            split_q(z[2 * c] * scale, z[2 * c + 1] * scale, p[0][c], p[1][c], p[2][c]);
+                        unsigned char* o = L.q + (ch >> 4) * (N * 128) + at * 128 + ((((ch & 15) >> 1) ^ (at & 7)) << 4) + (ch & 1) * 8;
 #pragma unroll
                         for (int c = 0; c < 3; ++c)
                             *reinterpret_cast<uint2*>(o + c * L.q_part) = make_uint2(p[c][0] | (p[c][1] << 16), p[c][2] | (p[c][3] << 16));
                     }
+                    y[0] = y[1];   // (rolled: the code is long)
+                    y[1] = y[2];
+                    y[2] = y[3];
+                }
             }
             fence_proxy_async();
             bar_sync(3, 128);   // (also: sh.top may be written again)
