@@ -277,25 +277,15 @@ struct Ring {
     }
 };
 
-// Four e4m3 values (bytes 0 .. 3 of w) as four bf16, in the order 0, 2, 1, 3,
-// exactly: the eight bits' exponent and mantissa fields land in the bf16's low
-// exponent and high mantissa bits, which is the value times 2^-120 (subnormals
-// included); one multiplication restores it.
-__device__ __forceinline__ uint32_t bf16x2_restore(uint32_t x)
+// Four e4m3 values as bf16, exactly (NaN as NaN): through fp16, which holds
+// them, and fp32.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t two)
 {
-    uint32_t y;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7b807b80u));   // 2^120
-    return y;
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+    return bf16_pair(f.x, f.y);
 }
 
-__device__ __forceinline__ uint2 e4m3_to_bf16(uint32_t w)
-{
-    constexpr uint32_t s = 0x80008000u, m = 0x07f007f0u;
-    return make_uint2(bf16x2_restore(((w << 8) & s) | ((w << 4) & m)), bf16x2_restore((w & s) | ((w >> 4) & m)));
-}
-
-// The head_dim element at a lane of the converted values' order.
-__device__ __forceinline__ int converted_element(int lane) { return (lane & ~3) | ((lane & 1) << 1) | ((lane >> 1) & 1); }
+__device__ __forceinline__ uint2 e4m3_to_bf16(uint32_t w) { return make_uint2(e4m3x2_to_bf16(w & 0xffffu), e4m3x2_to_bf16(w >> 16)); }
 
 __device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w)
 {
@@ -308,15 +298,6 @@ __device__ __forceinline__ bool chunk_nan_e4m3(uint4 w)
 {
     constexpr uint32_t low = 0x7f7f7f7fu, one = 0x01010101u;
     return ((((w.x & low) + one) | ((w.y & low) + one) | ((w.z & low) + one) | ((w.w & low) + one)) & 0x80808080u) != 0;
-}
-
-// NaN for the NaN bytes of w, which e4m3_to_bf16 reads as 480.
-__device__ __noinline__ uint2 e4m3_keep_nan(uint32_t w, uint2 y)
-{
-    const uint32_t m = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    y.x |= ((m >> 7) & 1u) * 0x7fffu | ((m >> 23) & 1u) * 0x7fff0000u;
-    y.y |= ((m >> 15) & 1u) * 0x7fffu | (m >> 31) * 0x7fff0000u;
-    return y;
 }
 
 __device__ __forceinline__ bool chunk_nonfinite(uint4 w, bool e4m3)
@@ -960,7 +941,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     bar_sync(bar, 128);
 #pragma unroll 1
                     for (int c = 0; c < a.nd && !abort; ++c) {
-                        const int d = 128 * c + (E4M3 ? converted_element(t) : t);
+                        const int d = 128 * c + t;
                         const int* const row_out = info.row_out + w * NT;
                         if (whole)
                             store_rows<NT>(tmem_o + c * N, row_out, fin, d, D, [&](int at, float x, float f) {
@@ -1153,11 +1134,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 x[k] = t < valid ? *reinterpret_cast<const uint4*>(src + (((i + k) ^ key) << 4)) : make_uint4(0, 0, 0, 0);
-                            const bool nan = chunk_nan_e4m3(x[0]) | chunk_nan_e4m3(x[1]) | chunk_nan_e4m3(x[2]) | chunk_nan_e4m3(x[3]);
-                            if (nan && t >= node0) {   // a node's values are seen by some rows only (which end as NaN)
+                            if (t >= node0) {   // a node's values are seen by some rows only (which end as NaN)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    x[k] = make_uint4(0, 0, 0, 0);
+                                    if (chunk_nan_e4m3(x[k]))
+                                        x[k] = make_uint4(0, 0, 0, 0);
                             }
                             unsigned char* o = dst + (i >> 2) * kHalfBytes;
 #pragma unroll
@@ -1165,14 +1146,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 const uint2 y0 = e4m3_to_bf16(x[k].x), y1 = e4m3_to_bf16(x[k].y), y2 = e4m3_to_bf16(x[k].z), y3 = e4m3_to_bf16(x[k].w);
                                 *reinterpret_cast<uint4*>(o + (((2 * k) ^ key) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
                                 *reinterpret_cast<uint4*>(o + (((2 * k + 1) ^ key) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
-                            }
-                            if (nan && t < node0) {   // NaN, which the conversion reads as 480
-#pragma unroll 1
-                                for (int k = 0; k < 64; ++k)
-                                    if ((src[(((i + (k >> 4)) ^ key) << 4) + (k & 15)] & 0x7f) == 0x7f) {
-                                        const int e = converted_element(k);   // where that element went
-                                        *reinterpret_cast<unsigned short*>(o + (((e >> 3) ^ key) << 4) + 2 * (e & 7)) = 0x7fff;
-                                    }
                             }
                         }
                     }
