@@ -33,8 +33,9 @@
 // them in one stream across items.
 //
 // Work is (sequence, key head, row group) items of 128-position tiles, laid
-// end to end and cut into equal runs, one to a CTA.  An item cut by a run's
-// end leaves partial sums in the workspace, which sv_attention_combine joins.
+// end to end and cut into runs of equal cost, one to a CTA (an item costs its
+// tiles and kItemCost more).  An item cut by a run's end leaves partial sums
+// in the workspace, which sv_attention_combine joins.
 #pragma once
 
 #include "sv_kv.cuh"
@@ -47,6 +48,7 @@ constexpr int kTile = 128;                 // positions a tile
 constexpr int kHalfBytes = kTile * 128;    // 128 swizzled rows of 128 bytes
 constexpr float kLazy = 24.0f;             // log2 of how far a weight may lie from one
 constexpr int kMaxSlots = 8;
+constexpr int kItemCost = 4;               // what an item's start and end cost, in tiles
 constexpr int kQuarter = kTile / 4;        // positions a loading warp takes care of
 // Query rows a CTA: 128, but 64 where the three 8-bit terms of wider heads'
 // queries would leave the loads no room.
@@ -506,17 +508,18 @@ __device__ __forceinline__ int page_entry(const AttnArgs& a, int b, int pos)
     return load_now(a.c.table + (long long)b * a.c.max_pages + (pos >> a.c.page_shift));
 }
 
-// The boxes of a quarter tile: lane l's is where its page starts, or nowhere.
+// The boxes of `count` positions of a tile from `first` on: lane l's is where
+// its page starts, or nowhere.
 struct Boxes {
     int page, pos, h;
 
     // asks for the pages (the entries are looked at by row(), a tile later)
-    __device__ __forceinline__ void ask(const AttnArgs& a, const Tiles& x, int quarter, int lane)
+    __device__ __forceinline__ void ask(const AttnArgs& a, const Tiles& x, int first, int count, int lane)
     {
-        pos = x.j * kTile + quarter * kQuarter + lane * a.box_rows;
+        pos = x.j * kTile + first + lane * a.box_rows;
         h = x.run.h;
         page = -1;
-        if (x.more && lane * a.box_rows < kQuarter && pos < x.run.s.len)
+        if (x.more && lane * a.box_rows < count && pos < x.run.s.len)
             page = page_entry(a, x.run.b, pos);
     }
     // its first row, -1 where the box holds no position (or its page is unusable)
@@ -526,7 +529,7 @@ struct Boxes {
     }
 };
 
-// One warp: the boxes of chunk c of a quarter tile into a slot's rows at dst.
+// One warp: chunk c of such boxes into a slot's rows at dst.
 template <bool E4M3>
 __device__ __forceinline__ void load_boxes(const AttnArgs& a, uint32_t dst, uint32_t bar, const CUtensorMap* map, int c, int row, int lane)
 {
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             sh.abort = 0;
 #pragma unroll 1
             for (int i = 0; i < a.kslots; ++i) {
-                mbar_init(smem_addr(&sh.kfull[i]), 4);
+                mbar_init(smem_addr(&sh.kfull[i]), E4M3 ? 1 : 4);
                 mbar_init(smem_addr(&sh.kempty[i]), 1);
             }
 #pragma unroll 1
@@ -692,7 +695,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         long long mine = 0;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b)
-            mine += (long long)seq_lens(a, b).tiles * per;
+            mine += (long long)(seq_lens(a, b).tiles + kItemCost) * per;
         long long incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -714,25 +717,38 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int act = (int)min((long long)gridDim.x, total), i = blockIdx.x;
         const long long each = total / act, extra = total - each * act;
         const long long begin = each * i + min((long long)i, extra), end = each * (i + 1) + min((long long)i + 1, extra);
-        if (i < act && begin >= excl && begin < excl + mine) {
-            long long at = excl;
-            int b = b0;
+        // the tile that a point of the cost line falls in (a point in an item's fixed cost: its first tile)
+        if (b1 > b0)
 #pragma unroll 1
-            for (;; ++b) {
-                const long long n = (long long)seq_lens(a, b).tiles * per;
-                if (begin < at + n)
-                    break;
-                at += n;
+            for (int which = 0; which < 2; ++which) {
+                const long long point = which ? end : begin;
+                if (point < excl || point >= excl + mine) {
+                    if (which && point == total && b1 == a.B)
+                        sh.t_end = total - (long long)kItemCost * per * a.B;
+                    continue;
+                }
+                long long at = excl;
+                int b = b0, cost;
+#pragma unroll 1
+                for (;; ++b) {
+                    cost = seq_lens(a, b).tiles + kItemCost;
+                    if (point < at + (long long)cost * per)
+                        break;
+                    at += (long long)cost * per;
+                }
+                const int hg = (int)((point - at) / cost);
+                const int tile = max(0, (int)(point - at - (long long)hg * cost) - kItemCost);
+                const long long t_index = at - (long long)kItemCost * per * b + (long long)hg * (cost - kItemCost) + tile;
+                if (which) {
+                    sh.t_end = t_index;
+                } else {
+                    sh.t_begin = t_index;
+                    sh.b = b;
+                    sh.h = hg / a.groups;
+                    sh.g = hg - sh.h * a.groups;
+                    sh.tile = tile;
+                }
             }
-            const int tiles = seq_lens(a, b).tiles;
-            sh.b = b;
-            const int hg = (int)((begin - at) / tiles);
-            sh.h = hg / a.groups;
-            sh.g = hg - sh.h * a.groups;
-            sh.tile = (int)((begin - at) - (long long)hg * tiles);
-            sh.t_begin = begin;
-            sh.t_end = end;
-        }
         if (tid == 0) {
             sh.active = i < act;
             a.meta[2 * i] = a.meta[2 * i + 1] = -1;
@@ -990,12 +1006,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         Ring rk, rv;
         int nk = 0, nv = 0;   // slots that may still be filling
         Boxes box_k, box_v;
-        box_k.ask(a, k, quarter, lane);
+        box_k.ask(a, k, quarter * kQuarter, kQuarter, lane);
         box_v = box_k;
         auto load_k = [&]() {
             const int now = box_k.row(a);
             k.step(a);
-            box_k.ask(a, k, quarter, lane);   // on its way while this tile is asked for
+            box_k.ask(a, k, quarter * kQuarter, kQuarter, lane);   // on its way while this tile is asked for
 #pragma unroll 1
             for (int c = 0; c < a.nd; ++c) {
                 if (!cta_wait(sh, &sh.kempty[rk.slot], rk.phase ^ 1))
@@ -1009,7 +1025,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         auto load_v = [&]() {
             const int now = box_v.row(a);
             v.step(a);
-            box_v.ask(a, v, quarter, lane);
+            box_v.ask(a, v, quarter * kQuarter, kQuarter, lane);
 #pragma unroll 1
             for (int c = 0; c < a.nd; ++c) {
                 // (an e4m3 quarter is reloaded by the warp that has read it)
@@ -1037,25 +1053,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int live = min(a.nodes, x.s.nn - node0), heads = min(a.heads, a.G - head0);
             const uint4* const q = reinterpret_cast<const uint4*>(a.q + ((long long)x.b * a.Nmax + node0) * a.q_stride +
                                                                   (long long)(x.h * a.G + head0) * D) + ch;
-            // the queries of four rows at a time, zeros where there is none
-            auto load_q = [&](int row, uint4 (&y)[4]) {
+            // eight rows a thread at a time (all of them, up to 64 rows of 128 elements), zeros where there is no query
+            const int turn = 8 * stride;
+            uint4 y[8];
+            auto load_q = [&](int row) {
                 int n = row / a.heads, head = row - n * a.heads;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     y[k] = n < live && head < heads && row0 < stride ? __ldg(q + n * (a.q_stride / 8) + head * per) : make_uint4(0, 0, 0, 0);
                     for (head += stride; head >= a.heads; head -= a.heads)
                         ++n;
                 }
             };
             // a power of two that brings the group's largest element to [128, 256)
-            float top = 0.0f;
+            uint32_t m = 0;   // (magnitudes order as integers; what is not finite does not count)
 #pragma unroll 1
-            for (int row = row0; row < a.rows; row += 4 * stride) {
-                uint4 y[4];
-                load_q(row, y);
-                uint32_t m = 0;   // magnitudes order as integers; what is not finite does not count
+            for (int row = row0; row < a.rows; row += turn) {
+                load_q(row);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     const uint32_t z[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -1063,9 +1079,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         m = max(m, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
                     }
                 }
-                top = fmaxf(top, __uint_as_float(m));
             }
-            top = warp_redux_max(top);
+            float top = warp_redux_max(__uint_as_float(m));
             if (lane == 0)
                 sh.top[warp & 3] = top;
             bar_sync(3, 128);
@@ -1076,27 +1091,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (t == 0)
                 sh.q_unscale[items & 3] = __uint_as_float((uint32_t)(254 - e) << 23);
 #pragma unroll 1
-            for (int row = row0; row < a.rows; row += 4 * stride) {
-                uint4 y[4];
-                load_q(row, y);
+            for (int row = row0; row < a.rows; row += turn) {
+                if (a.rows > turn)
+                    load_q(row);
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     const int at = row + k * stride;
-                    if (at < a.rows && row0 < stride) {
-                        float z[8];
-                        Elem<__nv_bfloat16>::unpack(y[0], z);
-                        uint32_t p[3][4];
+                    if (at >= a.rows || row0 >= stride)
+                        break;
+                    float z[8];
+                    Elem<__nv_bfloat16>::unpack(y[0], z);
+                    uint32_t p[3][4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            split_q(z[2 * c] * scale, z[2 * c + 1] * scale, p[0][c], p[1][c], p[2][c]);
-                        unsigned char* o = L.q + (ch >> 4) * (N * 128) + at * 128 + ((((ch & 15) >> 1) ^ (at & 7)) << 4) + (ch & 1) * 8;
+                    for (int c = 0; c < 4; ++c)
+                        split_q(z[2 * c] * scale, z[2 * c + 1] * scale, p[0][c], p[1][c], p[2][c]);
+                    unsigned char* o = L.q + (ch >> 4) * (N * 128) + at * 128 + ((((ch & 15) >> 1) ^ (at & 7)) << 4) + (ch & 1) * 8;
 #pragma unroll
-                        for (int c = 0; c < 3; ++c)
-                            *reinterpret_cast<uint2*>(o + c * L.q_part) = make_uint2(p[c][0] | (p[c][1] << 16), p[c][2] | (p[c][3] << 16));
-                    }
-                    y[0] = y[1];   // (rolled: the code is long)
-                    y[1] = y[2];
-                    y[2] = y[3];
+                    for (int c = 0; c < 3; ++c)
+                        *reinterpret_cast<uint2*>(o + c * L.q_part) = make_uint2(p[c][0] | (p[c][1] << 16), p[c][2] | (p[c][3] << 16));
+#pragma unroll
+                    for (int c = 0; c < 7; ++c)   // (rolled, the code being long: the next one to the front)
+                        y[c] = y[c + 1];
                 }
             }
             fence_proxy_async();
@@ -1105,12 +1120,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 mbar_arrive(smem_addr(&sh.q_full));
             ++items;
         };
-        // step g asks for tile g + k_ahead of the keys, then (e4m3) converts the values of tile g, then asks for
+        // step g asks for tile g + k_ahead of the keys (bf16) or converts the values of tile g (e4m3), then asks for
         // tile g + v_ahead of the values
 #pragma unroll 1
         for (int g = -max(k_ahead, v_ahead); E4M3 ? it.more : go && (k.more || v.more); ++g) {
             // (e4m3: the warps share a barrier: after a timeout they all run on, doing nothing)
-            if (go && k.more && g >= -k_ahead)
+            if (!E4M3 && go && k.more && g >= -k_ahead)
                 go = load_k();
             if (E4M3 && more && (items == 0 || (g >= 0 && it.j == it.run.t1 - 1))) {
                 // the first item's queries; the next one's, before this one's last values
@@ -1176,27 +1191,55 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const AttnLayout L = attn_layout<N, E4M3>(a, smem);
         AttnShared& sh = *L.sh;
         if (warp == 9) {
-            // --- bf16 queries --------------------------------------------------------------
+            // --- bf16 queries; e4m3 keys (whose other loading warps convert values) --------------
             Run run = run_of(a, sh);
             uint32_t items = 0;
             bool go = true;
+#pragma unroll 1
             while (!E4M3 && run.next(a)) {
                 go = cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
                 if (!go)
                     break;
                 ++items;
                 if (lane == 0) {
-                    const int h = run.h, g = run.g, nb = g / a.head_blocks;
+                    const int nb = run.g / a.head_blocks;
                     mbar_arrive_expect_tx(smem_addr(&sh.q_full), a.rows * 128 * ((D + 63) / 64));
 #pragma unroll 1
                     for (int c = 0; c < (D + 63) / 64; ++c)
-                        tma_load_3d(smem_addr(L.q) + c * (N * 128), &map_q, 64 * c, h * a.G + (g - nb * a.head_blocks) * a.heads,
+                        tma_load_3d(smem_addr(L.q) + c * (N * 128), &map_q, 64 * c, run.h * a.G + (run.g - nb * a.head_blocks) * a.heads,
                                     run.b * a.Nmax + nb * a.nodes, smem_addr(&sh.q_full));
                 }
                 __syncwarp();
             }
             if (!go && items)   // a copy in flight lands before the CTA's memory is given back
                 drain_wait(&sh.q_full, (items - 1) & 1);
+            if (E4M3) {
+                Tiles k;
+                Ring rk;
+                Boxes box;
+                int nk = 0;
+                k.start(a, run);
+                box.ask(a, k, 0, kTile, lane);
+#pragma unroll 1
+                while (go && k.more) {
+                    const int now = box.row(a);
+                    k.step(a);
+                    box.ask(a, k, 0, kTile, lane);   // on its way while this tile is asked for
+#pragma unroll 1
+                    for (int c = 0; go && c < a.nd; ++c) {
+                        go = cta_wait(sh, &sh.kempty[rk.slot], rk.phase ^ 1);
+                        if (!go)
+                            break;
+                        load_boxes<E4M3>(a, smem_addr(L.k) + rk.slot * a.k_bytes, smem_addr(&sh.kfull[rk.slot]), &map_k, c, now, lane);
+                        rk.step(a.kslots);
+                        nk = min(nk + 1, a.kslots);
+                    }
+                }
+                for (; !go && nk > 0; --nk) {
+                    rk.back(a.kslots);
+                    drain_wait(&sh.kfull[rk.slot], rk.phase);
+                }
+            }
         } else if (warp == 8) {
             // --- first product -----------------------------------------------------------
             const uint32_t tmem = sh.tmem, k0 = smem_addr(L.k), q0 = smem_addr(L.q);
