@@ -629,13 +629,14 @@ __device__ __forceinline__ bool prepare_item(const AttnArgs& a, AttnShared& sh, 
 }
 
 constexpr int kAttnThreads = 512;
-// Registers a thread: the softmax's warpgroups hold a row's scores and sums a
-// thread, the others little.  The shares add up to the launch's.
+// Registers a thread: the softmax's warpgroups (warps 0 .. 7) hold NT scores and
+// NT sums a thread, the issuing warps (8 .. 11) little; a spill costs a loop
+// its L2 latency, the caches being shared memory.  The shares add up to the
+// launch's.
 constexpr int kAttnRegs = 128;       // at launch
-constexpr int kRegsSoftmax = 168;    // warps 0 .. 7
-constexpr int kRegsIssue = 72;       // warps 8 .. 11
-constexpr int kRegsTiles = 104;       // warps 12 .. 15
-static_assert(4 * kAttnRegs == 2 * kRegsSoftmax + kRegsIssue + kRegsTiles, "register shares");
+constexpr int kRegsIssue = 72;
+template <int NT> constexpr int kRegsSoftmax = NT >= 64 ? 168 : 152;
+template <int NT> constexpr int kRegsTiles = 4 * kAttnRegs - kRegsIssue - 2 * kRegsSoftmax<NT>;
 
 // NT: rows (TMEM columns) a softmax warpgroup handles; NWG: softmax
 // warpgroups with rows.
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // (The register moves stand inside the warpgroups' branches: ptxas budgets
     // what they dominate.)
     if (warp < 8) {
-        regs_grow<kRegsSoftmax>();
+        regs_grow<kRegsSoftmax<NT>>();
         if (warp < 4 * NWG) {
             // --- softmax: one position a thread, NT rows --------------------------
             const AttnLayout L = attn_layout<N, E4M3>(a, smem);
@@ -992,7 +993,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         }
     } else if (warp >= 12) {
-        regs_shrink<kRegsTiles>();
+        if constexpr (kRegsTiles<NT> > kAttnRegs)
+            regs_grow<kRegsTiles<NT>>();
+        else
+            regs_shrink<kRegsTiles<NT>>();
         // --- tiles: a quarter of the positions a warp ----------------------------------
         const AttnLayout L = attn_layout<N, E4M3>(a, smem);
         AttnShared& sh = *L.sh;
@@ -1041,8 +1045,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         bool go = true;
         Tiles it;
         it.start(a, run_of(a, sh));
-        Run ahead = it.run;      // the next item whose queries are to be made
-        bool more = it.more;
         uint32_t items = 0;
         Ring r, w;
         // an item's queries, as three 8-bit terms (before its keys' first product): a thread takes one 8-element
@@ -1053,13 +1055,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int live = min(a.nodes, x.s.nn - node0), heads = min(a.heads, a.G - head0);
             const uint4* const q = reinterpret_cast<const uint4*>(a.q + ((long long)x.b * a.Nmax + node0) * a.q_stride +
                                                                   (long long)(x.h * a.G + head0) * D) + ch;
-            // eight rows a thread at a time (all of them, up to 64 rows of 128 elements), zeros where there is no query
-            const int turn = 8 * stride;
-            uint4 y[8];
+            // four rows a thread at a time (all of them, up to 32 rows of 128 elements), zeros where there is no query
+            const int turn = 4 * stride;
+            uint4 y[4];
             auto load_q = [&](int row) {
                 int n = row / a.heads, head = row - n * a.heads;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     y[k] = n < live && head < heads && row0 < stride ? __ldg(q + n * (a.q_stride / 8) + head * per) : make_uint4(0, 0, 0, 0);
                     for (head += stride; head >= a.heads; head -= a.heads)
                         ++n;
@@ -1071,7 +1073,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int row = row0; row < a.rows; row += turn) {
                 load_q(row);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     const uint32_t z[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -1095,7 +1097,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (a.rows > turn)
                     load_q(row);
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     const int at = row + k * stride;
                     if (at >= a.rows || row0 >= stride)
                         break;
@@ -1110,7 +1112,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int c = 0; c < 3; ++c)
                         *reinterpret_cast<uint2*>(o + c * L.q_part) = make_uint2(p[c][0] | (p[c][1] << 16), p[c][2] | (p[c][3] << 16));
 #pragma unroll
-                    for (int c = 0; c < 7; ++c)   // (rolled, the code being long: the next one to the front)
+                    for (int c = 0; c < 3; ++c)   // (rolled, the code being long: the next one to the front)
                         y[c] = y[c + 1];
                 }
             }
@@ -1127,10 +1129,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // (e4m3: the warps share a barrier: after a timeout they all run on, doing nothing)
             if (!E4M3 && go && k.more && g >= -k_ahead)
                 go = load_k();
-            if (E4M3 && more && (items == 0 || (g >= 0 && it.j == it.run.t1 - 1))) {
+            if (E4M3 && (g == -1 || (g >= 0 && it.j == it.run.t1 - 1))) {
                 // the first item's queries; the next one's, before this one's last values
-                queries(ahead);
-                more = ahead.next(a);
+                Run x = it.run;
+                if (g == -1 || x.next(a))
+                    queries(x);
             }
             if (E4M3 && g >= 0) {
                 const int valid = it.valid(), rows = (valid + 15) & ~15;
