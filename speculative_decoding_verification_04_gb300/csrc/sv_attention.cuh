@@ -12,17 +12,22 @@
 // rows: the e4m3 cache's scales are one multiplier a thread, the exponentials
 // cost what the rows cost (no padding to 128), and the tree mask is one bit a
 // row.  The price is that a row's maximum runs across threads, so it is not
-// kept: weights are exp2(score - reference) with a reference a row that starts
-// at zero and moves only when a score is above it by more than kLazy, or the
-// first scores are all below it by more (a vote a tile).  fp32 sums and bf16
-// weights keep their relative precision at any such distance, so this is the
-// softmax's value to rounding.
+// kept: weights are exp2(score - reference) with a reference a row that moves
+// only when some score lies too far above it (a vote a tile).
+//  * bf16 caches: references start at zero and stay there while scores are
+//    within 2^+-24 of them; bf16 weights and fp32 sums keep their relative
+//    precision at any such distance, so this is the softmax's value to rounding.
+//  * e4m3 caches: weights are fp16 (below), so references are the maxima of the
+//    first tile and move when a score is 2^8 above; a largest weight near 2^6
+//    leaves fp16's floor (2^-25) at 2^-31 of it.
 //
 // An e4m3 cache's keys go to the tensor core as they are: each query element
 // is split into an e4m3 and two e5m2 terms, which hold a bf16's eight bits
 // exactly (to 2^-25 of the row group's largest element), and the three
-// products add up in the same accumulator.  Its values become bf16 in shared
-// memory, because the weights need more range than two or three 8-bit terms.
+// products add up in the same accumulator.  Its values become fp16 in shared
+// memory (one instruction a pair; 8-bit weights would need three terms and
+// more range); their scales join the scores' exponents, so that weight times
+// scale is what fp16 holds.
 //
 // Warps: 0-7 softmax (two warpgroups), 8 and 10 the issue of the first and the
 // second product, 9 bf16 queries, 11 what an item needs before its first tile
@@ -46,7 +51,9 @@ namespace sv {
 constexpr int kAttnMaxCtas = 160;
 constexpr int kTile = 128;                 // positions a tile
 constexpr int kHalfBytes = kTile * 128;    // 128 swizzled rows of 128 bytes
-constexpr float kLazy = 24.0f;             // log2 of how far a weight may lie from one
+// log2 of a weight at its row's reference, and of the largest before that moves
+template <bool E4M3> constexpr float kAtRef = E4M3 ? 6.0f : 0.0f;
+template <bool E4M3> constexpr float kLazy = E4M3 ? 14.0f : 24.0f;
 constexpr int kMaxSlots = 8;
 constexpr int kItemCost = 4;               // what an item's start and end cost, in tiles
 constexpr int kQuarter = kTile / 4;        // positions a loading warp takes care of
@@ -279,15 +286,20 @@ struct Ring {
     }
 };
 
-// Four e4m3 values as bf16, exactly (NaN as NaN): through fp16, which holds
-// them, and fp32.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t two)
+// Four e4m3 values as fp16, exactly (NaN as NaN).
+__device__ __forceinline__ uint2 e4m3_to_f16(uint32_t w)
 {
-    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
-    return bf16_pair(f.x, f.y);
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    return make_uint2(lo.x | ((uint32_t)lo.y << 16), hi.x | ((uint32_t)hi.y << 16));
 }
 
-__device__ __forceinline__ uint2 e4m3_to_bf16(uint32_t w) { return make_uint2(e4m3x2_to_bf16(w & 0xffffu), e4m3x2_to_bf16(w >> 16)); }
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 
 __device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w)
 {
@@ -348,30 +360,31 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t k, uint32_t q, u
 #pragma unroll
         for (int s = 0; s < 8; ++s)
             if (s < steps)
-                tc_mma_bf16(d, tc_desc(ka + (s >> 2) * (kHalfBytes / 16) + (s & 3) * 2),
+                tc_mma_16(d, tc_desc(ka + (s >> 2) * (kHalfBytes / 16) + (s & 3) * 2),
                             tc_desc(qb + (s >> 2) * (N * 128 / 16) + (s & 3) * 2), id, add || s > 0);
     }
 }
 
-// One lane: a V slot (bf16 operands) times P.  `steps`: 16-position steps.
-template <int N>
+// One lane: a V slot (bf16, or fp16 from e4m3) times P.  `steps`: 16-position
+// steps.
+template <int N, bool E4M3>
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t v, uint32_t p, uint32_t lbo, int steps, bool add)
 {
-    constexpr uint32_t id = tc_idesc(128, N, 1, 1, true, true);
+    constexpr uint32_t id = tc_idesc(128, N, E4M3 ? 0 : 1, E4M3 ? 0 : 1, true, true);
     const uint32_t va = tc_desc_lo(v, lbo), pb = tc_desc_lo(p, kHalfBytes);
 #pragma unroll
     for (int s = 0; s < 8; ++s)
         if (s < steps)
-            tc_mma_bf16(d, tc_desc(va + s * (2048 / 16)), tc_desc(pb + s * (2048 / 16)), id, add || s > 0);
+            tc_mma_16(d, tc_desc(va + s * (2048 / 16)), tc_desc(pb + s * (2048 / 16)), id, add || s > 0);
 }
 
 // The rare step of the softmax, by the warpgroup's 128 threads: rows whose
 // scores lie too far from their references get new ones (their maxima over
 // this tile), and the sums in TMEM are rescaled.  scratch[0 .. NT) then holds
 // the factors of what was summed so far, [NT .. 2 NT) how far references rose.
-template <int NT>
+template <int NT, bool E4M3>
 __device__ __forceinline__ void move_references(float* scratch, float* negm, int* unset_flag, uint32_t s_at, uint32_t o_at,
-                                                int o_chunks, int o_pitch, float mult, unsigned long long seen, int t, int bar)
+                                                int o_chunks, int o_pitch, float mult, float add, unsigned long long seen, int t, int bar)
 {
     const int lane = t & 31, warp = t >> 5;
 #pragma unroll 1
@@ -381,7 +394,7 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
         tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            const float x = warp_redux_max((seen >> (c + k)) & 1 ? fmaf(s[k], mult, negm[c + k]) : -INFINITY);
+            const float x = warp_redux_max((seen >> (c + k)) & 1 ? fmaf(s[k], mult, negm[c + k] + add) : -INFINITY);
             keep = lane == k ? x : keep;
         }
         if (lane < 16)
@@ -396,10 +409,10 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
         const float old = negm[t];
         if (__float_as_uint(old) == 0u) {
             unset = x == -INFINITY;
-            delta = unset ? 0.0f : x;
-        } else if (x > 0.0f) {
-            delta = x;
-            f = ex2_approx(-x);
+            delta = unset ? 0.0f : x - kAtRef<E4M3>;
+        } else if (x > kAtRef<E4M3>) {
+            delta = x - kAtRef<E4M3>;
+            f = ex2_approx(-delta);
         }
         if (!unset) {
             const float now = old - delta;
@@ -426,32 +439,29 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
     tmem_wait_st();
 }
 
-// Weights exp2(s) of a position: rounded to bf16 once, with the position's value
-// scale on them, into P; their sums.  A weight's rounding (a bf16 unit of
-// 2^-8) averages out over the positions.  ROUNDED sums take what P holds, so
-// that the rounding of a weight that dominates its row cancels; that costs
-// three instructions a pair, which the launches of few rows have to spare.
+// Weights exp2(s) of a position, rounded once into P, and their sums.
+//  * bf16: a weight's rounding (a bf16 unit of 2^-8) averages out over the
+//    positions.  ROUNDED sums take what P holds, so that the rounding of a
+//    weight that dominates its row cancels; that costs three instructions a
+//    pair, which the launches of few rows have to spare.
+//  * e4m3: s holds the value's scale too; the sums take it back (unscale).
 template <int NT, bool E4M3, bool ROUNDED>
-__device__ __forceinline__ void weigh(const float (&s)[NT], float vscale, uint64_t (&l2)[NT / 2], unsigned char* p_row, int at, int t)
+__device__ __forceinline__ void weigh(const float (&s)[NT], float unscale, uint64_t (&l2)[NT / 2], unsigned char* p_row, int at, int t)
 {
-    const float unscale = E4M3 && ROUNDED ? __frcp_rn(vscale) : 1.0f;
-    const uint64_t v2 = f2_pack(vscale, vscale), u2 = f2_pack(unscale, unscale);
+    const uint64_t u2 = f2_pack(unscale, unscale);
 #pragma unroll
     for (int i = 0; i < NT / 8; ++i) {
         uint32_t x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            uint64_t e = f2_pack(ex2_approx(s[8 * i + 2 * k]), ex2_approx(s[8 * i + 2 * k + 1]));
-            if (!ROUNDED)
-                l2[4 * i + k] = f2_add(l2[4 * i + k], e);
-            if (E4M3)
-                e = f2_mul(e, v2);
-            float lo, hi;
-            f2_unpack(e, lo, hi);
-            x[k] = bf16_pair(lo, hi);
-            if (ROUNDED) {
-                const uint64_t r = f2_pack(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u));
-                l2[4 * i + k] = E4M3 ? f2_fma(r, u2, l2[4 * i + k]) : f2_add(r, l2[4 * i + k]);
+            const float lo = ex2_approx(s[8 * i + 2 * k]), hi = ex2_approx(s[8 * i + 2 * k + 1]);
+            uint64_t& l = l2[4 * i + k];
+            if (E4M3) {
+                l = f2_fma(f2_pack(lo, hi), u2, l);
+                x[k] = f16_pair(lo, hi);
+            } else {
+                x[k] = bf16_pair(lo, hi);
+                l = f2_add(l, ROUNDED ? f2_pack(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u)) : f2_pack(lo, hi));
             }
         }
         // P: rows of 64 of the CTA's N columns a position, swizzled
@@ -823,24 +833,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                         for (int i = 0; i < NT / 16; ++i)
                             tmem_ld16(s_at + 16 * i, s + 16 * i);
-                        float mult = a.scale_log2, vscale = 1.0f;
+                        float mult = a.scale_log2, add = 0.0f;   // add: log2 of the value's scale
                         if (E4M3) {
                             if (first_tile)
                                 scale_log2 = a.scale_log2 * sh.q_unscale[items & 3];
                             // a scale that is not finite marks a row that held something that was not
                             mult = scale_log2 * (isfinite(ks) ? ks : NAN);
-                            vscale = isfinite(vs) ? vs : NAN;
-                            vscale = fabsf(vscale) < 0x1p-100f ? 0x1p-100f : vscale;   // (all of such a row's values are zero in the sum)
+                            // (below 2^-100 all of a row's values are zero in the sum; a negative scale is none)
+                            add = isfinite(vs) ? __log2f(vs >= 0.0f && vs < 0x1p-100f ? 0x1p-100f : vs) : NAN;
                             scales_of(j + 1, page_next, ks_next, vs_next);
                             page_next = page_of(j + 2);
                         }
                         // scores in powers of two, relative to the rows' references
-                        const uint64_t m2 = f2_pack(mult, mult);
+                        const uint64_t m2 = f2_pack(mult, mult), a2 = f2_pack(add, add);
                         const ulonglong2* nm = reinterpret_cast<const ulonglong2*>(negm);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < NT / 4; ++i) {
-                            const ulonglong2 x = nm[i];
+                            ulonglong2 x = nm[i];
+                            if (E4M3)
+                                x = make_ulonglong2(f2_add(x.x, a2), f2_add(x.y, a2));
                             f2_unpack(f2_fma(f2_pack(s[4 * i], s[4 * i + 1]), m2, x.x), s[4 * i], s[4 * i + 1]);
                             f2_unpack(f2_fma(f2_pack(s[4 * i + 2], s[4 * i + 3]), m2, x.y), s[4 * i + 2], s[4 * i + 3]);
                         }
@@ -855,7 +867,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                     for (int i = 0; i < NT; ++i)
                                         seen |= (unsigned long long)((info.anc[w * NT + i] >> m) & 1u) << i;
                                 } else {   // nothing does: its scales may be anything
-                                    vscale = 1.0f;
+                                    add = 0.0f;
                                 }
                             }
 #pragma unroll
@@ -870,8 +882,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                         for (int i = 16; i < NT; i += 2)
                             top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], s[i], s[i + 1]);
-                        bool move = bar_any(bar, 128, max3(top[0], top[1], fmaxf(top[2], top[3])) > kLazy) || sh.unset[w];
-                        if (first_tile) {
+                        bool move = bar_any(bar, 128, max3(top[0], top[1], fmaxf(top[2], top[3])) > kLazy<E4M3>) || sh.unset[w];
+                        if (first_tile && E4M3) {
+                            move = true;
+                        } else if (first_tile) {
                             // no reference yet: zero will do if some position's scores are all near enough
                             float low[4];
 #pragma unroll
@@ -880,7 +894,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                             for (int i = 16; i < NT; i += 2)
                                 low[(i >> 1) & 3] = min3(low[(i >> 1) & 3], s[i], s[i + 1]);
-                            move = !bar_any(bar, 128, min3(low[0], low[1], fminf(low[2], low[3])) >= -kLazy) || move;
+                            move = !bar_any(bar, 128, min3(low[0], low[1], fminf(low[2], low[3])) >= -kLazy<E4M3>) || move;
                             if (!move && t < NT)
                                 negm[t] = -0.0f;   // (+0 marks a row without a reference)
                         } else {   // the previous tile's product is done with P (and O)
@@ -888,7 +902,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             tc_fence_after();
                         }
                         if (move) {
-                            move_references<NT>(scratch, negm, &sh.unset[w], s_at, tmem_o, first_tile ? 0 : a.nd, N, mult, seen, t, bar);
+                            move_references<NT, E4M3>(scratch, negm, &sh.unset[w], s_at, tmem_o, first_tile ? 0 : a.nd, N, mult, add, seen, t, bar);
 #pragma unroll
                             for (int i = 0; i < NT / 4; ++i) {
                                 const ulonglong2 f = reinterpret_cast<const ulonglong2*>(scratch)[i];
@@ -902,7 +916,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             }
                             bar_sync(bar, 128);   // the scratch may be written again
                         }
-                        weigh<NT, E4M3, NWG == 1>(s, vscale, l2, L.p + t * 128, w * (NT / 8), t);
+                        weigh<NT, E4M3, NWG == 1>(s, E4M3 ? ex2_approx(-add) : 1.0f, l2, L.p + t * 128, w * (NT / 8), t);
                         tc_fence_before();
                         fence_proxy_async();
                         __syncwarp();
@@ -1161,7 +1175,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             unsigned char* o = dst + (i >> 2) * kHalfBytes;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const uint2 y0 = e4m3_to_bf16(x[k].x), y1 = e4m3_to_bf16(x[k].y), y2 = e4m3_to_bf16(x[k].z), y3 = e4m3_to_bf16(x[k].w);
+                                const uint2 y0 = e4m3_to_f16(x[k].x), y1 = e4m3_to_f16(x[k].y), y2 = e4m3_to_f16(x[k].z), y3 = e4m3_to_f16(x[k].w);
                                 *reinterpret_cast<uint4*>(o + (((2 * k) ^ key) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
                                 *reinterpret_cast<uint4*>(o + (((2 * k + 1) ^ key) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
                             }
@@ -1335,7 +1349,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     tc_fence_after();
                     if (lane == 0) {
-                        mma_values<N>(tmem_o + c * N, v0 + rv.slot * v_bytes, p0, width > 64 ? kHalfBytes : 0, ksteps, v.j > v.run.t0);
+                        mma_values<N, E4M3>(tmem_o + c * N, v0 + rv.slot * v_bytes, p0, width > 64 ? kHalfBytes : 0, ksteps, v.j > v.run.t0);
                         if (c == a.nd - 1)
                             tc_commit(smem_addr(&sh.o_full));
                         tc_commit(smem_addr(&empty[rv.slot]));

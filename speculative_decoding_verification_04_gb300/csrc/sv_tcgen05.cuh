@@ -34,9 +34,9 @@ __device__ __forceinline__ void tc_commit(uint32_t mbar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar) : "memory");
 }
 
-// D[tmem] (+)= A B on shared-memory operands, fp32 accumulation: bf16, 16
-// elements of the contraction a call; 8-bit floats, 32.
-__device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+// D[tmem] (+)= A B on shared-memory operands, fp32 accumulation: 16-bit
+// floats, 16 elements of the contraction a call; 8-bit floats, 32.
+__device__ __forceinline__ void tc_mma_16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -55,7 +55,8 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, ui
 }
 
 // Instruction descriptors: fp32 result, M x N, and which operands lie with M
-// (N) contiguous instead of the contraction.  8-bit formats: 0 e4m3, 1 e5m2.
+// (N) contiguous instead of the contraction.  16-bit formats: 0 fp16,
+// 1 bf16; 8-bit: 0 e4m3, 1 e5m2.
 __host__ __device__ constexpr uint32_t tc_idesc(int M, int N, int a_format, int b_format, bool a_mn, bool b_mn)
 {
     return (1u << 4) | ((uint32_t)a_format << 7) | ((uint32_t)b_format << 10) | ((uint32_t)a_mn << 15) |
