@@ -289,9 +289,13 @@ struct Ring {
 // Four e4m3 values as fp16, exactly (NaN as NaN).
 __device__ __forceinline__ uint2 e4m3_to_f16(uint32_t w)
 {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    return make_uint2(lo.x | ((uint32_t)lo.y << 16), hi.x | ((uint32_t)hi.y << 16));
+    uint2 y;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(y.x), "=r"(y.y) : "r"(w));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t f16_pair(float lo, float hi)
