@@ -21,6 +21,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -46,7 +47,16 @@ class SVKvTokens(ctypes.Structure):
                 ("rotary_dim", _I32), ("interleaved", _I32), ("eps", ctypes.c_float)]
 
 
+# The calls pass the two structs as packed bytes: one call packs what would be a
+# dozen attribute assignments, which at the smallest shapes cost more than the
+# kernels run.
+_PACK_CACHE = struct.Struct("5P7i4x").pack
+_PACK_TOKENS = struct.Struct("3P3q7P8if4x").pack
+assert struct.calcsize("5P7i4x") == ctypes.sizeof(SVKvCache)
+assert struct.calcsize("3P3q7P8if4x") == ctypes.sizeof(SVKvTokens)
+
 _lib = None
+_workspace_sizes: dict = {}
 
 
 def _library():
@@ -66,80 +76,96 @@ def _library():
     return _lib
 
 
-def _ptr(t, name, dtype, shape=None):
-    """The address of an optional contiguous CUDA tensor, checked."""
-    if t is None:
-        return None
+def _refuse(t, name, dtype, shape):
+    """The exception for a tensor that _ptr does not take."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _ptr(t, name, dtype, shape):
+    """The address of an optional contiguous CUDA tensor, checked."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+        _refuse(t, name, dtype, shape)
     return t.data_ptr()
 
 
 def _errors_ptr(errors):
-    if errors is not None and errors.numel() < 1:
+    if errors is None:
+        return 0
+    if errors.numel() < 1:
         raise ValueError("errors must have an element")
-    return _ptr(errors, "errors", torch.int32)
+    return _ptr(errors, "errors", torch.int32, errors.shape)
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, page_table, layered=False):
-    c = SVKvCache()
-    if k_cache.dim() != 4 and not (layered and k_cache.dim() == 5):
+    """The packed sv_kv_cache, and the cache's shape."""
+    shape, dtype = k_cache.shape, k_cache.dtype
+    n = len(shape)
+    if n != 4 and not (layered and n == 5):
         raise ValueError("k_cache must be [num_pages, n_kv_heads, page_size, head_dim]"
                          + (" or [layers, ...]" if layered else ""))
-    shape, dtype = tuple(k_cache.shape), k_cache.dtype
-    if dtype == torch.bfloat16:
-        c.format = SV_KV_BF16
+    ks = vs = 0
+    if dtype is torch.bfloat16:
+        code = SV_KV_BF16
         if k_scale is not None or v_scale is not None:
             raise ValueError("bfloat16 caches have no scales")
-    elif dtype == torch.float8_e4m3fn:
-        c.format = SV_KV_E4M3
+    elif dtype is torch.float8_e4m3fn:
+        code = SV_KV_E4M3
         if k_scale is None or v_scale is None:
             raise ValueError("float8_e4m3fn caches need k_scale and v_scale")
-        c.k_scale = _ptr(k_scale, "k_scale", torch.float32, shape[:-1])
-        c.v_scale = _ptr(v_scale, "v_scale", torch.float32, shape[:-1])
+        rows = shape[:-1]
+        ks = _ptr(k_scale, "k_scale", torch.float32, rows)
+        vs = _ptr(v_scale, "v_scale", torch.float32, rows)
     else:
         raise TypeError(f"the cache must be bfloat16 or float8_e4m3fn, got {dtype}")
-    c.k = _ptr(k_cache, "k_cache", dtype)
-    c.v = _ptr(v_cache, "v_cache", dtype, shape)
-    if page_table.dim() != 2:
+    table = page_table.shape
+    if len(table) != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    c.page_table = _ptr(page_table, "page_table", torch.int32)
-    c.layers = shape[0] if len(shape) == 5 else 1
-    c.num_pages, c.n_kv_heads, c.page_size, c.head_dim = shape[-4:]
-    c.max_pages = page_table.shape[1]
-    return c
+    return _PACK_CACHE(_ptr(k_cache, "k_cache", dtype, shape), _ptr(v_cache, "v_cache", dtype, shape), ks, vs,
+                       _ptr(page_table, "page_table", torch.int32, table), table[1], code,
+                       shape[0] if n == 5 else 1, *shape[-4:-2], *shape[-2:]), shape, table[0]
 
 
 def _heads(t, name, dtype, lead):
     """Address, token stride and head count of [*lead, heads, head_dim] rows
     whose heads are adjacent (tokens may be strided, evenly)."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    st = t.stride()
-    if (not t.is_cuda or t.dim() != len(lead) + 2 or tuple(t.shape[:-2]) != lead or st[-1] != 1
-            or (t.shape[-2] > 1 and st[-2] != t.shape[-1])):
+    shape, st = t.shape, t.stride()
+    n = len(lead)
+    if (not t.is_cuda or len(shape) != n + 2 or shape[:n] != lead or st[-1] != 1
+            or (shape[-2] > 1 and st[-2] != shape[-1])):
         raise ValueError(f"{name} must be a CUDA tensor {list(lead)} + [heads, head_dim] with contiguous heads")
-    if len(lead) == 2:
+    if n == 2:
         if lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]:
             raise ValueError(f"{name}'s tokens must be evenly strided")
-        return t.data_ptr(), st[1] if lead[1] > 1 else st[0], t.shape[-2]
-    return t.data_ptr(), st[0], t.shape[-2]
+        return t.data_ptr(), st[1] if lead[1] > 1 else st[0], shape[-2]
+    return t.data_ptr(), st[0], shape[-2]
 
 
 def _code(dtype):
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return SV_DTYPE_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return SV_DTYPE_F32
     raise TypeError(f"rows must be float32 or bfloat16, got {dtype}")
 
 
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+# the current stream's handle, without a Stream object around it
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, like):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(like.get_device())
+    return torch.cuda.current_stream(like.device).cuda_stream
 
 
 def _empty(like, shape, dtype, stream):
@@ -163,49 +189,52 @@ def spec_kv_append(k, v, k_cache, v_cache, page_table, kv_len, n_new=None, q=Non
     heads.  Tokens may be strided: slices of one fused projection work as they
     are.  ``cos_sin`` [max_positions, rotary_dim] float32 holds each position's
     cosines, then its sines."""
-    c = _cache(k_cache, v_cache, k_scale, v_scale, page_table)
-    t = SVKvTokens()
-    dtype, B = k.dtype, page_table.shape[0]
+    c, cache, B = _cache(k_cache, v_cache, k_scale, v_scale, page_table)
+    dtype, D = k.dtype, cache[-1]
+    code = _code(dtype)
+    S = nn = par = starts = 0
     if row_start is None:
         if k.dim() != 4 or k.shape[0] != B:
             raise ValueError("k must be [B, S, n_kv_heads, head_dim]")
-        lead = (B, k.shape[1])
-        t.S, t.rows = lead[1], B * lead[1]
-        t.n_new = _ptr(n_new, "n_new", torch.int32, (B,))
-        t.parent = _ptr(parent, "parent", torch.int32, lead)
+        S = k.shape[1]
+        lead, rows = (B, S), B * S
+        nn = _ptr(n_new, "n_new", torch.int32, (B,))
+        par = _ptr(parent, "parent", torch.int32, lead)
     else:
         if k.dim() != 3 or n_new is not None or parent is not None:
             raise ValueError("packed k must be [rows, n_kv_heads, head_dim], without n_new and parent")
-        lead = (k.shape[0],)
-        t.rows = lead[0]
-        t.row_start = _ptr(row_start, "row_start", torch.int32, (B + 1,))
-    t.B, t.dtype, t.eps = B, _code(dtype), eps
-    t.k, t.k_stride, hk = _heads(k, "k", dtype, lead)
-    t.v, t.v_stride, hv = _heads(v, "v", dtype, lead)
-    D = c.head_dim
-    if hk != c.n_kv_heads or hv != hk or k.shape[-1] != D or v.shape[-1] != D:
+        rows = k.shape[0]
+        lead = (rows,)
+        starts = _ptr(row_start, "row_start", torch.int32, (B + 1,))
+    kp, k_stride, hk = _heads(k, "k", dtype, lead)
+    vp, v_stride, hv = _heads(v, "v", dtype, lead)
+    if hk != cache[-3] or hv != hk or k.shape[-1] != D or v.shape[-1] != D:
         raise ValueError("k and v must have the cache's heads and head_dim")
+    qp = q_stride = hq = op = qn = kn = cs = positions = rot = 0
     if q is not None:
-        t.q, t.q_stride, t.n_heads = _heads(q, "q", dtype, lead)
+        qp, q_stride, hq = _heads(q, "q", dtype, lead)
         if q.shape[-1] != D:
             raise ValueError("q must have the cache's head_dim")
         if q_out is None:
             q_out = _empty(q, q.shape, dtype, stream)
-        t.q_out = _ptr(q_out, "q_out", dtype, tuple(q.shape))
-        t.q_norm = _ptr(q_norm, "q_norm", dtype, (D,))
+            op = q_out.data_ptr()
+        else:
+            op = _ptr(q_out, "q_out", dtype, q.shape)
+        qn = _ptr(q_norm, "q_norm", dtype, (D,))
     elif q_out is not None or q_norm is not None:
         raise ValueError("q_out and q_norm go with q")
-    t.k_norm = _ptr(k_norm, "k_norm", dtype, (D,))
+    kn = _ptr(k_norm, "k_norm", dtype, (D,))
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_positions, rotary_dim]")
-        t.cos_sin = _ptr(cos_sin, "cos_sin", torch.float32)
-        t.max_positions, t.rotary_dim = cos_sin.shape
-        t.interleaved = 1 if interleaved else 0
-    st = _library().spec_kv_append(ctypes.addressof(c), ctypes.addressof(t),
-                                   _ptr(kv_len, "kv_len", torch.int32, (B,)), _errors_ptr(errors),
-                                   _raw_stream(stream))
-    _check(st, "spec_kv_append")
+        positions, rot = cos_sin.shape
+        cs = _ptr(cos_sin, "cos_sin", torch.float32, (positions, rot))
+    t = _PACK_TOKENS(qp, kp, vp, q_stride, k_stride, v_stride, qn, kn, cs, par, nn, starts, op, code, hq, B, S,
+                     rows, positions, rot, 1 if interleaved else 0, eps)
+    st = (_lib or _library()).spec_kv_append(c, t, _ptr(kv_len, "kv_len", torch.int32, (B,)), _errors_ptr(errors),
+                                             _raw_stream(stream, k))
+    if st:
+        _check(st, "spec_kv_append")
     return q_out
 
 
@@ -221,29 +250,39 @@ def spec_tree_attention(q, k_cache, v_cache, page_table, kv_len, n_nodes=None, p
     chain; Nmax = 1 an ordinary decode step.  ``scale`` defaults to
     head_dim ** -0.5.  ``workspace``: a uint8 CUDA tensor of at least
     sv_attention_workspace_size bytes (allocated when omitted)."""
-    c = _cache(k_cache, v_cache, k_scale, v_scale, page_table)
-    if q.dim() != 4:
+    c, cache, B = _cache(k_cache, v_cache, k_scale, v_scale, page_table)
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [B, Nmax, n_heads, head_dim]")
-    B, Nmax, Hq, D = q.shape
-    if B != page_table.shape[0] or D != c.head_dim:
+    _, Nmax, Hq, D = shape
+    if B != shape[0] or D != cache[-1]:
         raise ValueError("q must have the page table's B and the cache's head_dim")
     dtype = q.dtype
     code = _code(dtype)
     qp, q_stride, _ = _heads(q, "q", dtype, (B, Nmax))
-    lib = _library()
+    lib = _lib or _library()
     if out is None:
-        out = _empty(q, q.shape, dtype, stream)
-    need = lib.sv_attention_workspace_size(Nmax, Hq, c.n_kv_heads, D)
+        out = _empty(q, shape, dtype, stream)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", dtype, shape)
     if workspace is None:
-        workspace = _empty(q, max(need, 256), torch.uint8, stream)
-    st = lib.spec_tree_attention(ctypes.addressof(c), _ptr(kv_len, "kv_len", torch.int32, (B,)),
+        key = (Nmax, Hq, cache[-3], D)
+        need = _workspace_sizes.get(key)
+        if need is None:
+            need = _workspace_sizes[key] = max(256, lib.sv_attention_workspace_size(*key))
+        workspace = _empty(q, need, torch.uint8, stream)
+        wp = workspace.data_ptr()
+    else:
+        need = workspace.numel()
+        wp = _ptr(workspace, "workspace", torch.uint8, workspace.shape)
+    st = lib.spec_tree_attention(c, _ptr(kv_len, "kv_len", torch.int32, (B,)),
                                  _ptr(n_nodes, "n_nodes", torch.int32, (B,)),
                                  _ptr(parent, "parent", torch.int32, (B, Nmax)), qp, q_stride, code, Hq, B,
-                                 Nmax, D ** -0.5 if scale is None else scale,
-                                 _ptr(out, "out", dtype, (B, Nmax, Hq, D)), _errors_ptr(errors),
-                                 _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
-                                 _raw_stream(stream))
-    _check(st, "spec_tree_attention")
+                                 Nmax, D ** -0.5 if scale is None else scale, op, _errors_ptr(errors), wp, need,
+                                 _raw_stream(stream, q))
+    if st:
+        _check(st, "spec_tree_attention")
     return out
 
 
@@ -253,19 +292,20 @@ def spec_kv_commit(k_cache, v_cache, page_table, kv_len, out_path, out_len, k_sc
     [B] of spec_verify_tree) behind its root, in every layer of the caches
     ([layers, num_pages, ...], or one layer's [num_pages, ...]), and return the
     lengths kv_len + 1 + out_len: in ``kv_len`` itself, or in ``kv_len_out``."""
-    c = _cache(k_cache, v_cache, k_scale, v_scale, page_table, layered=True)
-    if out_path.dim() != 2:
+    c, _, B = _cache(k_cache, v_cache, k_scale, v_scale, page_table, layered=True)
+    path = out_path.shape
+    if len(path) != 2:
         raise ValueError("out_path must be [B, Nmax]")
-    B = page_table.shape[0]
-    Nmax = out_path.shape[1]
+    Nmax, one = path[1], (B,)
     if kv_len_out is None:
         kv_len_out = kv_len
-    st = _library().spec_kv_commit(ctypes.addressof(c), _ptr(kv_len, "kv_len", torch.int32, (B,)),
-                                   _ptr(out_path, "out_path", torch.int32, (B, Nmax)),
-                                   _ptr(out_len, "out_len", torch.int32, (B,)), B, Nmax,
-                                   _ptr(kv_len_out, "kv_len_out", torch.int32, (B,)), _errors_ptr(errors),
-                                   _raw_stream(stream))
-    _check(st, "spec_kv_commit")
+    st = (_lib or _library()).spec_kv_commit(c, _ptr(kv_len, "kv_len", torch.int32, one),
+                                             _ptr(out_path, "out_path", torch.int32, (B, Nmax)),
+                                             _ptr(out_len, "out_len", torch.int32, one), B, Nmax,
+                                             _ptr(kv_len_out, "kv_len_out", torch.int32, one),
+                                             _errors_ptr(errors), _raw_stream(stream, k_cache))
+    if st:
+        _check(st, "spec_kv_commit")
     return kv_len_out
 
 
@@ -274,17 +314,18 @@ def spec_kv_read(k_cache, v_cache, page_table, start, row_start, rows, dtype=tor
     """The entries of sequence b at positions start[b], start[b] + 1, ... as the
     dense rows row_start[b] .. row_start[b + 1] - 1 of (k_out, v_out)
     [rows, n_kv_heads, head_dim]; rows of no sequence are zeros."""
-    c = _cache(k_cache, v_cache, k_scale, v_scale, page_table)
-    B = page_table.shape[0]
-    shape = (int(rows), c.n_kv_heads, c.head_dim)
+    c, cache, B = _cache(k_cache, v_cache, k_scale, v_scale, page_table)
+    rows = int(rows)
+    shape = (rows, cache[-3], cache[-1])
     code = _code(dtype)
     if k_out is None:
         k_out = _empty(k_cache, shape, dtype, stream)
     if v_out is None:
         v_out = _empty(k_cache, shape, dtype, stream)
-    st = _library().spec_kv_read(ctypes.addressof(c), _ptr(start, "start", torch.int32, (B,)),
-                                 _ptr(row_start, "row_start", torch.int32, (B + 1,)), B, int(rows), code,
-                                 _ptr(k_out, "k_out", dtype, shape), _ptr(v_out, "v_out", dtype, shape),
-                                 _errors_ptr(errors), _raw_stream(stream))
-    _check(st, "spec_kv_read")
+    st = (_lib or _library()).spec_kv_read(c, _ptr(start, "start", torch.int32, (B,)),
+                                           _ptr(row_start, "row_start", torch.int32, (B + 1,)), B, rows, code,
+                                           _ptr(k_out, "k_out", dtype, shape), _ptr(v_out, "v_out", dtype, shape),
+                                           _errors_ptr(errors), _raw_stream(stream, k_cache))
+    if st:
+        _check(st, "spec_kv_read")
     return k_out, v_out
