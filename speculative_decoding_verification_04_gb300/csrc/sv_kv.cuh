@@ -132,8 +132,9 @@ __device__ __forceinline__ TokenPlace token_place(const AppendArgs& a, int t, in
     const int base = __ldg(a.kv_len + b);
     int depth = i;
     if (a.has_parent) {
-        int p;
-        const bool ok = tree_parents(a.parent + (long long)b * a.S, true, n, lane, p);
+        // (the whole row, so that it does not wait for the count)
+        const int p = lane > 0 && lane < a.S ? __ldg(a.parent + (long long)b * a.S + lane) : lane - 1;
+        const bool ok = !__any_sync(kFull, lane > 0 && lane < n && (p < 0 || p >= lane));
         depth = 0;
         for (int at = i; ok && i < n && at > 0 && depth < kNodeMax; ++depth)
             at = __shfl_sync(kFull, p, at);
@@ -230,7 +231,10 @@ __device__ __forceinline__ uint32_t e4m3_quad(const float* x)
 }
 
 // LPR lanes hold a head's row: 16 elements each, the lanes from D / 16 on none
-// (D = 80, 96, 112 of LPR 8; 144 ... 240 of LPR 16).
+// (D = 80, 96, 112 of LPR 8; 144 ... 240 of LPR 16).  A warp holds 32 / LPR
+// rows at a time; the next ones are on their way while it works, and the first
+// are asked for before the token's place is looked up (which takes three loads
+// that depend on one another).
 template <typename T, int LPR, bool E4M3>
 __global__ void __launch_bounds__(256) sv_append_kernel(const __grid_constant__ AppendArgs a)
 {
@@ -239,7 +243,7 @@ __global__ void __launch_bounds__(256) sv_append_kernel(const __grid_constant__ 
     const int t = gw / a.wpt;
     if (t >= a.rows)
         return;
-    constexpr int RPW = 32 / LPR;   // rows a warp holds at a time
+    constexpr int RPW = 32 / LPR;
     const int sub = gw - t * a.wpt;
     const int c = lane % LPR, D = a.c.D;
     const int Hk = a.c.Hkv, Hq = a.has_q ? a.Hq : 0, H = Hq + 2 * Hk;
@@ -249,6 +253,18 @@ __global__ void __launch_bounds__(256) sv_append_kernel(const __grid_constant__ 
     const int c0 = turn && !a.interleaved ? c : 2 * c;
     const int c1 = turn && !a.interleaved ? c + a.rot / 16 : 2 * c + 1;
 
+    // the rows that the lane's part of pass r0 lies in: queries, keys, values
+    auto load = [&](int r0, Row16<T>& w) {
+        const int r = r0 + lane / LPR;
+        if (r >= H || !live)
+            return;
+        const T* src = r < Hq        ? static_cast<const T*>(a.q) + t * a.q_stride + (long long)r * D
+                       : r < Hq + Hk ? static_cast<const T*>(a.k) + t * a.k_stride + (long long)(r - Hq) * D
+                                     : static_cast<const T*>(a.v) + t * a.v_stride + (long long)(r - Hq - Hk) * D;
+        w.load(src, c0, c1);
+    };
+    Row16<T> now{}, next{};
+    load(sub * RPW, now);
     const TokenPlace pl = token_place(a, t, lane);
     if (pl.state == 2 && a.has_err && sub == 0 && lane == 0)
         atomicOr(a.err, kErrCache);
@@ -265,21 +281,17 @@ __global__ void __launch_bounds__(256) sv_append_kernel(const __grid_constant__ 
         }
     }
     for (int r0 = sub * RPW; r0 < H; r0 += a.wpt * RPW) {   // uniform in the warp: the shuffles below need every lane
+        load(r0 + a.wpt * RPW, next);
         const int r = r0 + lane / LPR;
         const int kind = r < Hq ? 0 : r < Hq + Hk ? 1 : 2;
         const int h = kind == 0 ? r : kind == 1 ? r - Hq : r - Hq - Hk;
-        const bool act = r < H && live;
+        const bool act = r < H && live, here = act && pl.state == 0;
         float x[16];
+        now.get(x);
+        if (!here) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            x[j] = 0.0f;
-        if (act && pl.state == 0) {
-            const T* src = kind == 0   ? static_cast<const T*>(a.q) + t * a.q_stride
-                           : kind == 1 ? static_cast<const T*>(a.k) + t * a.k_stride
-                                       : static_cast<const T*>(a.v) + t * a.v_stride;
-            Row16<T> w;
-            w.load(src + (long long)h * D, c0, c1);
-            w.get(x);
+            for (int j = 0; j < 16; ++j)
+                x[j] = 0.0f;
         }
         const bool norm = kind == 0 ? a.has_qn : kind == 1 ? a.has_kn : false;
         if (a.has_qn | a.has_kn) {
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(256) sv_append_kernel(const __grid_constant__ 
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1)
                 ss += __shfl_xor_sync(kFull, ss, o);
-            if (norm && act && pl.state == 0) {
+            if (norm && here) {
                 Row16<T> w;
                 w.load(static_cast<const T*>(kind == 0 ? a.q_norm : a.k_norm), c0, c1);
                 float g[16];
@@ -328,38 +340,41 @@ __global__ void __launch_bounds__(256) sv_append_kernel(const __grid_constant__ 
             store_chunk(dst + 8 * c0, x);
             store_chunk(dst + 8 * c1, x + 8);
         }
-        float amax = 0.0f;
-        if (E4M3) {
+        if (E4M3 && __any_sync(kFull, kind > 0 && act)) {
+            // one scale a row: its largest magnitude becomes 448; the floor keeps it finite for rows of (nearly) zeros
+            float amax = 0.0f;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 amax = max_nan(amax, fabsf(x[j]));
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1)
                 amax = max_nan(amax, __shfl_xor_sync(kFull, amax, o));
-        }
-        if (kind > 0 && act && pl.state == 0) {
-            const long long row = kv_row(a.c, pl.page, pl.pos) + ((long long)h << a.c.page_shift);
-            unsigned char* base = kind == 1 ? a.c.k : a.c.v;
-            if (E4M3) {
-                // one scale a row: its largest magnitude becomes 448.  The quotient is rounded as a
-                // division is, so that the stored value depends on the row alone; the floor keeps it
-                // finite for rows of (nearly) zeros.
+            if (kind > 0 && here) {
+                const long long row = kv_row(a.c, pl.page, pl.pos) + ((long long)h << a.c.page_shift);
                 float step = amax / 448.0f;
                 step = step < 0x1p-100f ? 0x1p-100f : step;
+                // x / step, rounded as a division is (the quotient by the reciprocal and its remainder's correction,
+                // Markstein 1990), so that the stored value depends on the row alone
+                const float inv = __frcp_rn(step);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    x[j] = __fdiv_rn(x[j], step);
-                unsigned char* dst = base + row * D;
+                for (int j = 0; j < 16; ++j) {
+                    const float y = x[j] * inv;
+                    x[j] = fmaf(fmaf(-y, step, x[j]), inv, y);
+                }
+                unsigned char* dst = (kind == 1 ? a.c.k : a.c.v) + row * D;
                 *reinterpret_cast<uint2*>(dst + 8 * c0) = make_uint2(e4m3_quad(x), e4m3_quad(x + 4));
                 *reinterpret_cast<uint2*>(dst + 8 * c1) = make_uint2(e4m3_quad(x + 8), e4m3_quad(x + 12));
                 if (c == 0)
                     (kind == 1 ? a.c.k_scale : a.c.v_scale)[row] = step;
-            } else {
-                __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(base) + row * D;
-                store_chunk(dst + 8 * c0, x);
-                store_chunk(dst + 8 * c1, x + 8);
             }
         }
+        if (!E4M3 && kind > 0 && here) {
+            const long long row = kv_row(a.c, pl.page, pl.pos) + ((long long)h << a.c.page_shift);
+            __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(kind == 1 ? a.c.k : a.c.v) + row * D;
+            store_chunk(dst + 8 * c0, x);
+            store_chunk(dst + 8 * c1, x + 8);
+        }
+        now = next;
     }
 }
 
