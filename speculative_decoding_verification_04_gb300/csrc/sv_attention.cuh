@@ -190,6 +190,7 @@ struct AttnShared {
     uint32_t tmem;
     int abort;
     int b, h, g, tile, active;
+    SeqLens first;                                 // the first sequence's lengths
     int unset[2];
     float top[4];
     float q_unscale[4];                            // undoes the queries' power of two (e4m3), by item: the first
@@ -224,7 +225,7 @@ __device__ __forceinline__ AttnLayout attn_layout(const AttnArgs& a, unsigned ch
     return L;
 }
 
-__device__ __forceinline__ Run run_of(const AttnArgs& a, const AttnShared& shared)
+__device__ __forceinline__ Run run_of(const AttnShared& shared)
 {
     const volatile AttnShared& sh = shared;
     Run r;
@@ -234,7 +235,11 @@ __device__ __forceinline__ Run run_of(const AttnArgs& a, const AttnShared& share
     r.g = sh.g;
     r.tile = sh.tile;
     r.t0 = r.t1 = 0;
-    r.s = seq_lens(a, r.b);
+    r.s.ctx = sh.first.ctx;
+    r.s.nn = sh.first.nn;
+    r.s.len = sh.first.len;
+    r.s.tiles = sh.first.tiles;
+    r.s.ok = sh.first.ok;
     return r;
 }
 
@@ -762,6 +767,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     sh.h = hg / a.groups;
                     sh.g = hg - sh.h * a.groups;
                     sh.tile = tile;
+                    sh.first = seq_lens(a, b);
                 }
             }
         if (tid == 0) {
@@ -781,7 +787,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // --- softmax: one position a thread, NT rows --------------------------
             const AttnLayout L = attn_layout<N, E4M3>(a, smem);
             AttnShared& sh = *L.sh;
-            Run run = run_of(a, sh);
+            Run run = run_of(sh);
             const int w = warp >> 2, t = tid & 127, bar = 1 + w;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t tmem = sh.tmem + lanes + w * NT, tmem_o = tmem + 2 * N;   // S (two buffers of N columns), then O
@@ -814,8 +820,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     scales_of(run.t0, page_next, ks, vs);
                     page_next = page_of(run.t0 + 1);
                     const ItemInfo& info = sh.info[items & 1];
-                    cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
-                    const unsigned poison = info.poison;
                     if (t < NT)
                         negm[t] = 0.0f;
                     if (t == 0)
@@ -863,6 +867,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         // who sees this position: every row in the context, a node's descendants behind it
                         unsigned long long seen = ~0ull;
                         if ((j + 1) * kTile > ctx) {   // the tile holds nodes, or ends the sequence
+                            cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
+                            const unsigned poison = info.poison;
                             const int m = j * kTile + t - ctx;
                             if (m >= 0) {
                                 seen = 0;
@@ -957,6 +963,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     float* const fin = scratch + 4 * NT;
                     // (after a wait that gave up nothing of the item can be relied on)
+                    cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
                     const bool abort = bar_any(bar, 128, *reinterpret_cast<volatile int*>(&sh.abort) != 0), bad = abort || info.bad;
                     if (tid == 0 && bad && a.has_err)
                         atomicOr(a.err, abort ? kErrWaitTimeout : kErrCache);
@@ -964,7 +971,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (t < NT && !abort) {
                         const unsigned anc = info.anc[w * NT + t];
                         float l = (scratch[t] + scratch[NT + t]) + (scratch[2 * NT + t] + scratch[3 * NT + t]);
-                        if (bad || (anc & poison))
+                        if (bad || (anc & info.poison))
                             l = NAN;
                         fin[t] = l == 0.0f || anc == 0 ? 0.0f : __fdividef(1.0f, l);   // (anc == 0: no node's row)
                         const int at = info.row_out[w * NT + t];
@@ -1023,7 +1030,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // are, so that the one to be refilled is likely free
         const int k_ahead = max(1, a.kslots / a.nd - 1), v_ahead = max(1, a.vslots / a.nd - 1);
         Tiles k, v;
-        k.start(a, run_of(a, sh));
+        k.start(a, run_of(sh));
         v = k;
         Ring rk, rv;
         int nk = 0, nv = 0;   // slots that may still be filling
@@ -1062,7 +1069,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         };
         bool go = true;
         Tiles it;
-        it.start(a, run_of(a, sh));
+        it.start(a, run_of(sh));
         uint32_t items = 0;
         Ring r, w;
         // an item's queries, as three 8-bit terms (before its keys' first product): a thread takes one 8-element
@@ -1213,7 +1220,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         AttnShared& sh = *L.sh;
         if (warp == 9) {
             // --- bf16 queries; e4m3 keys (whose other loading warps convert values) --------------
-            Run run = run_of(a, sh);
+            Run run = run_of(sh);
             uint32_t items = 0;
             bool go = true;
 #pragma unroll 1
@@ -1268,7 +1275,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             uint32_t g = 0, items = 0;   // tiles, items so far
             Tiles k;
             bool go = true;
-            for (k.start(a, run_of(a, sh)); k.more; k.step(a), ++g) {
+            for (k.start(a, run_of(sh)); k.more; k.step(a), ++g) {
                 if (k.j == k.run.t0)
                     go = cta_wait(sh, &sh.q_full, items++ & 1);
                 go = go && cta_wait(sh, &sh.s_empty[g & 1], ((g >> 1) & 1) ^ 1);
@@ -1312,7 +1319,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             uint32_t g = 0, items = 0;
             Tiles v;
             bool go = true;
-            for (v.start(a, run_of(a, sh)); v.more; ++g) {
+            for (v.start(a, run_of(sh)); v.more; ++g) {
                 const int valid = v.valid(), ksteps = (valid + 15) / 16;
                 const bool tail = (v.j + 1) * kTile > v.run.s.ctx;
 #pragma unroll 1
@@ -1375,7 +1382,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         } else {
             // --- an item's rows ------------------------------------------------------------
-            Run run = run_of(a, sh);
+            Run run = run_of(sh);
             uint32_t items = 0;
             while (run.next(a) && prepare_item<N, E4M3>(a, sh, run, items, lane))
                 ++items;
@@ -1390,13 +1397,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // Items cut between CTAs: CTA i's last item, if it does not end it, is joined
-// with the parts of the CTAs that go on with it.  A warp takes one row.
+// with the parts of the CTAs that go on with it.  A warp takes one row, a lane
+// four elements at a time; what bounds it is latency (meta, sums, parts), so
+// four parts' loads are in flight at once.
 __global__ void __launch_bounds__(256) sv_attention_combine(const __grid_constant__ AttnArgs a, int ctas)
 {
-    pdl_wait();
     const int i = blockIdx.x, lane = threadIdx.x & 31, D = a.c.D;
+    const int row = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    pdl_wait();
     const int item = a.meta[2 * i];
-    if (item < 0)
+    if (item < 0 || row >= a.rows)
         return;
     int n = 1;
     for (;;) {   // parts: a ballot of the following CTAs that continue this item
@@ -1407,17 +1417,15 @@ __global__ void __launch_bounds__(256) sv_attention_combine(const __grid_constan
         if (more < 32)
             break;
     }
-    const int per = a.c.Hkv * a.groups, b = item / per, h = (item - b * per) / a.groups, g = item - (b * a.c.Hkv + h) * a.groups;
-    const int row = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    int node, head;
-    if (!attn_row(a, g, row, node, head))
-        return;
-    const SeqLens s = seq_lens(a, b);
     // part p: CTA i's begun slot, then the continued slots of CTAs i + 1 ...
-    auto slot = [&](int p) { return p == 0 ? 2LL * i + 1 : 2LL * (i + p); };
+    auto slot = [&](int p) { return (p == 0 ? 2LL * i + 1 : 2LL * (i + p)) * a.rows + row; };
+    auto sums = [&](int p) {
+        return p < n ? reinterpret_cast<const float2*>(a.part_ml)[slot(p)] : make_float2(-INFINITY, 0.0f);
+    };
+    const float2 mine = sums(lane);   // of the first 32 parts
     float m = -INFINITY;
     for (int p = lane; p < n; p += 32) {
-        const float2 x = *reinterpret_cast<const float2*>(a.part_ml + (slot(p) * a.rows + row) * 2);
+        const float2 x = p < 32 ? mine : sums(p);
         if (x.y != 0.0f)
             m = fmaxf(m, x.x);
     }
@@ -1428,33 +1436,55 @@ __global__ void __launch_bounds__(256) sv_attention_combine(const __grid_constan
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         acc[e] = 0.0f;
+    const int quads = D / 4;
     for (int p0 = 0; p0 < n; p0 += 32) {
-        float wgt = 0.0f, wl = 0.0f;
-        if (p0 + lane < n) {
-            const float2 x = *reinterpret_cast<const float2*>(a.part_ml + (slot(p0 + lane) * a.rows + row) * 2);
-            wgt = x.y == 0.0f ? 0.0f : ex2_approx(x.x - m);
-            wl = wgt * x.y;
-        }
+        const float2 x = p0 == 0 ? mine : sums(p0 + lane);
+        const float wgt = x.y == 0.0f ? 0.0f : ex2_approx(x.x - m);
+        float wl = wgt * x.y;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             wl += __shfl_xor_sync(kFull, wl, o);
         l += wl;
-        for (int p = p0; p < min(n, p0 + 32); ++p) {
-            const float wp = __shfl_sync(kFull, wgt, p - p0);
-            const float* o = a.part_o + (slot(p) * a.rows + row) * D;
-            if (wp != 0.0f)   // a part without weight may hold what no product has written
+        const int end = min(n - p0, 32);
+        for (int p = 0; p < end; p += 4) {
+            float4 y[4][2];
+            float wp[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (lane + 32 * e < D)
-                        acc[e] = fmaf(wp, o[lane + 32 * e], acc[e]);
+            for (int k = 0; k < 4; ++k) {
+                wp[k] = __shfl_sync(kFull, wgt, (p + k) & 31);
+                const float4* o = reinterpret_cast<const float4*>(a.part_o + slot(p0 + p + k) * D);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)   // (a part without weight may hold what no product has written)
+                    y[k][e] = p + k < end && wp[k] != 0.0f && lane + 32 * e < quads ? o[lane + 32 * e] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float w = p + k < end ? wp[k] : 0.0f;
+                    acc[4 * e] = fmaf(w, y[k][e].x, acc[4 * e]);
+                    acc[4 * e + 1] = fmaf(w, y[k][e].y, acc[4 * e + 1]);
+                    acc[4 * e + 2] = fmaf(w, y[k][e].z, acc[4 * e + 2]);
+                    acc[4 * e + 3] = fmaf(w, y[k][e].w, acc[4 * e + 3]);
+                }
         }
     }
+    const int per = a.c.Hkv * a.groups, b = item / per, h = (item - b * per) / a.groups, g = item - (b * a.c.Hkv + h) * a.groups;
+    int node, head;
+    if (!attn_row(a, g, row, node, head))
+        return;
+    const int nn = a.has_n ? __ldg(a.n_nodes + b) : a.Nmax;   // (an item of unusable lengths is never cut)
     __nv_bfloat16* out = a.out + (((long long)b * a.Nmax + node) * a.Hq + h * a.G + head) * D;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (lane + 32 * e < D)
-            out[lane + 32 * e] = __float2bfloat16_rn(node < s.nn ? acc[e] * inv : 0.0f);
+    for (int e = 0; e < 2; ++e)
+        if (lane + 32 * e < quads) {
+            const float f = node < nn ? inv : 0.0f;
+            const bool zero = f == 0.0f;
+            reinterpret_cast<uint2*>(out)[lane + 32 * e] =
+                zero ? make_uint2(0, 0)
+                     : make_uint2(bf16_pair(acc[4 * e] * f, acc[4 * e + 1] * f), bf16_pair(acc[4 * e + 2] * f, acc[4 * e + 3] * f));
+        }
 }
 
 }  // namespace sv
