@@ -66,15 +66,15 @@ cudaError_t launch_append(AppendArgs& a, cudaStream_t st)
 {
     const int units = a.c.D / 16, lpr = units <= 4 ? 4 : units <= 8 ? 8 : 16;
     const int heads = (a.has_q ? a.Hq : 0) + 2 * a.c.Hkv, rpw = 32 / lpr;
-    a.wpt = warps_per_token((heads + rpw - 1) / rpw, a.rows);
-    const long long warps = (long long)a.rows * a.wpt;
-    const unsigned grid = (unsigned)((warps + 7) / 8);
+    const int wpt = std::min(8, warps_per_token((heads + rpw - 1) / rpw, a.rows)), tpb = 8 / wpt;
+    const dim3 block(32, wpt, tpb);
+    const unsigned grid = (unsigned)((a.rows + tpb - 1) / tpb);
     if (lpr == 4)
-        sv_append_kernel<T, 4, E4M3><<<grid, 256, 0, st>>>(a);
+        sv_append_kernel<T, 4, E4M3><<<grid, block, 0, st>>>(a);
     else if (lpr == 8)
-        sv_append_kernel<T, 8, E4M3><<<grid, 256, 0, st>>>(a);
+        sv_append_kernel<T, 8, E4M3><<<grid, block, 0, st>>>(a);
     else
-        sv_append_kernel<T, 16, E4M3><<<grid, 256, 0, st>>>(a);
+        sv_append_kernel<T, 16, E4M3><<<grid, block, 0, st>>>(a);
     return cudaGetLastError();
 }
 

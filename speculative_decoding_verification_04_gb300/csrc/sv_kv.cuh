@@ -80,7 +80,6 @@ struct AppendArgs {
     uint32_t* err;
     int has_q, has_qn, has_kn, has_rot, has_parent, has_n, packed, has_err;
     int Hq, B, S, rows, max_positions, rot, interleaved;
-    int wpt;             // warps a token's heads are spread over
     float eps;
 };
 
@@ -157,6 +156,8 @@ __device__ __forceinline__ TokenPlace token_place(const AppendArgs& a, int t, in
     return r;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <typename T> struct Row16;   // 16 elements in two chunks of 8
 
 template <> struct Row16<__nv_bfloat16> {
@@ -225,26 +226,29 @@ __device__ __forceinline__ void store_chunk(float* p, const float* x)
 
 __device__ __forceinline__ uint32_t e4m3_quad(const float* x)
 {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
+    uint32_t y;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(y) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+    return y;
 }
 
 // LPR lanes hold a head's row: 16 elements each, the lanes from D / 16 on none
 // (D = 80, 96, 112 of LPR 8; 144 ... 240 of LPR 16).  A warp holds 32 / LPR
-// rows at a time; the next ones are on their way while it works, and the first
-// are asked for before the token's place is looked up (which takes three loads
+// rows at a time; the next four times as many (half that in fp32) are on their
+// way while it works, and the first are asked for before the token's place is looked up (which takes three loads
 // that depend on one another).
 template <typename T, int LPR, bool E4M3>
-__global__ void __launch_bounds__(256) sv_append_kernel(const __grid_constant__ AppendArgs a)
+__global__ void __launch_bounds__(256, 3) sv_append_kernel(const __grid_constant__ AppendArgs a)
 {
-    const int lane = threadIdx.x & 31;
-    const int gw = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int t = gw / a.wpt;
+    // a block is tpb tokens of wpt warps each
+    const int lane = threadIdx.x, sub = threadIdx.y, wpt = blockDim.y;
+    const int t = blockIdx.x * blockDim.z + threadIdx.z;
     if (t >= a.rows)
         return;
     constexpr int RPW = 32 / LPR;
-    const int sub = gw - t * a.wpt;
     const int c = lane % LPR, D = a.c.D;
     const int Hk = a.c.Hkv, Hq = a.has_q ? a.Hq : 0, H = Hq + 2 * Hk;
     const bool live = c < D / 16;
@@ -254,112 +258,136 @@ __global__ void __launch_bounds__(256) sv_append_kernel(const __grid_constant__ 
     const int c1 = turn && !a.interleaved ? c + a.rot / 16 : 2 * c + 1;
 
     // the rows that the lane's part of pass r0 lies in: queries, keys, values
-    auto load = [&](int r0, Row16<T>& w) {
-        const int r = r0 + lane / LPR;
-        if (r >= H || !live)
-            return;
-        const T* src = r < Hq        ? static_cast<const T*>(a.q) + t * a.q_stride + (long long)r * D
-                       : r < Hq + Hk ? static_cast<const T*>(a.k) + t * a.k_stride + (long long)(r - Hq) * D
-                                     : static_cast<const T*>(a.v) + t * a.v_stride + (long long)(r - Hq - Hk) * D;
-        w.load(src, c0, c1);
+    const T* const q = static_cast<const T*>(a.q) + t * a.q_stride;
+    const T* const k = static_cast<const T*>(a.k) + t * a.k_stride;
+    const T* const v = static_cast<const T*>(a.v) + t * a.v_stride;
+    auto at = [&](int r) -> const T* {
+        return r >= H || !live ? nullptr : r < Hq ? q + r * D : r < Hq + Hk ? k + (r - Hq) * D : v + (r - Hq - Hk) * D;
     };
-    Row16<T> now{}, next{};
-    load(sub * RPW, now);
+    auto load = [&](int r, Row16<T>& w) {
+        if (const T* const x = at(r))
+            w.load(x, c0, c1);
+    };
+    Row16<T> now{};
+    int r = sub * RPW + lane / LPR;
+    load(r, now);
+    // the three passes after it, into L2 (registers to hold them would cost a third of the warps): the first lane
+    // of each 128 bytes asks
+#pragma unroll
+    for (int j = 1; j < 4; ++j) {
+        const T* const x = at(r + j * wpt * RPW);
+        if (x && c % (128 / (16 * (int)sizeof(T))) == 0)
+            prefetch_l2(x + 16 * c);
+    }
     const TokenPlace pl = token_place(a, t, lane);
     if (pl.state == 2 && a.has_err && sub == 0 && lane == 0)
         atomicOr(a.err, kErrCache);
+    const bool placed = pl.state == 0;
 
-    float cs[8], sn[8];
-    if (turn && pl.state == 0) {
-        const float* r = a.cos_sin + (long long)pl.angle * a.rot + 8 * c;
+    // cosines and sines of the lane's eight pairs, two by two
+    uint64_t cs[4], sn[4];
+    if (turn && placed) {
+        const float* x = a.cos_sin + (long long)pl.angle * a.rot + 8 * c;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float4 u = __ldg(reinterpret_cast<const float4*>(r) + j);
-            const float4 w = __ldg(reinterpret_cast<const float4*>(r + a.rot / 2) + j);
-            cs[4 * j] = u.x, cs[4 * j + 1] = u.y, cs[4 * j + 2] = u.z, cs[4 * j + 3] = u.w;
-            sn[4 * j] = w.x, sn[4 * j + 1] = w.y, sn[4 * j + 2] = w.z, sn[4 * j + 3] = w.w;
+            const float4 u = __ldg(reinterpret_cast<const float4*>(x) + j);
+            const float4 w = __ldg(reinterpret_cast<const float4*>(x + a.rot / 2) + j);
+            cs[2 * j] = f2_pack(u.x, u.y), cs[2 * j + 1] = f2_pack(u.z, u.w);
+            sn[2 * j] = f2_pack(w.x, w.y), sn[2 * j + 1] = f2_pack(w.z, w.w);
         }
     }
-    for (int r0 = sub * RPW; r0 < H; r0 += a.wpt * RPW) {   // uniform in the warp: the shuffles below need every lane
-        load(r0 + a.wpt * RPW, next);
-        const int r = r0 + lane / LPR;
+    for (int r0 = sub * RPW; r0 < H; r0 += wpt * RPW, r += wpt * RPW) {   // uniform in the warp: the shuffles need every lane
         const int kind = r < Hq ? 0 : r < Hq + Hk ? 1 : 2;
-        const int h = kind == 0 ? r : kind == 1 ? r - Hq : r - Hq - Hk;
-        const bool act = r < H && live, here = act && pl.state == 0;
+        const bool act = r < H && live, here = act && placed;
         float x[16];
         now.get(x);
+        load(r + wpt * RPW, now);
         if (!here) {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 x[j] = 0.0f;
         }
-        const bool norm = kind == 0 ? a.has_qn : kind == 1 ? a.has_kn : false;
-        if (a.has_qn | a.has_kn) {
-            float ss = 0.0f;
+        uint64_t y[8];   // two by two
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                ss = fmaf(x[j], x[j], ss);
+        for (int j = 0; j < 8; ++j)
+            y[j] = f2_pack(x[2 * j], x[2 * j + 1]);
+        if (a.has_qn | a.has_kn) {
+            uint64_t s2 = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s2 = f2_fma(y[j], y[j], s2);
+            float ss, other;
+            f2_unpack(s2, ss, other);
+            ss += other;
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1)
                 ss += __shfl_xor_sync(kFull, ss, o);
-            if (norm && here) {
-                Row16<T> w;
-                w.load(static_cast<const T*>(kind == 0 ? a.q_norm : a.k_norm), c0, c1);
+            if (here && (kind == 0 ? a.has_qn : kind == 1 ? a.has_kn : false)) {
+                Row16<T> n;
+                n.load(static_cast<const T*>(kind == 0 ? a.q_norm : a.k_norm), c0, c1);
                 float g[16];
-                w.get(g);
+                n.get(g);
                 const float inv = rsqrtf(ss / (float)D + a.eps);
+                const uint64_t i2 = f2_pack(inv, inv);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    x[j] = x[j] * inv * g[j];
+                for (int j = 0; j < 8; ++j)
+                    y[j] = f2_mul(f2_mul(y[j], i2), f2_pack(g[2 * j], g[2 * j + 1]));
             }
         }
-        if (turn && kind < 2 && pl.state == 0) {
+        if (turn && kind < 2 && placed) {
             if (a.interleaved) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float u = x[2 * j], w = x[2 * j + 1];
-                    x[2 * j] = u * cs[j] - w * sn[j];
-                    x[2 * j + 1] = w * cs[j] + u * sn[j];
+                    float c2[2], s2[2], u, w;
+                    f2_unpack(cs[j / 2], c2[0], c2[1]);
+                    f2_unpack(sn[j / 2], s2[0], s2[1]);
+                    f2_unpack(y[j], u, w);
+                    y[j] = f2_pack(u * c2[j & 1] - w * s2[j & 1], w * c2[j & 1] + u * s2[j & 1]);
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float u = x[j], w = x[8 + j];
-                    x[j] = u * cs[j] - w * sn[j];
-                    x[8 + j] = w * cs[j] + u * sn[j];
+                for (int j = 0; j < 4; ++j) {
+                    const uint64_t u = y[j], z = y[4 + j];
+                    y[j] = f2_sub(f2_mul(u, cs[j]), f2_mul(z, sn[j]));
+                    y[4 + j] = f2_fma(u, sn[j], f2_mul(z, cs[j]));
                 }
             }
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f2_unpack(y[j], x[2 * j], x[2 * j + 1]);
         if (kind == 0 && act) {
             if (pl.state == 2) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     x[j] = NAN;
             }
-            T* dst = static_cast<T*>(a.q_out) + ((long long)t * a.Hq + h) * D;
+            T* dst = static_cast<T*>(a.q_out) + ((long long)t * a.Hq + r) * D;
             store_chunk(dst + 8 * c0, x);
             store_chunk(dst + 8 * c1, x + 8);
         }
+        const int h = kind == 1 ? r - Hq : r - Hq - Hk;
+        const long long row = kv_row(a.c, pl.page, pl.pos) + ((long long)h << a.c.page_shift);
         if (E4M3 && __any_sync(kFull, kind > 0 && act)) {
             // one scale a row: its largest magnitude becomes 448; the floor keeps it finite for rows of (nearly) zeros
-            float amax = 0.0f;
+            uint32_t m = 0;   // (magnitudes order as integers, NaN above infinity)
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                amax = max_nan(amax, fabsf(x[j]));
+                m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1)
-                amax = max_nan(amax, __shfl_xor_sync(kFull, amax, o));
+                m = max(m, __shfl_xor_sync(kFull, m, o));
             if (kind > 0 && here) {
-                const long long row = kv_row(a.c, pl.page, pl.pos) + ((long long)h << a.c.page_shift);
-                float step = amax / 448.0f;
+                float step = __uint_as_float(m) / 448.0f;
                 step = step < 0x1p-100f ? 0x1p-100f : step;
                 // x / step, rounded as a division is (the quotient by the reciprocal and its remainder's correction,
                 // Markstein 1990), so that the stored value depends on the row alone
                 const float inv = __frcp_rn(step);
+                const uint64_t i2 = f2_pack(inv, inv), n2 = f2_pack(-step, -step);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float y = x[j] * inv;
-                    x[j] = fmaf(fmaf(-y, step, x[j]), inv, y);
+                for (int j = 0; j < 8; ++j) {
+                    const uint64_t z = f2_pack(x[2 * j], x[2 * j + 1]), u = f2_mul(z, i2);
+                    f2_unpack(f2_fma(f2_fma(u, n2, z), i2, u), x[2 * j], x[2 * j + 1]);
                 }
                 unsigned char* dst = (kind == 1 ? a.c.k : a.c.v) + row * D;
                 *reinterpret_cast<uint2*>(dst + 8 * c0) = make_uint2(e4m3_quad(x), e4m3_quad(x + 4));
@@ -369,12 +397,10 @@ __global__ void __launch_bounds__(256) sv_append_kernel(const __grid_constant__ 
             }
         }
         if (!E4M3 && kind > 0 && here) {
-            const long long row = kv_row(a.c, pl.page, pl.pos) + ((long long)h << a.c.page_shift);
             __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(kind == 1 ? a.c.k : a.c.v) + row * D;
             store_chunk(dst + 8 * c0, x);
             store_chunk(dst + 8 * c1, x + 8);
         }
-        now = next;
     }
 }
 
