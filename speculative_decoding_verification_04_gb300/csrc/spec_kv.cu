@@ -51,12 +51,12 @@ sv_status check_cache(const sv_kv_cache* c, bool need_table, KvCache* out)
 sv_status launched(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 
 // Warps a token's work of `passes` warp passes is spread over: all of them
-// while the tokens alone leave the GPU's SMs short of warps, one per four
+// while the tokens alone leave the GPU's SMs short of warps, one per six
 // passes once there are plenty (a warp's token lookup is then shared by them).
 int warps_per_token(int passes, long long tokens)
 {
     const long long want = 152 * 16;
-    const int most = std::max(1, passes), least = std::max(1, (passes + 3) / 4);
+    const int most = std::max(1, passes), least = std::max(1, (passes + 5) / 6);
     const long long w = tokens > 0 ? (want + tokens - 1) / tokens : most;
     return (int)std::min<long long>(most, std::max<long long>(least, w));
 }
@@ -220,10 +220,12 @@ cudaError_t launch_attention_rows(AttnArgs& a, const CUtensorMap (&m)[3], int de
 {
     if (a.rows <= 16)
         return launch_attention<16, 1, E4M3>(a, m, dev, nsm, st);
-    switch ((a.rows + 31) / 32) {
-    case 1: return launch_attention<16, 2, E4M3>(a, m, dev, nsm, st);
-    case 2: return launch_attention<32, 2, E4M3>(a, m, dev, nsm, st);
-    case 3: return launch_attention<48, 2, E4M3>(a, m, dev, nsm, st);
+    switch ((a.rows + 15) / 16) {
+    case 2: return launch_attention<16, 2, E4M3>(a, m, dev, nsm, st);
+    case 3: return launch_attention<24, 2, E4M3>(a, m, dev, nsm, st);
+    case 4: return launch_attention<32, 2, E4M3>(a, m, dev, nsm, st);
+    case 5: return launch_attention<40, 2, E4M3>(a, m, dev, nsm, st);
+    case 6: return launch_attention<48, 2, E4M3>(a, m, dev, nsm, st);
     default: return launch_attention<64, 2, E4M3>(a, m, dev, nsm, st);
     }
 }

@@ -397,16 +397,16 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
 {
     const int lane = t & 31, warp = t >> 5;
 #pragma unroll 1
-    for (int c = 0; c < NT; c += 16) {
-        float s[16], keep = 0.0f;
-        tmem_ld16(s_at + c, s);
+    for (int c = 0; c < NT; c += 8) {
+        float s[8], keep = 0.0f;
+        tmem_ld8(s_at + c, s);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < 8; ++k) {
             const float x = warp_redux_max((seen >> (c + k)) & 1 ? fmaf(s[k], mult, negm[c + k] + add) : -INFINITY);
             keep = lane == k ? x : keep;
         }
-        if (lane < 16)
+        if (lane < 8)
             scratch[warp * NT + c + lane] = keep;
     }
     bar_sync(bar, 128);
@@ -436,14 +436,14 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
 #pragma unroll 1
     for (int i = 0; i < o_chunks; ++i)
 #pragma unroll 1
-        for (int c = 0; c < NT; c += 16) {
-            float o[16];
-            tmem_ld16(o_at + i * o_pitch + c, o);
+        for (int c = 0; c < NT; c += 8) {
+            float o[8];
+            tmem_ld8(o_at + i * o_pitch + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
+            for (int k = 0; k < 8; ++k)
                 o[k] *= scratch[c + k];
-            tmem_st16(o_at + i * o_pitch + c, o);
+            tmem_st8(o_at + i * o_pitch + c, o);
         }
     tmem_wait_st();
 }
@@ -841,6 +841,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                         for (int i = 0; i < NT / 16; ++i)
                             tmem_ld16(s_at + 16 * i, s + 16 * i);
+                        if (NT % 16)
+                            tmem_ld8(s_at + NT - 8, s + NT - 8);
                         float mult = a.scale_log2, add = 0.0f;   // add: log2 of the value's scale
                         if (E4M3) {
                             if (first_tile)
@@ -942,14 +944,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
                     // the rows' sums over the 128 threads, while the last product runs
 #pragma unroll
-                    for (int i = 0; i < NT / 16; ++i) {
-                        // lane c (of 16) ends with column 16 i + c: halve the columns, double the lanes summed
-                        float x[16];
+                    for (int i = 0; i < NT / 8; ++i) {
+                        // lane c (of 8) ends with column 8 i + c: halve the columns, double the lanes summed
+                        float x[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            f2_unpack(l2[8 * i + k], x[2 * k], x[2 * k + 1]);
+                        for (int k = 0; k < 4; ++k)
+                            f2_unpack(l2[4 * i + k], x[2 * k], x[2 * k + 1]);
 #pragma unroll
-                        for (int o = 8; o > 0; o >>= 1)
+                        for (int o = 4; o > 0; o >>= 1)
 #pragma unroll
                             for (int k = 0; k < o; ++k) {
                                 const bool up = lane & o;
@@ -957,9 +959,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 const float keep = up ? x[k + o] : x[k];
                                 x[k] = keep + __shfl_xor_sync(kFull, send, o);
                             }
+                        x[0] += __shfl_xor_sync(kFull, x[0], 8);
                         x[0] += __shfl_xor_sync(kFull, x[0], 16);
-                        if (lane < 16)
-                            scratch[(warp & 3) * NT + 16 * i + lane] = x[0];
+                        if (lane < 8)
+                            scratch[(warp & 3) * NT + 8 * i + lane] = x[0];
                     }
                     float* const fin = scratch + 4 * NT;
                     // (after a wait that gave up nothing of the item can be relied on)
@@ -1080,13 +1083,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int live = min(a.nodes, x.s.nn - node0), heads = min(a.heads, a.G - head0);
             const uint4* const q = reinterpret_cast<const uint4*>(a.q + ((long long)x.b * a.Nmax + node0) * a.q_stride +
                                                                   (long long)(x.h * a.G + head0) * D) + ch;
-            // four rows a thread at a time (all of them, up to 32 rows of 128 elements), zeros where there is no query
-            const int turn = 4 * stride;
-            uint4 y[4];
+            // kRows rows a thread at a time (which is all of up to 64, or 32, rows of 128 elements), zeros where there is
+            // no query
+            constexpr int kRows = NT >= 64 ? 4 : 8;
+            const int turn = kRows * stride;
+            uint4 y[kRows];
             auto load_q = [&](int row) {
                 int n = row / a.heads, head = row - n * a.heads;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kRows; ++k) {
                     y[k] = n < live && head < heads && row0 < stride ? __ldg(q + n * (a.q_stride / 8) + head * per) : make_uint4(0, 0, 0, 0);
                     for (head += stride; head >= a.heads; head -= a.heads)
                         ++n;
@@ -1098,7 +1103,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int row = row0; row < a.rows; row += turn) {
                 load_q(row);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kRows; ++k) {
                     const uint32_t z[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -1122,7 +1127,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (a.rows > turn)
                     load_q(row);
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kRows; ++k) {
                     const int at = row + k * stride;
                     if (at >= a.rows || row0 >= stride)
                         break;
@@ -1137,7 +1142,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int c = 0; c < 3; ++c)
                         *reinterpret_cast<uint2*>(o + c * L.q_part) = make_uint2(p[c][0] | (p[c][1] << 16), p[c][2] | (p[c][3] << 16));
 #pragma unroll
-                    for (int c = 0; c < 3; ++c)   // (rolled, the code being long: the next one to the front)
+                    for (int c = 0; c < kRows - 1; ++c)   // (rolled, the code being long: the next one to the front)
                         y[c] = y[c + 1];
                 }
             }
