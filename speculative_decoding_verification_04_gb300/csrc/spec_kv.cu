@@ -369,7 +369,7 @@ sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, c
     a.groups = rg.groups;
     a.rows = rg.rows;
     a.nd = cache->head_dim > 128 ? 2 : 1;
-    a.box_rows = std::min(cache->page_size, sv::kQuarter);
+    a.box_rows = std::min(cache->page_size, e4m3 ? sv::kTile : sv::kQuarter);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     a.part_o = reinterpret_cast<float*>(ws);
     ws += (size_t)2 * sv::kAttnMaxCtas * a.rows * cache->head_dim * 4;

@@ -181,8 +181,7 @@ struct alignas(16) ItemInfo {
 
 struct AttnShared {
     uint64_t kfull[kMaxSlots], kempty[kMaxSlots];  // K slots
-    uint64_t vfull[kMaxSlots], vempty[kMaxSlots];  // V slots (bf16)
-    uint64_t vpart[kMaxSlots][4];                  // quarters of V slots (e4m3)
+    uint64_t vfull[kMaxSlots], vempty[kMaxSlots];  // V slots
     uint64_t cfull[2], cempty[2];                  // converted V slots (e4m3)
     uint64_t q_full, q_empty, info_full[2], info_empty[2];
     uint64_t s_full[2], s_empty[2], p_full, o_full, drain[2];
@@ -330,22 +329,19 @@ __device__ __forceinline__ bool chunk_nonfinite(uint4 w, bool e4m3)
 }
 
 // Two query elements (scaled so that the group's largest is below 256) as an
-// e4m3 and two e5m2 terms each; what is not finite becomes NaN.  The
-// differences are exact in fp16 (down to 2^-24).
+// e4m3 and two e5m2 terms each.  The differences are exact in fp16 (down to
+// 2^-24).  NaN stays NaN; an infinity, which the conversions would saturate,
+// is made one by the difference with itself.
 __device__ __forceinline__ void split_q(float x0, float x1, uint32_t& h, uint32_t& m, uint32_t& l)
 {
+    const uint64_t z = f2_pack(x0, x1);
+    f2_unpack(f2_add(z, f2_sub(z, z)), x0, x1);
     const __half2 x = __floats2half2_rn(x0, x1);
     h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(x), __NV_SATFINITE, __NV_E4M3);
     const __half2 r = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3)));
     m = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(r), __NV_SATFINITE, __NV_E5M2);
     const __half2 r2 = __hsub2(r, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)m, __NV_E5M2)));
     l = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(r2), __NV_SATFINITE, __NV_E5M2);
-    if (!isfinite(x0) || !isfinite(x1)) {
-        const uint32_t keep = isfinite(x0) ? 0x00ffu : isfinite(x1) ? 0xff00u : 0u;
-        h = (h & keep) | (0x7f7fu & ~keep);
-        m &= keep;
-        l &= keep;
-    }
 }
 
 // One lane: the products of a K slot (bf16, or e4m3 with the three terms of
@@ -653,9 +649,9 @@ constexpr int kAttnThreads = 512;
 // its L2 latency, the caches being shared memory.  The shares add up to the
 // launch's.
 constexpr int kAttnRegs = 128;       // at launch
-constexpr int kRegsIssue = 72;
 template <int NT> constexpr int kRegsSoftmax = NT >= 64 ? 168 : 152;
-template <int NT> constexpr int kRegsTiles = 4 * kAttnRegs - kRegsIssue - 2 * kRegsSoftmax<NT>;
+template <int NT> constexpr int kRegsIssue = NT >= 64 ? 80 : 96;
+template <int NT> constexpr int kRegsTiles = 4 * kAttnRegs - kRegsIssue<NT> - 2 * kRegsSoftmax<NT>;
 
 // NT: rows (TMEM columns) a softmax warpgroup handles; NWG: softmax
 // warpgroups with rows.
@@ -681,10 +677,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
 #pragma unroll 1
             for (int i = 0; i < a.vslots; ++i) {
-                mbar_init(smem_addr(&sh.vfull[i]), 4);
-                mbar_init(smem_addr(&sh.vempty[i]), 1);
-                for (int k = 0; k < 4; ++k)
-                    mbar_init(smem_addr(&sh.vpart[i][k]), 1);
+                mbar_init(smem_addr(&sh.vfull[i]), E4M3 ? 1 : 4);
+                mbar_init(smem_addr(&sh.vempty[i]), E4M3 ? 4 : 1);
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_addr(&sh.cfull[i]), 4);
@@ -1021,10 +1015,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         }
     } else if (warp >= 12) {
-        if constexpr (kRegsTiles<NT> > kAttnRegs)
-            regs_grow<kRegsTiles<NT>>();
-        else
-            regs_shrink<kRegsTiles<NT>>();
+        regs_shrink<kRegsTiles<NT>>();
         // --- tiles: a quarter of the positions a warp ----------------------------------
         const AttnLayout L = attn_layout<N, E4M3>(a, smem);
         AttnShared& sh = *L.sh;
@@ -1060,11 +1051,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             box_v.ask(a, v, quarter * kQuarter, kQuarter, lane);
 #pragma unroll 1
             for (int c = 0; c < a.nd; ++c) {
-                // (an e4m3 quarter is reloaded by the warp that has read it)
-                if (!E4M3 && !cta_wait(sh, &sh.vempty[rv.slot], rv.phase ^ 1))
+                if (!cta_wait(sh, &sh.vempty[rv.slot], rv.phase ^ 1))
                     return false;
                 load_boxes<E4M3>(a, smem_addr(L.v) + rv.slot * a.v_bytes + quarter * kQuarter * 128,
-                                 smem_addr(E4M3 ? &sh.vpart[rv.slot][quarter] : &sh.vfull[rv.slot]), &map_v, c, now, lane);
+                                 smem_addr(&sh.vfull[rv.slot]), &map_v, c, now, lane);
                 rv.step(a.vslots);
                 nv = min(nv + 1, a.vslots);
             }
@@ -1152,8 +1142,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 mbar_arrive(smem_addr(&sh.q_full));
             ++items;
         };
-        // step g asks for tile g + k_ahead of the keys (bf16) or converts the values of tile g (e4m3), then asks for
-        // tile g + v_ahead of the values
+        // step g asks for tile g + k_ahead of the keys and g + v_ahead of the values (bf16), or converts the values of
+        // tile g (e4m3)
 #pragma unroll 1
         for (int g = -max(k_ahead, v_ahead); E4M3 ? it.more : go && (k.more || v.more); ++g) {
             // (e4m3: the warps share a barrier: after a timeout they all run on, doing nothing)
@@ -1170,7 +1160,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int node0 = it.run.s.nn > 1 ? it.run.s.ctx - it.j * kTile : kTile;   // first row of a node
 #pragma unroll 1
                 for (int c = 0; c < a.nd; ++c) {
-                    go = go && cta_wait(sh, &sh.vpart[r.slot][quarter], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
+                    go = go && cta_wait(sh, &sh.vfull[r.slot], r.phase) && cta_wait(sh, &sh.cempty[w.slot], w.phase ^ 1);
                     const unsigned char* src = L.v + r.slot * a.v_bytes + t * 128;
                     unsigned char* dst = L.c + w.slot * a.conv_bytes + t * 128;
                     const int pieces = min(128, D - 128 * c) / 16;
@@ -1199,14 +1189,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0)
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&sh.vempty[r.slot]));
                         mbar_arrive(smem_addr(&sh.cfull[w.slot]));
+                    }
                     r.step(a.vslots);
                     w.step(a.conv);
                 }
                 it.step(a);
             }
-            if (go && v.more && g >= -v_ahead)
+            if (!E4M3 && go && v.more && g >= -v_ahead)
                 go = load_v();
         }
         if (!go) {   // copies in flight land before the CTA's memory is given back
@@ -1216,15 +1208,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             for (; nv > 0; --nv) {
                 rv.back(a.vslots);
-                drain_wait(E4M3 ? &sh.vpart[rv.slot][quarter] : &sh.vfull[rv.slot], rv.phase);
+                drain_wait(&sh.vfull[rv.slot], rv.phase);
             }
         }
     } else {
-        regs_shrink<kRegsIssue>();
+        regs_shrink<kRegsIssue<NT>>();
         const AttnLayout L = attn_layout<N, E4M3>(a, smem);
         AttnShared& sh = *L.sh;
         if (warp == 9) {
-            // --- bf16 queries; e4m3 keys (whose other loading warps convert values) --------------
+            // --- bf16 queries; e4m3 keys (the loading warps of bf16 convert values there) -------
             Run run = run_of(sh);
             uint32_t items = 0;
             bool go = true;
@@ -1386,11 +1378,47 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 drain_wait(&sh.drain[1], 0);
             }
         } else {
-            // --- an item's rows ------------------------------------------------------------
-            Run run = run_of(sh);
+            // --- an item's rows; e4m3 values -------------------------------------------------
+            Run run = run_of(sh);   // the item to prepare next
             uint32_t items = 0;
-            while (run.next(a) && prepare_item<N, E4M3>(a, sh, run, items, lane))
-                ++items;
+            Tiles v;
+            Ring rv;
+            Boxes box;
+            int nv = 0;
+            v.start(a, run);
+            if (E4M3)
+                box.ask(a, v, 0, kTile, lane);
+            bool go = true, busy = true;
+            int owed = 1;   // items to prepare: the first, and the next one whenever an item's last values are asked for
+#pragma unroll 1
+            while (go && busy) {
+                busy = false;
+                if (E4M3 && v.more) {   // (bf16 values are loaded elsewhere)
+                    busy = true;
+                    owed += v.j == v.run.t1 - 1;
+                    const int now = box.row(a);
+                    v.step(a);
+                    box.ask(a, v, 0, kTile, lane);   // on its way while this tile is asked for
+#pragma unroll 1
+                    for (int c = 0; go && c < a.nd; ++c) {
+                        go = cta_wait(sh, &sh.vempty[rv.slot], rv.phase ^ 1);
+                        if (!go)
+                            break;
+                        load_boxes<E4M3>(a, smem_addr(L.v) + rv.slot * a.v_bytes, smem_addr(&sh.vfull[rv.slot]), &map_v, c, now, lane);
+                        rv.step(a.vslots);
+                        nv = min(nv + 1, a.vslots);
+                    }
+                }
+                if (go && (owed > 0 || !E4M3) && run.next(a)) {
+                    busy = true;
+                    go = prepare_item<N, E4M3>(a, sh, run, items++, lane);
+                    --owed;
+                }
+            }
+            for (; !go && nv > 0; --nv) {   // copies in flight land before the CTA's memory is given back
+                rv.back(a.vslots);
+                drain_wait(&sh.vfull[rv.slot], rv.phase);
+            }
         }
     }
     pdl_launch_dependents();
