@@ -84,6 +84,43 @@ def test_matches_definition(dev, case, fmt):
     check(call(q, cache, ctx, nodes, parents, dev, tree=tree), q, cache, ctx, nodes, parents)
 
 
+WIDE = [  # row groups: several nodes, one node, part of a node's heads
+    ([250, 3], 5, "random", 100, 2, 64, 16),      # 50 heads a node: two nodes a group
+    ([140], 3, "chain", 129, 1, 128, 32),         # 129 heads to one key head: two blocks of heads
+    ([70, 600], 2, "star", 200, 1, 64, 8),
+    ([33], 4, "random", 70, 1, 256, 16),
+    ([500], 32, "binary", 24, 8, 96, 8),          # three query heads a key head
+    ([260], 17, "random", 48, 16, 160, 128),
+]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: f"n{c[1]}h{c[3]}x{c[4]}d{c[5]}")
+def test_many_query_heads(dev, case, fmt):
+    ctx, N, tree, Hq, Hkv, D, page = case
+    q, cache, nodes, parents = make(ctx, N, tree, Hq, Hkv, D, fmt, page, dev, seed=21)
+    check(call(q, cache, ctx, nodes, parents, dev, tree=tree), q, cache, ctx, nodes, parents)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_scores_far_from_zero(dev, fmt):
+    """All scores of a row near +-several hundred: weights have to follow the
+    row's own level."""
+    ctx = [900, 130]
+    q, cache, nodes, parents = make(ctx, 5, "random", 4, 2, 64, fmt, 16, dev, seed=22)
+    q[:] = 4.0
+    q[:, :, 1::2] = -4.0
+    shift = torch.full((64,), 20.0, device=dev)
+    for b in range(2):
+        page, slot = cache.at(b, range(ctx[b] + 5))
+        if fmt == "bf16":
+            cache.k[page, :, slot] = (cache.k[page, :, slot].float() * 0.1 + shift).to(torch.bfloat16)
+        else:
+            cache.k.view(torch.uint8)[page, :, slot] = 0x38   # 1.0
+            cache.k_scale[page, :, slot] = 20.0 + 0.01 * torch.arange(ctx[b] + 5, device=dev)[:, None]
+    check(call(q, cache, ctx, nodes, parents, dev), q, cache, ctx, nodes, parents)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_every_length_around_a_tile(dev, fmt):
     """Lengths 0 ... 159 of one batch: the context ends at every slot of a page
@@ -282,6 +319,9 @@ def test_refusals(dev):
         sv.spec_tree_attention(q, cache.k, cache.v, cache.table.long(), kv)
     with pytest.raises(ValueError):
         sv.spec_tree_attention(q, cache.k, cache.v, cache.table, kv, k_scale=kv, v_scale=kv)
+    with pytest.raises(sv.SpecVerifyError):   # broadcast queries
+        two = Cache([9, 9], 2, 64, 8, "bf16", dev)
+        sv.spec_tree_attention(q[:, :1].expand(2, 1, 4, 64).as_strided((2, 1, 4, 64), (0, 256, 64, 1)), two.k, two.v, two.table, ints([3, 3], dev))
     with pytest.raises(sv.SpecVerifyError):   # more nodes than a tree may have
         sv.spec_tree_attention(torch.zeros(1, 33, 4, 64, device=dev, dtype=torch.bfloat16), *args)
     assert sv.spec_tree_attention(q[:0], cache.k, cache.v, cache.table[:0], kv[:0]).shape == (0, 4, 4, 64)
