@@ -528,9 +528,18 @@ sv_status spec_kv_append(const sv_kv_cache* cache, const sv_kv_tokens* tokens, c
  * an ordinary decode step.  q: element (b * Nmax + n) * q_stride, a multiple
  * of 8 and at least n_heads * head_dim; out [B][Nmax][n_heads][head_dim], zeros for n >= n_nodes[b]; both
  * bf16 (fp32 is SV_ERR_UNSUPPORTED).  Products accumulate in fp32, softmax
- * statistics are fp32; the weights are rounded to bf16 for the second
- * product.  Cache entries behind a sequence's nodes are never used: they may
- * hold anything.  workspace: >= sv_attention_workspace_size() bytes, 256-byte
+ * statistics are fp32; for the second product weights are rounded to bf16, or
+ * with SV_KV_E4M3 weights times value scales to fp16.  An e4m3 cache's first
+ * product takes each query element to 2^-25 of the largest finite one among
+ * the rows that a block works on together (nodes of one sequence and query
+ * heads of one key head).
+ * What is not finite: a query row, or a key or value scale that a row sees,
+ * makes that row NaN, and so does a node's value that it sees (ancestors and
+ * itself); rows that do not see the node are as without it.  The context is
+ * seen by all of a sequence's rows.  A negative value scale reads as NaN.  Cache entries behind a sequence's nodes are
+ * never used: they may hold anything.  Should a bounded wait inside the
+ * kernel give up, the rows concerned are NaN and bit 0 of
+ * `errors` is set.  workspace: >= sv_attention_workspace_size() bytes, 256-byte
  * aligned, not initialised; calls that overlap need one each.
  */
 size_t sv_attention_workspace_size(int32_t Nmax, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);

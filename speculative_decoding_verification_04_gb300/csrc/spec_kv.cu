@@ -52,7 +52,8 @@ sv_status launched(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUD
 
 // Warps a token's work of `passes` warp passes is spread over: all of them
 // while the tokens alone leave the GPU's SMs short of warps, one per six
-// passes once there are plenty (a warp's token lookup is then shared by them).
+// passes once there are plenty (a warp's token lookup is then shared by them:
+// 16411 prompt tokens take 81.8 us, 84.8 with one per four).
 int warps_per_token(int passes, long long tokens)
 {
     const long long want = 152 * 16;

@@ -30,16 +30,28 @@
 // scale is what fp16 holds.
 //
 // Warps: 0-7 softmax (two warpgroups), 8 and 10 the issue of the first and the
-// second product, 9 bf16 queries, 11 what an item needs before its first tile
-// (tree masks), 12-15 the tiles: each loads a quarter of the positions (a TMA
-// copy of a page holds its warp for about 130 cycles, so one warp cannot load
-// small pages as fast as memory delivers them) and, for e4m3 caches, converts
-// its quarter of the values and makes the queries' terms.  Tiles run through
-// them in one stream across items.
+// second product, 11 what an item needs before its first tile (tree masks).
+//  * bf16: 9 loads the queries, 12-15 a quarter of each tile's keys and values
+//    (a TMA copy of a page holds its warp for about 130 cycles, so one warp
+//    cannot load small pages as fast as memory delivers them: 371 us against
+//    275 for 256 trees at pages of 16).
+//  * e4m3: 9 loads the keys and 11 the values, 12-15 make the queries' terms
+//    and convert a quarter of the values each (converting warps that load as
+//    well: 118 us against 102 for 64 chains).
+// Tiles run through them in one stream across items.
+//
+// Measured on a GB300, a call (8 key heads of 128, 32 query heads):
+//  * 256 trees of 15 nodes over 100-1500 positions, bf16, pages of 16: 171 us,
+//    0.82 of the copy rate; HBM bounds it (914 MB read, nothing twice).
+//  * 64 chains of 9 over 200-3000 positions, e4m3: 102 us (bytes 34 us); what a
+//    tile takes from its load over conversion, products and softmax.
+//  * 2 x 32 nodes over 100-120 thousand positions, e4m3: 202 us, 600 TFLOP/s;
+//    tensor pipe 36 % and issue slots 41 % busy.
+//  * one token over 700 positions: 11.5 us on the GPU, latency.
 //
 // Work is (sequence, key head, row group) items of 128-position tiles, laid
 // end to end and cut into runs of equal cost, one to a CTA (an item costs its
-// tiles and kItemCost more).  An item cut by a run's end leaves partial sums
+// tiles and kItemCost more: 175 us for the 256 trees, 202 with equal tiles).  An item cut by a run's end leaves partial sums
 // in the workspace, which sv_attention_combine joins.
 #pragma once
 
@@ -55,7 +67,9 @@ constexpr int kHalfBytes = kTile * 128;    // 128 swizzled rows of 128 bytes
 template <bool E4M3> constexpr float kAtRef = E4M3 ? 6.0f : 0.0f;
 template <bool E4M3> constexpr float kLazy = E4M3 ? 14.0f : 24.0f;
 constexpr int kMaxSlots = 8;
-constexpr int kItemCost = 4;               // what an item's start and end cost, in tiles
+// What an item's start and end cost, in tiles.  Measured with 4, 2, 1 and 0: 256
+// trees 175, 178, 182, 202 us; odd sizes 57, 62, 66, 81; 64 chains 153, 174, 158, 178.
+constexpr int kItemCost = 4;
 constexpr int kQuarter = kTile / 4;        // positions a loading warp takes care of
 // Query rows a CTA: 128, but 64 where the three 8-bit terms of wider heads'
 // queries would leave the loads no room.
@@ -385,7 +399,10 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t v, uint32_t p, u
 
 // The rare step of the softmax, by the warpgroup's 128 threads: rows whose
 // scores lie too far from their references get new ones (their maxima over
-// this tile), and the sums in TMEM are rescaled.  scratch[0 .. NT) then holds
+// this tile), and the sums in TMEM are rescaled.  In bf16 each row goes by its
+// own scores, so that its rounding does not depend on the rows beside it.  In
+// e4m3, where moves are frequent, all rows that have risen move at once (two
+// sequences of 110 thousand positions: 200 us, 233 with a move a row).  scratch[0 .. NT) then holds
 // the factors of what was summed so far, [NT .. 2 NT) how far references rose.
 template <int NT, bool E4M3>
 __device__ __forceinline__ void move_references(float* scratch, float* negm, int* unset_flag, uint32_t s_at, uint32_t o_at,
@@ -414,8 +431,8 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
         const float old = negm[t];
         if (__float_as_uint(old) == 0u) {
             unset = x == -INFINITY;
-            delta = unset ? 0.0f : x - kAtRef<E4M3>;
-        } else if (x > kAtRef<E4M3>) {
+            delta = unset || (!E4M3 && fabsf(x) <= kLazy<E4M3>) ? 0.0f : x - kAtRef<E4M3>;
+        } else if (x > (E4M3 ? kAtRef<E4M3> : kLazy<E4M3>)) {
             delta = x - kAtRef<E4M3>;
             f = ex2_approx(-delta);
         }
@@ -970,7 +987,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         float l = (scratch[t] + scratch[NT + t]) + (scratch[2 * NT + t] + scratch[3 * NT + t]);
                         if (bad || (anc & info.poison))
                             l = NAN;
-                        fin[t] = l == 0.0f || anc == 0 ? 0.0f : __fdividef(1.0f, l);   // (anc == 0: no node's row)
+                        // (anc == 0: no node's row.  A node's sum is zero only where all its scores are -inf: NaN)
+                        fin[t] = anc == 0 ? 0.0f : __fdividef(1.0f, l);
                         const int at = info.row_out[w * NT + t];
                         if (!whole && at >= 0)
                             reinterpret_cast<float2*>(a.part_ml)[at] = make_float2(-negm[t], l);
@@ -1216,7 +1234,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const AttnLayout L = attn_layout<N, E4M3>(a, smem);
         AttnShared& sh = *L.sh;
         if (warp == 9) {
-            // --- bf16 queries; e4m3 keys (the loading warps of bf16 convert values there) -------
+            // --- bf16 queries; e4m3 keys ----------------------------------------------------
             Run run = run_of(sh);
             uint32_t items = 0;
             bool go = true;
@@ -1508,15 +1526,13 @@ __global__ void __launch_bounds__(256) sv_attention_combine(const __grid_constan
         return;
     const int nn = a.has_n ? __ldg(a.n_nodes + b) : a.Nmax;   // (an item of unusable lengths is never cut)
     __nv_bfloat16* out = a.out + (((long long)b * a.Nmax + node) * a.Hq + h * a.G + head) * D;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = 1.0f / l;   // (zero only where all of a node's scores are -inf: NaN)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
         if (lane + 32 * e < quads) {
-            const float f = node < nn ? inv : 0.0f;
-            const bool zero = f == 0.0f;
             reinterpret_cast<uint2*>(out)[lane + 32 * e] =
-                zero ? make_uint2(0, 0)
-                     : make_uint2(bf16_pair(acc[4 * e] * f, acc[4 * e + 1] * f), bf16_pair(acc[4 * e + 2] * f, acc[4 * e + 3] * f));
+                node < nn ? make_uint2(bf16_pair(acc[4 * e] * inv, acc[4 * e + 1] * inv), bf16_pair(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv))
+                          : make_uint2(0, 0);
         }
 }
 

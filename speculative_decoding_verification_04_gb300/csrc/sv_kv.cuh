@@ -4,9 +4,9 @@
 //
 // All three move each byte once and compute little, so what bounds them is
 // memory bandwidth for many tokens and the chain of dependent loads (length,
-// page, row) for few.  A lane holds 16 elements of a head's row (two 16-byte
-// bf16 vectors), so that both elements of every rotated pair are its own and a
-// row's sums take log2(head_dim / 16) shuffles.
+// page, row) for few.  A lane holds 16 elements of a head's row in two chunks
+// of 8, so that both elements of every rotated pair are its own and a row's
+// sums take log2(head_dim / 16) shuffles.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -235,11 +235,20 @@ __device__ __forceinline__ uint32_t e4m3_quad(const float* x)
     return y;
 }
 
+//   y = x rsqrt(mean(x^2) + eps) w;  (a, c) -> (a cos - c sin, c cos + a sin);
+//   e4m3: scale = max(amax |y| / 448, 2^-100), stored y / scale.
+// One pass: each element is read and written once.  On a GB300, 16411 prompt
+// tokens of 32 + 8 + 8 heads of 128 (bf16) take 82 us a call, 0.75 of the
+// copy rate (61.7 us); issue slots are 66 % busy, DRAM 58 %.  256 trees of 15
+// nodes written to e4m3 take 24 us on the GPU (13.3): too few bytes to hide the
+// lookups' three dependent loads.  8 single tokens take 4 us on the GPU.
+//
 // LPR lanes hold a head's row: 16 elements each, the lanes from D / 16 on none
 // (D = 80, 96, 112 of LPR 8; 144 ... 240 of LPR 16).  A warp holds 32 / LPR
-// rows at a time; the next four times as many (half that in fp32) are on their
-// way while it works, and the first are asked for before the token's place is looked up (which takes three loads
-// that depend on one another).
+// rows at a time; the next are on their way to registers while it works and
+// the two passes after them to L2, and the first are asked for before the
+// token's place is looked up (three loads that depend on one another).  With
+// rows loaded when they are needed the 16411 tokens took 104 us.
 template <typename T, int LPR, bool E4M3>
 __global__ void __launch_bounds__(256, 3) sv_append_kernel(const __grid_constant__ AppendArgs a)
 {
@@ -405,7 +414,9 @@ __global__ void __launch_bounds__(256, 3) sv_append_kernel(const __grid_constant
 }
 
 // ---------------------------------------------------------------------------
-// read
+// read: x scale, rounded once.  Bound by HBM where there is much to read:
+// 100003 rows of 8 heads of 128 from e4m3 to bf16 take 117 us on a GB300, 0.80
+// of the copy rate (93 us).
 // ---------------------------------------------------------------------------
 struct ReadArgs {
     KvCache c;
@@ -524,6 +535,9 @@ __device__ __forceinline__ int commit_moves(const CommitArgs& a, int b, int lane
     return base + 1 + kept;
 }
 
+// Latency bounds it: length, path, pages, then rows, each waiting for the one
+// before.  32 layers of 256 trees take 11 us on a GB300 (the bytes 10.4), two
+// layers of four 4 us.
 // One block per (sequence, layer).  A thread takes one 16-byte column of a
 // head's rows through all moves in order: path[i] > i strictly ascends, so a
 // move writes only rows that no later move reads.

@@ -122,6 +122,26 @@ def test_scores_far_from_zero(dev, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("ctx", [[0], [300], [40000]])
+def test_a_row_of_infinite_scores_is_nan(dev, ctx, fmt):
+    """All scores -inf: the softmax of that is NaN, whether one block has the
+    row or several do; the other rows are as without it."""
+    q, cache, nodes, parents = make(ctx, 3, "star", 4, 2, 64, fmt, 16, dev, seed=23)
+    page, slot = cache.at(0, range(ctx[0] + 3))
+    if fmt == "bf16":
+        cache.k[page, :, slot, 0] = -1.0
+    else:
+        cache.k.view(torch.uint8)[page, :, slot, 0] = 0xb8   # -1.0
+    q[0, 1, 2, 0] = float("inf")
+    got = call(q, cache, ctx, nodes, parents, dev)
+    assert torch.isnan(got[0, 1, 2]).all()
+    q[0, 1, 2, 0] = 0.0
+    want = call(q, cache, ctx, nodes, parents, dev)
+    want[0, 1, 2] = got[0, 1, 2] = 0.0
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_every_length_around_a_tile(dev, fmt):
     """Lengths 0 ... 159 of one batch: the context ends at every slot of a page
     and of a 128-position tile, and the tree straddles tiles."""
