@@ -530,9 +530,8 @@ sv_status spec_kv_append(const sv_kv_cache* cache, const sv_kv_tokens* tokens, c
  * bf16 (fp32 is SV_ERR_UNSUPPORTED).  Products accumulate in fp32, softmax
  * statistics are fp32; for the second product weights are rounded to bf16, or
  * with SV_KV_E4M3 weights times value scales to fp16.  An e4m3 cache's first
- * product takes each query element to 2^-25 of the largest finite one among
- * the rows that a block works on together (nodes of one sequence and query
- * heads of one key head).
+ * product takes each query element to 2^-17 or less of the largest finite one
+ * in its row, beside whatever other rows hold.
  * What is not finite: a query row, or a key or value scale that a row sees,
  * makes that row NaN, and so does a node's value that it sees (ancestors and
  * itself); rows that do not see the node are as without it.  The context is

@@ -23,8 +23,9 @@
 //
 // An e4m3 cache's keys go to the tensor core as they are: each query element
 // is split into an e4m3 and two e5m2 terms, which hold a bf16's eight bits
-// exactly (to 2^-25 of the row group's largest element), and the three
-// products add up in the same accumulator.  Its values become fp16 in shared
+// exactly (to 2^-25 of the largest element that it is scaled with: the row
+// group's, or the row's own where magnitudes spread by 2^8 or more), and the
+// three products add up in the same accumulator.  Its values become fp16 in shared
 // memory (one instruction a pair; 8-bit weights would need three terms and
 // more range); their scales join the scores' exponents, so that weight times
 // scale is what fp16 holds.
@@ -43,9 +44,9 @@
 // Measured on a GB300, a call (8 key heads of 128, 32 query heads):
 //  * 256 trees of 15 nodes over 100-1500 positions, bf16, pages of 16: 171 us,
 //    0.82 of the copy rate; HBM bounds it (914 MB read, nothing twice).
-//  * 64 chains of 9 over 200-3000 positions, e4m3: 102 us (bytes 34 us); what a
+//  * 64 chains of 9 over 200-3000 positions, e4m3: 100-110 us (bytes 34 us); what a
 //    tile takes from its load over conversion, products and softmax.
-//  * 2 x 32 nodes over 100-120 thousand positions, e4m3: 202 us, 600 TFLOP/s;
+//  * 2 x 32 nodes over 100-120 thousand positions, e4m3: 200 us, 610 TFLOP/s;
 //    tensor pipe 36 % and issue slots 41 % busy.
 //  * one token over 700 positions: 11.5 us on the GPU, latency.
 //
@@ -205,7 +206,10 @@ struct AttnShared {
     int b, h, g, tile, active;
     SeqLens first;                                 // the first sequence's lengths
     int unset[2];
-    float top[4];
+    uint32_t top[4], low[4];
+    uint32_t row_top[128];
+    int q_spread[4];                               // by item: the rows have powers of two of their own,
+    alignas(16) float q_row[4][128];               // these, over their group's
     float q_unscale[4];                            // undoes the queries' power of two (e4m3), by item: the first
                                                    // product runs at most two ahead of the softmax
     alignas(16) float negm[128];                   // minus the rows' references
@@ -458,6 +462,24 @@ __device__ __forceinline__ void move_references(float* scratch, float* negm, int
                 o[k] *= scratch[c + k];
             tmem_st8(o_at + i * o_pitch + c, o);
         }
+    tmem_wait_st();
+}
+
+// A thread's scores brought to one scale, where they are: for the rare items
+// whose queries spread widely.
+template <int NT>
+__device__ __forceinline__ void scale_rows(uint32_t s_at, const float* by)
+{
+#pragma unroll 1
+    for (int c = 0; c < NT; c += 8) {
+        float s[8];
+        tmem_ld8(s_at + c, s);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            s[k] *= by[c + k];
+        tmem_st8(s_at + c, s);
+    }
     tmem_wait_st();
 }
 
@@ -848,6 +870,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
                         tc_fence_after();
                         const uint32_t s_at = tmem + (gt & 1) * N;
+                        if (E4M3 && sh.q_spread[items & 3])
+                            scale_rows<NT>(s_at, sh.q_row[items & 3] + w * NT);
                         float s[NT];
 #pragma unroll
                         for (int i = 0; i < NT / 16; ++i)
@@ -1096,40 +1120,77 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             constexpr int kRows = NT >= 64 ? 4 : 8;
             const int turn = kRows * stride;
             uint4 y[kRows];
+            unsigned have = 0;   // which of them are queries
             auto load_q = [&](int row) {
+                have = 0;
                 int n = row / a.heads, head = row - n * a.heads;
 #pragma unroll
                 for (int k = 0; k < kRows; ++k) {
-                    y[k] = n < live && head < heads && row0 < stride ? __ldg(q + n * (a.q_stride / 8) + head * per) : make_uint4(0, 0, 0, 0);
+                    const bool real = n < live && head < heads && row0 < stride;
+                    y[k] = real ? __ldg(q + n * (a.q_stride / 8) + head * per) : make_uint4(0, 0, 0, 0);
+                    have |= (unsigned)real << k;
                     for (head += stride; head >= a.heads; head -= a.heads)
                         ++n;
                 }
             };
-            // a power of two that brings the group's largest element to [128, 256)
-            uint32_t m = 0;   // (magnitudes order as integers; what is not finite does not count)
+            // the largest magnitude of eight elements (magnitudes order as integers; what is not finite does not count)
+            auto largest = [](uint4 x) {
+                const uint32_t z[4] = {x.x, x.y, x.z, x.w};
+                uint32_t m = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t lo = (z[e] << 16) & 0x7fff0000u, hi = z[e] & 0x7fff0000u;
+                    m = max(m, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
+                }
+                return m;
+            };
+            // the exponent of the power of two that brings it to [128, 256)
+            auto raise = [](uint32_t m) { return m ? min(max(261 - (int)(m >> 23), 1), 253) : 127; };
+            uint32_t top = 0, low = ~0u;
 #pragma unroll 1
             for (int row = row0; row < a.rows; row += turn) {
                 load_q(row);
 #pragma unroll
                 for (int k = 0; k < kRows; ++k) {
-                    const uint32_t z[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t lo = (z[e] << 16) & 0x7fff0000u, hi = z[e] & 0x7fff0000u;
-                        m = max(m, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
-                    }
+                    const uint32_t m = largest(y[k]);
+                    top = max(top, m);
+                    low = (have >> k) & 1 ? min(low, m) : low;
                 }
             }
-            float top = warp_redux_max(__uint_as_float(m));
-            if (lane == 0)
+            top = __reduce_max_sync(kFull, top);
+            low = __reduce_min_sync(kFull, low);
+            if (lane == 0) {
                 sh.top[warp & 3] = top;
+                sh.low[warp & 3] = low;
+            }
             bar_sync(3, 128);
-            top = fmaxf(fmaxf(sh.top[0], sh.top[1]), fmaxf(sh.top[2], sh.top[3]));
-            const int e = top > 0.0f ? min(max(261 - (int)(__float_as_uint(top) >> 23), 1), 253) : 127;
-            const float scale = __uint_as_float((uint32_t)e << 23);
+            top = max(max(sh.top[0], sh.top[1]), max(sh.top[2], sh.top[3]));
+            low = min(min(sh.low[0], sh.low[1]), min(sh.low[2], sh.low[3]));
+            // One power of two for the group; where some eight elements lie 2^8 below its largest (which ordinary
+            // queries do not) one for each row, as the terms hold 2^-25 of the largest element that they share it with.
+            const int e = raise(top);
+            const bool spread = top > (8u << 23) && low < top - (8u << 23);
+            if (spread) {
+                sh.row_top[t] = 0;
+                bar_sync(3, 128);
+#pragma unroll 1
+                for (int row = row0; row < a.rows; row += turn) {
+                    load_q(row);
+#pragma unroll
+                    for (int k = 0; k < kRows; ++k)
+                        if ((have >> k) & 1)
+                            atomicMax(&sh.row_top[row + k * stride], largest(y[k]));
+                }
+                bar_sync(3, 128);
+            }
+            auto row_exponent = [&](int row) { return sh.row_top[row] ? min(raise(sh.row_top[row]), e + 126) : e; };
             cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
-            if (t == 0)
+            if (t == 0) {
                 sh.q_unscale[items & 3] = __uint_as_float((uint32_t)(254 - e) << 23);
+                sh.q_spread[items & 3] = spread;
+            }
+            if (spread)
+                sh.q_row[items & 3][t] = __uint_as_float((uint32_t)(127 + e - row_exponent(t)) << 23);
 #pragma unroll 1
             for (int row = row0; row < a.rows; row += turn) {
                 if (a.rows > turn)
@@ -1139,6 +1200,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int at = row + k * stride;
                     if (at >= a.rows || row0 >= stride)
                         break;
+                    const float scale = __uint_as_float((uint32_t)(spread ? row_exponent(at) : e) << 23);
                     float z[8];
                     Elem<__nv_bfloat16>::unpack(y[0], z);
                     uint32_t p[3][4];

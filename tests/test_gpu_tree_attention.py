@@ -121,6 +121,33 @@ def test_scores_far_from_zero(dev, fmt):
     check(call(q, cache, ctx, nodes, parents, dev), q, cache, ctx, nodes, parents)
 
 
+SPREAD = [([700, 0], 3, 8, 2, 64), ([9000], 32, 32, 8, 128), ([130, 1], 7, 20, 4, 80), ([1000], 5, 16, 2, 192), ([257], 1, 70, 1, 256)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", SPREAD, ids=lambda c: f"n{c[1]}h{c[2]}x{c[3]}d{c[4]}")
+def test_rows_of_different_magnitudes(dev, case, fmt):
+    """A row keeps its precision beside rows that are up to 2^46 larger, and
+    beside rows of zeros."""
+    ctx, N, Hq, Hkv, D = case
+    q, cache, nodes, parents = make(ctx, N, "random", Hq, Hkv, D, fmt, 16, dev, seed=24)
+    gen = torch.Generator(device=dev).manual_seed(25)
+    e = torch.randint(-40, 7, q.shape[:3], generator=gen, device=dev)
+    q = (q.float() * torch.exp2(e.float())[..., None] * (e % 5 != 0)[..., None]).to(torch.bfloat16)
+    check(call(q, cache, ctx, nodes, parents, dev), q, cache, ctx, nodes, parents)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", SPREAD, ids=lambda c: f"n{c[1]}h{c[2]}x{c[3]}d{c[4]}")
+def test_ordinary_rows_beside_huge_ones(dev, case, fmt):
+    ctx, N, Hq, Hkv, D = case
+    q, cache, nodes, parents = make(ctx, N, "random", Hq, Hkv, D, fmt, 16, dev, seed=26)
+    gen = torch.Generator(device=dev).manual_seed(27)
+    e = torch.tensor([-3, 0, 2, 30, 60], device=dev)[torch.randint(0, 5, q.shape[:3], generator=gen, device=dev)]
+    q = (q.float() * torch.exp2(e.float())[..., None]).to(torch.bfloat16)
+    check(call(q, cache, ctx, nodes, parents, dev), q, cache, ctx, nodes, parents)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("ctx", [[0], [300], [40000]])
 def test_a_row_of_infinite_scores_is_nan(dev, ctx, fmt):
