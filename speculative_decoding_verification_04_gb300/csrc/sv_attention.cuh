@@ -1120,15 +1120,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             constexpr int kRows = NT >= 64 ? 4 : 8;
             const int turn = kRows * stride;
             uint4 y[kRows];
-            unsigned have = 0;   // which of them are queries
             auto load_q = [&](int row) {
-                have = 0;
                 int n = row / a.heads, head = row - n * a.heads;
 #pragma unroll
                 for (int k = 0; k < kRows; ++k) {
-                    const bool real = n < live && head < heads && row0 < stride;
-                    y[k] = real ? __ldg(q + n * (a.q_stride / 8) + head * per) : make_uint4(0, 0, 0, 0);
-                    have |= (unsigned)real << k;
+                    y[k] = n < live && head < heads && row0 < stride ? __ldg(q + n * (a.q_stride / 8) + head * per) : make_uint4(0, 0, 0, 0);
                     for (head += stride; head >= a.heads; head -= a.heads)
                         ++n;
                 }
@@ -1146,43 +1142,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             };
             // the exponent of the power of two that brings it to [128, 256)
             auto raise = [](uint32_t m) { return m ? min(max(261 - (int)(m >> 23), 1), 253) : 127; };
-            uint32_t top = 0, low = ~0u;
-#pragma unroll 1
-            for (int row = row0; row < a.rows; row += turn) {
-                load_q(row);
-#pragma unroll
-                for (int k = 0; k < kRows; ++k) {
-                    const uint32_t m = largest(y[k]);
-                    top = max(top, m);
-                    low = (have >> k) & 1 ? min(low, m) : low;
-                }
-            }
-            top = __reduce_max_sync(kFull, top);
-            low = __reduce_min_sync(kFull, low);
-            if (lane == 0) {
-                sh.top[warp & 3] = top;
-                sh.low[warp & 3] = low;
-            }
-            bar_sync(3, 128);
-            top = max(max(sh.top[0], sh.top[1]), max(sh.top[2], sh.top[3]));
-            low = min(min(sh.low[0], sh.low[1]), min(sh.low[2], sh.low[3]));
             // One power of two for the group; where some eight elements lie 2^8 below its largest (which ordinary
             // queries do not) one for each row, as the terms hold 2^-25 of the largest element that they share it with.
-            const int e = raise(top);
-            const bool spread = top > (8u << 23) && low < top - (8u << 23);
-            if (spread) {
-                sh.row_top[t] = 0;
-                bar_sync(3, 128);
+            uint32_t top = 0, low = ~0u;
+            bool spread = false;
+#pragma unroll 1
+            for (;;) {   // (a second pass where spread: one place in the code for both)
 #pragma unroll 1
                 for (int row = row0; row < a.rows; row += turn) {
                     load_q(row);
 #pragma unroll
-                    for (int k = 0; k < kRows; ++k)
-                        if ((have >> k) & 1)
-                            atomicMax(&sh.row_top[row + k * stride], largest(y[k]));
+                    for (int k = 0; k < kRows; ++k) {
+                        const uint32_t m = largest(y[k]);
+                        top = max(top, m);
+                        low = min(low, m - 1u);   // (zeros do not count)
+                        if (spread && m)          // (zeros where there is no query)
+                            atomicMax(&sh.row_top[row + k * stride], m);
+                    }
                 }
+                if (spread)
+                    break;
+                top = __reduce_max_sync(kFull, top);
+                low = __reduce_min_sync(kFull, low);
+                if (lane == 0) {
+                    sh.top[warp & 3] = top;
+                    sh.low[warp & 3] = low;
+                }
+                sh.row_top[t] = 0;
                 bar_sync(3, 128);
+                top = max(max(sh.top[0], sh.top[1]), max(sh.top[2], sh.top[3]));
+                low = min(min(sh.low[0], sh.low[1]), min(sh.low[2], sh.low[3]));
+                spread = top > (8u << 23) && low < top - (8u << 23);
+                if (!spread)
+                    break;
             }
+            if (spread)
+                bar_sync(3, 128);
+            const int e = raise(top);
+            const float group_scale = __uint_as_float((uint32_t)e << 23);
             auto row_exponent = [&](int row) { return sh.row_top[row] ? min(raise(sh.row_top[row]), e + 126) : e; };
             cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
             if (t == 0) {
@@ -1200,7 +1197,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int at = row + k * stride;
                     if (at >= a.rows || row0 >= stride)
                         break;
-                    const float scale = __uint_as_float((uint32_t)(spread ? row_exponent(at) : e) << 23);
+                    float scale = group_scale;
+                    if (spread)
+                        scale = __uint_as_float((uint32_t)row_exponent(at) << 23);
                     float z[8];
                     Elem<__nv_bfloat16>::unpack(y[0], z);
                     uint32_t p[3][4];
