@@ -190,7 +190,7 @@ struct Tiles {
 struct alignas(16) ItemInfo {
     unsigned anc[128];     // the rows' ancestor bits (0: no row)
     int row_out[128];      // where their results go (-1: nowhere)
-    unsigned poison;       // nodes whose values are not finite
+    unsigned poison;       // nodes whose values are not finite (or have a negative scale)
     unsigned bad;          // malformed tree, unusable page
 };
 
@@ -640,8 +640,11 @@ __device__ __forceinline__ bool prepare_item(const AttnArgs& a, AttnShared& sh, 
             if (page >= 0)
                 row = kv_row(a.c, page, ctx + lane) + ((long long)h << a.c.page_shift);
         }
-        if (E4M3 && row >= 0 && !isfinite(a.c.v_scale[row]))
-            poison = 1u << lane;
+        if (E4M3 && row >= 0) {   // a negative scale reads as NaN
+            const float s = a.c.v_scale[row];
+            if (!(s >= 0.0f && s < INFINITY))
+                poison = 1u << lane;
+        }
         if (row >= 0) {   // a lane reads its node's row, eight pieces in flight
             const uint4* x = reinterpret_cast<const uint4*>(a.c.v + row * bytes);
             bool hit = false;
