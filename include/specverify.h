@@ -549,6 +549,25 @@ sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, c
                               cudaStream_t stream);
 
 /*
+ * spec_tree_attention_ex -- the same.  expire_waits: testing only; 0 in normal
+ * use.  Its bits, from the lowest, name what the waits inside a block wait
+ * for: queries there / their place free, a slot of keys there / free, of
+ * values there / free, of converted values there / free, what an item's rows
+ * need there / its place free, scores there / their place free, weights there,
+ * sums there.  A barrier of a kind whose bit is set lacks one arrival, so that
+ * waits for it run out, after 2^14 polls.  This exercises the timeout path: the
+ * rows concerned are NaN, bit 0 of `errors` is set, and the copies and products
+ * under way are waited for, with the normal bound, before a block ends.
+ * Nothing faults or hangs; the next call is unaffected.
+ */
+#define SV_ATTENTION_WAITS 14
+sv_status spec_tree_attention_ex(const sv_kv_cache* cache, const int32_t* kv_len, const int32_t* n_nodes,
+                                 const int32_t* parent, const void* q, int64_t q_stride, sv_dtype dtype,
+                                 int32_t n_heads, int32_t B, int32_t Nmax, float scale, void* out,
+                                 uint32_t* errors, void* workspace, size_t workspace_bytes,
+                                 uint32_t expire_waits, cudaStream_t stream);
+
+/*
  * spec_kv_commit -- after spec_verify_tree: in every layer the entries of the
  * kept nodes out_path[b][0 .. out_len[b] - 1] (out_path [B][Nmax], as
  * spec_verify_tree writes it) move to the positions kv_len[b] + 1, + 2, ...

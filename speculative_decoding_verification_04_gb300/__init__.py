@@ -471,7 +471,7 @@ def sv_workspace_errors(workspace: Workspace, stream=None) -> int:
 # the key/value cache (kv_cache.py imports torch, so it is loaded on first use)
 # ---------------------------------------------------------------------------
 _KV_NAMES = ("spec_kv_append", "spec_tree_attention", "spec_kv_commit", "spec_kv_read",
-             "sv_attention_workspace_size", "SVKvCache", "SVKvTokens", "SV_KV_BF16", "SV_KV_E4M3")
+             "sv_attention_workspace_size", "SVKvCache", "SVKvTokens", "SV_KV_BF16", "SV_KV_E4M3", "SV_ATTENTION_WAITS")
 
 
 def __getattr__(name):

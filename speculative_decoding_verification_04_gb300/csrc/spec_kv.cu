@@ -327,11 +327,21 @@ sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, c
                               int32_t n_heads, int32_t B, int32_t Nmax, float scale, void* out,
                               uint32_t* errors, void* workspace, size_t workspace_bytes, cudaStream_t stream)
 {
+    return spec_tree_attention_ex(cache, kv_len, n_nodes, parent, q, q_stride, dtype, n_heads, B, Nmax, scale, out, errors,
+                                  workspace, workspace_bytes, 0, stream);
+}
+
+sv_status spec_tree_attention_ex(const sv_kv_cache* cache, const int32_t* kv_len, const int32_t* n_nodes,
+                                 const int32_t* parent, const void* q, int64_t q_stride, sv_dtype dtype,
+                                 int32_t n_heads, int32_t B, int32_t Nmax, float scale, void* out,
+                                 uint32_t* errors, void* workspace, size_t workspace_bytes, uint32_t expire_waits,
+                                 cudaStream_t stream)
+{
     sv::AttnArgs a{};
     sv_status st = sv::check_cache(cache, B > 0, &a.c);
     if (st != SV_OK)
         return st;
-    if (B < 0 || Nmax < 1 || Nmax > sv::kNodeMax || n_heads < 1 || n_heads % cache->n_kv_heads ||
+    if (B < 0 || Nmax < 1 || Nmax > sv::kNodeMax || n_heads < 1 || n_heads % cache->n_kv_heads || expire_waits >> sv::kAttnWaits ||
         (dtype != SV_DTYPE_F32 && dtype != SV_DTYPE_BF16) || !(scale > -3e38f && scale < 3e38f))
         return SV_ERR_INVALID_ARG;
     if (dtype != SV_DTYPE_BF16)
@@ -361,6 +371,8 @@ sv_status spec_tree_attention(const sv_kv_cache* cache, const int32_t* kv_len, c
     a.B = B;
     a.Nmax = Nmax;
     a.scale_log2 = scale * 1.44269504088896341f;
+    a.hold = expire_waits;
+    a.limit = expire_waits ? 1u << 14 : sv::kWaitSpins;
     a.G = n_heads / cache->n_kv_heads;
     const bool e4m3 = cache->format == SV_KV_E4M3;
     const sv::RowGroups rg = sv::attention_rows(Nmax, a.G, sv::attn_rows_max(e4m3, cache->head_dim));

@@ -76,6 +76,14 @@ constexpr int kQuarter = kTile / 4;        // positions a loading warp takes car
 // queries would leave the loads no room.
 __host__ __device__ constexpr int attn_rows_max(bool e4m3, int D) { return e4m3 && D > 128 ? 64 : 128; }
 
+// What the waits inside a CTA wait for (there, or free again): queries, slots of
+// keys, values and converted values, what an item's rows need, scores, weights,
+// sums.
+enum AttnWait : int {
+    kQFull, kQEmpty, kKFull, kKEmpty, kVFull, kVEmpty, kCFull, kCEmpty, kInfoFull, kInfoEmpty, kSFull, kSEmpty, kPFull, kOFull, kAttnWaits
+};
+static_assert(kAttnWaits == SV_ATTENTION_WAITS, "the header lists them");
+
 struct AttnArgs {
     KvCache c;
     const __nv_bfloat16* q;
@@ -99,6 +107,8 @@ struct AttnArgs {
     int k_bytes, v_bytes, conv_bytes; // of one slot
     int box_rows;            // rows of one TMA box (a page, or a tile)
     float scale_log2;        // scale * log2(e)
+    uint32_t limit;          // polls before a wait gives up
+    uint32_t hold;           // kinds of barriers (bits) made to lack an arrival
 };
 
 // Row r of group g: its node (of the sequence) and query head (of the key
@@ -200,9 +210,10 @@ struct AttnShared {
     uint64_t cfull[2], cempty[2];                  // converted V slots (e4m3)
     uint64_t q_full, q_empty, info_full[2], info_empty[2];
     uint64_t s_full[2], s_empty[2], p_full, o_full, drain[2];
+    uint32_t fills[2][4];                          // slots of keys (values) that warps 12 .. 15 have asked for (bf16)
     long long t_begin, t_end, sum[16];
     uint32_t tmem;
-    int abort;
+    uint32_t limit;                                // polls a wait may take; zero once one has given up
     int b, h, g, tile, active;
     SeqLens first;                                 // the first sequence's lengths
     int unset[2];
@@ -260,25 +271,28 @@ __device__ __forceinline__ Run run_of(const AttnShared& shared)
     return r;
 }
 
-// A wait that ends: on a timeout every later wait of the CTA gives up too.
-// The warps that own named barriers run on regardless (they all reach the
-// same ones), the others stop.
+// A wait that ends, of a whole warp and alike in all its lanes: on a timeout
+// the CTA's limit becomes zero, so that every later wait gives up too (after a
+// poll that fails).  A warp whose wait gave up issues and arrives at nothing any
+// more: what the others still wait for is there when their waits pass.  The
+// warps that own named barriers run on (they all reach the same ones), the
+// others stop.
 __device__ __forceinline__ bool cta_wait(AttnShared& sh, uint64_t* bar, uint32_t parity)
 {
     const uint32_t addr = smem_addr(bar);
+    volatile uint32_t* const limit = &sh.limit;
     // (never unrolled: the kernel has some forty of these, and its code has to stay in the instruction caches)
 #pragma unroll 1
-    for (uint32_t i = 0; i < kWaitSpins; ++i) {
-        if (mbar_try_wait(addr, parity))
-            return true;
-        if ((i & 15) == 15 && *reinterpret_cast<volatile int*>(&sh.abort))
+    for (uint32_t i = 1; !__all_sync(kFull, mbar_try_wait(addr, parity)); ++i)
+        if (i >= *limit) {   // (one load of the converged warp)
+            *limit = 0;
             return false;
-    }
-    *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-    return false;
+        }
+    return true;
 }
 
-// The last resort's own wait, for copies and products in flight.
+// A role's last wait, for its own copies and products in flight: they land
+// before the CTA's memory is given back, whoever gave up.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity)
 {
     const uint32_t addr = smem_addr(bar);
@@ -307,6 +321,20 @@ struct Ring {
         --slot;
     }
 };
+
+// The last copies into each slot of a ring that has been filled `fills` times,
+// `r` standing at the next.  `held`: the slots' barriers lack an arrival (none
+// has been filled twice then), which one lane makes up for.
+__device__ __forceinline__ void drain_ring(uint64_t* full, Ring r, int slots, uint32_t fills, bool held)
+{
+#pragma unroll 1
+    for (uint32_t n = min(fills, (uint32_t)slots); n > 0; --n) {
+        r.back(slots);
+        if (held)
+            mbar_arrive(smem_addr(&full[r.slot]));
+        drain_wait(&full[r.slot], r.phase);
+    }
+}
 
 // Four e4m3 values as fp16, exactly (NaN as NaN).
 __device__ __forceinline__ uint2 e4m3_to_f16(uint32_t w)
@@ -711,29 +739,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (warp == 8) {
             tmem_alloc(smem_addr(&sh.tmem), 512);
         } else if (tid == 9 * 32) {
-            sh.abort = 0;
+            sh.limit = a.limit;
+            auto init = [&](uint64_t& bar, int count, int kind) { mbar_init(smem_addr(&bar), count + ((a.hold >> kind) & 1)); };
 #pragma unroll 1
             for (int i = 0; i < a.kslots; ++i) {
-                mbar_init(smem_addr(&sh.kfull[i]), E4M3 ? 1 : 4);
-                mbar_init(smem_addr(&sh.kempty[i]), 1);
+                init(sh.kfull[i], E4M3 ? 1 : 4, kKFull);
+                init(sh.kempty[i], 1, kKEmpty);
             }
 #pragma unroll 1
             for (int i = 0; i < a.vslots; ++i) {
-                mbar_init(smem_addr(&sh.vfull[i]), E4M3 ? 1 : 4);
-                mbar_init(smem_addr(&sh.vempty[i]), E4M3 ? 4 : 1);
+                init(sh.vfull[i], E4M3 ? 1 : 4, kVFull);
+                init(sh.vempty[i], E4M3 ? 4 : 1, kVEmpty);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(smem_addr(&sh.cfull[i]), 4);
-                mbar_init(smem_addr(&sh.cempty[i]), 1);
-                mbar_init(smem_addr(&sh.s_full[i]), 1);
-                mbar_init(smem_addr(&sh.s_empty[i]), 4 * NWG);
-                mbar_init(smem_addr(&sh.info_full[i]), 1);
-                mbar_init(smem_addr(&sh.info_empty[i]), 4 * NWG);
+                init(sh.cfull[i], 4, kCFull);
+                init(sh.cempty[i], 1, kCEmpty);
+                init(sh.s_full[i], 1, kSFull);
+                init(sh.s_empty[i], 4 * NWG, kSEmpty);
+                init(sh.info_full[i], 1, kInfoFull);
+                init(sh.info_empty[i], 4 * NWG, kInfoEmpty);
             }
-            mbar_init(smem_addr(&sh.q_full), 1);
-            mbar_init(smem_addr(&sh.q_empty), 1);
-            mbar_init(smem_addr(&sh.p_full), 4 * NWG);
-            mbar_init(smem_addr(&sh.o_full), 1);
+            init(sh.q_full, 1, kQFull);
+            init(sh.q_empty, 1, kQEmpty);
+            init(sh.p_full, 4 * NWG, kPFull);
+            init(sh.o_full, 1, kOFull);
             mbar_init(smem_addr(&sh.drain[0]), 1);
             mbar_init(smem_addr(&sh.drain[1]), 1);
             fence_mbar_init();
@@ -830,6 +859,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             float* const scratch = sh.scratch[w];
             float* const negm = sh.negm + w * NT;
             uint32_t gt = 0, items = 0;   // tiles, items so far
+            constexpr uint32_t kGaveUp = 1u << 31;   // in gt: a wait of this warp gave up (a flag of its own is a spill)
             while (run.next(a, true)) {
                 const int ctx = run.s.ctx, nn = run.s.nn, h = run.h;
                 const int part = 2 * blockIdx.x + (run.t0 > 0 ? 0 : 1);
@@ -870,7 +900,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
                     for (int j = run.t0; j < run.t1; ++j, ++gt) {
                         const bool first_tile = j == run.t0;
-                        cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1);
+                        if (!cta_wait(sh, &sh.s_full[gt & 1], (gt >> 1) & 1))
+                            gt |= kGaveUp;
                         tc_fence_after();
                         const uint32_t s_at = tmem + (gt & 1) * N;
                         if (E4M3 && sh.q_spread[items & 3])
@@ -907,7 +938,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         // who sees this position: every row in the context, a node's descendants behind it
                         unsigned long long seen = ~0ull;
                         if ((j + 1) * kTile > ctx) {   // the tile holds nodes, or ends the sequence
-                            cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
+                            if (!cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1))
+                                gt |= kGaveUp;
                             const unsigned poison = info.poison;
                             const int m = j * kTile + t - ctx;
                             if (m >= 0) {
@@ -948,7 +980,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             if (!move && t < NT)
                                 negm[t] = -0.0f;   // (+0 marks a row without a reference)
                         } else {   // the previous tile's product is done with P (and O)
-                            cta_wait(sh, &sh.o_full, (gt - 1) & 1);
+                            if (!cta_wait(sh, &sh.o_full, (gt - 1) & 1))
+                                gt |= kGaveUp;
                             tc_fence_after();
                         }
                         if (move) {
@@ -970,7 +1003,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         tc_fence_before();
                         fence_proxy_async();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (lane == 0 && gt < kGaveUp) {
                             mbar_arrive(smem_addr(&sh.s_empty[gt & 1]));
                             mbar_arrive(smem_addr(&sh.p_full));
                         }
@@ -1004,8 +1037,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     float* const fin = scratch + 4 * NT;
                     // (after a wait that gave up nothing of the item can be relied on)
-                    cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1);
-                    const bool abort = bar_any(bar, 128, *reinterpret_cast<volatile int*>(&sh.abort) != 0), bad = abort || info.bad;
+                    if (!cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1))
+                        gt |= kGaveUp;
+                    const bool abort = bar_any(bar, 128, *reinterpret_cast<volatile uint32_t*>(&sh.limit) == 0), bad = abort || info.bad;
                     if (tid == 0 && bad && a.has_err)
                         atomicOr(a.err, abort ? kErrWaitTimeout : kErrCache);
                     lost |= abort;
@@ -1020,7 +1054,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (!whole && at >= 0)
                             reinterpret_cast<float2*>(a.part_ml)[at] = make_float2(-negm[t], l);
                     }
-                    cta_wait(sh, &sh.o_full, (gt - 1) & 1);
+                    if (!cta_wait(sh, &sh.o_full, (gt - 1) & 1))
+                        gt |= kGaveUp;
                     tc_fence_after();
                     bar_sync(bar, 128);
 #pragma unroll 1
@@ -1036,7 +1071,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     tc_fence_before();
                     bar_sync(bar, 128);   // O, the scratch and the item's rows have been read
-                    if (lane == 0)
+                    if (lane == 0 && gt < kGaveUp)
                         mbar_arrive(smem_addr(&sh.info_empty[items & 1]));
                     ++items;
                 }
@@ -1072,7 +1107,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         k.start(a, run_of(sh));
         v = k;
         Ring rk, rv;
-        int nk = 0, nv = 0;   // slots that may still be filling
+        uint32_t fills_k = 0, fills_v = 0;   // slots asked for (bf16)
         Boxes box_k, box_v;
         box_k.ask(a, k, quarter * kQuarter, kQuarter, lane);
         box_v = box_k;
@@ -1086,7 +1121,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     return false;
                 load_boxes<E4M3>(a, smem_addr(L.k) + rk.slot * a.k_bytes + quarter * kQuarter * 128, smem_addr(&sh.kfull[rk.slot]), &map_k, c, now, lane);
                 rk.step(a.kslots);
-                nk = min(nk + 1, a.kslots);
+                ++fills_k;
             }
             return true;
         };
@@ -1101,7 +1136,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 load_boxes<E4M3>(a, smem_addr(L.v) + rv.slot * a.v_bytes + quarter * kQuarter * 128,
                                  smem_addr(&sh.vfull[rv.slot]), &map_v, c, now, lane);
                 rv.step(a.vslots);
-                nv = min(nv + 1, a.vslots);
+                ++fills_v;
             }
             return true;
         };
@@ -1184,7 +1219,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int e = raise(top);
             const float group_scale = __uint_as_float((uint32_t)e << 23);
             auto row_exponent = [&](int row) { return sh.row_top[row] ? min(raise(sh.row_top[row]), e + 126) : e; };
-            cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
+            go = go && cta_wait(sh, &sh.q_empty, (items & 1) ^ 1);
             if (t == 0) {
                 sh.q_unscale[items & 3] = __uint_as_float((uint32_t)(254 - e) << 23);
                 sh.q_spread[items & 3] = spread;
@@ -1192,7 +1227,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (spread)
                 sh.q_row[items & 3][t] = __uint_as_float((uint32_t)(127 + e - row_exponent(t)) << 23);
 #pragma unroll 1
-            for (int row = row0; row < a.rows; row += turn) {
+            for (int row = row0; go && row < a.rows; row += turn) {
                 if (a.rows > turn)
                     load_q(row);
 #pragma unroll 1
@@ -1219,8 +1254,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             fence_proxy_async();
-            bar_sync(3, 128);   // (also: sh.top may be written again)
-            if (t == 0)
+            go = !bar_any(3, 128, !go);   // (also: sh.top may be written again)
+            if (t == 0 && go)
                 mbar_arrive(smem_addr(&sh.q_full));
             ++items;
         };
@@ -1271,7 +1306,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0) {
+                    if (lane == 0 && go) {
                         mbar_arrive(smem_addr(&sh.vempty[r.slot]));
                         mbar_arrive(smem_addr(&sh.cfull[w.slot]));
                     }
@@ -1283,15 +1318,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!E4M3 && go && v.more && g >= -v_ahead)
                 go = load_v();
         }
-        if (!go) {   // copies in flight land before the CTA's memory is given back
-            for (; nk > 0; --nk) {
-                rk.back(a.kslots);
-                drain_wait(&sh.kfull[rk.slot], rk.phase);
+        if (!E4M3) {
+            // A warp that gave up before the others has not arrived for slots whose copies they have on their way: it
+            // does so now, with no bytes of its own (a warp is behind by at most the ring, so these are the slots'
+            // current phases), and all wait for the last copies of each slot.
+            if (lane == 0) {
+                sh.fills[0][quarter] = fills_k;
+                sh.fills[1][quarter] = fills_v;
             }
-            for (; nv > 0; --nv) {
-                rv.back(a.vslots);
-                drain_wait(&sh.vfull[rv.slot], rv.phase);
-            }
+            bar_sync(3, 128);
+            const uint32_t most_k = max(max(sh.fills[0][0], sh.fills[0][1]), max(sh.fills[0][2], sh.fills[0][3]));
+            const uint32_t most_v = max(max(sh.fills[1][0], sh.fills[1][1]), max(sh.fills[1][2], sh.fills[1][3]));
+#pragma unroll 1
+            for (; fills_k < most_k; ++fills_k, rk.step(a.kslots))
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sh.kfull[rk.slot]));
+#pragma unroll 1
+            for (; fills_v < most_v; ++fills_v, rv.step(a.vslots))
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sh.vfull[rv.slot]));
+            drain_ring(sh.kfull, rk, a.kslots, fills_k, t == 0 && ((a.hold >> kKFull) & 1));
+            drain_ring(sh.vfull, rv, a.vslots, fills_v, t == 0 && ((a.hold >> kVFull) & 1));
         }
     } else {
         regs_shrink<kRegsIssue<NT>>();
@@ -1318,13 +1365,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 __syncwarp();
             }
-            if (!go && items)   // a copy in flight lands before the CTA's memory is given back
+            if (items) {
+                if (lane == 0 && ((a.hold >> kQFull) & 1))
+                    mbar_arrive(smem_addr(&sh.q_full));
                 drain_wait(&sh.q_full, (items - 1) & 1);
+            }
             if (E4M3) {
                 Tiles k;
                 Ring rk;
                 Boxes box;
-                int nk = 0;
+                uint32_t fills = 0;
                 k.start(a, run);
                 box.ask(a, k, 0, kTile, lane);
 #pragma unroll 1
@@ -1339,13 +1389,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             break;
                         load_boxes<E4M3>(a, smem_addr(L.k) + rk.slot * a.k_bytes, smem_addr(&sh.kfull[rk.slot]), &map_k, c, now, lane);
                         rk.step(a.kslots);
-                        nk = min(nk + 1, a.kslots);
+                        ++fills;
                     }
                 }
-                for (; !go && nk > 0; --nk) {
-                    rk.back(a.kslots);
-                    drain_wait(&sh.kfull[rk.slot], rk.phase);
-                }
+                drain_ring(sh.kfull, rk, a.kslots, fills, lane == 0 && ((a.hold >> kKFull) & 1));
             }
         } else if (warp == 8) {
             // --- first product -----------------------------------------------------------
@@ -1353,7 +1400,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             Ring rk;
             uint32_t g = 0, items = 0;   // tiles, items so far
             Tiles k;
-            bool go = true;
+            bool go = true, issued = false;
             for (k.start(a, run_of(sh)); k.more; k.step(a), ++g) {
                 if (k.j == k.run.t0)
                     go = cta_wait(sh, &sh.q_full, items++ & 1);
@@ -1376,12 +1423,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         }
                     }
                     __syncwarp();
+                    issued = true;
                     rk.step(a.kslots);
                 }
                 if (!go)
                     break;
             }
-            if (!go) {   // products in flight end before TMEM is given back
+            if (issued) {   // products in flight end before the CTA's memory is given back
                 if (lane == 0)
                     tc_commit(smem_addr(&sh.drain[0]));
                 __syncwarp();
@@ -1398,6 +1446,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             uint32_t g = 0, items = 0;
             Tiles v;
             bool go = true;
+            bool issued = false;
             for (v.start(a, run_of(sh)); v.more; ++g) {
                 const int valid = v.valid(), ksteps = (valid + 15) / 16;
                 const bool tail = (v.j + 1) * kTile > v.run.s.ctx;
@@ -1445,6 +1494,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         tc_commit(smem_addr(&empty[rv.slot]));
                     }
                     __syncwarp();
+                    issued = true;
                     rv.step(ring);
                 }
                 if (!go)
@@ -1453,7 +1503,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     ++items;
                 v.step(a);
             }
-            if (!go) {
+            if (issued) {
                 if (lane == 0)
                     tc_commit(smem_addr(&sh.drain[1]));
                 __syncwarp();
@@ -1466,7 +1516,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             Tiles v;
             Ring rv;
             Boxes box;
-            int nv = 0;
+            uint32_t fills = 0;
             v.start(a, run);
             if (E4M3)
                 box.ask(a, v, 0, kTile, lane);
@@ -1488,7 +1538,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             break;
                         load_boxes<E4M3>(a, smem_addr(L.v) + rv.slot * a.v_bytes, smem_addr(&sh.vfull[rv.slot]), &map_v, c, now, lane);
                         rv.step(a.vslots);
-                        nv = min(nv + 1, a.vslots);
+                        ++fills;
                     }
                 }
                 if (go && (owed > 0 || !E4M3) && run.next(a)) {
@@ -1497,10 +1547,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     --owed;
                 }
             }
-            for (; !go && nv > 0; --nv) {   // copies in flight land before the CTA's memory is given back
-                rv.back(a.vslots);
-                drain_wait(&sh.vfull[rv.slot], rv.phase);
-            }
+            drain_ring(sh.vfull, rv, a.vslots, fills, lane == 0 && ((a.hold >> kVFull) & 1));
         }
     }
     pdl_launch_dependents();

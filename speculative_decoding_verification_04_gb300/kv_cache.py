@@ -29,6 +29,7 @@ from . import SV_DTYPE_BF16, SV_DTYPE_F32, _check, _load
 
 SV_KV_BF16 = 0
 SV_KV_E4M3 = 1
+SV_ATTENTION_WAITS = 14
 
 _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
@@ -66,9 +67,11 @@ def _library():
         lib.spec_kv_append.argtypes = [_P, _P, _P, _P, _P]
         lib.spec_tree_attention.argtypes = [_P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32,
                                             ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]
+        lib.spec_tree_attention_ex.argtypes = [*lib.spec_tree_attention.argtypes[:-1], ctypes.c_uint32, _P]
         lib.spec_kv_commit.argtypes = [_P, _P, _P, _P, _I32, _I32, _P, _P, _P]
         lib.spec_kv_read.argtypes = [_P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P]
-        for f in (lib.spec_kv_append, lib.spec_tree_attention, lib.spec_kv_commit, lib.spec_kv_read):
+        for f in (lib.spec_kv_append, lib.spec_tree_attention, lib.spec_tree_attention_ex, lib.spec_kv_commit,
+                  lib.spec_kv_read):
             f.restype = ctypes.c_int
         lib.sv_attention_workspace_size.argtypes = [_I32, _I32, _I32, _I32]
         lib.sv_attention_workspace_size.restype = ctypes.c_size_t
@@ -243,13 +246,16 @@ def sv_attention_workspace_size(Nmax: int, n_heads: int, n_kv_heads: int, head_d
 
 
 def spec_tree_attention(q, k_cache, v_cache, page_table, kv_len, n_nodes=None, parent=None, scale=None,
-                        k_scale=None, v_scale=None, out=None, workspace=None, errors=None, stream=None):
+                        k_scale=None, v_scale=None, out=None, workspace=None, errors=None, stream=None,
+                        expire_waits=0):
     """Attention of each sequence's tree nodes, q [B, Nmax, n_heads, head_dim]
     (bfloat16; tokens may be strided), to its context and their ancestors;
     returns out of q's shape, zeros past ``n_nodes``.  ``parent`` None is the
     chain; Nmax = 1 an ordinary decode step.  ``scale`` defaults to
     head_dim ** -0.5.  ``workspace``: a uint8 CUDA tensor of at least
-    sv_attention_workspace_size bytes (allocated when omitted)."""
+    sv_attention_workspace_size bytes (allocated when omitted).
+    ``expire_waits`` (testing only): bits of SV_ATTENTION_WAITS kinds of waits
+    inside the kernel that are made to run out, to exercise the timeout path."""
     c, cache, B = _cache(k_cache, v_cache, k_scale, v_scale, page_table)
     shape = q.shape
     if len(shape) != 4:
@@ -276,11 +282,11 @@ def spec_tree_attention(q, k_cache, v_cache, page_table, kv_len, n_nodes=None, p
     else:
         need = workspace.numel()
         wp = _ptr(workspace, "workspace", torch.uint8, workspace.shape)
-    st = lib.spec_tree_attention(c, _ptr(kv_len, "kv_len", torch.int32, (B,)),
-                                 _ptr(n_nodes, "n_nodes", torch.int32, (B,)),
-                                 _ptr(parent, "parent", torch.int32, (B, Nmax)), qp, q_stride, code, Hq, B,
-                                 Nmax, D ** -0.5 if scale is None else scale, op, _errors_ptr(errors), wp, need,
-                                 _raw_stream(stream, q))
+    st = lib.spec_tree_attention_ex(c, _ptr(kv_len, "kv_len", torch.int32, (B,)),
+                                    _ptr(n_nodes, "n_nodes", torch.int32, (B,)),
+                                    _ptr(parent, "parent", torch.int32, (B, Nmax)), qp, q_stride, code, Hq, B,
+                                    Nmax, D ** -0.5 if scale is None else scale, op, _errors_ptr(errors), wp, need,
+                                    expire_waits, _raw_stream(stream, q))
     if st:
         _check(st, "spec_tree_attention")
     return out
