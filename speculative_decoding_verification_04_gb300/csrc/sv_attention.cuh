@@ -322,16 +322,25 @@ struct Ring {
     }
 };
 
+// One lane: the arrival that a barrier was made to lack, once a wait has given up.
+__device__ __forceinline__ void make_up(AttnShared& sh, uint64_t* bar)
+{
+#pragma unroll 1
+    for (uint32_t i = 0; i < kWaitSpins && *reinterpret_cast<volatile uint32_t*>(&sh.limit); ++i)
+        __nanosleep(500);
+    mbar_arrive(smem_addr(bar));
+}
+
 // The last copies into each slot of a ring that has been filled `fills` times,
 // `r` standing at the next.  `held`: the slots' barriers lack an arrival (none
 // has been filled twice then), which one lane makes up for.
-__device__ __forceinline__ void drain_ring(uint64_t* full, Ring r, int slots, uint32_t fills, bool held)
+__device__ __forceinline__ void drain_ring(AttnShared& sh, uint64_t* full, Ring r, int slots, uint32_t fills, bool held)
 {
 #pragma unroll 1
     for (uint32_t n = min(fills, (uint32_t)slots); n > 0; --n) {
         r.back(slots);
         if (held)
-            mbar_arrive(smem_addr(&full[r.slot]));
+            make_up(sh, &full[r.slot]);
         drain_wait(&full[r.slot], r.phase);
     }
 }
@@ -1036,28 +1045,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             scratch[(warp & 3) * NT + 8 * i + lane] = x[0];
                     }
                     float* const fin = scratch + 4 * NT;
-                    // (after a wait that gave up nothing of the item can be relied on)
                     if (!cta_wait(sh, &sh.info_full[items & 1], (items >> 1) & 1))
                         gt |= kGaveUp;
-                    const bool abort = bar_any(bar, 128, *reinterpret_cast<volatile uint32_t*>(&sh.limit) == 0), bad = abort || info.bad;
-                    if (tid == 0 && bad && a.has_err)
-                        atomicOr(a.err, abort ? kErrWaitTimeout : kErrCache);
-                    lost |= abort;
-                    if (t < NT && !abort) {
+                    bar_sync(bar, 128);
+                    const bool bad = info.bad;
+                    float l = 0.0f;
+                    if (t < NT) {
                         const unsigned anc = info.anc[w * NT + t];
-                        float l = (scratch[t] + scratch[NT + t]) + (scratch[2 * NT + t] + scratch[3 * NT + t]);
+                        l = (scratch[t] + scratch[NT + t]) + (scratch[2 * NT + t] + scratch[3 * NT + t]);
                         if (bad || (anc & info.poison))
                             l = NAN;
                         // (anc == 0: no node's row.  A node's sum is zero only where all its scores are -inf: NaN)
                         fin[t] = anc == 0 ? 0.0f : __fdividef(1.0f, l);
-                        const int at = info.row_out[w * NT + t];
-                        if (!whole && at >= 0)
-                            reinterpret_cast<float2*>(a.part_ml)[at] = make_float2(-negm[t], l);
                     }
                     if (!cta_wait(sh, &sh.o_full, (gt - 1) & 1))
                         gt |= kGaveUp;
                     tc_fence_after();
-                    bar_sync(bar, 128);
+                    // After a wait that gave up, the item's last one among them, nothing of the item can be relied on: its
+                    // rows are written as NaN below, and reported when the CTA ends.
+                    const bool abort = bar_any(bar, 128, *reinterpret_cast<volatile uint32_t*>(&sh.limit) == 0);
+                    if (tid == 0 && bad && !abort && a.has_err)
+                        atomicOr(a.err, kErrCache);
+                    lost |= abort;
+                    if (t < NT && !whole && !abort) {
+                        const int at = info.row_out[w * NT + t];
+                        if (at >= 0)
+                            reinterpret_cast<float2*>(a.part_ml)[at] = make_float2(-negm[t], l);
+                    }
 #pragma unroll 1
                     for (int c = 0; c < a.nd && !abort; ++c) {
                         const int d = 128 * c + t;
@@ -1337,8 +1351,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (; fills_v < most_v; ++fills_v, rv.step(a.vslots))
                 if (lane == 0)
                     mbar_arrive(smem_addr(&sh.vfull[rv.slot]));
-            drain_ring(sh.kfull, rk, a.kslots, fills_k, t == 0 && ((a.hold >> kKFull) & 1));
-            drain_ring(sh.vfull, rv, a.vslots, fills_v, t == 0 && ((a.hold >> kVFull) & 1));
+            drain_ring(sh, sh.kfull, rk, a.kslots, fills_k, t == 0 && ((a.hold >> kKFull) & 1));
+            drain_ring(sh, sh.vfull, rv, a.vslots, fills_v, t == 0 && ((a.hold >> kVFull) & 1));
         }
     } else {
         regs_shrink<kRegsIssue<NT>>();
@@ -1367,7 +1381,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             if (items) {
                 if (lane == 0 && ((a.hold >> kQFull) & 1))
-                    mbar_arrive(smem_addr(&sh.q_full));
+                    make_up(sh, &sh.q_full);
                 drain_wait(&sh.q_full, (items - 1) & 1);
             }
             if (E4M3) {
@@ -1392,7 +1406,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         ++fills;
                     }
                 }
-                drain_ring(sh.kfull, rk, a.kslots, fills, lane == 0 && ((a.hold >> kKFull) & 1));
+                drain_ring(sh, sh.kfull, rk, a.kslots, fills, lane == 0 && ((a.hold >> kKFull) & 1));
             }
         } else if (warp == 8) {
             // --- first product -----------------------------------------------------------
@@ -1547,15 +1561,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     --owed;
                 }
             }
-            drain_ring(sh.vfull, rv, a.vslots, fills, lane == 0 && ((a.hold >> kVFull) & 1));
+            drain_ring(sh, sh.vfull, rv, a.vslots, fills, lane == 0 && ((a.hold >> kVFull) & 1));
         }
     }
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    const AttnShared& sh = *attn_layout<N, E4M3>(a, smem).sh;
     if (warp == 8)
-        tmem_free(attn_layout<N, E4M3>(a, smem).sh->tmem, 512);
+        tmem_free(sh.tmem, 512);
+    if (tid == 0 && a.has_err && *reinterpret_cast<const volatile uint32_t*>(&sh.limit) == 0)
+        atomicOr(a.err, kErrWaitTimeout);
 }
 
 // Items cut between CTAs: CTA i's last item, if it does not end it, is joined

@@ -1,5 +1,5 @@
-"""Waits inside the attention kernel that give up: the call returns, and the
-device and the next call are as if nothing had been.
+"""Waits inside the attention kernel that give up: the call returns, its rows
+are their values or NaN, and the next call is as if nothing had been.
 
 A kind of wait is made to run out by the test-only argument expire_waits (the
 barriers of that kind lack one arrival, and the limit is some milliseconds).
@@ -68,3 +68,35 @@ def test_all_waits_at_once(dev):
             ref = call()
             call(expire_waits=(1 << sv.SV_ATTENTION_WAITS) - 1)
             assert torch.equal(call(), ref)
+
+
+MORE = [  # several items to a block; items of many tiles
+    ([200] * 300, [3] * 300, 4, 2, 64, 16),
+    ([3000] * 24, [9] * 24, 16, 8, 64, 64),
+]
+PLACES = (1, 3, 5, 7, 9, 11)   # waits for something to be free again: the first passes
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind", range(sv.SV_ATTENTION_WAITS), ids=lambda k: KINDS[k].replace(" ", "_"))
+def test_rows_are_right_or_nan_and_reported(dev, kind, fmt):
+    """No row is anything but its value or NaN, and bit 0 says whether one is
+    NaN.  Where a kind's first wait is needed for any result, all are."""
+    some = False
+    for shape in SHAPES + MORE:
+        ctx, nodes, Hq, Hkv, D, page = shape
+        call = make(dev, fmt, shape)
+        ref = call()
+        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        # NaN where nothing is written would pass for a lost row: start from something else
+        out = torch.full_like(ref, 7.0)
+        got = call(expire_waits=1 << kind, errors=err, out=out)
+        lost = got.isnan().all(-1)
+        assert (lost | (got == ref).all(-1)).all()
+        real = torch.arange(ref.shape[1], device=dev) < torch.tensor(nodes, device=dev)[:, None]
+        assert not (lost & ~real[..., None]).any()
+        assert err.item() == (1 if lost.any() else 0)
+        some |= bool(lost.any())
+        if kind not in PLACES and not (fmt == "bf16" and kind in CONVERTED):
+            assert lost[real].all()
+    assert some == (fmt == "e4m3" or kind not in CONVERTED)
