@@ -474,6 +474,10 @@ typedef struct {
  *           n_new[b] <= S of them are real (NULL: all S).
  *   packed  row_start [B + 1]: sequence b's tokens are the rows row_start[b]
  *           to row_start[b + 1] - 1 of `rows`; n_new, parent and S unused.
+ *           Starts that do not ascend from 0 or more set bit 2 of `errors`; a
+ *           row between the first and the last start is then usable where a
+ *           search for it ends in a sequence whose rows hold it and lie
+ *           between those starts.
  * q may be NULL (keys and values only).  q_out [rows][n_heads][head_dim]
  * receives the queries, zeros in the rows of no real token; q_out may be q
  * where q_stride is n_heads * head_dim.
@@ -583,7 +587,8 @@ sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* kv_len, const 
  * spec_kv_read -- rows row_start[b] .. row_start[b + 1] - 1 of k_out and v_out
  * [rows][n_kv_heads][head_dim] (dtype, 16-byte aligned) receive the entries of
  * sequence b at the positions start[b], start[b] + 1, ..., each value (times
- * its scale) rounded once to dtype.  Rows of no sequence are zeros.
+ * its scale) rounded once to dtype.  Rows of no sequence are zeros.  Starts
+ * that do not ascend are treated as in spec_kv_append.
  */
 sv_status spec_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32_t* row_start,
                        int32_t B, int32_t rows, sv_dtype dtype, void* k_out, void* v_out,
