@@ -430,9 +430,10 @@ sv_status spec_verify_tree(const void* target_logits, const void* draft_logits, 
  *            SV_KV_E4M3 (each entry stands for its e4m3 value times its
  *            scale), NULL with SV_KV_BF16
  * All pointers are device memory, 16-byte aligned.  head_dim: a multiple of
- * 16 from 64 to 256; page_size: a power of two from 8 to 1024.  Only
- * spec_kv_commit looks past layer 0: for a call on layer l pass that layer's
- * pointers and layers = 1.
+ * 16 from 64 to 256; page_size: a power of two from 8 to 1024; max_pages times
+ * page_size: at most 2^31 - 2^16; a layer's rows (num_pages times heads times
+ * page_size): below 2^31.  Only spec_kv_commit looks past layer 0: for a call
+ * on layer l pass that layer's pointers and layers = 1.
  *
  * Node n of a sequence with kv_len context positions is stored at position
  * kv_len + n; trees are given as in spec_verify_tree (parent[n] < n for

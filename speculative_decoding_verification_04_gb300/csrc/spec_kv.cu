@@ -14,6 +14,10 @@ namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
+// Positions of a sequence: the kernels' positions are ints, and step past a
+// sequence's end by up to 32 pages of the largest size.
+constexpr long long kMaxPositions = 0x7fff0000LL;
+
 // The cache description, checked.  Row counts stay below 2^31 so that a row
 // is an int coordinate; byte offsets are 64-bit everywhere.
 sv_status check_cache(const sv_kv_cache* c, bool need_table, KvCache* out)
@@ -32,7 +36,7 @@ sv_status check_cache(const sv_kv_cache* c, bool need_table, KvCache* out)
         (c->page_size & (c->page_size - 1)))
         return SV_ERR_UNSUPPORTED;
     if ((long long)c->num_pages * c->n_kv_heads * c->page_size > 0x7fffffffLL ||
-        (long long)c->max_pages * c->page_size > 0x7fffffffLL)
+        (long long)c->max_pages * c->page_size > kMaxPositions)
         return SV_ERR_UNSUPPORTED;
     out->k = static_cast<unsigned char*>(c->k);
     out->v = static_cast<unsigned char*>(c->v);
