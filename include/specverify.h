@@ -587,8 +587,8 @@ sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* kv_len, const 
 /*
  * spec_kv_read -- rows row_start[b] .. row_start[b + 1] - 1 of k_out and v_out
  * [rows][n_kv_heads][head_dim] (dtype, 16-byte aligned) receive the entries of
- * sequence b at the positions start[b], start[b] + 1, ..., each value (times
- * its scale) rounded once to dtype.  Rows of no sequence are zeros.  Starts
+ * sequence b at the positions start[b], start[b] + 1, ..., rounded to dtype (an
+ * e4m3 value times its scale is an fp32 product first).  Rows of no sequence are zeros.  Starts
  * that do not ascend are treated as in spec_kv_append.
  */
 sv_status spec_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32_t* row_start,

@@ -34,26 +34,26 @@
 // second product, 11 what an item needs before its first tile (tree masks).
 //  * bf16: 9 loads the queries, 12-15 a quarter of each tile's keys and values
 //    (a TMA copy of a page holds its warp for about 130 cycles, so one warp
-//    cannot load small pages as fast as memory delivers them: 371 us against
-//    275 for 256 trees at pages of 16).
+//    cannot load small pages as fast as memory delivers them: on an earlier
+//    form of the kernel 256 trees at pages of 16 took 371 us, 275 with four).
 //  * e4m3: 9 loads the keys and 11 the values, 12-15 make the queries' terms
-//    and convert a quarter of the values each (converting warps that load as
-//    well: 118 us against 102 for 64 chains).
+//    and convert a quarter of the values each (on an earlier form, with
+//    converting warps that load as well, 64 chains took 118 us instead of 102).
 // Tiles run through them in one stream across items.
 //
 // Measured on a GB300, a call (8 key heads of 128, 32 query heads):
-//  * 256 trees of 15 nodes over 100-1500 positions, bf16, pages of 16: 171 us,
-//    0.82 of the copy rate; HBM bounds it (914 MB read, nothing twice).
-//  * 64 chains of 9 over 200-3000 positions, e4m3: 100-110 us (bytes 34 us); what a
+//  * 256 trees of 15 nodes over 100-1500 positions, bf16, pages of 16: 173 us,
+//    0.80 of the copy rate; HBM bounds it (914 MB read, nothing twice).
+//  * 64 chains of 9 over 200-3000 positions, e4m3: 104-110 us (bytes 34 us); what a
 //    tile takes from its load over conversion, products and softmax.
-//  * 2 x 32 nodes over 100-120 thousand positions, e4m3: 200 us, 610 TFLOP/s;
-//    tensor pipe 36 % and issue slots 41 % busy.
-//  * one token over 700 positions: 11.5 us on the GPU, latency.
+//  * 2 x 32 nodes over 100-120 thousand positions, e4m3: 199-207 us, 600 TFLOP/s;
+//    tensor pipe 36 % and issue slots 38 % busy.
+//  * one token over 700 positions: 11.7 us on the GPU, latency.
 //
 // Work is (sequence, key head, row group) items of 128-position tiles, laid
 // end to end and cut into runs of equal cost, one to a CTA (an item costs its
-// tiles and kItemCost more: 175 us for the 256 trees, 202 with equal tiles).  An item cut by a run's end leaves partial sums
-// in the workspace, which sv_attention_combine joins.
+// tiles and kItemCost more).  An item cut by a run's end leaves partial sums in
+// the workspace, which sv_attention_combine joins.
 #pragma once
 
 #include "sv_kv.cuh"
@@ -69,7 +69,9 @@ template <bool E4M3> constexpr float kAtRef = E4M3 ? 6.0f : 0.0f;
 template <bool E4M3> constexpr float kLazy = E4M3 ? 14.0f : 24.0f;
 constexpr int kMaxSlots = 8;
 // What an item's start and end cost, in tiles.  Measured with 4, 2, 1 and 0: 256
-// trees 175, 178, 182, 202 us; odd sizes 57, 62, 66, 81; 64 chains 153, 174, 158, 178.
+// trees 173, 176, 187, 204 us; odd sizes (heads of 80) 52, 57, 61, 67; 64 chains 108,
+// 114, 122, 132.  Wider heads were not measured: their tiles cost more, so that
+// less would do there.
 constexpr int kItemCost = 4;
 constexpr int kQuarter = kTile / 4;        // positions a loading warp takes care of
 // Query rows a CTA: 128, but 64 where the three 8-bit terms of wider heads'
@@ -443,7 +445,8 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t v, uint32_t p, u
 // this tile), and the sums in TMEM are rescaled.  In bf16 each row goes by its
 // own scores, so that its rounding does not depend on the rows beside it.  In
 // e4m3, where moves are frequent, all rows that have risen move at once (two
-// sequences of 110 thousand positions: 200 us, 233 with a move a row).  scratch[0 .. NT) then holds
+// sequences of 110 thousand positions: 200 us, 233 with a move a row on an
+// earlier form).  scratch[0 .. NT) then holds
 // the factors of what was summed so far, [NT .. 2 NT) how far references rose.
 template <int NT, bool E4M3>
 __device__ __forceinline__ void move_references(float* scratch, float* negm, int* unset_flag, uint32_t s_at, uint32_t o_at,
@@ -725,8 +728,9 @@ __device__ __forceinline__ bool prepare_item(const AttnArgs& a, AttnShared& sh, 
 constexpr int kAttnThreads = 512;
 // Registers a thread: the softmax's warpgroups (warps 0 .. 7) hold NT scores and
 // NT sums a thread, the issuing warps (8 .. 11) little; a spill costs a loop
-// its L2 latency, the caches being shared memory.  The shares add up to the
-// launch's.
+// its L2 latency, the caches being shared memory (bf16 spills 32 bytes at 48
+// rows a warpgroup and 28 at 64, e4m3 16 at 64, the others none).  The shares
+// add up to the launch's.
 constexpr int kAttnRegs = 128;       // at launch
 template <int NT> constexpr int kRegsSoftmax = NT >= 64 ? 168 : 152;
 template <int NT> constexpr int kRegsIssue = NT >= 64 ? 80 : 96;

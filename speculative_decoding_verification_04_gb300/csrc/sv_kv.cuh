@@ -257,16 +257,18 @@ __device__ __forceinline__ uint32_t e4m3_quad(const float* x)
 //   e4m3: scale = max(amax |y| / 448, 2^-100), stored y / scale.
 // One pass: each element is read and written once.  On a GB300, 16411 prompt
 // tokens of 32 + 8 + 8 heads of 128 (bf16) take 82 us a call, 0.75 of the
-// copy rate (61.7 us); issue slots are 66 % busy, DRAM 58 %.  256 trees of 15
-// nodes written to e4m3 take 24 us on the GPU (13.3): too few bytes to hide the
-// lookups' three dependent loads.  8 single tokens take 4 us on the GPU.
+// copy rate (61.7 us); issue slots are 62 % busy, DRAM 57 %.  256 trees of 15
+// nodes written to e4m3 take 22.6 us on the GPU (13.3): the lookups' three
+// dependent loads, and 960 blocks on 456 places, two waves and a tenth.  8
+// single tokens take 3 us on the GPU.
 //
 // LPR lanes hold a head's row: 16 elements each, the lanes from D / 16 on none
 // (D = 80, 96, 112 of LPR 8; 144 ... 240 of LPR 16).  A warp holds 32 / LPR
 // rows at a time; the next are on their way to registers while it works and
 // the two passes after them to L2, and the first are asked for before the
 // token's place is looked up (three loads that depend on one another).  With
-// rows loaded when they are needed the 16411 tokens took 104 us.
+// rows loaded when they are needed the 16411 tokens took 104 us.  At three
+// blocks an SM (80 registers) bf16 rows spill 20 to 24 bytes, fp32 rows 64 to 72.
 template <typename T, int LPR, bool E4M3>
 __global__ void __launch_bounds__(256, 3) sv_append_kernel(const __grid_constant__ AppendArgs a)
 {
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(256, 3) sv_append_kernel(const __grid_constant
 
 // ---------------------------------------------------------------------------
 // read: x scale, rounded once.  Bound by HBM where there is much to read:
-// 100003 rows of 8 heads of 128 from e4m3 to bf16 take 117 us on a GB300, 0.80
+// 100003 rows of 8 heads of 128 from e4m3 to bf16 take 118 us on a GB300, 0.79
 // of the copy rate (93 us).
 // ---------------------------------------------------------------------------
 struct ReadArgs {
@@ -558,8 +560,8 @@ __device__ __forceinline__ int commit_moves(const CommitArgs& a, int b, int lane
 }
 
 // Latency bounds it: length, path, pages, then rows, each waiting for the one
-// before.  32 layers of 256 trees take 11 us on a GB300 (the bytes 10.4), two
-// layers of four 4 us.
+// before.  32 layers of 256 trees take 10.5 us on a GB300 (the bytes 10.4), two
+// layers of four 3.3 us.
 // One block per (sequence, layer).  A thread takes one 16-byte column of a
 // head's rows through all moves in order: path[i] > i strictly ascends, so a
 // move writes only rows that no later move reads.
