@@ -536,7 +536,9 @@ sv_status spec_kv_append(const sv_kv_cache* cache, const sv_kv_tokens* tokens, c
  * statistics are fp32; for the second product weights are rounded to bf16, or
  * with SV_KV_E4M3 weights times value scales to fp16.  An e4m3 cache's first
  * product takes each query element to 2^-17 or less of the largest finite one
- * in its row, beside whatever other rows hold.
+ * in its row, beside whatever other rows hold.  Weights of a bf16 cache reach
+ * 2^24 before they are brought down, so values have to stay below 2^80 in
+ * magnitude for the sums to stay finite.
  * What is not finite: a query row, or a key or value scale that a row sees,
  * makes that row NaN, and so does a node's value that it sees (ancestors and
  * itself); rows that do not see the node are as without it.  The context is
