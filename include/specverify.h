@@ -413,6 +413,59 @@ sv_status spec_verify_tree(const void* target_logits, const void* draft_logits, 
                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Filtered distributions: min-p, top-k and top-p
+ * ------------------------------------------------------------------------
+ * Rows of logits [B][S][V] (dtype, contiguous), and per sequence b (device
+ * memory): temperature[b], top_k[b] int32 (0: off), top_p[b] float32 in [0, 1]
+ * (1: off) and min_p[b] float32 in [0, 1] (0: off); top_k, top_p and min_p may
+ * each be NULL (off for all).  With m the row's largest logit a token's weight
+ * is exp((l - m) / T).  Tokens are ordered by logit, the largest first, equal
+ * ones by index; then
+ *   min-p  keeps the tokens whose weight is at least min_p,
+ *   top-k  of these the first k,
+ *   top-p  of these the shortest prefix that holds the share top_p of their
+ *          mass (at least one token).
+ * T = 0 keeps the argmax alone (lowest index); its filters are not used.
+ * Sums are of whole numbers (weights in units of 2^-62 of the largest), so
+ * results do not depend on the order of the additions.
+ * A row with a NaN or +inf logit or no finite one, or with an unusable
+ * temperature, top_k (negative), top_p or min_p, has the kept count -1.
+ * Calls are asynchronous on `stream`, allocate nothing and need no workspace;
+ * they may be captured into CUDA graphs.  V: at most sv_max_vocab(dtype).
+ */
+
+/*
+ * spec_sample_filtered -- one token per row from the kept tokens' weights (the
+ * draft model's sampling step, S = 1): the first token of the order whose
+ * cumulative mass is above uniforms[b] times the kept mass.  (spec_sample
+ * draws in the order of the indices.)
+ *   uniforms    device, [B] float32 in [0, 1) (not read where T = 0)
+ *   out_tokens  device, [B] int32: the token, -1 for an unusable row or uniform
+ *   out_prob    device, [B] float32 or NULL: its share of the kept mass (1 where
+ *               T = 0, NaN where the token is -1)
+ *   out_kept    device, [B] int32 or NULL: how many tokens were kept (-1 for an
+ *               unusable row or uniform)
+ */
+sv_status spec_sample_filtered(const void* logits, sv_dtype dtype, const float* uniforms, const float* temperature,
+                               const int32_t* top_k, const float* top_p, const float* min_p, int32_t B, int32_t V,
+                               int32_t* out_tokens, float* out_prob, int32_t* out_kept, cudaStream_t stream);
+
+/*
+ * spec_filter_logits -- out [B][S][V] receives the kept tokens' logits and -inf
+ * for the rest, NaN throughout an unusable row: spec_verify and
+ * spec_verify_tree on filtered target and draft rows verify against the
+ * filtered distributions (a draft drawn by spec_sample_filtered needs its rows
+ * filtered the same way).  n_rows (device, [B] int32, or NULL: all S) says how
+ * many of a sequence's rows are real (K[b] + 1 of a target's, n_nodes[b] of a
+ * tree's); the others are neither read nor written, and their kept count is 0.
+ * out may be logits itself; otherwise the two do not overlap.
+ *   out_kept  device, [B][S] int32 or NULL
+ */
+sv_status spec_filter_logits(const void* logits, sv_dtype dtype, const float* temperature, const int32_t* top_k,
+                             const float* top_p, const float* min_p, int32_t B, int32_t S, const int32_t* n_rows, int32_t V,
+                             void* out, int32_t* out_kept, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
  * The target model's key/value cache around a verification step
  * ------------------------------------------------------------------------
  * A decode step over a tree (or chain) of drafted tokens writes the nodes'
@@ -596,6 +649,65 @@ sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* kv_len, const 
 sv_status spec_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32_t* row_start,
                        int32_t B, int32_t rows, sv_dtype dtype, void* k_out, void* v_out,
                        uint32_t* errors, cudaStream_t stream);
+
+/*
+ * The cache's pages.  A stack of free pages serves all sequences:
+ * free_pages[0 .. *free_count - 1] of at most `capacity`, the last on top.
+ * held[b] is how many entries of sequence b's page table are its own; entries
+ * behind them mean nothing.  All device memory.
+ */
+typedef struct {
+    int32_t* page_table;         /* [B][max_pages] */
+    const int32_t* held;         /* [B] */
+    int32_t* free_pages;         /* [capacity] */
+    const int32_t* free_count;   /* one int32 */
+    int32_t B;
+    int32_t max_pages;
+    int32_t page_size;           /* as in sv_kv_cache */
+    int32_t capacity;
+} sv_kv_pool;
+
+/*
+ * spec_kv_reserve -- room for new tokens behind each sequence's kv_len[b]
+ * positions: n_new[b] <= S of them (NULL: S), or with row_start [B + 1] (packed
+ * rows, as in spec_kv_append; n_new NULL, S unused) row_start[b + 1] -
+ * row_start[b].  A sequence that holds fewer than ceil((kv_len + new) /
+ * page_size) pages asks for the rest.  The requests are served in the order of
+ * the sequences, a request whole or not at all, until one is larger than what
+ * is left; it and those after it are refused (a sequence that asks for no page
+ * is not).  A served page is the top of the stack at that point, and goes
+ * behind the sequence's held ones.  A refused sequence's missing entries
+ * become -1 (spec_kv_append then reports them and writes nothing there), and
+ * bit 3 of `errors` is set.
+ *   held_out, free_count_out  the counts after that; may be held and free_count
+ *   slots   [B][S] ([rows] packed) int64 or NULL: token n's place in the cache,
+ *           page_table[b][p / page_size] * page_size + p % page_size for
+ *           p = kv_len[b] + n; -1 for tokens of a refused sequence, past
+ *           n_new[b], and in rows of no sequence
+ *   rows    B * S, or the packed rows
+ * The pages between 0 and the top of the stack stay as they are, so that a
+ * call can be made again from the counts before it.
+ * Sequences whose lengths or counts cannot be used (negative, more than S new
+ * tokens, past the page table) are refused and set bit 2 of `errors`, as do
+ * pages below 0; a free_count outside [0, capacity] and row starts that do not
+ * ascend from 0 or more to at most `rows` refuse the whole call.
+ */
+sv_status spec_kv_reserve(const sv_kv_pool* pool, const int32_t* kv_len, const int32_t* n_new, const int32_t* row_start, int32_t S,
+                          int32_t rows, int32_t* held_out, int32_t* free_count_out, int64_t* slots, uint32_t* errors,
+                          cudaStream_t stream);
+
+/*
+ * spec_kv_release -- after verification: the pages behind ceil(kv_len[b] /
+ * page_size) of each sequence go back onto the stack, so that they are handed
+ * out again in the same order (a release after a reserve with the lengths
+ * unchanged leaves the stack as it was).  kv_len[b] = 0 gives back all.  The
+ * page table is not written.  A sequence whose lengths cannot be used
+ * (negative, held outside [0, max_pages], longer than its pages) keeps its
+ * pages and sets bit 2 of `errors`; a free_count outside [0, capacity], or a
+ * stack that would grow past `capacity`, refuses the whole call.
+ */
+sv_status spec_kv_release(const sv_kv_pool* pool, const int32_t* kv_len, int32_t* held_out, int32_t* free_count_out,
+                          uint32_t* errors, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

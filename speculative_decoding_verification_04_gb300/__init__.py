@@ -16,6 +16,10 @@ sv_options / sv_diag), and, from ``kv_cache.py`` on first use, the paged
 key/value cache around a verification step:
   spec_kv_append, spec_tree_attention, spec_kv_commit, spec_kv_read,
   sv_attention_workspace_size
+from ``pages.py`` the pages behind it:
+  spec_kv_reserve, spec_kv_release
+and from ``filters.py`` min-p, top-k and top-p:
+  spec_sample_filtered, spec_filter_logits
 """
 from __future__ import annotations
 
@@ -457,7 +461,7 @@ def spec_verify_host(target, draft, draft_tokens, uniforms, temperature, K, stag
 def sv_workspace_errors(workspace: Workspace, stream=None) -> int:
     """Device-side error flags of the last call on ``workspace`` (synchronises):
     bit 0 a bounded wait gave up, bit 1 a wrong temperature hint, bit 2
-    unusable cache metadata."""
+    unusable cache metadata, bit 3 too few free pages."""
     flags = ctypes.c_uint32(0)
     sp, _ = _stream(stream)
     st = _load().sv_workspace_errors(workspace.ptr, ctypes.byref(flags), sp)
@@ -468,16 +472,21 @@ def sv_workspace_errors(workspace: Workspace, stream=None) -> int:
 
 
 # ---------------------------------------------------------------------------
-# the key/value cache (kv_cache.py imports torch, so it is loaded on first use)
+# the key/value cache, its pages and the filters (these modules import torch,
+# so they are loaded on first use)
 # ---------------------------------------------------------------------------
 _KV_NAMES = ("spec_kv_append", "spec_tree_attention", "spec_kv_commit", "spec_kv_read",
              "sv_attention_workspace_size", "SVKvCache", "SVKvTokens", "SV_KV_BF16", "SV_KV_E4M3", "SV_ATTENTION_WAITS")
+_PAGE_NAMES = ("spec_kv_reserve", "spec_kv_release", "SVKvPool")
+_FILTER_NAMES = ("spec_sample_filtered", "spec_filter_logits")
 
 
 def __getattr__(name):
-    if name not in _KV_NAMES:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import kv_cache
-    for n in _KV_NAMES:
-        globals()[n] = getattr(kv_cache, n)
-    return globals()[name]
+    import importlib
+    for module, names in (("kv_cache", _KV_NAMES), ("pages", _PAGE_NAMES), ("filters", _FILTER_NAMES)):
+        if name in names:
+            m = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(m, n)
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

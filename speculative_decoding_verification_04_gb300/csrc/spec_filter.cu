@@ -1,0 +1,93 @@
+// spec_filter.cu -- host layer and C ABI of filtered sampling and filtered
+// logits: argument checks, launch shapes.  Nothing here allocates,
+// synchronises or keeps state between calls.
+#include <cuda_runtime.h>
+
+#include "../../include/specverify.h"
+#include "sv_filter.cuh"
+
+namespace sv {
+namespace {
+
+sv_status check_rows(const void* logits, sv_dtype dtype, const float* temperature, const int32_t* top_k, const float* top_p,
+                     const float* min_p, int32_t B, int32_t S, int32_t V, FilterArgs* a)
+{
+    if (B < 0 || S < 1 || V < 1 || (dtype != SV_DTYPE_F32 && dtype != SV_DTYPE_BF16))
+        return SV_ERR_INVALID_ARG;
+    if (V > sv_max_vocab(dtype) || (long long)B * S > 0x3fffffffLL)
+        return SV_ERR_UNSUPPORTED;
+    if (B == 0)
+        return SV_OK;
+    if (!logits || !temperature || ((uintptr_t)logits & (dtype == SV_DTYPE_BF16 ? 1 : 3)) ||
+        (((uintptr_t)temperature | (uintptr_t)top_k | (uintptr_t)top_p | (uintptr_t)min_p) & 3))
+        return SV_ERR_INVALID_ARG;
+    a->logits = logits;
+    a->temperature = temperature;
+    a->top_k = top_k;
+    a->top_p = top_p;
+    a->min_p = min_p;
+    a->has_k = top_k != nullptr;
+    a->has_p = top_p != nullptr;
+    a->has_m = min_p != nullptr;
+    a->B = B;
+    a->S = S;
+    a->V = V;
+    return SV_OK;
+}
+
+template <bool DRAW> sv_status launch_rows(const FilterArgs& a, sv_dtype dtype, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)((long long)a.B * a.S);
+    if (dtype == SV_DTYPE_BF16)
+        sv_filter_kernel<__nv_bfloat16, DRAW><<<grid, kFilterThreads, 0, st>>>(a);
+    else
+        sv_filter_kernel<float, DRAW><<<grid, kFilterThreads, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" {
+
+sv_status spec_sample_filtered(const void* logits, sv_dtype dtype, const float* uniforms, const float* temperature,
+                               const int32_t* top_k, const float* top_p, const float* min_p, int32_t B, int32_t V,
+                               int32_t* out_tokens, float* out_prob, int32_t* out_kept, cudaStream_t stream)
+{
+    sv::FilterArgs a{};
+    const sv_status st = sv::check_rows(logits, dtype, temperature, top_k, top_p, min_p, B, 1, V, &a);
+    if (st != SV_OK || B == 0)
+        return st;
+    if (!uniforms || !out_tokens || (((uintptr_t)uniforms | (uintptr_t)out_tokens | (uintptr_t)out_prob | (uintptr_t)out_kept) & 3))
+        return SV_ERR_INVALID_ARG;
+    a.uniforms = uniforms;
+    a.out_tokens = out_tokens;
+    a.out_prob = out_prob;
+    a.out_kept = out_kept;
+    a.has_prob = out_prob != nullptr;
+    a.has_kept = out_kept != nullptr;
+    return sv::launch_rows<true>(a, dtype, stream);
+}
+
+sv_status spec_filter_logits(const void* logits, sv_dtype dtype, const float* temperature, const int32_t* top_k,
+                             const float* top_p, const float* min_p, int32_t B, int32_t S, const int32_t* n_rows, int32_t V,
+                             void* out, int32_t* out_kept, cudaStream_t stream)
+{
+    sv::FilterArgs a{};
+    const sv_status st = sv::check_rows(logits, dtype, temperature, top_k, top_p, min_p, B, S, V, &a);
+    if (st != SV_OK || B == 0)
+        return st;
+    const size_t elem = dtype == SV_DTYPE_BF16 ? 2 : 4, bytes = (size_t)B * S * V * elem;
+    const uintptr_t x = (uintptr_t)logits, y = (uintptr_t)out;
+    if (!out || y % elem || (((uintptr_t)n_rows | (uintptr_t)out_kept) & 3) || (x != y && x < y + bytes && y < x + bytes))
+        return SV_ERR_INVALID_ARG;
+    a.out = out;
+    a.n_rows = n_rows;
+    a.out_kept = out_kept;
+    a.has_n = n_rows != nullptr;
+    a.has_kept = out_kept != nullptr;
+    a.same_phase = (x & 15) == (y & 15);
+    return sv::launch_rows<false>(a, dtype, stream);
+}
+
+}  // extern "C"
