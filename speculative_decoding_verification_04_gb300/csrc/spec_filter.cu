@@ -3,6 +3,8 @@
 // synchronises or keeps state between calls.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "../../include/specverify.h"
 #include "sv_filter.cuh"
 
@@ -35,14 +37,56 @@ sv_status check_rows(const void* logits, sv_dtype dtype, const float* temperatur
     return SV_OK;
 }
 
-template <bool DRAW> sv_status launch_rows(const FilterArgs& a, sv_dtype dtype, cudaStream_t st)
+// CTAs a row is spread over: as many as leave each SM two while the rows alone
+// do not, at least kGroup vectors a thread's worth apart, and no more rows in
+// flight than L2 holds for the later passes.
+int row_ctas(long long rows, long long row_bytes, int nsm)
 {
-    const unsigned grid = (unsigned)((long long)a.B * a.S);
-    if (dtype == SV_DTYPE_BF16)
-        sv_filter_kernel<__nv_bfloat16, DRAW><<<grid, kFilterThreads, 0, st>>>(a);
-    else
-        sv_filter_kernel<float, DRAW><<<grid, kFilterThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    int C = 1;
+    while (C < 16 && rows * C < nsm && row_bytes / C > 16384)
+        C *= 2;
+    while (C < 8 && row_bytes * (2 * nsm / C) > (64ll << 20) && row_bytes / C > 65536)
+        C *= 2;
+    return C;
+}
+
+template <typename T, bool DRAW> cudaError_t launch(FilterArgs& a, cudaStream_t st)
+{
+    int dev = 0, nsm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return e;
+    static std::atomic<unsigned long long> ready{0};   // devices whose limits have been raised
+    if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
+        e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(FilterShared));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    const long long rows = (long long)a.B * a.S;
+    a.C = row_ctas(rows, (long long)a.V * sizeof(T), nsm);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(rows * a.C));
+    cfg.blockDim = dim3(kFilterThreads);
+    cfg.dynamicSmemBytes = sizeof(FilterShared);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)a.C;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = a.C > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, sv_filter_kernel<T, DRAW>, a);
+}
+
+template <bool DRAW> sv_status launch_rows(FilterArgs& a, sv_dtype dtype, cudaStream_t st)
+{
+    return (dtype == SV_DTYPE_BF16 ? launch<__nv_bfloat16, DRAW>(a, st) : launch<float, DRAW>(a, st)) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace
