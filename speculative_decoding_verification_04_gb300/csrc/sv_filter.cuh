@@ -63,6 +63,8 @@ struct FilterShared {
     u128 part[kFilterWarps];
     u128 sum, found_mass;
     Command cmd;
+    RowScale scale;
+    uint32_t least_key;    // min-p's border
     float max_of[kFilterWarps];
     float top;             // this CTA's largest logit
     uint32_t bound;        // this CTA's lower bound for the top-k
@@ -257,8 +259,10 @@ struct Settings {
     int k;
 };
 
+// A row's numbers.  (64-bit floating point runs at a hundredth of the fp32
+// rate: one thread's at most, never a block's.)
 template <bool DRAW>
-__device__ __forceinline__ void put_draw(const FilterArgs& a, long long r, int token, float prob, int kept)
+__device__ __forceinline__ void put_row(const FilterArgs& a, long long r, int kept, int token = -1, uint64_t weight = 0, u128 mass = 0)
 {
     if (threadIdx.x == 0) {
         if (a.has_kept)
@@ -266,7 +270,7 @@ __device__ __forceinline__ void put_draw(const FilterArgs& a, long long r, int t
         if (DRAW) {
             a.out_tokens[r] = token;
             if (a.has_prob)
-                a.out_prob[r] = prob;
+                a.out_prob[r] = token < 0 ? __int_as_float(0x7fc00000) : (float)((double)weight / (double)mass);
         }
     }
 }
@@ -352,20 +356,19 @@ __device__ __forceinline__ void fill_row(const RowSpan<T>& row, T* out, bool sam
 }
 
 // The lowest logit that min-p keeps: the least float at or above m + T ln(min_p).
-__device__ __forceinline__ uint32_t min_p_key(float m, float T, float min_p)
+__device__ __forceinline__ uint32_t min_p_key(float m, double t_log)
 {
-    const double t = (double)m + (double)T * log((double)min_p);
+    const double t = (double)m + t_log;
     const float least = (float)fmax(t, -3.4028234663852886e38);
     return (double)least < t ? key_of(least) + 1 : key_of(least);
 }
 
 // By bisection, rank 0 alone.
 template <typename T, bool DRAW>
-__device__ __noinline__ void whole_row(const FilterArgs& a, long long r, const Settings& g, float m, Prefix end, FilterShared& s)
+__device__ __noinline__ void whole_row(const FilterArgs& a, long long r, const Settings& g, float m, Prefix end, const RowScale& sc, FilterShared& s)
 {
     const RowSpan<T> row(static_cast<const T*>(a.logits) + r * a.V, a.V, 0, 1);
     const uint32_t top = key_of(m);
-    const RowScale sc = row_scale(m, g.T);
     u128 mass = 0;
     if (g.k > 0 && prefix_sum<true>(row, end, sc, s) > (u128)g.k)
         end = prefix_reaching<true>(row, (u128)g.k, end, top, sc, s);
@@ -380,9 +383,9 @@ __device__ __noinline__ void whole_row(const FilterArgs& a, long long r, const S
     const int kept = a.has_kept ? (int)prefix_sum<true>(row, end, sc, s) : 0;
     if (DRAW) {
         const Prefix at = prefix_reaching<false>(row, share_of(g.u, mass, false) + 1, end, top, sc, s);
-        put_draw<DRAW>(a, r, at.index, (float)((double)weight62(value_of(at.key), sc, s.roots) / (double)mass), kept);
+        put_row<DRAW>(a, r, kept, at.index, weight62(value_of(at.key), sc, s.roots), mass);
     } else {
-        put_draw<DRAW>(a, r, 0, 0.0f, kept);
+        put_row<DRAW>(a, r, kept);
         write_row(row, static_cast<T*>(a.out) + r * a.V, a.same_phase, end);
     }
 }
@@ -538,13 +541,13 @@ struct BinScale {
     uint32_t ref;          // the bits of the largest logit's rounded product
 };
 
-__device__ __forceinline__ BinScale bin_scale(float m, const RowScale& sc)
+__device__ __forceinline__ BinScale bin_scale(float m, float T, const RowScale& sc)
 {
     BinScale b;
     b.ch = sc.ch;
     b.cl = sc.cl;
     b.ref = __float_as_uint(__fadd_rn(__fmul_rn(m, sc.ch), kMagicBin));
-    b.least = (float)fmax(sc.m - 64.25 / sc.c, -3.4028234663852886e38);
+    b.least = fmaxf(m - 44.6f * T, -3.4028234e38f);   // (64.3 octaves)
     return b;
 }
 
@@ -682,6 +685,13 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
     T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * V);
     const RowSpan<T> row(logits, V, rank, C);
 
+    double t_log = 0.0;   // thread 0's: what of the row's constants does not need its maximum
+    if (t == 0 && good && !greedy) {
+        s.scale = row_scale(g.T);
+        if (g.min_p > 0.0f)
+            t_log = (double)g.T * log((double)g.min_p);
+    }
+
     // 1. The maxima of the row, of each thread, and of each thread's groups of
     // vectors: the one pass that has to read everything from memory.
     const int groups = (row.v1 - row.v0 + kGroup * kFilterThreads - 1) / (kGroup * kFilterThreads);
@@ -768,7 +778,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
     const bool usable = good && m > -INFINITY && m < INFINITY;
     if (!usable) {
         if (rank == 0)
-            put_draw<DRAW>(a, r, -1, __int_as_float(0x7fc00000), -1);
+            put_row<DRAW>(a, r, -1);
         if (!DRAW)
             fill_row(row, out, a.same_phase, Bits<T>::nan);
         row_sync(C);
@@ -796,17 +806,20 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
         for (int c = 1; c < C; ++c)
             first = min(first, (int)ld_rank(&s.first, c == rank ? 0 : c));
         if (rank == 0)
-            put_draw<DRAW>(a, r, first, 1.0f, 1);
+            put_row<DRAW>(a, r, 1, first, 1, 1);
         row_sync(C);
         if (!DRAW)
             write_row(row, out, a.same_phase, Prefix{top_key, first});
         return;
     }
 
-    Prefix end{kKeyNegInf + 1, INT_MAX};
-    if (g.min_p > 0.0f)
-        end.key = max(end.key, min_p_key(m, g.T, g.min_p));
-    RowScale sc = row_scale(m, g.T);
+    if (t == 0) {
+        s.scale.at(m, g.T);
+        s.least_key = max(kKeyNegInf + 1, g.min_p > 0.0f ? min_p_key(m, t_log) : 0u);
+    }
+    __syncthreads();
+    Prefix end{s.least_key, INT_MAX};
+    RowScale sc = s.scale;
 
     // 3. Few candidates (a top-k bound, min-p, or a short row): they are read
     // again, by the groups that hold one, sorted and weighed.
@@ -850,9 +863,9 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
                 u128 to;
                 const int at = rank_reaching(q, 0, n, 0, share_of(g.u, mass, false) + 1, s, to);
                 const uint64_t e = s.list[at];
-                put_draw<DRAW>(a, r, entry_index(e), (float)((double)weight62(value_of(entry_key(e)), sc, s.roots) / (double)mass), n);
+                put_row<DRAW>(a, r, n, entry_index(e), weight62(value_of(entry_key(e)), sc, s.roots), mass);
             } else {
-                put_draw<DRAW>(a, r, 0, 0.0f, n);
+                put_row<DRAW>(a, r, n);
                 for (int i = t; i < n; i += kFilterThreads) {
                     const int j = entry_index(s.list[i]);
                     out[j] = (T)value_of(entry_key(s.list[i]));
@@ -876,7 +889,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
         for (int c = 0; c < C; ++c)
             total += C > 1 ? (int)ld_rank(&s.count, c) : all;
         if (rank == 0)
-            put_draw<DRAW>(a, r, 0, 0.0f, total);
+            put_row<DRAW>(a, r, total);
         row_sync(C);
         write_row(row, out, a.same_phase, end);
         return;
@@ -885,11 +898,11 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
     // 5. The bins.
     if (sc.cold) {
         if (rank == 0)
-            whole_row<T, DRAW>(a, r, g, m, end, s);
+            whole_row<T, DRAW>(a, r, g, m, end, s.scale, s);
         row_sync(C);
         return;
     }
-    const BinScale bs = bin_scale(m, sc);
+    const BinScale bs = bin_scale(m, g.T, sc);
     sc.top = ((long long)(int)(bs.ref - __float_as_uint(kMagicBin)) + 1) * (1ll << (48 - kBinShift));   // as the bins' masses
     int k = g.k;
     for (;;) {
@@ -970,7 +983,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
                                 n += (int)bin_count(s, i);
                             kept = (int)block_sum((u128)n, s);
                         } else if (!DRAW) {   // top-k reaches past the last token
-                            put_draw<DRAW>(a, r, 0, 0.0f, kept);
+                            put_row<DRAW>(a, r, kept);
                             c.op = kCmdWrite;
                             c.key = end.key;
                             c.index = end.index;
@@ -1008,7 +1021,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
                         stop = Prefix{entry_key(s.list[end_r]), entry_index(s.list[end_r])};
                         hi = end_r + 1;
                         if (!DRAW) {
-                            put_draw<DRAW>(a, r, 0, 0.0f, kept);
+                            put_row<DRAW>(a, r, kept);
                             c.op = kCmdWrite;
                             c.key = stop.key;
                             c.index = stop.index;
@@ -1024,7 +1037,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
                             // the point is in the last bin after all
                             const int at = rank_reaching(q, lo, hi, above, share_of(g.u, mass, false) + 1, s, at_mass);
                             const uint64_t e = s.list[at];
-                            put_draw<DRAW>(a, r, entry_index(e), (float)((double)weight62(value_of(entry_key(e)), sc, s.roots) / (double)mass), kept);
+                            put_row<DRAW>(a, r, kept, entry_index(e), weight62(value_of(entry_key(e)), sc, s.roots), mass);
                             draw_now = false;
                         } else if (stage == 2 && first_bin < last) {
                             hi = n_first < lo ? n_first : lo;
@@ -1034,14 +1047,14 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
                     if (draw_now) {
                         const int at = rank_reaching(q, 0, hi, above_first, share_of(g.u, mass, false) + 1, s, at_mass);
                         const uint64_t e = s.list[at];
-                        put_draw<DRAW>(a, r, entry_index(e), (float)((double)weight62(value_of(entry_key(e)), sc, s.roots) / (double)mass), kept);
+                        put_row<DRAW>(a, r, kept, entry_index(e), weight62(value_of(entry_key(e)), sc, s.roots), mass);
                     }
                 }
                 if (give_up) {
                     Settings rest = g;
                     rest.k = k;
                     c = Command{kCmdEnd, 0, 0, -1, 0, 0};
-                    whole_row<T, DRAW>(a, r, rest, m, end, s);
+                    whole_row<T, DRAW>(a, r, rest, m, end, s.scale, s);
                 }
                 __syncthreads();
                 if (t == 0) {
@@ -1083,7 +1096,7 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
             return;
         if (!DRAW && g.p >= 1.0f) {   // top-k was all there was
             if (rank == 0)
-                put_draw<DRAW>(a, r, 0, 0.0f, k);
+                put_row<DRAW>(a, r, k);
             write_row(row, out, a.same_phase, end);
             return;
         }

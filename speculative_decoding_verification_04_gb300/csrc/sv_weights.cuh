@@ -52,10 +52,11 @@ constexpr uint32_t kKeyPosInf = 0xff800000u;
 // to 2^12); rows beyond that take differences in 64 bits.
 struct RowScale {
     float ch, cl;       // log2(e) / T
-    float least;        // logits below it weigh nothing (less than 2^-64)
+    float m, least;     // logits below `least` weigh nothing (less than 2^-64)
     long long top;      // m log2(e) / T, units of 2^-48
-    double c, m;
+    double c;
     bool cold;
+    __device__ __forceinline__ void at(float m, float T);
 };
 
 __device__ __forceinline__ long long scaled48(float l, float ch, float cl)
@@ -65,17 +66,22 @@ __device__ __forceinline__ long long scaled48(float l, float ch, float cl)
     return __float2ll_rn(t * 281474976710656.0f) + __float2ll_rn(e * 281474976710656.0f);
 }
 
-__device__ __forceinline__ RowScale row_scale(float m, float T)
+// The constants of temperature T; the row's maximum goes in by at().
+__device__ __forceinline__ RowScale row_scale(float T)
 {
-    RowScale r;
+    RowScale r{};
     r.c = 1.4426950408889634 / (double)T;
-    r.m = (double)m;
     r.ch = (float)r.c;
     r.cl = (float)(r.c - (double)r.ch);
-    r.cold = !(fabs(r.m * r.c) < 4096.0) || T > 1e30f;   // (the split constant would be subnormal)
-    r.least = (float)fmax(r.m - 70.0 * (double)T, -3.4028234e38);
-    r.top = r.cold ? 0 : scaled48(m, r.ch, r.cl);
     return r;
+}
+
+__device__ __forceinline__ void RowScale::at(float m_, float T)
+{
+    m = m_;
+    cold = !(fabsf(m_) * ch < 4096.0f) || T > 1e30f;   // (the split constant would be subnormal)
+    least = fmaxf(m_ - 70.0f * T, -3.4028234e38f);
+    top = cold ? 0 : scaled48(m_, ch, cl);
 }
 
 // 2^-x in units of 2^-62, x >= 0 in units of 2^-48.  2^-x = 2^-n 2^(-j / 64) e^-y
@@ -102,7 +108,7 @@ __device__ __forceinline__ uint64_t weight62(float l, const RowScale& r, const u
         return 0;
     long long x;
     if (r.cold) {
-        const double d = (r.m - (double)l) * r.c;
+        const double d = ((double)r.m - (double)l) * r.c;
         x = d < 64.0 ? (long long)(d * 281474976710656.0) : 64ll << 48;
     } else {
         x = r.top - scaled48(l, r.ch, r.cl);
