@@ -43,9 +43,7 @@ sv_status check_rows(const void* logits, sv_dtype dtype, const float* temperatur
 int row_ctas(long long rows, long long row_bytes, int nsm)
 {
     int C = 1;
-    while (C < 16 && rows * C < nsm && row_bytes / C > 16384)
-        C *= 2;
-    while (C < 8 && row_bytes * (2 * nsm / C) > (64ll << 20) && row_bytes / C > 65536)
+    while (C < kClusterMost && rows * C < nsm && row_bytes / C > 16384)
         C *= 2;
     return C;
 }
@@ -60,7 +58,7 @@ template <typename T, bool DRAW> cudaError_t launch(FilterArgs& a, cudaStream_t 
         return e;
     static std::atomic<unsigned long long> ready{0};   // devices whose limits have been raised
     if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
-        e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(FilterShared));
+        e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)filter_smem_bytes(kGroupsMost));
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess)
@@ -70,10 +68,11 @@ template <typename T, bool DRAW> cudaError_t launch(FilterArgs& a, cudaStream_t 
     }
     const long long rows = (long long)a.B * a.S;
     a.C = row_ctas(rows, (long long)a.V * sizeof(T), nsm);
+    const int vectors = a.V / Elem<T>::E / a.C + 1, per = kGroup * kFilterThreads;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(rows * a.C));
     cfg.blockDim = dim3(kFilterThreads);
-    cfg.dynamicSmemBytes = sizeof(FilterShared);
+    cfg.dynamicSmemBytes = filter_smem_bytes((vectors + per - 1) / per);
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;

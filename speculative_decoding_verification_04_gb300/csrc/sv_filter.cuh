@@ -31,47 +31,66 @@ struct FilterArgs {
 };
 
 
-constexpr int kFilterThreads = 512;
+constexpr int kFilterThreads = 256;
 constexpr int kFilterWarps = kFilterThreads / 32;
+constexpr int kClusterMost = 16;
 constexpr int kGroup = 8;          // vectors of a thread whose maximum is kept
-constexpr int kGroupsMost = 24;    // sv_max_vocab on one CTA
+constexpr int kGroupsMost = 49;    // sv_max_vocab on one CTA
 constexpr int kList = 2048;        // tokens sorted at a time
-constexpr int kBoundMost = 384;    // thread maxima a top-k bound may count down
 constexpr int kBinShift = 6;       // 64 bins an octave of weights
 constexpr int kBins = 64 << kBinShift;
+constexpr int kBinsEach = kBins / kFilterThreads;
 constexpr uint32_t kCarryBits = 12;   // of a bin's upper word; its count above (V < 2^20)
+constexpr int kQueue = 320;        // a warp's tokens on their way to the bins: 63 and a vector each
 
 // What rank 0 of a row's cluster asks of all its CTAs next.
 enum : int { kCmdEnd = 0, kCmdGather = 1, kCmdWrite = 2, kCmdRecount = 3 };
 
-struct Command {
+struct alignas(16) Command {
     int op;
     int from, to, also;    // kCmdGather: bins from .. to, and bin `also`
     uint32_t key;          // kCmdWrite, kCmdRecount: the kept prefix's last token
     int index;
+    int top_k;             // kCmdRecount: the prefix is top-k's
+    int pad;
 };
 
 struct FilterShared {
     union {
+        uint64_t list[kList];
+        float queue[kFilterWarps][kQueue];
+    };
+    uint64_t roots[64];
+    u128 part[kFilterWarps];
+    u128 skip, found_mass;
+    Command cmd;
+    uint32_t warp_top[kFilterWarps], warp_low[kFilterWarps];
+    int warp_count[2][kFilterWarps];
+    uint32_t peer_top[kClusterMost], peer_bound[kClusterMost];   // what each CTA of the cluster found
+    int peer_cutoff[kClusterMost];
+    u128 peer_tail[kClusterMost];
+    int peer_gone[kClusterMost];
+    uint32_t least_key;    // min-p's border
+    int count;             // rank 0: entries of the list
+    int hits;              // groups that hold a candidate
+    int first;             // lowest index of the largest logit
+    int found, found_count;
+    uint16_t hit[kList];
+    // the maxima of each thread's groups (as many as the row has), then the bins
+    union alignas(16) {
         struct {
             uint32_t lo[kBins], hi[kBins];
         } bin;
         float group[kGroupsMost][kFilterThreads];
     };
-    uint64_t list[kList];
-    uint64_t roots[64];
-    u128 part[kFilterWarps];
-    u128 sum, found_mass;
-    Command cmd;
-    RowScale scale;
-    uint32_t least_key;    // min-p's border
-    float max_of[kFilterWarps];
-    float top;             // this CTA's largest logit
-    uint32_t bound;        // this CTA's lower bound for the top-k
-    int count;             // entries of this CTA's list
-    int first;             // lowest index of the largest logit
-    int found, found_r;
 };
+
+// Shared memory for rows of `groups` groups a CTA.
+constexpr size_t filter_smem_bytes(int groups)
+{
+    const size_t g = (size_t)groups * kFilterThreads * 4, b = (size_t)kBins * 8;
+    return sizeof(FilterShared) - sizeof(float) * kGroupsMost * kFilterThreads + (g > b ? g : b);
+}
 
 // ---------------------------------------------------------------------------
 // the row, the block and the cluster
@@ -83,7 +102,7 @@ struct FilterShared {
 template <typename T> struct RowSpan {
     static constexpr int E = Elem<T>::E;
     const T* p;
-    int V, head, nvec, v0, v1;
+    int V, head, nvec, v0, v1, rest;
     __device__ RowSpan(const T* row, int V_, int rank, int C) : p(row), V(V_)
     {
         const int phase = (int)(((uintptr_t)row & 15) / sizeof(T));
@@ -93,7 +112,6 @@ template <typename T> struct RowSpan {
         v1 = (int)((long long)nvec * (rank + 1) / C);
         rest = rank == 0 ? V - nvec * E : 0;
     }
-    int rest;
     __device__ __forceinline__ const uint4* vec() const { return reinterpret_cast<const uint4*>(p + head); }
     // the index of this thread's element outside the vectors, or -1
     __device__ __forceinline__ int lone() const
@@ -141,16 +159,28 @@ __device__ __forceinline__ uint32_t ld_rank(const void* p, int rank)
     return v;
 }
 
-__device__ __forceinline__ uint64_t ld_rank64(const void* p, int rank)
+__device__ __forceinline__ uint4 ld_rank128(const void* p, int rank)
 {
-    uint64_t v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to_rank(smem_addr(p), rank)) : "memory");
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(map_to_rank(smem_addr(p), rank)) : "memory");
     return v;
+}
+
+__device__ __forceinline__ void st_rank(void* p, int rank, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_addr(p), rank)), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_rank64(void* p, int rank, uint64_t v)
+{
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_to_rank(smem_addr(p), rank)), "l"(v) : "memory");
 }
 
 __device__ __forceinline__ void row_sync(int C)
 {
     if (C > 1) {
+        __syncwarp();
         cluster_arrive();
         cluster_wait();
     } else {
@@ -259,8 +289,7 @@ struct Settings {
     int k;
 };
 
-// A row's numbers.  (64-bit floating point runs at a hundredth of the fp32
-// rate: one thread's at most, never a block's.)
+// A row's numbers.
 template <bool DRAW>
 __device__ __forceinline__ void put_row(const FilterArgs& a, long long r, int kept, int token = -1, uint64_t weight = 0, u128 mass = 0)
 {
@@ -270,7 +299,7 @@ __device__ __forceinline__ void put_row(const FilterArgs& a, long long r, int ke
         if (DRAW) {
             a.out_tokens[r] = token;
             if (a.has_prob)
-                a.out_prob[r] = token < 0 ? __int_as_float(0x7fc00000) : (float)((double)weight / (double)mass);
+                a.out_prob[r] = token < 0 ? __int_as_float(0x7fc00000) : quotient(weight, mass);
         }
     }
 }
@@ -397,34 +426,45 @@ __device__ __forceinline__ uint64_t entry_of(uint32_t key, int index) { return (
 __device__ __forceinline__ uint32_t entry_key(uint64_t e) { return (uint32_t)(e >> 32); }
 __device__ __forceinline__ int entry_index(uint64_t e) { return (int)(0xffffffffu - (uint32_t)e); }
 
-__device__ __forceinline__ void append(FilterShared& s, uint32_t key, int index)
+// Into rank 0's list.
+__device__ __forceinline__ void append(FilterShared& s, int C, uint32_t key, int index, int n = 1)
 {
-    const int at = atomicAdd(&s.count, 1);
-    if (at < kList)
-        s.list[at] = entry_of(key, index);
+    if (C == 1) {
+        const int at = atomicAdd(&s.count, n);
+        if (at < kList)
+            s.list[at] = entry_of(key, index);
+    } else {
+        int at;
+        asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(map_to_rank(smem_addr(&s.count), 0)), "r"(n) : "memory");
+        if (at < kList)
+            st_rank64(&s.list[at], 0, entry_of(key, index));
+    }
 }
 
-// The lists of the cluster's CTAs one after the other in rank 0's; the total,
-// which every CTA learns (above kList: nothing is copied).  Ends the phase that
-// reads other CTAs' lists only with the next row_sync.
-__device__ __forceinline__ int collect(FilterShared& s, int rank, int C)
+// f(values, index of the first) for the vectors of the groups that reach `least`:
+// the groups are listed, then read by all threads, a vector each.
+template <typename T, typename F>
+__device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, float least, FilterShared& s, F&& f)
 {
-    row_sync(C);
-    int total = s.count;
-    if (C > 1) {
-        total = 0;
-        int before = 0;
-        for (int c = 0; c < C; ++c) {
-            const int n = (int)ld_rank(&s.count, c);
-            before = total;
-            total += n;
-            if (rank == 0 && c > 0 && total <= kList)
-                for (int i = threadIdx.x; i < n; i += kFilterThreads)
-                    s.list[before + i] = ld_rank64(&s.list[i], c);
+    constexpr int E = Elem<T>::E;
+    const int t = threadIdx.x;
+    for (int n = 0; n < groups; ++n)
+        if (s.group[n][t] >= least) {
+            const int at = atomicAdd(&s.hits, 1);
+            if (at < kList)
+                s.hit[at] = (uint16_t)(n * kFilterThreads + t);
         }
-        __syncthreads();
+    __syncthreads();
+    const int hits = min(s.hits, kList);
+    for (int j = t; j < hits * kGroup; j += kFilterThreads) {
+        const int h = s.hit[j / kGroup], n = h / kFilterThreads;
+        const int i = row.v0 + (n * kGroup + j % kGroup) * kFilterThreads + h % kFilterThreads;
+        if (i < row.v1) {
+            float x[E];
+            Elem<T>::unpack(row.vec()[i], x);
+            f(x, row.head + i * E);
+        }
     }
-    return total;
 }
 
 // Sorts list[0 .. n), the largest first.
@@ -441,7 +481,7 @@ __device__ __forceinline__ void sort_list(FilterShared& s, int n)
         if (t < n)
             s.list[r] = e;
     } else {
-        int size = 1024;
+        int size = 2 * kFilterThreads;
         while (size < n)
             size *= 2;
         for (int i = n + t; i < size; i += kFilterThreads)
@@ -491,39 +531,31 @@ __device__ __forceinline__ ListPart weigh_list(FilterShared& s, int n, const Row
 __device__ __forceinline__ int rank_reaching(const ListPart& q, int lo, int hi, u128 base, u128 goal, FilterShared& s, u128& mass)
 {
     __syncthreads();
-    if (threadIdx.x == 0) {
-        s.found_r = lo;
-        s.sum = 0;
-    }
-    __syncthreads();
-    u128 c = q.before;
-    if (lo > 0) {   // what is before rank lo
+    if (lo > 0) {   // less what is before rank lo
+        u128 c = q.before;
 #pragma unroll
         for (int i = 0; i < kList / kFilterThreads; ++i) {
             if (i < q.n && q.r0 + i == lo)
-                s.sum = c;
+                s.skip = c;
             c += q.w[i];
         }
+        __syncthreads();
+        base -= s.skip;   // (modulo 2^128: added to sums that hold it)
     }
-    __syncthreads();
-    const u128 skip = s.sum;
-    c = q.before;
+    u128 c = base + q.before;
 #pragma unroll
     for (int i = 0; i < kList / kFilterThreads; ++i) {
         const int r = q.r0 + i;
-        const u128 was = c;
+        const bool before = r > lo && c >= goal;
         c += q.w[i];
-        if (i < q.n && r >= lo && r < hi) {
-            const bool reached = base + (c - skip) >= goal, before = r > lo && base + (was - skip) >= goal;
-            if ((reached && !before) || (r == hi - 1 && !reached)) {
-                s.found_r = r;
-                s.found_mass = base + (c - skip);
-            }
+        if (i < q.n && r >= lo && r < hi && !before && (c >= goal || r == hi - 1)) {
+            s.found = r;
+            s.found_mass = c;
         }
     }
     __syncthreads();
     mass = s.found_mass;
-    return s.found_r;
+    return s.found;
 }
 
 // ---------------------------------------------------------------------------
@@ -532,22 +564,25 @@ __device__ __forceinline__ int rank_reaching(const ListPart& q, int lo, int hi, 
 // A bin holds the tokens whose l log2(e) / T rounds to the same 64th; it sums
 // 2^f - 1 of the remainders f, in units of 2^-29, and counts.  Bin 0 holds the
 // largest logit.  The last bin holds whatever weighs less than 2^-63 too; its
-// mass does not count.
+// mass does not count.  Weights are relative to 2^(1/64) times bin 0's centre.
 constexpr float kMagicBin = 196608.0f;       // 1.5 * 2^17: adding it rounds to 64ths
 constexpr float kMagicSum = 0.0234375f;      // 1.5 * 2^-6: adding it rounds to 2^-29
 
 struct BinScale {
     float ch, cl, least;   // least: below it, the last bin
+    float unit;            // the centre of the bin before the first, in 64ths of an octave
     uint32_t ref;          // the bits of the largest logit's rounded product
 };
 
-__device__ __forceinline__ BinScale bin_scale(float m, float T, const RowScale& sc)
+__device__ __forceinline__ BinScale bin_scale(const RowScale& sc)
 {
     BinScale b;
     b.ch = sc.ch;
     b.cl = sc.cl;
-    b.ref = __float_as_uint(__fadd_rn(__fmul_rn(m, sc.ch), kMagicBin));
-    b.least = fmaxf(m - 44.6f * T, -3.4028234e38f);   // (64.3 octaves)
+    const float at = __fadd_rn(__fmul_rn(sc.m, sc.ch), kMagicBin);
+    b.ref = __float_as_uint(at);
+    b.unit = (at - kMagicBin) + 0.015625f;
+    b.least = fmaxf(sc.m - 44.6f * sc.T, -3.4028234e38f);   // 64.3 octaves
     return b;
 }
 
@@ -582,48 +617,104 @@ __device__ __forceinline__ void bin_pair(FilterShared& s, float l0, float l1, bo
         bin_add(s, b.ref - (uint32_t)(at >> 32), (uint32_t)(q >> 32) - unit);
 }
 
+// 2^x of two x in (-100, 1) for sums of many: what matters is that errors cancel.
+// 2^f, |f| <= 1/2, by a polynomial fitted by least squares with no mean error:
+// 2^-22 at most, 2^-31 on average over f (ex2.approx leans to one side).
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x)
+{
+    const uint64_t magic = f2_pack(12582912.0f, 12582912.0f);   // 1.5 * 2^23: adding it rounds to whole numbers
+    const uint64_t n = f2_add(x, magic), f = f2_sub(x, f2_sub(n, magic));
+    uint64_t y = f2_fma(f, f2_pack(0x1.5a077ep-10f, 0x1.5a077ep-10f), f2_pack(0x1.3cb782p-7f, 0x1.3cb782p-7f));
+    y = f2_fma(f, y, f2_pack(0x1.c6ba68p-5f, 0x1.c6ba68p-5f));
+    y = f2_fma(f, y, f2_pack(0x1.ebfa54p-3f, 0x1.ebfa54p-3f));
+    y = f2_fma(f, y, f2_pack(0x1.62e428p-1f, 0x1.62e428p-1f));
+    y = f2_fma(f, y, f2_pack(1.0f, 1.0f));
+    const uint32_t lo = (uint32_t)y + ((uint32_t)n << 23), hi = (uint32_t)(y >> 32) + ((uint32_t)(n >> 32) << 23);
+    return ((uint64_t)hi << 32) | lo;
+}
+
 __device__ __forceinline__ uint32_t bin_count(const FilterShared& s, int i) { return s.bin.hi[i] >> kCarryBits; }
 
-// The mass of bin i in units of 2^-62, weights relative to 2^(1/64) times bin 0's centre.
+// The mass of bin i in units of 2^-62.
 __device__ __forceinline__ u128 bin_mass(const FilterShared& s, int i)
 {
-    if (i == kBins - 1)
-        return 0;
     const uint32_t hi = s.bin.hi[i], n = hi >> kCarryBits;
-    if (n == 0)
+    if (n == 0 || i == kBins - 1)
         return 0;
     const uint64_t sum = (((uint64_t)(hi & ((1u << kCarryBits) - 1)) << 32) | s.bin.lo[i]) + ((uint64_t)n << 29) - ((uint64_t)n << 22);
     return ((u128)sum * s.roots[(i + 1) & 63]) >> (29 + ((i + 1) >> 6));
 }
 
-// The bin where a running sum over all bins (counts, or masses) reaches `goal`;
-// what is before the bin in `before`.  kBins if it is not reached.
-template <bool kCount>
-__device__ __forceinline__ int bin_reaching(FilterShared& s, u128 goal, u128& before, u128& total)
+// A thread's bins (kBinsEach of them), and what is before them.
+struct BinPart {
+    u128 before, own;
+    int n_before, n_own;
+};
+
+__device__ __forceinline__ BinPart scan_bins(FilterShared& s, u128& mass, int& count)
 {
-    constexpr int per = kBins / kFilterThreads;
-    const int i0 = threadIdx.x * per;
-    u128 v = 0;
-    for (int i = 0; i < per; ++i)
-        v += kCount ? bin_count(s, i0 + i) : bin_mass(s, i0 + i);
-    u128 c = block_scan(v, s, total);
+    BinPart q;
+    q.own = 0;
+    q.n_own = 0;
+    const int i0 = threadIdx.x * kBinsEach;
+    for (int i = 0; i < kBinsEach; ++i) {
+        const int j = i0 + ((i + threadIdx.x) & (kBinsEach - 1));   // (lanes on different banks)
+        q.own += bin_mass(s, j);
+        q.n_own += (int)bin_count(s, j);
+    }
+    u128 total;
+    // the count in the low bits of one sum with the mass: masses are below 2^83
+    const u128 both = block_scan((q.own << 24) | (u128)(uint32_t)q.n_own, s, total);
+    q.before = both >> 24;
+    q.n_before = (int)((uint32_t)both & 0xffffffu);
+    mass = total >> 24;
+    count = (int)((uint32_t)total & 0xffffffu);
+    return q;
+}
+
+// The bin where the running sum over all bins, of counts or of masses, reaches
+// `goal` (kBins if it is not reached), and what is before it.
+struct BinAt {
+    int bin, n_before;
+    u128 before;
+};
+
+template <bool kCount> __device__ __forceinline__ BinAt bin_reaching(const BinPart& q, FilterShared& s, u128 goal)
+{
     __syncthreads();
     if (threadIdx.x == 0)
-        s.found = kBins;
+        s.found = -1;
     __syncthreads();
-    if (c < goal && goal <= c + v)
-        for (int i = 0; i < per; ++i) {
-            const u128 x = kCount ? bin_count(s, i0 + i) : bin_mass(s, i0 + i);
-            if (goal <= c + x) {
-                s.found = i0 + i;
-                s.found_mass = c;
-                break;
-            }
-            c += x;
+    const u128 c = kCount ? (u128)(uint32_t)q.n_before : q.before, v = kCount ? (u128)(uint32_t)q.n_own : q.own;
+    if (c < goal && goal <= c + v) {
+        s.found = threadIdx.x;
+        s.found_count = q.n_before;
+        s.found_mass = q.before;
+    }
+    __syncthreads();
+    BinAt r{kBins, 0, 0};
+    if (s.found >= 0) {   // every warp goes through that thread's bins, one a lane
+        const int lane = threadIdx.x & 31, i = s.found * kBinsEach + lane;
+        u128 own = 0;
+        if (lane < kBinsEach)
+            own = (bin_mass(s, i) << 24) | bin_count(s, i);
+        u128 x = own;
+#pragma unroll
+        for (int o = 1; o < kBinsEach; o <<= 1) {
+            const u128 y = shfl_up128(x, o);
+            if (lane >= o)
+                x += y;
         }
-    __syncthreads();
-    before = s.found_mass;
-    return s.found;
+        const u128 base = (s.found_mass << 24) | (u128)(uint32_t)s.found_count;
+        const u128 to = base + x, from = to - own;
+        const bool here = lane < kBinsEach && (kCount ? (u128)((uint32_t)to & 0xffffffu) : to >> 24) >= goal;
+        const int l = __ffs(__ballot_sync(kFull, here)) - 1;
+        r.bin = s.found * kBinsEach + l;
+        r.before = ((u128)__shfl_sync(kFull, (unsigned long long)(from >> 64), l) << 64) | __shfl_sync(kFull, (unsigned long long)from, l);
+        r.n_before = (int)((uint32_t)r.before & 0xffffffu);
+        r.before >>= 24;
+    }
+    return r;
 }
 
 // All of the cluster's bins in rank 0's.
@@ -632,33 +723,378 @@ __device__ __forceinline__ void merge_bins(FilterShared& s, int rank, int C)
     row_sync(C);
     if (C == 1)
         return;
-    const int per = (kBins + C - 1) / C, i0 = rank * per, i1 = min(kBins, i0 + per);
-    for (int i = i0 + threadIdx.x; i < i1; i += kFilterThreads) {
-        uint64_t lo = 0;
-        uint32_t hi = 0;
+    const int per = kBins / C, i0 = rank * per, t = threadIdx.x;   // (C is a power of two)
+    for (int i = i0 + 4 * t; i < i0 + per; i += 4 * kFilterThreads) {
+        uint64_t lo[4] = {0, 0, 0, 0};
+        uint32_t hi[4] = {0, 0, 0, 0};
+#pragma unroll 4
         for (int c = 0; c < C; ++c) {
-            lo += ld_rank(&s.bin.lo[i], c);
-            hi += ld_rank(&s.bin.hi[i], c);
+            const uint4 x = ld_rank128(&s.bin.lo[i], c), y = ld_rank128(&s.bin.hi[i], c);
+            lo[0] += x.x, lo[1] += x.y, lo[2] += x.z, lo[3] += x.w;
+            hi[0] += y.x, hi[1] += y.y, hi[2] += y.z, hi[3] += y.w;
         }
-        s.bin.lo[i] = (uint32_t)lo;
-        s.bin.hi[i] = hi + (uint32_t)(lo >> 32);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s.bin.lo[i + j] = (uint32_t)lo[j];
+            s.bin.hi[i + j] = hi[j] + (uint32_t)(lo[j] >> 32);
+        }
     }
     row_sync(C);
     if (rank == 0) {
-        for (int i = per + threadIdx.x; i < kBins; i += kFilterThreads) {
+#pragma unroll 4
+        for (int i = per + 4 * t; i < kBins; i += 4 * kFilterThreads) {
             const int c = i / per;
-            s.bin.lo[i] = ld_rank(&s.bin.lo[i], c);
-            s.bin.hi[i] = ld_rank(&s.bin.hi[i], c);
+            *reinterpret_cast<uint4*>(&s.bin.lo[i]) = ld_rank128(&s.bin.lo[i], c);
+            *reinterpret_cast<uint4*>(&s.bin.hi[i]) = ld_rank128(&s.bin.hi[i], c);
         }
         __syncthreads();
     }
+}
+
+// The sums of a CTA's part of the row.  With `tail` only the tokens around and
+// above where a sample of the row reaches the share `target` go through the
+// bins, and the rest are summed on the way (fp32 weights, their sums
+// compensated: the rest is a small part of the mass).  Returns the last bin that
+// is complete, the mass that is in no bin, and with `tail` how many logits are
+// -inf.
+template <typename T>
+__device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Prefix end, bool tail, float target, const BinScale& b,
+                                         FilterShared& s, u128& rest, int& gone)
+{
+    constexpr int E = Elem<T>::E;
+    const int t = threadIdx.x, lane = t & 31;
+    rest = 0;
+    gone = 0;
+    __syncthreads();
+    for (int i = t; i < kBins; i += kFilterThreads)
+        s.bin.lo[i] = s.bin.hi[i] = 0;
+    __syncthreads();
+    const float least = value_of(end.key);
+    const int lone = row.lone();
+    if (lone >= 0)
+        bin_pair(s, lone_x, lone_x, end.has(key_of(lone_x), lone), false, b);
+    if (!tail) {
+        row.vectors([&](const float (&x)[E], int i) {
+#pragma unroll
+            for (int j = 0; j < E; j += 2)
+                bin_pair(s, x[j], x[j + 1], x[j] > least || (x[j] == least && i + j <= end.index),
+                         x[j + 1] > least || (x[j + 1] == least && i + j + 1 <= end.index), b);
+        });
+        return kBins - 1;
+    }
+    int none = lone >= 0 && lone_x < least;
+    // the sample: every eighth stretch of vectors
+    const uint4* v = row.vec();
+    for (int i = row.v0 + t; i < row.v1; i += kGroup * kFilterThreads) {
+        float x[E];
+        Elem<T>::unpack(v[i], x);
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+            bin_pair(s, x[j], x[j + 1], x[j] >= least, x[j + 1] >= least, b);
+            none += (x[j] < least) + (x[j + 1] < least);
+        }
+    }
+    __syncthreads();
+    u128 mass;
+    int count;
+    const BinPart part = scan_bins(s, mass, count);
+    int cutoff = kBins - 1;
+    if (count > 0) {   // a quarter of what the sample leaves behind the target, a 64th of the mass at most
+        const u128 quarter = share_of(1.0f - target, mass, false) >> 2, beyond = quarter < mass >> 6 ? quarter : mass >> 6;
+        const BinAt at = bin_reaching<false>(part, s, mass - beyond);
+        cutoff = min(kBins - 1, at.bin + 8);
+    }
+    const float from = fmaxf(least, (b.unit - (float)(cutoff + 3) * 0.015625f) / b.ch);
+    float* queue = s.queue[t >> 5];
+    float sum = 0.0f, carry = 0.0f;
+    int waiting = 0;
+    const uint64_t ch2 = f2_pack(b.ch, b.ch), cl2 = f2_pack(b.cl, b.cl), unit2 = f2_pack(-b.unit, -b.unit);
+    auto take = [&](uint4 w, bool there) {
+        float x[E];
+        Elem<T>::unpack(w, x);
+        uint64_t add = 0;   // (+0, +0)
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+            const uint64_t L = f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least));
+            float w0, w1;
+            f2_unpack(exp2_pair(f2_fma(L, cl2, f2_fma(L, ch2, unit2))), w0, w1);
+            add = f2_add(add, f2_pack(x[j] < from ? w0 : 0.0f, x[j + 1] < from ? w1 : 0.0f));
+        }
+        float lo, hi, low = x[0];
+        f2_unpack(add, lo, hi);
+#pragma unroll
+        for (int j = 1; j < E; ++j)
+            low = fminf(low, x[j]);
+        if (there && low < least)
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                none += x[j] < least;
+        if (there) {
+            float e;
+            two_sum(sum, lo + hi, sum, e);
+            carry += e;
+        }
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const bool in = there && x[j] >= from;
+            const uint32_t who = __ballot_sync(kFull, in);
+            if (in)
+                queue[waiting + __popc(who & ((1u << lane) - 1))] = x[j];
+            waiting += __popc(who);
+        }
+        __syncwarp();
+        if (waiting >= 64) {
+            int at = 0;
+            for (; at + 64 <= waiting; at += 64)
+                bin_pair(s, queue[at + lane], queue[at + 32 + lane], true, true, b);
+            const float left0 = at + lane < waiting ? queue[at + lane] : 0.0f, left1 = at + 32 + lane < waiting ? queue[at + 32 + lane] : 0.0f;
+            __syncwarp();
+            queue[lane] = left0;
+            queue[lane + 32] = left1;
+            waiting -= at;
+            __syncwarp();
+        }
+    };
+    for (int n0 = row.v0; n0 < row.v1; n0 += kGroup * kFilterThreads) {
+        uint4 w[kGroup - 1];
+#pragma unroll
+        for (int u = 1; u < kGroup; ++u) {
+            const int i = n0 + u * kFilterThreads + t;
+            w[u - 1] = i < row.v1 ? v[i] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 1; u < kGroup; ++u)
+            take(w[u - 1], n0 + u * kFilterThreads + t < row.v1);
+    }
+    if (lane < waiting)
+        bin_pair(s, queue[lane], queue[lane + 32], true, lane + 32 < waiting, b);
+    // units of 2^-62, and the count below them
+    const u128 both = block_sum((u128)__float2ull_rn((sum + carry) * 1125899906842624.0f) << 36 | (u128)(uint32_t)none, s);
+    rest = both >> 24;
+    gone = (int)((uint32_t)both & 0xffffffu);
+    return cutoff;
 }
 
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
 template <typename T, bool DRAW>
-__global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs a)
+__device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const Settings& g, const RowSpan<T>& row, int rank, Prefix end,
+                                        float lone_x, const RowScale& whole, FilterShared& s)
+{
+    const int C = a.C, t = threadIdx.x;
+    T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * a.V);
+    const BinScale bs = bin_scale(whole);
+    RowScale sc = whole;
+    sc.top = ((long long)(int)(bs.ref - __float_as_uint(kMagicBin)) + 1) * (1ll << (48 - kBinShift));   // as the bins' masses
+    int k = g.k;
+    bool tail = k == 0 && g.min_p == 0.0f;
+    for (;;) {
+        u128 rest;
+        int gone, complete = fill_bins(row, lone_x, end, tail, g.p < 1.0f ? g.p : g.u, bs, s, rest, gone);
+        if (C > 1 && t == 0) {
+            st_rank(&s.peer_cutoff[rank], 0, (uint32_t)complete);
+            st_rank(&s.peer_gone[rank], 0, (uint32_t)gone);
+            st_rank64(&s.peer_tail[rank], 0, (uint64_t)rest);
+            st_rank64(reinterpret_cast<uint64_t*>(&s.peer_tail[rank]) + 1, 0, (uint64_t)(rest >> 64));
+        }
+        merge_bins(s, rank, C);
+        bool again = false, c_top_k = false;
+        int stage = 0;   // rank 0's: what the gathered list is for
+        int kept = 0, last = 0, lo_first = 0, n_last = 0;
+        u128 above = 0, above_first = 0, total = 0, mass = 0;
+        BinPart part{};
+        for (;;) {
+            if (rank == 0) {
+                Command c{kCmdEnd, 0, 0, -1, 0, 0, 0, 0};
+                bool give_up = false;
+                if (stage == 0) {
+                    int n_all;
+                    if (C > 1) {
+                        rest = 0;
+                        gone = 0;
+                        for (int i = 0; i < C; ++i) {
+                            gone += s.peer_gone[i];
+                            complete = min(complete, s.peer_cutoff[i]);
+                            rest += s.peer_tail[i];
+                        }
+                    }
+                    part = scan_bins(s, total, n_all);
+                    total += rest;
+                    if (tail)
+                        n_all = a.V - gone;
+                    if (k > 0 && k < n_all) {   // top-k first: its last token
+                        const BinAt at = bin_reaching<true>(part, s, (u128)(uint32_t)k);
+                        stage = 1;
+                        kept = k - at.n_before;
+                        c.op = kCmdGather;
+                        c.from = c.to = c.also = at.bin;
+                        give_up = bin_count(s, at.bin) > kList;
+                    } else if (g.p < 1.0f) {
+                        stage = 2;
+                        const u128 share = share_of(g.p, total, true), goal = share > 1 ? share : 1;
+                        const BinAt end_at = bin_reaching<false>(part, s, goal);
+                        last = end_at.bin;
+                        above = above_first = end_at.before;
+                        kept = end_at.n_before;
+                        int first = last, n_first = end_at.n_before;
+                        if (last > complete) {
+                            c.op = kCmdRecount;   // the sample misled: all of it through the bins
+                        } else {
+                            n_last = (int)bin_count(s, last);
+                            if (DRAW) {
+                                // the draw's point lies between u times the goal and that plus u times a token of the last bin
+                                const BinAt d0 = bin_reaching<false>(part, s, share_of(g.u, goal, false) + 1);
+                                const u128 one = ((u128)s.roots[last & 63] >> (last >> 6)) + (total >> 24);
+                                const BinAt d1 = bin_reaching<false>(part, s, share_of(g.u, goal + one, false) + 1);
+                                first = min(d0.bin, last);
+                                c.to = min(d1.bin, last);
+                                // bins first .. to and the last one
+                                n_first = (c.to < last ? d1.n_before + (int)bin_count(s, c.to) : kept) - d0.n_before;
+                                above_first = d0.before;
+                                if (d0.bin >= last || n_first + n_last > kList) {   // not both at once: the last bin first
+                                    first = last;
+                                    above_first = above;
+                                }
+                            }
+                            c.op = kCmdGather;
+                            c.from = first;
+                            c.to = first == last ? last : c.to;
+                            c.also = last;
+                            lo_first = first;
+                            give_up = n_last > kList;
+                        }
+                    } else if (!DRAW) {   // top-k reaches past the last token
+                        put_row<DRAW>(a, r, n_all);
+                        c.op = kCmdWrite;
+                        c.key = end.key;
+                        c.index = end.index;
+                    } else {
+                        kept = n_all;
+                        mass = total;
+                        const BinAt at = bin_reaching<false>(part, s, share_of(g.u, total, false) + 1);
+                        stage = 4;
+                        above_first = at.before;
+                        if (at.bin > complete) {
+                            c.op = kCmdRecount;
+                        } else {
+                            c.op = kCmdGather;
+                            c.from = c.to = c.also = at.bin;
+                            give_up = bin_count(s, at.bin) > kList;
+                        }
+                    }
+                    if (c.op == kCmdRecount) {
+                        c.key = end.key;
+                        c.index = end.index;
+                    }
+                } else {
+                    const int n = s.count;
+                    sort_list(s, n);
+                    if (stage == 1) {
+                        const uint64_t e = s.list[kept - 1];
+                        c.op = kCmdRecount;
+                        c.top_k = 1;
+                        c.key = entry_key(e);
+                        c.index = entry_index(e);
+                    } else {
+                        u128 sum, to;
+                        const ListPart q = weigh_list(s, n, sc, sum);
+                        int lo = 0, hi = n;   // where the draw is looked for
+                        bool draw_now = DRAW;
+                        if (stage == 2) {
+                            const int from = n - n_last;   // the last bin's tokens
+                            u128 own;
+                            rank_reaching(q, from, n, 0, ~(u128)0, s, own);
+                            // the goal again, with that bin's mass by its tokens
+                            const u128 goal = share_of(g.p, total - bin_mass(s, last) + own, true);
+                            const int end_r = rank_reaching(q, from, n, above, goal > 1 ? goal : 1, s, mass);
+                            kept += end_r - from + 1;
+                            if (!DRAW) {
+                                put_row<DRAW>(a, r, kept);
+                                c.op = kCmdWrite;
+                                c.key = entry_key(s.list[end_r]);
+                                c.index = entry_index(s.list[end_r]);
+                            } else if (share_of(g.u, mass, false) + 1 > above) {   // the draw is in the last bin
+                                lo = from;
+                                hi = end_r + 1;
+                                above_first = above;
+                            } else if (lo_first < last) {                          // in the bins before it that are here
+                                hi = from;
+                            } else {                                               // in one that is not
+                                draw_now = false;
+                                const BinAt at = bin_reaching<false>(part, s, share_of(g.u, mass, false) + 1);
+                                stage = 4;
+                                above_first = at.before;
+                                c.op = kCmdGather;
+                                c.from = c.to = c.also = at.bin;
+                                give_up = bin_count(s, at.bin) > kList;
+                            }
+                        }
+                        if (draw_now) {
+                            const int at = rank_reaching(q, lo, hi, above_first, share_of(g.u, mass, false) + 1, s, to);
+                            const uint64_t e = s.list[at];
+                            put_row<DRAW>(a, r, kept, entry_index(e), weight62(value_of(entry_key(e)), sc, s.roots), mass);
+                        }
+                    }
+                }
+                if (give_up) {
+                    Settings left = g;
+                    left.k = k;
+                    c = Command{kCmdEnd, 0, 0, -1, 0, 0, 0, 0};
+                    whole_row<T, DRAW>(a, r, left, whole.m, end, whole, s);
+                }
+                __syncthreads();
+                if (t == 0) {
+                    s.cmd = c;
+                    s.count = 0;
+                }
+            }
+            row_sync(C);
+            Command c;
+            if (C > 1) {
+                const uint4 x = ld_rank128(&s.cmd, 0), y = ld_rank128(reinterpret_cast<const char*>(&s.cmd) + 16, 0);
+                c = Command{(int)x.x, (int)x.y, (int)x.z, (int)x.w, y.x, (int)y.y, (int)y.z, 0};
+            } else {
+                c = s.cmd;
+            }
+            if (c.op == kCmdEnd)
+                break;
+            if (c.op == kCmdGather) {
+                row.each([&](float x, int i) {
+                    const int n = bin_of(x, bs);
+                    if (((n >= c.from && n <= c.to) || n == c.also) && end.has(key_of(x), i))
+                        append(s, C, key_of(x), i);
+                });
+                row_sync(C);
+                continue;
+            }
+            if (c.op == kCmdWrite) {
+                write_row(row, out, a.same_phase, Prefix{c.key, c.index});
+                break;
+            }
+            again = true;   // kCmdRecount
+            c_top_k = c.top_k;
+            end = Prefix{c.key, c.index};
+            break;
+        }
+        if (!again)
+            return;
+        row_sync(C);   // the bins and the command have been read
+        if (c_top_k) {
+            if (!DRAW && g.p >= 1.0f) {   // top-k was all there was
+                if (rank == 0)
+                    put_row<DRAW>(a, r, k);
+                write_row(row, out, a.same_phase, end);
+                return;
+            }
+            k = 0;
+        }
+        tail = false;
+    }
+}
+
+template <typename T, bool DRAW>
+__global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs a)
 {
     extern __shared__ __align__(16) unsigned char filter_smem[];
     FilterShared& s = *reinterpret_cast<FilterShared*>(filter_smem);
@@ -685,12 +1121,9 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
     T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * V);
     const RowSpan<T> row(logits, V, rank, C);
 
-    double t_log = 0.0;   // thread 0's: what of the row's constants does not need its maximum
-    if (t == 0 && good && !greedy) {
-        s.scale = row_scale(g.T);
-        if (g.min_p > 0.0f)
-            t_log = (double)g.T * log((double)g.min_p);
-    }
+    double t_log = 0.0;   // one thread's: 64-bit floating point runs at a hundredth of the fp32 rate
+    if (t == kFilterThreads - 32 && good && !greedy && g.min_p > 0.0f)
+        t_log = (double)g.T * log((double)g.min_p);
 
     // 1. The maxima of the row, of each thread, and of each thread's groups of
     // vectors: the one pass that has to read everything from memory.
@@ -731,31 +1164,54 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
         s.roots[t] = root_power(t);
     if (t == 0) {
         s.count = 0;
+        s.hits = 0;
         s.first = INT_MAX;
     }
-    const float warp_top = warp_max_nan(mine);
-    if ((t & 31) == 0)
-        s.max_of[t >> 5] = warp_top;
+    const uint32_t own_key = key_of(mine);
+    {
+        const uint32_t top = __reduce_max_sync(kFull, own_key), low = __reduce_min_sync(kFull, own_key);
+        if ((t & 31) == 0) {
+            s.warp_top[t >> 5] = top;
+            s.warp_low[t >> 5] = low;
+        }
+    }
     __syncthreads();
-    float m = s.max_of[0];
+    uint32_t top_key = 0, low_key = 0xffffffffu;
 #pragma unroll
-    for (int i = 1; i < kFilterWarps; ++i)
-        m = max_nan(m, s.max_of[i]);
+    for (int i = 0; i < kFilterWarps; ++i) {
+        top_key = max(top_key, s.warp_top[i]);
+        low_key = min(low_key, s.warp_low[i]);
+    }
 
     // 2. With top-k, a logit that at least k of the row reach: in each of C CTAs
-    // the k / C-th of the threads' maxima (about), the lowest of these.
+    // the k / C-th (or a few after it) of the threads' or the groups' maxima, and
+    // the lowest of these.
     const int share = (g.k + C - 1) / C;
-    const bool bounded = !greedy && g.k > 0 && share <= kBoundMost;
+    const bool by_thread = share <= kFilterThreads / 2;
+    const bool bounded = !greedy && g.k > 0 && (by_thread || (share <= groups * (kFilterThreads / 2) && g.k <= kList / 2));
     uint32_t bound = 0;
-    if (bounded) {
-        const uint32_t key = key_of(mine);
-        uint32_t lo = 0, hi = m < INFINITY ? key_of(m) : 0;   // (a NaN or +inf: no token will come of it)
-        while (lo < hi) {
+    if (bounded && top_key < kKeyPosInf) {   // (a NaN or +inf: no token will come of it)
+        uint32_t lo = by_thread ? low_key : 0, hi = top_key;
+        for (int turn = 0; lo < hi; turn ^= 1) {
             const uint32_t mid = lo + (hi - lo) / 2 + 1;
-            const int n = __syncthreads_count(key >= mid);
+            int n = own_key >= mid;
+            if (!by_thread) {
+                const float pivot = value_of(mid);
+                n = 0;
+                for (int i = 0; i < groups; ++i)
+                    n += s.group[i][t] >= pivot;
+            }
+            n = __reduce_add_sync(kFull, n);
+            if ((t & 31) == 0)
+                s.warp_count[turn][t >> 5] = n;
+            __syncthreads();
+            n = 0;
+#pragma unroll
+            for (int i = 0; i < kFilterWarps; ++i)
+                n += s.warp_count[turn][i];
             if (n >= share) {
                 lo = mid;
-                if (n <= share + share / 4 + 4)
+                if (n <= share + share / 2 + 8)
                     break;
             } else {
                 hi = mid - 1;
@@ -764,90 +1220,90 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
         bound = lo;
     }
     if (C > 1) {
-        if (t == 0) {
-            s.top = m;
-            s.bound = bound;
+        if (t < C) {
+            st_rank(&s.peer_top[rank], t, top_key);
+            st_rank(&s.peer_bound[rank], t, bound);
         }
         row_sync(C);
         for (int c = 0; c < C; ++c) {
-            m = max_nan(m, __uint_as_float(ld_rank(&s.top, c)));
-            bound = min(bound, ld_rank(&s.bound, c));
+            top_key = max(top_key, s.peer_top[c]);
+            bound = min(bound, s.peer_bound[c]);
         }
     }
 
-    const bool usable = good && m > -INFINITY && m < INFINITY;
-    if (!usable) {
+    if (!good || top_key <= kKeyNegInf || top_key >= kKeyPosInf) {
         if (rank == 0)
             put_row<DRAW>(a, r, -1);
         if (!DRAW)
             fill_row(row, out, a.same_phase, Bits<T>::nan);
-        row_sync(C);
         return;
     }
-    const uint32_t top_key = key_of(m);
+    const float m = value_of(top_key);
     if (greedy) {
-        for (int n = 0; n < groups; ++n)
-            if (s.group[n][t] == m)
-                for (int u = 0; u < kGroup; ++u) {
-                    const int i = row.v0 + (n * kGroup + u) * kFilterThreads + t;
-                    if (i < row.v1) {
-                        float x[E];
-                        Elem<T>::unpack(row.vec()[i], x);
+        each_hit(row, groups, m, s, [&](const float (&x)[E], int i) {
 #pragma unroll
-                        for (int k = E - 1; k >= 0; --k)
-                            if (x[k] == m)
-                                atomicMin(&s.first, row.head + i * E + k);
-                    }
-                }
+            for (int k = E - 1; k >= 0; --k)
+                if (x[k] == m)
+                    atomicMin(&s.first, i + k);
+        });
+        // (more hits than the list of them holds: by all threads' groups)
+        if (s.hits > kList)
+            row.each([&](float x, int i) {
+                if (x == m)
+                    atomicMin(&s.first, i);
+            });
         if (lone >= 0 && lone_x == m)
             atomicMin(&s.first, lone);
         row_sync(C);
         int first = s.first;
-        for (int c = 1; c < C; ++c)
-            first = min(first, (int)ld_rank(&s.first, c == rank ? 0 : c));
+        for (int c = 0; c < C; ++c)
+            if (c != rank)
+                first = min(first, (int)ld_rank(&s.first, c));
         if (rank == 0)
             put_row<DRAW>(a, r, 1, first, 1, 1);
-        row_sync(C);
         if (!DRAW)
             write_row(row, out, a.same_phase, Prefix{top_key, first});
+        row_sync(C);
         return;
     }
 
-    if (t == 0) {
-        s.scale.at(m, g.T);
-        s.least_key = max(kKeyNegInf + 1, g.min_p > 0.0f ? min_p_key(m, t_log) : 0u);
+    Prefix end{kKeyNegInf + 1, INT_MAX};
+    if (g.min_p > 0.0f) {
+        if (t == kFilterThreads - 32)
+            s.least_key = min_p_key(m, t_log);
+        __syncthreads();
+        end.key = max(end.key, s.least_key);
     }
-    __syncthreads();
-    Prefix end{s.least_key, INT_MAX};
-    RowScale sc = s.scale;
+    const RowScale sc = row_scale(m, g.T);
 
     // 3. Few candidates (a top-k bound, min-p, or a short row): they are read
     // again, by the groups that hold one, sorted and weighed.
     if (bounded || g.min_p > 0.0f || V <= kList) {
         const uint32_t cut = max(end.key, bound);
         const float cv = value_of(cut);
-        for (int n = 0; n < groups; ++n)
-            if (s.group[n][t] >= cv)
-                for (int u = 0; u < kGroup; ++u) {
-                    const int i = row.v0 + (n * kGroup + u) * kFilterThreads + t;
-                    if (i < row.v1) {
-                        float x[E];
-                        Elem<T>::unpack(row.vec()[i], x);
+        each_hit(row, groups, cv, s, [&](const float (&x)[E], int i) {
 #pragma unroll
-                        for (int k = 0; k < E; ++k)
-                            if (x[k] >= cv)
-                                append(s, key_of(x[k]), row.head + i * E + k);
-                    }
-                }
+            for (int k = 0; k < E; ++k)
+                if (x[k] >= cv)
+                    append(s, C, key_of(x[k]), i + k);
+        });
         if (lone >= 0 && lone_x >= cv)
-            append(s, key_of(lone_x), lone);
-        int n = collect(s, rank, C);
+            append(s, C, key_of(lone_x), lone);
+        if (t == 0 && s.hits > kList)   // (each holds a candidate)
+            append(s, C, 0, 0, kList + 1);
+        row_sync(C);
+        int n = C > 1 && rank != 0 ? (int)ld_rank(&s.count, 0) : s.count;
         if (n <= kList) {
             if (!DRAW)
                 fill_row(row, out, a.same_phase, Bits<T>::ninf);
-            row_sync(C);   // lists have been read; all of out is -inf
-            if (rank != 0)
-                return;
+            if (C > 1) {   // the count has been read, and this part of out is -inf
+                __syncwarp();
+                cluster_arrive();
+                if (rank != 0) {
+                    cluster_wait();
+                    return;
+                }
+            }
             sort_list(s, n);
             if (g.k > 0)
                 n = min(n, g.k);
@@ -866,14 +1322,20 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
                 put_row<DRAW>(a, r, n, entry_index(e), weight62(value_of(entry_key(e)), sc, s.roots), mass);
             } else {
                 put_row<DRAW>(a, r, n);
-                for (int i = t; i < n; i += kFilterThreads) {
-                    const int j = entry_index(s.list[i]);
-                    out[j] = (T)value_of(entry_key(s.list[i]));
-                }
             }
+            __syncwarp();
+            if (C > 1)
+                cluster_wait();
+            else
+                __syncthreads();
+            if (!DRAW)
+                for (int i = t; i < n; i += kFilterThreads)
+                    out[entry_index(s.list[i])] = (T)value_of(entry_key(s.list[i]));
             return;
         }
-        row_sync(C);   // too many (every CTA has read the counts): the bins take them
+        row_sync(C);   // too many (every CTA has read the count): the bins take them
+        if (t == 0)
+            s.count = 0;
     }
 
     // 4. Nothing but min-p, if that: every token above its border stays.
@@ -881,227 +1343,29 @@ __global__ void __launch_bounds__(kFilterThreads, 2) sv_filter_kernel(FilterArgs
         int n = 0;
         const float least = value_of(end.key);
         row.each([&](float x, int) { n += x >= least; });
-        const int all = (int)block_sum((u128)n, s);
-        if (t == 0)
-            s.count = all;
-        row_sync(C);
-        int total = 0;
-        for (int c = 0; c < C; ++c)
-            total += C > 1 ? (int)ld_rank(&s.count, c) : all;
+        const int all = (int)block_sum((u128)(uint32_t)n, s);
+        write_row(row, out, a.same_phase, end);
+        if (C > 1) {
+            if (t == 0)
+                st_rank(&s.peer_gone[rank], 0, (uint32_t)all);
+            row_sync(C);
+        }
+        int total = all;
+        for (int c = 1; c < C; ++c)
+            total += s.peer_gone[c];
         if (rank == 0)
             put_row<DRAW>(a, r, total);
-        row_sync(C);
-        write_row(row, out, a.same_phase, end);
         return;
     }
 
     // 5. The bins.
     if (sc.cold) {
         if (rank == 0)
-            whole_row<T, DRAW>(a, r, g, m, end, s.scale, s);
-        row_sync(C);
+            whole_row<T, DRAW>(a, r, g, m, end, sc, s);
         return;
     }
-    const BinScale bs = bin_scale(m, g.T, sc);
-    sc.top = ((long long)(int)(bs.ref - __float_as_uint(kMagicBin)) + 1) * (1ll << (48 - kBinShift));   // as the bins' masses
-    int k = g.k;
-    for (;;) {
-        __syncthreads();
-        for (int i = t; i < kBins; i += kFilterThreads)
-            s.bin.lo[i] = s.bin.hi[i] = 0;
-        __syncthreads();
-        const float least = value_of(end.key);
-        const bool all = end.index == INT_MAX;
-        row.vectors([&](const float (&x)[E], int i) {
-#pragma unroll
-            for (int j = 0; j < E; j += 2)
-                bin_pair(s, x[j], x[j + 1], x[j] > least || (x[j] == least && (all || i + j <= end.index)),
-                         x[j + 1] > least || (x[j + 1] == least && (all || i + j + 1 <= end.index)), bs);
-        });
-        if (lone >= 0)
-            bin_pair(s, lone_x, lone_x, lone_x > least || (lone_x == least && lone <= end.index), false, bs);
-        merge_bins(s, rank, C);
-        bool again = false;
-        Prefix stop{0, 0};
-        int stage = 0;   // rank 0's: what the gathered list is for
-        int kept = 0, last = 0, first_bin = 0, n_first = 0, listed = 0;
-        u128 above = 0, above_first = 0, total = 0, mass = 0, goal = 0;
-        for (;;) {
-            if (rank == 0) {
-                Command c{kCmdEnd, 0, 0, -1, 0, 0};
-                bool give_up = false;
-                if (stage == 0) {
-                    u128 n_all, before;
-                    const int bk = bin_reaching<true>(s, k > 0 ? (u128)k : ~(u128)0, before, n_all);
-                    if (k > 0 && (u128)k < n_all) {   // top-k first: its last token
-                        stage = 1;
-                        kept = k - (int)before;
-                        c.op = kCmdGather;
-                        c.from = c.to = c.also = bk;
-                        give_up = bin_count(s, bk) > kList;
-                    } else {
-                        kept = (int)n_all;
-                        u128 none;
-                        bin_reaching<false>(s, ~(u128)0, none, total);
-                        mass = total;
-                        stage = 2;
-                        if (g.p < 1.0f) {
-                            goal = share_of(g.p, total, true);
-                            goal = goal > 1 ? goal : 1;
-                            last = bin_reaching<false>(s, goal, above, none);
-                            // the draw's point lies between u times the goal and that plus u times a token of the last bin
-                            int d0 = last, d1 = last;
-                            above_first = above;
-                            if (DRAW) {
-                                u128 x;
-                                d0 = bin_reaching<false>(s, share_of(g.u, goal, false) + 1, above_first, none);
-                                const u128 one = ((u128)s.roots[last & 63] >> (last >> 6)) + (total >> 24);
-                                d1 = bin_reaching<false>(s, share_of(g.u, goal + one, false) + 1, x, none);
-                                d0 = min(d0, last);
-                                d1 = max(d0, min(d1, last));
-                            }
-                            int n = 0, nl = 0;
-                            for (int i = d0 + t; i <= d1; i += kFilterThreads)
-                                n += (int)bin_count(s, i);
-                            n_first = (int)block_sum((u128)n, s);
-                            nl = d1 < last ? (int)bin_count(s, last) : 0;
-                            c.op = kCmdGather;
-                            c.from = d0;
-                            c.to = d1;
-                            c.also = last;
-                            first_bin = d0;
-                            if (n_first + nl > kList) {   // not both at once: the last bin first
-                                stage = 3;
-                                c.from = c.to = last;
-                                first_bin = last;
-                                above_first = above;
-                                n_first = (int)bin_count(s, last);
-                                give_up = n_first > kList;
-                            }
-                            n = 0;
-                            for (int i = t; i < last; i += kFilterThreads)
-                                n += (int)bin_count(s, i);
-                            kept = (int)block_sum((u128)n, s);
-                        } else if (!DRAW) {   // top-k reaches past the last token
-                            put_row<DRAW>(a, r, kept);
-                            c.op = kCmdWrite;
-                            c.key = end.key;
-                            c.index = end.index;
-                        } else {
-                            stage = 4;
-                            first_bin = bin_reaching<false>(s, share_of(g.u, total, false) + 1, above_first, none);
-                            c.op = kCmdGather;
-                            c.from = c.to = c.also = first_bin;
-                            give_up = bin_count(s, first_bin) > kList;
-                        }
-                    }
-                } else if (stage == 1) {
-                    sort_list(s, listed);
-                    const uint64_t e = s.list[kept - 1];
-                    c.op = kCmdRecount;
-                    c.key = entry_key(e);
-                    c.index = entry_index(e);
-                } else {
-                    const int n = listed;
-                    u128 sum;
-                    sort_list(s, n);
-                    const ListPart q = weigh_list(s, n, sc, sum);
-                    bool draw_now = DRAW;
-                    int hi = n;
-                    u128 at_mass;
-                    if (stage == 2 || stage == 3) {
-                        // the last bin's tokens are the list's last ones, or all of a range that ends with it
-                        const int nl = (int)bin_count(s, last), lo = n - nl;
-                        u128 own = 0;
-                        rank_reaching(q, lo, n, 0, ~(u128)0, s, own);
-                        goal = share_of(g.p, total - bin_mass(s, last) + own, true);   // with that bin's exact mass
-                        goal = goal > 1 ? goal : 1;
-                        const int end_r = rank_reaching(q, lo, n, above, goal, s, mass);
-                        kept += end_r - lo + 1;
-                        stop = Prefix{entry_key(s.list[end_r]), entry_index(s.list[end_r])};
-                        hi = end_r + 1;
-                        if (!DRAW) {
-                            put_row<DRAW>(a, r, kept);
-                            c.op = kCmdWrite;
-                            c.key = stop.key;
-                            c.index = stop.index;
-                        } else if (stage == 3 && share_of(g.u, mass, false) + 1 <= above) {   // the draw is in a bin before
-                            draw_now = false;
-                            stage = 4;
-                            u128 none;
-                            first_bin = bin_reaching<false>(s, share_of(g.u, mass, false) + 1, above_first, none);
-                            c.op = kCmdGather;
-                            c.from = c.to = c.also = first_bin;
-                            give_up = bin_count(s, first_bin) > kList;
-                        } else if (stage == 2 && first_bin < last && share_of(g.u, mass, false) + 1 > above) {
-                            // the point is in the last bin after all
-                            const int at = rank_reaching(q, lo, hi, above, share_of(g.u, mass, false) + 1, s, at_mass);
-                            const uint64_t e = s.list[at];
-                            put_row<DRAW>(a, r, kept, entry_index(e), weight62(value_of(entry_key(e)), sc, s.roots), mass);
-                            draw_now = false;
-                        } else if (stage == 2 && first_bin < last) {
-                            hi = n_first < lo ? n_first : lo;
-                            hi = hi > 0 ? hi : 1;
-                        }
-                    }
-                    if (draw_now) {
-                        const int at = rank_reaching(q, 0, hi, above_first, share_of(g.u, mass, false) + 1, s, at_mass);
-                        const uint64_t e = s.list[at];
-                        put_row<DRAW>(a, r, kept, entry_index(e), weight62(value_of(entry_key(e)), sc, s.roots), mass);
-                    }
-                }
-                if (give_up) {
-                    Settings rest = g;
-                    rest.k = k;
-                    c = Command{kCmdEnd, 0, 0, -1, 0, 0};
-                    whole_row<T, DRAW>(a, r, rest, m, end, s.scale, s);
-                }
-                __syncthreads();
-                if (t == 0) {
-                    s.cmd = c;
-                    s.count = 0;
-                }
-            } else if (t == 0) {
-                s.count = 0;
-            }
-            row_sync(C);
-            const int op = C > 1 ? (int)ld_rank(&s.cmd.op, 0) : s.cmd.op;
-            if (op == kCmdEnd)
-                break;
-            if (op == kCmdGather) {
-                const int from = C > 1 ? (int)ld_rank(&s.cmd.from, 0) : s.cmd.from, to = C > 1 ? (int)ld_rank(&s.cmd.to, 0) : s.cmd.to;
-                const int also = C > 1 ? (int)ld_rank(&s.cmd.also, 0) : s.cmd.also;
-                row.each([&](float x, int i) {
-                    const int n = bin_of(x, bs);
-                    if (((n >= from && n <= to) || n == also) && end.has(key_of(x), i))
-                        append(s, key_of(x), i);
-                });
-                listed = collect(s, rank, C);
-                row_sync(C);   // the lists have been read
-                continue;
-            }
-            stop.key = C > 1 ? ld_rank(&s.cmd.key, 0) : s.cmd.key;
-            stop.index = C > 1 ? (int)ld_rank(&s.cmd.index, 0) : s.cmd.index;
-            if (op == kCmdWrite) {
-                row_sync(C);
-                write_row(row, out, a.same_phase, stop);
-                return;
-            }
-            again = true;   // kCmdRecount
-            end = stop;
-            break;
-        }
-        row_sync(C);
-        if (!again)
-            return;
-        if (!DRAW && g.p >= 1.0f) {   // top-k was all there was
-            if (rank == 0)
-                put_row<DRAW>(a, r, k);
-            write_row(row, out, a.same_phase, end);
-            return;
-        }
-        k = 0;
-    }
+    binned_row<T, DRAW>(a, r, g, row, rank, end, lone_x, sc, s);
+    row_sync(C);
 }
 
 }  // namespace sv

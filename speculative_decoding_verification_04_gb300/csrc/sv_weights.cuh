@@ -52,11 +52,10 @@ constexpr uint32_t kKeyPosInf = 0xff800000u;
 // to 2^12); rows beyond that take differences in 64 bits.
 struct RowScale {
     float ch, cl;       // log2(e) / T
-    float m, least;     // logits below `least` weigh nothing (less than 2^-64)
+    float m, T;
+    float least;        // logits below it weigh nothing (less than 2^-64)
     long long top;      // m log2(e) / T, units of 2^-48
-    double c;
     bool cold;
-    __device__ __forceinline__ void at(float m, float T);
 };
 
 __device__ __forceinline__ long long scaled48(float l, float ch, float cl)
@@ -66,22 +65,17 @@ __device__ __forceinline__ long long scaled48(float l, float ch, float cl)
     return __float2ll_rn(t * 281474976710656.0f) + __float2ll_rn(e * 281474976710656.0f);
 }
 
-// The constants of temperature T; the row's maximum goes in by at().
-__device__ __forceinline__ RowScale row_scale(float T)
+__device__ __forceinline__ RowScale row_scale(float m, float T)
 {
-    RowScale r{};
-    r.c = 1.4426950408889634 / (double)T;
-    r.ch = (float)r.c;
-    r.cl = (float)(r.c - (double)r.ch);
+    RowScale r;
+    r.ch = __fdiv_rn(1.44269502162933349609375f, T);   // log2(e) is this and 1.92596e-8
+    r.cl = __fdiv_rn(__fmaf_rn(-r.ch, T, 1.44269502162933349609375f) + 1.92596299112661746887e-8f, T);
+    r.m = m;
+    r.T = T;
+    r.cold = !(fabsf(m) * r.ch < 4096.0f) || T > 1e30f;   // (the constant's second part would be subnormal)
+    r.least = fmaxf(m - 70.0f * T, -3.4028234e38f);
+    r.top = r.cold ? 0 : scaled48(m, r.ch, r.cl);
     return r;
-}
-
-__device__ __forceinline__ void RowScale::at(float m_, float T)
-{
-    m = m_;
-    cold = !(fabsf(m_) * ch < 4096.0f) || T > 1e30f;   // (the split constant would be subnormal)
-    least = fmaxf(m_ - 70.0f * T, -3.4028234e38f);
-    top = cold ? 0 : scaled48(m_, ch, cl);
 }
 
 // 2^-x in units of 2^-62, x >= 0 in units of 2^-48.  2^-x = 2^-n 2^(-j / 64) e^-y
@@ -108,7 +102,7 @@ __device__ __forceinline__ uint64_t weight62(float l, const RowScale& r, const u
         return 0;
     long long x;
     if (r.cold) {
-        const double d = ((double)r.m - (double)l) * r.c;
+        const double d = ((double)r.m - (double)l) * (1.4426950408889634 / (double)r.T);
         x = d < 64.0 ? (long long)(d * 281474976710656.0) : 64ll << 48;
     } else {
         x = r.top - scaled48(l, r.ch, r.cl);
@@ -128,6 +122,23 @@ __device__ __forceinline__ u128 share_of(float p, u128 z, bool up)
     if (s > 126)
         return up && n != 0 ? 1 : 0;
     return up ? (n + (((u128)1 << s) - 1)) >> s : n >> s;
+}
+
+// w / z as the nearest fp32, z < 2^96: a quotient of the leading 24 bits, and
+// one step by what is left.
+__device__ __forceinline__ float quotient(uint64_t w, u128 z)
+{
+    int up = 0;
+    while (z >> 63) {   // z to 63 bits: its rounding is far below the quotient's
+        z >>= 8;
+        up += 8;
+    }
+    const uint64_t y = (uint64_t)z;
+    const float wh = __ull2float_rz(w), yh = __ull2float_rz(y);
+    const float wl = (float)(w - (uint64_t)wh), yl = (float)(y - (uint64_t)yh);
+    const float q = __fdiv_rn(wh, yh);
+    const float rest = __fmaf_rn(-q, yl, __fmaf_rn(-q, yh, wh) + wl);
+    return ldexpf(q + __fdiv_rn(rest, yh), -up);
 }
 
 }  // namespace sv
