@@ -62,7 +62,7 @@ struct FilterShared {
     };
     uint64_t roots[64];
     u128 part[kFilterWarps];
-    u128 skip, found_mass;
+    u128 found_mass;
     Command cmd;
     uint32_t warp_top[kFilterWarps], warp_low[kFilterWarps];
     int warp_count[2][kFilterWarps];
@@ -119,23 +119,20 @@ template <typename T> struct RowSpan {
         const int t = threadIdx.x;
         return t < rest ? (t < head ? t : nvec * E + t) : -1;
     }
-    // f(values, index of the first) for every vector, four loads in flight
+    // f(values, index of the first) for every vector, the next one on its way.
+    // (Rolled: code that runs once a row comes from L2, and costs more than it does.)
     template <typename F> __device__ __forceinline__ void vectors(F&& f) const
     {
         const uint4* v = vec();
-        for (int i0 = v0 + threadIdx.x; i0 < v1; i0 += 4 * kFilterThreads) {
-            uint4 w[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i0 + u * kFilterThreads < v1)
-                    w[u] = v[i0 + u * kFilterThreads];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i0 + u * kFilterThreads < v1) {
-                    float x[E];
-                    Elem<T>::unpack(w[u], x);
-                    f(x, head + (i0 + u * kFilterThreads) * E);
-                }
+        int i = v0 + threadIdx.x;
+        uint4 next = i < v1 ? v[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (; i < v1; i += kFilterThreads) {
+            float x[E];
+            Elem<T>::unpack(next, x);
+            if (i + kFilterThreads < v1)
+                next = v[i + kFilterThreads];
+            f(x, head + i * E);
         }
     }
     // f(value, index) for every element
@@ -196,7 +193,7 @@ __device__ __forceinline__ u128 shfl_up128(u128 v, int o)
 }
 
 // Exclusive prefix sum over the block; `total` gets the whole.
-__device__ __forceinline__ u128 block_scan(u128 v, FilterShared& s, u128& total)
+__device__ __noinline__ u128 block_scan(u128 v, FilterShared& s, u128& total)
 {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     u128 x = v;
@@ -427,7 +424,7 @@ __device__ __forceinline__ uint32_t entry_key(uint64_t e) { return (uint32_t)(e 
 __device__ __forceinline__ int entry_index(uint64_t e) { return (int)(0xffffffffu - (uint32_t)e); }
 
 // Into rank 0's list.
-__device__ __forceinline__ void append(FilterShared& s, int C, uint32_t key, int index, int n = 1)
+__device__ __noinline__ void append(FilterShared& s, int C, uint32_t key, int index, int n = 1)
 {
     if (C == 1) {
         const int at = atomicAdd(&s.count, n);
@@ -468,7 +465,7 @@ __device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, floa
 }
 
 // Sorts list[0 .. n), the largest first.
-__device__ __forceinline__ void sort_list(FilterShared& s, int n)
+__device__ __noinline__ void sort_list(FilterShared& s, int n)
 {
     const int t = threadIdx.x;
     if (n <= kFilterThreads) {   // each entry counts those before it
@@ -502,60 +499,43 @@ __device__ __forceinline__ void sort_list(FilterShared& s, int n)
     __syncthreads();
 }
 
-// A thread's entries of the sorted list, and the mass before each of its own.
-struct ListPart {
-    int r0, n;                         // ranks r0 .. r0 + n - 1
-    uint64_t w[kList / kFilterThreads];
-    u128 before;                       // mass of the ranks below r0
-};
-
-__device__ __forceinline__ ListPart weigh_list(FilterShared& s, int n, const RowScale& sc, u128& total)
+__device__ __noinline__ uint64_t entry_weight(const FilterShared& s, int r, const RowScale& sc)
 {
-    ListPart q;
-    const int per = (n + kFilterThreads - 1) / kFilterThreads;
-    q.r0 = min(n, (int)threadIdx.x * per);
-    q.n = min(n, q.r0 + per) - q.r0;
-    u128 sum = 0;
-#pragma unroll
-    for (int i = 0; i < kList / kFilterThreads; ++i) {
-        q.w[i] = i < q.n ? weight62(value_of(entry_key(s.list[q.r0 + i])), sc, s.roots) : 0;
-        sum += q.w[i];
-    }
-    q.before = block_scan(sum, s, total);
-    return q;
+    return weight62(value_of(entry_key(s.list[r])), sc, s.roots);
+}
+
+// The mass of the sorted list's ranks lo .. hi - 1, a block's worth at a time;
+// `first` is the weight of rank lo + threadIdx.x (0 from hi on).
+__device__ __noinline__ u128 list_mass(FilterShared& s, int lo, int hi, uint64_t first, const RowScale& sc)
+{
+    u128 sum = first;
+    for (int r = lo + kFilterThreads + (int)threadIdx.x; r < hi; r += kFilterThreads)
+        sum += entry_weight(s, r, sc);
+    return block_sum(sum, s);
 }
 
 // The first rank of lo .. hi - 1 whose cumulative mass, counted from rank lo on
 // and with `base` before it, reaches goal (hi - 1 if none does); its mass in
 // `mass`.
-__device__ __forceinline__ int rank_reaching(const ListPart& q, int lo, int hi, u128 base, u128 goal, FilterShared& s, u128& mass)
+__device__ __noinline__ int list_reaching(FilterShared& s, int lo, int hi, uint64_t first, u128 base, u128 goal, const RowScale& sc, u128& mass)
 {
-    __syncthreads();
-    if (lo > 0) {   // less what is before rank lo
-        u128 c = q.before;
-#pragma unroll
-        for (int i = 0; i < kList / kFilterThreads; ++i) {
-            if (i < q.n && q.r0 + i == lo)
-                s.skip = c;
-            c += q.w[i];
+    for (int r0 = lo;; r0 += kFilterThreads) {
+        const int r = r0 + (int)threadIdx.x;
+        const uint64_t w = r0 == lo ? first : r < hi ? entry_weight(s, r, sc) : 0;
+        u128 total;
+        const u128 c = base + block_scan(w, s, total);
+        base += total;
+        if (base < goal && r0 + kFilterThreads < hi)
+            continue;
+        __syncthreads();
+        if (r < hi && (base >= goal ? (c < goal || r == lo) && c + w >= goal : r == hi - 1)) {
+            s.found = r;
+            s.found_mass = c + w;
         }
         __syncthreads();
-        base -= s.skip;   // (modulo 2^128: added to sums that hold it)
+        mass = s.found_mass;
+        return s.found;
     }
-    u128 c = base + q.before;
-#pragma unroll
-    for (int i = 0; i < kList / kFilterThreads; ++i) {
-        const int r = q.r0 + i;
-        const bool before = r > lo && c >= goal;
-        c += q.w[i];
-        if (i < q.n && r >= lo && r < hi && !before && (c >= goal || r == hi - 1)) {
-            s.found = r;
-            s.found_mass = c;
-        }
-    }
-    __syncthreads();
-    mass = s.found_mass;
-    return s.found;
 }
 
 // ---------------------------------------------------------------------------
@@ -651,12 +631,13 @@ struct BinPart {
     int n_before, n_own;
 };
 
-__device__ __forceinline__ BinPart scan_bins(FilterShared& s, u128& mass, int& count)
+__device__ __noinline__ BinPart scan_bins(FilterShared& s, u128& mass, int& count)
 {
     BinPart q;
     q.own = 0;
     q.n_own = 0;
     const int i0 = threadIdx.x * kBinsEach;
+#pragma unroll 1
     for (int i = 0; i < kBinsEach; ++i) {
         const int j = i0 + ((i + threadIdx.x) & (kBinsEach - 1));   // (lanes on different banks)
         q.own += bin_mass(s, j);
@@ -679,7 +660,7 @@ struct BinAt {
     u128 before;
 };
 
-template <bool kCount> __device__ __forceinline__ BinAt bin_reaching(const BinPart& q, FilterShared& s, u128 goal)
+template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart& q, FilterShared& s, u128 goal)
 {
     __syncthreads();
     if (threadIdx.x == 0)
@@ -718,7 +699,7 @@ template <bool kCount> __device__ __forceinline__ BinAt bin_reaching(const BinPa
 }
 
 // All of the cluster's bins in rank 0's.
-__device__ __forceinline__ void merge_bins(FilterShared& s, int rank, int C)
+__device__ __noinline__ void merge_bins(FilterShared& s, int rank, int C)
 {
     row_sync(C);
     if (C == 1)
@@ -727,7 +708,7 @@ __device__ __forceinline__ void merge_bins(FilterShared& s, int rank, int C)
     for (int i = i0 + 4 * t; i < i0 + per; i += 4 * kFilterThreads) {
         uint64_t lo[4] = {0, 0, 0, 0};
         uint32_t hi[4] = {0, 0, 0, 0};
-#pragma unroll 4
+#pragma unroll 2
         for (int c = 0; c < C; ++c) {
             const uint4 x = ld_rank128(&s.bin.lo[i], c), y = ld_rank128(&s.bin.hi[i], c);
             lo[0] += x.x, lo[1] += x.y, lo[2] += x.z, lo[3] += x.w;
@@ -751,49 +732,154 @@ __device__ __forceinline__ void merge_bins(FilterShared& s, int rank, int C)
     }
 }
 
+// A CTA's part of the row into its bins: every eighth stretch of its vectors, or
+// all of them.
+template <typename T>
+__device__ __noinline__ void bin_vectors(const RowSpan<T> row, int stride, Prefix end, const BinScale b, FilterShared& s)
+{
+    constexpr int E = Elem<T>::E;
+    const float least = value_of(end.key);
+    const uint4* v = row.vec();
+    int i = row.v0 + (int)threadIdx.x;
+    uint4 next = i < row.v1 ? v[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (; i < row.v1; i += stride) {
+        float x[E];
+        Elem<T>::unpack(next, x);
+        if (i + stride < row.v1)
+            next = v[i + stride];
+        const int left = end.index - (row.head + i * E);   // ties up to this one count
+#pragma unroll
+        for (int j = 0; j < E; j += 2)
+            bin_pair(s, x[j], x[j + 1], x[j] > least || (x[j] == least && j <= left),
+                     x[j + 1] > least || (x[j + 1] == least && j + 1 <= left), b);
+    }
+}
+
+// The other seven eighths: tokens from `from` up go through the bins, 64 of a
+// warp at a time, and the rest are summed on the way (fp32 weights, the sums
+// compensated).  Returns this thread's sum; `gone` counts the logits of -inf.
+template <typename T>
+__device__ __noinline__ float tail_vectors(const RowSpan<T> row, float from, const BinScale b, FilterShared& s, int& gone)
+{
+    constexpr int E = Elem<T>::E;
+    const int t = threadIdx.x, lane = t & 31;
+    float* queue = s.queue[t >> 5];
+    const uint4* v = row.vec();
+    float sum = 0.0f, carry = 0.0f;
+    int waiting = 0, none = 0;
+    const uint64_t ch2 = f2_pack(b.ch, b.ch), cl2 = f2_pack(b.cl, b.cl), unit2 = f2_pack(-b.unit, -b.unit);
+    // stretches 0, 8, 16, ... are the sample; all of a warp's lanes go through every stretch
+    int n = 1;
+    auto at = [&](int k) { return row.v0 + k * kFilterThreads + t; };
+    const int stretches = (row.v1 - row.v0 + kFilterThreads - 1) / kFilterThreads;
+    uint4 next = at(n) < row.v1 ? v[at(n)] : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    while (n < stretches) {
+        const bool there = at(n) < row.v1;
+        float x[E];
+        Elem<T>::unpack(next, x);
+        n += n % kGroup == kGroup - 1 ? 2 : 1;
+        if (n < stretches && at(n) < row.v1)
+            next = v[at(n)];
+        uint64_t add = 0;   // (+0, +0)
+        float low = x[0];
+        uint32_t in = 0;
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+            const uint64_t L = f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least));
+            float w0, w1;
+            f2_unpack(exp2_pair(f2_fma(L, cl2, f2_fma(L, ch2, unit2))), w0, w1);
+            const bool in0 = x[j] >= from, in1 = x[j + 1] >= from;
+            add = f2_add(add, f2_pack(in0 ? 0.0f : w0, in1 ? 0.0f : w1));
+            in |= (in0 ? 1u << j : 0u) | (in1 ? 2u << j : 0u);
+            low = fminf(low, fminf(x[j], x[j + 1]));
+        }
+        if (there) {
+            float lo, hi, e;
+            f2_unpack(add, lo, hi);
+            two_sum(sum, lo + hi, sum, e);
+            carry += e;
+            if (low == -INFINITY)
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    none += x[j] == -INFINITY;
+        } else {
+            in = 0;
+        }
+        // the lanes' tokens one after the other
+        int upto = __popc(in);
+        const int own = upto;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o)
+                upto += y;
+        }
+        int to = waiting + upto - own;
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            if (in >> j & 1)
+                queue[to++] = x[j];
+        waiting += __shfl_sync(kFull, upto, 31);
+        __syncwarp();
+        if (waiting >= 64) {
+            int done = 0;
+#pragma unroll 1
+            for (; done + 64 <= waiting; done += 64)
+                bin_pair(s, queue[done + lane], queue[done + 32 + lane], true, true, b);
+            const float left0 = queue[done + lane], left1 = queue[min(done + 32 + lane, kQueue - 1)];
+            __syncwarp();
+            queue[lane] = left0;
+            queue[lane + 32] = left1;
+            waiting -= done;
+            __syncwarp();
+        }
+    }
+    if (lane < waiting)
+        bin_pair(s, queue[lane], queue[lane + 32], true, lane + 32 < waiting, b);
+    gone = none;
+    return sum + carry;
+}
+
+// The -inf among the sample's vectors.
+template <typename T> __device__ __forceinline__ int sample_gone(const RowSpan<T>& row)
+{
+    constexpr int E = Elem<T>::E;
+    int n = 0;
+#pragma unroll 1
+    for (int i = row.v0 + (int)threadIdx.x; i < row.v1; i += kGroup * kFilterThreads) {
+        float x[E];
+        Elem<T>::unpack(row.vec()[i], x);
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            n += x[j] == -INFINITY;
+    }
+    return n;
+}
+
 // The sums of a CTA's part of the row.  With `tail` only the tokens around and
 // above where a sample of the row reaches the share `target` go through the
-// bins, and the rest are summed on the way (fp32 weights, their sums
-// compensated: the rest is a small part of the mass).  Returns the last bin that
-// is complete, the mass that is in no bin, and with `tail` how many logits are
-// -inf.
+// bins; the rest are a 64th of the mass at most, if the sample is right.  Returns
+// the last bin that is complete, the mass that is in no bin, and with `tail` how
+// many logits are -inf.
 template <typename T>
 __device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Prefix end, bool tail, float target, const BinScale& b,
                                          FilterShared& s, u128& rest, int& gone)
 {
-    constexpr int E = Elem<T>::E;
-    const int t = threadIdx.x, lane = t & 31;
+    const int t = threadIdx.x;
     rest = 0;
     gone = 0;
     __syncthreads();
-    for (int i = t; i < kBins; i += kFilterThreads)
-        s.bin.lo[i] = s.bin.hi[i] = 0;
+    for (int i = 4 * t; i < kBins; i += 4 * kFilterThreads)
+        *reinterpret_cast<uint4*>(&s.bin.lo[i]) = *reinterpret_cast<uint4*>(&s.bin.hi[i]) = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    const float least = value_of(end.key);
     const int lone = row.lone();
     if (lone >= 0)
         bin_pair(s, lone_x, lone_x, end.has(key_of(lone_x), lone), false, b);
-    if (!tail) {
-        row.vectors([&](const float (&x)[E], int i) {
-#pragma unroll
-            for (int j = 0; j < E; j += 2)
-                bin_pair(s, x[j], x[j + 1], x[j] > least || (x[j] == least && i + j <= end.index),
-                         x[j + 1] > least || (x[j + 1] == least && i + j + 1 <= end.index), b);
-        });
+    bin_vectors(row, tail ? kGroup * kFilterThreads : kFilterThreads, end, b, s);
+    if (!tail)
         return kBins - 1;
-    }
-    int none = lone >= 0 && lone_x < least;
-    // the sample: every eighth stretch of vectors
-    const uint4* v = row.vec();
-    for (int i = row.v0 + t; i < row.v1; i += kGroup * kFilterThreads) {
-        float x[E];
-        Elem<T>::unpack(v[i], x);
-#pragma unroll
-        for (int j = 0; j < E; j += 2) {
-            bin_pair(s, x[j], x[j + 1], x[j] >= least, x[j + 1] >= least, b);
-            none += (x[j] < least) + (x[j + 1] < least);
-        }
-    }
     __syncthreads();
     u128 mass;
     int count;
@@ -801,75 +887,14 @@ __device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Pr
     int cutoff = kBins - 1;
     if (count > 0) {   // a quarter of what the sample leaves behind the target, a 64th of the mass at most
         const u128 quarter = share_of(1.0f - target, mass, false) >> 2, beyond = quarter < mass >> 6 ? quarter : mass >> 6;
-        const BinAt at = bin_reaching<false>(part, s, mass - beyond);
-        cutoff = min(kBins - 1, at.bin + 8);
+        cutoff = min(kBins - 1, bin_reaching<false>(part, s, mass - beyond).bin + 8);
     }
-    const float from = fmaxf(least, (b.unit - (float)(cutoff + 3) * 0.015625f) / b.ch);
-    float* queue = s.queue[t >> 5];
-    float sum = 0.0f, carry = 0.0f;
-    int waiting = 0;
-    const uint64_t ch2 = f2_pack(b.ch, b.ch), cl2 = f2_pack(b.cl, b.cl), unit2 = f2_pack(-b.unit, -b.unit);
-    auto take = [&](uint4 w, bool there) {
-        float x[E];
-        Elem<T>::unpack(w, x);
-        uint64_t add = 0;   // (+0, +0)
-#pragma unroll
-        for (int j = 0; j < E; j += 2) {
-            const uint64_t L = f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least));
-            float w0, w1;
-            f2_unpack(exp2_pair(f2_fma(L, cl2, f2_fma(L, ch2, unit2))), w0, w1);
-            add = f2_add(add, f2_pack(x[j] < from ? w0 : 0.0f, x[j + 1] < from ? w1 : 0.0f));
-        }
-        float lo, hi, low = x[0];
-        f2_unpack(add, lo, hi);
-#pragma unroll
-        for (int j = 1; j < E; ++j)
-            low = fminf(low, x[j]);
-        if (there && low < least)
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                none += x[j] < least;
-        if (there) {
-            float e;
-            two_sum(sum, lo + hi, sum, e);
-            carry += e;
-        }
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const bool in = there && x[j] >= from;
-            const uint32_t who = __ballot_sync(kFull, in);
-            if (in)
-                queue[waiting + __popc(who & ((1u << lane) - 1))] = x[j];
-            waiting += __popc(who);
-        }
-        __syncwarp();
-        if (waiting >= 64) {
-            int at = 0;
-            for (; at + 64 <= waiting; at += 64)
-                bin_pair(s, queue[at + lane], queue[at + 32 + lane], true, true, b);
-            const float left0 = at + lane < waiting ? queue[at + lane] : 0.0f, left1 = at + 32 + lane < waiting ? queue[at + 32 + lane] : 0.0f;
-            __syncwarp();
-            queue[lane] = left0;
-            queue[lane + 32] = left1;
-            waiting -= at;
-            __syncwarp();
-        }
-    };
-    for (int n0 = row.v0; n0 < row.v1; n0 += kGroup * kFilterThreads) {
-        uint4 w[kGroup - 1];
-#pragma unroll
-        for (int u = 1; u < kGroup; ++u) {
-            const int i = n0 + u * kFilterThreads + t;
-            w[u - 1] = i < row.v1 ? v[i] : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 1; u < kGroup; ++u)
-            take(w[u - 1], n0 + u * kFilterThreads + t < row.v1);
-    }
-    if (lane < waiting)
-        bin_pair(s, queue[lane], queue[lane + 32], true, lane + 32 < waiting, b);
+    const float from = fmaxf(value_of(end.key), (b.unit - (float)(cutoff + 3) * 0.015625f) / b.ch);
+    int none;
+    const float sum = tail_vectors(row, from, b, s, none);
+    none += sample_gone(row) + (lone >= 0 && lone_x == -INFINITY);
     // units of 2^-62, and the count below them
-    const u128 both = block_sum((u128)__float2ull_rn((sum + carry) * 1125899906842624.0f) << 36 | (u128)(uint32_t)none, s);
+    const u128 both = block_sum((u128)__float2ull_rn(sum * 1125899906842624.0f) << 36 | (u128)(uint32_t)none, s);
     rest = both >> 24;
     gone = (int)((uint32_t)both & 0xffffffu);
     return cutoff;
@@ -878,6 +903,17 @@ __device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Pr
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
+// The tokens of the prefix that are in bins from .. to, or in `also`.
+template <typename T>
+__device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to, int also, Prefix end, const BinScale b, int C, FilterShared& s)
+{
+    row.each([&](float x, int i) {
+        const int n = bin_of(x, b);
+        if (((n >= from && n <= to) || n == also) && end.has(key_of(x), i))
+            append(s, C, key_of(x), i);
+    });
+}
+
 template <typename T, bool DRAW>
 __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const Settings& g, const RowSpan<T>& row, int rank, Prefix end,
                                         float lone_x, const RowScale& whole, FilterShared& s)
@@ -997,17 +1033,17 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                         c.key = entry_key(e);
                         c.index = entry_index(e);
                     } else {
-                        u128 sum, to;
-                        const ListPart q = weigh_list(s, n, sc, sum);
+                        u128 to;
                         int lo = 0, hi = n;   // where the draw is looked for
+                        uint64_t w = 0;
                         bool draw_now = DRAW;
                         if (stage == 2) {
                             const int from = n - n_last;   // the last bin's tokens
-                            u128 own;
-                            rank_reaching(q, from, n, 0, ~(u128)0, s, own);
+                            w = from + t < n ? entry_weight(s, from + t, sc) : 0;
+                            const u128 own = list_mass(s, from, n, w, sc);
                             // the goal again, with that bin's mass by its tokens
                             const u128 goal = share_of(g.p, total - bin_mass(s, last) + own, true);
-                            const int end_r = rank_reaching(q, from, n, above, goal > 1 ? goal : 1, s, mass);
+                            const int end_r = list_reaching(s, from, n, w, above, goal > 1 ? goal : 1, sc, mass);
                             kept += end_r - from + 1;
                             if (!DRAW) {
                                 put_row<DRAW>(a, r, kept);
@@ -1031,9 +1067,9 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                             }
                         }
                         if (draw_now) {
-                            const int at = rank_reaching(q, lo, hi, above_first, share_of(g.u, mass, false) + 1, s, to);
-                            const uint64_t e = s.list[at];
-                            put_row<DRAW>(a, r, kept, entry_index(e), weight62(value_of(entry_key(e)), sc, s.roots), mass);
+                            w = lo + t < hi ? entry_weight(s, lo + t, sc) : 0;
+                            const int at = list_reaching(s, lo, hi, w, above_first, share_of(g.u, mass, false) + 1, sc, to);
+                            put_row<DRAW>(a, r, kept, entry_index(s.list[at]), entry_weight(s, at, sc), mass);
                         }
                     }
                 }
@@ -1060,11 +1096,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
             if (c.op == kCmdEnd)
                 break;
             if (c.op == kCmdGather) {
-                row.each([&](float x, int i) {
-                    const int n = bin_of(x, bs);
-                    if (((n >= c.from && n <= c.to) || n == c.also) && end.has(key_of(x), i))
-                        append(s, C, key_of(x), i);
-                });
+                gather_bins(row, c.from, c.to, c.also, end, bs, C, s);
                 row_sync(C);
                 continue;
             }
@@ -1308,18 +1340,20 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
             if (g.k > 0)
                 n = min(n, g.k);
             u128 mass = 0;
-            ListPart q;
-            if (DRAW || g.p < 1.0f)
-                q = weigh_list(s, n, sc, mass);
+            uint64_t w = 0;
+            if (DRAW || g.p < 1.0f) {
+                w = t < n ? entry_weight(s, t, sc) : 0;
+                mass = list_mass(s, 0, n, w, sc);
+            }
             if (g.p < 1.0f) {
                 const u128 goal = share_of(g.p, mass, true);
-                n = rank_reaching(q, 0, n, 0, goal > 1 ? goal : 1, s, mass) + 1;
+                n = list_reaching(s, 0, n, w, 0, goal > 1 ? goal : 1, sc, mass) + 1;
+                w = t < n ? w : 0;
             }
             if (DRAW) {
                 u128 to;
-                const int at = rank_reaching(q, 0, n, 0, share_of(g.u, mass, false) + 1, s, to);
-                const uint64_t e = s.list[at];
-                put_row<DRAW>(a, r, n, entry_index(e), weight62(value_of(entry_key(e)), sc, s.roots), mass);
+                const int at = list_reaching(s, 0, n, w, 0, share_of(g.u, mass, false) + 1, sc, to);
+                put_row<DRAW>(a, r, n, entry_index(s.list[at]), entry_weight(s, at, sc), mass);
             } else {
                 put_row<DRAW>(a, r, n);
             }
