@@ -63,6 +63,7 @@ struct FilterShared {
     uint64_t roots[64];
     u128 part[kFilterWarps];
     u128 found_mass;
+    uint64_t part64[kFilterWarps], found64;
     Command cmd;
     uint32_t warp_top[kFilterWarps], warp_low[kFilterWarps];
     int warp_count[2][kFilterWarps];
@@ -288,7 +289,7 @@ struct Settings {
 
 // A row's numbers.
 template <bool DRAW>
-__device__ __forceinline__ void put_row(const FilterArgs& a, long long r, int kept, int token = -1, uint64_t weight = 0, u128 mass = 0)
+__device__ __forceinline__ void put_row(const FilterArgs& a, long long r, int kept, int token = -1, uint64_t weight = 1, u128 mass = 1)
 {
     if (threadIdx.x == 0) {
         if (a.has_kept)
@@ -452,14 +453,28 @@ __device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, floa
                 s.hit[at] = (uint16_t)(n * kFilterThreads + t);
         }
     __syncthreads();
-    const int hits = min(s.hits, kList);
-    for (int j = t; j < hits * kGroup; j += kFilterThreads) {
-        const int h = s.hit[j / kGroup], n = h / kFilterThreads;
-        const int i = row.v0 + (n * kGroup + j % kGroup) * kFilterThreads + h % kFilterThreads;
-        if (i < row.v1) {
+    const int n = min(s.hits, kList) * kGroup;
+    auto place = [&](int j) {   // the vector of item j, or -1
+        if (j >= n)
+            return -1;
+        const int h = s.hit[j / kGroup], i = row.v0 + (h / kFilterThreads * kGroup + j % kGroup) * kFilterThreads + h % kFilterThreads;
+        return i < row.v1 ? i : -1;
+    };
+#pragma unroll 1
+    for (int j = t; j < n; j += 2 * kFilterThreads) {
+        int i[2] = {place(j), place(j + kFilterThreads)};
+        uint4 w[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            w[u] = i[u] >= 0 ? row.vec()[i[u]] : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
             float x[E];
-            Elem<T>::unpack(row.vec()[i], x);
-            f(x, row.head + i * E);
+            Elem<T>::unpack(w[0], x);
+            if (i[0] >= 0)
+                f(x, row.head + i[0] * E);
+            w[0] = w[1];
+            i[0] = i[1];
         }
     }
 }
@@ -468,14 +483,18 @@ __device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, floa
 __device__ __noinline__ void sort_list(FilterShared& s, int n)
 {
     const int t = threadIdx.x;
-    if (n <= kFilterThreads) {   // each entry counts those before it
-        const uint64_t e = t < n ? s.list[t] : 0;
+    if (n <= kFilterThreads) {   // each entry counts those before it, by one thread or up to eight
+        const int g = n <= 32 ? 8 : n <= 64 ? 4 : n <= 128 ? 2 : 1, i = t / g, each = (n + g - 1) / g;
+        const uint64_t e = i < n ? s.list[i] : 0;
+        const int j1 = min(n, (t % g + 1) * each);
         int r = 0;
-        if (t < n)
-            for (int j = 0; j < n; ++j)
-                r += s.list[j] > e;
+#pragma unroll 4
+        for (int j = t % g * each; j < j1; ++j)
+            r += s.list[j] > e;
+        for (int o = 1; o < g; o <<= 1)
+            r += __shfl_xor_sync(kFull, r, o);
         __syncthreads();
-        if (t < n)
+        if (i < n && t % g == 0)
             s.list[r] = e;
     } else {
         int size = 2 * kFilterThreads;
@@ -504,36 +523,69 @@ __device__ __noinline__ uint64_t entry_weight(const FilterShared& s, int r, cons
     return weight62(value_of(entry_key(s.list[r])), sc, s.roots);
 }
 
-// The mass of the sorted list's ranks lo .. hi - 1, a block's worth at a time;
-// `first` is the weight of rank lo + threadIdx.x (0 from hi on).
-__device__ __noinline__ u128 list_mass(FilterShared& s, int lo, int hi, uint64_t first, const RowScale& sc)
+// Sums over the list are in units of 2^-52: 2048 weights fit 64 bits, and what
+// their rounding moves stays below a thousandth of a token of weight 2^-32.
+__device__ __forceinline__ uint64_t weight52(uint64_t w62) { return (w62 + 512) >> 10; }
+
+__device__ __noinline__ uint64_t list_weight(const FilterShared& s, int r, const RowScale& sc) { return weight52(entry_weight(s, r, sc)); }
+
+// Exclusive prefix sum over the block; `total` gets the whole.
+__device__ __noinline__ uint64_t block_scan(uint64_t v, FilterShared& s, uint64_t& total)
 {
-    u128 sum = first;
-    for (int r = lo + kFilterThreads + (int)threadIdx.x; r < hi; r += kFilterThreads)
-        sum += entry_weight(s, r, sc);
-    return block_sum(sum, s);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    uint64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(kFull, (unsigned long long)x, o);
+        if (lane >= o)
+            x += y;
+    }
+    __syncthreads();
+    if (lane == 31)
+        s.part64[w] = x;
+    __syncthreads();
+    uint64_t before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kFilterWarps; ++i) {
+        const uint64_t q = s.part64[i];
+        if (i < w)
+            before += q;
+        all += q;
+    }
+    total = all;
+    return before + x - v;
 }
 
-// The first rank of lo .. hi - 1 whose cumulative mass, counted from rank lo on
-// and with `base` before it, reaches goal (hi - 1 if none does); its mass in
-// `mass`.
-__device__ __noinline__ int list_reaching(FilterShared& s, int lo, int hi, uint64_t first, u128 base, u128 goal, const RowScale& sc, u128& mass)
+// The mass of the sorted list's ranks lo .. hi - 1, a block's worth at a time;
+// `first` is the weight of rank lo + threadIdx.x (0 from hi on).
+__device__ __noinline__ uint64_t list_mass(FilterShared& s, int lo, int hi, uint64_t first, const RowScale& sc)
 {
+    uint64_t sum = first, total;
+    for (int r = lo + kFilterThreads + (int)threadIdx.x; r < hi; r += kFilterThreads)
+        sum += list_weight(s, r, sc);
+    block_scan(sum, s, total);
+    return total;
+}
+
+// The first rank of lo .. hi - 1 whose cumulative mass, counted from rank lo on,
+// reaches goal (hi - 1 if none does); its mass in `mass`.
+__device__ __noinline__ int list_reaching(FilterShared& s, int lo, int hi, uint64_t first, uint64_t goal, const RowScale& sc, uint64_t& mass)
+{
+    uint64_t base = 0;
     for (int r0 = lo;; r0 += kFilterThreads) {
         const int r = r0 + (int)threadIdx.x;
-        const uint64_t w = r0 == lo ? first : r < hi ? entry_weight(s, r, sc) : 0;
-        u128 total;
-        const u128 c = base + block_scan(w, s, total);
+        const uint64_t w = r0 == lo ? first : r < hi ? list_weight(s, r, sc) : 0;
+        uint64_t total;
+        const uint64_t c = base + block_scan(w, s, total);
         base += total;
         if (base < goal && r0 + kFilterThreads < hi)
             continue;
-        __syncthreads();
         if (r < hi && (base >= goal ? (c < goal || r == lo) && c + w >= goal : r == hi - 1)) {
             s.found = r;
-            s.found_mass = c + w;
+            s.found64 = c + w;
         }
         __syncthreads();
-        mass = s.found_mass;
+        mass = s.found64;
         return s.found;
     }
 }
@@ -903,14 +955,22 @@ __device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Pr
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-// The tokens of the prefix that are in bins from .. to, or in `also`.
+// The tokens of the prefix that are in bins from .. to, or in `also`: a compare
+// with the bins' bounds (wider by half a bin, for the rounding) before the bin
+// itself.
 template <typename T>
 __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to, int also, Prefix end, const BinScale b, int C, FilterShared& s)
 {
+    auto bound = [&](float i) { return (b.unit - (i + 1.0f) * 0.015625f) / b.ch; };   // bin 0's centre is one 64th below `unit`
+    const bool last = to == kBins - 1 || also == kBins - 1;
+    const float top = bound((float)from - 1.0f), low = bound((float)to + 1.0f), top2 = bound((float)also - 1.0f);
+    const float least = last ? -INFINITY : bound((float)max(to, also) + 1.0f);
     row.each([&](float x, int i) {
-        const int n = bin_of(x, b);
-        if (((n >= from && n <= to) || n == also) && end.has(key_of(x), i))
-            append(s, C, key_of(x), i);
+        if (x >= least && (x <= top2 || x >= low) && x <= fmaxf(top, top2)) {
+            const int n = bin_of(x, b);
+            if (((n >= from && n <= to) || n == also) && end.has(key_of(x), i))
+                append(s, C, key_of(x), i);
+        }
     });
 }
 
@@ -1033,17 +1093,21 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                         c.key = entry_key(e);
                         c.index = entry_index(e);
                     } else {
-                        u128 to;
+                        uint64_t w = 0, to;
                         int lo = 0, hi = n;   // where the draw is looked for
-                        uint64_t w = 0;
+                        auto after = [](u128 goal, u128 base) {   // what of a goal is left to the list
+                            const u128 d = goal > base ? goal - base : 1;
+                            return (uint64_t)((d + 1023) >> 10);
+                        };
                         bool draw_now = DRAW;
                         if (stage == 2) {
                             const int from = n - n_last;   // the last bin's tokens
-                            w = from + t < n ? entry_weight(s, from + t, sc) : 0;
-                            const u128 own = list_mass(s, from, n, w, sc);
+                            w = from + t < n ? list_weight(s, from + t, sc) : 0;
+                            const u128 own = (u128)list_mass(s, from, n, w, sc) << 10;
                             // the goal again, with that bin's mass by its tokens
                             const u128 goal = share_of(g.p, total - bin_mass(s, last) + own, true);
-                            const int end_r = list_reaching(s, from, n, w, above, goal > 1 ? goal : 1, sc, mass);
+                            const int end_r = list_reaching(s, from, n, w, after(goal, above), sc, to);
+                            mass = above + ((u128)to << 10);
                             kept += end_r - from + 1;
                             if (!DRAW) {
                                 put_row<DRAW>(a, r, kept);
@@ -1067,8 +1131,8 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                             }
                         }
                         if (draw_now) {
-                            w = lo + t < hi ? entry_weight(s, lo + t, sc) : 0;
-                            const int at = list_reaching(s, lo, hi, w, above_first, share_of(g.u, mass, false) + 1, sc, to);
+                            w = lo + t < hi ? list_weight(s, lo + t, sc) : 0;
+                            const int at = list_reaching(s, lo, hi, w, after(share_of(g.u, mass, false) + 1, above_first), sc, to);
                             put_row<DRAW>(a, r, kept, entry_index(s.list[at]), entry_weight(s, at, sc), mass);
                         }
                     }
@@ -1292,7 +1356,7 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
             if (c != rank)
                 first = min(first, (int)ld_rank(&s.first, c));
         if (rank == 0)
-            put_row<DRAW>(a, r, 1, first, 1, 1);
+            put_row<DRAW>(a, r, 1, first);
         if (!DRAW)
             write_row(row, out, a.same_phase, Prefix{top_key, first});
         row_sync(C);
@@ -1339,21 +1403,20 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
             sort_list(s, n);
             if (g.k > 0)
                 n = min(n, g.k);
-            u128 mass = 0;
-            uint64_t w = 0;
+            uint64_t mass = 0, w = 0;
             if (DRAW || g.p < 1.0f) {
-                w = t < n ? entry_weight(s, t, sc) : 0;
+                w = t < n ? list_weight(s, t, sc) : 0;
                 mass = list_mass(s, 0, n, w, sc);
             }
             if (g.p < 1.0f) {
-                const u128 goal = share_of(g.p, mass, true);
-                n = list_reaching(s, 0, n, w, 0, goal > 1 ? goal : 1, sc, mass) + 1;
+                const uint64_t goal = share_of(g.p, mass, true);
+                n = list_reaching(s, 0, n, w, goal > 1 ? goal : 1, sc, mass) + 1;
                 w = t < n ? w : 0;
             }
             if (DRAW) {
-                u128 to;
-                const int at = list_reaching(s, 0, n, w, 0, share_of(g.u, mass, false) + 1, sc, to);
-                put_row<DRAW>(a, r, n, entry_index(s.list[at]), entry_weight(s, at, sc), mass);
+                uint64_t to;
+                const int at = list_reaching(s, 0, n, w, share_of(g.u, mass, false) + 1, sc, to);
+                put_row<DRAW>(a, r, n, entry_index(s.list[at]), entry_weight(s, at, sc), (u128)mass << 10);
             } else {
                 put_row<DRAW>(a, r, n);
             }

@@ -62,7 +62,12 @@ __device__ __forceinline__ long long scaled48(float l, float ch, float cl)
 {
     const float t = __fmul_rn(l, ch);
     const float e = __fmaf_rn(l, cl, __fmaf_rn(l, ch, -t));
-    return __float2ll_rn(t * 281474976710656.0f) + __float2ll_rn(e * 281474976710656.0f);
+    // t = n + f, |f| <= 1/2, and f in steps of 2^-24, the rest with e in steps of
+    // 2^-48 (|e| < 2^-10): conversions to 32 bits, which are fast
+    const float n = rintf(t), f = (t - n) * 16777216.0f, a = rintf(f);
+    const float b = fmaf(e, 16777216.0f, f - a) * 16777216.0f;   // (below 2^39: as two)
+    const float b1 = rintf(b * 5.9604644775390625e-8f);
+    return ((long long)(int)n << 48) + ((long long)((int)a + (int)b1) << 24) + (long long)(int)rintf(fmaf(b1, -16777216.0f, b));
 }
 
 __device__ __forceinline__ RowScale row_scale(float m, float T)
@@ -90,7 +95,7 @@ __device__ __forceinline__ uint64_t exp2_neg(uint64_t x, const uint64_t* roots)
     const uint64_t y = __umul64hi((x & ((1ull << 42) - 1)) << 16, 0xb17217f7d1cf79acull);   // 2^64 ln 2
     const float f = (float)(y >> 32) * 2.3283064365386963e-10f;
     const float c = f * f * f * (1.0f / 6 - f * (1.0f / 24 - f * (1.0f / 120)));
-    const uint64_t q = y - (__umul64hi(y, y) >> 1) + ((uint64_t)(c * 9.223372036854775808e18f) << 1);   // 1 - e^-y
+    const uint64_t q = y - (__umul64hi(y, y) >> 1) + ((uint64_t)(uint32_t)(c * 1.8014398509481984e16f) << 10);   // 1 - e^-y; c < 2^-22, in 2^-54
     const uint64_t w = roots[j] - __umul64hi(roots[j], q);
     return n ? ((w >> (n - 1)) + 1) >> 1 : w;
 }
@@ -124,21 +129,23 @@ __device__ __forceinline__ u128 share_of(float p, u128 z, bool up)
     return up ? (n + (((u128)1 << s) - 1)) >> s : n >> s;
 }
 
-// w / z as the nearest fp32, z < 2^96: a quotient of the leading 24 bits, and
-// one step by what is left.
+// The same of a whole number below 2^64.
+__device__ __forceinline__ uint64_t share_of(float p, uint64_t z, bool up)
+{
+    return (uint64_t)share_of(p, (u128)z, up);
+}
+
+// w / z as the nearest fp32 (but for one case in 2^20), z < 2^96: a quotient of
+// the leading bits, and a correction by the rest.
 __device__ __forceinline__ float quotient(uint64_t w, u128 z)
 {
-    int up = 0;
-    while (z >> 63) {   // z to 63 bits: its rounding is far below the quotient's
-        z >>= 8;
-        up += 8;
-    }
-    const uint64_t y = (uint64_t)z;
+    const uint64_t over = (uint64_t)(z >> 64);
+    const int down = over ? 64 - __clzll(over) : 0;
+    const uint64_t y = (uint64_t)(z >> down);
     const float wh = __ull2float_rz(w), yh = __ull2float_rz(y);
     const float wl = (float)(w - (uint64_t)wh), yl = (float)(y - (uint64_t)yh);
     const float q = __fdiv_rn(wh, yh);
-    const float rest = __fmaf_rn(-q, yl, __fmaf_rn(-q, yh, wh) + wl);
-    return ldexpf(q + __fdiv_rn(rest, yh), -up);
+    return (q + __fdiv_rn(__fmaf_rn(-q, yl, __fmaf_rn(-q, yh, wh) + wl), yh)) * __int_as_float((127 - down) << 23);
 }
 
 }  // namespace sv
