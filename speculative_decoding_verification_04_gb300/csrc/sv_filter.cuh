@@ -63,6 +63,7 @@ struct FilterShared {
     uint64_t roots[64];
     u128 part[kFilterWarps];
     u128 found_mass;
+    RowScale scale;
     uint64_t part64[kFilterWarps], found64;
     Command cmd;
     uint32_t warp_top[kFilterWarps], warp_low[kFilterWarps];
@@ -97,6 +98,36 @@ constexpr size_t filter_smem_bytes(int groups)
 // the row, the block and the cluster
 // ---------------------------------------------------------------------------
 
+// A thread's vectors at i, i + stride, ...: four on their way while one is
+// worked on.  The loops over them stay rolled: code that runs a few times a row
+// comes from L2, and costs more than it does.
+struct VectorQueue {
+    const uint4* v;
+    int at, end, stride;
+    uint4 w[4];
+    __device__ __forceinline__ VectorQueue(const uint4* v_, int i, int end_, int stride_) : v(v_), at(i), end(end_), stride(stride_)
+    {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            w[u] = load();
+    }
+    __device__ __forceinline__ uint4 load()
+    {
+        const uint4 x = at < end ? v[at] : make_uint4(0, 0, 0, 0);
+        at += stride;
+        return x;
+    }
+    __device__ __forceinline__ uint4 next()
+    {
+        const uint4 x = w[0];
+        w[0] = w[1];
+        w[1] = w[2];
+        w[2] = w[3];
+        w[3] = load();
+        return x;
+    }
+};
+
 // A CTA's part of a row: a range of its 16-byte vectors, and for rank 0 the
 // elements before and after them.  Plain loads throughout: the filtered row may
 // be written where the row is.
@@ -120,19 +151,14 @@ template <typename T> struct RowSpan {
         const int t = threadIdx.x;
         return t < rest ? (t < head ? t : nvec * E + t) : -1;
     }
-    // f(values, index of the first) for every vector, the next one on its way.
-    // (Rolled: code that runs once a row comes from L2, and costs more than it does.)
+    // f(values, index of the first) for every vector.
     template <typename F> __device__ __forceinline__ void vectors(F&& f) const
     {
-        const uint4* v = vec();
-        int i = v0 + threadIdx.x;
-        uint4 next = i < v1 ? v[i] : make_uint4(0, 0, 0, 0);
+        VectorQueue q(vec(), v0 + (int)threadIdx.x, v1, kFilterThreads);
 #pragma unroll 1
-        for (; i < v1; i += kFilterThreads) {
+        for (int i = v0 + (int)threadIdx.x; i < v1; i += kFilterThreads) {
             float x[E];
-            Elem<T>::unpack(next, x);
-            if (i + kFilterThreads < v1)
-                next = v[i + kFilterThreads];
+            Elem<T>::unpack(q.next(), x);
             f(x, head + i * E);
         }
     }
@@ -242,31 +268,31 @@ struct Prefix {
 
 // The sum over a prefix of 1 (kCount) or of the weights.
 template <bool kCount, typename T>
-__device__ u128 prefix_sum(const RowSpan<T>& row, Prefix p, const RowScale& sc, FilterShared& s)
+__device__ u128 prefix_sum(const RowSpan<T>& row, Prefix p, FilterShared& s)
 {
     u128 a = 0;
     row.each([&](float x, int i) {
         if (p.has(key_of(x), i))
-            a += kCount ? 1 : weight62(x, sc, s.roots);
+            a += kCount ? 1 : weight62(x, s.scale, s.roots);
     });
     return block_sum(a, s);
 }
 
 // The shortest prefix within `most` that sums to `goal` (which `most` does).
 template <bool kCount, typename T>
-__device__ Prefix prefix_reaching(const RowSpan<T>& row, u128 goal, Prefix most, uint32_t top, const RowScale& sc, FilterShared& s)
+__device__ Prefix prefix_reaching(const RowSpan<T>& row, u128 goal, Prefix most, uint32_t top, FilterShared& s)
 {
     uint32_t lo = most.key, hi = top;
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo) / 2 + 1;
-        if (prefix_sum<kCount>(row, Prefix{mid, INT_MAX}, sc, s) >= goal)
+        if (prefix_sum<kCount>(row, Prefix{mid, INT_MAX}, s) >= goal)
             lo = mid;
         else
             hi = mid - 1;
     }
-    const u128 above = prefix_sum<kCount>(row, Prefix{lo + 1, INT_MAX}, sc, s);
+    const u128 above = prefix_sum<kCount>(row, Prefix{lo + 1, INT_MAX}, s);
     int a = 0, b = most.key == lo ? min(most.index, row.V - 1) : row.V - 1;
-    const u128 each = kCount ? 1 : weight62(value_of(lo), sc, s.roots);
+    const u128 each = kCount ? 1 : weight62(value_of(lo), s.scale, s.roots);
     while (a < b) {
         const int mid = a + (b - a) / 2;
         int n = 0;
@@ -287,18 +313,16 @@ struct Settings {
     int k;
 };
 
-// A row's numbers.
+// A row's numbers, by one thread.
 template <bool DRAW>
 __device__ __forceinline__ void put_row(const FilterArgs& a, long long r, int kept, int token = -1, uint64_t weight = 1, u128 mass = 1)
 {
-    if (threadIdx.x == 0) {
-        if (a.has_kept)
-            a.out_kept[r] = kept;
-        if (DRAW) {
-            a.out_tokens[r] = token;
-            if (a.has_prob)
-                a.out_prob[r] = token < 0 ? __int_as_float(0x7fc00000) : quotient(weight, mass);
-        }
+    if (a.has_kept)
+        a.out_kept[r] = kept;
+    if (DRAW) {
+        a.out_tokens[r] = token;
+        if (a.has_prob)
+            a.out_prob[r] = token < 0 ? __int_as_float(0x7fc00000) : quotient(weight, mass);
     }
 }
 
@@ -392,27 +416,29 @@ __device__ __forceinline__ uint32_t min_p_key(float m, double t_log)
 
 // By bisection, rank 0 alone.
 template <typename T, bool DRAW>
-__device__ __noinline__ void whole_row(const FilterArgs& a, long long r, const Settings& g, float m, Prefix end, const RowScale& sc, FilterShared& s)
+__device__ __noinline__ void whole_row(const FilterArgs& a, long long r, const Settings& g, float m, Prefix end, FilterShared& s)
 {
     const RowSpan<T> row(static_cast<const T*>(a.logits) + r * a.V, a.V, 0, 1);
     const uint32_t top = key_of(m);
     u128 mass = 0;
-    if (g.k > 0 && prefix_sum<true>(row, end, sc, s) > (u128)g.k)
-        end = prefix_reaching<true>(row, (u128)g.k, end, top, sc, s);
+    if (g.k > 0 && prefix_sum<true>(row, end, s) > (u128)g.k)
+        end = prefix_reaching<true>(row, (u128)g.k, end, top, s);
     if (g.p < 1.0f || DRAW)
-        mass = prefix_sum<false>(row, end, sc, s);
+        mass = prefix_sum<false>(row, end, s);
     if (g.p < 1.0f) {
         const u128 goal = share_of(g.p, mass, true);
-        end = prefix_reaching<false>(row, goal > 1 ? goal : 1, end, top, sc, s);
+        end = prefix_reaching<false>(row, goal > 1 ? goal : 1, end, top, s);
         if (DRAW)
-            mass = prefix_sum<false>(row, end, sc, s);
+            mass = prefix_sum<false>(row, end, s);
     }
-    const int kept = a.has_kept ? (int)prefix_sum<true>(row, end, sc, s) : 0;
+    const int kept = a.has_kept ? (int)prefix_sum<true>(row, end, s) : 0;
     if (DRAW) {
-        const Prefix at = prefix_reaching<false>(row, share_of(g.u, mass, false) + 1, end, top, sc, s);
-        put_row<DRAW>(a, r, kept, at.index, weight62(value_of(at.key), sc, s.roots), mass);
+        const Prefix at = prefix_reaching<false>(row, share_of(g.u, mass, false) + 1, end, top, s);
+        if (threadIdx.x == 0)
+            put_row<DRAW>(a, r, kept, at.index, weight62(value_of(at.key), s.scale, s.roots), mass);
     } else {
-        put_row<DRAW>(a, r, kept);
+        if (threadIdx.x == 0)
+            put_row<DRAW>(a, r, kept);
         write_row(row, static_cast<T*>(a.out) + r * a.V, a.same_phase, end);
     }
 }
@@ -518,16 +544,16 @@ __device__ __noinline__ void sort_list(FilterShared& s, int n)
     __syncthreads();
 }
 
-__device__ __noinline__ uint64_t entry_weight(const FilterShared& s, int r, const RowScale& sc)
+__device__ __noinline__ uint64_t entry_weight(const FilterShared& s, int r)
 {
-    return weight62(value_of(entry_key(s.list[r])), sc, s.roots);
+    return weight62(value_of(entry_key(s.list[r])), s.scale, s.roots);
 }
 
 // Sums over the list are in units of 2^-52: 2048 weights fit 64 bits, and what
 // their rounding moves stays below a thousandth of a token of weight 2^-32.
 __device__ __forceinline__ uint64_t weight52(uint64_t w62) { return (w62 + 512) >> 10; }
 
-__device__ __noinline__ uint64_t list_weight(const FilterShared& s, int r, const RowScale& sc) { return weight52(entry_weight(s, r, sc)); }
+__device__ __noinline__ uint64_t list_weight(const FilterShared& s, int r) { return weight52(entry_weight(s, r)); }
 
 // Exclusive prefix sum over the block; `total` gets the whole.
 __device__ __noinline__ uint64_t block_scan(uint64_t v, FilterShared& s, uint64_t& total)
@@ -558,23 +584,23 @@ __device__ __noinline__ uint64_t block_scan(uint64_t v, FilterShared& s, uint64_
 
 // The mass of the sorted list's ranks lo .. hi - 1, a block's worth at a time;
 // `first` is the weight of rank lo + threadIdx.x (0 from hi on).
-__device__ __noinline__ uint64_t list_mass(FilterShared& s, int lo, int hi, uint64_t first, const RowScale& sc)
+__device__ __noinline__ uint64_t list_mass(FilterShared& s, int lo, int hi, uint64_t first)
 {
     uint64_t sum = first, total;
     for (int r = lo + kFilterThreads + (int)threadIdx.x; r < hi; r += kFilterThreads)
-        sum += list_weight(s, r, sc);
+        sum += list_weight(s, r);
     block_scan(sum, s, total);
     return total;
 }
 
 // The first rank of lo .. hi - 1 whose cumulative mass, counted from rank lo on,
 // reaches goal (hi - 1 if none does); its mass in `mass`.
-__device__ __noinline__ int list_reaching(FilterShared& s, int lo, int hi, uint64_t first, uint64_t goal, const RowScale& sc, uint64_t& mass)
+__device__ __noinline__ int list_reaching(FilterShared& s, int lo, int hi, uint64_t first, uint64_t goal, uint64_t& mass)
 {
     uint64_t base = 0;
     for (int r0 = lo;; r0 += kFilterThreads) {
         const int r = r0 + (int)threadIdx.x;
-        const uint64_t w = r0 == lo ? first : r < hi ? list_weight(s, r, sc) : 0;
+        const uint64_t w = r0 == lo ? first : r < hi ? list_weight(s, r) : 0;
         uint64_t total;
         const uint64_t c = base + block_scan(w, s, total);
         base += total;
@@ -775,15 +801,12 @@ __device__ __noinline__ void bin_vectors(const RowSpan<T> row, int stride, Prefi
 {
     constexpr int E = Elem<T>::E;
     const float least = value_of(end.key);
-    const uint4* v = row.vec();
     int i = row.v0 + (int)threadIdx.x;
-    uint4 next = i < row.v1 ? v[i] : make_uint4(0, 0, 0, 0);
+    VectorQueue q(row.vec(), i, row.v1, stride);
 #pragma unroll 1
     for (; i < row.v1; i += stride) {
         float x[E];
-        Elem<T>::unpack(next, x);
-        if (i + stride < row.v1)
-            next = v[i + stride];
+        Elem<T>::unpack(q.next(), x);
         const int left = end.index - (row.head + i * E);   // ties up to this one count
 #pragma unroll
         for (int j = 0; j < E; j += 2)
@@ -810,18 +833,26 @@ __device__ __noinline__ float tail_vectors(const RowSpan<T> row, float from, con
     int waiting = 0, none = 0;
     const uint64_t ch2 = f2_pack(b.ch, b.ch), cl2 = f2_pack(b.cl, b.cl), unit2 = f2_pack(-b.unit, -b.unit);
     // stretches 0, 8, 16, ... are the sample; all of a warp's lanes go through every stretch
-    int n = 1;
-    auto at = [&](int k) { return row.v0 + k * kFilterThreads + t; };
     const int stretches = (row.v1 - row.v0 + kFilterThreads - 1) / kFilterThreads;
-    uint4 next = at(n) < row.v1 ? v[at(n)] : make_uint4(0, 0, 0, 0);
+    int ahead = 1;
+    auto load = [&]() {
+        const int i = row.v0 + ahead * kFilterThreads + t;
+        ahead += ahead % kGroup == kGroup - 1 ? 2 : 1;
+        return i < row.v1 ? v[i] : make_uint4(0, 0, 0, 0);
+    };
+    uint4 w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        w[u] = load();
 #pragma unroll 1
-    while (n < stretches) {
-        const bool there = at(n) < row.v1;
+    for (int n = 1; n < stretches; n += n % kGroup == kGroup - 1 ? 2 : 1) {
+        const bool there = row.v0 + n * kFilterThreads + t < row.v1;
         float x[E];
-        Elem<T>::unpack(next, x);
-        n += n % kGroup == kGroup - 1 ? 2 : 1;
-        if (n < stretches && at(n) < row.v1)
-            next = v[at(n)];
+        Elem<T>::unpack(w[0], x);
+        w[0] = w[1];
+        w[1] = w[2];
+        w[2] = w[3];
+        w[3] = load();
         uint64_t add = 0;   // (+0, +0)
         float low = x[0];
         uint32_t in = 0;
@@ -964,13 +995,13 @@ __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to,
 
 template <typename T, bool DRAW>
 __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const Settings& g, const RowSpan<T>& row, int rank, Prefix end,
-                                        float lone_x, const RowScale& whole, FilterShared& s)
+                                        float lone_x, FilterShared& s)
 {
     const int C = a.C, t = threadIdx.x;
     T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * a.V);
-    const BinScale bs = bin_scale(whole);
-    RowScale sc = whole;
-    sc.top = ((long long)(int)(bs.ref - __float_as_uint(kMagicBin)) + 1) * (1ll << (48 - kBinShift));   // as the bins' masses
+    const BinScale bs = bin_scale(s.scale);
+    if (t == 0)   // (read behind the barriers of fill_bins)
+        s.scale.top = ((long long)(int)(bs.ref - __float_as_uint(kMagicBin)) + 1) * (1ll << (48 - kBinShift));   // as the bins' masses
     int k = g.k;
     bool tail = k == 0 && g.min_p == 0.0f;
     for (;;) {
@@ -1049,7 +1080,8 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                             give_up = n_last > kList;
                         }
                     } else if (!DRAW) {   // top-k reaches past the last token
-                        put_row<DRAW>(a, r, n_all);
+                        if (t == 0)
+                            put_row<DRAW>(a, r, n_all);
                         c.op = kCmdWrite;
                         c.key = end.key;
                         c.index = end.index;
@@ -1090,15 +1122,16 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                         bool draw_now = DRAW;
                         if (stage == 2) {
                             const int from = n - n_last;   // the last bin's tokens
-                            w = from + t < n ? list_weight(s, from + t, sc) : 0;
-                            const u128 own = (u128)list_mass(s, from, n, w, sc) << 10;
+                            w = from + t < n ? list_weight(s, from + t) : 0;
+                            const u128 own = (u128)list_mass(s, from, n, w) << 10;
                             // the goal again, with that bin's mass by its tokens
                             const u128 goal = share_of(g.p, total - bin_mass(s, last) + own, true);
-                            const int end_r = list_reaching(s, from, n, w, after(goal, above), sc, to);
+                            const int end_r = list_reaching(s, from, n, w, after(goal, above), to);
                             mass = above + ((u128)to << 10);
                             kept += end_r - from + 1;
                             if (!DRAW) {
-                                put_row<DRAW>(a, r, kept);
+                                if (t == 0)
+                                    put_row<DRAW>(a, r, kept);
                                 c.op = kCmdWrite;
                                 c.key = entry_key(s.list[end_r]);
                                 c.index = entry_index(s.list[end_r]);
@@ -1119,9 +1152,10 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                             }
                         }
                         if (draw_now) {
-                            w = lo + t < hi ? list_weight(s, lo + t, sc) : 0;
-                            const int at = list_reaching(s, lo, hi, w, after(share_of(g.u, mass, false) + 1, above_first), sc, to);
-                            put_row<DRAW>(a, r, kept, entry_index(s.list[at]), entry_weight(s, at, sc), mass);
+                            w = lo + t < hi ? list_weight(s, lo + t) : 0;
+                            const int at = list_reaching(s, lo, hi, w, after(share_of(g.u, mass, false) + 1, above_first), to);
+                            if (t == 0)
+                                put_row<DRAW>(a, r, kept, entry_index(s.list[at]), entry_weight(s, at), mass);
                         }
                     }
                 }
@@ -1129,7 +1163,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                     Settings left = g;
                     left.k = k;
                     c = Command{kCmdEnd, 0, 0, -1, 0, 0, 0, 0};
-                    whole_row<T, DRAW>(a, r, left, whole.m, end, whole, s);
+                    whole_row<T, DRAW>(a, r, left, s.scale.m, end, s);
                 }
                 __syncthreads();
                 if (t == 0) {
@@ -1166,7 +1200,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
         row_sync(C);   // the bins and the command have been read
         if (c_top_k) {
             if (!DRAW && g.p >= 1.0f) {   // top-k was all there was
-                if (rank == 0)
+                if (rank == 0 && t == 0)
                     put_row<DRAW>(a, r, k);
                 write_row(row, out, a.same_phase, end);
                 return;
@@ -1295,7 +1329,7 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
                 n += s.warp_count[turn][i];
             if (n >= share) {
                 lo = mid;
-                if (n <= share + share / 2 + 8)
+                if (n <= share + share / 4 + (C > 1 ? 1 : 8))
                     break;
             } else {
                 hi = mid - 1;
@@ -1316,7 +1350,7 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
     }
 
     if (!good || top_key <= kKeyNegInf || top_key >= kKeyPosInf) {
-        if (rank == 0)
+        if (rank == 0 && t == 0)
             put_row<DRAW>(a, r, -1);
         if (!DRAW)
             fill_row(row, out, a.same_phase, Bits<T>::nan);
@@ -1343,7 +1377,7 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
         for (int c = 0; c < C; ++c)
             if (c != rank)
                 first = min(first, (int)ld_rank(&s.first, c));
-        if (rank == 0)
+        if (rank == 0 && t == 0)
             put_row<DRAW>(a, r, 1, first);
         if (!DRAW)
             write_row(row, out, a.same_phase, Prefix{top_key, first});
@@ -1352,13 +1386,13 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
     }
 
     Prefix end{kKeyNegInf + 1, INT_MAX};
-    if (g.min_p > 0.0f) {
-        if (t == kFilterThreads - 32)
-            s.least_key = min_p_key(m, t_log);
-        __syncthreads();
+    if (t == 0)
+        s.scale = row_scale(m, g.T);
+    if (t == kFilterThreads - 32 && g.min_p > 0.0f)
+        s.least_key = min_p_key(m, t_log);
+    __syncthreads();
+    if (g.min_p > 0.0f)
         end.key = max(end.key, s.least_key);
-    }
-    const RowScale sc = row_scale(m, g.T);
 
     // 3. Few candidates (a top-k bound, min-p, or a short row): they are read
     // again, by the groups that hold one, sorted and weighed.
@@ -1392,21 +1426,43 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
             if (g.k > 0)
                 n = min(n, g.k);
             uint64_t mass = 0, w = 0;
-            if (DRAW || g.p < 1.0f) {
-                w = t < n ? list_weight(s, t, sc) : 0;
-                mass = list_mass(s, 0, n, w, sc);
-            }
-            if (g.p < 1.0f) {
-                const uint64_t goal = share_of(g.p, mass, true);
-                n = list_reaching(s, 0, n, w, goal > 1 ? goal : 1, sc, mass) + 1;
-                w = t < n ? w : 0;
-            }
-            if (DRAW) {
-                uint64_t to;
-                const int at = list_reaching(s, 0, n, w, share_of(g.u, mass, false) + 1, sc, to);
-                put_row<DRAW>(a, r, n, entry_index(s.list[at]), entry_weight(s, at, sc), (u128)mass << 10);
+            if (n <= kFilterThreads) {   // a rank a thread: one sum answers both questions
+                if (DRAW || g.p < 1.0f) {
+                    const uint64_t w62 = t < n ? entry_weight(s, t) : 0;
+                    w = weight52(w62);
+                    const uint64_t c = block_scan(w, s, mass);
+                    if (g.p < 1.0f) {
+                        const uint64_t share = share_of(g.p, mass, true), goal = share > 1 ? share : 1;
+                        if (c < goal && c + w >= goal) {
+                            s.found = t;
+                            s.found64 = c + w;
+                        }
+                        __syncthreads();
+                        n = s.found + 1;
+                        mass = s.found64;
+                    }
+                    if (DRAW) {
+                        const uint64_t goal = share_of(g.u, mass, false) + 1;
+                        if (c < goal && c + w >= goal)
+                            put_row<DRAW>(a, r, n, entry_index(s.list[t]), w62, (u128)mass << 10);
+                    }
+                }
+                if (!DRAW && t == 0)
+                    put_row<DRAW>(a, r, n);
             } else {
-                put_row<DRAW>(a, r, n);
+                if (DRAW || g.p < 1.0f) {
+                    w = list_weight(s, t);
+                    mass = list_mass(s, 0, n, w);
+                }
+                if (g.p < 1.0f) {
+                    const uint64_t goal = share_of(g.p, mass, true);
+                    n = list_reaching(s, 0, n, w, goal > 1 ? goal : 1, mass) + 1;
+                    w = t < n ? w : 0;
+                }
+                uint64_t to;
+                const int at = DRAW ? list_reaching(s, 0, n, w, share_of(g.u, mass, false) + 1, to) : 0;
+                if (t == 0)
+                    put_row<DRAW>(a, r, n, entry_index(s.list[at]), entry_weight(s, at), (u128)mass << 10);
             }
             __syncwarp();
             if (C > 1)
@@ -1438,18 +1494,18 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
         int total = all;
         for (int c = 1; c < C; ++c)
             total += s.peer_gone[c];
-        if (rank == 0)
+        if (rank == 0 && t == 0)
             put_row<DRAW>(a, r, total);
         return;
     }
 
     // 5. The bins.
-    if (sc.cold) {
+    if (s.scale.cold) {
         if (rank == 0)
-            whole_row<T, DRAW>(a, r, g, m, end, sc, s);
+            whole_row<T, DRAW>(a, r, g, m, end, s);
         return;
     }
-    binned_row<T, DRAW>(a, r, g, row, rank, end, lone_x, sc, s);
+    binned_row<T, DRAW>(a, r, g, row, rank, end, lone_x, s);
     row_sync(C);
 }
 
