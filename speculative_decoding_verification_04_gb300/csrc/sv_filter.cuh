@@ -37,11 +37,11 @@ constexpr int kClusterMost = 16;
 constexpr int kGroup = 8;          // vectors of a thread whose maximum is kept
 constexpr int kGroupsMost = 49;    // sv_max_vocab on one CTA
 constexpr int kList = 2048;        // tokens sorted at a time
-constexpr int kBinShift = 6;       // 64 bins an octave of weights
-constexpr int kBins = 64 << kBinShift;
+constexpr int kBins = 4096;
+constexpr int kBinShift = 6;       // 64 bins an octave of weights or more,
+constexpr int kBinShiftMost = 9;   // up to 512
 constexpr int kBinsEach = kBins / kFilterThreads;
 constexpr uint32_t kCarryBits = 12;   // of a bin's upper word; its count above (V < 2^20)
-constexpr int kQueue = 320;        // a warp's tokens on their way to the bins: 63 and a vector each
 
 // What rank 0 of a row's cluster asks of all its CTAs next.
 enum : int { kCmdEnd = 0, kCmdGather = 1, kCmdWrite = 2, kCmdRecount = 3 };
@@ -56,10 +56,7 @@ struct alignas(16) Command {
 };
 
 struct FilterShared {
-    union {
-        uint64_t list[kList];
-        float queue[kFilterWarps][kQueue];
-    };
+    uint64_t list[kList];
     uint64_t roots[64];
     u128 part[kFilterWarps];
     u128 found_mass;
@@ -619,72 +616,74 @@ __device__ __noinline__ int list_reaching(FilterShared& s, int lo, int hi, uint6
 // ---------------------------------------------------------------------------
 // Any number of candidates: bins of weight
 // ---------------------------------------------------------------------------
-// A bin holds the tokens whose l log2(e) / T rounds to the same 64th; it sums
-// 2^f - 1 of the remainders f, in units of 2^-29, and counts.  Bin 0 holds the
-// largest logit.  The last bin holds whatever weighs less than 2^-63 too; its
-// mass does not count.  Weights are relative to 2^(1/64) times bin 0's centre.
-constexpr float kMagicBin = 196608.0f;       // 1.5 * 2^17: adding it rounds to 64ths
-constexpr float kMagicSum = 0.0234375f;      // 1.5 * 2^-6: adding it rounds to 2^-29
-
+// A bin holds the tokens whose l log2(e) / T rounds to the same multiple of
+// 2^-shift; it sums 2^f - 1 of the remainders f, in units of 2^-(23 + shift), and
+// counts.  Bin 0 holds the largest logit.  The last bin holds whatever weighs
+// less than the bins reach too; its mass does not count.  Weights are relative
+// to a bin's width above bin 0's centre.
 struct BinScale {
-    float ch, cl, least;   // least: below it, the last bin
-    float unit;            // the centre of the bin before the first, in 64ths of an octave
+    float ch, cl, least;   // least: logits below it count as it
+    float step, magic;     // 2^-shift; adding magic (1.5 * 2^23 steps) rounds to steps
+    float unit;            // the centre of the bin before the first, in octaves
     uint32_t ref;          // the bits of the largest logit's rounded product
+    int shift;
 };
 
-__device__ __forceinline__ BinScale bin_scale(const RowScale& sc)
+__device__ __forceinline__ BinScale bin_scale(const RowScale& sc, int shift)
 {
     BinScale b;
     b.ch = sc.ch;
     b.cl = sc.cl;
-    const float at = __fadd_rn(__fmul_rn(sc.m, sc.ch), kMagicBin);
+    b.shift = shift;
+    b.step = __int_as_float((127 - shift) << 23);
+    b.magic = 12582912.0f * b.step;
+    const float at = __fadd_rn(__fmul_rn(sc.m, sc.ch), b.magic);
     b.ref = __float_as_uint(at);
-    b.unit = (at - kMagicBin) + 0.015625f;
-    b.least = fmaxf(sc.m - 44.6f * sc.T, -3.4028234e38f);   // 64.3 octaves
+    b.unit = (at - b.magic) + b.step;
+    b.least = fmaxf(sc.m - 44.6f * sc.T, -3.4028234e38f);   // 64.3 octaves: no weight
     return b;
 }
 
 __device__ __forceinline__ int bin_of(float l, const BinScale& b)
 {
-    const uint32_t x = b.ref - __float_as_uint(__fadd_rn(__fmul_rn(fmaxf(l, b.least), b.ch), kMagicBin));
+    const uint32_t x = b.ref - __float_as_uint(__fadd_rn(__fmul_rn(fmaxf(l, b.least), b.ch), b.magic));
     return (int)min(x, (uint32_t)kBins - 1);
 }
 
-__device__ __forceinline__ void bin_add(FilterShared& s, uint32_t x, uint32_t q)
+__device__ __forceinline__ void bin_add(FilterShared& s, uint32_t i, uint32_t q)
 {
-    const uint32_t i = min(x, (uint32_t)kBins - 1);
     const uint32_t old = atomicAdd(&s.bin.lo[i], q);
     atomicAdd(&s.bin.hi[i], (1u << kCarryBits) + (old + q < old ? 1u : 0u));
 }
 
-// Two tokens; `in` says which of them count.
-__device__ __forceinline__ void bin_pair(FilterShared& s, float l0, float l1, bool in0, bool in1, const BinScale& b)
+// Two tokens of at least b.least, the packed pair L; `in` says which of them count.
+__device__ __forceinline__ void bin_pair(FilterShared& s, uint64_t L, bool in0, bool in1, const BinScale& b)
 {
-    const uint64_t L = f2_pack(fmaxf(l0, b.least), fmaxf(l1, b.least));
-    const uint64_t nt = f2_mul(L, f2_pack(-b.ch, -b.ch));
+    const uint64_t magic = f2_pack(b.magic, b.magic), nt = f2_mul(L, f2_pack(-b.ch, -b.ch));
     const uint64_t e = f2_fma(L, f2_pack(b.cl, b.cl), f2_fma(L, f2_pack(b.ch, b.ch), nt));
-    const uint64_t at = f2_sub(f2_pack(kMagicBin, kMagicBin), nt);
-    const uint64_t f = f2_sub(e, f2_add(nt, f2_sub(at, f2_pack(kMagicBin, kMagicBin))));
-    // 2^f - 1, |f| < 2^-7 + 2^-11: ln 2 f + (ln 2 f)^2 / 2 + (ln 2 f)^3 / 6, the next term below 2^-35
+    const uint64_t at = f2_sub(magic, nt);
+    const uint64_t f = f2_sub(e, f2_add(nt, f2_sub(at, magic)));
+    // 2^f - 1, |f| < 2^-7 + 2^-11: ln 2 f + (ln 2 f)^2 / 2 + (ln 2 f)^3 / 6, the next term below
+    // 2^-35; adding one and a half steps rounds it to steps 2^-23
     const uint64_t g = f2_fma(f, f2_fma(f, f2_pack(0.05550411f, 0.05550411f), f2_pack(0.24022651f, 0.24022651f)), f2_pack(0.69314718f, 0.69314718f));
-    const uint64_t q = f2_fma(f, g, f2_pack(kMagicSum, kMagicSum));
-    const uint32_t unit = 0x3c800000u;   // 2^-6: q's bits less these are (2^f - 1 + 2^-7) 2^29
+    const uint64_t q = f2_fma(f, g, f2_pack(1.5f * b.step, 1.5f * b.step));
+    const uint32_t unit = __float_as_uint(b.step);   // q's bits less these are (2^f - 1) / step 2^23 + 2^22
     if (in0)
-        bin_add(s, b.ref - (uint32_t)at, (uint32_t)q - unit);
+        bin_add(s, min(b.ref - (uint32_t)at, (uint32_t)kBins - 1), (uint32_t)q - unit);
     if (in1)
-        bin_add(s, b.ref - (uint32_t)(at >> 32), (uint32_t)(q >> 32) - unit);
+        bin_add(s, min(b.ref - (uint32_t)(at >> 32), (uint32_t)kBins - 1), (uint32_t)(q >> 32) - unit);
 }
 
 __device__ __forceinline__ uint32_t bin_count(const FilterShared& s, int i) { return s.bin.hi[i] >> kCarryBits; }
 
 // The mass of bin i in units of 2^-62.
-__device__ __forceinline__ u128 bin_mass(const FilterShared& s, int i)
+__device__ __forceinline__ u128 bin_mass(const FilterShared& s, int i, int shift)
 {
     const uint32_t hi = s.bin.hi[i], n = hi >> kCarryBits;
     if (n == 0 || i == kBins - 1)
         return 0;
-    const uint64_t sum = (((uint64_t)(hi & ((1u << kCarryBits) - 1)) << 32) | s.bin.lo[i]) + ((uint64_t)n << 29) - ((uint64_t)n << 22);
-    return ((u128)sum * s.roots[(i + 1) & 63]) >> (29 + ((i + 1) >> 6));
+    const uint64_t sum = (((uint64_t)(hi & ((1u << kCarryBits) - 1)) << 32) | s.bin.lo[i]) + ((uint64_t)n << (23 + shift)) - ((uint64_t)n << 22);
+    return ((u128)sum * exp2_neg((uint64_t)(i + 1) << (48 - shift), s.roots)) >> (23 + shift);
 }
 
 // A thread's bins (kBinsEach of them), and what is before them.
@@ -693,7 +692,7 @@ struct BinPart {
     int n_before, n_own;
 };
 
-__device__ __noinline__ BinPart scan_bins(FilterShared& s, u128& mass, int& count)
+__device__ __noinline__ BinPart scan_bins(FilterShared& s, int shift, u128& mass, int& count)
 {
     BinPart q;
     q.own = 0;
@@ -702,7 +701,7 @@ __device__ __noinline__ BinPart scan_bins(FilterShared& s, u128& mass, int& coun
 #pragma unroll 1
     for (int i = 0; i < kBinsEach; ++i) {
         const int j = i0 + ((i + threadIdx.x) & (kBinsEach - 1));   // (lanes on different banks)
-        q.own += bin_mass(s, j);
+        q.own += bin_mass(s, j, shift);
         q.n_own += (int)bin_count(s, j);
     }
     u128 total;
@@ -722,7 +721,7 @@ struct BinAt {
     u128 before;
 };
 
-template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart& q, FilterShared& s, u128 goal)
+template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart& q, FilterShared& s, int shift, u128 goal)
 {
     __syncthreads();
     if (threadIdx.x == 0)
@@ -740,7 +739,7 @@ template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart&
         const int lane = threadIdx.x & 31, i = s.found * kBinsEach + lane;
         u128 own = 0;
         if (lane < kBinsEach)
-            own = (bin_mass(s, i) << 24) | bin_count(s, i);
+            own = (bin_mass(s, i, shift) << 24) | bin_count(s, i);
         u128 x = own;
 #pragma unroll
         for (int o = 1; o < kBinsEach; o <<= 1) {
@@ -810,7 +809,7 @@ __device__ __noinline__ void bin_vectors(const RowSpan<T> row, int stride, Prefi
         const int left = end.index - (row.head + i * E);   // ties up to this one count
 #pragma unroll
         for (int j = 0; j < E; j += 2)
-            bin_pair(s, x[j], x[j + 1], x[j] > least || (x[j] == least && j <= left),
+            bin_pair(s, f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least)), x[j] > least || (x[j] == least && j <= left),
                      x[j + 1] > least || (x[j + 1] == least && j + 1 <= left), b);
     }
 }
@@ -819,155 +818,109 @@ __device__ __noinline__ void bin_vectors(const RowSpan<T> row, int stride, Prefi
 // in [-30, 0] (measured; 1.3e-7 at most), which sums of many would keep.
 constexpr float kExp2Lean = 5.07e-8f;
 
-// The other seven eighths: tokens from `from` up go through the bins, 64 of a
-// warp at a time, and the rest are summed on the way (fp32 weights, the sums
-// compensated).  Returns this thread's sum; `gone` counts the logits of -inf.
+// The same with tokens below `from` summed on the way (fp32 weights, the sums
+// compensated) instead.  Returns this thread's sum; `gone` counts the logits of
+// -inf.
 template <typename T>
 __device__ __noinline__ float tail_vectors(const RowSpan<T> row, float from, const BinScale b, FilterShared& s, int& gone)
 {
     constexpr int E = Elem<T>::E;
-    const int t = threadIdx.x, lane = t & 31;
-    float* queue = s.queue[t >> 5];
-    const uint4* v = row.vec();
     float sum = 0.0f, carry = 0.0f;
-    int waiting = 0, none = 0;
-    const uint64_t ch2 = f2_pack(b.ch, b.ch), cl2 = f2_pack(b.cl, b.cl), unit2 = f2_pack(-b.unit, -b.unit);
-    // stretches 0, 8, 16, ... are the sample; all of a warp's lanes go through every stretch
-    const int stretches = (row.v1 - row.v0 + kFilterThreads - 1) / kFilterThreads;
-    int ahead = 1;
-    auto load = [&]() {
-        const int i = row.v0 + ahead * kFilterThreads + t;
-        ahead += ahead % kGroup == kGroup - 1 ? 2 : 1;
-        return i < row.v1 ? v[i] : make_uint4(0, 0, 0, 0);
-    };
-    uint4 w[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-        w[u] = load();
+    int none = 0;
+    VectorQueue q(row.vec(), row.v0 + (int)threadIdx.x, row.v1, kFilterThreads);
 #pragma unroll 1
-    for (int n = 1; n < stretches; n += n % kGroup == kGroup - 1 ? 2 : 1) {
-        const bool there = row.v0 + n * kFilterThreads + t < row.v1;
+    for (int i = row.v0 + (int)threadIdx.x; i < row.v1; i += kFilterThreads) {
         float x[E];
-        Elem<T>::unpack(w[0], x);
-        w[0] = w[1];
-        w[1] = w[2];
-        w[2] = w[3];
-        w[3] = load();
+        Elem<T>::unpack(q.next(), x);
         uint64_t add = 0;   // (+0, +0)
         float low = x[0];
-        uint32_t in = 0;
 #pragma unroll
         for (int j = 0; j < E; j += 2) {
             const uint64_t L = f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least));
-            float w0, w1;
-            f2_unpack(f2_fma(L, cl2, f2_fma(L, ch2, unit2)), w0, w1);
             const bool in0 = x[j] >= from, in1 = x[j + 1] >= from;
+            float w0, w1;
+            f2_unpack(f2_fma(L, f2_pack(b.cl, b.cl), f2_fma(L, f2_pack(b.ch, b.ch), f2_pack(-b.unit, -b.unit))), w0, w1);
             add = f2_add(add, f2_pack(in0 ? 0.0f : ex2_approx(w0), in1 ? 0.0f : ex2_approx(w1)));
-            in |= (in0 ? 1u << j : 0u) | (in1 ? 2u << j : 0u);
             low = fminf(low, fminf(x[j], x[j + 1]));
+            bin_pair(s, L, in0, in1, b);
         }
-        if (there) {
-            float lo, hi, e;
-            f2_unpack(add, lo, hi);
-            two_sum(sum, lo + hi, sum, e);
-            carry += e;
-            if (low == -INFINITY)
+        float lo, hi, e;
+        f2_unpack(add, lo, hi);
+        two_sum(sum, lo + hi, sum, e);
+        carry += e;
+        if (low == -INFINITY)
 #pragma unroll
-                for (int j = 0; j < E; ++j)
-                    none += x[j] == -INFINITY;
-        } else {
-            in = 0;
-        }
-        // the lanes' tokens one after the other
-        int upto = __popc(in);
-        const int own = upto;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, upto, o);
-            if (lane >= o)
-                upto += y;
-        }
-        int to = waiting + upto - own;
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (in >> j & 1)
-                queue[to++] = x[j];
-        waiting += __shfl_sync(kFull, upto, 31);
-        __syncwarp();
-        if (waiting >= 64) {
-            int done = 0;
-#pragma unroll 1
-            for (; done + 64 <= waiting; done += 64)
-                bin_pair(s, queue[done + lane], queue[done + 32 + lane], true, true, b);
-            const float left0 = queue[done + lane], left1 = queue[min(done + 32 + lane, kQueue - 1)];
-            __syncwarp();
-            queue[lane] = left0;
-            queue[lane + 32] = left1;
-            waiting -= done;
-            __syncwarp();
-        }
+            for (int j = 0; j < E; ++j)
+                none += x[j] == -INFINITY;
     }
-    if (lane < waiting)
-        bin_pair(s, queue[lane], queue[lane + 32], true, lane + 32 < waiting, b);
     gone = none;
     return sum + fmaf(sum, kExp2Lean, carry);
 }
 
-// The -inf among the sample's vectors.
-template <typename T> __device__ __forceinline__ int sample_gone(const RowSpan<T>& row)
+__device__ __forceinline__ void clear_bins(FilterShared& s)
 {
-    constexpr int E = Elem<T>::E;
-    int n = 0;
-#pragma unroll 1
-    for (int i = row.v0 + (int)threadIdx.x; i < row.v1; i += kGroup * kFilterThreads) {
-        float x[E];
-        Elem<T>::unpack(row.vec()[i], x);
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-            n += x[j] == -INFINITY;
-    }
-    return n;
-}
-
-// The sums of a CTA's part of the row.  With `tail` only the tokens around and
-// above where a sample of the row reaches the share `target` go through the
-// bins; the rest are a 64th of the mass at most, if the sample is right.  Returns
-// the last bin that is complete, the mass that is in no bin, and with `tail` how
-// many logits are -inf.
-template <typename T>
-__device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Prefix end, bool tail, float target, const BinScale& b,
-                                         FilterShared& s, u128& rest, int& gone)
-{
-    const int t = threadIdx.x;
-    rest = 0;
-    gone = 0;
     __syncthreads();
-    for (int i = 4 * t; i < kBins; i += 4 * kFilterThreads)
+    for (int i = 4 * threadIdx.x; i < kBins; i += 4 * kFilterThreads)
         *reinterpret_cast<uint4*>(&s.bin.lo[i]) = *reinterpret_cast<uint4*>(&s.bin.hi[i]) = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    const int lone = row.lone();
-    if (lone >= 0)
-        bin_pair(s, lone_x, lone_x, end.has(key_of(lone_x), lone), false, b);
+}
+
+// The sums of a CTA's part of the row.  With `tail` an eighth of it says first
+// where the row's mass reaches the share `target`, about; the bins then cover
+// the tokens around and above that place alone, in as fine steps as they can, and
+// the rest are summed on the way: a 64th of the mass at most, if the eighth was
+// right.  Returns the last bin that is complete, the mass that is in no bin, and
+// with `tail` how many logits are -inf; `b` is the bins' scale.
+template <typename T>
+__device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Prefix end, bool tail, float target, int rank, int C,
+                                         FilterShared& s, BinScale& b, u128& rest, int& gone)
+{
+    const int t = threadIdx.x, lone = row.lone();
+    rest = 0;
+    gone = 0;
+    b = bin_scale(s.scale, kBinShift);
+    clear_bins(s);
     bin_vectors(row, tail ? kGroup * kFilterThreads : kFilterThreads, end, b, s);
-    if (!tail)
-        return kBins - 1;
-    __syncthreads();
-    u128 mass;
-    int count;
-    const BinPart part = scan_bins(s, mass, count);
     int cutoff = kBins - 1;
-    if (count > 0) {   // a quarter of what the sample leaves behind the target, a 64th of the mass at most
-        const u128 quarter = share_of(1.0f - target, mass, false) >> 2, beyond = quarter < mass >> 6 ? quarter : mass >> 6;
-        cutoff = min(kBins - 1, bin_reaching<false>(part, s, mass - beyond).bin + 8);
+    float from = value_of(end.key);
+    if (tail) {
+        __syncthreads();
+        u128 mass;
+        int count;
+        const BinPart part = scan_bins(s, kBinShift, mass, count);
+        if (mass > 0) {   // a quarter of what the sample leaves behind the target, a 64th of the mass at most
+            const u128 quarter = share_of(1.0f - target, mass, false) >> 2, beyond = quarter < mass >> 6 ? quarter : mass >> 6;
+            cutoff = min(kBins - 1, bin_reaching<false>(part, s, kBinShift, mass - beyond).bin + 8);
+        }
+        if (C > 1) {   // the furthest of the CTAs'
+            if (t < C)
+                st_rank(&s.peer_cutoff[rank], t, (uint32_t)cutoff);
+            row_sync(C);
+            for (int c = 0; c < C; ++c)
+                cutoff = max(cutoff, s.peer_cutoff[c]);
+        }
+        const float octaves = (float)(cutoff + 5) * b.step;
+        int shift = kBinShift;
+        while (shift < kBinShiftMost && (octaves + 0.05f) * (float)(2 << shift) <= (float)(kBins - 2))   // (the two units differ by up to 1.5 / 64)
+            ++shift;
+        const float border = fmaxf(from, (b.unit - octaves) / b.ch);
+        b = bin_scale(s.scale, shift);
+        cutoff = cutoff < kBins - 8 ? (cutoff + 1) << (shift - kBinShift) : kBins - 1;
+        from = border;
+        clear_bins(s);
+        float sum = tail_vectors(row, from, b, s, gone);
+        if (lone >= 0 && lone_x < from && lone_x >= b.least)
+            sum += ex2_approx(fmaf(lone_x, b.cl, fmaf(lone_x, b.ch, -b.unit)));
+        gone += lone >= 0 && lone_x == -INFINITY;
+        // units of 2^-62, and the count below them
+        const u128 both = block_sum((u128)__float2ull_rn(sum * 1125899906842624.0f) << 36 | (u128)(uint32_t)gone, s);
+        rest = both >> 24;
+        gone = (int)((uint32_t)both & 0xffffffu);
     }
-    const float from = fmaxf(value_of(end.key), (b.unit - (float)(cutoff + 3) * 0.015625f) / b.ch);
-    int none;
-    const float sum = tail_vectors(row, from, b, s, none);
-    none += sample_gone(row) + (lone >= 0 && lone_x == -INFINITY);
-    // units of 2^-62, and the count below them
-    const u128 both = block_sum((u128)__float2ull_rn(sum * 1125899906842624.0f) << 36 | (u128)(uint32_t)none, s);
-    rest = both >> 24;
-    gone = (int)((uint32_t)both & 0xffffffu);
+    if (lone >= 0) {
+        const float x = fmaxf(lone_x, b.least);
+        bin_pair(s, f2_pack(x, x), end.has(key_of(lone_x), lone) && lone_x >= from, false, b);
+    }
     return cutoff;
 }
 
@@ -980,7 +933,7 @@ __device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Pr
 template <typename T>
 __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to, int also, Prefix end, const BinScale b, int C, FilterShared& s)
 {
-    auto bound = [&](float i) { return (b.unit - (i + 1.0f) * 0.015625f) / b.ch; };   // bin 0's centre is one 64th below `unit`
+    auto bound = [&](float i) { return (b.unit - (i + 1.0f) * b.step) / b.ch; };   // bin 0's centre is a step below `unit`
     const bool last = to == kBins - 1 || also == kBins - 1;
     const float top = bound((float)from - 1.0f), low = bound((float)to + 1.0f), top2 = bound((float)also - 1.0f);
     const float least = last ? -INFINITY : bound((float)max(to, also) + 1.0f);
@@ -999,20 +952,21 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
 {
     const int C = a.C, t = threadIdx.x;
     T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * a.V);
-    const BinScale bs = bin_scale(s.scale);
-    if (t == 0)   // (read behind the barriers of fill_bins)
-        s.scale.top = ((long long)(int)(bs.ref - __float_as_uint(kMagicBin)) + 1) * (1ll << (48 - kBinShift));   // as the bins' masses
     int k = g.k;
     bool tail = k == 0 && g.min_p == 0.0f;
     for (;;) {
         u128 rest;
-        int gone, complete = fill_bins(row, lone_x, end, tail, g.p < 1.0f ? g.p : g.u, bs, s, rest, gone);
+        int gone;
+        BinScale bs;
+        int complete = fill_bins(row, lone_x, end, tail, g.p < 1.0f ? g.p : g.u, rank, C, s, bs, rest, gone);
+        const int shift = bs.shift;
         if (C > 1 && t == 0) {
-            st_rank(&s.peer_cutoff[rank], 0, (uint32_t)complete);
             st_rank(&s.peer_gone[rank], 0, (uint32_t)gone);
             st_rank64(&s.peer_tail[rank], 0, (uint64_t)rest);
             st_rank64(reinterpret_cast<uint64_t*>(&s.peer_tail[rank]) + 1, 0, (uint64_t)(rest >> 64));
         }
+        if (t == 0)   // the list's weights as the bins' masses (read behind the next barriers)
+            s.scale.top = ((long long)(int)(bs.ref - __float_as_uint(bs.magic)) + 1) * (1ll << (48 - shift));
         merge_bins(s, rank, C);
         bool again = false, c_top_k = false;
         int stage = 0;   // rank 0's: what the gathered list is for
@@ -1030,16 +984,15 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                         gone = 0;
                         for (int i = 0; i < C; ++i) {
                             gone += s.peer_gone[i];
-                            complete = min(complete, s.peer_cutoff[i]);
                             rest += s.peer_tail[i];
                         }
                     }
-                    part = scan_bins(s, total, n_all);
+                    part = scan_bins(s, shift, total, n_all);
                     total += rest;
                     if (tail)
                         n_all = a.V - gone;
                     if (k > 0 && k < n_all) {   // top-k first: its last token
-                        const BinAt at = bin_reaching<true>(part, s, (u128)(uint32_t)k);
+                        const BinAt at = bin_reaching<true>(part, s, shift, (u128)(uint32_t)k);
                         stage = 1;
                         kept = k - at.n_before;
                         c.op = kCmdGather;
@@ -1048,7 +1001,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                     } else if (g.p < 1.0f) {
                         stage = 2;
                         const u128 share = share_of(g.p, total, true), goal = share > 1 ? share : 1;
-                        const BinAt end_at = bin_reaching<false>(part, s, goal);
+                        const BinAt end_at = bin_reaching<false>(part, s, shift, goal);
                         last = end_at.bin;
                         above = above_first = end_at.before;
                         kept = end_at.n_before;
@@ -1059,9 +1012,9 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                             n_last = (int)bin_count(s, last);
                             if (DRAW) {
                                 // the draw's point lies between u times the goal and that plus u times a token of the last bin
-                                const BinAt d0 = bin_reaching<false>(part, s, share_of(g.u, goal, false) + 1);
-                                const u128 one = ((u128)s.roots[last & 63] >> (last >> 6)) + (total >> 24);
-                                const BinAt d1 = bin_reaching<false>(part, s, share_of(g.u, goal + one, false) + 1);
+                                const BinAt d0 = bin_reaching<false>(part, s, shift, share_of(g.u, goal, false) + 1);
+                                const u128 one = (u128)exp2_neg((uint64_t)last << (48 - shift), s.roots) + (total >> 24);
+                                const BinAt d1 = bin_reaching<false>(part, s, shift, share_of(g.u, goal + one, false) + 1);
                                 first = min(d0.bin, last);
                                 c.to = min(d1.bin, last);
                                 // bins first .. to and the last one
@@ -1088,7 +1041,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                     } else {
                         kept = n_all;
                         mass = total;
-                        const BinAt at = bin_reaching<false>(part, s, share_of(g.u, total, false) + 1);
+                        const BinAt at = bin_reaching<false>(part, s, shift, share_of(g.u, total, false) + 1);
                         stage = 4;
                         above_first = at.before;
                         if (at.bin > complete) {
@@ -1125,7 +1078,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                             w = from + t < n ? list_weight(s, from + t) : 0;
                             const u128 own = (u128)list_mass(s, from, n, w) << 10;
                             // the goal again, with that bin's mass by its tokens
-                            const u128 goal = share_of(g.p, total - bin_mass(s, last) + own, true);
+                            const u128 goal = share_of(g.p, total - bin_mass(s, last, shift) + own, true);
                             const int end_r = list_reaching(s, from, n, w, after(goal, above), to);
                             mass = above + ((u128)to << 10);
                             kept += end_r - from + 1;
@@ -1143,7 +1096,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                                 hi = from;
                             } else {                                               // in one that is not
                                 draw_now = false;
-                                const BinAt at = bin_reaching<false>(part, s, share_of(g.u, mass, false) + 1);
+                                const BinAt at = bin_reaching<false>(part, s, shift, share_of(g.u, mass, false) + 1);
                                 stage = 4;
                                 above_first = at.before;
                                 c.op = kCmdGather;
