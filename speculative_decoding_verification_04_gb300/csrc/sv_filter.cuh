@@ -41,6 +41,7 @@ constexpr int kBins = 4096;
 constexpr int kBinShift = 6;       // 64 bins an octave of weights or more,
 constexpr int kBinShiftMost = 9;   // up to 512
 constexpr int kBinsEach = kBins / kFilterThreads;
+constexpr int kFewKept = 512;      // kept tokens that are all listed
 constexpr uint32_t kCarryBits = 12;   // of a bin's upper word; its count above (V < 2^20)
 
 // What rank 0 of a row's cluster asks of all its CTAs next.
@@ -62,6 +63,7 @@ struct FilterShared {
     u128 found_mass;
     RowScale scale;
     uint64_t part64[kFilterWarps], found64;
+    uint32_t steps[kBinsEach];   // 2^31 times 2^(-j 2^-shift)
     Command cmd;
     uint32_t warp_top[kFilterWarps], warp_low[kFilterWarps];
     int warp_count[2][kFilterWarps];
@@ -462,8 +464,44 @@ __device__ __noinline__ void append(FilterShared& s, int C, uint32_t key, int in
     }
 }
 
-// f(values, index of the first) for the vectors of the groups that reach `least`:
-// the groups are listed, then read by all threads, a vector each.
+// The marked ones of a vector's values (bit j: x[j]), by all lanes of a warp:
+// one atomic a warp.
+template <int E>
+__device__ __forceinline__ void append_marked(FilterShared& s, int C, uint32_t marks, const float (&x)[E], int index)
+{
+    if (!__any_sync(kFull, marks))
+        return;
+    const int lane = threadIdx.x & 31, n = __popc(marks);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o)
+            upto += y;
+    }
+    int at = 0;
+    if (lane == 31) {
+        if (C == 1)
+            at = atomicAdd(&s.count, upto);
+        else
+            asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(map_to_rank(smem_addr(&s.count), 0)), "r"(upto) : "memory");
+    }
+    at = __shfl_sync(kFull, at, 31) + upto - n;
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (marks >> j & 1) {
+            if (at < kList) {
+                if (C == 1)
+                    s.list[at] = entry_of(key_of(x[j]), index + j);
+                else
+                    st_rank64(&s.list[at], 0, entry_of(key_of(x[j]), index + j));
+            }
+            ++at;
+        }
+}
+
+// f(values, index of the first, whether there) for the vectors of the groups that reach `least`:
+// the groups are listed, then read by all threads, a vector each (f by whole warps).
 template <typename T, typename F>
 __device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, float least, FilterShared& s, F&& f)
 {
@@ -484,7 +522,7 @@ __device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, floa
         return i < row.v1 ? i : -1;
     };
 #pragma unroll 1
-    for (int j = t; j < n; j += 2 * kFilterThreads) {
+    for (int j = t; j - t < n; j += 2 * kFilterThreads) {
         int i[2] = {place(j), place(j + kFilterThreads)};
         uint4 w[2];
 #pragma unroll
@@ -494,8 +532,7 @@ __device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, floa
         for (int u = 0; u < 2; ++u) {
             float x[E];
             Elem<T>::unpack(w[0], x);
-            if (i[0] >= 0)
-                f(x, row.head + i[0] * E);
+            f(x, row.head + i[0] * E, i[0] >= 0);
             w[0] = w[1];
             i[0] = i[1];
         }
@@ -676,17 +713,25 @@ __device__ __forceinline__ void bin_pair(FilterShared& s, uint64_t L, bool in0, 
 
 __device__ __forceinline__ uint32_t bin_count(const FilterShared& s, int i) { return s.bin.hi[i] >> kCarryBits; }
 
-// The mass of bin i in units of 2^-62.
-__device__ __forceinline__ u128 bin_mass(const FilterShared& s, int i, int shift)
+// Bin i's share of its thread's bins: the sum of its weights over the weight of
+// the thread's first bin's centre, in units of 2^-(23 + shift).
+__device__ __forceinline__ uint64_t bin_part(const FilterShared& s, int i, int shift)
 {
     const uint32_t hi = s.bin.hi[i], n = hi >> kCarryBits;
-    if (n == 0 || i == kBins - 1)
-        return 0;
     const uint64_t sum = (((uint64_t)(hi & ((1u << kCarryBits) - 1)) << 32) | s.bin.lo[i]) + ((uint64_t)n << (23 + shift)) - ((uint64_t)n << 22);
-    return ((u128)sum * exp2_neg((uint64_t)(i + 1) << (48 - shift), s.roots)) >> (23 + shift);
+    const uint64_t f = i == kBins - 1 ? 0 : s.steps[i % kBinsEach];
+    return ((sum & 0xffffffffu) * f >> 31) + ((sum >> 32) * f << 1);
 }
 
-// A thread's bins (kBinsEach of them), and what is before them.
+// The weight that multiplies the parts of thread t's bins.
+__device__ __forceinline__ uint64_t part_weight(const FilterShared& s, int t, int shift)
+{
+    return exp2_neg((uint64_t)(t * kBinsEach + 1) << (48 - shift), s.roots);
+}
+
+__device__ __forceinline__ u128 part_mass(uint64_t part, uint64_t weight, int shift) { return ((u128)part * weight) >> (23 + shift); }
+
+// A thread's bins (kBinsEach of them), and what is before them; masses in units of 2^-62.
 struct BinPart {
     u128 before, own;
     int n_before, n_own;
@@ -695,23 +740,32 @@ struct BinPart {
 __device__ __noinline__ BinPart scan_bins(FilterShared& s, int shift, u128& mass, int& count)
 {
     BinPart q;
-    q.own = 0;
+    const int t = threadIdx.x;
+    if (t < kBinsEach)
+        s.steps[t] = (uint32_t)(exp2_neg((uint64_t)t << (48 - shift), s.roots) >> 31);
+    __syncthreads();
+    uint64_t part = 0;
     q.n_own = 0;
-    const int i0 = threadIdx.x * kBinsEach;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < kBinsEach; ++i) {
-        const int j = i0 + ((i + threadIdx.x) & (kBinsEach - 1));   // (lanes on different banks)
-        q.own += bin_mass(s, j, shift);
+        const int j = t * kBinsEach + ((i + t) & (kBinsEach - 1));   // (lanes on different banks)
+        part += bin_part(s, j, shift);
         q.n_own += (int)bin_count(s, j);
     }
-    u128 total;
+    q.own = part ? part_mass(part, part_weight(s, t, shift), shift) : 0;
     // the count in the low bits of one sum with the mass: masses are below 2^83
+    u128 total;
     const u128 both = block_scan((q.own << 24) | (u128)(uint32_t)q.n_own, s, total);
     q.before = both >> 24;
     q.n_before = (int)((uint32_t)both & 0xffffffu);
     mass = total >> 24;
     count = (int)((uint32_t)total & 0xffffffu);
     return q;
+}
+
+__device__ __forceinline__ u128 bin_mass(const FilterShared& s, int i, int shift)
+{
+    return part_mass(bin_part(s, i, shift), part_weight(s, i / kBinsEach, shift), shift);
 }
 
 // The bin where the running sum over all bins, of counts or of masses, reaches
@@ -736,25 +790,26 @@ template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart&
     __syncthreads();
     BinAt r{kBins, 0, 0};
     if (s.found >= 0) {   // every warp goes through that thread's bins, one a lane
-        const int lane = threadIdx.x & 31, i = s.found * kBinsEach + lane;
-        u128 own = 0;
-        if (lane < kBinsEach)
-            own = (bin_mass(s, i, shift) << 24) | bin_count(s, i);
-        u128 x = own;
+        const int lane = threadIdx.x & 31, i = s.found * kBinsEach + (lane & (kBinsEach - 1));
+        const uint64_t weight = part_weight(s, s.found, shift), own = lane < kBinsEach ? bin_part(s, i, shift) : 0;
+        const int n_own = lane < kBinsEach ? (int)bin_count(s, i) : 0;
+        uint64_t x = own;
+        int n = n_own;
 #pragma unroll
         for (int o = 1; o < kBinsEach; o <<= 1) {
-            const u128 y = shfl_up128(x, o);
-            if (lane >= o)
+            const uint64_t y = __shfl_up_sync(kFull, (unsigned long long)x, o);
+            const int z = __shfl_up_sync(kFull, n, o);
+            if (lane >= o) {
                 x += y;
+                n += z;
+            }
         }
-        const u128 base = (s.found_mass << 24) | (u128)(uint32_t)s.found_count;
-        const u128 to = base + x, from = to - own;
-        const bool here = lane < kBinsEach && (kCount ? (u128)((uint32_t)to & 0xffffffu) : to >> 24) >= goal;
+        const u128 base = s.found_mass, from = base + part_mass(x - own, weight, shift);
+        const bool here = lane < kBinsEach && (kCount ? (u128)(uint32_t)(s.found_count + n) : base + part_mass(x, weight, shift)) >= goal;
         const int l = __ffs(__ballot_sync(kFull, here)) - 1;
         r.bin = s.found * kBinsEach + l;
         r.before = ((u128)__shfl_sync(kFull, (unsigned long long)(from >> 64), l) << 64) | __shfl_sync(kFull, (unsigned long long)from, l);
-        r.n_before = (int)((uint32_t)r.before & 0xffffffu);
-        r.before >>= 24;
+        r.n_before = s.found_count + __shfl_sync(kFull, n - n_own, l);
     }
     return r;
 }
@@ -937,13 +992,30 @@ __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to,
     const bool last = to == kBins - 1 || also == kBins - 1;
     const float top = bound((float)from - 1.0f), low = bound((float)to + 1.0f), top2 = bound((float)also - 1.0f);
     const float least = last ? -INFINITY : bound((float)max(to, also) + 1.0f);
-    row.each([&](float x, int i) {
-        if (x >= least && (x <= top2 || x >= low) && x <= fmaxf(top, top2)) {
-            const int n = bin_of(x, b);
-            if (((n >= from && n <= to) || n == also) && end.has(key_of(x), i))
-                append(s, C, key_of(x), i);
-        }
-    });
+    auto in = [&](float x, int i) {
+        if (!(x >= least && (x <= top2 || x >= low) && x <= fmaxf(top, top2)))
+            return false;
+        const int n = bin_of(x, b);
+        return ((n >= from && n <= to) || n == also) && end.has(key_of(x), i);
+    };
+    constexpr int E = Elem<T>::E;
+    const int t = threadIdx.x;
+    VectorQueue q(row.vec(), row.v0 + t, row.v1, kFilterThreads);
+#pragma unroll 1
+    for (int i = row.v0 + t; i - t < row.v1; i += kFilterThreads) {
+        float x[E];
+        Elem<T>::unpack(q.next(), x);
+        uint32_t marks = 0;
+        if (i < row.v1)
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                marks |= in(x[j], row.head + i * E + j) ? 1u << j : 0u;
+        __syncwarp();
+        append_marked(s, C, marks, x, row.head + i * E);
+    }
+    const int lone = row.lone();
+    if (lone >= 0 && in((float)row.p[lone], lone))
+        append(s, C, key_of((float)row.p[lone]), lone);
 }
 
 template <typename T, bool DRAW>
@@ -1005,32 +1077,26 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                         last = end_at.bin;
                         above = above_first = end_at.before;
                         kept = end_at.n_before;
-                        int first = last, n_first = end_at.n_before;
                         if (last > complete) {
                             c.op = kCmdRecount;   // the sample misled: all of it through the bins
                         } else {
                             n_last = (int)bin_count(s, last);
-                            if (DRAW) {
-                                // the draw's point lies between u times the goal and that plus u times a token of the last bin
-                                const BinAt d0 = bin_reaching<false>(part, s, shift, share_of(g.u, goal, false) + 1);
-                                const u128 one = (u128)exp2_neg((uint64_t)last << (48 - shift), s.roots) + (total >> 24);
-                                const BinAt d1 = bin_reaching<false>(part, s, shift, share_of(g.u, goal + one, false) + 1);
-                                first = min(d0.bin, last);
-                                c.to = min(d1.bin, last);
-                                // bins first .. to and the last one
-                                n_first = (c.to < last ? d1.n_before + (int)bin_count(s, c.to) : kept) - d0.n_before;
-                                above_first = d0.before;
-                                if (d0.bin >= last || n_first + n_last > kList) {   // not both at once: the last bin first
-                                    first = last;
-                                    above_first = above;
+                            give_up = n_last > kList;
+                            c.op = kCmdGather;
+                            c.from = c.to = c.also = last;
+                            if (DRAW && kept + n_last <= kFewKept) {   // all of them
+                                c.from = 0;
+                                above_first = 0;
+                            } else if (DRAW) {   // and the bins the draw is in, if the kept mass is the goal or little more
+                                const BinAt at = bin_reaching<false>(part, s, shift, share_of(g.u, goal, false) + 1);
+                                const int to = min(at.bin + 1, last);
+                                if (at.bin < last && (int)bin_count(s, at.bin) + (int)bin_count(s, to) + n_last <= kList) {
+                                    c.from = at.bin;
+                                    c.to = to;
+                                    above_first = at.before;
                                 }
                             }
-                            c.op = kCmdGather;
-                            c.from = first;
-                            c.to = first == last ? last : c.to;
-                            c.also = last;
-                            lo_first = first;
-                            give_up = n_last > kList;
+                            lo_first = c.from;
                         }
                     } else if (!DRAW) {   // top-k reaches past the last token
                         if (t == 0)
@@ -1072,7 +1138,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                             const u128 d = goal > base ? goal - base : 1;
                             return (uint64_t)((d + 1023) >> 10);
                         };
-                        bool draw_now = DRAW;
+                        bool draw_now = DRAW, sure = stage == 4;
                         if (stage == 2) {
                             const int from = n - n_last;   // the last bin's tokens
                             w = from + t < n ? list_weight(s, from + t) : 0;
@@ -1091,24 +1157,30 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                             } else if (share_of(g.u, mass, false) + 1 > above) {   // the draw is in the last bin
                                 lo = from;
                                 hi = end_r + 1;
+                                sure = true;
                                 above_first = above;
-                            } else if (lo_first < last) {                          // in the bins before it that are here
+                            } else {                                               // in a bin before it
                                 hi = from;
-                            } else {                                               // in one that is not
-                                draw_now = false;
-                                const BinAt at = bin_reaching<false>(part, s, shift, share_of(g.u, mass, false) + 1);
-                                stage = 4;
-                                above_first = at.before;
-                                c.op = kCmdGather;
-                                c.from = c.to = c.also = at.bin;
-                                give_up = bin_count(s, at.bin) > kList;
+                                draw_now = lo_first < last;
                             }
                         }
+                        int at = 0;
                         if (draw_now) {
+                            const uint64_t want = after(share_of(g.u, mass, false) + 1, above_first);
                             w = lo + t < hi ? list_weight(s, lo + t) : 0;
-                            const int at = list_reaching(s, lo, hi, w, after(share_of(g.u, mass, false) + 1, above_first), to);
+                            at = list_reaching(s, lo, hi, w, want, to);
+                            draw_now = to >= want || sure;
+                        }
+                        if (draw_now) {
                             if (t == 0)
                                 put_row<DRAW>(a, r, kept, entry_index(s.list[at]), entry_weight(s, at), mass);
+                        } else if (DRAW) {   // not in the bins that are here
+                            const BinAt b = bin_reaching<false>(part, s, shift, share_of(g.u, mass, false) + 1);
+                            stage = 4;
+                            above_first = b.before;
+                            c.op = kCmdGather;
+                            c.from = c.to = c.also = b.bin;
+                            give_up = bin_count(s, b.bin) > kList;
                         }
                     }
                 }
@@ -1311,10 +1383,10 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
     }
     const float m = value_of(top_key);
     if (greedy) {
-        each_hit(row, groups, m, s, [&](const float (&x)[E], int i) {
+        each_hit(row, groups, m, s, [&](const float (&x)[E], int i, bool there) {
 #pragma unroll
             for (int k = E - 1; k >= 0; --k)
-                if (x[k] == m)
+                if (there && x[k] == m)
                     atomicMin(&s.first, i + k);
         });
         // (more hits than the list of them holds: by all threads' groups)
@@ -1352,11 +1424,12 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
     if (bounded || g.min_p > 0.0f || V <= kList) {
         const uint32_t cut = max(end.key, bound);
         const float cv = value_of(cut);
-        each_hit(row, groups, cv, s, [&](const float (&x)[E], int i) {
+        each_hit(row, groups, cv, s, [&](const float (&x)[E], int i, bool there) {
+            uint32_t marks = 0;
 #pragma unroll
             for (int k = 0; k < E; ++k)
-                if (x[k] >= cv)
-                    append(s, C, key_of(x[k]), i + k);
+                marks |= there && x[k] >= cv ? 1u << k : 0u;
+            append_marked(s, C, marks, x, i);
         });
         if (lone >= 0 && lone_x >= cv)
             append(s, C, key_of(lone_x), lone);
