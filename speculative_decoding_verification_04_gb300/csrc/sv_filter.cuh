@@ -41,6 +41,9 @@ constexpr int kBins = 4096;
 constexpr int kBinShift = 6;       // 64 bins an octave of weights or more,
 constexpr int kBinShiftMost = 9;   // up to 512
 constexpr int kBinsEach = kBins / kFilterThreads;
+constexpr int kLevelsSide = 4098;   // bf16 magnitudes: below 2^-24, 2^-24 to 2^8 one by one, from 2^8
+constexpr int kLevels = 2 * kLevelsSide;
+constexpr int kLevelsEach = 4096 * 2 / kFilterThreads;
 constexpr int kFewKept = 512;      // kept tokens that are all listed
 constexpr uint32_t kCarryBits = 12;   // of a bin's upper word; its count above (V < 2^20)
 
@@ -53,7 +56,7 @@ struct alignas(16) Command {
     uint32_t key;          // kCmdWrite, kCmdRecount: the kept prefix's last token
     int index;
     int top_k;             // kCmdRecount: the prefix is top-k's
-    int pad;
+    float value;           // kCmdGather of bf16 levels: the logit
 };
 
 struct FilterShared {
@@ -82,6 +85,7 @@ struct FilterShared {
         struct {
             uint32_t lo[kBins], hi[kBins];
         } bin;
+        uint32_t level[kLevels];
         float group[kGroupsMost][kFilterThreads];
     };
 };
@@ -89,7 +93,7 @@ struct FilterShared {
 // Shared memory for rows of `groups` groups a CTA.
 constexpr size_t filter_smem_bytes(int groups)
 {
-    const size_t g = (size_t)groups * kFilterThreads * 4, b = (size_t)kBins * 8;
+    const size_t g = (size_t)groups * kFilterThreads * 4, b = ((size_t)kLevels * 4 + 15) / 16 * 16;   // (more than the bins)
     return sizeof(FilterShared) - sizeof(float) * kGroupsMost * kFilterThreads + (g > b ? g : b);
 }
 
@@ -302,6 +306,22 @@ __device__ Prefix prefix_reaching(const RowSpan<T>& row, u128 goal, Prefix most,
             a = mid + 1;
     }
     return Prefix{lo, a};
+}
+
+// The index of the n-th logit (from 1) that equals x.
+template <typename T> __device__ __noinline__ int index_of_nth(const RowSpan<T>& row, float x, int n, FilterShared& s)
+{
+    int a = 0, b = row.V - 1;
+    while (a < b) {
+        const int mid = a + (b - a) / 2;
+        int here = 0;
+        row.each([&](float y, int i) { here += y == x && i <= mid; });
+        if (block_sum((u128)(uint32_t)here, s) >= (u128)(uint32_t)n)
+            b = mid;
+        else
+            a = mid + 1;
+    }
+    return a;
 }
 
 // ---------------------------------------------------------------------------
@@ -814,6 +834,15 @@ template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart&
     return r;
 }
 
+// What rank 0 asks for, behind a row_sync.
+__device__ __forceinline__ Command command_of(const FilterShared& s, int C)
+{
+    if (C == 1)
+        return s.cmd;
+    const uint4 x = ld_rank128(&s.cmd, 0), y = ld_rank128(reinterpret_cast<const char*>(&s.cmd) + 16, 0);
+    return Command{(int)x.x, (int)x.y, (int)x.z, (int)x.w, y.x, (int)y.y, (int)y.z, __uint_as_float(y.w)};
+}
+
 // All of the cluster's bins in rank 0's.
 __device__ __noinline__ void merge_bins(FilterShared& s, int rank, int C)
 {
@@ -1047,7 +1076,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
         BinPart part{};
         for (;;) {
             if (rank == 0) {
-                Command c{kCmdEnd, 0, 0, -1, 0, 0, 0, 0};
+                Command c{kCmdEnd, 0, 0, -1, 0, 0, 0, 0.0f};
                 bool give_up = false;
                 if (stage == 0) {
                     int n_all;
@@ -1187,7 +1216,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                 if (give_up) {
                     Settings left = g;
                     left.k = k;
-                    c = Command{kCmdEnd, 0, 0, -1, 0, 0, 0, 0};
+                    c = Command{kCmdEnd, 0, 0, -1, 0, 0, 0, 0.0f};
                     whole_row<T, DRAW>(a, r, left, s.scale.m, end, s);
                 }
                 __syncthreads();
@@ -1197,13 +1226,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                 }
             }
             row_sync(C);
-            Command c;
-            if (C > 1) {
-                const uint4 x = ld_rank128(&s.cmd, 0), y = ld_rank128(reinterpret_cast<const char*>(&s.cmd) + 16, 0);
-                c = Command{(int)x.x, (int)x.y, (int)x.z, (int)x.w, y.x, (int)y.y, (int)y.z, 0};
-            } else {
-                c = s.cmd;
-            }
+            const Command c = command_of(s, C);
             if (c.op == kCmdEnd)
                 break;
             if (c.op == kCmdGather) {
@@ -1236,6 +1259,346 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
     }
 }
 
+// ---------------------------------------------------------------------------
+// bf16 rows where every token counts: how often each value occurs
+// ---------------------------------------------------------------------------
+// 8192 values (both signs, 32 octaves of 128) are counted one by one, in the one
+// pass over the row; their weights times their counts are the exact sums, and a
+// border lies inside one value's tokens.  An atomic a token, where bins of fp32
+// logits take two and the arithmetic of the remainders.
+struct LevelScale {
+    uint64_t first, ratio;   // the weight of the thread's first value, and from one value to the next
+    float value, step;
+};
+
+// Thread t's values: kLevelsEach of them in descending order, all of one octave.
+__device__ __forceinline__ float level_value(int t, int j)
+{
+    const int o = t * kLevelsEach + j;
+    return o < 4096 ? __uint_as_float((uint32_t)(13183 + 4096 - o) << 16) : __uint_as_float(((uint32_t)(13184 + o - 4096) << 16) | 0x80000000u);
+}
+
+__device__ __forceinline__ uint32_t level_count(const FilterShared& s, int t, int j)
+{
+    const int o = t * kLevelsEach + j;
+    return s.level[o < 4096 ? 4096 - o : kLevelsSide + 1 + o - 4096];
+}
+
+__device__ __forceinline__ LevelScale level_scale(const FilterShared& s, int t)
+{
+    LevelScale l;
+    l.value = level_value(t, 0);
+    l.step = l.value - level_value(t, 1);
+    l.first = l.value > s.scale.m ? 0 : weight62(l.value, s.scale, s.roots);   // (above the row's first value's: none there)
+    l.ratio = l.step * s.scale.ch > 63.0f ? 0 : exp2_neg((uint64_t)scaled48(l.step, s.scale.ch, s.scale.cl), s.roots);
+    return l;
+}
+
+// From one value's weight over the thread's first to the next one's; in units of 2^-62.
+__device__ __forceinline__ uint64_t next_level(uint64_t f, uint64_t ratio) { return __umul64hi(f, ratio) << 2; }
+
+__device__ __forceinline__ u128 level_mass(uint64_t part, uint64_t first) { return ((u128)part * first) >> 38; }
+
+__device__ __noinline__ BinPart scan_levels(FilterShared& s, u128& mass, int& count)
+{
+    BinPart q;
+    const int t = threadIdx.x;
+    int some = 0;
+#pragma unroll 4
+    for (int j = 0; j < kLevelsEach; ++j)
+        some += (int)level_count(s, t, (j + t) & (kLevelsEach - 1));
+    q.n_own = some;
+    q.own = 0;
+    if (some) {
+        const LevelScale l = level_scale(s, t);
+        uint64_t part = 0, f = kOne62;
+#pragma unroll 4
+        for (int j = 0; j < kLevelsEach; ++j) {
+            part += level_count(s, t, j) * (f >> 24);
+            f = next_level(f, l.ratio);
+        }
+        q.own = level_mass(part, l.first);
+    }
+    u128 total;
+    const u128 both = block_scan((q.own << 24) | (u128)(uint32_t)q.n_own, s, total);
+    q.before = both >> 24;
+    q.n_before = (int)((uint32_t)both & 0xffffffu);
+    mass = total >> 24;
+    count = (int)((uint32_t)total & 0xffffffu);
+    return q;
+}
+
+struct LevelAt {
+    float value;
+    uint64_t weight;        // of one of its tokens, in units of 2^-62
+    int n, n_before;        // its tokens, and those before them
+    u128 before, mass;      // the mass before them, and theirs in the sums
+};
+
+// The value among whose tokens the running count, or mass, reaches goal (which
+// the row does).
+template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const BinPart& q, FilterShared& s, u128 goal)
+{
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s.found = 0;
+    __syncthreads();
+    const u128 c = kCount ? (u128)(uint32_t)q.n_before : q.before, v = kCount ? (u128)(uint32_t)q.n_own : q.own;
+    if (c < goal && goal <= c + v) {
+        s.found = threadIdx.x;
+        s.found_count = q.n_before;
+        s.found_mass = q.before;
+    }
+    __syncthreads();
+    // every warp goes through that thread's values, one a lane
+    const int lane = threadIdx.x & 31;
+    const LevelScale l = level_scale(s, s.found);
+    uint64_t f = kOne62;
+    for (int j = 0; j < lane; ++j)
+        f = next_level(f, l.ratio);
+    const int n_own = (int)level_count(s, s.found, lane);
+    uint64_t x = n_own * (f >> 24);
+    const uint64_t own = x;
+    int n = n_own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(kFull, (unsigned long long)x, o);
+        const int z = __shfl_up_sync(kFull, n, o);
+        if (lane >= o) {
+            x += y;
+            n += z;
+        }
+    }
+    const u128 from = s.found_mass + level_mass(x - own, l.first);
+    const bool here = (kCount ? (u128)(uint32_t)(s.found_count + n) : s.found_mass + level_mass(x, l.first)) >= goal;
+    const int i = __ffs(__ballot_sync(kFull, here)) - 1;
+    LevelAt r;
+    r.value = level_value(s.found, i);
+    r.weight = __shfl_sync(kFull, (unsigned long long)level_mass(f >> 24, l.first), i);
+    r.n = __shfl_sync(kFull, n_own, i);
+    r.n_before = s.found_count + __shfl_sync(kFull, n - n_own, i);
+    r.before = ((u128)__shfl_sync(kFull, (unsigned long long)(from >> 64), i) << 64) | __shfl_sync(kFull, (unsigned long long)from, i);
+    const u128 to = s.found_mass + level_mass(x, l.first) - from;
+    r.mass = ((u128)__shfl_sync(kFull, (unsigned long long)(to >> 64), i) << 64) | __shfl_sync(kFull, (unsigned long long)to, i);
+    return r;
+}
+
+// How many tokens of weight w (at least one, at most n) reach a mass.
+__device__ __forceinline__ int tokens_for(u128 mass, uint64_t w, int n)
+{
+    if (w == 0 || mass >= (u128)w * (uint32_t)n)
+        return n;
+    int j = max(1, (int)((float)mass / (float)w));   // within 2^-22 of itself
+    j = min(j, n);
+    while ((u128)w * (uint32_t)j < mass)
+        ++j;
+    while (j > 1 && (u128)w * (uint32_t)(j - 1) >= mass)
+        --j;
+    return j;
+}
+
+// Counts this CTA's part; returns the largest logit (NaN if there is one).
+__device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, FilterShared& s)
+{
+    uint32_t top = 0xff80ff80u;
+    auto one = [&](uint32_t w, bool both) {
+        uint32_t m = w & 0x7fff7fffu;
+        asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(0x337f337fu));
+        asm("min.u16x2 %0, %0, %1;" : "+r"(m) : "r"(0x43804380u));
+        const uint32_t i = m - 0x337f337fu + ((w >> 15) & 0x00010001u) * (uint32_t)kLevelsSide;
+        atomicAdd(&s.level[i & 0xffffu], 1u);
+        if (both)
+            atomicAdd(&s.level[i >> 16], 1u);
+        top = bmax2_nan(top, both ? w : w | 0xff800000u);
+    };
+    VectorQueue q(row.vec(), row.v0 + (int)threadIdx.x, row.v1, kFilterThreads);
+#pragma unroll 1
+    for (int i = row.v0 + (int)threadIdx.x; i < row.v1; i += kFilterThreads) {
+        const uint4 w = q.next();
+        one(w.x, true);
+        one(w.y, true);
+        one(w.z, true);
+        one(w.w, true);
+    }
+    const int lone = row.lone();
+    if (lone >= 0)
+        one(reinterpret_cast<const unsigned short*>(row.p)[lone], false);
+    return max_nan(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
+}
+
+// The tokens of one value into rank 0's list.
+__device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, float value, int C, FilterShared& s)
+{
+    const int t = threadIdx.x;
+    VectorQueue q(row.vec(), row.v0 + t, row.v1, kFilterThreads);
+#pragma unroll 1
+    for (int i = row.v0 + t; i - t < row.v1; i += kFilterThreads) {
+        float x[8];
+        Elem<__nv_bfloat16>::unpack(q.next(), x);
+        uint32_t marks = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            marks |= x[j] == value ? 1u << j : 0u;
+        append_marked(s, C, i < row.v1 ? marks : 0u, x, row.head + i * 8);
+    }
+    const int lone = row.lone();
+    if (lone >= 0 && (float)row.p[lone] == value)
+        append(s, C, key_of(value), lone);
+}
+
+// False: some logits are not among the values (or not finite): to be done
+// another way.
+template <bool DRAW>
+__device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const Settings& g, const RowSpan<__nv_bfloat16>& row, int rank, FilterShared& s)
+{
+    typedef __nv_bfloat16 T;
+    const int C = a.C, t = threadIdx.x;
+    __syncthreads();
+    for (int i = t; i < kLevels; i += kFilterThreads)
+        s.level[i] = 0;
+    __syncthreads();
+    const uint32_t key = __reduce_max_sync(kFull, key_of(count_levels(row, s)));
+    if ((t & 31) == 0)
+        s.warp_top[t >> 5] = key;
+    __syncthreads();
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kFilterWarps; ++i)
+        top = max(top, s.warp_top[i]);
+    if (C > 1) {
+        if (t < C)
+            st_rank(&s.peer_top[rank], t, top);
+        row_sync(C);
+        for (int c = 0; c < C; ++c)
+            top = max(top, s.peer_top[c]);
+        const int per = (kLevels + C - 1) / C, i0 = rank * per, i1 = min(kLevels, i0 + per);
+        for (int i = i0 + t; i < i1; i += kFilterThreads) {
+            uint32_t n = 0;
+#pragma unroll 4
+            for (int c = 0; c < C; ++c)
+                n += ld_rank(&s.level[i], c);
+            s.level[i] = n;
+        }
+        row_sync(C);
+        if (rank == 0) {
+#pragma unroll 4
+            for (int i = per + t; i < kLevels; i += kFilterThreads)
+                s.level[i] = ld_rank(&s.level[i], i / per);
+            __syncthreads();
+        }
+    }
+    // rank 0's: `stage` says what its list is for
+    int stage = 0, kept = 0, nth = 0;
+    LevelAt at{};
+    u128 mass = 0;
+    for (;;) {
+        if (rank == 0) {
+            Command c{kCmdEnd, 0, 0, -1, 0, 0, 0, 0.0f};
+            int index = -1;   // of the nth token of at.value, where it is known
+            if (stage == 0) {
+                const float m = value_of(top);
+                const uint32_t low = s.level[2 * kLevelsSide - 1];
+                const bool fit = top > kKeyNegInf && top < kKeyPosInf && m < 256.0f && m > -256.0f && s.level[0] == 0 && s.level[kLevelsSide] == 0;
+                if (t == 0 && fit) {   // weights relative to the first of the values around the maximum: none is above one
+                    const uint32_t bits = __float_as_uint(m) >> 16, mag = (bits & 0x7fffu) - 13184;
+                    const float from = bits >> 15 ? __uint_as_float(((13184 + mag / kLevelsEach * kLevelsEach) << 16) | 0x80000000u)
+                                                  : __uint_as_float((13184 + mag / kLevelsEach * kLevelsEach + kLevelsEach - 1) << 16);
+                    s.scale = row_scale(from, g.T);
+                }
+                __syncthreads();
+                // logits below -256 have to weigh nothing, and their number is not known
+                const bool able = fit && !s.scale.cold && (low == 0 || ((m + 256.0f) * s.scale.ch > 64.0f && g.k == 0 && g.p < 1.0f));
+                if (!able) {
+                    c.op = kCmdRecount;
+                } else {
+                    int n_all;
+                    u128 total;
+                    const BinPart part = scan_levels(s, total, n_all);
+                    bool cut = false;   // whether the prefix ends inside the row
+                    kept = n_all;
+                    mass = total;
+                    if (g.k > 0 && g.k < n_all) {
+                        at = level_reaching<true>(part, s, (u128)(uint32_t)g.k);
+                        kept = g.k;
+                        nth = g.k - at.n_before;
+                        mass = at.before + (u128)at.weight * (uint32_t)nth;
+                        cut = true;
+                    }
+                    if (g.p < 1.0f) {
+                        u128 goal = share_of(g.p, mass, true);
+                        goal = goal > 1 ? goal : 1;
+                        const bool in_last = cut && goal > at.before;   // among the tokens that top-k cut
+                        int most = nth;
+                        if (!in_last) {
+                            const u128 all = mass;
+                            at = level_reaching<false>(part, s, goal);
+                            most = at.n;
+                            // the goal again, that value's mass by its tokens
+                            const u128 own = (u128)at.weight * (uint32_t)at.n;
+                            goal = share_of(g.p, all - at.mass + own, true);
+                            goal = goal > 1 ? goal : 1;
+                        }
+                        nth = tokens_for(goal > at.before ? goal - at.before : 1, at.weight, most);
+                        kept = at.n_before + nth;
+                        mass = at.before + (u128)at.weight * (uint32_t)nth;
+                        cut = true;
+                    }
+                    if (DRAW) {
+                        const u128 point = share_of(g.u, mass, false) + 1;
+                        if (!cut || point <= at.before) {
+                            at = level_reaching<false>(part, s, point);
+                            nth = at.n;
+                        }
+                        nth = tokens_for(point > at.before ? point - at.before : 1, at.weight, nth);
+                    }
+                    if (!DRAW && (!cut || nth == at.n)) {   // whole values
+                        stage = 2;
+                        index = INT_MAX;
+                        if (!cut)
+                            at.value = -3.4028234663852886e38f;
+                    } else if (at.n <= kList) {
+                        stage = 1;
+                        c.op = kCmdGather;
+                        c.value = at.value;
+                    } else {
+                        stage = 2;
+                        index = index_of_nth(RowSpan<T>(row.p, row.V, 0, 1), at.value, nth, s);
+                    }
+                }
+            } else {
+                sort_list(s, s.count);
+                index = entry_index(s.list[nth - 1]);
+                stage = 2;
+            }
+            if (stage == 2) {
+                if (t == 0)
+                    put_row<DRAW>(a, r, kept, index, at.weight, mass);
+                if (!DRAW) {
+                    c.op = kCmdWrite;
+                    c.key = key_of(at.value);
+                    c.index = index;
+                }
+            }
+            __syncthreads();
+            if (t == 0) {
+                s.cmd = c;
+                s.count = 0;
+            }
+        }
+        row_sync(C);
+        const Command c = command_of(s, C);
+        if (c.op == kCmdGather) {
+            gather_level(row, c.value, C, s);
+            row_sync(C);
+            continue;
+        }
+        if (c.op == kCmdWrite)
+            write_row(row, static_cast<T*>(a.out) + r * a.V, a.same_phase, Prefix{c.key, c.index});
+        row_sync(C);   // the command has been read
+        return c.op != kCmdRecount;
+    }
+}
+
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs a)
 {
@@ -1263,6 +1626,18 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
     const T* logits = static_cast<const T*>(a.logits) + r * V;
     T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * V);
     const RowSpan<T> row(logits, V, rank, C);
+
+    if (t < 64)
+        s.roots[t] = root_power(t);
+    if (t == 0) {
+        s.count = 0;
+        s.hits = 0;
+        s.first = INT_MAX;
+    }
+    if constexpr (sizeof(T) == 2)
+        if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : g.k > C * (kFilterThreads / 2)))
+            if (levels_row<DRAW>(a, r, g, row, rank, s))
+                return;
 
     double t_log = 0.0;   // one thread's: 64-bit floating point runs at a hundredth of the fp32 rate
     if (t == kFilterThreads - 32 && good && !greedy && g.min_p > 0.0f)
@@ -1303,13 +1678,6 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
     const int lone = row.lone();
     const float lone_x = lone >= 0 ? (float)logits[lone] : -INFINITY;
     mine = max_nan(mine, lone_x);
-    if (t < 64)
-        s.roots[t] = root_power(t);
-    if (t == 0) {
-        s.count = 0;
-        s.hits = 0;
-        s.first = INT_MAX;
-    }
     const uint32_t own_key = key_of(mine);
     {
         const uint32_t top = __reduce_max_sync(kFull, own_key), low = __reduce_min_sync(kFull, own_key);
