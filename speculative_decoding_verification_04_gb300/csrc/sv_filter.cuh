@@ -101,35 +101,35 @@ constexpr size_t filter_smem_bytes(int groups)
 // the row, the block and the cluster
 // ---------------------------------------------------------------------------
 
-// A thread's vectors at i, i + stride, ...: four on their way while one is
-// worked on.  The loops over them stay rolled: code that runs a few times a row
-// comes from L2, and costs more than it does.
-struct VectorQueue {
-    const uint4* v;
-    int at, end, stride;
-    uint4 w[4];
-    __device__ __forceinline__ VectorQueue(const uint4* v_, int i, int end_, int stride_) : v(v_), at(i), end(end_), stride(stride_)
-    {
+// f(vector, its place, whether there) for the vectors at first + threadIdx.x,
+// + stride, ... below `end`, by whole warps; four are fetched at a time.  kRolled:
+// f is in the code once, for longer ones: code that runs a few times a row comes
+// from L2, and costs more than the moves do.
+template <bool kRolled, typename F>
+__device__ __forceinline__ void each_vector(const uint4* v, int first, int end, int stride, F&& f)
+{
+    const int t = threadIdx.x;
+#pragma unroll 1
+    for (int i = first + t; i - t < end; i += 4 * stride) {
+        uint4 w[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            w[u] = load();
+            w[u] = i + u * stride < end ? v[i + u * stride] : make_uint4(0, 0, 0, 0);
+        if (kRolled) {
+#pragma unroll 1
+            for (int u = 0; u < 4; ++u) {
+                f(w[0], i + u * stride, i + u * stride < end);
+                w[0] = w[1];
+                w[1] = w[2];
+                w[2] = w[3];
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                f(w[u], i + u * stride, i + u * stride < end);
+        }
     }
-    __device__ __forceinline__ uint4 load()
-    {
-        const uint4 x = at < end ? v[at] : make_uint4(0, 0, 0, 0);
-        at += stride;
-        return x;
-    }
-    __device__ __forceinline__ uint4 next()
-    {
-        const uint4 x = w[0];
-        w[0] = w[1];
-        w[1] = w[2];
-        w[2] = w[3];
-        w[3] = load();
-        return x;
-    }
-};
+}
 
 // A CTA's part of a row: a range of its 16-byte vectors, and for rank 0 the
 // elements before and after them.  Plain loads throughout: the filtered row may
@@ -157,13 +157,12 @@ template <typename T> struct RowSpan {
     // f(values, index of the first) for every vector.
     template <typename F> __device__ __forceinline__ void vectors(F&& f) const
     {
-        VectorQueue q(vec(), v0 + (int)threadIdx.x, v1, kFilterThreads);
-#pragma unroll 1
-        for (int i = v0 + (int)threadIdx.x; i < v1; i += kFilterThreads) {
+        each_vector<true>(vec(), v0, v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
             float x[E];
-            Elem<T>::unpack(q.next(), x);
-            f(x, head + i * E);
-        }
+            Elem<T>::unpack(w, x);
+            if (there)
+                f(x, head + i * E);
+        });
     }
     // f(value, index) for every element
     template <typename F> __device__ __forceinline__ void each(F&& f) const
@@ -884,18 +883,16 @@ __device__ __noinline__ void bin_vectors(const RowSpan<T> row, int stride, Prefi
 {
     constexpr int E = Elem<T>::E;
     const float least = value_of(end.key);
-    int i = row.v0 + (int)threadIdx.x;
-    VectorQueue q(row.vec(), i, row.v1, stride);
-#pragma unroll 1
-    for (; i < row.v1; i += stride) {
+    each_vector<true>(row.vec(), row.v0, row.v1, stride, [&](const uint4& w, int i, bool there) {
         float x[E];
-        Elem<T>::unpack(q.next(), x);
-        const int left = end.index - (row.head + i * E);   // ties up to this one count
+        Elem<T>::unpack(w, x);
+        const int left = there ? end.index - (row.head + i * E) : -1;   // ties up to this one count
+        const float above = there ? least : INFINITY;
 #pragma unroll
         for (int j = 0; j < E; j += 2)
-            bin_pair(s, f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least)), x[j] > least || (x[j] == least && j <= left),
-                     x[j + 1] > least || (x[j + 1] == least && j + 1 <= left), b);
-    }
+            bin_pair(s, f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least)), x[j] > above || (x[j] == above && j <= left),
+                     x[j + 1] > above || (x[j + 1] == above && j + 1 <= left), b);
+    });
 }
 
 // ex2.approx leans to one side: -5.07e-8 of its value on average over arguments
@@ -911,11 +908,11 @@ __device__ __noinline__ float tail_vectors(const RowSpan<T> row, float from, con
     constexpr int E = Elem<T>::E;
     float sum = 0.0f, carry = 0.0f;
     int none = 0;
-    VectorQueue q(row.vec(), row.v0 + (int)threadIdx.x, row.v1, kFilterThreads);
-#pragma unroll 1
-    for (int i = row.v0 + (int)threadIdx.x; i < row.v1; i += kFilterThreads) {
+    each_vector<true>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int, bool there) {
         float x[E];
-        Elem<T>::unpack(q.next(), x);
+        Elem<T>::unpack(w, x);
+        if (!there)
+            return;
         uint64_t add = 0;   // (+0, +0)
         float low = x[0];
 #pragma unroll
@@ -936,7 +933,7 @@ __device__ __noinline__ float tail_vectors(const RowSpan<T> row, float from, con
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 none += x[j] == -INFINITY;
-    }
+    });
     gone = none;
     return sum + fmaf(sum, kExp2Lean, carry);
 }
@@ -1028,20 +1025,17 @@ __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to,
         return ((n >= from && n <= to) || n == also) && end.has(key_of(x), i);
     };
     constexpr int E = Elem<T>::E;
-    const int t = threadIdx.x;
-    VectorQueue q(row.vec(), row.v0 + t, row.v1, kFilterThreads);
-#pragma unroll 1
-    for (int i = row.v0 + t; i - t < row.v1; i += kFilterThreads) {
+    each_vector<true>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
         float x[E];
-        Elem<T>::unpack(q.next(), x);
+        Elem<T>::unpack(w, x);
         uint32_t marks = 0;
-        if (i < row.v1)
+        if (there)
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 marks |= in(x[j], row.head + i * E + j) ? 1u << j : 0u;
         __syncwarp();
         append_marked(s, C, marks, x, row.head + i * E);
-    }
+    });
     const int lone = row.lone();
     if (lone >= 0 && in((float)row.p[lone], lone))
         append(s, C, key_of((float)row.p[lone]), lone);
@@ -1266,8 +1260,11 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
 // pass over the row; their weights times their counts are the exact sums, and a
 // border lies inside one value's tokens.  An atomic a token, where bins of fp32
 // logits take two and the arithmetic of the remainders.
+__device__ __forceinline__ uint64_t times62(uint64_t f, uint64_t g) { return __umul64hi(f, g) << 2; }
+
 struct LevelScale {
     uint64_t first, ratio;   // the weight of the thread's first value, and from one value to the next
+    uint64_t f[4], fourth;   // ratio^0 .. 3, and ratio^4
     float value, step;
 };
 
@@ -1291,11 +1288,13 @@ __device__ __forceinline__ LevelScale level_scale(const FilterShared& s, int t)
     l.step = l.value - level_value(t, 1);
     l.first = l.value > s.scale.m ? 0 : weight62(l.value, s.scale, s.roots);   // (above the row's first value's: none there)
     l.ratio = l.step * s.scale.ch > 63.0f ? 0 : exp2_neg((uint64_t)scaled48(l.step, s.scale.ch, s.scale.cl), s.roots);
+    l.f[0] = kOne62;
+    l.f[1] = l.ratio;
+    l.f[2] = times62(l.ratio, l.ratio);
+    l.f[3] = times62(l.f[2], l.ratio);
+    l.fourth = times62(l.f[2], l.f[2]);
     return l;
 }
-
-// From one value's weight over the thread's first to the next one's; in units of 2^-62.
-__device__ __forceinline__ uint64_t next_level(uint64_t f, uint64_t ratio) { return __umul64hi(f, ratio) << 2; }
 
 __device__ __forceinline__ u128 level_mass(uint64_t part, uint64_t first) { return ((u128)part * first) >> 38; }
 
@@ -1310,12 +1309,15 @@ __device__ __noinline__ BinPart scan_levels(FilterShared& s, u128& mass, int& co
     q.n_own = some;
     q.own = 0;
     if (some) {
-        const LevelScale l = level_scale(s, t);
-        uint64_t part = 0, f = kOne62;
-#pragma unroll 4
-        for (int j = 0; j < kLevelsEach; ++j) {
-            part += level_count(s, t, j) * (f >> 24);
-            f = next_level(f, l.ratio);
+        LevelScale l = level_scale(s, t);
+        uint64_t part = 0;
+#pragma unroll 1
+        for (int j = 0; j < kLevelsEach; j += 4) {   // four chains of powers
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                part += level_count(s, t, j + u) * (l.f[u] >> 24);
+                l.f[u] = times62(l.f[u], l.fourth);
+            }
         }
         q.own = level_mass(part, l.first);
     }
@@ -1353,9 +1355,9 @@ template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const BinP
     // every warp goes through that thread's values, one a lane
     const int lane = threadIdx.x & 31;
     const LevelScale l = level_scale(s, s.found);
-    uint64_t f = kOne62;
-    for (int j = 0; j < lane; ++j)
-        f = next_level(f, l.ratio);
+    uint64_t f = (lane & 2) ? (lane & 1 ? l.f[3] : l.f[2]) : (lane & 1 ? l.f[1] : l.f[0]);
+    for (int j = 0; j < lane / 4; ++j)
+        f = times62(f, l.fourth);
     const int n_own = (int)level_count(s, s.found, lane);
     uint64_t x = n_own * (f >> 24);
     const uint64_t own = x;
@@ -1388,7 +1390,9 @@ __device__ __forceinline__ int tokens_for(u128 mass, uint64_t w, int n)
 {
     if (w == 0 || mass >= (u128)w * (uint32_t)n)
         return n;
-    int j = max(1, (int)((float)mass / (float)w));   // within 2^-22 of itself
+    const uint64_t over = (uint64_t)(mass >> 64);
+    const int down = over ? 64 - __clzll(over) : 0;
+    int j = max(1, (int)__fdividef((float)(uint64_t)(mass >> down), (float)(w >> down)));   // within 2^-20 of itself
     j = min(j, n);
     while ((u128)w * (uint32_t)j < mass)
         ++j;
@@ -1411,15 +1415,14 @@ __device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, Fil
             atomicAdd(&s.level[i >> 16], 1u);
         top = bmax2_nan(top, both ? w : w | 0xff800000u);
     };
-    VectorQueue q(row.vec(), row.v0 + (int)threadIdx.x, row.v1, kFilterThreads);
-#pragma unroll 1
-    for (int i = row.v0 + (int)threadIdx.x; i < row.v1; i += kFilterThreads) {
-        const uint4 w = q.next();
-        one(w.x, true);
-        one(w.y, true);
-        one(w.z, true);
-        one(w.w, true);
-    }
+    each_vector<false>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int, bool there) {
+        if (there) {
+            one(w.x, true);
+            one(w.y, true);
+            one(w.z, true);
+            one(w.w, true);
+        }
+    });
     const int lone = row.lone();
     if (lone >= 0)
         one(reinterpret_cast<const unsigned short*>(row.p)[lone], false);
@@ -1429,18 +1432,18 @@ __device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, Fil
 // The tokens of one value into rank 0's list.
 __device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, float value, int C, FilterShared& s)
 {
-    const int t = threadIdx.x;
-    VectorQueue q(row.vec(), row.v0 + t, row.v1, kFilterThreads);
-#pragma unroll 1
-    for (int i = row.v0 + t; i - t < row.v1; i += kFilterThreads) {
+    const uint32_t both = (__float_as_uint(value) >> 16) * 0x10001u;
+    each_vector<true>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
+        // (no value here is a zero: equal logits are equal bits)
+        const uint32_t m = __vcmpeq2(w.x, both) & 0x00020001u, n = __vcmpeq2(w.y, both) & 0x00080004u;
+        const uint32_t o = __vcmpeq2(w.z, both) & 0x00200010u, p = __vcmpeq2(w.w, both) & 0x00800040u;
+        const uint32_t all = m | n | o | p, marks = there ? (all | all >> 16) & 0xffu : 0u;
         float x[8];
-        Elem<__nv_bfloat16>::unpack(q.next(), x);
-        uint32_t marks = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            marks |= x[j] == value ? 1u << j : 0u;
-        append_marked(s, C, i < row.v1 ? marks : 0u, x, row.head + i * 8);
-    }
+            x[j] = value;
+        append_marked(s, C, marks, x, row.head + i * 8);
+    });
     const int lone = row.lone();
     if (lone >= 0 && (float)row.p[lone] == value)
         append(s, C, key_of(value), lone);
