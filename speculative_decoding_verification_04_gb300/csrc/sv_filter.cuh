@@ -65,7 +65,7 @@ struct FilterShared {
     u128 part[kFilterWarps];
     u128 found_mass;
     RowScale scale;
-    uint64_t part64[kFilterWarps], found64;
+    uint64_t part64[kFilterWarps], found64, found_ratio;
     uint32_t steps[kBinsEach];   // 2^31 times 2^(-j 2^-shift)
     Command cmd;
     uint32_t warp_top[kFilterWarps], warp_low[kFilterWarps];
@@ -483,11 +483,13 @@ __device__ __noinline__ void append(FilterShared& s, int C, uint32_t key, int in
     }
 }
 
-// The marked ones of a vector's values (bit j: x[j]), by all lanes of a warp:
-// one atomic a warp.
-template <int E>
-__device__ __forceinline__ void append_marked(FilterShared& s, int C, uint32_t marks, const float (&x)[E], int index)
+// The marked logits of a few vectors (bit u E + j: logit j of the vector at
+// place[u], or place + u stride), by all lanes of a warp: one atomic a warp.  Few
+// are marked, so that their logits are read again.
+template <typename T, typename P>
+__device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShared& s, int C, uint32_t marks, P&& place)
 {
+    constexpr int E = Elem<T>::E;
     if (!__any_sync(kFull, marks))
         return;
     const int lane = threadIdx.x & 31, n = __popc(marks);
@@ -506,23 +508,47 @@ __device__ __forceinline__ void append_marked(FilterShared& s, int C, uint32_t m
             asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(map_to_rank(smem_addr(&s.count), 0)), "r"(upto) : "memory");
     }
     at = __shfl_sync(kFull, at, 31) + upto - n;
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-        if (marks >> j & 1) {
-            if (at < kList) {
-                if (C == 1)
-                    s.list[at] = entry_of(key_of(x[j]), index + j);
-                else
-                    st_rank64(&s.list[at], 0, entry_of(key_of(x[j]), index + j));
-            }
-            ++at;
+    for (; marks; marks &= marks - 1, ++at)
+        if (at < kList) {
+            const int bit = __ffs(marks) - 1, i = row.head + place(bit / E) * E + bit % E;
+            const uint64_t e = entry_of(key_of((float)row.p[i]), i);
+            if (C == 1)
+                s.list[at] = e;
+            else
+                st_rank64(&s.list[at], 0, e);
         }
+    __syncwarp();
 }
 
-// f(values, index of the first, whether there) for the vectors of the groups that reach `least`:
-// the groups are listed, then read by all threads, a vector each (f by whole warps).
+// The logits of a CTA's part that mark(vector, its place) marks (E bits), into
+// rank 0's list; `lone` says it of the thread's logit outside the vectors.
+template <typename T, typename M>
+__device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, int C, M&& mark)
+{
+    constexpr int E = Elem<T>::E;
+    const uint4* v = row.vec();
+#pragma unroll 1
+    for (int i0 = row.v0; i0 < row.v1; i0 += 4 * kFilterThreads) {
+        const int i = i0 + (int)threadIdx.x;
+        uint4 w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            w[u] = i + u * kFilterThreads < row.v1 ? v[i + u * kFilterThreads] : make_uint4(0, 0, 0, 0);
+        uint32_t marks = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + u * kFilterThreads < row.v1)
+                marks |= mark(w[u], i + u * kFilterThreads) << (u * E);
+        __syncwarp();
+        append_marked(row, s, C, marks, [&](int u) { return i + u * kFilterThreads; });
+    }
+}
+
+// f(values, index of the first) for the vectors of the groups that reach `least`:
+// the groups are listed, then read by all threads, a vector each.  What f returns
+// marks the values that go into rank 0's list.
 template <typename T, typename F>
-__device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, float least, FilterShared& s, F&& f)
+__device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, float least, int C, FilterShared& s, F&& f)
 {
     constexpr int E = Elem<T>::E;
     const int t = threadIdx.x;
@@ -547,14 +573,16 @@ __device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, floa
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             w[u] = i[u] >= 0 ? row.vec()[i[u]] : make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-            float x[E];
-            Elem<T>::unpack(w[0], x);
-            f(x, row.head + i[0] * E, i[0] >= 0);
-            w[0] = w[1];
-            i[0] = i[1];
-        }
+        uint32_t marks = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (i[u] >= 0) {
+                float x[E];
+                Elem<T>::unpack(w[u], x);
+                marks |= f(x, row.head + i[u] * E) << (u * E);
+            }
+        __syncwarp();
+        append_marked(row, s, C, marks, [&](int u) { return u ? i[1] : i[0]; });
     }
 }
 
@@ -1018,23 +1046,25 @@ __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to,
     const bool last = to == kBins - 1 || also == kBins - 1;
     const float top = bound((float)from - 1.0f), low = bound((float)to + 1.0f), top2 = bound((float)also - 1.0f);
     const float least = last ? -INFINITY : bound((float)max(to, also) + 1.0f);
+    const float most = fmaxf(top, top2);
     auto in = [&](float x, int i) {
-        if (!(x >= least && (x <= top2 || x >= low) && x <= fmaxf(top, top2)))
-            return false;
         const int n = bin_of(x, b);
         return ((n >= from && n <= to) || n == also) && end.has(key_of(x), i);
     };
     constexpr int E = Elem<T>::E;
-    each_vector<true>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
+    gather(row, s, C, [&](const uint4& w, int i) {
         float x[E];
         Elem<T>::unpack(w, x);
         uint32_t marks = 0;
-        if (there)
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-                marks |= in(x[j], row.head + i * E + j) ? 1u << j : 0u;
-        __syncwarp();
-        append_marked(s, C, marks, x, row.head + i * E);
+        for (int j = 0; j < E; ++j)   // (few pass: the bin itself is looked at for those)
+            marks |= x[j] >= least && (x[j] <= top2 || x[j] >= low) && x[j] <= most ? 1u << j : 0u;
+        uint32_t sure = 0;
+        for (uint32_t left = marks; left; left &= left - 1) {
+            const int j = __ffs(left) - 1, at = row.head + i * E + j;
+            sure |= in((float)row.p[at], at) ? 1u << j : 0u;
+        }
+        return sure;
     });
     const int lone = row.lone();
     if (lone >= 0 && in((float)row.p[lone], lone))
@@ -1264,8 +1294,6 @@ __device__ __forceinline__ uint64_t times62(uint64_t f, uint64_t g) { return __u
 
 struct LevelScale {
     uint64_t first, ratio;   // the weight of the thread's first value, and from one value to the next
-    uint64_t f[4], fourth;   // ratio^0 .. 3, and ratio^4
-    float value, step;
 };
 
 // Thread t's values: kLevelsEach of them in descending order, all of one octave.
@@ -1284,43 +1312,47 @@ __device__ __forceinline__ uint32_t level_count(const FilterShared& s, int t, in
 __device__ __forceinline__ LevelScale level_scale(const FilterShared& s, int t)
 {
     LevelScale l;
-    l.value = level_value(t, 0);
-    l.step = l.value - level_value(t, 1);
-    l.first = l.value > s.scale.m ? 0 : weight62(l.value, s.scale, s.roots);   // (above the row's first value's: none there)
-    l.ratio = l.step * s.scale.ch > 63.0f ? 0 : exp2_neg((uint64_t)scaled48(l.step, s.scale.ch, s.scale.cl), s.roots);
-    l.f[0] = kOne62;
-    l.f[1] = l.ratio;
-    l.f[2] = times62(l.ratio, l.ratio);
-    l.f[3] = times62(l.f[2], l.ratio);
-    l.fourth = times62(l.f[2], l.f[2]);
+    const float value = level_value(t, 0), step = value - level_value(t, 1);
+    l.first = value > s.scale.m ? 0 : weight62(value, s.scale, s.roots);   // (above the row's first value's: none there)
+    l.ratio = step * s.scale.ch > 63.0f ? 0 : exp2_neg((uint64_t)scaled48(step, s.scale.ch, s.scale.cl), s.roots);
     return l;
+}
+
+// f^n, n < 32, in units of 2^-62.
+__device__ __forceinline__ uint64_t power62(uint64_t f, int n)
+{
+    uint64_t y = kOne62;
+#pragma unroll
+    for (int b = 0; b < 5; ++b) {
+        if (n >> b & 1)
+            y = times62(y, f);
+        f = times62(f, f);
+    }
+    return y;
 }
 
 __device__ __forceinline__ u128 level_mass(uint64_t part, uint64_t first) { return ((u128)part * first) >> 38; }
 
-__device__ __noinline__ BinPart scan_levels(FilterShared& s, u128& mass, int& count)
+struct LevelPart : BinPart {
+    LevelScale scale;
+};
+
+__device__ __noinline__ LevelPart scan_levels(FilterShared& s, u128& mass, int& count)
 {
-    BinPart q;
-    const int t = threadIdx.x;
-    int some = 0;
+    LevelPart q;
+    const int t = threadIdx.x, lane = t & 31;
+    q.scale = level_scale(s, t);
+    uint64_t part = 0, f = power62(q.scale.ratio, lane);
+    q.n_own = 0;
 #pragma unroll 4
-    for (int j = 0; j < kLevelsEach; ++j)
-        some += (int)level_count(s, t, (j + t) & (kLevelsEach - 1));
-    q.n_own = some;
-    q.own = 0;
-    if (some) {
-        LevelScale l = level_scale(s, t);
-        uint64_t part = 0;
-#pragma unroll 1
-        for (int j = 0; j < kLevelsEach; j += 4) {   // four chains of powers
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                part += level_count(s, t, j + u) * (l.f[u] >> 24);
-                l.f[u] = times62(l.f[u], l.fourth);
-            }
-        }
-        q.own = level_mass(part, l.first);
+    for (int j = 0; j < kLevelsEach; ++j) {   // (each lane from another value on: other banks)
+        const int i = (j + lane) & (kLevelsEach - 1);
+        const uint32_t n = level_count(s, t, i);
+        q.n_own += (int)n;
+        part += n * (f >> 24);
+        f = i == kLevelsEach - 1 ? kOne62 : times62(f, q.scale.ratio);
     }
+    q.own = level_mass(part, q.scale.first);
     u128 total;
     const u128 both = block_scan((q.own << 24) | (u128)(uint32_t)q.n_own, s, total);
     q.before = both >> 24;
@@ -1339,7 +1371,7 @@ struct LevelAt {
 
 // The value among whose tokens the running count, or mass, reaches goal (which
 // the row does).
-template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const BinPart& q, FilterShared& s, u128 goal)
+template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const LevelPart& q, FilterShared& s, u128 goal)
 {
     __syncthreads();
     if (threadIdx.x == 0)
@@ -1350,14 +1382,14 @@ template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const BinP
         s.found = threadIdx.x;
         s.found_count = q.n_before;
         s.found_mass = q.before;
+        s.found64 = q.scale.first;
+        s.found_ratio = q.scale.ratio;
     }
     __syncthreads();
     // every warp goes through that thread's values, one a lane
     const int lane = threadIdx.x & 31;
-    const LevelScale l = level_scale(s, s.found);
-    uint64_t f = (lane & 2) ? (lane & 1 ? l.f[3] : l.f[2]) : (lane & 1 ? l.f[1] : l.f[0]);
-    for (int j = 0; j < lane / 4; ++j)
-        f = times62(f, l.fourth);
+    const LevelScale l{s.found64, s.found_ratio};
+    const uint64_t f = power62(l.ratio, lane);
     const int n_own = (int)level_count(s, s.found, lane);
     uint64_t x = n_own * (f >> 24);
     const uint64_t own = x;
@@ -1373,7 +1405,9 @@ template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const BinP
     }
     const u128 from = s.found_mass + level_mass(x - own, l.first);
     const bool here = (kCount ? (u128)(uint32_t)(s.found_count + n) : s.found_mass + level_mass(x, l.first)) >= goal;
-    const int i = __ffs(__ballot_sync(kFull, here)) - 1;
+    // (the sums above went through other roundings of the powers: a goal may lie between)
+    const uint32_t at = __ballot_sync(kFull, here), some = __ballot_sync(kFull, n_own > 0);
+    const int i = at ? __ffs(at) - 1 : 31 - __clz(some | 1u);
     LevelAt r;
     r.value = level_value(s.found, i);
     r.weight = __shfl_sync(kFull, (unsigned long long)level_mass(f >> 24, l.first), i);
@@ -1433,16 +1467,11 @@ __device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, Fil
 __device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, float value, int C, FilterShared& s)
 {
     const uint32_t both = (__float_as_uint(value) >> 16) * 0x10001u;
-    each_vector<true>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
-        // (no value here is a zero: equal logits are equal bits)
+    gather(row, s, C, [&](const uint4& w, int) {   // (no value here is a zero: equal logits are equal bits)
         const uint32_t m = __vcmpeq2(w.x, both) & 0x00020001u, n = __vcmpeq2(w.y, both) & 0x00080004u;
         const uint32_t o = __vcmpeq2(w.z, both) & 0x00200010u, p = __vcmpeq2(w.w, both) & 0x00800040u;
-        const uint32_t all = m | n | o | p, marks = there ? (all | all >> 16) & 0xffu : 0u;
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = value;
-        append_marked(s, C, marks, x, row.head + i * 8);
+        const uint32_t all = m | n | o | p;
+        return (all | all >> 16) & 0xffu;
     });
     const int lone = row.lone();
     if (lone >= 0 && (float)row.p[lone] == value)
@@ -1516,7 +1545,7 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
                 } else {
                     int n_all;
                     u128 total;
-                    const BinPart part = scan_levels(s, total, n_all);
+                    const LevelPart part = scan_levels(s, total, n_all);
                     bool cut = false;   // whether the prefix ends inside the row
                     kept = n_all;
                     mass = total;
@@ -1754,11 +1783,12 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
     }
     const float m = value_of(top_key);
     if (greedy) {
-        each_hit(row, groups, m, s, [&](const float (&x)[E], int i, bool there) {
+        each_hit(row, groups, m, C, s, [&](const float (&x)[E], int i) {
 #pragma unroll
             for (int k = E - 1; k >= 0; --k)
-                if (there && x[k] == m)
+                if (x[k] == m)
                     atomicMin(&s.first, i + k);
+            return 0u;
         });
         // (more hits than the list of them holds: by all threads' groups)
         if (s.hits > kList)
@@ -1795,12 +1825,12 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
     if (bounded || g.min_p > 0.0f || V <= kList) {
         const uint32_t cut = max(end.key, bound);
         const float cv = value_of(cut);
-        each_hit(row, groups, cv, s, [&](const float (&x)[E], int i, bool there) {
+        each_hit(row, groups, cv, C, s, [&](const float (&x)[E], int) {
             uint32_t marks = 0;
 #pragma unroll
             for (int k = 0; k < E; ++k)
-                marks |= there && x[k] >= cv ? 1u << k : 0u;
-            append_marked(s, C, marks, x, i);
+                marks |= x[k] >= cv ? 1u << k : 0u;
+            return marks;
         });
         if (lone >= 0 && lone_x >= cv)
             append(s, C, key_of(lone_x), lone);
