@@ -41,7 +41,7 @@ constexpr int kBins = 4096;
 constexpr int kBinShift = 6;       // 64 bins an octave of weights or more,
 constexpr int kBinShiftMost = 9;   // up to 512
 constexpr int kBinsEach = kBins / kFilterThreads;
-constexpr int kLevelsSide = 4098;   // bf16 magnitudes: below 2^-24, 2^-24 to 2^8 one by one, from 2^8
+constexpr int kLevelsSide = 4097;   // bf16 magnitudes: 2^-24 (and below) to 2^8 one by one, from 2^8
 constexpr int kLevels = 2 * kLevelsSide;
 constexpr int kLevelsEach = 4096 * 2 / kFilterThreads;
 constexpr int kFewKept = 512;      // kept tokens that are all listed
@@ -355,9 +355,11 @@ template <> struct Bits<__nv_bfloat16> {
     static constexpr unsigned short ninf = 0xff80u, nan = 0x7fc0u;
 };
 
+// Returns how many this thread kept.
 template <typename T>
-__device__ __forceinline__ void write_row(const RowSpan<T>& row, T* out, bool same_phase, Prefix end)
+__device__ __noinline__ int write_row(const RowSpan<T> row, T* out, bool same_phase, Prefix end)
 {
+    int n = 0;
     typedef typename Bits<T>::type U;
     constexpr int E = Elem<T>::E;
     const float kv = value_of(end.key);
@@ -385,7 +387,9 @@ __device__ __forceinline__ void write_row(const RowSpan<T>& row, T* out, bool sa
                     y.v = w[u];
 #pragma unroll
                     for (int k = 0; k < E; ++k)
-                        if (!(f[k] > kv || (f[k] == kv && row.head + i * E + k <= end.index)))
+                        if (f[k] > kv || (f[k] == kv && row.head + i * E + k <= end.index))
+                            ++n;
+                        else
                             y.e[k] = Bits<T>::ninf;
                     ov[i] = y.v;
                 }
@@ -394,14 +398,19 @@ __device__ __forceinline__ void write_row(const RowSpan<T>& row, T* out, bool sa
     } else {
         for (int j = row.head + row.v0 * E + threadIdx.x; j < row.head + row.v1 * E; j += kFilterThreads) {
             const float f = (float)row.p[j];
-            o[j] = f > kv || (f == kv && j <= end.index) ? x[j] : Bits<T>::ninf;
+            const bool keep = f > kv || (f == kv && j <= end.index);
+            o[j] = keep ? x[j] : Bits<T>::ninf;
+            n += keep;
         }
     }
     const int j = row.lone();
     if (j >= 0) {
         const float f = (float)row.p[j];
-        o[j] = f > kv || (f == kv && j <= end.index) ? x[j] : Bits<T>::ninf;
+        const bool keep = f > kv || (f == kv && j <= end.index);
+        o[j] = keep ? x[j] : Bits<T>::ninf;
+        n += keep;
     }
+    return n;
 }
 
 template <typename T>
@@ -1292,6 +1301,8 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
 // logits take two and the arithmetic of the remainders.
 __device__ __forceinline__ uint64_t times62(uint64_t f, uint64_t g) { return __umul64hi(f, g) << 2; }
 
+constexpr float kLeastLevel = 5.9604644775390625e-8f;   // 2^-24
+
 struct LevelScale {
     uint64_t first, ratio;   // the weight of the thread's first value, and from one value to the next
 };
@@ -1306,7 +1317,7 @@ __device__ __forceinline__ float level_value(int t, int j)
 __device__ __forceinline__ uint32_t level_count(const FilterShared& s, int t, int j)
 {
     const int o = t * kLevelsEach + j;
-    return s.level[o < 4096 ? 4096 - o : kLevelsSide + 1 + o - 4096];
+    return s.level[o < 4096 ? 4095 - o : kLevelsSide + o - 4096];
 }
 
 __device__ __forceinline__ LevelScale level_scale(const FilterShared& s, int t)
@@ -1441,9 +1452,9 @@ __device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, Fil
     uint32_t top = 0xff80ff80u;
     auto one = [&](uint32_t w, bool both) {
         uint32_t m = w & 0x7fff7fffu;
-        asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(0x337f337fu));
+        asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(0x33803380u));
         asm("min.u16x2 %0, %0, %1;" : "+r"(m) : "r"(0x43804380u));
-        const uint32_t i = m - 0x337f337fu + ((w >> 15) & 0x00010001u) * (uint32_t)kLevelsSide;
+        const uint32_t i = m - 0x33803380u + ((w >> 15) & 0x00010001u) * (uint32_t)kLevelsSide;
         atomicAdd(&s.level[i & 0xffffu], 1u);
         if (both)
             atomicAdd(&s.level[i >> 16], 1u);
@@ -1530,7 +1541,7 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
             if (stage == 0) {
                 const float m = value_of(top);
                 const uint32_t low = s.level[2 * kLevelsSide - 1];
-                const bool fit = top > kKeyNegInf && top < kKeyPosInf && m < 256.0f && m > -256.0f && s.level[0] == 0 && s.level[kLevelsSide] == 0;
+                const bool fit = top > kKeyNegInf && top < kKeyPosInf && m < 256.0f && m > -256.0f && fabsf(m) >= kLeastLevel;
                 if (t == 0 && fit) {   // weights relative to the first of the values around the maximum: none is above one
                     const uint32_t bits = __float_as_uint(m) >> 16, mag = (bits & 0x7fffu) - 13184;
                     const float from = bits >> 15 ? __uint_as_float(((13184 + mag / kLevelsEach * kLevelsEach) << 16) | 0x80000000u)
@@ -1538,8 +1549,11 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
                     s.scale = row_scale(from, g.T);
                 }
                 __syncthreads();
-                // logits below -256 have to weigh nothing, and their number is not known
-                const bool able = fit && !s.scale.cold && (low == 0 || ((m + 256.0f) * s.scale.ch > 64.0f && g.k == 0 && g.p < 1.0f));
+                // Logits below -256 have to weigh nothing, and their number is not known.  Those
+                // nearer to zero than 2^-24 are counted with that value: a few of them move the
+                // sums by nothing that shows, but none of them is told from the others.
+                const bool able = fit && !s.scale.cold && (low == 0 || ((m + 256.0f) * s.scale.ch > 64.0f && g.k == 0 && g.p < 1.0f)) &&
+                                  s.level[0] + s.level[kLevelsSide] <= 16 && s.scale.ch < 256.0f;
                 if (!able) {
                     c.op = kCmdRecount;
                 } else {
@@ -1583,7 +1597,9 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
                         }
                         nth = tokens_for(point > at.before ? point - at.before : 1, at.weight, nth);
                     }
-                    if (!DRAW && (!cut || nth == at.n)) {   // whole values
+                    if (fabsf(at.value) == kLeastLevel) {
+                        c.op = kCmdRecount;
+                    } else if (!DRAW && (!cut || nth == at.n)) {   // whole values
                         stage = 2;
                         index = INT_MAX;
                         if (!cut)
@@ -1806,8 +1822,10 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
         if (rank == 0 && t == 0)
             put_row<DRAW>(a, r, 1, first);
         if (!DRAW)
-            write_row(row, out, a.same_phase, Prefix{top_key, first});
+            fill_row(row, out, a.same_phase, Bits<T>::ninf);
         row_sync(C);
+        if (!DRAW && rank == 0 && t == 0)
+            out[first] = (T)m;
         return;
     }
 
@@ -1908,11 +1926,7 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
 
     // 4. Nothing but min-p, if that: every token above its border stays.
     if (!DRAW && g.p >= 1.0f && g.k == 0) {
-        int n = 0;
-        const float least = value_of(end.key);
-        row.each([&](float x, int) { n += x >= least; });
-        const int all = (int)block_sum((u128)(uint32_t)n, s);
-        write_row(row, out, a.same_phase, end);
+        const int all = (int)block_sum((u128)(uint32_t)write_row(row, out, a.same_phase, end), s);
         if (C > 1) {
             if (t == 0)
                 st_rank(&s.peer_gone[rank], 0, (uint32_t)all);
