@@ -103,6 +103,7 @@ sv_status spec_kv_reserve(const sv_kv_pool* pool, const int32_t* kv_len, const i
     a.has_n = n_new != nullptr;
     a.packed = packed;
     a.has_slots = slots != nullptr;
+    a.slots16 = ((uintptr_t)slots & 15) == 0;
     const long long pages = rows / pool->page_size + pool->B;   // about: what the tokens need
     return sv::launch_pages(sv::sv_reserve_kernel, a, pages + (slots ? rows : 0), stream);
 }
@@ -114,7 +115,7 @@ sv_status spec_kv_release(const sv_kv_pool* pool, const int32_t* kv_len, int32_t
     const sv_status st = sv::check_pool(pool, kv_len, held_out, free_count_out, errors, &a);
     if (st != SV_OK || pool->B == 0)
         return st;
-    return sv::launch_pages(sv::sv_release_kernel, a, (long long)pool->B * std::min(pool->max_pages, 8), stream);
+    return sv::launch_pages(sv::sv_release_kernel, a, (long long)pool->B * pool->max_pages / 8, stream);
 }
 
 }  // extern "C"

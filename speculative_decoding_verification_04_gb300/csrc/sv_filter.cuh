@@ -60,7 +60,7 @@ struct alignas(16) Command {
 };
 
 struct FilterShared {
-    uint64_t list[kList];
+    alignas(16) uint64_t list[kList];
     uint64_t roots[64];
     u128 part[kFilterWarps];
     u128 found_mass;
@@ -600,13 +600,18 @@ __device__ __noinline__ void sort_list(FilterShared& s, int n)
 {
     const int t = threadIdx.x;
     if (n <= kFilterThreads) {   // each entry counts those before it, by one thread or up to eight
-        const int g = n <= 32 ? 8 : n <= 64 ? 4 : n <= 128 ? 2 : 1, i = t / g, each = (n + g - 1) / g;
+        const int g = n <= 32 ? 8 : n <= 64 ? 4 : n <= 128 ? 2 : 1, i = t / g, each = ((n + g - 1) / g + 1) & ~1;
         const uint64_t e = i < n ? s.list[i] : 0;
-        const int j1 = min(n, (t % g + 1) * each);
-        int r = 0;
+        const int j0 = min(n, t % g * each), j1 = min(n, j0 + each);   // (j0 even, or at the end)
+        const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(s.list);
+        int r = 0, j = j0 / 2;
 #pragma unroll 4
-        for (int j = t % g * each; j < j1; ++j)
-            r += s.list[j] > e;
+        for (; j < j1 / 2; ++j) {
+            const ulonglong2 p = pairs[j];
+            r += (p.x > e) + (p.y > e);
+        }
+        if ((j1 & 1) && j1 > j0)
+            r += s.list[j1 - 1] > e;
         for (int o = 1; o < g; o <<= 1)
             r += __shfl_xor_sync(kFull, r, o);
         __syncthreads();
@@ -1861,7 +1866,10 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
                 fill_row(row, out, a.same_phase, Bits<T>::ninf);
             if (C > 1) {   // the count has been read, and this part of out is -inf
                 __syncwarp();
-                cluster_arrive();
+                if (DRAW)
+                    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+                else
+                    cluster_arrive();
                 if (rank != 0) {
                     cluster_wait();
                     return;

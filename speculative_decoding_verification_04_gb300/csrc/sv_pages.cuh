@@ -31,6 +31,7 @@ struct PoolArgs {
     uint32_t* err;
     int B, S, rows, max_pages, page_shift, capacity;
     int has_n, packed, has_slots, has_err;
+    int slots16;               // slots is 16-byte aligned
     int update;                // write held_out and free_out
     int work;                  // write pages and slots
     int clustered;             // the grid is one cluster
@@ -175,20 +176,47 @@ __global__ void __launch_bounds__(kPageThreads) sv_reserve_kernel(PoolArgs a)
             if (a.has_slots && !(a.packed && all_bad)) {
                 const long long r0 = a.packed ? s.first[0] : (long long)b0 * a.S;
                 const long long r1 = a.packed ? s.first[nb] : (long long)(b0 + nb) * a.S;
-                for (long long r = r0 + me; r < r1; r += nthr) {
-                    const int i = a.packed ? last_at_most(s.first, nb, (int)r) : (int)(r / a.S) - b0;
-                    const int n = a.packed ? (int)r - s.first[i] : (int)(r % a.S);
-                    long long slot = -1;
-                    if (n < s.count[i]) {
-                        const int pos = s.len[i] + n, pg = pos >> a.page_shift;
-                        const int page = pg < s.held[i] ? a.table[(long long)(b0 + i) * a.max_pages + pg]
-                                                        : a.stack[avail - 1 - (asked + s.before[i] + pg - s.held[i])];
-                        if (page >= 0)
-                            slot = ((long long)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-                        else
-                            err |= kErrCache;
+                // four tokens a thread, from a multiple of four on: one search, stores of 16 bytes
+                for (long long r = (r0 & ~3ll) + 4ll * me; r < r1; r += 4ll * nthr) {
+                    long long x = max(r, r0);
+                    const long long to = min(r + 4, r1);
+                    int i = a.packed ? last_at_most(s.first, nb, (int)x) : (int)(x / a.S) - b0;
+                    int n = a.packed ? (int)x - s.first[i] : (int)(x - (long long)(b0 + i) * a.S);
+                    long long slot[4] = {-1, -1, -1, -1};
+                    int at_page = -1, page = -1;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        if (r + u < x || r + u >= to)
+                            continue;
+                        while (a.packed ? (int)(r + u) >= s.first[i + 1] : n >= a.S) {
+                            ++i;
+                            n = 0;
+                            at_page = -1;
+                        }
+                        if (n < s.count[i]) {
+                            const int pos = s.len[i] + n, pg = pos >> a.page_shift;
+                            if (pg != at_page) {
+                                at_page = pg;
+                                page = pg < s.held[i] ? a.table[(long long)(b0 + i) * a.max_pages + pg]
+                                                      : a.stack[avail - 1 - (asked + s.before[i] + pg - s.held[i])];
+                            }
+                            if (page >= 0)
+                                slot[u] = ((long long)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+                            else
+                                err |= kErrCache;
+                        }
+                        ++n;
                     }
-                    a.slots[r] = slot;
+                    if (a.slots16 && r >= r0 && r + 4 <= r1) {
+                        longlong2* out = reinterpret_cast<longlong2*>(a.slots + r);
+                        out[0] = make_longlong2(slot[0], slot[1]);
+                        out[1] = make_longlong2(slot[2], slot[3]);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (r + u >= x && r + u < to)
+                                a.slots[r + u] = slot[u];
+                    }
                 }
             }
         }
