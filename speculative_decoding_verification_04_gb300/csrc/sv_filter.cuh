@@ -748,10 +748,17 @@ __device__ __forceinline__ int bin_of(float l, const BinScale& b)
     return (int)min(x, (uint32_t)kBins - 1);
 }
 
-__device__ __forceinline__ void bin_add(FilterShared& s, uint32_t i, uint32_t q)
+// (Predicated rather than branched around: most lanes of a warp are out, in every
+// warp some are in.)
+__device__ __forceinline__ void bin_add(FilterShared& s, uint32_t i, uint32_t q, bool in)
 {
-    const uint32_t old = atomicAdd(&s.bin.lo[i], q);
-    atomicAdd(&s.bin.hi[i], (1u << kCarryBits) + (old + q < old ? 1u : 0u));
+    const uint32_t lo = smem_addr(&s.bin.lo[i]);
+    uint32_t old = 0;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p atom.shared.add.u32 %0, [%1], %2;\n\t}"
+                 : "+r"(old) : "r"(lo), "r"(q), "r"((uint32_t)in) : "memory");
+    const uint32_t more = (1u << kCarryBits) + (old + q < old ? 1u : 0u);
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p red.shared.add.u32 [%0], %1;\n\t}"
+                 ::"r"(lo + (uint32_t)sizeof(s.bin.lo)), "r"(more), "r"((uint32_t)in) : "memory");
 }
 
 // Two tokens of at least b.least, the packed pair L; `in` says which of them count.
@@ -766,10 +773,8 @@ __device__ __forceinline__ void bin_pair(FilterShared& s, uint64_t L, bool in0, 
     const uint64_t g = f2_fma(f, f2_fma(f, f2_pack(0.05550411f, 0.05550411f), f2_pack(0.24022651f, 0.24022651f)), f2_pack(0.69314718f, 0.69314718f));
     const uint64_t q = f2_fma(f, g, f2_pack(1.5f * b.step, 1.5f * b.step));
     const uint32_t unit = __float_as_uint(b.step);   // q's bits less these are (2^f - 1) / step 2^23 + 2^22
-    if (in0)
-        bin_add(s, min(b.ref - (uint32_t)at, (uint32_t)kBins - 1), (uint32_t)q - unit);
-    if (in1)
-        bin_add(s, min(b.ref - (uint32_t)(at >> 32), (uint32_t)kBins - 1), (uint32_t)(q >> 32) - unit);
+    bin_add(s, min(b.ref - (uint32_t)at, (uint32_t)kBins - 1), (uint32_t)q - unit, in0);
+    bin_add(s, min(b.ref - (uint32_t)(at >> 32), (uint32_t)kBins - 1), (uint32_t)(q >> 32) - unit, in1);
 }
 
 __device__ __forceinline__ uint32_t bin_count(const FilterShared& s, int i) { return s.bin.hi[i] >> kCarryBits; }

@@ -32,6 +32,7 @@ struct PoolArgs {
     int B, S, rows, max_pages, page_shift, capacity;
     int has_n, packed, has_slots, has_err;
     int slots16;               // slots is 16-byte aligned
+    int each;                  // slots a thread writes at a time: 1 or 4
     int update;                // write held_out and free_out
     int work;                  // write pages and slots
     int clustered;             // the grid is one cluster
@@ -176,17 +177,20 @@ __global__ void __launch_bounds__(kPageThreads) sv_reserve_kernel(PoolArgs a)
             if (a.has_slots && !(a.packed && all_bad)) {
                 const long long r0 = a.packed ? s.first[0] : (long long)b0 * a.S;
                 const long long r1 = a.packed ? s.first[nb] : (long long)(b0 + nb) * a.S;
-                // four tokens a thread, from a multiple of four on: one search, stores of 16 bytes
-                for (long long r = (r0 & ~3ll) + 4ll * me; r < r1; r += 4ll * nthr) {
-                    long long x = max(r, r0);
-                    const long long to = min(r + 4, r1);
+                // a token a thread, or four from a multiple of four on where there are many: one
+                // search, stores of 16 bytes
+                const int each = a.each;
+                for (long long r = r0 / each * each + (long long)each * me; r < r1; r += (long long)each * nthr) {
+                    const long long x = max(r, r0), to = min(r + each, r1);
                     int i = a.packed ? last_at_most(s.first, nb, (int)x) : (int)(x / a.S) - b0;
                     int n = a.packed ? (int)x - s.first[i] : (int)(x - (long long)(b0 + i) * a.S);
                     long long slot[4] = {-1, -1, -1, -1};
                     int at_page = -1, page = -1;
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        if (r + u < x || r + u >= to)
+                        if (r + u >= to)
+                            break;
+                        if (r + u < x)
                             continue;
                         while (a.packed ? (int)(r + u) >= s.first[i + 1] : n >= a.S) {
                             ++i;
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(kPageThreads) sv_reserve_kernel(PoolArgs a)
                         }
                         ++n;
                     }
-                    if (a.slots16 && r >= r0 && r + 4 <= r1) {
+                    if (each == 4 && a.slots16 && r >= r0 && r + 4 <= r1) {
                         longlong2* out = reinterpret_cast<longlong2*>(a.slots + r);
                         out[0] = make_longlong2(slot[0], slot[1]);
                         out[1] = make_longlong2(slot[2], slot[3]);

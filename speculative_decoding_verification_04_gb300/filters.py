@@ -71,6 +71,13 @@ def _settings(temperature, top_k, top_p, min_p, B, dev):
             _ptr(top_p, "top_p", torch.float32, one, dev), _ptr(min_p, "min_p", torch.float32, one, dev))
 
 
+def _like(t, dtype, stream):
+    """A new tensor of t's shape that belongs to the call's stream."""
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype)
+    return _empty(t, t.shape, dtype, stream)
+
+
 def spec_sample_filtered(logits, uniforms, temperature, top_k=None, top_p=None, min_p=None, out_tokens=None, out_prob=None,
                          out_kept=None, stream=None):
     """One token per row of ``logits`` [B, V] from the tokens that the filters
@@ -81,11 +88,11 @@ def spec_sample_filtered(logits, uniforms, temperature, top_k=None, top_p=None, 
         raise ValueError("uniforms must be a [B] tensor")
     one = (B,)
     if out_tokens is None:
-        out_tokens = _empty(logits, one, torch.int32, stream)
+        out_tokens = _like(uniforms, torch.int32, stream)
     if out_prob is None:
-        out_prob = _empty(logits, one, torch.float32, stream)
+        out_prob = _like(uniforms, torch.float32, stream)
     if out_kept is None:
-        out_kept = _empty(logits, one, torch.int32, stream)
+        out_kept = _like(uniforms, torch.int32, stream)
     st = (_lib or _library()).spec_sample_filtered(
         logits.data_ptr(), code, _ptr(uniforms, "uniforms", torch.float32, one, dev),
         *_settings(temperature, top_k, top_p, min_p, B, dev), B, V, _ptr(out_tokens, "out_tokens", torch.int32, one, dev),
