@@ -37,6 +37,8 @@ constexpr int kClusterMost = 16;
 constexpr int kGroup = 8;          // vectors of a thread whose maximum is kept
 constexpr int kGroupsMost = 49;    // sv_max_vocab on one CTA
 constexpr int kList = 2048;        // tokens sorted at a time
+constexpr int kTake = 16;          // logits of a thread summed at a time
+constexpr int kQueue = 63 + 32 * kTake + 1;   // a warp's logits on their way to the bins
 constexpr int kBins = 4096;
 constexpr int kBinShift = 6;       // 64 bins an octave of weights or more,
 constexpr int kBinShiftMost = 9;   // up to 512
@@ -60,7 +62,13 @@ struct alignas(16) Command {
 };
 
 struct FilterShared {
-    alignas(16) uint64_t list[kList];
+    union {
+        struct {
+            alignas(16) uint64_t list[kList];
+            uint16_t hit[kList];
+        };
+        float queue[kFilterWarps][kQueue];
+    };
     uint64_t roots[64];
     u128 part[kFilterWarps];
     u128 found_mass;
@@ -79,7 +87,6 @@ struct FilterShared {
     int hits;              // groups that hold a candidate
     int first;             // lowest index of the largest logit
     int found, found_count;
-    uint16_t hit[kList];
     // the maxima of each thread's groups (as many as the row has), then the bins
     union alignas(16) {
         struct {
@@ -493,10 +500,10 @@ __device__ __noinline__ void append(FilterShared& s, int C, uint32_t key, int in
 }
 
 // The marked logits of a few vectors (bit u E + j: logit j of the vector at
-// place[u], or place + u stride), by all lanes of a warp: one atomic a warp.  Few
-// are marked, so that their logits are read again.
-template <typename T, typename P>
-__device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShared& s, int C, uint32_t marks, P&& place)
+// place(u)), by all lanes of a warp: one atomic a warp.  Few are marked; key(i) is
+// the key of logit i.
+template <typename T, typename K, typename P>
+__device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShared& s, int C, uint32_t marks, K&& key, P&& place)
 {
     constexpr int E = Elem<T>::E;
     if (!__any_sync(kFull, marks))
@@ -520,7 +527,7 @@ __device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShare
     for (; marks; marks &= marks - 1, ++at)
         if (at < kList) {
             const int bit = __ffs(marks) - 1, i = row.head + place(bit / E) * E + bit % E;
-            const uint64_t e = entry_of(key_of((float)row.p[i]), i);
+            const uint64_t e = entry_of(key(i), i);
             if (C == 1)
                 s.list[at] = e;
             else
@@ -531,8 +538,8 @@ __device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShare
 
 // The logits of a CTA's part that mark(vector, its place) marks (E bits), into
 // rank 0's list; `lone` says it of the thread's logit outside the vectors.
-template <typename T, typename M>
-__device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, int C, M&& mark)
+template <typename T, typename K, typename M>
+__device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, int C, K&& key, M&& mark)
 {
     constexpr int E = Elem<T>::E;
     const uint4* v = row.vec();
@@ -549,7 +556,7 @@ __device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, i
             if (i + u * kFilterThreads < row.v1)
                 marks |= mark(w[u], i + u * kFilterThreads) << (u * E);
         __syncwarp();
-        append_marked(row, s, C, marks, [&](int u) { return i + u * kFilterThreads; });
+        append_marked(row, s, C, marks, key, [&](int u) { return i + u * kFilterThreads; });
     }
 }
 
@@ -591,7 +598,7 @@ __device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, floa
                 marks |= f(x, row.head + i[u] * E) << (u * E);
             }
         __syncwarp();
-        append_marked(row, s, C, marks, [&](int u) { return u ? i[1] : i[0]; });
+        append_marked(row, s, C, marks, [&](int k) { return key_of((float)row.p[k]); }, [&](int u) { return u ? i[1] : i[0]; });
     }
 }
 
@@ -947,30 +954,43 @@ __device__ __noinline__ void bin_vectors(const RowSpan<T> row, int stride, Prefi
 constexpr float kExp2Lean = 5.07e-8f;
 
 // The same with tokens below `from` summed on the way (fp32 weights, the sums
-// compensated) instead.  Returns this thread's sum; `gone` counts the logits of
-// -inf.
+// compensated) instead.  The others, fewer, go through the bins 64 of a warp at a
+// time: half of what the bins take for each logit is arithmetic that the others do
+// not need.  Returns this thread's sum; `gone` counts the logits of -inf.
 template <typename T>
 __device__ __noinline__ float tail_vectors(const RowSpan<T> row, float from, const BinScale b, FilterShared& s, int& gone)
 {
-    constexpr int E = Elem<T>::E;
+    constexpr int E = Elem<T>::E, N = kTake / E;
+    const int t = threadIdx.x, lane = t & 31;
+    float* queue = s.queue[t >> 5];
+    const uint4* v = row.vec();
     float sum = 0.0f, carry = 0.0f;
-    int none = 0;
-    each_vector<true>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int, bool there) {
-        float x[E];
-        Elem<T>::unpack(w, x);
-        if (!there)
-            return;
-        uint64_t add = 0;   // (+0, +0)
-        float low = x[0];
+    int waiting = 0, none = 0;
+    const uint64_t ch = f2_pack(b.ch, b.ch), cl = f2_pack(b.cl, b.cl), unit = f2_pack(-b.unit, -b.unit);
+#pragma unroll 1
+    for (int i = row.v0 + t; i - t < row.v1; i += N * kFilterThreads) {
+        uint4 w[N];
+        const uint32_t out = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
 #pragma unroll
-        for (int j = 0; j < E; j += 2) {
-            const uint64_t L = f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least));
-            const bool in0 = x[j] >= from, in1 = x[j + 1] >= from;
-            float w0, w1;
-            f2_unpack(f2_fma(L, f2_pack(b.cl, b.cl), f2_fma(L, f2_pack(b.ch, b.ch), f2_pack(-b.unit, -b.unit))), w0, w1);
-            add = f2_add(add, f2_pack(in0 ? 0.0f : ex2_approx(w0), in1 ? 0.0f : ex2_approx(w1)));
-            low = fminf(low, fminf(x[j], x[j + 1]));
-            bin_pair(s, L, in0, in1, b);
+        for (int u = 0; u < N; ++u)
+            w[u] = i + u * kFilterThreads < row.v1 ? v[i + u * kFilterThreads] : make_uint4(out, out, out, out);
+        uint64_t add = 0;   // (+0, +0)
+        float low = INFINITY;
+        uint32_t in = 0;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            float x[E];
+            Elem<T>::unpack(w[u], x);
+#pragma unroll
+            for (int j = 0; j < E; j += 2) {
+                const uint64_t L = f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least));
+                const bool in0 = x[j] >= from, in1 = x[j + 1] >= from;
+                float w0, w1;
+                f2_unpack(f2_fma(L, cl, f2_fma(L, ch, unit)), w0, w1);
+                add = f2_add(add, f2_pack(in0 ? 0.0f : ex2_approx(w0), in1 ? 0.0f : ex2_approx(w1)));
+                in |= (in0 ? 1u << (u * E + j) : 0u) | (in1 ? 2u << (u * E + j) : 0u);
+                low = fminf(low, fminf(x[j], x[j + 1]));
+            }
         }
         float lo, hi, e;
         f2_unpack(add, lo, hi);
@@ -978,9 +998,50 @@ __device__ __noinline__ float tail_vectors(const RowSpan<T> row, float from, con
         carry += e;
         if (low == -INFINITY)
 #pragma unroll
+            for (int u = 0; u < N; ++u) {
+                float x[E];
+                Elem<T>::unpack(w[u], x);
+                if (i + u * kFilterThreads < row.v1)
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        none += x[j] == -INFINITY;
+            }
+        __syncwarp();
+        // the lanes' logits one after the other
+        int upto = __popc(in);
+        int to = waiting - upto;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o)
+                upto += y;
+        }
+        to += upto;
+        waiting += __shfl_sync(kFull, upto, 31);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            float x[E];
+            Elem<T>::unpack(w[u], x);
+#pragma unroll
             for (int j = 0; j < E; ++j)
-                none += x[j] == -INFINITY;
-    });
+                if (in >> (u * E + j) & 1)
+                    queue[to++] = x[j];
+        }
+        __syncwarp();
+        if (waiting >= 64) {
+            int done = 0;
+#pragma unroll 1
+            for (; done + 64 <= waiting; done += 64)
+                bin_pair(s, f2_pack(queue[done + lane], queue[done + 32 + lane]), true, true, b);
+            const float left0 = queue[done + lane], left1 = queue[min(done + 32 + lane, kQueue - 1)];
+            __syncwarp();
+            queue[lane] = left0;
+            queue[lane + 32] = left1;
+            waiting -= done;
+            __syncwarp();
+        }
+    }
+    bin_pair(s, f2_pack(queue[lane], queue[lane + 32]), lane < waiting, lane + 32 < waiting, b);
     gone = none;
     return sum + fmaf(sum, kExp2Lean, carry);
 }
@@ -1055,35 +1116,44 @@ __device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Pr
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-// The tokens of the prefix that are in bins from .. to, or in `also`: a compare
-// with the bins' bounds (wider by half a bin, for the rounding) before the bin
-// itself.
+// The lowest logit of bin i or one before it: near where the bin's border should
+// be, by bisection (bin_of does not increase with the logit).
+__device__ __noinline__ float bin_floor(int i, float m, const BinScale& b)
+{
+    if (i >= kBins - 1)
+        return -INFINITY;
+    const float at = (b.unit - ((float)i + 1.5f) * b.step) / b.ch, wide = 2.0f * b.step / b.ch;
+    uint32_t lo = key_of(fmaxf(at - wide, -3.4028234e38f)), hi = key_of(fminf(at + wide, m));   // bin_of(lo) > i >= bin_of(hi)
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (bin_of(value_of(mid), b) <= i)
+            hi = mid;
+        else
+            lo = mid;
+    }
+    return value_of(hi);
+}
+
+// The tokens of the prefix that are in bins from .. to, or in `also`.
 template <typename T>
 __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to, int also, Prefix end, const BinScale b, int C, FilterShared& s)
 {
-    auto bound = [&](float i) { return (b.unit - (i + 1.0f) * b.step) / b.ch; };   // bin 0's centre is a step below `unit`
-    const bool last = to == kBins - 1 || also == kBins - 1;
-    const float top = bound((float)from - 1.0f), low = bound((float)to + 1.0f), top2 = bound((float)also - 1.0f);
-    const float least = last ? -INFINITY : bound((float)max(to, also) + 1.0f);
-    const float most = fmaxf(top, top2);
-    auto in = [&](float x, int i) {
-        const int n = bin_of(x, b);
-        return ((n >= from && n <= to) || n == also) && end.has(key_of(x), i);
-    };
     constexpr int E = Elem<T>::E;
-    gather(row, s, C, [&](const uint4& w, int i) {
+    const float m = s.scale.m;
+    const float low = bin_floor(to, m, b), top = from > 0 ? bin_floor(from - 1, m, b) : INFINITY;        // [low, top)
+    const float low2 = bin_floor(also, m, b), top2 = also > 0 ? bin_floor(also - 1, m, b) : INFINITY;
+    const float least = value_of(end.key);
+    auto in = [&](float x, int i) {
+        return ((x >= low && x < top) || (x >= low2 && x < top2)) && (x > least || (x == least && i <= end.index));
+    };
+    gather(row, s, C, [&](int i) { return key_of((float)row.p[i]); }, [&](const uint4& w, int i) {
         float x[E];
         Elem<T>::unpack(w, x);
         uint32_t marks = 0;
 #pragma unroll
-        for (int j = 0; j < E; ++j)   // (few pass: the bin itself is looked at for those)
-            marks |= x[j] >= least && (x[j] <= top2 || x[j] >= low) && x[j] <= most ? 1u << j : 0u;
-        uint32_t sure = 0;
-        for (uint32_t left = marks; left; left &= left - 1) {
-            const int j = __ffs(left) - 1, at = row.head + i * E + j;
-            sure |= in((float)row.p[at], at) ? 1u << j : 0u;
-        }
-        return sure;
+        for (int j = 0; j < E; ++j)
+            marks |= in(x[j], row.head + i * E + j) ? 1u << j : 0u;
+        return marks;
     });
     const int lone = row.lone();
     if (lone >= 0 && in((float)row.p[lone], lone))
@@ -1488,7 +1558,8 @@ __device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, Fil
 __device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, float value, int C, FilterShared& s)
 {
     const uint32_t both = (__float_as_uint(value) >> 16) * 0x10001u;
-    gather(row, s, C, [&](const uint4& w, int) {   // (no value here is a zero: equal logits are equal bits)
+    const uint32_t key = key_of(value);
+    gather(row, s, C, [&](int) { return key; }, [&](const uint4& w, int) {   // (no value here is a zero: equal logits are equal bits)
         const uint32_t m = __vcmpeq2(w.x, both) & 0x00020001u, n = __vcmpeq2(w.y, both) & 0x00080004u;
         const uint32_t o = __vcmpeq2(w.z, both) & 0x00200010u, p = __vcmpeq2(w.w, both) & 0x00800040u;
         const uint32_t all = m | n | o | p;
