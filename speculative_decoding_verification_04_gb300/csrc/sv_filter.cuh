@@ -108,32 +108,43 @@ constexpr size_t filter_smem_bytes(int groups)
 // the row, the block and the cluster
 // ---------------------------------------------------------------------------
 
+// N of a thread's vectors, at i, i + stride, ...; `none` stands for those past the end.
+template <int N> struct Vectors {
+    uint4 w[N];
+    __device__ __forceinline__ void load(const uint4* v, int i, int end, int stride, uint32_t none = 0)
+    {
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            w[u] = i + u * stride < end ? v[i + u * stride] : make_uint4(none, none, none, none);
+    }
+};
+
 // f(vector, its place, whether there) for the vectors at first + threadIdx.x,
-// + stride, ... below `end`, by whole warps; four are fetched at a time.  kRolled:
-// f is in the code once, for longer ones: code that runs a few times a row comes
-// from L2, and costs more than the moves do.
+// + stride, ... below `end`, by whole warps; four are on their way while four are
+// worked on.  kRolled: f is in the code once, for longer ones: code that runs a
+// few times a row comes from L2, and costs more than the moves do.
 template <bool kRolled, typename F>
 __device__ __forceinline__ void each_vector(const uint4* v, int first, int end, int stride, F&& f)
 {
     const int t = threadIdx.x;
+    Vectors<4> next;
+    next.load(v, first + t, end, stride);
 #pragma unroll 1
     for (int i = first + t; i - t < end; i += 4 * stride) {
-        uint4 w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            w[u] = i + u * stride < end ? v[i + u * stride] : make_uint4(0, 0, 0, 0);
+        Vectors<4> now = next;
+        next.load(v, i + 4 * stride, end, stride);
         if (kRolled) {
 #pragma unroll 1
             for (int u = 0; u < 4; ++u) {
-                f(w[0], i + u * stride, i + u * stride < end);
-                w[0] = w[1];
-                w[1] = w[2];
-                w[2] = w[3];
+                f(now.w[0], i + u * stride, i + u * stride < end);
+                now.w[0] = now.w[1];
+                now.w[1] = now.w[2];
+                now.w[2] = now.w[3];
             }
         } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                f(w[u], i + u * stride, i + u * stride < end);
+                f(now.w[u], i + u * stride, i + u * stride < end);
         }
     }
 }
@@ -499,16 +510,11 @@ __device__ __noinline__ void append(FilterShared& s, int C, uint32_t key, int in
     }
 }
 
-// The marked logits of a few vectors (bit u E + j: logit j of the vector at
-// place(u)), by all lanes of a warp: one atomic a warp.  Few are marked; key(i) is
-// the key of logit i.
-template <typename T, typename K, typename P>
-__device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShared& s, int C, uint32_t marks, K&& key, P&& place)
+// Room in rank 0's list for each lane's n entries, by all lanes of a warp: one
+// atomic a warp.  The place of the lane's first.
+__device__ __forceinline__ int list_room(FilterShared& s, int C, int n)
 {
-    constexpr int E = Elem<T>::E;
-    if (!__any_sync(kFull, marks))
-        return;
-    const int lane = threadIdx.x & 31, n = __popc(marks);
+    const int lane = threadIdx.x & 31;
     int upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -523,40 +529,61 @@ __device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShare
         else
             asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(map_to_rank(smem_addr(&s.count), 0)), "r"(upto) : "memory");
     }
-    at = __shfl_sync(kFull, at, 31) + upto - n;
-    for (; marks; marks &= marks - 1, ++at)
-        if (at < kList) {
-            const int bit = __ffs(marks) - 1, i = row.head + place(bit / E) * E + bit % E;
-            const uint64_t e = entry_of(key(i), i);
-            if (C == 1)
-                s.list[at] = e;
-            else
-                st_rank64(&s.list[at], 0, e);
-        }
+    return __shfl_sync(kFull, at, 31) + upto - n;
+}
+
+__device__ __forceinline__ void list_put(FilterShared& s, int C, int at, uint64_t e)
+{
+    if (at >= kList)
+        return;
+    if (C == 1)
+        s.list[at] = e;
+    else
+        st_rank64(&s.list[at], 0, e);
+}
+
+// The marked logits of N vectors (bit u E + j: logit j of vector u, which is at
+// place(u)) into rank 0's list, by all lanes of a warp.
+template <typename T, int N, typename P>
+__device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShared& s, int C, uint32_t marks, const uint4 (&w)[N], P&& place)
+{
+    constexpr int E = Elem<T>::E;
+    if (!__any_sync(kFull, marks))
+        return;
+    int at = list_room(s, C, __popc(marks));
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        float x[E];
+        Elem<T>::unpack(w[u], x);
+        if (marks >> (u * E) & ((1u << E) - 1))
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (marks >> (u * E + j) & 1)
+                    list_put(s, C, at++, entry_of(key_of(x[j]), row.head + place(u) * E + j));
+    }
     __syncwarp();
 }
 
 // The logits of a CTA's part that mark(vector, its place) marks (E bits), into
-// rank 0's list; `lone` says it of the thread's logit outside the vectors.
-template <typename T, typename K, typename M>
-__device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, int C, K&& key, M&& mark)
+// rank 0's list.
+template <typename T, typename M>
+__device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, int C, M&& mark)
 {
     constexpr int E = Elem<T>::E;
-    const uint4* v = row.vec();
+    const int t = threadIdx.x;
+    Vectors<4> next;
+    next.load(row.vec(), row.v0 + t, row.v1, kFilterThreads);
 #pragma unroll 1
-    for (int i0 = row.v0; i0 < row.v1; i0 += 4 * kFilterThreads) {
-        const int i = i0 + (int)threadIdx.x;
-        uint4 w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            w[u] = i + u * kFilterThreads < row.v1 ? v[i + u * kFilterThreads] : make_uint4(0, 0, 0, 0);
+    for (int i = row.v0 + t; i - t < row.v1; i += 4 * kFilterThreads) {
+        const Vectors<4> now = next;
+        next.load(row.vec(), i + 4 * kFilterThreads, row.v1, kFilterThreads);
         uint32_t marks = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             if (i + u * kFilterThreads < row.v1)
-                marks |= mark(w[u], i + u * kFilterThreads) << (u * E);
+                marks |= mark(now.w[u], i + u * kFilterThreads) << (u * E);
         __syncwarp();
-        append_marked(row, s, C, marks, key, [&](int u) { return i + u * kFilterThreads; });
+        append_marked(row, s, C, marks, now.w, [&](int u) { return i + u * kFilterThreads; });
     }
 }
 
@@ -598,7 +625,7 @@ __device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, floa
                 marks |= f(x, row.head + i[u] * E) << (u * E);
             }
         __syncwarp();
-        append_marked(row, s, C, marks, [&](int k) { return key_of((float)row.p[k]); }, [&](int u) { return u ? i[1] : i[0]; });
+        append_marked(row, s, C, marks, w, [&](int u) { return u ? i[1] : i[0]; });
     }
 }
 
@@ -967,13 +994,14 @@ __device__ __noinline__ float tail_vectors(const RowSpan<T> row, float from, con
     float sum = 0.0f, carry = 0.0f;
     int waiting = 0, none = 0;
     const uint64_t ch = f2_pack(b.ch, b.ch), cl = f2_pack(b.cl, b.cl), unit = f2_pack(-b.unit, -b.unit);
+    const uint32_t out = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+    Vectors<N> next;
+    next.load(v, row.v0 + t, row.v1, kFilterThreads, out);
 #pragma unroll 1
     for (int i = row.v0 + t; i - t < row.v1; i += N * kFilterThreads) {
-        uint4 w[N];
-        const uint32_t out = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-#pragma unroll
-        for (int u = 0; u < N; ++u)
-            w[u] = i + u * kFilterThreads < row.v1 ? v[i + u * kFilterThreads] : make_uint4(out, out, out, out);
+        const Vectors<N> now = next;
+        const uint4(&w)[N] = now.w;
+        next.load(v, i + N * kFilterThreads, row.v1, kFilterThreads, out);
         uint64_t add = 0;   // (+0, +0)
         float low = INFINITY;
         uint32_t in = 0;
@@ -1146,7 +1174,7 @@ __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to,
     auto in = [&](float x, int i) {
         return ((x >= low && x < top) || (x >= low2 && x < top2)) && (x > least || (x == least && i <= end.index));
     };
-    gather(row, s, C, [&](int i) { return key_of((float)row.p[i]); }, [&](const uint4& w, int i) {
+    gather(row, s, C, [&](const uint4& w, int i) {
         float x[E];
         Elem<T>::unpack(w, x);
         uint32_t marks = 0;
@@ -1558,8 +1586,7 @@ __device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, Fil
 __device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, float value, int C, FilterShared& s)
 {
     const uint32_t both = (__float_as_uint(value) >> 16) * 0x10001u;
-    const uint32_t key = key_of(value);
-    gather(row, s, C, [&](int) { return key; }, [&](const uint4& w, int) {   // (no value here is a zero: equal logits are equal bits)
+    gather(row, s, C, [&](const uint4& w, int) {   // (no value here is a zero: equal logits are equal bits)
         const uint32_t m = __vcmpeq2(w.x, both) & 0x00020001u, n = __vcmpeq2(w.y, both) & 0x00080004u;
         const uint32_t o = __vcmpeq2(w.z, both) & 0x00200010u, p = __vcmpeq2(w.w, both) & 0x00800040u;
         const uint32_t all = m | n | o | p;
@@ -1728,6 +1755,76 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
     }
 }
 
+// A row that no filter touches, in the one pass that has to read it anyway; if it
+// turns out unusable, NaN over it.
+template <typename T>
+__device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const RowSpan<T> row, int rank, FilterShared& s)
+{
+    typedef typename Bits<T>::type U;
+    constexpr int E = Elem<T>::E;
+    const int C = a.C, t = threadIdx.x;
+    T* out = static_cast<T*>(a.out) + r * a.V;
+    U* o = reinterpret_cast<U*>(out);
+    float top = -INFINITY;
+    int n = 0;
+    each_vector<false>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
+        if (!there)
+            return;
+        float x[E];
+        Elem<T>::unpack(w, x);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            top = max_nan(top, x[j]);
+            n += x[j] > -INFINITY;
+        }
+        if (a.same_phase) {
+            reinterpret_cast<uint4*>(o + row.head)[i] = w;
+        } else {
+            union {
+                uint4 v;
+                U e[E];
+            } y;
+            y.v = w;
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                o[row.head + i * E + j] = y.e[j];
+        }
+    });
+    const int lone = row.lone();
+    if (lone >= 0) {
+        const float x = (float)row.p[lone];
+        top = max_nan(top, x);
+        n += x > -INFINITY;
+        o[lone] = reinterpret_cast<const U*>(row.p)[lone];
+    }
+    const uint32_t key = __reduce_max_sync(kFull, key_of(top));
+    if ((t & 31) == 0)
+        s.warp_top[t >> 5] = key;
+    const int own = (int)block_sum((u128)(uint32_t)n, s);   // (a barrier behind warp_top)
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < kFilterWarps; ++i)
+        most = max(most, s.warp_top[i]);
+    int all = own;
+    if (C > 1) {
+        if (t < C) {
+            st_rank(&s.peer_top[rank], t, most);
+            st_rank(&s.peer_gone[rank], t, (uint32_t)own);
+        }
+        row_sync(C);
+        all = 0;
+        for (int c = 0; c < C; ++c) {
+            most = max(most, s.peer_top[c]);
+            all += s.peer_gone[c];
+        }
+    }
+    const bool usable = most > kKeyNegInf && most < kKeyPosInf;
+    if (rank == 0 && t == 0)
+        put_row<false>(a, r, usable ? all : -1);
+    if (!usable)
+        fill_row(row, out, a.same_phase, Bits<T>::nan);
+}
+
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs a)
 {
@@ -1767,6 +1864,11 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
         if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : g.k > C * (kFilterThreads / 2)))
             if (levels_row<DRAW>(a, r, g, row, rank, s))
                 return;
+
+    if (!DRAW && good && !greedy && g.min_p == 0.0f && g.p >= 1.0f && (g.k == 0 || g.k >= V)) {
+        copy_row<T>(a, r, row, rank, s);
+        return;
+    }
 
     double t_log = 0.0;   // one thread's: 64-bit floating point runs at a hundredth of the fp32 rate
     if (t == kFilterThreads - 32 && good && !greedy && g.min_p > 0.0f)
