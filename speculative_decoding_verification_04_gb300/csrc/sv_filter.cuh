@@ -383,44 +383,32 @@ __device__ __noinline__ int write_row(const RowSpan<T> row, T* out, bool same_ph
     const float kv = value_of(end.key);
     U* o = reinterpret_cast<U*>(out);
     const U* x = reinterpret_cast<const U*>(row.p);
-    if (same_phase) {
-        const uint4* v = row.vec();
-        uint4* ov = reinterpret_cast<uint4*>(o + row.head);
-        for (int i0 = row.v0 + threadIdx.x; i0 < row.v1; i0 += 4 * kFilterThreads) {
-            uint4 w[4];
+    // (a thread's vectors are its own: fetched before any of them is written, where out is the row)
+    each_vector<false>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
+        if (!there)
+            return;
+        float f[E];
+        Elem<T>::unpack(w, f);
+        union {
+            uint4 v;
+            U e[E];
+        } y;
+        y.v = w;
+        const int left = end.index - (row.head + i * E);   // ties up to this one stay
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i0 + u * kFilterThreads < row.v1)
-                    w[u] = v[i0 + u * kFilterThreads];   // (out may be the row)
+        for (int k = 0; k < E; ++k)
+            if (f[k] > kv || (f[k] == kv && k <= left))
+                ++n;
+            else
+                y.e[k] = Bits<T>::ninf;
+        if (same_phase) {
+            reinterpret_cast<uint4*>(o + row.head)[i] = y.v;
+        } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u * kFilterThreads;
-                if (i < row.v1) {
-                    float f[E];
-                    Elem<T>::unpack(w[u], f);
-                    union {
-                        uint4 v;
-                        U e[E];
-                    } y;
-                    y.v = w[u];
-#pragma unroll
-                    for (int k = 0; k < E; ++k)
-                        if (f[k] > kv || (f[k] == kv && row.head + i * E + k <= end.index))
-                            ++n;
-                        else
-                            y.e[k] = Bits<T>::ninf;
-                    ov[i] = y.v;
-                }
-            }
+            for (int k = 0; k < E; ++k)
+                o[row.head + i * E + k] = y.e[k];
         }
-    } else {
-        for (int j = row.head + row.v0 * E + threadIdx.x; j < row.head + row.v1 * E; j += kFilterThreads) {
-            const float f = (float)row.p[j];
-            const bool keep = f > kv || (f == kv && j <= end.index);
-            o[j] = keep ? x[j] : Bits<T>::ninf;
-            n += keep;
-        }
-    }
+    });
     const int j = row.lone();
     if (j >= 0) {
         const float f = (float)row.p[j];
@@ -1129,8 +1117,8 @@ __device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Pr
         if (lone >= 0 && lone_x < from && lone_x >= b.least)
             sum += ex2_approx(fmaf(lone_x, b.cl, fmaf(lone_x, b.ch, -b.unit)));
         gone += lone >= 0 && lone_x == -INFINITY;
-        // units of 2^-62, and the count below them
-        const u128 both = block_sum((u128)__float2ull_rn(sum * 1125899906842624.0f) << 36 | (u128)(uint32_t)gone, s);
+        // units of 2^-62 from 2^-42 (the sum may reach 2^20), and the count below them
+        const u128 both = block_sum((u128)__float2ull_rn(sum * 4398046511104.0f) << 44 | (u128)(uint32_t)gone, s);
         rest = both >> 24;
         gone = (int)((uint32_t)both & 0xffffffu);
     }
@@ -1843,6 +1831,8 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
     Settings g;
     g.T = a.temperature[b];
     g.k = a.has_k ? a.top_k[b] : 0;
+    if (g.k >= V)
+        g.k = 0;   // (all of the row)
     g.p = a.has_p ? a.top_p[b] : 1.0f;
     g.min_p = a.has_m ? a.min_p[b] : 0.0f;
     g.u = DRAW && g.T != 0.0f ? a.uniforms[r] : 0.0f;
@@ -1865,7 +1855,7 @@ __global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs
             if (levels_row<DRAW>(a, r, g, row, rank, s))
                 return;
 
-    if (!DRAW && good && !greedy && g.min_p == 0.0f && g.p >= 1.0f && (g.k == 0 || g.k >= V)) {
+    if (!DRAW && good && !greedy && g.min_p == 0.0f && g.p >= 1.0f && g.k == 0) {
         copy_row<T>(a, r, row, rank, s);
         return;
     }

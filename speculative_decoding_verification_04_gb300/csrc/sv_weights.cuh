@@ -48,8 +48,8 @@ constexpr uint32_t kKeyPosInf = 0xff800000u;
 
 // What the weights of one row are made with: x = (m - l) log2(e) / T in units
 // of 2^-48 from products with a constant split in two floats (each product is
-// exact with its remainder, so x is good to about 2^-41 at |l| log2(e) / T up
-// to 2^12); rows beyond that take differences in 64 bits.
+// exact with its remainder, so x is good to about 2^-42 at |l| log2(e) / T up
+// to 2^6, to 2^-36 at 2^12); rows beyond that take differences in 64 bits.
 struct RowScale {
     float ch, cl;       // log2(e) / T
     float m, T;

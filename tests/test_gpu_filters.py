@@ -190,6 +190,92 @@ def test_unusable_rows(dev, bad, V, dtype):
         check_filter(logits, s, (out, kept))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,B", [(2049, 3), (30011, 3), (60000, 1)])
+@pytest.mark.parametrize("bad", [float("nan"), -float("nan"), float("inf"), None])
+def test_unusable_rows_whatever_the_filters(dev, bad, V, B, dtype):
+    logits, u = rows(B, V, dtype, dev, 15)
+    if bad is None:
+        logits[B - 1] = float("-inf")
+    else:
+        logits[B - 1, V // 3] = bad
+        if bad != bad and dtype == "bf16":   # both signs of a NaN
+            logits.view(torch.int16)[B - 1, V // 3] = 0x7fc1 if str(bad)[0] != "-" else -0x3f
+    for one in (dict(), dict(k=[0] * B, p=[0.9] * B), dict(k=[700] * B), dict(k=[V] * B), dict(m=[0.1] * B), dict(k=[3] * B, p=[0.5] * B)):
+        s = settings(dev, [0.8] * B, **one)
+        check_draw(logits, u, s)
+        check_filter(logits, s)
+    s = settings(dev, [0.0] * B)
+    check_draw(logits, u, s)
+    check_filter(logits, s)
+
+
+@pytest.mark.parametrize("V", [2500, 40000, 128256])
+def test_top_k_of_every_size(dev, V):
+    for dtype in ("bf16", "f32"):
+        ks = [1, 2, 127, 128, 129, 1000, 1025, 2048, 2049, V - 1, V, V + 1, 2 ** 31 - 1]
+        logits, u = rows(len(ks), V, dtype, dev, V + 2)
+        for p in (None, [0.7] * len(ks)):
+            s = settings(dev, [0.9] * len(ks), ks, p)
+            check_draw(logits, u, s)
+            check_filter(logits, s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logits_beyond_the_usual_range(dev, dtype):
+    """Near zero, far below, and around 256: what the counted levels of bf16 rows do not cover."""
+    V = 9000
+    base, u = rows(8, V, dtype, dev, 60)
+    x = base.float()
+    x[0, ::2] *= 1e-9                       # half of the row next to zero
+    x[1] *= 1e-9
+    x[2, ::3] = 0.0
+    x[2, 1::3] = -0.0
+    x[3, ::2] = -1e4                        # a finite mask
+    x[4] += 300
+    x[5] -= 300
+    x[6, 5:] = -300 - x[6, 5:].abs()        # five tokens and a far tail
+    x[7, :10] = torch.arange(10, device=dev) * 1e-8
+    x = x.to(DT[dtype])
+    for T, k, p in ((1.0, None, [0.9] * 8), (20.0, None, [0.5] * 8), (0.7, [600] * 8, [0.99] * 8), (1.0, None, None), (300.0, None, [0.999] * 8)):
+        s = settings(dev, [T] * 8, k, p)
+        check_draw(x, u, s)
+        check_filter(x, s)
+
+
+def test_a_large_batch_against_a_plain_sort(dev):
+    """Whole numbers over many rows: nothing that happens once in a few hundred."""
+    B, V = 700, 20011
+    for dtype in ("bf16", "f32"):
+        logits, u = rows(B, V, dtype, dev, 70, sigma=2.5)
+        T = torch.rand(B, device=dev) + 0.4
+        p = torch.rand(B, device=dev) * 0.9 + 0.05
+        tok, _, kept = sv.spec_sample_filtered(logits, u, T, top_p=p)
+        value, order = torch.sort(logits.double(), dim=-1, descending=True, stable=True)
+        w = torch.exp((value - value[:, :1]) / T.double()[:, None])
+        mass = torch.cumsum(w, -1)
+        n = (mass - w < p.double()[:, None] * mass[:, -1:]).sum(-1)
+        end = mass.gather(1, n[:, None] - 1)
+        r = (mass <= u.double()[:, None] * end).sum(-1)
+        assert torch.equal(kept.long(), n) and torch.equal(tok.long(), order.gather(1, r[:, None])[:, 0])
+
+
+def test_a_capture_may_be_the_first_call():
+    code = ("import torch, speculative_decoding_verification_04_gb300 as sv\n"
+            "x = torch.randn(2, 9000, device='cuda'); T = torch.ones(2, device='cuda'); u = torch.full((2,), 0.5, device='cuda')\n"
+            "p = torch.full((2,), 0.9, device='cuda')\n"
+            "g = torch.cuda.CUDAGraph()\n"
+            "with torch.cuda.graph(g):\n    a = sv.spec_sample_filtered(x, u, T, top_p=p)\n"
+            "g.replay(); torch.cuda.synchronize()\n"
+            "b = sv.spec_sample_filtered(x, u, T, top_p=p)\n"
+            "assert all(torch.equal(i, j) for i, j in zip(a, b))\n")
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=120)
+
+
 def test_greedy_rows_read_no_uniform_and_no_filter_value(dev):
     logits, u = rows(2, 3001, "bf16", dev, 12)
     u[:] = float("nan")
