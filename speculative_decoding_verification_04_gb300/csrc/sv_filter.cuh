@@ -46,6 +46,7 @@ constexpr int kBinsEach = kBins / kFilterThreads;
 constexpr int kLevelsSide = 4097;   // bf16 magnitudes: 2^-24 (and below) to 2^8 one by one, from 2^8
 constexpr int kLevels = 2 * kLevelsSide;
 constexpr int kLevelsEach = 4096 * 2 / kFilterThreads;
+constexpr int kTailLeast = 40000;  // logits a CTA for the bins to leave a tail out
 constexpr int kFewKept = 512;      // kept tokens that are all listed
 constexpr uint32_t kCarryBits = 12;   // of a bin's upper word; its count above (V < 2^20)
 
@@ -1156,11 +1157,17 @@ __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to,
 {
     constexpr int E = Elem<T>::E;
     const float m = s.scale.m;
-    const float low = bin_floor(to, m, b), top = from > 0 ? bin_floor(from - 1, m, b) : INFINITY;        // [low, top)
-    const float low2 = bin_floor(also, m, b), top2 = also > 0 ? bin_floor(also - 1, m, b) : INFINITY;
+    // [low, top) and [low2, top2), the four borders at once
+    float border = 0.0f;
+    const int lane = threadIdx.x & 31, of = lane == 0 ? to : lane == 1 ? from - 1 : lane == 2 ? also : also - 1;
+    if (lane < 4)
+        border = of < 0 ? INFINITY : bin_floor(of, m, b);
+    const float low = fmaxf(__shfl_sync(kFull, border, 0), value_of(end.key)), top = __shfl_sync(kFull, border, 1);
+    const float low2 = fmaxf(__shfl_sync(kFull, border, 2), value_of(end.key)), top2 = __shfl_sync(kFull, border, 3);
     const float least = value_of(end.key);
+    const bool both = also < from || also > to, ties = end.index != INT_MAX;
     auto in = [&](float x, int i) {
-        return ((x >= low && x < top) || (x >= low2 && x < top2)) && (x > least || (x == least && i <= end.index));
+        return ((x >= low && x < top) || (both && x >= low2 && x < top2)) && (x > least || (x == least && i <= end.index));
     };
     gather(row, s, C, [&](const uint4& w, int i) {
         float x[E];
@@ -1168,7 +1175,16 @@ __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to,
         uint32_t marks = 0;
 #pragma unroll
         for (int j = 0; j < E; ++j)
-            marks |= in(x[j], row.head + i * E + j) ? 1u << j : 0u;
+            marks |= x[j] >= low && x[j] < top ? 1u << j : 0u;
+        if (both)
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                marks |= x[j] >= low2 && x[j] < top2 ? 1u << j : 0u;
+        if (ties && marks)
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (!in(x[j], row.head + i * E + j))
+                    marks &= ~(1u << j);
         return marks;
     });
     const int lone = row.lone();
@@ -1183,7 +1199,8 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
     const int C = a.C, t = threadIdx.x;
     T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * a.V);
     int k = g.k;
-    bool tail = k == 0 && g.min_p == 0.0f;
+    // (a small part of a row is through the bins before an eighth of it has been looked at)
+    bool tail = k == 0 && g.min_p == 0.0f && a.V / C > kTailLeast;
     for (;;) {
         u128 rest;
         int gone;
