@@ -37,15 +37,14 @@ sv_status check_rows(const void* logits, sv_dtype dtype, const float* temperatur
     return SV_OK;
 }
 
-// CTAs a row is spread over: two on every SM while the rows alone are fewer (four
-// for parts of more than 256 KB), 16 KB or more each.  Rows of 128256 bf16 drawn
-// with top-k 50: one row 16.0 us by 8 CTAs, 16.7 by 4, 18.1 by 16; 64 rows 20.1 us
-// by 4, 22.9 by one; 400 rows 45 us by one, 57 by 2.  256 rows of 151936 fp32, top-p
-// alone: 212 us by 2, 239 by one, 242 by 4.
+// CTAs a row is spread over: one for each SM at most while the rows alone are
+// fewer, 56 KB or more each.  One row of 128256 bf16 with top-k 50: 16.0 us by 4
+// CTAs, 18.0 by one; 37 rows of 50257 bf16, top-p alone: 36 us by one, 43 by 2; 145
+// rows of 32003 fp32: 57 us by one, 61 by 2; 256 rows of 151936 fp32: 174 and 233.
 int row_ctas(long long rows, long long row_bytes, int nsm)
 {
     int C = 1;
-    while (C < 8 && rows * 2 * C <= (row_bytes / C > (256 << 10) ? 4 : 2) * (long long)nsm && row_bytes / C >= (32 << 10))
+    while (C < 8 && rows * 2 * C <= nsm && row_bytes / C >= (112 << 10))
         C *= 2;
     return C;
 }

@@ -31,13 +31,13 @@ struct FilterArgs {
 };
 
 
-constexpr int kFilterThreads = 256;
+constexpr int kFilterThreads = 512;
 constexpr int kFilterWarps = kFilterThreads / 32;
 constexpr int kClusterMost = 16;
 constexpr int kGroup = 8;          // vectors of a thread whose maximum is kept
-constexpr int kGroupsMost = 49;    // sv_max_vocab on one CTA
+constexpr int kGroupsMost = 25;    // sv_max_vocab on one CTA
 constexpr int kList = 2048;        // tokens sorted at a time
-constexpr int kTake = 16;          // logits of a thread summed at a time
+constexpr int kTake = 8 * (512 / kFilterThreads);          // logits of a thread summed at a time
 constexpr int kQueue = 63 + 32 * kTake + 1;   // a warp's logits on their way to the bins
 constexpr int kBins = 4096;
 constexpr int kBinShift = 6;       // 64 bins an octave of weights or more,
@@ -1466,7 +1466,7 @@ __device__ __noinline__ LevelPart scan_levels(FilterShared& s, u128& mass, int& 
     LevelPart q;
     const int t = threadIdx.x, lane = t & 31;
     q.scale = level_scale(s, t);
-    uint64_t part = 0, f = power62(q.scale.ratio, lane);
+    uint64_t part = 0, f = power62(q.scale.ratio, lane & (kLevelsEach - 1));
     q.n_own = 0;
 #pragma unroll 4
     for (int j = 0; j < kLevelsEach; ++j) {   // (each lane from another value on: other banks)
@@ -1514,7 +1514,7 @@ template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const Leve
     const int lane = threadIdx.x & 31;
     const LevelScale l{s.found64, s.found_ratio};
     const uint64_t f = power62(l.ratio, lane);
-    const int n_own = (int)level_count(s, s.found, lane);
+    const int n_own = lane < kLevelsEach ? (int)level_count(s, s.found, lane) : 0;
     uint64_t x = n_own * (f >> 24);
     const uint64_t own = x;
     int n = n_own;
@@ -1831,7 +1831,7 @@ __device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const Ro
 }
 
 template <typename T, bool DRAW>
-__global__ void __launch_bounds__(kFilterThreads, 4) sv_filter_kernel(FilterArgs a)
+__global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filter_kernel(FilterArgs a)
 {
     extern __shared__ __align__(16) unsigned char filter_smem[];
     FilterShared& s = *reinterpret_cast<FilterShared*>(filter_smem);
