@@ -12,7 +12,7 @@ namespace sv {
 namespace {
 
 constexpr int kClusterMost = 8;
-constexpr int kBlocksMost = 304;
+constexpr int kBlocksMost = 152;
 
 sv_status check_pool(const sv_kv_pool* p, const int32_t* kv_len, int32_t* held_out, int32_t* free_count_out, uint32_t* errors,
                      PoolArgs* a)
@@ -45,8 +45,8 @@ sv_status check_pool(const sv_kv_pool* p, const int32_t* kv_len, int32_t* held_o
     return SV_OK;
 }
 
-// One cluster while `items` (pages and slots) are few, else up to two blocks
-// an SM, with the in-place updates in a launch of their own.
+// One cluster while `items` (pages and slots) are few, else up to a block an SM,
+// with the in-place updates in a launch of their own.
 template <typename K> sv_status launch_pages(K kernel, PoolArgs a, long long items, cudaStream_t st)
 {
     const long long per = 4 * kPageThreads;

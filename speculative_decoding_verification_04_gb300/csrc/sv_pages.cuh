@@ -14,7 +14,7 @@
 
 namespace sv {
 
-constexpr int kPageThreads = 512;          // and sequences worked on at a time
+constexpr int kPageThreads = 1024;         // and sequences worked on at a time
 constexpr uint32_t kErrPages = 8u;         // bit 3: the stack holds too few pages
 
 struct PoolArgs {
@@ -43,7 +43,6 @@ struct PageShared {
     int len[kPageThreads], held[kPageThreads], count[kPageThreads];   // count: new tokens, -1: none granted
     int first[kPageThreads + 1];          // packed rows
     long long part[kPageThreads / 32];
-    int bad;
 };
 
 // Exclusive prefix sum over the block; `total` gets the whole.
@@ -96,32 +95,47 @@ __device__ __forceinline__ int pages_for(long long positions, int shift)
     return (int)((positions + (1 << shift) - 1) >> shift);
 }
 
+// What sequence b asks for (count 0 past the last one).
+struct Request {
+    int len, held, count, first;
+};
+
+__device__ __forceinline__ Request load_request(const PoolArgs& a, int b)
+{
+    Request q{0, 0, 0, 0};
+    if (b < a.B) {
+        q.len = a.kv_len[b];
+        q.held = a.held[b];
+        q.count = a.has_n ? a.n_new[b] : a.S;
+        if (a.packed) {
+            q.first = a.row_start[b];
+            q.count = a.row_start[b + 1] - q.first;
+        }
+    }
+    return q;
+}
+
 __global__ void __launch_bounds__(kPageThreads) sv_reserve_kernel(PoolArgs a)
 {
     __shared__ PageShared s;
     const int t = threadIdx.x;
     const unsigned nthr = gridDim.x * kPageThreads, me = blockIdx.x * kPageThreads + t;
     const bool first_block = blockIdx.x == 0;
+    // the loads that need no other's result, before anything waits: what is left is
+    // the chain length, page, slot
+    Request q = load_request(a, t);
     const int avail = *a.free_count;
+    const int row0 = a.packed ? a.row_start[0] : 0, row1 = a.packed ? a.row_start[a.B] : 0;
     uint32_t err = 0;
-    if (t == 0)
-        s.bad = avail < 0 || avail > a.capacity;
-    __syncthreads();
-    if (a.packed) {   // starts that do not ascend: no row could be told whose it is
-        bool bad = false;
-        for (int b = t; b < a.B; b += kPageThreads)
+    bool bad = avail < 0 || avail > a.capacity || (a.packed && (row0 < 0 || row1 > a.rows || q.count < 0));
+    if (a.packed)   // starts that do not ascend: no row could be told whose it is
+        for (int b = t + kPageThreads; b < a.B; b += kPageThreads)
             bad |= a.row_start[b] > a.row_start[b + 1];
-        if (t == 0)
-            bad |= a.row_start[0] < 0 || a.row_start[a.B] > a.rows;
-        if (bad)
-            s.bad = 1;
-    }
-    __syncthreads();
-    const bool all_bad = s.bad != 0;
+    const bool all_bad = __syncthreads_or(bad) != 0;
     if (all_bad)
         err |= kErrCache;
     if (a.work && a.has_slots && a.packed) {   // rows of no sequence
-        const int lo = all_bad ? a.rows : a.row_start[0], hi = all_bad ? a.rows : a.row_start[a.B];
+        const int lo = all_bad ? a.rows : row0, hi = all_bad ? a.rows : row1;
         for (int r = me; r < lo; r += nthr)
             a.slots[r] = -1;
         for (int r = hi + me; r < a.rows; r += nthr)
@@ -130,17 +144,15 @@ __global__ void __launch_bounds__(kPageThreads) sv_reserve_kernel(PoolArgs a)
     long long asked = 0, took = 0;   // by the sequences before this chunk
     for (int b0 = 0; b0 < a.B; b0 += kPageThreads) {
         const int b = b0 + t, nb = min(kPageThreads, a.B - b0);
-        int len = 0, held = 0, count = -1;
+        if (b0 > 0)
+            q = load_request(a, b);
+        const int len = q.len, held = q.held, count = q.count;
         long long want = 0;
         bool ok = false;
         if (t < nb) {
-            len = a.kv_len[b];
-            held = a.held[b];
-            const int f = a.packed ? a.row_start[b] : 0;
-            count = a.packed ? a.row_start[b + 1] - f : a.has_n ? a.n_new[b] : a.S;
-            s.first[t] = f;
+            s.first[t] = q.first;
             if (a.packed && t == nb - 1)
-                s.first[nb] = f + count;
+                s.first[nb] = q.first + count;
             ok = !all_bad && len >= 0 && count >= 0 && (a.packed || count <= a.S) && held >= 0 && held <= a.max_pages &&
                  (long long)len + count <= ((long long)a.max_pages << a.page_shift);
             if (ok)
@@ -224,11 +236,12 @@ __global__ void __launch_bounds__(kPageThreads) sv_reserve_kernel(PoolArgs a)
                 }
             }
         }
-        // the granted requests are the first of them: all that end within the stack
-        long long chunk_took;
-        block_scan(granted ? want : 0, s, chunk_took);
+        if (a.update && first_block) {
+            long long chunk_took;
+            block_scan(granted ? want : 0, s, chunk_took);
+            took += chunk_took;
+        }
         asked += total;
-        took += chunk_took;
         __syncthreads();
     }
     if (a.update && first_block && t == 0)
@@ -252,6 +265,7 @@ __global__ void __launch_bounds__(kPageThreads) sv_release_kernel(PoolArgs a)
         return len < 0 || held < 0 || held > a.max_pages || keep > held ? -1 : held - keep;
     };
     long long mine = 0, all;
+#pragma unroll 4
     for (int b = t; b < a.B; b += kPageThreads) {
         int keep;
         mine += max(0, spare(b, keep));
