@@ -44,7 +44,7 @@ sv_status check_rows(const void* logits, sv_dtype dtype, const float* temperatur
 int row_ctas(long long rows, long long row_bytes, int nsm)
 {
     int C = 1;
-    while (C < 8 && rows * 2 * C <= nsm && row_bytes / C >= (112 << 10))
+    while (C < kClusterMost && rows * 2 * C <= nsm && row_bytes / C >= (112 << 10))
         C *= 2;
     return C;
 }
@@ -57,11 +57,9 @@ template <typename T, bool DRAW> cudaError_t launch(FilterArgs& a, cudaStream_t 
         e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    static std::atomic<unsigned long long> ready{0};   // devices whose limits have been raised
+    static std::atomic<unsigned long long> ready{0};   // devices whose limit has been raised
     if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
         e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)filter_smem_bytes(kGroupsMost));
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess)
             return e;
         if (dev < 64)
