@@ -57,16 +57,12 @@ constexpr int kClusterMost = 8;
 constexpr int kGroup = 8;          // vectors of a thread whose maximum is kept
 constexpr int kGroupsMost = 25;    // sv_max_vocab on one CTA
 constexpr int kList = 2048;        // tokens sorted at a time
-constexpr int kTake = 8;           // logits of a thread summed at a time
-constexpr int kQueue = 63 + 32 * kTake + 1;   // a warp's logits on their way to the bins
 constexpr int kBins = 4096;
-constexpr int kBinShift = 6;       // 64 bins an octave of weights or more,
-constexpr int kBinShiftMost = 9;   // up to 512
+constexpr int kBinShift = 6;       // 64 bins an octave of weights
 constexpr int kBinsEach = kBins / kFilterThreads;
 constexpr int kLevelsSide = 4097;   // bf16 magnitudes: 2^-24 (and below) to 2^8 one by one, from 2^8
 constexpr int kLevels = 2 * kLevelsSide;
 constexpr int kLevelsEach = 4096 * 2 / kFilterThreads;
-constexpr int kTailLeast = 40000;  // logits a CTA for the bins to leave a tail out
 constexpr int kFewKept = 512;      // kept tokens that are all listed
 constexpr uint32_t kCarryBits = 12;   // of a bin's upper word; its count above (V < 2^20)
 
@@ -76,33 +72,26 @@ enum : int { kCmdEnd = 0, kCmdGather = 1, kCmdWrite = 2, kCmdRecount = 3 };
 struct alignas(16) Command {
     int op;
     int from, to, also;    // kCmdGather: bins from .. to, and bin `also`
-    uint32_t key;          // kCmdWrite, kCmdRecount: the kept prefix's last token
+    uint32_t key;          // kCmdWrite: the kept prefix's last token; kCmdRecount: top-k's
     int index;
-    int top_k;             // kCmdRecount: the prefix is top-k's
+    int pad;
     float value;           // kCmdGather of bf16 levels: the logit
 };
 
 struct FilterShared {
-    union {
-        struct {
-            alignas(16) uint64_t list[kList];
-            uint16_t hit[kList];
-        };
-        float queue[kFilterWarps][kQueue];
-    };
+    alignas(16) uint64_t list[kList];
+    uint16_t hit[kList];
     uint64_t roots[64];
     u128 part[kFilterWarps];
     u128 found_mass;
     RowScale scale;
     uint64_t part64[kFilterWarps], found64, found_ratio;
-    uint32_t steps[kBinsEach];   // 2^31 times 2^(-j 2^-shift)
+    uint32_t steps[kBinsEach];   // 2^31 times 2^(-j / 64)
     Command cmd;
     uint32_t warp_top[kFilterWarps], warp_low[kFilterWarps];
     int warp_count[2][kFilterWarps];
     uint32_t peer_top[kClusterMost], peer_bound[kClusterMost];   // what each CTA of the cluster found
-    int peer_cutoff[kClusterMost];
-    u128 peer_tail[kClusterMost];
-    int peer_gone[kClusterMost];
+    int peer_kept[kClusterMost];
     uint32_t least_key;    // min-p's border
     int count;             // rank 0: entries of the list
     int hits;              // groups that hold a candidate
@@ -757,37 +746,36 @@ __device__ __noinline__ int list_reaching(FilterShared& s, int lo, int hi, uint6
 // ---------------------------------------------------------------------------
 // Any number of candidates: bins of weight
 // ---------------------------------------------------------------------------
-// A bin holds the tokens whose l log2(e) / T rounds to the same multiple of
-// 2^-shift; it sums 2^f - 1 of the remainders f, in units of 2^-(23 + shift), and
-// counts.  Bin 0 holds the largest logit.  The last bin holds whatever weighs
-// less than the bins reach too; its mass does not count.  Weights are relative
-// to a bin's width above bin 0's centre.
+// A bin holds the tokens whose l log2(e) / T rounds to the same 64th; it sums
+// 2^f - 1 of the remainders f, in units of 2^-29, and counts.  Bin 0 holds the
+// largest logit.  The last bin holds whatever weighs less than 2^-63 too; its
+// mass does not count.  Weights are relative to a bin's width above bin 0's centre.
+// (Bins for the tokens near the border alone, found from an eighth of the row, the
+// rest summed on the way: 174 us where this takes 159, 256 rows of 151936.)
+constexpr float kBinStep = 0.015625f;
+constexpr float kBinMagic = 196608.0f;   // 1.5 * 2^23 steps: adding it rounds to steps
+
 struct BinScale {
     float ch, cl, least;   // least: logits below it count as it
-    float step, magic;     // 2^-shift; adding magic (1.5 * 2^23 steps) rounds to steps
     float unit;            // the centre of the bin before the first, in octaves
     uint32_t ref;          // the bits of the largest logit's rounded product
-    int shift;
 };
 
-__device__ __forceinline__ BinScale bin_scale(const RowScale& sc, int shift)
+__device__ __forceinline__ BinScale bin_scale(const RowScale& sc)
 {
     BinScale b;
     b.ch = sc.ch;
     b.cl = sc.cl;
-    b.shift = shift;
-    b.step = __int_as_float((127 - shift) << 23);
-    b.magic = 12582912.0f * b.step;
-    const float at = __fadd_rn(__fmul_rn(sc.m, sc.ch), b.magic);
+    const float at = __fadd_rn(__fmul_rn(sc.m, sc.ch), kBinMagic);
     b.ref = __float_as_uint(at);
-    b.unit = (at - b.magic) + b.step;
+    b.unit = (at - kBinMagic) + kBinStep;
     b.least = fmaxf(sc.m - 44.6f * sc.T, -3.4028234e38f);   // 64.3 octaves: no weight
     return b;
 }
 
 __device__ __forceinline__ int bin_of(float l, const BinScale& b)
 {
-    const uint32_t x = b.ref - __float_as_uint(__fadd_rn(__fmul_rn(fmaxf(l, b.least), b.ch), b.magic));
+    const uint32_t x = b.ref - __float_as_uint(__fadd_rn(__fmul_rn(fmaxf(l, b.least), b.ch), kBinMagic));
     return (int)min(x, (uint32_t)kBins - 1);
 }
 
@@ -807,15 +795,15 @@ __device__ __forceinline__ void bin_add(FilterShared& s, uint32_t i, uint32_t q,
 // Two tokens of at least b.least, the packed pair L; `in` says which of them count.
 __device__ __forceinline__ void bin_pair(FilterShared& s, uint64_t L, bool in0, bool in1, const BinScale& b)
 {
-    const uint64_t magic = f2_pack(b.magic, b.magic), nt = f2_mul(L, f2_pack(-b.ch, -b.ch));
+    const uint64_t magic = f2_pack(kBinMagic, kBinMagic), nt = f2_mul(L, f2_pack(-b.ch, -b.ch));
     const uint64_t e = f2_fma(L, f2_pack(b.cl, b.cl), f2_fma(L, f2_pack(b.ch, b.ch), nt));
     const uint64_t at = f2_sub(magic, nt);
     const uint64_t f = f2_sub(e, f2_add(nt, f2_sub(at, magic)));
     // 2^f - 1, |f| < 2^-7 + 2^-11: ln 2 f + (ln 2 f)^2 / 2 + (ln 2 f)^3 / 6, the next term below
-    // 2^-35; adding one and a half steps rounds it to steps 2^-23
+    // 2^-35; adding one and a half steps rounds it to 2^-29
     const uint64_t g = f2_fma(f, f2_fma(f, f2_pack(0.05550411f, 0.05550411f), f2_pack(0.24022651f, 0.24022651f)), f2_pack(0.69314718f, 0.69314718f));
-    const uint64_t q = f2_fma(f, g, f2_pack(1.5f * b.step, 1.5f * b.step));
-    const uint32_t unit = __float_as_uint(b.step);   // q's bits less these are (2^f - 1) / step 2^23 + 2^22
+    const uint64_t q = f2_fma(f, g, f2_pack(1.5f * kBinStep, 1.5f * kBinStep));
+    const uint32_t unit = 0x3c800000u;   // one step: q's bits less these are (2^f - 1) 2^29 + 2^22
     bin_add(s, min(b.ref - (uint32_t)at, (uint32_t)kBins - 1), (uint32_t)q - unit, in0);
     bin_add(s, min(b.ref - (uint32_t)(at >> 32), (uint32_t)kBins - 1), (uint32_t)(q >> 32) - unit, in1);
 }
@@ -823,22 +811,22 @@ __device__ __forceinline__ void bin_pair(FilterShared& s, uint64_t L, bool in0, 
 __device__ __forceinline__ uint32_t bin_count(const FilterShared& s, int i) { return s.bin.hi[i] >> kCarryBits; }
 
 // Bin i's share of its thread's bins: the sum of its weights over the weight of
-// the thread's first bin's centre, in units of 2^-(23 + shift).
-__device__ __forceinline__ uint64_t bin_part(const FilterShared& s, int i, int shift)
+// the thread's first bin's centre, in units of 2^-29.
+__device__ __forceinline__ uint64_t bin_part(const FilterShared& s, int i)
 {
     const uint32_t hi = s.bin.hi[i], n = hi >> kCarryBits;
-    const uint64_t sum = (((uint64_t)(hi & ((1u << kCarryBits) - 1)) << 32) | s.bin.lo[i]) + ((uint64_t)n << (23 + shift)) - ((uint64_t)n << 22);
+    const uint64_t sum = (((uint64_t)(hi & ((1u << kCarryBits) - 1)) << 32) | s.bin.lo[i]) + ((uint64_t)n << 29) - ((uint64_t)n << 22);
     const uint64_t f = i == kBins - 1 ? 0 : s.steps[i % kBinsEach];
     return ((sum & 0xffffffffu) * f >> 31) + ((sum >> 32) * f << 1);
 }
 
 // The weight that multiplies the parts of thread t's bins.
-__device__ __forceinline__ uint64_t part_weight(const FilterShared& s, int t, int shift)
+__device__ __forceinline__ uint64_t part_weight(const FilterShared& s, int t)
 {
-    return exp2_neg((uint64_t)(t * kBinsEach + 1) << (48 - shift), s.roots);
+    return exp2_neg((uint64_t)(t * kBinsEach + 1) << (48 - kBinShift), s.roots);
 }
 
-__device__ __forceinline__ u128 part_mass(uint64_t part, uint64_t weight, int shift) { return ((u128)part * weight) >> (23 + shift); }
+__device__ __forceinline__ u128 part_mass(uint64_t part, uint64_t weight) { return ((u128)part * weight) >> 29; }
 
 // A thread's bins (kBinsEach of them), and what is before them; masses in units of 2^-62.
 struct BinPart {
@@ -846,22 +834,22 @@ struct BinPart {
     int n_before, n_own;
 };
 
-__device__ __noinline__ BinPart scan_bins(FilterShared& s, int shift, u128& mass, int& count)
+__device__ __noinline__ BinPart scan_bins(FilterShared& s, u128& mass, int& count)
 {
     BinPart q;
     const int t = threadIdx.x;
     if (t < kBinsEach)
-        s.steps[t] = (uint32_t)(exp2_neg((uint64_t)t << (48 - shift), s.roots) >> 31);
+        s.steps[t] = (uint32_t)(exp2_neg((uint64_t)t << (48 - kBinShift), s.roots) >> 31);
     __syncthreads();
     uint64_t part = 0;
     q.n_own = 0;
 #pragma unroll 4
     for (int i = 0; i < kBinsEach; ++i) {
         const int j = t * kBinsEach + ((i + t) & (kBinsEach - 1));   // (lanes on different banks)
-        part += bin_part(s, j, shift);
+        part += bin_part(s, j);
         q.n_own += (int)bin_count(s, j);
     }
-    q.own = part ? part_mass(part, part_weight(s, t, shift), shift) : 0;
+    q.own = part ? part_mass(part, part_weight(s, t)) : 0;
     // the count in the low bits of one sum with the mass: masses are below 2^83
     u128 total;
     const u128 both = block_scan((q.own << 24) | (u128)(uint32_t)q.n_own, s, total);
@@ -872,9 +860,9 @@ __device__ __noinline__ BinPart scan_bins(FilterShared& s, int shift, u128& mass
     return q;
 }
 
-__device__ __forceinline__ u128 bin_mass(const FilterShared& s, int i, int shift)
+__device__ __forceinline__ u128 bin_mass(const FilterShared& s, int i)
 {
-    return part_mass(bin_part(s, i, shift), part_weight(s, i / kBinsEach, shift), shift);
+    return part_mass(bin_part(s, i), part_weight(s, i / kBinsEach));
 }
 
 // The bin where the running sum over all bins, of counts or of masses, reaches
@@ -884,7 +872,7 @@ struct BinAt {
     u128 before;
 };
 
-template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart& q, FilterShared& s, int shift, u128 goal)
+template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart& q, FilterShared& s, u128 goal)
 {
     __syncthreads();
     if (threadIdx.x == 0)
@@ -900,7 +888,7 @@ template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart&
     BinAt r{kBins, 0, 0};
     if (s.found >= 0) {   // every warp goes through that thread's bins, one a lane
         const int lane = threadIdx.x & 31, i = s.found * kBinsEach + (lane & (kBinsEach - 1));
-        const uint64_t weight = part_weight(s, s.found, shift), own = lane < kBinsEach ? bin_part(s, i, shift) : 0;
+        const uint64_t weight = part_weight(s, s.found), own = lane < kBinsEach ? bin_part(s, i) : 0;
         const int n_own = lane < kBinsEach ? (int)bin_count(s, i) : 0;
         uint64_t x = own;
         int n = n_own;
@@ -913,8 +901,8 @@ template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart&
                 n += z;
             }
         }
-        const u128 base = s.found_mass, from = base + part_mass(x - own, weight, shift);
-        const bool here = lane < kBinsEach && (kCount ? (u128)(uint32_t)(s.found_count + n) : base + part_mass(x, weight, shift)) >= goal;
+        const u128 base = s.found_mass, from = base + part_mass(x - own, weight);
+        const bool here = lane < kBinsEach && (kCount ? (u128)(uint32_t)(s.found_count + n) : base + part_mass(x, weight)) >= goal;
         const int l = __ffs(__ballot_sync(kFull, here)) - 1;
         r.bin = s.found * kBinsEach + l;
         r.before = ((u128)__shfl_sync(kFull, (unsigned long long)(from >> 64), l) << 64) | __shfl_sync(kFull, (unsigned long long)from, l);
@@ -966,14 +954,17 @@ __device__ __noinline__ void merge_bins(FilterShared& s, int rank, int C)
     }
 }
 
-// A CTA's part of the row into its bins: every eighth stretch of its vectors, or
-// all of them.
+// A CTA's part of the row, as far as it is in the prefix, into its bins.
 template <typename T>
-__device__ __noinline__ void bin_vectors(const RowSpan<T> row, int stride, Prefix end, const BinScale b, FilterShared& s)
+__device__ __noinline__ void fill_bins(const RowSpan<T> row, Prefix end, const BinScale b, FilterShared& s)
 {
     constexpr int E = Elem<T>::E;
+    __syncthreads();
+    for (int i = 4 * threadIdx.x; i < kBins; i += 4 * kFilterThreads)
+        *reinterpret_cast<uint4*>(&s.bin.lo[i]) = *reinterpret_cast<uint4*>(&s.bin.hi[i]) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
     const float least = value_of(end.key);
-    each_vector<true>(row.vec(), row.v0, row.v1, stride, [&](const uint4& w, int i, bool there) {
+    each_vector<true>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
         float x[E];
         Elem<T>::unpack(w, x);
         const int left = there ? end.index - (row.head + i * E) : -1;   // ties up to this one count
@@ -983,171 +974,11 @@ __device__ __noinline__ void bin_vectors(const RowSpan<T> row, int stride, Prefi
             bin_pair(s, f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least)), x[j] > above || (x[j] == above && j <= left),
                      x[j + 1] > above || (x[j + 1] == above && j + 1 <= left), b);
     });
-}
-
-// ex2.approx leans to one side: -5.07e-8 of its value on average over arguments
-// in [-30, 0] (measured; 1.3e-7 at most), which sums of many would keep.
-constexpr float kExp2Lean = 5.07e-8f;
-
-// The same with tokens below `from` summed on the way (fp32 weights, the sums
-// compensated) instead.  The others, fewer, go through the bins 64 of a warp at a
-// time: half of what the bins take for each logit is arithmetic that the others do
-// not need.  Returns this thread's sum; `gone` counts the logits of -inf.
-template <typename T>
-__device__ __noinline__ float tail_vectors(const RowSpan<T> row, float from, const BinScale b, FilterShared& s, int& gone)
-{
-    constexpr int E = Elem<T>::E, N = kTake / E;
-    const int t = threadIdx.x, lane = t & 31;
-    float* queue = s.queue[t >> 5];
-    const uint4* v = row.vec();
-    float sum = 0.0f, carry = 0.0f;
-    int waiting = 0, none = 0;
-    const uint64_t ch = f2_pack(b.ch, b.ch), cl = f2_pack(b.cl, b.cl), unit = f2_pack(-b.unit, -b.unit);
-    const uint32_t out = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-    Vectors<N> next;
-    next.load(v, row.v0 + t, row.v1, kFilterThreads, out);
-#pragma unroll 1
-    for (int i = row.v0 + t; i - t < row.v1; i += N * kFilterThreads) {
-        const Vectors<N> now = next;
-        const uint4(&w)[N] = now.w;
-        next.load(v, i + N * kFilterThreads, row.v1, kFilterThreads, out);
-        uint64_t add = 0;   // (+0, +0)
-        float low = INFINITY;
-        uint32_t in = 0;
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            float x[E];
-            Elem<T>::unpack(w[u], x);
-#pragma unroll
-            for (int j = 0; j < E; j += 2) {
-                const uint64_t L = f2_pack(fmaxf(x[j], b.least), fmaxf(x[j + 1], b.least));
-                const bool in0 = x[j] >= from, in1 = x[j + 1] >= from;
-                float w0, w1;
-                f2_unpack(f2_fma(L, cl, f2_fma(L, ch, unit)), w0, w1);
-                add = f2_add(add, f2_pack(in0 ? 0.0f : ex2_approx(w0), in1 ? 0.0f : ex2_approx(w1)));
-                in |= (in0 ? 1u << (u * E + j) : 0u) | (in1 ? 2u << (u * E + j) : 0u);
-                low = fminf(low, fminf(x[j], x[j + 1]));
-            }
-        }
-        float lo, hi, e;
-        f2_unpack(add, lo, hi);
-        two_sum(sum, lo + hi, sum, e);
-        carry += e;
-        if (low == -INFINITY)
-#pragma unroll
-            for (int u = 0; u < N; ++u) {
-                float x[E];
-                Elem<T>::unpack(w[u], x);
-                if (i + u * kFilterThreads < row.v1)
-#pragma unroll
-                    for (int j = 0; j < E; ++j)
-                        none += x[j] == -INFINITY;
-            }
-        __syncwarp();
-        // the lanes' logits one after the other
-        int upto = __popc(in);
-        int to = waiting - upto;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, upto, o);
-            if (lane >= o)
-                upto += y;
-        }
-        to += upto;
-        waiting += __shfl_sync(kFull, upto, 31);
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            float x[E];
-            Elem<T>::unpack(w[u], x);
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (in >> (u * E + j) & 1)
-                    queue[to++] = x[j];
-        }
-        __syncwarp();
-        if (waiting >= 64) {
-            int done = 0;
-#pragma unroll 1
-            for (; done + 64 <= waiting; done += 64)
-                bin_pair(s, f2_pack(queue[done + lane], queue[done + 32 + lane]), true, true, b);
-            const float left0 = queue[done + lane], left1 = queue[min(done + 32 + lane, kQueue - 1)];
-            __syncwarp();
-            queue[lane] = left0;
-            queue[lane + 32] = left1;
-            waiting -= done;
-            __syncwarp();
-        }
-    }
-    bin_pair(s, f2_pack(queue[lane], queue[lane + 32]), lane < waiting, lane + 32 < waiting, b);
-    gone = none;
-    return sum + fmaf(sum, kExp2Lean, carry);
-}
-
-__device__ __forceinline__ void clear_bins(FilterShared& s)
-{
-    __syncthreads();
-    for (int i = 4 * threadIdx.x; i < kBins; i += 4 * kFilterThreads)
-        *reinterpret_cast<uint4*>(&s.bin.lo[i]) = *reinterpret_cast<uint4*>(&s.bin.hi[i]) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-}
-
-// The sums of a CTA's part of the row.  With `tail` an eighth of it says first
-// where the row's mass reaches the share `target`, about; the bins then cover
-// the tokens around and above that place alone, in as fine steps as they can, and
-// the rest are summed on the way: a 64th of the mass at most, if the eighth was
-// right.  Returns the last bin that is complete, the mass that is in no bin, and
-// with `tail` how many logits are -inf; `b` is the bins' scale.
-template <typename T>
-__device__ __forceinline__ int fill_bins(const RowSpan<T>& row, float lone_x, Prefix end, bool tail, float target, int rank, int C,
-                                         FilterShared& s, BinScale& b, u128& rest, int& gone)
-{
-    const int t = threadIdx.x, lone = row.lone();
-    rest = 0;
-    gone = 0;
-    b = bin_scale(s.scale, kBinShift);
-    clear_bins(s);
-    bin_vectors(row, tail ? kGroup * kFilterThreads : kFilterThreads, end, b, s);
-    int cutoff = kBins - 1;
-    float from = value_of(end.key);
-    if (tail) {
-        __syncthreads();
-        u128 mass;
-        int count;
-        const BinPart part = scan_bins(s, kBinShift, mass, count);
-        if (mass > 0) {   // a quarter of what the sample leaves behind the target, a 64th of the mass at most
-            const u128 quarter = share_of(1.0f - target, mass, false) >> 2, beyond = quarter < mass >> 6 ? quarter : mass >> 6;
-            cutoff = min(kBins - 1, bin_reaching<false>(part, s, kBinShift, mass - beyond).bin + 8);
-        }
-        if (C > 1) {   // the furthest of the CTAs'
-            if (t < C)
-                st_rank(&s.peer_cutoff[rank], t, (uint32_t)cutoff);
-            row_sync(C);
-            for (int c = 0; c < C; ++c)
-                cutoff = max(cutoff, s.peer_cutoff[c]);
-        }
-        const float octaves = (float)(cutoff + 5) * b.step;
-        int shift = kBinShift;
-        while (shift < kBinShiftMost && (octaves + 0.05f) * (float)(2 << shift) <= (float)(kBins - 2))   // (the two units differ by up to 1.5 / 64)
-            ++shift;
-        const float border = fmaxf(from, (b.unit - octaves) / b.ch);
-        b = bin_scale(s.scale, shift);
-        cutoff = cutoff < kBins - 8 ? (cutoff + 1) << (shift - kBinShift) : kBins - 1;
-        from = border;
-        clear_bins(s);
-        float sum = tail_vectors(row, from, b, s, gone);
-        if (lone >= 0 && lone_x < from && lone_x >= b.least)
-            sum += ex2_approx(fmaf(lone_x, b.cl, fmaf(lone_x, b.ch, -b.unit)));
-        gone += lone >= 0 && lone_x == -INFINITY;
-        // units of 2^-62 from 2^-42 (the sum may reach 2^20), and the count below them
-        const u128 both = block_sum((u128)__float2ull_rn(sum * 4398046511104.0f) << 44 | (u128)(uint32_t)gone, s);
-        rest = both >> 24;
-        gone = (int)((uint32_t)both & 0xffffffu);
-    }
+    const int lone = row.lone();
     if (lone >= 0) {
-        const float x = fmaxf(lone_x, b.least);
-        bin_pair(s, f2_pack(x, x), end.has(key_of(lone_x), lone) && lone_x >= from, false, b);
+        const float x = (float)row.p[lone], y = fmaxf(x, b.least);
+        bin_pair(s, f2_pack(y, y), end.has(key_of(x), lone), false, b);
     }
-    return cutoff;
 }
 
 // The lowest logit of bin i or one before it: near where the bin's border should
@@ -1156,7 +987,7 @@ __device__ __noinline__ float bin_floor(int i, float m, const BinScale& b)
 {
     if (i >= kBins - 1)
         return -INFINITY;
-    const float at = (b.unit - ((float)i + 1.5f) * b.step) / b.ch, wide = 2.0f * b.step / b.ch;
+    const float at = (b.unit - ((float)i + 1.5f) * kBinStep) / b.ch, wide = 2.0f * kBinStep / b.ch;
     uint32_t lo = key_of(fmaxf(at - wide, -3.4028234e38f)), hi = key_of(fminf(at + wide, m));   // bin_of(lo) > i >= bin_of(hi)
     while (hi - lo > 1) {
         const uint32_t mid = lo + (hi - lo) / 2;
@@ -1211,28 +1042,18 @@ __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to,
 
 template <typename T, bool DRAW>
 __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const Settings& g, const RowSpan<T>& row, int rank, Prefix end,
-                                        float lone_x, FilterShared& s)
+                                        FilterShared& s)
 {
     const int C = a.C, t = threadIdx.x;
     T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * a.V);
     int k = g.k;
-    // (a small part of a row is through the bins before an eighth of it has been looked at)
-    bool tail = k == 0 && g.min_p == 0.0f && a.V / C > kTailLeast;
+    const BinScale bs = bin_scale(s.scale);
     for (;;) {
-        u128 rest;
-        int gone;
-        BinScale bs;
-        int complete = fill_bins(row, lone_x, end, tail, g.p < 1.0f ? g.p : g.u, rank, C, s, bs, rest, gone);
-        const int shift = bs.shift;
-        if (C > 1 && t == 0) {
-            st_rank(&s.peer_gone[rank], 0, (uint32_t)gone);
-            st_rank64(&s.peer_tail[rank], 0, (uint64_t)rest);
-            st_rank64(reinterpret_cast<uint64_t*>(&s.peer_tail[rank]) + 1, 0, (uint64_t)(rest >> 64));
-        }
+        fill_bins(row, end, bs, s);
         if (t == 0)   // the list's weights as the bins' masses (read behind the next barriers)
-            s.scale.top = ((long long)(int)(bs.ref - __float_as_uint(bs.magic)) + 1) * (1ll << (48 - shift));
+            s.scale.top = ((long long)(int)(bs.ref - __float_as_uint(kBinMagic)) + 1) * (1ll << (48 - kBinShift));
         merge_bins(s, rank, C);
-        bool again = false, c_top_k = false;
+        bool again = false;
         int stage = 0;   // rank 0's: what the gathered list is for
         int kept = 0, last = 0, lo_first = 0, n_last = 0;
         u128 above = 0, above_first = 0, total = 0, mass = 0;
@@ -1243,20 +1064,9 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                 bool give_up = false;
                 if (stage == 0) {
                     int n_all;
-                    if (C > 1) {
-                        rest = 0;
-                        gone = 0;
-                        for (int i = 0; i < C; ++i) {
-                            gone += s.peer_gone[i];
-                            rest += s.peer_tail[i];
-                        }
-                    }
-                    part = scan_bins(s, shift, total, n_all);
-                    total += rest;
-                    if (tail)
-                        n_all = a.V - gone;
+                    part = scan_bins(s, total, n_all);
                     if (k > 0 && k < n_all) {   // top-k first: its last token
-                        const BinAt at = bin_reaching<true>(part, s, shift, (u128)(uint32_t)k);
+                        const BinAt at = bin_reaching<true>(part, s, (u128)(uint32_t)k);
                         stage = 1;
                         kept = k - at.n_before;
                         c.op = kCmdGather;
@@ -1265,31 +1075,27 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                     } else if (g.p < 1.0f) {
                         stage = 2;
                         const u128 share = share_of(g.p, total, true), goal = share > 1 ? share : 1;
-                        const BinAt end_at = bin_reaching<false>(part, s, shift, goal);
+                        const BinAt end_at = bin_reaching<false>(part, s, goal);
                         last = end_at.bin;
                         above = above_first = end_at.before;
                         kept = end_at.n_before;
-                        if (last > complete) {
-                            c.op = kCmdRecount;   // the sample misled: all of it through the bins
-                        } else {
-                            n_last = (int)bin_count(s, last);
-                            give_up = n_last > kList;
-                            c.op = kCmdGather;
-                            c.from = c.to = c.also = last;
-                            if (DRAW && kept + n_last <= kFewKept) {   // all of them
-                                c.from = 0;
-                                above_first = 0;
-                            } else if (DRAW) {   // and the bins the draw is in, if the kept mass is the goal or little more
-                                const BinAt at = bin_reaching<false>(part, s, shift, share_of(g.u, goal, false) + 1);
-                                const int to = min(at.bin + 1, last);
-                                if (at.bin < last && (int)bin_count(s, at.bin) + (int)bin_count(s, to) + n_last <= kList) {
-                                    c.from = at.bin;
-                                    c.to = to;
-                                    above_first = at.before;
-                                }
+                        n_last = (int)bin_count(s, last);
+                        give_up = n_last > kList;
+                        c.op = kCmdGather;
+                        c.from = c.to = c.also = last;
+                        if (DRAW && kept + n_last <= kFewKept) {   // all of them
+                            c.from = 0;
+                            above_first = 0;
+                        } else if (DRAW) {   // and the bins the draw is in, if the kept mass is the goal or little more
+                            const BinAt at = bin_reaching<false>(part, s, share_of(g.u, goal, false) + 1);
+                            const int to = min(at.bin + 1, last);
+                            if (at.bin < last && (int)bin_count(s, at.bin) + (int)bin_count(s, to) + n_last <= kList) {
+                                c.from = at.bin;
+                                c.to = to;
+                                above_first = at.before;
                             }
-                            lo_first = c.from;
                         }
+                        lo_first = c.from;
                     } else if (!DRAW) {   // top-k reaches past the last token
                         if (t == 0)
                             put_row<DRAW>(a, r, n_all);
@@ -1299,20 +1105,12 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                     } else {
                         kept = n_all;
                         mass = total;
-                        const BinAt at = bin_reaching<false>(part, s, shift, share_of(g.u, total, false) + 1);
+                        const BinAt at = bin_reaching<false>(part, s, share_of(g.u, total, false) + 1);
                         stage = 4;
                         above_first = at.before;
-                        if (at.bin > complete) {
-                            c.op = kCmdRecount;
-                        } else {
-                            c.op = kCmdGather;
-                            c.from = c.to = c.also = at.bin;
-                            give_up = bin_count(s, at.bin) > kList;
-                        }
-                    }
-                    if (c.op == kCmdRecount) {
-                        c.key = end.key;
-                        c.index = end.index;
+                        c.op = kCmdGather;
+                        c.from = c.to = c.also = at.bin;
+                        give_up = bin_count(s, at.bin) > kList;
                     }
                 } else {
                     const int n = s.count;
@@ -1320,7 +1118,6 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                     if (stage == 1) {
                         const uint64_t e = s.list[kept - 1];
                         c.op = kCmdRecount;
-                        c.top_k = 1;
                         c.key = entry_key(e);
                         c.index = entry_index(e);
                     } else {
@@ -1336,7 +1133,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                             w = from + t < n ? list_weight(s, from + t) : 0;
                             const u128 own = (u128)list_mass(s, from, n, w) << 10;
                             // the goal again, with that bin's mass by its tokens
-                            const u128 goal = share_of(g.p, total - bin_mass(s, last, shift) + own, true);
+                            const u128 goal = share_of(g.p, total - bin_mass(s, last) + own, true);
                             const int end_r = list_reaching(s, from, n, w, after(goal, above), to);
                             mass = above + ((u128)to << 10);
                             kept += end_r - from + 1;
@@ -1367,7 +1164,7 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                             if (t == 0)
                                 put_row<DRAW>(a, r, kept, entry_index(s.list[at]), entry_weight(s, at), mass);
                         } else if (DRAW) {   // not in the bins that are here
-                            const BinAt b = bin_reaching<false>(part, s, shift, share_of(g.u, mass, false) + 1);
+                            const BinAt b = bin_reaching<false>(part, s, share_of(g.u, mass, false) + 1);
                             stage = 4;
                             above_first = b.before;
                             c.op = kCmdGather;
@@ -1402,23 +1199,19 @@ __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const 
                 break;
             }
             again = true;   // kCmdRecount
-            c_top_k = c.top_k;
             end = Prefix{c.key, c.index};
             break;
         }
         if (!again)
             return;
         row_sync(C);   // the bins and the command have been read
-        if (c_top_k) {
-            if (!DRAW && g.p >= 1.0f) {   // top-k was all there was
-                if (rank == 0 && t == 0)
-                    put_row<DRAW>(a, r, k);
-                write_row(row, out, a.same_phase, end);
-                return;
-            }
-            k = 0;
+        if (!DRAW && g.p >= 1.0f) {   // top-k was all there was
+            if (rank == 0 && t == 0)
+                put_row<DRAW>(a, r, k);
+            write_row(row, out, a.same_phase, end);
+            return;
         }
-        tail = false;
+        k = 0;
     }
 }
 
@@ -1831,13 +1624,13 @@ __device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const Ro
     if (C > 1) {
         if (t < C) {
             st_rank(&s.peer_top[rank], t, most);
-            st_rank(&s.peer_gone[rank], t, (uint32_t)own);
+            st_rank(&s.peer_kept[rank], t, (uint32_t)own);
         }
         row_sync(C);
         all = 0;
         for (int c = 0; c < C; ++c) {
             most = max(most, s.peer_top[c]);
-            all += s.peer_gone[c];
+            all += s.peer_kept[c];
         }
     }
     const bool usable = most > kKeyNegInf && most < kKeyPosInf;
@@ -1887,8 +1680,16 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
         s.hits = 0;
         s.first = INT_MAX;
     }
+    const int groups = (row.v1 - row.v0 + kGroup * kFilterThreads - 1) / (kGroup * kFilterThreads);
+    // How a top-k is bounded: by the threads' maxima, or with a larger share of them
+    // by the groups'; not where too many would pass.
+    const int share = (g.k + C - 1) / C;
+    const bool by_thread = share <= kFilterThreads / 2;
+    const bool bounded = !greedy && g.k > 0 && (by_thread || (share <= groups * (kFilterThreads / 2) && g.k <= kList / 2));
+    // bf16 rows where every token counts, or nearly: top-k 500 of 1024 rows of 128256
+    // is 165 us by the bound and 185 by levels, top-k 1000 258 and 185.
     if constexpr (sizeof(T) == 2)
-        if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : g.k > C * (kFilterThreads / 2)))
+        if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : share > kFilterThreads || !bounded))
             if (levels_row<DRAW>(a, r, g, row, rank, s))
                 return;
 
@@ -1903,7 +1704,6 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
 
     // 1. The maxima of the row, of each thread, and of each thread's groups of
     // vectors: the one pass that has to read everything from memory.
-    const int groups = (row.v1 - row.v0 + kGroup * kFilterThreads - 1) / (kGroup * kFilterThreads);
     float mine = -INFINITY;
     for (int n = 0; n < groups; ++n) {
         const int i0 = row.v0 + n * kGroup * kFilterThreads + t;
@@ -1954,10 +1754,7 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
 
     // 2. With top-k, a logit that at least k of the row reach: in each of C CTAs
     // the k / C-th (or a few after it) of the threads' or the groups' maxima, and
-    // the lowest of these.
-    const int share = (g.k + C - 1) / C;
-    const bool by_thread = share <= kFilterThreads / 2;
-    const bool bounded = !greedy && g.k > 0 && (by_thread || (share <= groups * (kFilterThreads / 2) && g.k <= kList / 2));
+    // the lowest of these.  (A k of which the row has no finite logits leaves them all.)
     uint32_t bound = 0;
     if (bounded && top_key < kKeyPosInf) {   // (a NaN or +inf: no token will come of it)
         uint32_t lo = by_thread ? low_key : 0, hi = top_key;
@@ -2142,12 +1939,12 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
         const int all = (int)block_sum((u128)(uint32_t)write_row(row, out, a.same_phase, end), s);
         if (C > 1) {
             if (t == 0)
-                st_rank(&s.peer_gone[rank], 0, (uint32_t)all);
+                st_rank(&s.peer_kept[rank], 0, (uint32_t)all);
             row_sync(C);
         }
         int total = all;
         for (int c = 1; c < C; ++c)
-            total += s.peer_gone[c];
+            total += s.peer_kept[c];
         if (rank == 0 && t == 0)
             put_row<DRAW>(a, r, total);
         return;
@@ -2159,7 +1956,7 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
             whole_row<T, DRAW>(a, r, g, m, end, s);
         return;
     }
-    binned_row<T, DRAW>(a, r, g, row, rank, end, lone_x, s);
+    binned_row<T, DRAW>(a, r, g, row, rank, end, s);
     row_sync(C);
 }
 
