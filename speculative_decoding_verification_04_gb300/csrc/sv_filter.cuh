@@ -78,6 +78,19 @@ struct alignas(16) Command {
     float value;           // kCmdGather of bf16 levels: the logit
 };
 
+// A value among whose tokens a running sum reaches a goal.
+struct LevelAt {
+    float value;
+    uint64_t weight;        // of one of its tokens, in units of 2^-62
+    int n, n_before;        // its tokens, and those before them
+    u128 before, mass;      // the mass before them, and theirs in the sums
+};
+
+struct BinAt {
+    int bin, n_before;     // a bin, and what is before it
+    u128 before;
+};
+
 struct FilterShared {
     alignas(16) uint64_t list[kList];
     uint16_t hit[kList];
@@ -85,6 +98,8 @@ struct FilterShared {
     u128 part[kFilterWarps];
     u128 found_mass;
     RowScale scale;
+    LevelAt level_at;
+    BinAt bin_at;
     uint64_t part64[kFilterWarps], found64, found_ratio;
     uint32_t steps[kBinsEach];   // 2^31 times 2^(-j / 64)
     Command cmd;
@@ -563,9 +578,9 @@ __device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShare
 }
 
 // The logits of a CTA's part that mark(vector, its place) marks (E bits), into
-// rank 0's list.
-template <typename T, typename M>
-__device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, int C, M&& mark)
+// rank 0's list.  kOneKey: all of them are the key `key`.
+template <bool kOneKey, typename T, typename M>
+__device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, int C, uint32_t key, M&& mark)
 {
     constexpr int E = Elem<T>::E;
     const int t = threadIdx.x;
@@ -581,7 +596,16 @@ __device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, i
             if (i + u * kFilterThreads < row.v1)
                 marks |= mark(now.w[u], i + u * kFilterThreads) << (u * E);
         __syncwarp();
-        append_marked(row, s, C, marks, now.w, [&](int u) { return i + u * kFilterThreads; });
+        if (!kOneKey) {
+            append_marked(row, s, C, marks, now.w, [&](int u) { return i + u * kFilterThreads; });
+        } else if (__any_sync(kFull, marks)) {
+            int at = list_room(s, C, __popc(marks));
+            for (; marks; marks &= marks - 1) {
+                const int bit = __ffs(marks) - 1;
+                list_put(s, C, at++, entry_of(key, row.head + (i + bit / E * kFilterThreads) * E + bit % E));
+            }
+            __syncwarp();
+        }
     }
 }
 
@@ -865,18 +889,41 @@ __device__ __forceinline__ u128 bin_mass(const FilterShared& s, int i)
     return part_mass(bin_part(s, i), part_weight(s, i / kBinsEach));
 }
 
-// The bin where the running sum over all bins, of counts or of masses, reaches
-// `goal` (kBins if it is not reached), and what is before it.
-struct BinAt {
-    int bin, n_before;
-    u128 before;
-};
+// Where in the bins of thread s.found: one warp, a bin a lane.
+template <bool kCount> __device__ __noinline__ void bin_within(FilterShared& s, u128 goal)
+{
+    const int lane = threadIdx.x, i = s.found * kBinsEach + (lane & (kBinsEach - 1));
+    const uint64_t weight = part_weight(s, s.found), own = lane < kBinsEach ? bin_part(s, i) : 0;
+    const int n_own = lane < kBinsEach ? (int)bin_count(s, i) : 0;
+    uint64_t x = own;
+    int n = n_own;
+#pragma unroll
+    for (int o = 1; o < kBinsEach; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(kFull, (unsigned long long)x, o);
+        const int z = __shfl_up_sync(kFull, n, o);
+        if (lane >= o) {
+            x += y;
+            n += z;
+        }
+    }
+    const u128 base = s.found_mass, from = base + part_mass(x - own, weight);
+    const bool here = lane < kBinsEach && (kCount ? (u128)(uint32_t)(s.found_count + n) : base + part_mass(x, weight)) >= goal;
+    const int l = max(0, __ffs(__ballot_sync(kFull, here)) - 1);
+    BinAt r;
+    r.bin = s.found * kBinsEach + l;
+    r.before = ((u128)__shfl_sync(kFull, (unsigned long long)(from >> 64), l) << 64) | __shfl_sync(kFull, (unsigned long long)from, l);
+    r.n_before = s.found_count + __shfl_sync(kFull, n - n_own, l);
+    if (lane == 0)
+        s.bin_at = r;
+}
 
+// The bin where the running sum over all bins, of counts or of masses, reaches
+// `goal` (which all of them do).
 template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart& q, FilterShared& s, u128 goal)
 {
     __syncthreads();
     if (threadIdx.x == 0)
-        s.found = -1;
+        s.found = 0;
     __syncthreads();
     const u128 c = kCount ? (u128)(uint32_t)q.n_before : q.before, v = kCount ? (u128)(uint32_t)q.n_own : q.own;
     if (c < goal && goal <= c + v) {
@@ -885,30 +932,10 @@ template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart&
         s.found_mass = q.before;
     }
     __syncthreads();
-    BinAt r{kBins, 0, 0};
-    if (s.found >= 0) {   // every warp goes through that thread's bins, one a lane
-        const int lane = threadIdx.x & 31, i = s.found * kBinsEach + (lane & (kBinsEach - 1));
-        const uint64_t weight = part_weight(s, s.found), own = lane < kBinsEach ? bin_part(s, i) : 0;
-        const int n_own = lane < kBinsEach ? (int)bin_count(s, i) : 0;
-        uint64_t x = own;
-        int n = n_own;
-#pragma unroll
-        for (int o = 1; o < kBinsEach; o <<= 1) {
-            const uint64_t y = __shfl_up_sync(kFull, (unsigned long long)x, o);
-            const int z = __shfl_up_sync(kFull, n, o);
-            if (lane >= o) {
-                x += y;
-                n += z;
-            }
-        }
-        const u128 base = s.found_mass, from = base + part_mass(x - own, weight);
-        const bool here = lane < kBinsEach && (kCount ? (u128)(uint32_t)(s.found_count + n) : base + part_mass(x, weight)) >= goal;
-        const int l = __ffs(__ballot_sync(kFull, here)) - 1;
-        r.bin = s.found * kBinsEach + l;
-        r.before = ((u128)__shfl_sync(kFull, (unsigned long long)(from >> 64), l) << 64) | __shfl_sync(kFull, (unsigned long long)from, l);
-        r.n_before = s.found_count + __shfl_sync(kFull, n - n_own, l);
-    }
-    return r;
+    if (threadIdx.x < 32)
+        bin_within<kCount>(s, goal);
+    __syncthreads();
+    return s.bin_at;
 }
 
 // What rank 0 asks for, behind a row_sync.
@@ -1017,7 +1044,7 @@ __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to,
     auto in = [&](float x, int i) {
         return ((x >= low && x < top) || (both && x >= low2 && x < top2)) && (x > least || (x == least && i <= end.index));
     };
-    gather(row, s, C, [&](const uint4& w, int i) {
+    gather<false>(row, s, C, 0, [&](const uint4& w, int i) {
         float x[E];
         Elem<T>::unpack(w, x);
         uint32_t marks = 0;
@@ -1296,32 +1323,10 @@ __device__ __noinline__ LevelPart scan_levels(FilterShared& s, u128& mass, int& 
     return q;
 }
 
-struct LevelAt {
-    float value;
-    uint64_t weight;        // of one of its tokens, in units of 2^-62
-    int n, n_before;        // its tokens, and those before them
-    u128 before, mass;      // the mass before them, and theirs in the sums
-};
-
-// The value among whose tokens the running count, or mass, reaches goal (which
-// the row does).
-template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const LevelPart& q, FilterShared& s, u128 goal)
+// Where in the values of thread s.found: one warp, a value a lane.
+template <bool kCount> __device__ __noinline__ void level_within(FilterShared& s, u128 goal)
 {
-    __syncthreads();
-    if (threadIdx.x == 0)
-        s.found = 0;
-    __syncthreads();
-    const u128 c = kCount ? (u128)(uint32_t)q.n_before : q.before, v = kCount ? (u128)(uint32_t)q.n_own : q.own;
-    if (c < goal && goal <= c + v) {
-        s.found = threadIdx.x;
-        s.found_count = q.n_before;
-        s.found_mass = q.before;
-        s.found64 = q.scale.first;
-        s.found_ratio = q.scale.ratio;
-    }
-    __syncthreads();
-    // every warp goes through that thread's values, one a lane
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x;
     const LevelScale l{s.found64, s.found_ratio};
     const uint64_t f = power62(l.ratio, lane);
     const int n_own = lane < kLevelsEach ? (int)level_count(s, s.found, lane) : 0;
@@ -1350,7 +1355,31 @@ template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const Leve
     r.before = ((u128)__shfl_sync(kFull, (unsigned long long)(from >> 64), i) << 64) | __shfl_sync(kFull, (unsigned long long)from, i);
     const u128 to = s.found_mass + level_mass(x, l.first) - from;
     r.mass = ((u128)__shfl_sync(kFull, (unsigned long long)(to >> 64), i) << 64) | __shfl_sync(kFull, (unsigned long long)to, i);
-    return r;
+    if (lane == 0)
+        s.level_at = r;
+}
+
+// The value among whose tokens the running count, or mass, reaches goal (which
+// the row does).
+template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const LevelPart& q, FilterShared& s, u128 goal)
+{
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s.found = 0;
+    __syncthreads();
+    const u128 c = kCount ? (u128)(uint32_t)q.n_before : q.before, v = kCount ? (u128)(uint32_t)q.n_own : q.own;
+    if (c < goal && goal <= c + v) {
+        s.found = threadIdx.x;
+        s.found_count = q.n_before;
+        s.found_mass = q.before;
+        s.found64 = q.scale.first;
+        s.found_ratio = q.scale.ratio;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32)
+        level_within<kCount>(s, goal);
+    __syncthreads();
+    return s.level_at;
 }
 
 // How many tokens of weight w (at least one, at most n) reach a mass.
@@ -1401,7 +1430,7 @@ __device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, Fil
 __device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, float value, int C, FilterShared& s)
 {
     const uint32_t both = (__float_as_uint(value) >> 16) * 0x10001u;
-    gather(row, s, C, [&](const uint4& w, int) {   // (no value here is a zero: equal logits are equal bits)
+    gather<true>(row, s, C, key_of(value), [&](const uint4& w, int) {   // (no value here is a zero: equal logits are equal bits)
         const uint32_t m = __vcmpeq2(w.x, both) & 0x00020001u, n = __vcmpeq2(w.y, both) & 0x00080004u;
         const uint32_t o = __vcmpeq2(w.z, both) & 0x00200010u, p = __vcmpeq2(w.w, both) & 0x00800040u;
         const uint32_t all = m | n | o | p;
