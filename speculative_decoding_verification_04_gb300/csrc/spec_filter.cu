@@ -38,19 +38,24 @@ sv_status check_rows(const void* logits, sv_dtype dtype, const float* temperatur
 }
 
 // CTAs a row is spread over: one for each SM at most while the rows alone are
-// fewer, 56 KB or more each.  One row of 128256 bf16 with top-k 50: 16.0 us by 4
-// CTAs, 18.0 by one; 37 rows of 50257 bf16, top-p alone: 36 us by one, 43 by 2; 145
-// rows of 32003 fp32: 57 us by one, 61 by 2; 256 rows of 151936 fp32: 174 and 233.
+// fewer, 56 KB or more each; of long rows half that each, once half the SMs do.
+// More and smaller parts read faster and then wait for one another more often.
+// Nine rows of 128256 bf16 filtered by top-k: 16.2 us by eight CTAs, 22.2 by four;
+// one row drawn by top-k 50: 8.5 by four, 11.4 by one; 16 rows of 151936 fp32, top-p
+// alone: 49 by eight, 76 by one; 37 rows of 50257 bf16, top-p: 21.2 by one, 25.4 by two;
+// 145 rows of 32003 fp32: 42 and 52; 256 rows of 151936 fp32: 141 and 177.
 int row_ctas(long long rows, long long row_bytes, int nsm)
 {
     int C = 1;
-    while (C < kClusterMost && rows * 2 * C <= nsm && row_bytes / C >= (112 << 10))
+    while (C < kClusterMost && ((rows * 2 * C <= nsm && row_bytes / C >= (112 << 10)) ||
+                                (C > 1 && rows * 4 * C <= nsm && row_bytes / C >= (56 << 10))))
         C *= 2;
     return C;
 }
 
 template <typename T, bool DRAW> cudaError_t launch(FilterArgs& a, cudaStream_t st)
 {
+    constexpr int NT = kThreadsOf<T>;
     int dev = 0, nsm = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
@@ -59,7 +64,7 @@ template <typename T, bool DRAW> cudaError_t launch(FilterArgs& a, cudaStream_t 
         return e;
     static std::atomic<unsigned long long> ready{0};   // devices whose limit has been raised
     if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
-        e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)filter_smem_bytes(kGroupsMost));
+        e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)filter_smem_bytes<NT>(kGroupsMost<NT>));
         if (e != cudaSuccess)
             return e;
         if (dev < 64)
@@ -67,11 +72,11 @@ template <typename T, bool DRAW> cudaError_t launch(FilterArgs& a, cudaStream_t 
     }
     const long long rows = (long long)a.B * a.S;
     a.C = row_ctas(rows, (long long)a.V * sizeof(T), nsm);
-    const int vectors = a.V / Elem<T>::E / a.C + 1, per = kGroup * kFilterThreads;
+    const int vectors = a.V / Elem<T>::E / a.C + 1, per = kGroup * NT;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(rows * a.C));
-    cfg.blockDim = dim3(kFilterThreads);
-    cfg.dynamicSmemBytes = filter_smem_bytes((vectors + per - 1) / per);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = filter_smem_bytes<NT>((vectors + per - 1) / per);
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;

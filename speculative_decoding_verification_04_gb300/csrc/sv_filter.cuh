@@ -8,19 +8,21 @@
 // where does a prefix reach a given count or mass?
 //
 // Four ways to the answer, by a row's settings:
-//  - a list (top-k up to 256 a CTA, min-p, short rows): the row's one pass from
-//    memory keeps the maxima of each thread and of its groups of eight vectors;
+//  - a list (top-k up to 128 or 256 a CTA, min-p, short rows): the row's one pass
+//    from memory keeps the maxima of each thread and of its groups of four vectors;
 //    the k-th largest of the threads' maxima bounds the k-th largest logit, the
 //    few groups above it are read again, and what passes is sorted and weighed.
-//    Bounded by the bytes for many rows: 1024 rows of 128256 bf16 draw in 86 us
-//    (3.1 TB/s, 0.46 of the copy rate), filtered rows write at 3.5 TB/s in all;
-//    by the chain of steps for one row (15 us).
+//    Bounded by the bytes for many rows: 1024 rows of 128256 bf16 draw in 60 us
+//    (4.4 TB/s, 0.66 of the copy rate), 900 are filtered in 86 (5.4 TB/s read and
+//    written, 0.80); by the chain of steps for one row (15 us).
 //  - levels (bf16 where every token counts): the one pass counts how often each
 //    of 8192 values occurs, an atomic a token; weights times counts are the sums.
-//    37 rows of 50257 draw in 25 us.
+//    1024 rows of 128256 draw in 134 us (2.0 TB/s): what bounds it is the atomics
+//    in shared memory, some ten cycles for each warp's.
 //  - bins (fp32 where every token counts): sums by weight, and the border's bins
-//    read once more.  256 rows of 151936 draw in 176 us (0.9 TB/s): what bounds it
-//    is the arithmetic and the shared-memory atomics of the sums.
+//    read once more.  256 rows of 151936 draw in 136 us (1.1 TB/s of the one pass
+//    that has to be): bounded by two atomics a token, the arithmetic of the
+//    remainders, and three sweeps of rows that L2 does not hold all of.
 //  - bisection, for what none of these settles.
 // All four compare whole numbers, so that they agree where they meet.
 #pragma once
@@ -47,22 +49,25 @@ struct FilterArgs {
     int same_phase;          // out's rows have the 16-byte phase of logits' rows
 };
 
-// 512 threads, two blocks an SM: what a row costs beside its bytes is a chain of
-// short steps (maxima, bound, candidates, sums, the crossing), and more threads a
-// row shorten most of them.  With 256 (four blocks) 256 rows of 151936 fp32 take
-// 190 us instead of 176, 900 filtered rows of 128256 bf16 131 instead of 104.
-constexpr int kFilterThreads = 512;
-constexpr int kFilterWarps = kFilterThreads / 32;
+// Threads a row: 256 for bf16 (three blocks an SM), 512 for fp32 (two).  What a row
+// costs beside its bytes is a chain of short steps (maxima, bound, candidates, sums,
+// the crossing), which more threads shorten and more rows at a time hide.  By 256 and
+// by 512: 1024 rows of 128256 bf16 with top-p 134 and 154 us, with top-k 50 64 and 70;
+// 256 rows of 151936 fp32 with top-p 139 and 136 us, 64 rows 68 and 58.  A fourth block
+// an SM leaves L1, through which the loads in flight pass, 28 KB: top-k 50 75 us, 900
+// filtered rows 118 for 92.
+template <typename T> constexpr int kThreadsOf = sizeof(T) == 2 ? 256 : 512;
+template <typename T> constexpr int kBlocksOf = sizeof(T) == 2 ? 3 : 2;
 constexpr int kClusterMost = 8;
-constexpr int kGroup = 8;          // vectors of a thread whose maximum is kept
-constexpr int kGroupsMost = 25;    // sv_max_vocab on one CTA
+constexpr int kGroup = 4;          // vectors of a thread whose maximum is kept (1024 rows, top-k 50: 60 us; by eights 64)
 constexpr int kList = 2048;        // tokens sorted at a time
 constexpr int kBins = 4096;
 constexpr int kBinShift = 6;       // 64 bins an octave of weights
-constexpr int kBinsEach = kBins / kFilterThreads;
+template <int NT> constexpr int kBinsEach = kBins / NT;
 constexpr int kLevelsSide = 4097;   // bf16 magnitudes: 2^-24 (and below) to 2^8 one by one, from 2^8
 constexpr int kLevels = 2 * kLevelsSide;
-constexpr int kLevelsEach = 4096 * 2 / kFilterThreads;
+template <int NT> constexpr int kLevelsEach = 4096 * 2 / NT;
+template <int NT> constexpr int kGroupsMost = 50 * 512 / NT;   // sv_max_vocab on one CTA
 constexpr int kFewKept = 512;      // kept tokens that are all listed
 constexpr uint32_t kCarryBits = 12;   // of a bin's upper word; its count above (V < 2^20)
 
@@ -91,20 +96,19 @@ struct BinAt {
     u128 before;
 };
 
-struct FilterShared {
+template <int NT> struct FilterShared {
     alignas(16) uint64_t list[kList];
-    uint16_t hit[kList];
     uint64_t roots[64];
-    u128 part[kFilterWarps];
+    u128 part[NT / 32];
     u128 found_mass;
     RowScale scale;
     LevelAt level_at;
     BinAt bin_at;
-    uint64_t part64[kFilterWarps], found64, found_ratio;
-    uint32_t steps[kBinsEach];   // 2^31 times 2^(-j / 64)
+    uint64_t part64[NT / 32], found64, found_ratio;
+    uint32_t steps[kBinsEach<NT>];   // 2^31 times 2^(-j / 64)
     Command cmd;
-    uint32_t warp_top[kFilterWarps], warp_low[kFilterWarps];
-    int warp_count[2][kFilterWarps];
+    uint32_t warp_top[NT / 32], warp_low[NT / 32];
+    int warp_count[2][NT / 32];
     uint32_t peer_top[kClusterMost], peer_bound[kClusterMost];   // what each CTA of the cluster found
     int peer_kept[kClusterMost];
     uint32_t least_key;    // min-p's border
@@ -112,35 +116,46 @@ struct FilterShared {
     int hits;              // groups that hold a candidate
     int first;             // lowest index of the largest logit
     int found, found_count;
-    // the maxima of each thread's groups (as many as the row has), then the bins
+    // the maxima of each thread's groups (as many as the row has) and behind them the
+    // groups that hold a candidate (`hit`, kList of them), then the bins
     union alignas(16) {
         struct {
             uint32_t lo[kBins], hi[kBins];
         } bin;
         uint32_t level[kLevels];
-        float group[kGroupsMost][kFilterThreads];
+        float group[kGroupsMost<NT>][NT];
     };
 };
 
 // Shared memory for rows of `groups` groups a CTA.
-constexpr size_t filter_smem_bytes(int groups)
+template <int NT> constexpr size_t filter_smem_bytes(int groups)
 {
-    const size_t g = (size_t)groups * kFilterThreads * 4, b = ((size_t)kLevels * 4 + 15) / 16 * 16;   // (more than the bins)
-    return sizeof(FilterShared) - sizeof(float) * kGroupsMost * kFilterThreads + (g > b ? g : b);
+    const size_t g = (size_t)groups * NT * 4 + kList * sizeof(uint16_t), b = ((size_t)kLevels * 4 + 15) / 16 * 16;   // (more than the bins)
+    return sizeof(FilterShared<NT>) - sizeof(float) * kGroupsMost<NT> * NT + (g > b ? g : b);
 }
 
 // ---------------------------------------------------------------------------
 // the row, the block and the cluster
 // ---------------------------------------------------------------------------
 
-// N of a thread's vectors, at i, i + stride, ...; `none` stands for those past the end.
+// A row's vector, past L1 (no use of it there: 1024 rows of 128256 bf16 with top-p
+// draw in 134 us, 140 by plain loads).  Not through the read-only path: the filtered
+// row may be written where the row is.
+__device__ __forceinline__ uint4 ld_row(const uint4* p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
+// N of a thread's vectors, at i, i + stride, ...; zeros for those past the end.
 template <int N> struct Vectors {
     uint4 w[N];
-    __device__ __forceinline__ void load(const uint4* v, int i, int end, int stride, uint32_t none = 0)
+    __device__ __forceinline__ void load(const uint4* v, int i, int end, int stride)
     {
 #pragma unroll
         for (int u = 0; u < N; ++u)
-            w[u] = i + u * stride < end ? v[i + u * stride] : make_uint4(none, none, none, none);
+            w[u] = i + u * stride < end ? ld_row(v + i + u * stride) : make_uint4(0, 0, 0, 0);
     }
 };
 
@@ -175,8 +190,7 @@ __device__ __forceinline__ void each_vector(const uint4* v, int first, int end, 
 }
 
 // A CTA's part of a row: a range of its 16-byte vectors, and for rank 0 the
-// elements before and after them.  Plain loads throughout: the filtered row may
-// be written where the row is.
+// elements before and after them.
 template <typename T> struct RowSpan {
     static constexpr int E = Elem<T>::E;
     const T* p;
@@ -200,7 +214,7 @@ template <typename T> struct RowSpan {
     // f(values, index of the first) for every vector.
     template <typename F> __device__ __forceinline__ void vectors(F&& f) const
     {
-        each_vector<true>(vec(), v0, v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
+        each_vector<true>(vec(), v0, v1, kThreadsOf<T>, [&](const uint4& w, int i, bool there) {
             float x[E];
             Elem<T>::unpack(w, x);
             if (there)
@@ -265,7 +279,7 @@ __device__ __forceinline__ u128 shfl_up128(u128 v, int o)
 }
 
 // Exclusive prefix sum over the block; `total` gets the whole.
-__device__ __noinline__ u128 block_scan(u128 v, FilterShared& s, u128& total)
+template <int NT> __device__ __noinline__ u128 block_scan(u128 v, FilterShared<NT>& s, u128& total)
 {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     u128 x = v;
@@ -281,7 +295,7 @@ __device__ __noinline__ u128 block_scan(u128 v, FilterShared& s, u128& total)
     __syncthreads();
     u128 before = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < kFilterWarps; ++i) {
+    for (int i = 0; i < NT / 32; ++i) {
         const u128 q = s.part[i];
         if (i < w)
             before += q;
@@ -291,7 +305,7 @@ __device__ __noinline__ u128 block_scan(u128 v, FilterShared& s, u128& total)
     return before + x - v;
 }
 
-__device__ __forceinline__ u128 block_sum(u128 v, FilterShared& s)
+template <int NT> __device__ __forceinline__ u128 block_sum(u128 v, FilterShared<NT>& s)
 {
     u128 t;
     block_scan(v, s, t);
@@ -312,8 +326,8 @@ struct Prefix {
 // ---------------------------------------------------------------------------
 
 // The sum over a prefix of 1 (kCount) or of the weights.
-template <bool kCount, typename T>
-__device__ u128 prefix_sum(const RowSpan<T>& row, Prefix p, FilterShared& s)
+template <bool kCount, typename T, int NT>
+__device__ u128 prefix_sum(const RowSpan<T>& row, Prefix p, FilterShared<NT>& s)
 {
     u128 a = 0;
     row.each([&](float x, int i) {
@@ -324,8 +338,8 @@ __device__ u128 prefix_sum(const RowSpan<T>& row, Prefix p, FilterShared& s)
 }
 
 // The shortest prefix within `most` that sums to `goal` (which `most` does).
-template <bool kCount, typename T>
-__device__ Prefix prefix_reaching(const RowSpan<T>& row, u128 goal, Prefix most, uint32_t top, FilterShared& s)
+template <bool kCount, typename T, int NT>
+__device__ Prefix prefix_reaching(const RowSpan<T>& row, u128 goal, Prefix most, uint32_t top, FilterShared<NT>& s)
 {
     uint32_t lo = most.key, hi = top;
     while (lo < hi) {
@@ -351,7 +365,7 @@ __device__ Prefix prefix_reaching(const RowSpan<T>& row, u128 goal, Prefix most,
 }
 
 // The index of the n-th logit (from 1) that equals x.
-template <typename T> __device__ __noinline__ int index_of_nth(const RowSpan<T>& row, float x, int n, FilterShared& s)
+template <typename T, int NT> __device__ __noinline__ int index_of_nth(const RowSpan<T>& row, float x, int n, FilterShared<NT>& s)
 {
     int a = 0, b = row.V - 1;
     while (a < b) {
@@ -409,7 +423,7 @@ __device__ __noinline__ int write_row(const RowSpan<T> row, T* out, bool same_ph
     U* o = reinterpret_cast<U*>(out);
     const U* x = reinterpret_cast<const U*>(row.p);
     // (a thread's vectors are its own: fetched before any of them is written, where out is the row)
-    each_vector<false>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
+    each_vector<false>(row.vec(), row.v0, row.v1, kThreadsOf<T>, [&](const uint4& w, int i, bool there) {
         if (!there)
             return;
         float f[E];
@@ -427,7 +441,7 @@ __device__ __noinline__ int write_row(const RowSpan<T> row, T* out, bool same_ph
             else
                 y.e[k] = Bits<T>::ninf;
         if (same_phase) {
-            reinterpret_cast<uint4*>(o + row.head)[i] = y.v;
+            __stcs(reinterpret_cast<uint4*>(o + row.head) + i, y.v);
         } else {
 #pragma unroll
             for (int k = 0; k < E; ++k)
@@ -453,10 +467,10 @@ __device__ __forceinline__ void fill_row(const RowSpan<T>& row, T* out, bool sam
     if (same_phase) {
         const uint32_t w = sizeof(T) == 4 ? (uint32_t)what : (uint32_t)what * 0x10001u;
         uint4* ov = reinterpret_cast<uint4*>(o + row.head);
-        for (int i = row.v0 + threadIdx.x; i < row.v1; i += kFilterThreads)
-            ov[i] = make_uint4(w, w, w, w);
+        for (int i = row.v0 + threadIdx.x; i < row.v1; i += kThreadsOf<T>)
+            __stcs(ov + i, make_uint4(w, w, w, w));
     } else {
-        for (int j = row.head + row.v0 * E + threadIdx.x; j < row.head + row.v1 * E; j += kFilterThreads)
+        for (int j = row.head + row.v0 * E + threadIdx.x; j < row.head + row.v1 * E; j += kThreadsOf<T>)
             o[j] = what;
     }
     const int j = row.lone();
@@ -473,8 +487,8 @@ __device__ __forceinline__ uint32_t min_p_key(float m, double t_log)
 }
 
 // By bisection, rank 0 alone.
-template <typename T, bool DRAW>
-__device__ __noinline__ void whole_row(const FilterArgs& a, long long r, const Settings& g, float m, Prefix end, FilterShared& s)
+template <typename T, bool DRAW, int NT>
+__device__ __noinline__ void whole_row(const FilterArgs& a, long long r, const Settings& g, float m, Prefix end, FilterShared<NT>& s)
 {
     const RowSpan<T> row(static_cast<const T*>(a.logits) + r * a.V, a.V, 0, 1);
     const uint32_t top = key_of(m);
@@ -509,7 +523,7 @@ __device__ __forceinline__ uint32_t entry_key(uint64_t e) { return (uint32_t)(e 
 __device__ __forceinline__ int entry_index(uint64_t e) { return (int)(0xffffffffu - (uint32_t)e); }
 
 // Into rank 0's list.
-__device__ __noinline__ void append(FilterShared& s, int C, uint32_t key, int index, int n = 1)
+template <int NT> __device__ __noinline__ void append(FilterShared<NT>& s, int C, uint32_t key, int index, int n = 1)
 {
     if (C == 1) {
         const int at = atomicAdd(&s.count, n);
@@ -525,7 +539,7 @@ __device__ __noinline__ void append(FilterShared& s, int C, uint32_t key, int in
 
 // Room in rank 0's list for each lane's n entries, by all lanes of a warp: one
 // atomic a warp.  The place of the lane's first.
-__device__ __forceinline__ int list_room(FilterShared& s, int C, int n)
+template <int NT> __device__ __forceinline__ int list_room(FilterShared<NT>& s, int C, int n)
 {
     const int lane = threadIdx.x & 31;
     int upto = n;
@@ -545,7 +559,7 @@ __device__ __forceinline__ int list_room(FilterShared& s, int C, int n)
     return __shfl_sync(kFull, at, 31) + upto - n;
 }
 
-__device__ __forceinline__ void list_put(FilterShared& s, int C, int at, uint64_t e)
+template <int NT> __device__ __forceinline__ void list_put(FilterShared<NT>& s, int C, int at, uint64_t e)
 {
     if (at >= kList)
         return;
@@ -557,8 +571,8 @@ __device__ __forceinline__ void list_put(FilterShared& s, int C, int at, uint64_
 
 // The marked logits of N vectors (bit u E + j: logit j of vector u, which is at
 // place(u)) into rank 0's list, by all lanes of a warp.
-template <typename T, int N, typename P>
-__device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShared& s, int C, uint32_t marks, const uint4 (&w)[N], P&& place)
+template <typename T, int N, typename P, int NT>
+__device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShared<NT>& s, int C, uint32_t marks, const uint4 (&w)[N], P&& place)
 {
     constexpr int E = Elem<T>::E;
     if (!__any_sync(kFull, marks))
@@ -579,30 +593,30 @@ __device__ __forceinline__ void append_marked(const RowSpan<T>& row, FilterShare
 
 // The logits of a CTA's part that mark(vector, its place) marks (E bits), into
 // rank 0's list.  kOneKey: all of them are the key `key`.
-template <bool kOneKey, typename T, typename M>
-__device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, int C, uint32_t key, M&& mark)
+template <bool kOneKey, typename T, typename M, int NT>
+__device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared<NT>& s, int C, uint32_t key, M&& mark)
 {
     constexpr int E = Elem<T>::E;
     const int t = threadIdx.x;
     Vectors<4> next;
-    next.load(row.vec(), row.v0 + t, row.v1, kFilterThreads);
+    next.load(row.vec(), row.v0 + t, row.v1, NT);
 #pragma unroll 1
-    for (int i = row.v0 + t; i - t < row.v1; i += 4 * kFilterThreads) {
+    for (int i = row.v0 + t; i - t < row.v1; i += 4 * NT) {
         const Vectors<4> now = next;
-        next.load(row.vec(), i + 4 * kFilterThreads, row.v1, kFilterThreads);
+        next.load(row.vec(), i + 4 * NT, row.v1, NT);
         uint32_t marks = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (i + u * kFilterThreads < row.v1)
-                marks |= mark(now.w[u], i + u * kFilterThreads) << (u * E);
+            if (i + u * NT < row.v1)
+                marks |= mark(now.w[u], i + u * NT) << (u * E);
         __syncwarp();
         if (!kOneKey) {
-            append_marked(row, s, C, marks, now.w, [&](int u) { return i + u * kFilterThreads; });
+            append_marked(row, s, C, marks, now.w, [&](int u) { return i + u * NT; });
         } else if (__any_sync(kFull, marks)) {
             int at = list_room(s, C, __popc(marks));
             for (; marks; marks &= marks - 1) {
                 const int bit = __ffs(marks) - 1;
-                list_put(s, C, at++, entry_of(key, row.head + (i + bit / E * kFilterThreads) * E + bit % E));
+                list_put(s, C, at++, entry_of(key, row.head + (i + bit / E * NT) * E + bit % E));
             }
             __syncwarp();
         }
@@ -612,28 +626,29 @@ __device__ __forceinline__ void gather(const RowSpan<T>& row, FilterShared& s, i
 // f(values, index of the first) for the vectors of the groups that reach `least`:
 // the groups are listed, then read by all threads, a vector each.  What f returns
 // marks the values that go into rank 0's list.
-template <typename T, typename F>
-__device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, float least, int C, FilterShared& s, F&& f)
+template <typename T, typename F, int NT>
+__device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, float least, int C, FilterShared<NT>& s, F&& f)
 {
     constexpr int E = Elem<T>::E;
     const int t = threadIdx.x;
+    uint16_t* hit = reinterpret_cast<uint16_t*>(s.group[groups]);
     for (int n = 0; n < groups; ++n)
         if (s.group[n][t] >= least) {
             const int at = atomicAdd(&s.hits, 1);
             if (at < kList)
-                s.hit[at] = (uint16_t)(n * kFilterThreads + t);
+                hit[at] = (uint16_t)(n * NT + t);
         }
     __syncthreads();
     const int n = min(s.hits, kList) * kGroup;
     auto place = [&](int j) {   // the vector of item j, or -1
         if (j >= n)
             return -1;
-        const int h = s.hit[j / kGroup], i = row.v0 + (h / kFilterThreads * kGroup + j % kGroup) * kFilterThreads + h % kFilterThreads;
+        const int h = hit[j / kGroup], i = row.v0 + (h / NT * kGroup + j % kGroup) * NT + h % NT;
         return i < row.v1 ? i : -1;
     };
 #pragma unroll 1
-    for (int j = t; j - t < n; j += 2 * kFilterThreads) {
-        int i[2] = {place(j), place(j + kFilterThreads)};
+    for (int j = t; j - t < n; j += 2 * NT) {
+        int i[2] = {place(j), place(j + NT)};
         uint4 w[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -652,10 +667,10 @@ __device__ __forceinline__ void each_hit(const RowSpan<T>& row, int groups, floa
 }
 
 // Sorts list[0 .. n), the largest first.
-__device__ __noinline__ void sort_list(FilterShared& s, int n)
+template <int NT> __device__ __noinline__ void sort_list(FilterShared<NT>& s, int n)
 {
     const int t = threadIdx.x;
-    if (n <= kFilterThreads) {   // each entry counts those before it, by one thread or up to eight
+    if (n <= NT) {   // each entry counts those before it, by one thread or up to eight
         const int g = n <= 32 ? 8 : n <= 64 ? 4 : n <= 128 ? 2 : 1, i = t / g, each = ((n + g - 1) / g + 1) & ~1;
         const uint64_t e = i < n ? s.list[i] : 0;
         const int j0 = min(n, t % g * each), j1 = min(n, j0 + each);   // (j0 even, or at the end)
@@ -674,15 +689,15 @@ __device__ __noinline__ void sort_list(FilterShared& s, int n)
         if (i < n && t % g == 0)
             s.list[r] = e;
     } else {
-        int size = 2 * kFilterThreads;
+        int size = 2 * NT;
         while (size < n)
             size *= 2;
-        for (int i = n + t; i < size; i += kFilterThreads)
+        for (int i = n + t; i < size; i += NT)
             s.list[i] = 0;
         for (int k = 2; k <= size; k <<= 1)
             for (int j = k >> 1; j > 0; j >>= 1) {
                 __syncthreads();
-                for (int i = t; i < size / 2; i += kFilterThreads) {
+                for (int i = t; i < size / 2; i += NT) {
                     const int x = 2 * i - (i & (j - 1)), y = x + j;
                     const uint64_t p = s.list[x], q = s.list[y];
                     if ((p < q) == ((x & k) == 0)) {
@@ -695,7 +710,7 @@ __device__ __noinline__ void sort_list(FilterShared& s, int n)
     __syncthreads();
 }
 
-__device__ __noinline__ uint64_t entry_weight(const FilterShared& s, int r)
+template <int NT> __device__ __noinline__ uint64_t entry_weight(const FilterShared<NT>& s, int r)
 {
     return weight62(value_of(entry_key(s.list[r])), s.scale, s.roots);
 }
@@ -704,10 +719,11 @@ __device__ __noinline__ uint64_t entry_weight(const FilterShared& s, int r)
 // their rounding moves stays below a thousandth of a token of weight 2^-32.
 __device__ __forceinline__ uint64_t weight52(uint64_t w62) { return (w62 + 512) >> 10; }
 
-__device__ __noinline__ uint64_t list_weight(const FilterShared& s, int r) { return weight52(entry_weight(s, r)); }
+template <int NT>
+__device__ __noinline__ uint64_t list_weight(const FilterShared<NT>& s, int r) { return weight52(entry_weight(s, r)); }
 
 // Exclusive prefix sum over the block; `total` gets the whole.
-__device__ __noinline__ uint64_t block_scan(uint64_t v, FilterShared& s, uint64_t& total)
+template <int NT> __device__ __noinline__ uint64_t block_scan(uint64_t v, FilterShared<NT>& s, uint64_t& total)
 {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     uint64_t x = v;
@@ -723,7 +739,7 @@ __device__ __noinline__ uint64_t block_scan(uint64_t v, FilterShared& s, uint64_
     __syncthreads();
     uint64_t before = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < kFilterWarps; ++i) {
+    for (int i = 0; i < NT / 32; ++i) {
         const uint64_t q = s.part64[i];
         if (i < w)
             before += q;
@@ -735,10 +751,10 @@ __device__ __noinline__ uint64_t block_scan(uint64_t v, FilterShared& s, uint64_
 
 // The mass of the sorted list's ranks lo .. hi - 1, a block's worth at a time;
 // `first` is the weight of rank lo + threadIdx.x (0 from hi on).
-__device__ __noinline__ uint64_t list_mass(FilterShared& s, int lo, int hi, uint64_t first)
+template <int NT> __device__ __noinline__ uint64_t list_mass(FilterShared<NT>& s, int lo, int hi, uint64_t first)
 {
     uint64_t sum = first, total;
-    for (int r = lo + kFilterThreads + (int)threadIdx.x; r < hi; r += kFilterThreads)
+    for (int r = lo + NT + (int)threadIdx.x; r < hi; r += NT)
         sum += list_weight(s, r);
     block_scan(sum, s, total);
     return total;
@@ -746,16 +762,17 @@ __device__ __noinline__ uint64_t list_mass(FilterShared& s, int lo, int hi, uint
 
 // The first rank of lo .. hi - 1 whose cumulative mass, counted from rank lo on,
 // reaches goal (hi - 1 if none does); its mass in `mass`.
-__device__ __noinline__ int list_reaching(FilterShared& s, int lo, int hi, uint64_t first, uint64_t goal, uint64_t& mass)
+template <int NT>
+__device__ __noinline__ int list_reaching(FilterShared<NT>& s, int lo, int hi, uint64_t first, uint64_t goal, uint64_t& mass)
 {
     uint64_t base = 0;
-    for (int r0 = lo;; r0 += kFilterThreads) {
+    for (int r0 = lo;; r0 += NT) {
         const int r = r0 + (int)threadIdx.x;
         const uint64_t w = r0 == lo ? first : r < hi ? list_weight(s, r) : 0;
         uint64_t total;
         const uint64_t c = base + block_scan(w, s, total);
         base += total;
-        if (base < goal && r0 + kFilterThreads < hi)
+        if (base < goal && r0 + NT < hi)
             continue;
         if (r < hi && (base >= goal ? (c < goal || r == lo) && c + w >= goal : r == hi - 1)) {
             s.found = r;
@@ -775,7 +792,7 @@ __device__ __noinline__ int list_reaching(FilterShared& s, int lo, int hi, uint6
 // largest logit.  The last bin holds whatever weighs less than 2^-63 too; its
 // mass does not count.  Weights are relative to a bin's width above bin 0's centre.
 // (Bins for the tokens near the border alone, found from an eighth of the row, the
-// rest summed on the way: 174 us where this takes 159, 256 rows of 151936.)
+// rest summed on the way, took 174 us where this took 159, 256 rows of 151936.)
 constexpr float kBinStep = 0.015625f;
 constexpr float kBinMagic = 196608.0f;   // 1.5 * 2^23 steps: adding it rounds to steps
 
@@ -805,7 +822,7 @@ __device__ __forceinline__ int bin_of(float l, const BinScale& b)
 
 // (Predicated rather than branched around: most lanes of a warp are out, in every
 // warp some are in.)
-__device__ __forceinline__ void bin_add(FilterShared& s, uint32_t i, uint32_t q, bool in)
+template <int NT> __device__ __forceinline__ void bin_add(FilterShared<NT>& s, uint32_t i, uint32_t q, bool in)
 {
     const uint32_t lo = smem_addr(&s.bin.lo[i]);
     uint32_t old = 0;
@@ -817,7 +834,8 @@ __device__ __forceinline__ void bin_add(FilterShared& s, uint32_t i, uint32_t q,
 }
 
 // Two tokens of at least b.least, the packed pair L; `in` says which of them count.
-__device__ __forceinline__ void bin_pair(FilterShared& s, uint64_t L, bool in0, bool in1, const BinScale& b)
+template <int NT>
+__device__ __forceinline__ void bin_pair(FilterShared<NT>& s, uint64_t L, bool in0, bool in1, const BinScale& b)
 {
     const uint64_t magic = f2_pack(kBinMagic, kBinMagic), nt = f2_mul(L, f2_pack(-b.ch, -b.ch));
     const uint64_t e = f2_fma(L, f2_pack(b.cl, b.cl), f2_fma(L, f2_pack(b.ch, b.ch), nt));
@@ -832,22 +850,23 @@ __device__ __forceinline__ void bin_pair(FilterShared& s, uint64_t L, bool in0, 
     bin_add(s, min(b.ref - (uint32_t)(at >> 32), (uint32_t)kBins - 1), (uint32_t)(q >> 32) - unit, in1);
 }
 
-__device__ __forceinline__ uint32_t bin_count(const FilterShared& s, int i) { return s.bin.hi[i] >> kCarryBits; }
+template <int NT>
+__device__ __forceinline__ uint32_t bin_count(const FilterShared<NT>& s, int i) { return s.bin.hi[i] >> kCarryBits; }
 
 // Bin i's share of its thread's bins: the sum of its weights over the weight of
 // the thread's first bin's centre, in units of 2^-29.
-__device__ __forceinline__ uint64_t bin_part(const FilterShared& s, int i)
+template <int NT> __device__ __forceinline__ uint64_t bin_part(const FilterShared<NT>& s, int i)
 {
     const uint32_t hi = s.bin.hi[i], n = hi >> kCarryBits;
     const uint64_t sum = (((uint64_t)(hi & ((1u << kCarryBits) - 1)) << 32) | s.bin.lo[i]) + ((uint64_t)n << 29) - ((uint64_t)n << 22);
-    const uint64_t f = i == kBins - 1 ? 0 : s.steps[i % kBinsEach];
+    const uint64_t f = i == kBins - 1 ? 0 : s.steps[i % kBinsEach<NT>];
     return ((sum & 0xffffffffu) * f >> 31) + ((sum >> 32) * f << 1);
 }
 
 // The weight that multiplies the parts of thread t's bins.
-__device__ __forceinline__ uint64_t part_weight(const FilterShared& s, int t)
+template <int NT> __device__ __forceinline__ uint64_t part_weight(const FilterShared<NT>& s, int t)
 {
-    return exp2_neg((uint64_t)(t * kBinsEach + 1) << (48 - kBinShift), s.roots);
+    return exp2_neg((uint64_t)(t * kBinsEach<NT> + 1) << (48 - kBinShift), s.roots);
 }
 
 __device__ __forceinline__ u128 part_mass(uint64_t part, uint64_t weight) { return ((u128)part * weight) >> 29; }
@@ -858,18 +877,18 @@ struct BinPart {
     int n_before, n_own;
 };
 
-__device__ __noinline__ BinPart scan_bins(FilterShared& s, u128& mass, int& count)
+template <int NT> __device__ __noinline__ BinPart scan_bins(FilterShared<NT>& s, u128& mass, int& count)
 {
     BinPart q;
     const int t = threadIdx.x;
-    if (t < kBinsEach)
+    if (t < kBinsEach<NT>)
         s.steps[t] = (uint32_t)(exp2_neg((uint64_t)t << (48 - kBinShift), s.roots) >> 31);
     __syncthreads();
     uint64_t part = 0;
     q.n_own = 0;
 #pragma unroll 4
-    for (int i = 0; i < kBinsEach; ++i) {
-        const int j = t * kBinsEach + ((i + t) & (kBinsEach - 1));   // (lanes on different banks)
+    for (int i = 0; i < kBinsEach<NT>; ++i) {
+        const int j = t * kBinsEach<NT> + ((i + t) & (kBinsEach<NT> - 1));   // (lanes on different banks)
         part += bin_part(s, j);
         q.n_own += (int)bin_count(s, j);
     }
@@ -884,21 +903,21 @@ __device__ __noinline__ BinPart scan_bins(FilterShared& s, u128& mass, int& coun
     return q;
 }
 
-__device__ __forceinline__ u128 bin_mass(const FilterShared& s, int i)
+template <int NT> __device__ __forceinline__ u128 bin_mass(const FilterShared<NT>& s, int i)
 {
-    return part_mass(bin_part(s, i), part_weight(s, i / kBinsEach));
+    return part_mass(bin_part(s, i), part_weight(s, i / kBinsEach<NT>));
 }
 
 // Where in the bins of thread s.found: one warp, a bin a lane.
-template <bool kCount> __device__ __noinline__ void bin_within(FilterShared& s, u128 goal)
+template <bool kCount, int NT> __device__ __noinline__ void bin_within(FilterShared<NT>& s, u128 goal)
 {
-    const int lane = threadIdx.x, i = s.found * kBinsEach + (lane & (kBinsEach - 1));
-    const uint64_t weight = part_weight(s, s.found), own = lane < kBinsEach ? bin_part(s, i) : 0;
-    const int n_own = lane < kBinsEach ? (int)bin_count(s, i) : 0;
+    const int lane = threadIdx.x, i = s.found * kBinsEach<NT> + (lane & (kBinsEach<NT> - 1));
+    const uint64_t weight = part_weight(s, s.found), own = lane < kBinsEach<NT> ? bin_part(s, i) : 0;
+    const int n_own = lane < kBinsEach<NT> ? (int)bin_count(s, i) : 0;
     uint64_t x = own;
     int n = n_own;
 #pragma unroll
-    for (int o = 1; o < kBinsEach; o <<= 1) {
+    for (int o = 1; o < kBinsEach<NT>; o <<= 1) {
         const uint64_t y = __shfl_up_sync(kFull, (unsigned long long)x, o);
         const int z = __shfl_up_sync(kFull, n, o);
         if (lane >= o) {
@@ -907,10 +926,10 @@ template <bool kCount> __device__ __noinline__ void bin_within(FilterShared& s, 
         }
     }
     const u128 base = s.found_mass, from = base + part_mass(x - own, weight);
-    const bool here = lane < kBinsEach && (kCount ? (u128)(uint32_t)(s.found_count + n) : base + part_mass(x, weight)) >= goal;
+    const bool here = lane < kBinsEach<NT> && (kCount ? (u128)(uint32_t)(s.found_count + n) : base + part_mass(x, weight)) >= goal;
     const int l = max(0, __ffs(__ballot_sync(kFull, here)) - 1);
     BinAt r;
-    r.bin = s.found * kBinsEach + l;
+    r.bin = s.found * kBinsEach<NT> + l;
     r.before = ((u128)__shfl_sync(kFull, (unsigned long long)(from >> 64), l) << 64) | __shfl_sync(kFull, (unsigned long long)from, l);
     r.n_before = s.found_count + __shfl_sync(kFull, n - n_own, l);
     if (lane == 0)
@@ -919,7 +938,7 @@ template <bool kCount> __device__ __noinline__ void bin_within(FilterShared& s, 
 
 // The bin where the running sum over all bins, of counts or of masses, reaches
 // `goal` (which all of them do).
-template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart& q, FilterShared& s, u128 goal)
+template <bool kCount, int NT> __device__ __noinline__ BinAt bin_reaching(const BinPart& q, FilterShared<NT>& s, u128 goal)
 {
     __syncthreads();
     if (threadIdx.x == 0)
@@ -939,7 +958,7 @@ template <bool kCount> __device__ __noinline__ BinAt bin_reaching(const BinPart&
 }
 
 // What rank 0 asks for, behind a row_sync.
-__device__ __forceinline__ Command command_of(const FilterShared& s, int C)
+template <int NT> __device__ __forceinline__ Command command_of(const FilterShared<NT>& s, int C)
 {
     if (C == 1)
         return s.cmd;
@@ -948,13 +967,13 @@ __device__ __forceinline__ Command command_of(const FilterShared& s, int C)
 }
 
 // All of the cluster's bins in rank 0's.
-__device__ __noinline__ void merge_bins(FilterShared& s, int rank, int C)
+template <int NT> __device__ __noinline__ void merge_bins(FilterShared<NT>& s, int rank, int C)
 {
     row_sync(C);
     if (C == 1)
         return;
     const int per = kBins / C, i0 = rank * per, t = threadIdx.x;   // (C is a power of two)
-    for (int i = i0 + 4 * t; i < i0 + per; i += 4 * kFilterThreads) {
+    for (int i = i0 + 4 * t; i < i0 + per; i += 4 * NT) {
         uint64_t lo[4] = {0, 0, 0, 0};
         uint32_t hi[4] = {0, 0, 0, 0};
 #pragma unroll 2
@@ -972,7 +991,7 @@ __device__ __noinline__ void merge_bins(FilterShared& s, int rank, int C)
     row_sync(C);
     if (rank == 0) {
 #pragma unroll 4
-        for (int i = per + 4 * t; i < kBins; i += 4 * kFilterThreads) {
+        for (int i = per + 4 * t; i < kBins; i += 4 * NT) {
             const int c = i / per;
             *reinterpret_cast<uint4*>(&s.bin.lo[i]) = ld_rank128(&s.bin.lo[i], c);
             *reinterpret_cast<uint4*>(&s.bin.hi[i]) = ld_rank128(&s.bin.hi[i], c);
@@ -982,16 +1001,16 @@ __device__ __noinline__ void merge_bins(FilterShared& s, int rank, int C)
 }
 
 // A CTA's part of the row, as far as it is in the prefix, into its bins.
-template <typename T>
-__device__ __noinline__ void fill_bins(const RowSpan<T> row, Prefix end, const BinScale b, FilterShared& s)
+template <typename T, int NT>
+__device__ __noinline__ void fill_bins(const RowSpan<T> row, Prefix end, const BinScale b, FilterShared<NT>& s)
 {
     constexpr int E = Elem<T>::E;
     __syncthreads();
-    for (int i = 4 * threadIdx.x; i < kBins; i += 4 * kFilterThreads)
+    for (int i = 4 * threadIdx.x; i < kBins; i += 4 * NT)
         *reinterpret_cast<uint4*>(&s.bin.lo[i]) = *reinterpret_cast<uint4*>(&s.bin.hi[i]) = make_uint4(0, 0, 0, 0);
     __syncthreads();
     const float least = value_of(end.key);
-    each_vector<true>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
+    each_vector<true>(row.vec(), row.v0, row.v1, NT, [&](const uint4& w, int i, bool there) {
         float x[E];
         Elem<T>::unpack(w, x);
         const int left = there ? end.index - (row.head + i * E) : -1;   // ties up to this one count
@@ -1027,8 +1046,9 @@ __device__ __noinline__ float bin_floor(int i, float m, const BinScale& b)
 }
 
 // The tokens of the prefix that are in bins from .. to, or in `also`.
-template <typename T>
-__device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to, int also, Prefix end, const BinScale b, int C, FilterShared& s)
+template <typename T, int NT>
+__device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to, int also, Prefix end, const BinScale b, int C,
+                                         FilterShared<NT>& s)
 {
     constexpr int E = Elem<T>::E;
     const float m = s.scale.m;
@@ -1067,9 +1087,9 @@ __device__ __noinline__ void gather_bins(const RowSpan<T> row, int from, int to,
         append(s, C, key_of((float)row.p[lone]), lone);
 }
 
-template <typename T, bool DRAW>
+template <typename T, bool DRAW, int NT>
 __device__ __noinline__ void binned_row(const FilterArgs& a, long long r, const Settings& g, const RowSpan<T>& row, int rank, Prefix end,
-                                        FilterShared& s)
+                                        FilterShared<NT>& s)
 {
     const int C = a.C, t = threadIdx.x;
     T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * a.V);
@@ -1258,22 +1278,22 @@ struct LevelScale {
 };
 
 // Thread t's values: kLevelsEach of them in descending order, all of one octave.
-__device__ __forceinline__ float level_value(int t, int j)
+template <int NT> __device__ __forceinline__ float level_value(int t, int j)
 {
-    const int o = t * kLevelsEach + j;
+    const int o = t * kLevelsEach<NT> + j;
     return o < 4096 ? __uint_as_float((uint32_t)(13183 + 4096 - o) << 16) : __uint_as_float(((uint32_t)(13184 + o - 4096) << 16) | 0x80000000u);
 }
 
-__device__ __forceinline__ uint32_t level_count(const FilterShared& s, int t, int j)
+template <int NT> __device__ __forceinline__ uint32_t level_count(const FilterShared<NT>& s, int t, int j)
 {
-    const int o = t * kLevelsEach + j;
+    const int o = t * kLevelsEach<NT> + j;
     return s.level[o < 4096 ? 4095 - o : kLevelsSide + o - 4096];
 }
 
-__device__ __forceinline__ LevelScale level_scale(const FilterShared& s, int t)
+template <int NT> __device__ __forceinline__ LevelScale level_scale(const FilterShared<NT>& s, int t)
 {
     LevelScale l;
-    const float value = level_value(t, 0), step = value - level_value(t, 1);
+    const float value = level_value<NT>(t, 0), step = value - level_value<NT>(t, 1);
     l.first = value > s.scale.m ? 0 : weight62(value, s.scale, s.roots);   // (above the row's first value's: none there)
     l.ratio = step * s.scale.ch > 63.0f ? 0 : exp2_neg((uint64_t)scaled48(step, s.scale.ch, s.scale.cl), s.roots);
     return l;
@@ -1298,20 +1318,20 @@ struct LevelPart : BinPart {
     LevelScale scale;
 };
 
-__device__ __noinline__ LevelPart scan_levels(FilterShared& s, u128& mass, int& count)
+template <int NT> __device__ __noinline__ LevelPart scan_levels(FilterShared<NT>& s, u128& mass, int& count)
 {
     LevelPart q;
     const int t = threadIdx.x, lane = t & 31;
     q.scale = level_scale(s, t);
-    uint64_t part = 0, f = power62(q.scale.ratio, lane & (kLevelsEach - 1));
+    uint64_t part = 0, f = power62(q.scale.ratio, lane & (kLevelsEach<NT> - 1));
     q.n_own = 0;
 #pragma unroll 4
-    for (int j = 0; j < kLevelsEach; ++j) {   // (each lane from another value on: other banks)
-        const int i = (j + lane) & (kLevelsEach - 1);
+    for (int j = 0; j < kLevelsEach<NT>; ++j) {   // (each lane from another value on: other banks)
+        const int i = (j + lane) & (kLevelsEach<NT> - 1);
         const uint32_t n = level_count(s, t, i);
         q.n_own += (int)n;
         part += n * (f >> 24);
-        f = i == kLevelsEach - 1 ? kOne62 : times62(f, q.scale.ratio);
+        f = i == kLevelsEach<NT> - 1 ? kOne62 : times62(f, q.scale.ratio);
     }
     q.own = level_mass(part, q.scale.first);
     u128 total;
@@ -1324,12 +1344,12 @@ __device__ __noinline__ LevelPart scan_levels(FilterShared& s, u128& mass, int& 
 }
 
 // Where in the values of thread s.found: one warp, a value a lane.
-template <bool kCount> __device__ __noinline__ void level_within(FilterShared& s, u128 goal)
+template <bool kCount, int NT> __device__ __noinline__ void level_within(FilterShared<NT>& s, u128 goal)
 {
     const int lane = threadIdx.x;
     const LevelScale l{s.found64, s.found_ratio};
     const uint64_t f = power62(l.ratio, lane);
-    const int n_own = lane < kLevelsEach ? (int)level_count(s, s.found, lane) : 0;
+    const int n_own = lane < kLevelsEach<NT> ? (int)level_count(s, s.found, lane) : 0;
     uint64_t x = n_own * (f >> 24);
     const uint64_t own = x;
     int n = n_own;
@@ -1348,7 +1368,7 @@ template <bool kCount> __device__ __noinline__ void level_within(FilterShared& s
     const uint32_t at = __ballot_sync(kFull, here), some = __ballot_sync(kFull, n_own > 0);
     const int i = at ? __ffs(at) - 1 : 31 - __clz(some | 1u);
     LevelAt r;
-    r.value = level_value(s.found, i);
+    r.value = level_value<NT>(s.found, i);
     r.weight = __shfl_sync(kFull, (unsigned long long)level_mass(f >> 24, l.first), i);
     r.n = __shfl_sync(kFull, n_own, i);
     r.n_before = s.found_count + __shfl_sync(kFull, n - n_own, i);
@@ -1361,7 +1381,7 @@ template <bool kCount> __device__ __noinline__ void level_within(FilterShared& s
 
 // The value among whose tokens the running count, or mass, reaches goal (which
 // the row does).
-template <bool kCount> __device__ __noinline__ LevelAt level_reaching(const LevelPart& q, FilterShared& s, u128 goal)
+template <bool kCount, int NT> __device__ __noinline__ LevelAt level_reaching(const LevelPart& q, FilterShared<NT>& s, u128 goal)
 {
     __syncthreads();
     if (threadIdx.x == 0)
@@ -1399,7 +1419,7 @@ __device__ __forceinline__ int tokens_for(u128 mass, uint64_t w, int n)
 }
 
 // Counts this CTA's part; returns the largest logit (NaN if there is one).
-__device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, FilterShared& s)
+template <int NT> __device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, FilterShared<NT>& s)
 {
     uint32_t top = 0xff80ff80u;
     auto one = [&](uint32_t w, bool both) {
@@ -1412,7 +1432,7 @@ __device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, Fil
             atomicAdd(&s.level[i >> 16], 1u);
         top = bmax2_nan(top, both ? w : w | 0xff800000u);
     };
-    each_vector<false>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int, bool there) {
+    each_vector<false>(row.vec(), row.v0, row.v1, NT, [&](const uint4& w, int, bool there) {
         if (there) {
             one(w.x, true);
             one(w.y, true);
@@ -1427,7 +1447,8 @@ __device__ __noinline__ float count_levels(const RowSpan<__nv_bfloat16> row, Fil
 }
 
 // The tokens of one value into rank 0's list.
-__device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, float value, int C, FilterShared& s)
+template <int NT>
+__device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, float value, int C, FilterShared<NT>& s)
 {
     const uint32_t both = (__float_as_uint(value) >> 16) * 0x10001u;
     gather<true>(row, s, C, key_of(value), [&](const uint4& w, int) {   // (no value here is a zero: equal logits are equal bits)
@@ -1443,13 +1464,14 @@ __device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, floa
 
 // False: some logits are not among the values (or not finite): to be done
 // another way.
-template <bool DRAW>
-__device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const Settings& g, const RowSpan<__nv_bfloat16>& row, int rank, FilterShared& s)
+template <bool DRAW, int NT>
+__device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const Settings& g, const RowSpan<__nv_bfloat16>& row, int rank,
+                                        FilterShared<NT>& s)
 {
     typedef __nv_bfloat16 T;
     const int C = a.C, t = threadIdx.x;
     __syncthreads();
-    for (int i = t; i < kLevels; i += kFilterThreads)
+    for (int i = t; i < kLevels; i += NT)
         s.level[i] = 0;
     __syncthreads();
     const uint32_t key = __reduce_max_sync(kFull, key_of(count_levels(row, s)));
@@ -1458,7 +1480,7 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
     __syncthreads();
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kFilterWarps; ++i)
+    for (int i = 0; i < NT / 32; ++i)
         top = max(top, s.warp_top[i]);
     if (C > 1) {
         if (t < C)
@@ -1467,7 +1489,7 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
         for (int c = 0; c < C; ++c)
             top = max(top, s.peer_top[c]);
         const int per = (kLevels + C - 1) / C, i0 = rank * per, i1 = min(kLevels, i0 + per);
-        for (int i = i0 + t; i < i1; i += kFilterThreads) {
+        for (int i = i0 + t; i < i1; i += NT) {
             uint32_t n = 0;
 #pragma unroll 4
             for (int c = 0; c < C; ++c)
@@ -1477,7 +1499,7 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
         row_sync(C);
         if (rank == 0) {
 #pragma unroll 4
-            for (int i = per + t; i < kLevels; i += kFilterThreads)
+            for (int i = per + t; i < kLevels; i += NT)
                 s.level[i] = ld_rank(&s.level[i], i / per);
             __syncthreads();
         }
@@ -1496,8 +1518,8 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
                 const bool fit = top > kKeyNegInf && top < kKeyPosInf && m < 256.0f && m > -256.0f && fabsf(m) >= kLeastLevel;
                 if (t == 0 && fit) {   // weights relative to the first of the values around the maximum: none is above one
                     const uint32_t bits = __float_as_uint(m) >> 16, mag = (bits & 0x7fffu) - 13184;
-                    const float from = bits >> 15 ? __uint_as_float(((13184 + mag / kLevelsEach * kLevelsEach) << 16) | 0x80000000u)
-                                                  : __uint_as_float((13184 + mag / kLevelsEach * kLevelsEach + kLevelsEach - 1) << 16);
+                    const float from = bits >> 15 ? __uint_as_float(((13184 + mag / kLevelsEach<NT> * kLevelsEach<NT>) << 16) | 0x80000000u)
+                                                  : __uint_as_float((13184 + mag / kLevelsEach<NT> * kLevelsEach<NT> + kLevelsEach<NT> - 1) << 16);
                     s.scale = row_scale(from, g.T);
                 }
                 __syncthreads();
@@ -1601,8 +1623,8 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
 
 // A row that no filter touches, in the one pass that has to read it anyway; if it
 // turns out unusable, NaN over it.
-template <typename T>
-__device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const RowSpan<T> row, int rank, FilterShared& s)
+template <typename T, int NT>
+__device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const RowSpan<T> row, int rank, FilterShared<NT>& s)
 {
     typedef typename Bits<T>::type U;
     constexpr int E = Elem<T>::E;
@@ -1611,7 +1633,7 @@ __device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const Ro
     U* o = reinterpret_cast<U*>(out);
     float top = -INFINITY;
     int n = 0;
-    each_vector<false>(row.vec(), row.v0, row.v1, kFilterThreads, [&](const uint4& w, int i, bool there) {
+    each_vector<false>(row.vec(), row.v0, row.v1, NT, [&](const uint4& w, int i, bool there) {
         if (!there)
             return;
         float x[E];
@@ -1622,7 +1644,7 @@ __device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const Ro
             n += x[j] > -INFINITY;
         }
         if (a.same_phase) {
-            reinterpret_cast<uint4*>(o + row.head)[i] = w;
+            __stcs(reinterpret_cast<uint4*>(o + row.head) + i, w);
         } else {
             union {
                 uint4 v;
@@ -1647,7 +1669,7 @@ __device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const Ro
     const int own = (int)block_sum((u128)(uint32_t)n, s);   // (a barrier behind warp_top)
     uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < kFilterWarps; ++i)
+    for (int i = 0; i < NT / 32; ++i)
         most = max(most, s.warp_top[i]);
     int all = own;
     if (C > 1) {
@@ -1673,10 +1695,11 @@ __device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const Ro
 // the kernel: a row a cluster
 // ---------------------------------------------------------------------------
 template <typename T, bool DRAW>
-__global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filter_kernel(FilterArgs a)
+__global__ void __launch_bounds__(kThreadsOf<T>, kBlocksOf<T>) sv_filter_kernel(FilterArgs a)
 {
     extern __shared__ __align__(16) unsigned char filter_smem[];
-    FilterShared& s = *reinterpret_cast<FilterShared*>(filter_smem);
+    constexpr int NT = kThreadsOf<T>;
+    FilterShared<NT>& s = *reinterpret_cast<FilterShared<NT>*>(filter_smem);
     constexpr int E = Elem<T>::E;
     const int C = a.C, t = threadIdx.x, V = a.V;
     const int rank = C > 1 ? (int)cluster_ctarank() : 0;
@@ -1709,16 +1732,17 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
         s.hits = 0;
         s.first = INT_MAX;
     }
-    const int groups = (row.v1 - row.v0 + kGroup * kFilterThreads - 1) / (kGroup * kFilterThreads);
+    const int groups = (row.v1 - row.v0 + kGroup * NT - 1) / (kGroup * NT);
     // How a top-k is bounded: by the threads' maxima, or with a larger share of them
     // by the groups'; not where too many would pass.
     const int share = (g.k + C - 1) / C;
-    const bool by_thread = share <= kFilterThreads / 2;
-    const bool bounded = !greedy && g.k > 0 && (by_thread || (share <= groups * (kFilterThreads / 2) && g.k <= kList / 2));
-    // bf16 rows where every token counts, or nearly: top-k 500 of 1024 rows of 128256
-    // is 165 us by the bound and 185 by levels, top-k 1000 258 and 185.
+    const bool by_thread = share <= NT / 2;
+    const bool bounded = !greedy && g.k > 0 && (by_thread || (share <= groups * (NT / 2) && g.k <= kList / 2));
+    // bf16 rows where every token counts, or nearly: 1024 rows of 128256 with top-k 250
+    // take 104 us by the bound and 128 by levels, with top-k 500 167 and 137, with 1000
+    // 252 and 138.
     if constexpr (sizeof(T) == 2)
-        if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : share > kFilterThreads || !bounded))
+        if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : share > NT || !bounded))
             if (levels_row<DRAW>(a, r, g, row, rank, s))
                 return;
 
@@ -1728,21 +1752,21 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
     }
 
     double t_log = 0.0;   // one thread's: 64-bit floating point runs at a hundredth of the fp32 rate
-    if (t == kFilterThreads - 32 && good && !greedy && g.min_p > 0.0f)
+    if (t == NT - 32 && good && !greedy && g.min_p > 0.0f)
         t_log = (double)g.T * log((double)g.min_p);
 
     // 1. The maxima of the row, of each thread, and of each thread's groups of
     // vectors: the one pass that has to read everything from memory.
     float mine = -INFINITY;
     for (int n = 0; n < groups; ++n) {
-        const int i0 = row.v0 + n * kGroup * kFilterThreads + t;
+        const int i0 = row.v0 + n * kGroup * NT + t;
         uint4 w[kGroup];
 #pragma unroll
         for (int u = 0; u < kGroup; ++u) {
             const uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
             w[u] = make_uint4(none, none, none, none);
-            if (i0 + u * kFilterThreads < row.v1)
-                w[u] = row.vec()[i0 + u * kFilterThreads];
+            if (i0 + u * NT < row.v1)
+                w[u] = ld_row(row.vec() + i0 + u * NT);
         }
         float top;
         if (sizeof(T) == 4) {
@@ -1776,7 +1800,7 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
     __syncthreads();
     uint32_t top_key = 0, low_key = 0xffffffffu;
 #pragma unroll
-    for (int i = 0; i < kFilterWarps; ++i) {
+    for (int i = 0; i < NT / 32; ++i) {
         top_key = max(top_key, s.warp_top[i]);
         low_key = min(low_key, s.warp_low[i]);
     }
@@ -1802,7 +1826,7 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
             __syncthreads();
             n = 0;
 #pragma unroll
-            for (int i = 0; i < kFilterWarps; ++i)
+            for (int i = 0; i < NT / 32; ++i)
                 n += s.warp_count[turn][i];
             if (n >= share) {
                 lo = mid;
@@ -1868,7 +1892,7 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
     Prefix end{kKeyNegInf + 1, INT_MAX};
     if (t == 0)
         s.scale = row_scale(m, g.T);
-    if (t == kFilterThreads - 32 && g.min_p > 0.0f)
+    if (t == NT - 32 && g.min_p > 0.0f)
         s.least_key = min_p_key(m, t_log);
     __syncthreads();
     if (g.min_p > 0.0f)
@@ -1910,7 +1934,7 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
             if (g.k > 0)
                 n = min(n, g.k);
             uint64_t mass = 0, w = 0;
-            if (n <= kFilterThreads) {   // a rank a thread: one sum answers both questions
+            if (n <= NT) {   // a rank a thread: one sum answers both questions
                 if (DRAW || g.p < 1.0f) {
                     const uint64_t w62 = t < n ? entry_weight(s, t) : 0;
                     w = weight52(w62);
@@ -1954,7 +1978,7 @@ __global__ void __launch_bounds__(kFilterThreads, 1024 / kFilterThreads) sv_filt
             else
                 __syncthreads();
             if (!DRAW)
-                for (int i = t; i < n; i += kFilterThreads)
+                for (int i = t; i < n; i += NT)
                     out[entry_index(s.list[i])] = (T)value_of(entry_key(s.list[i]));
             return;
         }
