@@ -451,8 +451,8 @@ sv_status spec_sample_filtered(const void* logits, sv_dtype dtype, const float* 
                                int32_t* out_tokens, float* out_prob, int32_t* out_kept, cudaStream_t stream);
 
 /*
- * spec_filter_logits -- out [B][S][V] receives the kept tokens' logits and -inf
- * for the rest, NaN throughout an unusable row: spec_verify and
+ * spec_filter_logits -- out [B][S][V] receives the kept tokens' logits (a zero
+ * may lose its sign) and -inf for the rest, NaN throughout an unusable row: spec_verify and
  * spec_verify_tree on filtered target and draft rows verify against the
  * filtered distributions (a draft drawn by spec_sample_filtered needs its rows
  * filtered the same way).  n_rows (device, [B] int32, or NULL: all S) says how
@@ -701,7 +701,8 @@ sv_status spec_kv_reserve(const sv_kv_pool* pool, const int32_t* kv_len, const i
  * page_size) of each sequence go back onto the stack, so that they are handed
  * out again in the same order (a release after a reserve with the lengths
  * unchanged leaves the stack as it was).  kv_len[b] = 0 gives back all.  The
- * page table is not written.  A sequence whose lengths cannot be used
+ * page table is not written.  A page below 0 among them goes onto the stack as
+ * it is and sets bit 2 of `errors`.  A sequence whose lengths cannot be used
  * (negative, held outside [0, max_pages], longer than its pages) keeps its
  * pages and sets bit 2 of `errors`; a free_count outside [0, capacity], or a
  * stack that would grow past `capacity`, refuses the whole call.

@@ -53,9 +53,8 @@ int row_ctas(long long rows, long long row_bytes, int nsm)
     return C;
 }
 
-template <typename T, bool DRAW> cudaError_t launch(FilterArgs& a, cudaStream_t st)
+template <typename T, bool DRAW, int NT> cudaError_t launch(FilterArgs& a, cudaStream_t st)
 {
-    constexpr int NT = kThreadsOf<T>;
     int dev = 0, nsm = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
@@ -64,7 +63,7 @@ template <typename T, bool DRAW> cudaError_t launch(FilterArgs& a, cudaStream_t 
         return e;
     static std::atomic<unsigned long long> ready{0};   // devices whose limit has been raised
     if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
-        e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)filter_smem_bytes<NT>(kGroupsMost<NT>));
+        e = cudaFuncSetAttribute(sv_filter_kernel<T, DRAW, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)filter_smem_bytes<NT>(kGroupsMost<NT>));
         if (e != cudaSuccess)
             return e;
         if (dev < 64)
@@ -84,12 +83,18 @@ template <typename T, bool DRAW> cudaError_t launch(FilterArgs& a, cudaStream_t 
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = a.C > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, sv_filter_kernel<T, DRAW>, a);
+    return cudaLaunchKernelEx(&cfg, sv_filter_kernel<T, DRAW, NT>, a);
 }
 
 template <bool DRAW> sv_status launch_rows(FilterArgs& a, sv_dtype dtype, cudaStream_t st)
 {
-    return (dtype == SV_DTYPE_BF16 ? launch<__nv_bfloat16, DRAW>(a, st) : launch<float, DRAW>(a, st)) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    const bool small = a.V <= kShortMost;
+    cudaError_t e;
+    if (dtype == SV_DTYPE_BF16)
+        e = small ? launch<__nv_bfloat16, DRAW, kShortThreads>(a, st) : launch<__nv_bfloat16, DRAW, kThreadsOf<__nv_bfloat16>>(a, st);
+    else
+        e = small ? launch<float, DRAW, kShortThreads>(a, st) : launch<float, DRAW, kThreadsOf<float>>(a, st);
+    return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace

@@ -58,6 +58,10 @@ struct FilterArgs {
 // filtered rows 118 for 92.
 template <typename T> constexpr int kThreadsOf = sizeof(T) == 2 ? 256 : 512;
 template <typename T> constexpr int kBlocksOf = sizeof(T) == 2 ? 3 : 2;
+// Rows of at most kShortMost tokens, all of them in the list: 128 threads, eight blocks
+// an SM without the sums' shared memory.  7680 rows of 1000 fp32 filtered by top-p take
+// 186 us, 600 rows of 300 drawn 19; one row of 300 12, where 512 threads take 11.
+constexpr int kShortThreads = 128, kShortBlocks = 8, kShortMost = 8 * kShortThreads;
 constexpr int kClusterMost = 8;
 constexpr int kGroup = 4;          // vectors of a thread whose maximum is kept (1024 rows, top-k 50: 60 us; by eights 64)
 constexpr int kList = 2048;        // tokens sorted at a time
@@ -130,7 +134,8 @@ template <int NT> struct FilterShared {
 // Shared memory for rows of `groups` groups a CTA.
 template <int NT> constexpr size_t filter_smem_bytes(int groups)
 {
-    const size_t g = (size_t)groups * NT * 4 + kList * sizeof(uint16_t), b = ((size_t)kLevels * 4 + 15) / 16 * 16;   // (more than the bins)
+    const size_t g = (size_t)groups * NT * 4 + kList * sizeof(uint16_t);
+    const size_t b = NT == kShortThreads ? 0 : ((size_t)kLevels * 4 + 15) / 16 * 16;   // (more than the bins)
     return sizeof(FilterShared<NT>) - sizeof(float) * kGroupsMost<NT> * NT + (g > b ? g : b);
 }
 
@@ -214,7 +219,7 @@ template <typename T> struct RowSpan {
     // f(values, index of the first) for every vector.
     template <typename F> __device__ __forceinline__ void vectors(F&& f) const
     {
-        each_vector<true>(vec(), v0, v1, kThreadsOf<T>, [&](const uint4& w, int i, bool there) {
+        each_vector<true>(vec(), v0, v1, (int)blockDim.x, [&](const uint4& w, int i, bool there) {
             float x[E];
             Elem<T>::unpack(w, x);
             if (there)
@@ -423,7 +428,7 @@ __device__ __noinline__ int write_row(const RowSpan<T> row, T* out, bool same_ph
     U* o = reinterpret_cast<U*>(out);
     const U* x = reinterpret_cast<const U*>(row.p);
     // (a thread's vectors are its own: fetched before any of them is written, where out is the row)
-    each_vector<false>(row.vec(), row.v0, row.v1, kThreadsOf<T>, [&](const uint4& w, int i, bool there) {
+    each_vector<false>(row.vec(), row.v0, row.v1, (int)blockDim.x, [&](const uint4& w, int i, bool there) {
         if (!there)
             return;
         float f[E];
@@ -467,10 +472,10 @@ __device__ __forceinline__ void fill_row(const RowSpan<T>& row, T* out, bool sam
     if (same_phase) {
         const uint32_t w = sizeof(T) == 4 ? (uint32_t)what : (uint32_t)what * 0x10001u;
         uint4* ov = reinterpret_cast<uint4*>(o + row.head);
-        for (int i = row.v0 + threadIdx.x; i < row.v1; i += kThreadsOf<T>)
+        for (int i = row.v0 + threadIdx.x; i < row.v1; i += (int)blockDim.x)
             __stcs(ov + i, make_uint4(w, w, w, w));
     } else {
-        for (int j = row.head + row.v0 * E + threadIdx.x; j < row.head + row.v1 * E; j += kThreadsOf<T>)
+        for (int j = row.head + row.v0 * E + threadIdx.x; j < row.head + row.v1 * E; j += (int)blockDim.x)
             o[j] = what;
     }
     const int j = row.lone();
@@ -671,7 +676,7 @@ template <int NT> __device__ __noinline__ void sort_list(FilterShared<NT>& s, in
 {
     const int t = threadIdx.x;
     if (n <= NT) {   // each entry counts those before it, by one thread or up to eight
-        const int g = n <= 32 ? 8 : n <= 64 ? 4 : n <= 128 ? 2 : 1, i = t / g, each = ((n + g - 1) / g + 1) & ~1;
+        const int g = n <= NT / 8 ? 8 : n <= NT / 4 ? 4 : n <= NT / 2 ? 2 : 1, i = t / g, each = ((n + g - 1) / g + 1) & ~1;
         const uint64_t e = i < n ? s.list[i] : 0;
         const int j0 = min(n, t % g * each), j1 = min(n, j0 + each);   // (j0 even, or at the end)
         const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(s.list);
@@ -688,24 +693,53 @@ template <int NT> __device__ __noinline__ void sort_list(FilterShared<NT>& s, in
         __syncthreads();
         if (i < n && t % g == 0)
             s.list[r] = e;
-    } else {
+    } else {   // bitonic, kEach neighbours a thread: three of four steps need registers and shuffles alone
+        constexpr int kEach = NT == kShortThreads ? 8 : kList / NT;
         int size = 2 * NT;
         while (size < n)
             size *= 2;
-        for (int i = n + t; i < size; i += NT)
-            s.list[i] = 0;
-        for (int k = 2; k <= size; k <<= 1)
-            for (int j = k >> 1; j > 0; j >>= 1) {
+        const int i0 = t * kEach;
+        uint64_t e[kEach];
+#pragma unroll
+        for (int x = 0; x < kEach; ++x)
+            e[x] = i0 + x < n ? s.list[i0 + x] : 0;
+        // of a pair: the larger one where the run of k descends and this is its first, or neither
+        auto pick = [](uint64_t a, uint64_t b, bool larger) { return (a > b) == larger ? a : b; };
+#pragma unroll 1
+        for (int k = 2; k <= size; k <<= 1) {
+            int j = k >> 1;
+#pragma unroll 1
+            for (; j >= 32 * kEach; j >>= 1) {
                 __syncthreads();
-                for (int i = t; i < size / 2; i += NT) {
-                    const int x = 2 * i - (i & (j - 1)), y = x + j;
-                    const uint64_t p = s.list[x], q = s.list[y];
-                    if ((p < q) == ((x & k) == 0)) {
-                        s.list[x] = q;
-                        s.list[y] = p;
-                    }
-                }
+#pragma unroll
+                for (int x = 0; x < kEach; ++x)
+                    s.list[x * NT + t] = e[x];
+                __syncthreads();
+#pragma unroll
+                for (int x = 0; x < kEach; ++x)
+                    e[x] = pick(e[x], s.list[x * NT + (t ^ (j / kEach))], ((i0 & k) == 0) == ((i0 & j) == 0));
             }
+#pragma unroll 1
+            for (; j >= kEach; j >>= 1)
+#pragma unroll
+                for (int x = 0; x < kEach; ++x)
+                    e[x] = pick(e[x], __shfl_xor_sync(kFull, (unsigned long long)e[x], j / kEach), ((i0 & k) == 0) == ((i0 & j) == 0));
+#pragma unroll
+            for (int y = kEach / 2; y > 0; y >>= 1)
+                if (y <= j)
+#pragma unroll
+                    for (int x = 0; x < kEach; ++x)
+                        if (!(x & y)) {
+                            const uint64_t a = e[x], b = e[x | y];
+                            const bool swap = (a < b) == (((i0 | x) & k) == 0);
+                            e[x] = swap ? b : a;
+                            e[x | y] = swap ? a : b;
+                        }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kEach; ++x)
+            s.list[i0 + x] = e[x];
     }
     __syncthreads();
 }
@@ -1691,14 +1725,45 @@ __device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const Ro
         fill_row(row, out, a.same_phase, Bits<T>::nan);
 }
 
+// Rows whose candidates, the tokens up to `end`, no list holds.
+template <typename T, bool DRAW, int NT>
+__device__ __forceinline__ void many_candidates(const FilterArgs& a, long long r, const Settings& g, const RowSpan<T>& row, int rank, Prefix end,
+                                                FilterShared<NT>& s)
+{
+    const int C = a.C, t = threadIdx.x;
+    T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * a.V);
+    // Nothing but min-p, if that: every token above its border stays.
+    if (!DRAW && g.p >= 1.0f && g.k == 0) {
+        const int all = (int)block_sum((u128)(uint32_t)write_row(row, out, a.same_phase, end), s);
+        if (C > 1) {
+            if (t == 0)
+                st_rank(&s.peer_kept[rank], 0, (uint32_t)all);
+            row_sync(C);
+        }
+        int total = all;
+        for (int c = 1; c < C; ++c)
+            total += s.peer_kept[c];
+        if (rank == 0 && t == 0)
+            put_row<DRAW>(a, r, total);
+        return;
+    }
+
+    if (s.scale.cold) {
+        if (rank == 0)
+            whole_row<T, DRAW>(a, r, g, s.scale.m, end, s);
+        return;
+    }
+    binned_row<T, DRAW>(a, r, g, row, rank, end, s);
+    row_sync(C);
+}
+
 // ---------------------------------------------------------------------------
 // the kernel: a row a cluster
 // ---------------------------------------------------------------------------
-template <typename T, bool DRAW>
-__global__ void __launch_bounds__(kThreadsOf<T>, kBlocksOf<T>) sv_filter_kernel(FilterArgs a)
+template <typename T, bool DRAW, int NT>
+__global__ void __launch_bounds__(NT, NT == kShortThreads ? kShortBlocks : kBlocksOf<T>) sv_filter_kernel(FilterArgs a)
 {
     extern __shared__ __align__(16) unsigned char filter_smem[];
-    constexpr int NT = kThreadsOf<T>;
     FilterShared<NT>& s = *reinterpret_cast<FilterShared<NT>*>(filter_smem);
     constexpr int E = Elem<T>::E;
     const int C = a.C, t = threadIdx.x, V = a.V;
@@ -1741,7 +1806,7 @@ __global__ void __launch_bounds__(kThreadsOf<T>, kBlocksOf<T>) sv_filter_kernel(
     // bf16 rows where every token counts, or nearly: 1024 rows of 128256 with top-k 250
     // take 104 us by the bound and 128 by levels, with top-k 500 167 and 137, with 1000
     // 252 and 138.
-    if constexpr (sizeof(T) == 2)
+    if constexpr (sizeof(T) == 2 && NT != kShortThreads)
         if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : share > NT || !bounded))
             if (levels_row<DRAW>(a, r, g, row, rank, s))
                 return;
@@ -1982,35 +2047,14 @@ __global__ void __launch_bounds__(kThreadsOf<T>, kBlocksOf<T>) sv_filter_kernel(
                     out[entry_index(s.list[i])] = (T)value_of(entry_key(s.list[i]));
             return;
         }
+        if constexpr (NT == kShortThreads)   // (V <= kShortMost: they have been listed)
+            return;
         row_sync(C);   // too many (every CTA has read the count): the bins take them
         if (t == 0)
             s.count = 0;
     }
-
-    // 4. Nothing but min-p, if that: every token above its border stays.
-    if (!DRAW && g.p >= 1.0f && g.k == 0) {
-        const int all = (int)block_sum((u128)(uint32_t)write_row(row, out, a.same_phase, end), s);
-        if (C > 1) {
-            if (t == 0)
-                st_rank(&s.peer_kept[rank], 0, (uint32_t)all);
-            row_sync(C);
-        }
-        int total = all;
-        for (int c = 1; c < C; ++c)
-            total += s.peer_kept[c];
-        if (rank == 0 && t == 0)
-            put_row<DRAW>(a, r, total);
-        return;
-    }
-
-    // 5. The bins.
-    if (s.scale.cold) {
-        if (rank == 0)
-            whole_row<T, DRAW>(a, r, g, m, end, s);
-        return;
-    }
-    binned_row<T, DRAW>(a, r, g, row, rank, end, s);
-    row_sync(C);
+    if constexpr (NT != kShortThreads)
+        many_candidates<T, DRAW>(a, r, g, row, rank, end, s);
 }
 
 }  // namespace sv

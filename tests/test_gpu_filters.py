@@ -80,6 +80,21 @@ def test_settings_of_their_own(dev, V, dtype):
     check_filter(logits, s)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1, 2, 7, 33, 100, 129, 300, 511, 513, 1000, 1024, 1025])
+def test_many_short_rows(dev, V, dtype):
+    """More of them than fill the device, around the sizes where rows change their blocks and their sort."""
+    logits, u = rows(530, V, dtype, dev, V)
+    logits[7, V // 2] = float("nan")
+    logits[8] = -float("inf")
+    s = settings(dev, **{n: v * 53 for n, v in MIXED.items()})
+    check_draw(logits, u, s)
+    check_filter(logits, s)
+    out = logits.reshape(53, 10, V).clone()
+    few = {n: t[:53].contiguous() for n, t in s.items()}
+    check_filter(logits.reshape(53, 10, V), few, sv.spec_filter_logits(out, out=out, **few))
+
+
 @pytest.mark.parametrize("dtype,V,B", [("bf16", 128256, 10), ("f32", 151936, 10), ("bf16", 200003, 10)])
 def test_large_vocabularies(dev, dtype, V, B):
     logits, u = rows(B, V, dtype, dev, V)
