@@ -40,10 +40,9 @@ sv_status check_rows(const void* logits, sv_dtype dtype, const float* temperatur
 // CTAs a row is spread over: one for each SM at most while the rows alone are
 // fewer, 56 KB or more each; of long rows half that each, once half the SMs do.
 // More and smaller parts read faster and then wait for one another more often.
-// Nine rows of 128256 bf16 filtered by top-k: 16.2 us by eight CTAs, 22.2 by four;
-// one row drawn by top-k 50: 8.5 by four, 11.4 by one; 16 rows of 151936 fp32, top-p
-// alone: 49 by eight, 76 by one; 37 rows of 50257 bf16, top-p: 21.2 by one, 25.4 by two;
-// 145 rows of 32003 fp32: 42 and 52; 256 rows of 151936 fp32: 141 and 177.
+// One row of 128256 bf16, top-p alone: 23 us by eight CTAs, 25 by four, 29 by one; 16
+// rows of 151936 fp32: 49 by eight, 75 by one; 37 rows of 50257 bf16: 21 by one, 25 by
+// two; 145 rows of 32003 fp32: 41 and 51; 256 rows of 151936 fp32: 136 and 170.
 int row_ctas(long long rows, long long row_bytes, int nsm)
 {
     int C = 1;

@@ -17,7 +17,7 @@
 //    written, 0.80); by the chain of steps for one row (15 us).
 //  - levels (bf16 where every token counts): the one pass counts how often each
 //    of 8192 values occurs, an atomic a token; weights times counts are the sums.
-//    1024 rows of 128256 draw in 134 us (2.0 TB/s): what bounds it is the atomics
+//    1024 rows of 128256 draw in 137 us (1.9 TB/s): what bounds it is the atomics
 //    in shared memory, some ten cycles for each warp's.
 //  - bins (fp32 where every token counts): sums by weight, and the border's bins
 //    read once more.  256 rows of 151936 draw in 136 us (1.1 TB/s of the one pass
@@ -119,7 +119,8 @@ template <int NT> struct FilterShared {
     int count;             // rank 0: entries of the list
     int hits;              // groups that hold a candidate
     int first;             // lowest index of the largest logit
-    int found, found_count;
+    int found, found_count, found_at;
+    int top_level;         // the maximum's place among the levels, the largest first
     // the maxima of each thread's groups (as many as the row has) and behind them the
     // groups that hold a candidate (`hit`, kList of them), then the bins
     union alignas(16) {
@@ -1308,7 +1309,8 @@ __device__ __forceinline__ uint64_t times62(uint64_t f, uint64_t g) { return __u
 constexpr float kLeastLevel = 5.9604644775390625e-8f;   // 2^-24
 
 struct LevelScale {
-    uint64_t first, ratio;   // the weight of the thread's first value, and from one value to the next
+    uint64_t first, ratio;   // the weight of the thread's first value up to the maximum, and from one value to the next
+    int at;                  // which of its values that first one is
 };
 
 // Thread t's values: kLevelsEach of them in descending order, all of one octave.
@@ -1327,8 +1329,9 @@ template <int NT> __device__ __forceinline__ uint32_t level_count(const FilterSh
 template <int NT> __device__ __forceinline__ LevelScale level_scale(const FilterShared<NT>& s, int t)
 {
     LevelScale l;
-    const float value = level_value<NT>(t, 0), step = value - level_value<NT>(t, 1);
-    l.first = value > s.scale.m ? 0 : weight62(value, s.scale, s.roots);   // (above the row's first value's: none there)
+    l.at = max(0, min(s.top_level - t * kLevelsEach<NT>, kLevelsEach<NT> - 1));
+    const float value = level_value<NT>(t, l.at), step = level_value<NT>(t, 0) - level_value<NT>(t, 1);
+    l.first = value > s.scale.m ? 0 : weight62(value, s.scale, s.roots);   // (all above the maximum: none there)
     l.ratio = step * s.scale.ch > 63.0f ? 0 : exp2_neg((uint64_t)scaled48(step, s.scale.ch, s.scale.cl), s.roots);
     return l;
 }
@@ -1346,7 +1349,11 @@ __device__ __forceinline__ uint64_t power62(uint64_t f, int n)
     return y;
 }
 
-__device__ __forceinline__ u128 level_mass(uint64_t part, uint64_t first) { return ((u128)part * first) >> 38; }
+// Parts are in units of 2^-42 of a thread's first weight: those of 2^20 tokens fit 64
+// bits, and what the rounding of 2^17 tokens moves is 2^-25 of the largest one's weight.
+__device__ __forceinline__ uint64_t part42(uint64_t f) { return (f + (1u << 19)) >> 20; }
+
+__device__ __forceinline__ u128 level_mass(uint64_t part, uint64_t first) { return ((u128)part * first) >> 42; }
 
 struct LevelPart : BinPart {
     LevelScale scale;
@@ -1357,15 +1364,15 @@ template <int NT> __device__ __noinline__ LevelPart scan_levels(FilterShared<NT>
     LevelPart q;
     const int t = threadIdx.x, lane = t & 31;
     q.scale = level_scale(s, t);
-    uint64_t part = 0, f = power62(q.scale.ratio, lane & (kLevelsEach<NT> - 1));
+    uint64_t part = 0, f = power62(q.scale.ratio, max(0, (lane & (kLevelsEach<NT> - 1)) - q.scale.at));
     q.n_own = 0;
 #pragma unroll 4
     for (int j = 0; j < kLevelsEach<NT>; ++j) {   // (each lane from another value on: other banks)
         const int i = (j + lane) & (kLevelsEach<NT> - 1);
         const uint32_t n = level_count(s, t, i);
         q.n_own += (int)n;
-        part += n * (f >> 24);
-        f = i == kLevelsEach<NT> - 1 ? kOne62 : times62(f, q.scale.ratio);
+        part += n * part42(f);   // (nothing above the maximum: n is 0 before `at`)
+        f = i == kLevelsEach<NT> - 1 || i < q.scale.at ? kOne62 : times62(f, q.scale.ratio);
     }
     q.own = level_mass(part, q.scale.first);
     u128 total;
@@ -1381,10 +1388,10 @@ template <int NT> __device__ __noinline__ LevelPart scan_levels(FilterShared<NT>
 template <bool kCount, int NT> __device__ __noinline__ void level_within(FilterShared<NT>& s, u128 goal)
 {
     const int lane = threadIdx.x;
-    const LevelScale l{s.found64, s.found_ratio};
-    const uint64_t f = power62(l.ratio, lane);
+    const LevelScale l{s.found64, s.found_ratio, s.found_at};
+    const uint64_t f = power62(l.ratio, max(0, lane - l.at));
     const int n_own = lane < kLevelsEach<NT> ? (int)level_count(s, s.found, lane) : 0;
-    uint64_t x = n_own * (f >> 24);
+    uint64_t x = n_own * part42(f);
     const uint64_t own = x;
     int n = n_own;
 #pragma unroll
@@ -1403,7 +1410,7 @@ template <bool kCount, int NT> __device__ __noinline__ void level_within(FilterS
     const int i = at ? __ffs(at) - 1 : 31 - __clz(some | 1u);
     LevelAt r;
     r.value = level_value<NT>(s.found, i);
-    r.weight = __shfl_sync(kFull, (unsigned long long)level_mass(f >> 24, l.first), i);
+    r.weight = weight62(r.value, s.scale, s.roots);
     r.n = __shfl_sync(kFull, n_own, i);
     r.n_before = s.found_count + __shfl_sync(kFull, n - n_own, i);
     r.before = ((u128)__shfl_sync(kFull, (unsigned long long)(from >> 64), i) << 64) | __shfl_sync(kFull, (unsigned long long)from, i);
@@ -1428,6 +1435,7 @@ template <bool kCount, int NT> __device__ __noinline__ LevelAt level_reaching(co
         s.found_mass = q.before;
         s.found64 = q.scale.first;
         s.found_ratio = q.scale.ratio;
+        s.found_at = q.scale.at;
     }
     __syncthreads();
     if (threadIdx.x < 32)
@@ -1550,11 +1558,10 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
                 const float m = value_of(top);
                 const uint32_t low = s.level[2 * kLevelsSide - 1];
                 const bool fit = top > kKeyNegInf && top < kKeyPosInf && m < 256.0f && m > -256.0f && fabsf(m) >= kLeastLevel;
-                if (t == 0 && fit) {   // weights relative to the first of the values around the maximum: none is above one
-                    const uint32_t bits = __float_as_uint(m) >> 16, mag = (bits & 0x7fffu) - 13184;
-                    const float from = bits >> 15 ? __uint_as_float(((13184 + mag / kLevelsEach<NT> * kLevelsEach<NT>) << 16) | 0x80000000u)
-                                                  : __uint_as_float((13184 + mag / kLevelsEach<NT> * kLevelsEach<NT> + kLevelsEach<NT> - 1) << 16);
-                    s.scale = row_scale(from, g.T);
+                if (t == 0 && fit) {
+                    const int bits = (int)(__float_as_uint(m) >> 16);
+                    s.top_level = bits >> 15 ? 4096 + (bits & 0x7fff) - 13184 : 13183 + 4096 - bits;
+                    s.scale = row_scale(m, g.T);
                 }
                 __syncthreads();
                 // Logits below -256 have to weigh nothing, and their number is not known.  Those
@@ -1804,8 +1811,8 @@ __global__ void __launch_bounds__(NT, NT == kShortThreads ? kShortBlocks : kBloc
     const bool by_thread = share <= NT / 2;
     const bool bounded = !greedy && g.k > 0 && (by_thread || (share <= groups * (NT / 2) && g.k <= kList / 2));
     // bf16 rows where every token counts, or nearly: 1024 rows of 128256 with top-k 250
-    // take 104 us by the bound and 128 by levels, with top-k 500 167 and 137, with 1000
-    // 252 and 138.
+    // take 102 us by the bound and 133 by levels, with top-k 500 167 and 133, with 1000
+    // 252 and 133.
     if constexpr (sizeof(T) == 2 && NT != kShortThreads)
         if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : share > NT || !bounded))
             if (levels_row<DRAW>(a, r, g, row, rank, s))

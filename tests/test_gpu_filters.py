@@ -81,7 +81,7 @@ def test_settings_of_their_own(dev, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("V", [1, 2, 7, 33, 100, 129, 300, 511, 513, 1000, 1024, 1025])
+@pytest.mark.parametrize("V", [1, 2, 7, 33, 100, 129, 300, 511, 513, 1000, 1024, 1025, 2048])
 def test_many_short_rows(dev, V, dtype):
     """More of them than fill the device, around the sizes where rows change their blocks and their sort."""
     logits, u = rows(530, V, dtype, dev, V)
@@ -234,6 +234,24 @@ def test_top_k_of_every_size(dev, V):
             s = settings(dev, [0.9] * len(ks), ks, p)
             check_draw(logits, u, s)
             check_filter(logits, s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [2049, 4096, 30011])
+@pytest.mark.parametrize("sigma", [6.0, 40.0, -40.0])
+def test_logits_far_apart(dev, sigma, V, dtype):
+    """Neighbouring bf16 values of these weigh 2^-10 of one another and less; the largest logit is a large one, or
+    (sigma below 0) below zero."""
+    logits, u = rows(40, V, dtype, dev, V, abs(sigma))
+    if sigma < 0:
+        logits = -logits.abs() - 3
+    rng = np.random.default_rng(V)
+    T = rng.uniform(0.05, 2.0, 40)
+    check_draw(logits, u, settings(dev, T))
+    check_filter(logits, settings(dev, T, p=rng.uniform(0.1, 1.0, 40)))
+    s = settings(dev, T, k=rng.integers(1, V, 40), p=rng.uniform(0.5, 1.0, 40))
+    check_draw(logits, u, s)
+    check_filter(logits, s)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
