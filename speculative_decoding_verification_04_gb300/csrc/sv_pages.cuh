@@ -90,6 +90,14 @@ template <typename V> __device__ __forceinline__ int last_at_most(const V* v, in
     return lo;
 }
 
+// f(r) for every n-th row of [from, to), from the me-th on.  Rows are counted in 64
+// bits: up to 2^31 - 1 of them and a step of up to 152 blocks pass 32.
+template <typename F> __host__ __device__ __forceinline__ void every(long long from, long long to, unsigned me, unsigned n, F&& f)
+{
+    for (long long r = from + me; r < to; r += n)
+        f(r);
+}
+
 __device__ __forceinline__ int pages_for(long long positions, int shift)
 {
     return (int)((positions + (1 << shift) - 1) >> shift);
@@ -135,11 +143,9 @@ __global__ void __launch_bounds__(kPageThreads) sv_reserve_kernel(PoolArgs a)
     if (all_bad)
         err |= kErrCache;
     if (a.work && a.has_slots && a.packed) {   // rows of no sequence
-        const int lo = all_bad ? a.rows : row0, hi = all_bad ? a.rows : row1;
-        for (int r = me; r < lo; r += nthr)
-            a.slots[r] = -1;
-        for (int r = hi + me; r < a.rows; r += nthr)
-            a.slots[r] = -1;
+        auto none = [&](long long r) { a.slots[r] = -1; };
+        every(0, all_bad ? a.rows : row0, me, nthr, none);
+        every(all_bad ? a.rows : row1, a.rows, me, nthr, none);
     }
     long long asked = 0, took = 0;   // by the sequences before this chunk
     for (int b0 = 0; b0 < a.B; b0 += kPageThreads) {
