@@ -277,6 +277,25 @@ __device__ __forceinline__ void row_sync(int C)
     }
 }
 
+// A CTA's shared memory may be reached from its cluster once it has started: every
+// CTA says so as it begins, and waits for the others before its first store to one
+// of them, behind its pass over the row.
+__device__ __forceinline__ void peers_announce(int C)
+{
+    if (C > 1) {
+        __syncwarp();
+        cluster_arrive();
+    }
+}
+
+__device__ __forceinline__ void peers_started(int C)
+{
+    if (C > 1) {
+        __syncwarp();
+        cluster_wait();
+    }
+}
+
 __device__ __forceinline__ u128 shfl_up128(u128 v, int o)
 {
     const unsigned long long lo = __shfl_up_sync(kFull, (unsigned long long)v, o);
@@ -1505,7 +1524,7 @@ __device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, floa
 }
 
 // False: some logits are not among the values (or not finite): to be done
-// another way.
+// another way.  Waits for the cluster's CTAs to have started (peers_started).
 template <bool DRAW, int NT>
 __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const Settings& g, const RowSpan<__nv_bfloat16>& row, int rank,
                                         FilterShared<NT>& s)
@@ -1525,6 +1544,7 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
     for (int i = 0; i < NT / 32; ++i)
         top = max(top, s.warp_top[i]);
     if (C > 1) {
+        peers_started(C);
         if (t < C)
             st_rank(&s.peer_top[rank], t, top);
         row_sync(C);
@@ -1663,7 +1683,7 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
 }
 
 // A row that no filter touches, in the one pass that has to read it anyway; if it
-// turns out unusable, NaN over it.
+// turns out unusable, NaN over it.  Waits as levels_row does.
 template <typename T, int NT>
 __device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const RowSpan<T> row, int rank, FilterShared<NT>& s)
 {
@@ -1714,6 +1734,7 @@ __device__ __noinline__ void copy_row(const FilterArgs& a, long long r, const Ro
         most = max(most, s.warp_top[i]);
     int all = own;
     if (C > 1) {
+        peers_started(C);
         if (t < C) {
             st_rank(&s.peer_top[rank], t, most);
             st_rank(&s.peer_kept[rank], t, (uint32_t)own);
@@ -1804,6 +1825,8 @@ __global__ void __launch_bounds__(NT, NT == kShortThreads ? kShortBlocks : kBloc
         s.hits = 0;
         s.first = INT_MAX;
     }
+    peers_announce(C);
+    bool started = false;
     const int groups = (row.v1 - row.v0 + kGroup * NT - 1) / (kGroup * NT);
     // How a top-k is bounded: by the threads' maxima, or with a larger share of them
     // by the groups'; not where too many would pass.
@@ -1814,9 +1837,11 @@ __global__ void __launch_bounds__(NT, NT == kShortThreads ? kShortBlocks : kBloc
     // take 102 us by the bound and 133 by levels, with top-k 500 167 and 133, with 1000
     // 252 and 133.
     if constexpr (sizeof(T) == 2 && NT != kShortThreads)
-        if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : share > NT || !bounded))
+        if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : share > NT || !bounded)) {
             if (levels_row<DRAW>(a, r, g, row, rank, s))
                 return;
+            started = true;   // (it has waited)
+        }
 
     if (!DRAW && good && !greedy && g.min_p == 0.0f && g.p >= 1.0f && g.k == 0) {
         copy_row<T>(a, r, row, rank, s);
@@ -1911,6 +1936,8 @@ __global__ void __launch_bounds__(NT, NT == kShortThreads ? kShortBlocks : kBloc
         bound = lo;
     }
     if (C > 1) {
+        if (!started)
+            peers_started(C);
         if (t < C) {
             st_rank(&s.peer_top[rank], t, top_key);
             st_rank(&s.peer_bound[rank], t, bound);
