@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kPageThreads) sv_reserve_kernel(PoolArgs a)
                 err |= kErrCache;
         }
         if (a.clustered) {   // every block has read what the first one may write
+            __syncwarp();    // (the barrier is for whole warps; the last sequences' lanes have just parted)
             cluster_arrive();
             cluster_wait();
         }
@@ -296,6 +297,7 @@ __global__ void __launch_bounds__(kPageThreads) sv_release_kernel(PoolArgs a)
             s.len[t] = keep;
         }
         if (a.clustered) {
+            __syncwarp();
             cluster_arrive();
             cluster_wait();
         }

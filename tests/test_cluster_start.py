@@ -47,3 +47,14 @@ def test_the_filter_kernel_announces_itself_and_waits():
     assert "started = true;" in between[between.index("levels_row<"):between.index("copy_row<")]
     # and none of the cluster returns before it while another one stays: the rows of a cluster are one row
     assert REMOTE.search(text[:said]) is None
+
+
+@pytest.mark.parametrize("name", ["sv_pages.cuh", "sv_filter.cuh"])
+def test_cluster_barriers_are_met_by_whole_warps(name):
+    """barrier.cluster's .aligned form: no lane of a warp may still be on another way to it."""
+    steps = [line.strip() for line in source(name).splitlines() if line.strip()]
+    at = [i for i, line in enumerate(steps) if line == "cluster_arrive();" or "barrier.cluster.arrive" in line]
+    assert at
+    for i in at:
+        before = [line for line in steps[i - 4:i] if line not in ("else", "if (DRAW)") and "barrier.cluster" not in line]
+        assert before[-1] == "__syncwarp();", steps[i - 4:i + 1]
