@@ -103,6 +103,13 @@ __device__ __forceinline__ int pages_for(long long positions, int shift)
     return (int)((positions + (1 << shift) - 1) >> shift);
 }
 
+// How many packed rows lie between two starts; -1 where they do not ascend from 0 or
+// more (starts may be any numbers: what their difference wraps to says nothing).
+__host__ __device__ __forceinline__ int packed_count(int start, int next)
+{
+    return start < 0 || next < start ? -1 : next - start;
+}
+
 // What sequence b asks for (count 0 past the last one).
 struct Request {
     int len, held, count, first;
@@ -117,7 +124,7 @@ __device__ __forceinline__ Request load_request(const PoolArgs& a, int b)
         q.count = a.has_n ? a.n_new[b] : a.S;
         if (a.packed) {
             q.first = a.row_start[b];
-            q.count = a.row_start[b + 1] - q.first;
+            q.count = packed_count(q.first, a.row_start[b + 1]);
         }
     }
     return q;
@@ -138,7 +145,7 @@ __global__ void __launch_bounds__(kPageThreads) sv_reserve_kernel(PoolArgs a)
     bool bad = avail < 0 || avail > a.capacity || (a.packed && (row0 < 0 || row1 > a.rows || q.count < 0));
     if (a.packed)   // starts that do not ascend: no row could be told whose it is
         for (int b = t + kPageThreads; b < a.B; b += kPageThreads)
-            bad |= a.row_start[b] > a.row_start[b + 1];
+            bad |= packed_count(a.row_start[b], a.row_start[b + 1]) < 0;
     const bool all_bad = __syncthreads_or(bad) != 0;
     if (all_bad)
         err |= kErrCache;

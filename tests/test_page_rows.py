@@ -13,11 +13,16 @@ PROGRAM = r"""
 #include <cstdio>
 #include "sv_pages.cuh"
 
-// argv: from, to, threads: the lowest and highest row that any of the first, middle and last threads takes, and how many.
+// argv: a start and the next: how many rows lie between them.  Or from, to, threads: the lowest and highest row that any of the first, middle and last threads takes, and how many.
 int main(int argc, char** argv)
 {
     long long from, to;
     unsigned n;
+    int start, next;
+    if (argc == 3 && sscanf(argv[1], "%d", &start) == 1 && sscanf(argv[2], "%d", &next) == 1) {
+        printf("%d\n", sv::packed_count(start, next));
+        return 0;
+    }
     if (argc != 4 || sscanf(argv[1], "%lld", &from) != 1 || sscanf(argv[2], "%lld", &to) != 1 || sscanf(argv[3], "%u", &n) != 1)
         return 1;
     const unsigned threads[3] = {0, n / 2, n - 1};
@@ -69,3 +74,10 @@ def test_no_row_is_counted_in_32_bits():
     with open(os.path.join(CSRC, "sv_pages.cuh")) as f:
         loops = [line.strip() for line in f if "for (" in line and "nthr" in line]
     assert loops and all(line.startswith("for (long long ") for line in loops)
+
+
+@pytest.mark.parametrize("start,next,count", [(0, 0, 0), (3, 10, 7), (0, MOST, MOST), (MOST, MOST, 0), (5, 4, -1), (-1, 3, -1), (-1, -1, -1), (-3, -2, -1), (MOST, 0, -1),
+                                              (2000000000, -2000000000, -1), (-2000000000, 100, -1), (-2000000000, 2000000000, -1), (MOST, -MOST - 1, -1)])
+def test_starts_whose_difference_wraps(program, start, next, count):
+    got = subprocess.run([program, str(start), str(next)], check=True, capture_output=True, text=True, timeout=60).stdout
+    assert int(got) == count
