@@ -688,8 +688,10 @@ typedef struct {
  * The pages between 0 and the top of the stack stay as they are, so that a
  * call can be made again from the counts before it.
  * Sequences whose lengths or counts cannot be used (negative, more than S new
- * tokens, past the page table) are refused and set bit 2 of `errors`, as do
- * pages below 0; a free_count outside [0, capacity] and row starts that do not
+ * tokens, past the page table) are refused and set bit 2 of `errors`.  A page
+ * below 0 that is served, or that new tokens go to, sets it too, whether slots
+ * are asked for or not; it stays in the page table, and its tokens' slots are
+ * -1.  A free_count outside [0, capacity] and row starts that do not
  * ascend from 0 or more to at most `rows` refuse the whole call.
  */
 sv_status spec_kv_reserve(const sv_kv_pool* pool, const int32_t* kv_len, const int32_t* n_new, const int32_t* row_start, int32_t S,

@@ -197,9 +197,22 @@ __global__ void __launch_bounds__(kPageThreads) sv_reserve_kernel(PoolArgs a)
         if (a.work) {
             for (long long j = me; j < total; j += nthr) {
                 const int i = last_at_most(s.before, nb, j);
-                const int page = s.count[i] >= 0 ? a.stack[avail - 1 - (asked + j)] : -1;
+                const bool granted = s.count[i] >= 0;
+                const int page = granted ? a.stack[avail - 1 - (asked + j)] : -1;
+                if (granted && page < 0)
+                    err |= kErrCache;
                 a.table[(long long)(b0 + i) * a.max_pages + s.held[i] + (int)(j - s.before[i])] = page;
             }
+            if (!a.has_slots && a.has_err)   // (slots look at every page that new tokens go to; without them, a warp a sequence)
+                for (long long i = me >> 5; i < nb; i += nthr >> 5) {
+                    if (s.count[i] <= 0)
+                        continue;
+                    const int first = s.len[i] >> a.page_shift;
+                    const int end = min(s.held[i], pages_for((long long)s.len[i] + s.count[i], a.page_shift));
+                    for (int pg = first + (t & 31); pg < end; pg += 32)
+                        if (a.table[(b0 + i) * a.max_pages + pg] < 0)
+                            err |= kErrCache;
+                }
             if (a.has_slots && !(a.packed && all_bad)) {
                 const long long r0 = a.packed ? s.first[0] : (long long)b0 * a.S;
                 const long long r1 = a.packed ? s.first[nb] : (long long)(b0 + nb) * a.S;
