@@ -425,11 +425,13 @@ sv_status spec_verify_tree(const void* target_logits, const void* draft_logits, 
  *   top-k  of these the first k,
  *   top-p  of these the shortest prefix that holds the share top_p of their
  *          mass (at least one token).
- * T = 0 keeps the argmax alone (lowest index); its filters are not used.
+ * T = 0 keeps the argmax alone (lowest index); its filters are not used, and
+ * may hold anything.
  * Sums are of whole numbers (weights in units of 2^-62 of the largest), so
  * results do not depend on the order of the additions.
- * A row with a NaN or +inf logit or no finite one, or with an unusable
- * temperature, top_k (negative), top_p or min_p, has the kept count -1.
+ * A row with a NaN or +inf logit or no finite one, with an unusable
+ * temperature, or with T > 0 and an unusable top_k (negative), top_p or min_p,
+ * has the kept count -1.
  * Calls are asynchronous on `stream`, allocate nothing and need no workspace;
  * they may be captured into CUDA graphs.  V: at most sv_max_vocab(dtype).
  */

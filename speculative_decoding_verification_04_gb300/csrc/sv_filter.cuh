@@ -1812,8 +1812,8 @@ __global__ void __launch_bounds__(NT, NT == kShortThreads ? kShortBlocks : kBloc
     g.min_p = a.has_m ? a.min_p[b] : 0.0f;
     g.u = DRAW && g.T != 0.0f ? a.uniforms[r] : 0.0f;
     const bool greedy = g.T == 0.0f;
-    const bool good = temperature_usable(g.T) && g.k >= 0 && g.p >= 0.0f && g.p <= 1.0f && g.min_p >= 0.0f && g.min_p <= 1.0f &&
-                      g.u >= 0.0f && g.u < 1.0f;
+    const bool good = temperature_usable(g.T) && (greedy || (g.k >= 0 && g.p >= 0.0f && g.p <= 1.0f && g.min_p >= 0.0f && g.min_p <= 1.0f &&
+                                                             g.u >= 0.0f && g.u < 1.0f));
     const T* logits = static_cast<const T*>(a.logits) + r * V;
     T* out = static_cast<T*>(a.out) + (DRAW ? 0 : r * V);
     const RowSpan<T> row(logits, V, rank, C);
