@@ -1585,10 +1585,13 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
                 }
                 __syncthreads();
                 // Logits below -256 have to weigh nothing, and their number is not known.  Those
-                // nearer to zero than 2^-24 are counted with that value: a few of them move the
-                // sums by nothing that shows, but none of them is told from the others.
+                // nearer to zero than 2^-24 are counted with that value, and none of them is told
+                // from the others.  That changes a weight by up to ch 2^-24 of itself: all of them
+                // together may move the sums by 2^-40 of the largest weight.
+                const uint32_t near = s.level[0] + s.level[kLevelsSide];
                 const bool able = fit && !s.scale.cold && (low == 0 || ((m + 256.0f) * s.scale.ch > 64.0f && g.k == 0 && g.p < 1.0f)) &&
-                                  s.level[0] + s.level[kLevelsSide] <= 16 && s.scale.ch < 256.0f;
+                                  s.scale.ch < 256.0f &&
+                                  (near == 0 || (float)near * s.scale.ch * (float)weight62(kLeastLevel, s.scale, s.roots) <= 70368744177664.0f);   // 2^(62 + 24 - 40)
                 if (!able) {
                     c.op = kCmdRecount;
                 } else {

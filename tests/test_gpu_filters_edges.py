@@ -39,3 +39,28 @@ def test_greedy_rows_use_no_filter(dev, V, B, dtype):  # noqa: F811
     one = settings(dev, T[11:], k[11:], p[11:], m[11:])
     check_draw(logits[11:], u[11:], one, (tok[11:], prob[11:], kept[11:]))
     check_filter(logits[11:], one, (out[11:], kept2[11:]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("near", [0.0, -0.0, 3e-8, -5.9604644775390625e-08, 1e-12])
+@pytest.mark.parametrize("n", [1, 5, 16, 40, 3000])
+@pytest.mark.parametrize("reach", [14.0, 45.0])
+def test_logits_at_zero(dev, reach, n, near, dtype):  # noqa: F811
+    """Logits nearer to zero than 2^-24 at low temperatures, where 2^-24 is a thousandth of a percent of a weight: shares
+    within the rounding of one quotient, draws and kept sets as they are defined."""
+    V, B = 9001, 60
+    rng = np.random.default_rng(n)
+    T = rng.choice([0.006, 0.0072, 0.01, 0.03, 0.8], B)
+    top = (T * rng.uniform(0.0, reach, B)).astype(np.float32)
+    x = torch.full((B, V), -2.0, device=dev) - torch.rand(B, V, generator=torch.Generator(device=dev).manual_seed(n), device=dev)
+    for b in range(B):
+        at = rng.permutation(V)
+        x[b, torch.from_numpy(at[:n]).to(dev)] = near
+        x[b, at[n]] = float(top[b])
+        x[b, at[n + 1]] = float(top[b]) * 0.75
+    x = x.to(DT[dtype])
+    u = torch.from_numpy(rng.uniform(0, 1, B).astype(np.float32)).to(dev)
+    for k, p in ((None, None), (None, rng.uniform(0.3, 0.9999, B)), ([n // 2 + 400] * B, None)):
+        s = settings(dev, T, k, p)
+        check_draw(x, u, s)
+        check_filter(x, s)
