@@ -64,3 +64,34 @@ def test_logits_at_zero(dev, reach, n, near, dtype):  # noqa: F811
         s = settings(dev, T, k, p)
         check_draw(x, u, s)
         check_filter(x, s)
+
+
+NAN_BITS = {"bf16": (torch.int16, [0x7fc1, 0xffc1 - 0x10000, 0x7f81, 0xff81 - 0x10000, 0x7fff, -1]),
+            "f32": (torch.int32, [0x7fc00001, 0xffc00001 - 2 ** 32, 0x7f800001, 0xff800001 - 2 ** 32, 0x7fffffff, -1])}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [7, 1000, 2049, 30011, 128256])
+@pytest.mark.parametrize("one", [dict(), dict(p=0.9), dict(k=700), dict(k=20), dict(m=0.1), dict(k=3, p=0.5), dict(greedy=True)], ids=str)
+def test_every_nan_makes_a_row_unusable(dev, one, V, dtype):  # noqa: F811
+    """Both signs, quiet and signalling, at the row's ends and inside; the rows between are as without it."""
+    view, bits = NAN_BITS[dtype]
+    at = [0, V - 1, V // 2]
+    B = 2 * len(bits) * len(at)
+    if B * V > 2000000:                      # a few rows, each over several CTAs
+        at, B = [V // 3], 2 * len(bits)
+    logits, u = rows(B, V, dtype, dev, V + 3)
+    raw = logits.view(view)
+    for i, b in enumerate(bits):
+        for j, a in enumerate(at):
+            raw[2 * (i * len(at) + j), a] = b
+    assert logits[::2].isnan().any(-1).all()
+    s = settings(dev, [0.0 if "greedy" in one else 0.8] * B, *([one[n]] * B if n in one else None for n in "kpm"))
+    tok, prob, kept = sv.spec_sample_filtered(logits, u, **s)
+    out, n = sv.spec_filter_logits(logits, **s)
+    assert (tok[::2] == -1).all() and prob[::2].isnan().all() and (kept[::2] == -1).all() and (n[::2] == -1).all() and out[::2].isnan().all()
+    few = slice(1, 8, 2)
+    half = {k: None if t is None else t[few].contiguous() for k, t in s.items()}
+    check_draw(logits[few], u[few], half, (tok[few], prob[few], kept[few]))
+    check_filter(logits[few], half, (out[few], n[few]))
+    assert (kept[1::2] > 0).all() and (n[1::2] == kept[1::2]).all()

@@ -72,3 +72,63 @@ def test_pages_below_zero(dev, where, B, with_slots, packed):  # noqa: F811
     assert negative_pages(pool, new) == want
     pool.same()
     assert pool.errors.item() == (CACHE_BIT if want else 0) | (PAGES_BIT if where == "served, refused" else 0)
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("first", [0, 3])
+@pytest.mark.parametrize("B,kind", [(5, "any"), (64, "any"), (1500, "short"), (2600, "empty"), (1025, "long last"), (2048, "mixed")])
+def test_many_packed_rows(dev, B, kind, first, offset):  # noqa: F811
+    """From 131072 rows on a thread writes four slots: groups that hold several sequences, start before the first row or
+    end behind the last, lie across 1024 sequences, and slots that are not 16-byte aligned."""
+    total, page = 140003, 16
+    rng = random.Random(B)
+    if kind == "short":      # most of one to three tokens
+        new = [rng.randint(1, 3) for _ in range(B)]
+    elif kind == "empty":
+        new = [rng.choice([0, 0, 0, 1, 2, 70]) for _ in range(B)]
+    elif kind == "mixed":
+        new = [rng.choice([0, 1, 5, 60, 61, 62, 63]) for _ in range(B)]
+    else:
+        new = [rng.randint(0, 2 * total // B) if kind == "any" else 1 for _ in range(B)]
+    new[B // 2] += 1
+    big = B - 1 if kind == "long last" else 1023 if B > 1024 else 0     # the last of the first 1024, where there are more
+    new[big] += max(0, total - sum(new))
+    total = sum(new)
+    lengths = [rng.choice([0, 0, rng.randint(0, 40)]) for _ in range(B)]
+    ask = [-(-(a + n) // page) - -(-a // page) for a, n in zip(lengths, new)]
+    stock = sum(ask) - ask[-1]                                          # the last that asks is refused
+    pool = Pool(dev, lengths, page, -(-(40 + max(new)) // page), stock, seed=B)
+    rows = total + first + 2
+    starts = [first]
+    for n in new:
+        starts.append(starts[-1] + n)
+    room = torch.full((rows + 4,), 55, dtype=torch.int64, device=dev)
+    slots = room[offset:offset + rows]
+    sv.spec_kv_reserve(*pool.args(), row_start=ints(starts, dev), slots=slots, errors=pool.errors)
+    want, bits = pool.reserve(new)
+    pool.same()
+    assert pool.errors.item() == bits
+    flat = [-1] * first
+    for s, n in zip(want, new):
+        flat += [-1] * n if s is None else s
+    assert slots.tolist() == flat + [-1] * 2
+    assert (room[:offset] == 55).all() and (room[offset + rows:] == 55).all()
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("B,S", [(1500, 101), (3, 50001), (1030, 131)])
+def test_many_rows_a_sequence(dev, B, S, offset):  # noqa: F811
+    """The same with S rows a sequence, not all of them real."""
+    rng = random.Random(S)
+    page = 8
+    new = [rng.randint(0, S) for _ in range(B)]
+    lengths = [rng.randint(0, 30) for _ in range(B)]
+    pool = Pool(dev, lengths, page, -(-(30 + S) // page), sum(new) // page + B, seed=S)
+    room = torch.full((B * S + 4,), 55, dtype=torch.int64, device=dev)
+    slots = room[offset:offset + B * S].view(B, S)
+    sv.spec_kv_reserve(*pool.args(), S=S, n_new=ints(new, dev), slots=slots, errors=pool.errors)
+    want, bits = pool.reserve(new, S)
+    pool.same()
+    assert pool.errors.item() == bits
+    assert slots.tolist() == [(s or []) + [-1] * (S - len(s or [])) for s in want]
+    assert (room[:offset] == 55).all() and (room[offset + B * S:] == 55).all()
