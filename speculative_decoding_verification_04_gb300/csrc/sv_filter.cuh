@@ -1523,6 +1523,16 @@ __device__ __noinline__ void gather_level(const RowSpan<__nv_bfloat16> row, floa
         append(s, C, key_of(value), lone);
 }
 
+// Logits nearer to zero than 2^-24 are counted with that value, and none of them is
+// told from the others.  That changes a weight by up to ch 2^-24 of itself: all of
+// them may move the row's mass by 2^-34 of it.  (One row in 130 of 128256 normal
+// logits of deviation 2 has such a logit; at T = 0.8 it moves the mass by 2^-44.)
+template <int NT> __device__ __noinline__ bool near_zero_close(const FilterShared<NT>& s, u128 total)
+{
+    const float near = (float)(s.level[0] + s.level[kLevelsSide]) * (float)weight62(kLeastLevel, s.scale, s.roots);
+    return near * s.scale.ch <= (float)(uint64_t)(total >> 20) * 1024.0f;   // 2^(24 - 34 + 20)
+}
+
 // False: some logits are not among the values (or not finite): to be done
 // another way.  Waits for the cluster's CTAs to have started (peers_started).
 template <bool DRAW, int NT>
@@ -1584,20 +1594,16 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
                     s.scale = row_scale(m, g.T);
                 }
                 __syncthreads();
-                // Logits below -256 have to weigh nothing, and their number is not known.  Those
-                // nearer to zero than 2^-24 are counted with that value, and none of them is told
-                // from the others.  That changes a weight by up to ch 2^-24 of itself: all of them
-                // together may move the sums by 2^-40 of the largest weight.
-                const uint32_t near = s.level[0] + s.level[kLevelsSide];
+                // Logits below -256 have to weigh nothing, and their number is not known.
                 const bool able = fit && !s.scale.cold && (low == 0 || ((m + 256.0f) * s.scale.ch > 64.0f && g.k == 0 && g.p < 1.0f)) &&
-                                  s.scale.ch < 256.0f &&
-                                  (near == 0 || (float)near * s.scale.ch * (float)weight62(kLeastLevel, s.scale, s.roots) <= 70368744177664.0f);   // 2^(62 + 24 - 40)
+                                  s.scale.ch < 256.0f;
                 if (!able) {
                     c.op = kCmdRecount;
                 } else {
                     int n_all;
                     u128 total;
                     const LevelPart part = scan_levels(s, total, n_all);
+                    const bool close = s.level[0] + s.level[kLevelsSide] == 0 || near_zero_close(s, total);
                     bool cut = false;   // whether the prefix ends inside the row
                     kept = n_all;
                     mass = total;
@@ -1635,7 +1641,7 @@ __device__ __noinline__ bool levels_row(const FilterArgs& a, long long r, const 
                         }
                         nth = tokens_for(point > at.before ? point - at.before : 1, at.weight, nth);
                     }
-                    if (fabsf(at.value) == kLeastLevel) {
+                    if (!close || fabsf(at.value) == kLeastLevel) {
                         c.op = kCmdRecount;
                     } else if (!DRAW && (!cut || nth == at.n)) {   // whole values
                         stage = 2;
