@@ -53,8 +53,9 @@ def test_the_filter_kernel_announces_itself_and_waits():
 def test_cluster_barriers_are_met_by_whole_warps(name):
     """barrier.cluster's .aligned form: no lane of a warp may still be on another way to it."""
     steps = [line.strip() for line in source(name).splitlines() if line.strip()]
-    at = [i for i, line in enumerate(steps) if line == "cluster_arrive();" or "barrier.cluster.arrive" in line]
+    arrivals = ("cluster_arrive();", "cluster_arrive_relaxed();")
+    at = [i for i, line in enumerate(steps) if line in arrivals]
     assert at
     for i in at:
-        before = [line for line in steps[i - 4:i] if line not in ("else", "if (DRAW)") and "barrier.cluster" not in line]
+        before = [line for line in steps[i - 4:i] if line not in ("else", "if (DRAW)", *arrivals)]
         assert before[-1] == "__syncwarp();", steps[i - 4:i + 1]
