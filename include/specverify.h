@@ -427,8 +427,14 @@ sv_status spec_verify_tree(const void* target_logits, const void* draft_logits, 
  *          mass (at least one token).
  * T = 0 keeps the argmax alone (lowest index); its filters are not used, and
  * may hold anything.
- * Sums are of whole numbers (weights in units of 2^-62 of the largest), so
- * results do not depend on the order of the additions.
+ * Sums are of whole numbers, so results do not depend on the order of the
+ * additions.  A weight is good to 2^-42 of itself at |l| / T up to 44, to 2^-36
+ * at 2800.  Before it is added it is rounded: to 2^-52 of the largest weight
+ * where at most 2048 tokens are left by top-k, min-p or the row's length; where
+ * more tokens count, to 2^-40 of the largest of 32 neighbouring values in bf16
+ * rows (where logits nearer to zero than 2^-24 may move the sum by 2^-34 of it),
+ * to 2^-29 of itself in fp32 rows.  A border that is nearer to the edge of a
+ * token than these errors add up to may fall on the other side of it.
  * A row with a NaN or +inf logit or no finite one, with an unusable
  * temperature, or with T > 0 and an unusable top_k (negative), top_p or min_p,
  * has the kept count -1.

@@ -40,9 +40,10 @@ sv_status check_rows(const void* logits, sv_dtype dtype, const float* temperatur
 // CTAs a row is spread over: one for each SM at most while the rows alone are
 // fewer, 56 KB or more each; of long rows half that each, once half the SMs do.
 // More and smaller parts read faster and then wait for one another more often.
-// One row of 128256 bf16, top-p alone: 23 us by eight CTAs, 25 by four, 29 by one; 16
-// rows of 151936 fp32: 49 by eight, 75 by one; 37 rows of 50257 bf16: 21 by one, 25 by
-// two; 145 rows of 32003 fp32: 41 and 51; 256 rows of 151936 fp32: 136 and 170.
+// By this rule and by others: one row of 128256 bf16, top-p alone, 26 us by eight CTAs, 28
+// by four, 32 by one; 16 rows of 151936 fp32 57 by eight, 47 by four, 62 by two, 86 by one;
+// 37 rows of 50257 bf16 22 by one, 26 by two; 145 rows of 32003 fp32 35 and 45; 256 rows
+// of 151936 fp32 154 and 182.
 int row_ctas(long long rows, long long row_bytes, int nsm)
 {
     int C = 1;

@@ -104,7 +104,9 @@ sv_status spec_kv_reserve(const sv_kv_pool* pool, const int32_t* kv_len, const i
     a.packed = packed;
     a.has_slots = slots != nullptr;
     a.slots16 = ((uintptr_t)slots & 15) == 0;
-    a.each = rows >= 1 << 17 ? 4 : 1;   // 2000003 slots: 12.6 us by fours, 16.4 one by one; 15360: 12.3 and 10.2
+    // By fours and one by one: 2000003 rows 13.3 and 19.9 us, 131072 6.8 and 9.4, 15360 6.7
+    // and 9.2, 4000 6.5 and 6.8, 1000 6.4 and 5.5.  (Fours would pay from some 4000 rows on.)
+    a.each = rows >= 1 << 17 ? 4 : 1;
     const long long pages = rows / pool->page_size + pool->B;   // about: what the tokens need
     return sv::launch_pages(sv::sv_reserve_kernel, a, pages + (slots ? rows : 0), stream);
 }

@@ -12,19 +12,23 @@
 //    from memory keeps the maxima of each thread and of its groups of four vectors;
 //    the k-th largest of the threads' maxima bounds the k-th largest logit, the
 //    few groups above it are read again, and what passes is sorted and weighed.
-//    Bounded by the bytes for many rows: 1024 rows of 128256 bf16 draw in 60 us
-//    (4.4 TB/s, 0.66 of the copy rate), 900 are filtered in 86 (5.4 TB/s read and
-//    written, 0.80); by the chain of steps for one row (15 us).
+//    Bounded by the bytes for many rows: 1024 rows of 128256 bf16 draw by top-k 50
+//    in 59 us (4.4 TB/s, 0.66 of the copy rate), 900 are filtered in 86 (5.4 TB/s
+//    read and written, 0.80); by the chain of steps for one row (9 us).
 //  - levels (bf16 where every token counts): the one pass counts how often each
 //    of 8192 values occurs, an atomic a token; weights times counts are the sums.
-//    1024 rows of 128256 draw in 137 us (1.9 TB/s): what bounds it is the atomics
+//    1024 rows of 128256 draw in 141 us (1.9 TB/s): what bounds it is the atomics
 //    in shared memory, some ten cycles for each warp's.
 //  - bins (fp32 where every token counts): sums by weight, and the border's bins
-//    read once more.  256 rows of 151936 draw in 136 us (1.1 TB/s of the one pass
+//    read once more.  256 rows of 151936 draw in 154 us (1.0 TB/s of the one pass
 //    that has to be): bounded by two atomics a token, the arithmetic of the
 //    remainders, and three sweeps of rows that L2 does not hold all of.
-//  - bisection, for what none of these settles.
-// All four compare whole numbers, so that they agree where they meet.
+//  - bisection, for what none of these settles: right for any row and slow, 2 to 11
+//    ms for one of them (which ones stands there).
+// All four compare whole numbers, so that none depends on the order of its sums.
+// How finely they count: sums of a list in 2^-52 of the largest weight, of levels in
+// 2^-42 of the largest of 32 neighbouring values, of bins in 2^-29 of the bin's own
+// weight, of bisection in 2^-62 of the largest weight.
 #pragma once
 
 #include "sv_weights.cuh"
@@ -52,18 +56,19 @@ struct FilterArgs {
 // Threads a row: 256 for bf16 (three blocks an SM), 512 for fp32 (two).  What a row
 // costs beside its bytes is a chain of short steps (maxima, bound, candidates, sums,
 // the crossing), which more threads shorten and more rows at a time hide.  By 256 and
-// by 512: 1024 rows of 128256 bf16 with top-p 134 and 154 us, with top-k 50 64 and 70;
-// 256 rows of 151936 fp32 with top-p 139 and 136 us, 64 rows 68 and 58.  A fourth block
-// an SM leaves L1, through which the loads in flight pass, 28 KB: top-k 50 75 us, 900
-// filtered rows 118 for 92.
+// by 512: 1024 rows of 128256 bf16 with top-p 141 and 165 us, with top-k 50 59 and 67;
+// 256 rows of 151936 fp32 with top-p 159 and 154 us, 64 rows 81 and 68.  A fourth block
+// an SM leaves L1, through which the loads in flight pass, 28 KB: top-k 50 64 us for
+// 59, 900 filtered rows 104 for 86, top-p 139 for 141.
 template <typename T> constexpr int kThreadsOf = sizeof(T) == 2 ? 256 : 512;
 template <typename T> constexpr int kBlocksOf = sizeof(T) == 2 ? 3 : 2;
 // Rows of at most kShortMost tokens, all of them in the list: 128 threads, eight blocks
-// an SM without the sums' shared memory.  7680 rows of 1000 fp32 filtered by top-p take
-// 186 us, 600 rows of 300 drawn 19; one row of 300 12, where 512 threads take 11.
+// an SM without the sums' shared memory.  By these and by 512 threads: 7680 rows of 1000
+// fp32 filtered by top-p 207 and 487 us, 600 rows of 300 drawn 18 and 29, one row of 300
+// 12 and 10.
 constexpr int kShortThreads = 128, kShortBlocks = 8, kShortMost = 8 * kShortThreads;
 constexpr int kClusterMost = 8;
-constexpr int kGroup = 4;          // vectors of a thread whose maximum is kept (1024 rows, top-k 50: 60 us; by eights 64)
+constexpr int kGroup = 4;          // vectors of a thread whose maximum is kept (1024 rows, top-k 50: 59 us; by eights 65)
 constexpr int kList = 2048;        // tokens sorted at a time
 constexpr int kBins = 4096;
 constexpr int kBinShift = 6;       // 64 bins an octave of weights
@@ -145,7 +150,7 @@ template <int NT> constexpr size_t filter_smem_bytes(int groups)
 // ---------------------------------------------------------------------------
 
 // A row's vector, past L1 (no use of it there: 1024 rows of 128256 bf16 with top-p
-// draw in 134 us, 140 by plain loads).  Not through the read-only path: the filtered
+// draw in 141 us, 148 by plain loads).  Not through the read-only path: the filtered
 // row may be written where the row is.
 __device__ __forceinline__ uint4 ld_row(const uint4* p)
 {
@@ -350,7 +355,16 @@ struct Prefix {
 // ---------------------------------------------------------------------------
 // Any row: bisection (one CTA).  Tens of passes over the row; it takes rows whose
 // border lies among more equal or nearly equal logits than a list holds, and
-// rows of nearly no temperature.
+// rows of nearly no temperature.  Which ones, what one of them and many of them take,
+// and in brackets what a sort in torch operations takes for the same:
+//  - |m| / T of 2839 and more, with top-p or no filter.  128256 bf16, T = 0.01, a
+//    largest logit of 30: 1.7 ms, 1024 rows 6.4 (0.7 and 22).
+//  - fewer than k logits over a finite mask.  128256 bf16, ten tokens over -1e4,
+//    top-k 50: 2.8 ms, 1024 rows 13 (0.8 and 22).
+//  - fp32 rows with more than 2048 tokens in the bin (T ln 2 / 64 wide) of the border
+//    or of the draw.  151936 normal logits of deviation 0.5 with top-p 0.9, T = 3: a
+//    draw 11 ms, a filtered row 5.4; 256 rows 17 and 8.7 (0.7 and 7).  Such draws from
+//    T = 1.5 on, filtered rows from T = 3; at T = 1, 256 rows take 0.22 and 0.19 ms.
 // ---------------------------------------------------------------------------
 
 // The sum over a prefix of 1 (kCount) or of the weights.
@@ -1846,8 +1860,9 @@ __global__ void __launch_bounds__(NT, NT == kShortThreads ? kShortBlocks : kBloc
     const bool by_thread = share <= NT / 2;
     const bool bounded = !greedy && g.k > 0 && (by_thread || (share <= groups * (NT / 2) && g.k <= kList / 2));
     // bf16 rows where every token counts, or nearly: 1024 rows of 128256 with top-k 250
-    // take 102 us by the bound and 133 by levels, with top-k 500 167 and 133, with 1000
-    // 252 and 133.
+    // take 101 us by the bound and 132 by levels, with top-k 500 125 and 133, with 700
+    // 139 and 133, with 1000 164 and 133.  (Between 256 and 600 the bound would be the
+    // faster one for these; where the row is spread over CTAs k is shared among them.)
     if constexpr (sizeof(T) == 2 && NT != kShortThreads)
         if (good && !greedy && g.min_p == 0.0f && V > kList && (g.k == 0 ? DRAW || g.p < 1.0f : share > NT || !bounded)) {
             if (levels_row<DRAW>(a, r, g, row, rank, s))
